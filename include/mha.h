@@ -340,6 +340,110 @@ mha_status mha_decode(mha_t handle, int B, int T_q, int T_max, const void* Q, in
                       const int32_t* cache_lengths, void* O, int64_t ldo, void* stream);
 
 /*
+ * Long-context operators.  K and V rows of cached or valid tokens (j < L_b) must be finite; rows at or
+ * past L_b may hold anything and reach no output.
+ *
+ * mha_attention_window -- causal sliding-window attention with sinks for all heads: row i of a sequence
+ * sees key j iff j <= i, j < L_b and (i - j < window or j < sinks), so the work grows with T * window
+ * instead of T^2.  window >= T is mha_attention with causal = 1.
+ *   Q, K, V, O, G  as for mha_attention_ex with T_q == T_kv == T (G: NULL, or gate pre-activations)
+ *   window         keys a row sees, itself included; >= 1
+ *   sinks          first tokens that stay visible to every row; >= 0
+ *   kv_lengths     device int32[B] or NULL (every L_b = T); a value outside [1, T] makes that batch's
+ *                  rows NaN and records MHA_ERR_BAD_LENGTH
+ * A row that sees no key (only a padding row i >= L_b can) is written as zeros.  O must not overlap an
+ * input.  dtype, shape and alignment rules of mha_attention; fp32 needs T <= 2097120.  One launch.
+ */
+mha_status mha_attention_window(mha_t handle, int B, int T, const void* Q, int64_t ldq, const void* K,
+                                int64_t ldk, const void* V, int64_t ldv, const void* G, int64_t ldg,
+                                int window, int sinks, const int32_t* kv_lengths, void* O, int64_t ldo,
+                                void* stream);
+
+/*
+ * mha_forward_window -- the self-attention layer with mha_attention_window in the place of the causal
+ * attention: Y = residual + Concat(heads) W_o + b_o.  Other arguments, checks and workspace
+ * (mha_workspace_size(B, T, T)) as for mha_forward_ex with X_kv == NULL.  Three launches.
+ */
+mha_status mha_forward_window(mha_t handle, const void* X, int B, int T, const void* W_qkv,
+                              const void* b_qkv, const void* W_o, const void* b_o, int window, int sinks,
+                              const int32_t* kv_lengths, const void* residual, void* out, void* stream);
+
+/*
+ * mha_cache_step_workspace_size -- bytes of workspace mha_decode_window (T_prefix = weights = 0),
+ * mha_decode_shared (weights = 0) and mha_decode_weights (T_prefix = 0, weights = 1) need: the 256-byte
+ * status block, the partial results of the split over the cache and, with weights, the fp32 scores of
+ * every query row.  0 for an invalid handle or size.
+ */
+size_t mha_cache_step_workspace_size(mha_t handle, int B, int T_q, int T_prefix, int T_max, int weights);
+
+/*
+ * mha_decode_window -- mha_decode under a sliding window with sinks: new token t, at position
+ * p = L_b - T_q + t of its cache, sees keys j <= p with p - j < window or j < sinks.  Reads only
+ * those keys: a step costs the same at every cache length.  window >= 1, sinks >= 0; other arguments
+ * as for mha_decode.  O must not overlap an input.
+ * Both dtypes need a workspace of mha_cache_step_workspace_size(B, T_q, 0, T_max, 0) bytes
+ * (MHA_ERR_WORKSPACE otherwise).  Two launches.
+ */
+mha_status mha_decode_window(mha_t handle, int B, int T_q, int T_max, const void* Q, int64_t ldq,
+                             const void* K_cache, int64_t ldk, const void* V_cache, int64_t ldv, int window,
+                             int sinks, const int32_t* cache_lengths, void* O, int64_t ldo, void* stream);
+
+/*
+ * mha_decode_shared -- a decode step of a batch whose sequences share their first T_prefix tokens
+ * (samples of one prompt, requests behind one system prompt): the prefix's keys and values are stored
+ * once and read once for the whole batch.
+ *   K_prefix  T_prefix rows of stride ldkp, K/V head g at columns [g*d_k, (g+1)*d_k); V_prefix likewise
+ *             (T_prefix == 0: ignored, the call is mha_decode)
+ *   K_cache, V_cache, cache_lengths  each sequence's own tokens after the prefix, as for mha_decode:
+ *             L_b of them, the T_q new ones included
+ * New token t sees the whole prefix and its own cache rows j <= L_b - T_q + t.  O must not overlap an
+ * input.  Workspace: mha_cache_step_workspace_size(B, T_q, T_prefix, T_max, 0).  Two launches.
+ */
+mha_status mha_decode_shared(mha_t handle, int B, int T_q, int T_prefix, const void* K_prefix, int64_t ldkp,
+                             const void* V_prefix, int64_t ldvp, int T_max, const void* Q, int64_t ldq,
+                             const void* K_cache, int64_t ldk, const void* V_cache, int64_t ldv,
+                             const int32_t* cache_lengths, void* O, int64_t ldo, void* stream);
+
+/*
+ * mha_decode_weights -- mha_decode that also accumulates the attention every cached token receives, the
+ * measure mha_cache_evict goes by:
+ *   weights  device fp32 (B, h_kv, T_max), contiguous; entry (b, g, j) grows by the softmax weight of
+ *            key j summed over the query heads of group g and the T_q new tokens.  The new tokens'
+ *            own entries (j >= L_b - T_q) have no history and are written, not added to; entries at or
+ *            past L_b, and those of a batch with an invalid length, stay as they are.
+ * O is mha_decode's.  The sums are made in a fixed order.  weights and O must not overlap an input or
+ * each other.  Workspace: mha_cache_step_workspace_size(B, T_q, 0, T_max, 1).  Two launches.
+ */
+mha_status mha_decode_weights(mha_t handle, int B, int T_q, int T_max, const void* Q, int64_t ldq,
+                              const void* K_cache, int64_t ldk, const void* V_cache, int64_t ldv,
+                              const int32_t* cache_lengths, float* weights, void* O, int64_t ldo,
+                              void* stream);
+
+/*
+ * mha_cache_evict -- cut every sequence's cache to at most `keep` tokens per K/V head: the last `recent`
+ * tokens and, of the earlier ones, the keep - recent of largest weight (equal weights: the lower index;
+ * NaN counts as lowest).  The kept tokens keep their order.
+ *   cache_lengths  device int32[B], L_b in [0, T_max]; a batch with another value is not touched, its
+ *                  new length is 0 and MHA_ERR_BAD_LENGTH is recorded
+ *   weights        device fp32 (B, h_kv, T_max) as mha_decode_weights accumulates them
+ *   K_out, V_out   rows (B, T_out) of strides ldko, ldvo, T_out >= keep; weights_out fp32
+ *                  (B, h_kv, T_out).  Entries 0 .. min(L_b, keep) - 1 are written, the others stay.
+ *                  In place: K_out == K_cache, V_out == V_cache and weights_out == weights with the
+ *                  same strides and T_out == T_max; otherwise no output may overlap an input.
+ *   kept           device int32 (B, h_kv, keep): the kept tokens' indices, ascending, then -1
+ *   new_lengths    device int32[B]: min(L_b, keep); may be cache_lengths
+ * 1 <= keep, 0 <= recent <= keep.  With recent >= T_q the next decode steps' rule that the new tokens
+ * are the last ones holds.  K and V may be column views of one buffer.  Needs no workspace (one that is
+ * attached receives the status).  bf16: B <= 65535, d_k == d_v in {64, 128}, strides multiples of 8 and
+ * 16-byte aligned pointers.  Two launches.
+ */
+mha_status mha_cache_evict(mha_t handle, int B, int T_max, int keep, int recent, const void* K_cache,
+                           int64_t ldk, const void* V_cache, int64_t ldv, const int32_t* cache_lengths,
+                           const float* weights, int T_out, void* K_out, int64_t ldko, void* V_out,
+                           int64_t ldvo, float* weights_out, int32_t* kept, int32_t* new_lengths,
+                           void* stream);
+
+/*
  * mha_get_status -- copy the device status word of the attached workspace to
  * *status_out (an mha_status: MHA_OK, MHA_ERR_TIMEOUT or MHA_ERR_BAD_LENGTH;
  * the first error recorded wins) and reset it to MHA_OK.  Synchronises

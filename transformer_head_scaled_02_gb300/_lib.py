@@ -53,6 +53,18 @@ _SIGNATURES = {
                               _vp, _i64, _vp]),
     "mha_decode_workspace_size": (_sz, [_vp, _i, _i, _i]),
     "mha_decode": (_i, [_vp, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp]),
+    "mha_attention_window": (_i, [_vp, _i, _i, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i, _i, _vp,
+                                  _vp, _i64, _vp]),
+    "mha_forward_window": (_i, [_vp, _vp, _i, _i, _vp, _vp, _vp, _vp, _i, _i, _vp, _vp, _vp, _vp]),
+    "mha_cache_step_workspace_size": (_sz, [_vp, _i, _i, _i, _i, _i]),
+    "mha_decode_window": (_i, [_vp, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _i64, _i, _i, _vp, _vp, _i64,
+                               _vp]),
+    "mha_decode_shared": (_i, [_vp, _i, _i, _i, _vp, _i64, _vp, _i64, _i, _vp, _i64, _vp, _i64, _vp,
+                               _i64, _vp, _vp, _i64, _vp]),
+    "mha_decode_weights": (_i, [_vp, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64,
+                                _vp]),
+    "mha_cache_evict": (_i, [_vp, _i, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _vp, _i, _vp, _i64, _vp,
+                             _i64, _vp, _vp, _vp, _vp]),
     "mha_get_status": (_i, [_vp, ctypes.POINTER(ctypes.c_int32), _vp]),
     "mha_forward_static_workspace": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp,
                                           _vp, _vp, _vp]),
@@ -213,6 +225,55 @@ def mha_decode(handle, B, T_q, T_max, Q, ldq, K_cache, ldk, V_cache, ldv, cache_
     code = load().mha_decode(handle, B, T_q, T_max, Q, ldq, K_cache, ldk, V_cache, ldv,
                              cache_lengths, O, ldo, stream)
     return _check("mha_decode", code) if check else code
+
+
+def mha_attention_window(handle, B, T, Q, ldq, K, ldk, V, ldv, G, ldg, window, sinks, kv_lengths, O,
+                         ldo, stream, check: bool = True) -> int:
+    code = load().mha_attention_window(handle, B, T, Q, ldq, K, ldk, V, ldv, G, ldg, window, sinks,
+                                       kv_lengths, O, ldo, stream)
+    return _check("mha_attention_window", code) if check else code
+
+
+def mha_forward_window(handle, X, B, T, W_qkv, b_qkv, W_o, b_o, window, sinks, kv_lengths, residual,
+                       out, stream, check: bool = True) -> int:
+    code = load().mha_forward_window(handle, X, B, T, W_qkv, b_qkv, W_o, b_o, window, sinks, kv_lengths,
+                                     residual, out, stream)
+    return _check("mha_forward_window", code) if check else code
+
+
+def mha_cache_step_workspace_size(handle: int, B: int, T_q: int, T_prefix: int, T_max: int,
+                                  weights: int) -> int:
+    return int(load().mha_cache_step_workspace_size(handle, B, T_q, T_prefix, T_max, int(weights)))
+
+
+def mha_decode_window(handle, B, T_q, T_max, Q, ldq, K_cache, ldk, V_cache, ldv, window, sinks,
+                      cache_lengths, O, ldo, stream, check: bool = True) -> int:
+    code = load().mha_decode_window(handle, B, T_q, T_max, Q, ldq, K_cache, ldk, V_cache, ldv, window,
+                                    sinks, cache_lengths, O, ldo, stream)
+    return _check("mha_decode_window", code) if check else code
+
+
+def mha_decode_shared(handle, B, T_q, T_prefix, K_prefix, ldkp, V_prefix, ldvp, T_max, Q, ldq, K_cache,
+                      ldk, V_cache, ldv, cache_lengths, O, ldo, stream, check: bool = True) -> int:
+    code = load().mha_decode_shared(handle, B, T_q, T_prefix, K_prefix, ldkp, V_prefix, ldvp, T_max, Q,
+                                    ldq, K_cache, ldk, V_cache, ldv, cache_lengths, O, ldo, stream)
+    return _check("mha_decode_shared", code) if check else code
+
+
+def mha_decode_weights(handle, B, T_q, T_max, Q, ldq, K_cache, ldk, V_cache, ldv, cache_lengths,
+                       weights, O, ldo, stream, check: bool = True) -> int:
+    code = load().mha_decode_weights(handle, B, T_q, T_max, Q, ldq, K_cache, ldk, V_cache, ldv,
+                                     cache_lengths, weights, O, ldo, stream)
+    return _check("mha_decode_weights", code) if check else code
+
+
+def mha_cache_evict(handle, B, T_max, keep, recent, K_cache, ldk, V_cache, ldv, cache_lengths, weights,
+                    T_out, K_out, ldko, V_out, ldvo, weights_out, kept, new_lengths, stream,
+                    check: bool = True) -> int:
+    code = load().mha_cache_evict(handle, B, T_max, keep, recent, K_cache, ldk, V_cache, ldv,
+                                  cache_lengths, weights, T_out, K_out, ldko, V_out, ldvo, weights_out,
+                                  kept, new_lengths, stream)
+    return _check("mha_cache_evict", code) if check else code
 
 
 def mha_get_status(handle: int, stream: int) -> int:

@@ -1,0 +1,305 @@
+// span_api.cu -- the C ABI of the long-context operators (include/mha.h): windowed attention with
+// sinks, the windowed, shared-prefix and weight-accumulating decode steps, and the eviction.  Host
+// checks, workspace layout and launch sequences; nothing is allocated or synchronised here.
+#include <math.h>
+#include <stdint.h>
+
+#include "../../include/mha.h"
+#include "api_util.h"
+#include "internal.h"
+#include "span_records.cuh"
+
+using namespace mha;
+
+namespace {
+
+// Query rows of a row block: the smallest of 16, 32 and 64 that holds the rows (a thread of the
+// CUDA-core kernel owns 1, 2 or 4 of them).
+int row_block(const mha_s*, int64_t rows) { return span_simt_rows(rows); }
+
+SpanShape span_shape(const mha_s* m, int B, int T_q, int T_max, int T_p, int window, int sinks, int* bm) {
+    SpanShape p;
+    p.B = B;
+    p.h_kv = m->h_kv;
+    p.per = m->h / m->h_kv;
+    p.T_q = T_q;
+    p.T_max = T_max;
+    p.rows = p.per * T_q;
+    p.T_p = T_p;
+    // a prefix's rows are those of the whole batch
+    const int64_t rows_p = (int64_t)B * p.rows;
+    *bm = row_block(m, T_p > 0 ? rows_p : p.rows);
+    p.nrb = (p.rows + *bm - 1) / *bm;
+    p.nrbp = T_p > 0 ? (int)((rows_p + *bm - 1) / *bm) : 0;
+    p.window = window < T_max ? window : T_max;
+    p.sinks = sinks < T_max ? sinks : T_max;
+    return p;
+}
+
+// Bytes from the first to the last element of `rows` rows of `width` elements.
+size_t extent(int64_t rows, int64_t ld, int64_t width, size_t elem) {
+    return rows > 0 ? ((size_t)(rows - 1) * (size_t)ld + (size_t)width) * elem : 0;
+}
+
+bool rows_ok(const mha_s* m, const void* p, int64_t ld, int64_t width) {
+    if (p == nullptr || ld < width) return false;
+    return m->dtype != MHA_BF16 || (ld % 8 == 0 && aligned16(p));
+}
+
+mha_status shape_supported(const mha_s* m) {
+    if (m->dtype == MHA_BF16) return bf16_shape_supported(m) ? MHA_OK : MHA_ERR_UNSUPPORTED;
+    return m->dk <= 256 && m->dv <= 256 ? MHA_OK : MHA_ERR_UNSUPPORTED;
+}
+
+struct CacheStep {
+    int B, T_q, T_max, T_p, window, sinks;
+    const void *Q, *K, *V, *Kp, *Vp;
+    int64_t ldq, ldk, ldv, ldkp, ldvp;
+    const int32_t* lengths;
+    float* weights;
+    void* O;
+    int64_t ldo;
+};
+
+// Sizes that every cache step shares (the int32 row arithmetic of the kernels).
+bool step_sizes_ok(const mha_s* m, int B, int T_q, int T_p, int T_max) {
+    return B >= 0 && T_q >= 0 && T_p >= 0 && T_max >= 0 && (int64_t)B * T_max <= INT32_MAX &&
+           (int64_t)B * m->h * T_q <= INT32_MAX;
+}
+
+mha_status run_cache_step(mha_s* m, const CacheStep& a, cudaStream_t stream) {
+    if (m == nullptr) return MHA_ERR_INVALID_ARG;
+    if (!step_sizes_ok(m, a.B, a.T_q, a.T_p, a.T_max) || a.window < 1 || a.sinks < 0) return MHA_ERR_INVALID_ARG;
+    if (a.B == 0 || a.T_q == 0) return MHA_OK;
+    if (a.T_q > a.T_max || a.lengths == nullptr) return MHA_ERR_INVALID_ARG;
+    const Widths wd = widths(m);
+    const int64_t hv = (int64_t)m->h * m->dv;
+    const size_t s = elem_bytes(m->dtype);
+    const mha_status sup = shape_supported(m);
+    if (sup != MHA_OK) return sup;
+    if (!rows_ok(m, a.Q, a.ldq, wd.q) || !rows_ok(m, a.K, a.ldk, wd.k) || !rows_ok(m, a.V, a.ldv, wd.v) ||
+        !rows_ok(m, a.O, a.ldo, hv))
+        return MHA_ERR_INVALID_ARG;
+    if (a.T_p > 0 && (!rows_ok(m, a.Kp, a.ldkp, wd.k) || !rows_ok(m, a.Vp, a.ldvp, wd.v))) return MHA_ERR_INVALID_ARG;
+    const int64_t nq = (int64_t)a.B * a.T_q, nc = (int64_t)a.B * a.T_max;
+    const size_t wbytes = a.weights != nullptr ? (size_t)nc * m->h_kv * sizeof(float) : 0;
+    struct Span {
+        const void* p;
+        size_t n;
+    };
+    const Span in[5] = {{a.Q, extent(nq, a.ldq, wd.q, s)},
+                        {a.K, extent(nc, a.ldk, wd.k, s)},
+                        {a.V, extent(nc, a.ldv, wd.v, s)},
+                        {a.T_p > 0 ? a.Kp : nullptr, extent(a.T_p, a.ldkp, wd.k, s)},
+                        {a.T_p > 0 ? a.Vp : nullptr, extent(a.T_p, a.ldvp, wd.v, s)}};
+    const size_t obytes = extent(nq, a.ldo, hv, s);
+    for (const Span& x : in)
+        if (overlaps(a.O, obytes, x.p, x.n) || overlaps(a.weights, wbytes, x.p, x.n)) return MHA_ERR_INVALID_ARG;
+    if (overlaps(a.O, obytes, a.weights, wbytes)) return MHA_ERR_INVALID_ARG;
+
+    int bm;
+    const SpanShape p = span_shape(m, a.B, a.T_q, a.T_max, a.T_p, a.window, a.sinks, &bm);
+    const SpanLayout w = span_layout(p, m->dv, bm, a.weights != nullptr);
+    if (m->ws == nullptr || m->ws_bytes < kStatusBytes + w.total) return MHA_ERR_WORKSPACE;
+    uint8_t* ws = static_cast<uint8_t*>(m->ws) + kStatusBytes;
+    SpanRecords rec;
+    rec.ml = reinterpret_cast<float2*>(ws + w.ml_off);
+    rec.o = reinterpret_cast<float*>(ws + w.o_off);
+    rec.rps_p = w.rps_p;
+    rec.rps_c = w.rps_c;
+    rec.base_c = w.base_c;
+    rec.dv = m->dv;
+    float* scores = a.weights != nullptr ? reinterpret_cast<float*>(ws + w.s_off) : nullptr;
+    int sms = 0;
+    const mha_status st = query_sms(&sms);
+    if (st != MHA_OK) return st;
+    int grid = 0;
+    cudaError_t err;
+    if (m->dtype == MHA_F32) {
+        auto f = [](const void* x) { return static_cast<const float*>(x); };
+        err = launch_span_f32(p, rec, bm, f(a.Q), a.ldq, f(a.K), a.ldk, f(a.V), a.ldv, f(a.Kp), a.ldkp, f(a.Vp),
+                              a.ldvp, static_cast<float*>(a.O), a.ldo, m->dk, m->dv, a.lengths, scores, sms, &grid,
+                              status_ptr(m), stream);
+    } else {
+        err = launch_span_bf16(p, rec, bm, a.Q, a.ldq, a.K, a.ldk, a.V, a.ldv, a.Kp, a.ldkp, a.Vp, a.ldvp, a.O, a.ldo,
+                               m->dk, a.lengths, scores, sms, &grid, status_ptr(m), stream);
+    }
+    if (err != cudaSuccess) return MHA_ERR_CUDA;
+    err = launch_span_merge(m->dtype, p, rec, bm, grid, a.O, a.ldo, a.lengths, scores, a.weights, stream);
+    return err == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+mha_status mha_attention_window(mha_t handle, int B, int T, const void* Q, int64_t ldq, const void* K, int64_t ldk,
+                                const void* V, int64_t ldv, const void* G, int64_t ldg, int window, int sinks,
+                                const int32_t* kv_lengths, void* O, int64_t ldo, void* stream) {
+    const mha_s* m = handle;
+    if (m == nullptr) return MHA_ERR_INVALID_ARG;
+    if (B < 0 || T < 0 || window < 1 || sinks < 0) return MHA_ERR_INVALID_ARG;
+    if ((int64_t)B * T > INT32_MAX || (int64_t)B * m->h > INT32_MAX) return MHA_ERR_INVALID_ARG;
+    const mha_status sup = shape_supported(m);
+    if (sup != MHA_OK) return sup;
+    if (B == 0 || T == 0) return MHA_OK;
+    const Widths wd = widths(m);
+    const int64_t hv = (int64_t)m->h * m->dv, n = (int64_t)B * T;
+    const size_t s = elem_bytes(m->dtype);
+    if (!rows_ok(m, Q, ldq, wd.q) || !rows_ok(m, K, ldk, wd.k) || !rows_ok(m, V, ldv, wd.v) || !rows_ok(m, O, ldo, hv) ||
+        (G != nullptr && !rows_ok(m, G, ldg, hv)))
+        return MHA_ERR_INVALID_ARG;
+    const size_t ob = extent(n, ldo, hv, s);
+    if (overlaps(O, ob, Q, extent(n, ldq, wd.q, s)) || overlaps(O, ob, K, extent(n, ldk, wd.k, s)) ||
+        overlaps(O, ob, V, extent(n, ldv, wd.v, s)) || overlaps(O, ob, G, extent(n, ldg, hv, s)))
+        return MHA_ERR_INVALID_ARG;
+    window = window < T ? window : T;
+    sinks = sinks < T ? sinks : T;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    cudaError_t err;
+    if (m->dtype == MHA_F32) {
+        if ((T + 31) / 32 > 65535) return MHA_ERR_UNSUPPORTED;
+        auto f = [](const void* x) { return static_cast<const float*>(x); };
+        err = launch_window_f32(f(Q), ldq, f(K), ldk, f(V), ldv, f(G), ldg, static_cast<float*>(O), ldo, B, m->h,
+                                m->h_kv, T, m->dk, m->dv, window, sinks, kv_lengths, status_ptr(m), cs);
+    } else {
+        if ((int64_t)B * m->h * ((T + 127) / 128) > INT32_MAX) return MHA_ERR_UNSUPPORTED;
+        int sms = 0;
+        const mha_status st = query_sms(&sms);
+        if (st != MHA_OK) return st;
+        err = launch_window_bf16(Q, ldq, K, ldk, V, ldv, G, ldg, O, ldo, B, m->h, m->h_kv, T, m->dk, window, sinks,
+                                 kv_lengths, sms, status_ptr(m), cs);
+    }
+    return err == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
+}
+
+mha_status mha_forward_window(mha_t handle, const void* X, int B, int T, const void* W_qkv, const void* b_qkv,
+                              const void* W_o, const void* b_o, int window, int sinks, const int32_t* kv_lengths,
+                              const void* residual, void* out, void* stream) {
+    const mha_s* m = handle;
+    if (window < 1 || sinks < 0) return MHA_ERR_INVALID_ARG;
+    mha_status st = check_forward(m, X, nullptr, B, T, T, W_qkv, b_qkv, W_o, b_o, 1, residual, out);
+    if (st != MHA_OK) return st;
+    if (B == 0 || T == 0) return MHA_OK;
+    const WsLayout w = ws_layout(m, B, T, T);
+    if (m->ws == nullptr || m->ws_bytes < w.total) return MHA_ERR_WORKSPACE;
+    const Widths wd = widths(m);
+    const int64_t n = wd.all(), hv = (int64_t)m->h * m->dv;
+    const size_t s = elem_bytes(m->dtype);
+    uint8_t* qkv = static_cast<uint8_t*>(m->ws) + w.q_off;
+    void* ocat = static_cast<uint8_t*>(m->ws) + w.o_off;
+    st = mha_linear_ex(handle, X, m->D, B * T, m->D, W_qkv, n, (int)n, b_qkv, nullptr, 0, qkv, n, stream);
+    if (st != MHA_OK) return st;
+    st = mha_attention_window(handle, B, T, qkv, n, qkv + wd.q * s, n, qkv + (wd.q + wd.k) * s, n,
+                              m->gated ? qkv + (wd.q + wd.k + wd.v) * s : nullptr, n, window, sinks, kv_lengths, ocat,
+                              hv, stream);
+    if (st != MHA_OK) return st;
+    return mha_linear_ex(handle, ocat, hv, B * T, (int)hv, W_o, m->D, m->D, b_o, residual, m->D, out, m->D, stream);
+}
+
+size_t mha_cache_step_workspace_size(mha_t handle, int B, int T_q, int T_prefix, int T_max, int weights) {
+    if (handle == nullptr || !step_sizes_ok(handle, B, T_q, T_prefix, T_max)) return 0;
+    if (B == 0 || T_q == 0 || T_max == 0) return kStatusBytes;
+    int bm;
+    const SpanShape p = span_shape(handle, B, T_q, T_max, T_prefix, T_max, 0, &bm);
+    return kStatusBytes + span_layout(p, handle->dv, bm, weights != 0).total;
+}
+
+mha_status mha_decode_window(mha_t handle, int B, int T_q, int T_max, const void* Q, int64_t ldq, const void* K_cache,
+                             int64_t ldk, const void* V_cache, int64_t ldv, int window, int sinks,
+                             const int32_t* cache_lengths, void* O, int64_t ldo, void* stream) {
+    const CacheStep a{B, T_q, T_max, 0, window, sinks, Q, K_cache, V_cache, nullptr, nullptr, ldq, ldk, ldv, 0, 0,
+                      cache_lengths, nullptr, O, ldo};
+    return run_cache_step(handle, a, static_cast<cudaStream_t>(stream));
+}
+
+mha_status mha_decode_shared(mha_t handle, int B, int T_q, int T_prefix, const void* K_prefix, int64_t ldkp,
+                             const void* V_prefix, int64_t ldvp, int T_max, const void* Q, int64_t ldq,
+                             const void* K_cache, int64_t ldk, const void* V_cache, int64_t ldv,
+                             const int32_t* cache_lengths, void* O, int64_t ldo, void* stream) {
+    const CacheStep a{B, T_q, T_max, T_prefix, T_max > 0 ? T_max : 1, 0, Q, K_cache, V_cache, K_prefix, V_prefix, ldq,
+                      ldk, ldv, ldkp, ldvp, cache_lengths, nullptr, O, ldo};
+    return run_cache_step(handle, a, static_cast<cudaStream_t>(stream));
+}
+
+mha_status mha_decode_weights(mha_t handle, int B, int T_q, int T_max, const void* Q, int64_t ldq,
+                              const void* K_cache, int64_t ldk, const void* V_cache, int64_t ldv,
+                              const int32_t* cache_lengths, float* weights, void* O, int64_t ldo, void* stream) {
+    if (handle != nullptr && B > 0 && T_q > 0 && weights == nullptr) return MHA_ERR_INVALID_ARG;
+    const CacheStep a{B, T_q, T_max, 0, T_max > 0 ? T_max : 1, 0, Q, K_cache, V_cache, nullptr, nullptr, ldq, ldk, ldv,
+                      0, 0, cache_lengths, weights, O, ldo};
+    return run_cache_step(handle, a, static_cast<cudaStream_t>(stream));
+}
+
+mha_status mha_cache_evict(mha_t handle, int B, int T_max, int keep, int recent, const void* K_cache, int64_t ldk,
+                           const void* V_cache, int64_t ldv, const int32_t* cache_lengths, const float* weights,
+                           int T_out, void* K_out, int64_t ldko, void* V_out, int64_t ldvo, float* weights_out,
+                           int32_t* kept, int32_t* new_lengths, void* stream) {
+    const mha_s* m = handle;
+    if (m == nullptr) return MHA_ERR_INVALID_ARG;
+    if (B < 0 || T_max < 0 || keep < 1 || recent < 0 || recent > keep || T_out < keep) return MHA_ERR_INVALID_ARG;
+    if ((int64_t)B * T_max > INT32_MAX || (int64_t)B * T_out > INT32_MAX || (int64_t)B * m->h_kv > INT32_MAX)
+        return MHA_ERR_INVALID_ARG;
+    const mha_status sup = shape_supported(m);
+    if (sup != MHA_OK) return sup;
+    if (B > 65535) return MHA_ERR_UNSUPPORTED;
+    if (B == 0) return MHA_OK;
+    if (T_max == 0) return MHA_ERR_INVALID_ARG;
+    const Widths wd = widths(m);
+    if (cache_lengths == nullptr || weights == nullptr || weights_out == nullptr || kept == nullptr ||
+        new_lengths == nullptr)
+        return MHA_ERR_INVALID_ARG;
+    if (!rows_ok(m, K_cache, ldk, wd.k) || !rows_ok(m, V_cache, ldv, wd.v) || !rows_ok(m, K_out, ldko, wd.k) ||
+        !rows_ok(m, V_out, ldvo, wd.v))
+        return MHA_ERR_INVALID_ARG;
+    // in place: all three at once, with the same layout; else no output may touch an input
+    const size_t s = elem_bytes(m->dtype);
+    const bool in_place = K_out == K_cache;
+    if (in_place) {
+        if (V_out != V_cache || weights_out != weights || T_out != T_max || ldko != ldk || ldvo != ldv)
+            return MHA_ERR_INVALID_ARG;
+    }
+    const int64_t ni = (int64_t)B * T_max, no = (int64_t)B * T_out;
+    struct Span {
+        const void* p;
+        size_t n;
+    };
+    const Span in[4] = {{K_cache, extent(ni, ldk, wd.k, s)},
+                        {V_cache, extent(ni, ldv, wd.v, s)},
+                        {weights, (size_t)ni * m->h_kv * sizeof(float)},
+                        {cache_lengths, (size_t)B * sizeof(int32_t)}};
+    const Span out[5] = {{K_out, extent(no, ldko, wd.k, s)},
+                         {V_out, extent(no, ldvo, wd.v, s)},
+                         {weights_out, (size_t)no * m->h_kv * sizeof(float)},
+                         {new_lengths, (size_t)B * sizeof(int32_t)},
+                         {kept, (size_t)B * m->h_kv * keep * sizeof(int32_t)}};
+    // K and V may be column views of one buffer: rows interleave, so two views of the same rows
+    // overlap only if their columns do
+    auto touch = [&](const Span& x, int64_t ldx, int64_t wx, const Span& y, int64_t ldy, int64_t wy) {
+        if (!overlaps(x.p, x.n, y.p, y.n)) return false;
+        if (ldx != ldy || ldx <= 0) return true;
+        const int64_t d = static_cast<const uint8_t*>(y.p) - static_cast<const uint8_t*>(x.p);
+        const int64_t ld = ldx * (int64_t)s, c = ((d % ld) + ld) % ld;  // y's first column, x's at 0
+        return c < wx * (int64_t)s || c + wy * (int64_t)s > ld;
+    };
+    const int64_t ldi[2] = {ldk, ldv}, ldo[2] = {ldko, ldvo}, wk[2] = {wd.k, wd.v};
+    for (int o = 0; o < 5; ++o) {
+        for (int i = 0; i < 4; ++i) {
+            if ((o == i && o < 3 && in_place) || (o == 3 && i == 3 && new_lengths == cache_lengths)) continue;
+            const bool hit = o < 2 && i < 2 ? touch(in[i], ldi[i], wk[i], out[o], ldo[o], wk[o])
+                                            : overlaps(out[o].p, out[o].n, in[i].p, in[i].n);
+            if (hit) return MHA_ERR_INVALID_ARG;
+        }
+        for (int q = o + 1; q < 5; ++q) {
+            const bool hit = o < 2 && q < 2 ? touch(out[o], ldo[o], wk[o], out[q], ldo[q], wk[q])
+                                            : overlaps(out[o].p, out[o].n, out[q].p, out[q].n);
+            if (hit) return MHA_ERR_INVALID_ARG;
+        }
+    }
+    const cudaError_t err = launch_evict(K_cache, ldk, V_cache, ldv, K_out, ldko, V_out, ldvo, (int)s, B, m->h_kv, T_max,
+                                         T_out, m->dk, m->dv, keep, recent, cache_lengths, weights, weights_out, kept,
+                                         new_lengths, status_ptr(m), static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
+}
+
+}  // extern "C"

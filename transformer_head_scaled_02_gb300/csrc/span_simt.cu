@@ -1,0 +1,416 @@
+// span_simt.cu -- the windowed attention and the cache operators on CUDA cores (fp32 layers):
+//   window_simt_kernel  causal sliding-window attention with sinks over whole sequences
+//   span_simt_kernel    the pieces of span.cuh: windowed, shared-prefix and weight-accumulating
+//                       decode steps
+// Both form score tiles of BQ = 16 RQ query rows x 64 keys as small matrix products in full fp32
+// (256 threads: thread (tx, ty) owns rows RQ ty.. and keys tx + 16 c), keep the online softmax in
+// base 2 (log2(e) / sqrt(d_k) folded into one multiply per score; row maximum and sum over the 16
+// threads sharing the rows, by shuffles), stage P in shared memory and add P V to RQ x 4 CV outputs
+// per thread.  Q, K and V tiles are row-major in shared memory with rows padded by 4 floats: global
+// loads are coalesced 16-byte pieces and the 16-byte reads of a product step (8 keys a quarter
+// warp apart by d_k + 4 floats) touch every bank once.
+#include <math.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+#include "span_records.cuh"
+
+namespace mha {
+namespace {
+
+constexpr int SS_BK = 64;
+constexpr int SS_THREADS = 256;
+constexpr int SS_PS = SS_BK + 4;  // row stride of P
+
+template <typename T, int RQ, int CV>
+struct SimtTile {
+    static constexpr int BQ = 16 * RQ;
+    static constexpr int VS = 64 * CV;
+    float *Qs, *Ks, *Vs, *Ps;
+    int ks;  // row stride of Qs and Ks
+    int dk, dk4, dv;
+    float m[RQ], l[RQ], o[RQ][4 * CV];
+
+    static size_t smem_bytes(int dk) {
+        const size_t ks = (size_t)((dk + 3) & ~3) + 4;
+        return sizeof(float) * (BQ * ks + SS_BK * ks + (size_t)SS_BK * VS + (size_t)BQ * SS_PS);
+    }
+
+    __device__ SimtTile(float* smem, int dk_, int dv_) : dk(dk_), dk4((dk_ + 3) & ~3), dv(dv_) {
+        ks = dk4 + 4;
+        Qs = smem;
+        Ks = Qs + BQ * ks;
+        Vs = Ks + SS_BK * ks;
+        Ps = Vs + SS_BK * VS;
+    }
+
+    __device__ void reset() {
+#pragma unroll
+        for (int r = 0; r < RQ; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+#pragma unroll
+            for (int u = 0; u < 4 * CV; ++u) o[r][u] = 0.f;
+        }
+    }
+
+    // 4 consecutive elements of a row, zeros past n
+    static __device__ float4 load4(const T* p, int n, bool vec) {
+        if constexpr (sizeof(T) == 4) {
+            if (vec && n >= 4) return __ldg(reinterpret_cast<const float4*>(p));
+        }
+        return make_float4(n > 0 ? (float)p[0] : 0.f, n > 1 ? (float)p[1] : 0.f, n > 2 ? (float)p[2] : 0.f, n > 3 ? (float)p[3] : 0.f);
+    }
+
+    // Row r of the query tile is at row(r), nullptr for rows that do not exist (zeros).
+    template <class F>
+    __device__ void load_q(F row, bool vec) {
+        const int n4 = dk4 / 4;
+        for (int i = (int)threadIdx.x; i < BQ * n4; i += SS_THREADS) {
+            const int r = i / n4, e = (i - r * n4) * 4;
+            const T* p = row(r);
+            *reinterpret_cast<float4*>(&Qs[r * ks + e]) =
+                p != nullptr ? load4(p + e, dk - e, vec) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
+
+    // n keys (rows past n are zero: whatever lies there never reaches a product)
+    __device__ void load_kv(const T* K, int64_t ldk, const T* V, int64_t ldv, int n, bool vec) {
+        const int k4 = dk4 / 4;
+        for (int i = (int)threadIdx.x; i < SS_BK * k4; i += SS_THREADS) {
+            const int j = i / k4, e = (i - j * k4) * 4;
+            *reinterpret_cast<float4*>(&Ks[j * ks + e]) =
+                j < n ? load4(K + j * ldk + e, dk - e, vec) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        for (int i = (int)threadIdx.x; i < SS_BK * (VS / 4); i += SS_THREADS) {
+            const int j = i / (VS / 4), e = (i - j * (VS / 4)) * 4;
+            *reinterpret_cast<float4*>(&Vs[j * VS + e]) =
+                j < n && e < dv ? load4(V + j * ldv + e, dv - e, vec) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
+
+    // One key tile: visible(row in block, key in tile); score(row in block, key in tile, s) sees
+    // every masked base-2 score.  The caller synchronises before and after.
+    template <class F, class G>
+    __device__ void step(int n, float scale_log2, F visible, G score) {
+        const int tx = (int)threadIdx.x & 15, ty = (int)threadIdx.x >> 4;
+        float sc[RQ][4];
+#pragma unroll
+        for (int r = 0; r < RQ; ++r)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) sc[r][c] = 0.f;
+#pragma unroll 2
+        for (int e = 0; e < dk4; e += 4) {
+            float4 q[RQ], k[4];
+#pragma unroll
+            for (int r = 0; r < RQ; ++r) q[r] = *reinterpret_cast<const float4*>(&Qs[(ty * RQ + r) * ks + e]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) k[c] = *reinterpret_cast<const float4*>(&Ks[(tx + 16 * c) * ks + e]);
+#pragma unroll
+            for (int r = 0; r < RQ; ++r)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    sc[r][c] = fmaf(q[r].x, k[c].x, sc[r][c]);
+                    sc[r][c] = fmaf(q[r].y, k[c].y, sc[r][c]);
+                    sc[r][c] = fmaf(q[r].z, k[c].z, sc[r][c]);
+                    sc[r][c] = fmaf(q[r].w, k[c].w, sc[r][c]);
+                }
+        }
+#pragma unroll
+        for (int r = 0; r < RQ; ++r) {
+            float tmax = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int j = tx + 16 * c;
+                sc[r][c] = j < n && visible(ty * RQ + r, j) ? sc[r][c] * scale_log2 : -INFINITY;
+                if (j < n) score(ty * RQ + r, j, sc[r][c]);
+                tmax = fmaxf(tmax, sc[r][c]);
+            }
+#pragma unroll
+            for (int off = 8; off > 0; off >>= 1) tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, off));
+            const float m_new = fmaxf(m[r], tmax);
+            float psum = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                sc[r][c] = m_new == -INFINITY ? 0.f : exp2f(sc[r][c] - m_new);  // masked: 2^-inf = 0
+                psum += sc[r][c];
+            }
+#pragma unroll
+            for (int off = 8; off > 0; off >>= 1) psum += __shfl_xor_sync(0xffffffffu, psum, off);
+            const float alpha = m_new == -INFINITY ? 1.f : exp2f(m[r] - m_new);  // 0 when m = -inf
+            l[r] = l[r] * alpha + psum;
+            m[r] = m_new;
+#pragma unroll
+            for (int u = 0; u < 4 * CV; ++u) o[r][u] *= alpha;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) Ps[(ty * RQ + r) * SS_PS + tx + 16 * c] = sc[r][c];
+        }
+        __syncwarp();  // a row's P is written and read by the same half warp
+        const int n4 = (n + 3) & ~3;  // rows past n are zero on both sides
+        for (int j = 0; j < n4; j += 4) {
+            float p[RQ][4];
+#pragma unroll
+            for (int r = 0; r < RQ; ++r) {
+                const float4 p4 = *reinterpret_cast<const float4*>(&Ps[(ty * RQ + r) * SS_PS + j]);
+                p[r][0] = p4.x; p[r][1] = p4.y; p[r][2] = p4.z; p[r][3] = p4.w;
+            }
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+                for (int c = 0; c < CV; ++c) {
+                    const float4 v = *reinterpret_cast<const float4*>(&Vs[(j + jj) * VS + c * 64 + tx * 4]);
+#pragma unroll
+                    for (int r = 0; r < RQ; ++r) {
+                        o[r][4 * c + 0] = fmaf(p[r][jj], v.x, o[r][4 * c + 0]);
+                        o[r][4 * c + 1] = fmaf(p[r][jj], v.y, o[r][4 * c + 1]);
+                        o[r][4 * c + 2] = fmaf(p[r][jj], v.z, o[r][4 * c + 2]);
+                        o[r][4 * c + 3] = fmaf(p[r][jj], v.w, o[r][4 * c + 3]);
+                    }
+                }
+        }
+    }
+};
+
+// One block = BQ query rows of one (batch, head): the sinks below the rows' windows, then the keys
+// from the first row's window to the last row.
+template <typename T, int RQ, int CV>
+__global__ void __launch_bounds__(SS_THREADS)
+    window_simt_kernel(const T* __restrict__ Q, int64_t ldq, const T* __restrict__ K, int64_t ldk,
+                       const T* __restrict__ V, int64_t ldv, const T* __restrict__ G, int64_t ldg,
+                       T* __restrict__ O, int64_t ldo, int h, int h_kv, int T_, int dk, int dv,
+                       int window, int sinks, const int32_t* __restrict__ kv_lengths, float scale_log2,
+                       bool vec, int* status) {
+    using X = SimtTile<T, RQ, CV>;
+    extern __shared__ __align__(16) float fsm[];
+    X x(fsm, dk, dv);
+    const int tid = (int)threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int b = (int)blockIdx.x / h, head = (int)blockIdx.x - b * h;
+    const int kvh = head / (h / h_kv);
+    const int q0 = (int)blockIdx.y * X::BQ;
+    const int L = kv_lengths != nullptr ? kv_lengths[b] : T_;
+    const int64_t row0 = (int64_t)b * T_ + q0;
+    if (L < 1 || L > T_) {
+        if (tid == 0) record_status(status, kStatusBadLength);
+        for (int i = tid; i < X::BQ * dv; i += SS_THREADS) {
+            const int r = i / dv;
+            if (q0 + r < T_) O[(row0 + r) * ldo + (int64_t)head * dv + (i - r * dv)] = (T)NAN;
+        }
+        return;
+    }
+    x.load_q([&](int r) { return q0 + r < T_ ? Q + (row0 + r) * ldq + (int64_t)head * dk : nullptr; }, vec);
+    x.reset();
+    const T* Kb = K + (int64_t)b * T_ * ldk + (int64_t)kvh * dk;
+    const T* Vb = V + (int64_t)b * T_ * ldv + (int64_t)kvh * dv;
+    const int end = min(L, q0 + X::BQ);
+    int lo = max(0, q0 - window + 1);
+    int s_end = min(sinks, L);  // sinks below the windows
+    if (s_end >= lo) s_end = lo = 0;
+    for (int part = 0; part < 2; ++part) {
+        const int k_end = part == 0 ? s_end : end;
+        for (int k0 = part == 0 ? 0 : lo; k0 < k_end; k0 += SS_BK) {
+            const int n = min(SS_BK, k_end - k0);
+            __syncthreads();  // the previous tile is no longer read
+            x.load_kv(Kb + k0 * ldk, ldk, Vb + k0 * ldv, ldv, n, vec);
+            __syncthreads();
+            x.step(n, scale_log2,
+                   [&](int r, int j) {
+                       const int i = q0 + r, key = k0 + j;
+                       return key <= i && (i - key < window || key < sinks);
+                   },
+                   [](int, int, float) {});
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < RQ; ++r) {
+        const int t = ty * RQ + r;
+        if (q0 + t >= T_) continue;
+        const float inv = x.l[r] > 0.f ? 1.f / x.l[r] : 0.f;  // nothing visible: zeros
+#pragma unroll
+        for (int u = 0; u < 4 * CV; ++u) {
+            const int e = (u >> 2) * 64 + tx * 4 + (u & 3);
+            if (e >= dv) continue;
+            float y = x.o[r][u] * inv;
+            if (G != nullptr) y *= 1.f / (1.f + expf(-(float)G[(row0 + t) * ldg + (int64_t)head * dv + e]));
+            O[(row0 + t) * ldo + (int64_t)head * dv + e] = (T)y;
+        }
+    }
+}
+
+template <typename T, int RQ, int CV>
+__global__ void __launch_bounds__(SS_THREADS)
+    span_simt_kernel(const SpanShape p, const SpanRecords rec, const T* __restrict__ Q, int64_t ldq,
+                     const T* __restrict__ K, int64_t ldk, const T* __restrict__ V, int64_t ldv,
+                     const T* __restrict__ Kp, int64_t ldkp, const T* __restrict__ Vp, int64_t ldvp,
+                     T* __restrict__ O, int64_t ldo, int dk, int dv,
+                     const int32_t* __restrict__ lengths, float* __restrict__ scores, float scale_log2,
+                     bool vec, int* status) {
+    using X = SimtTile<T, RQ, CV>;
+    extern __shared__ __align__(16) float fsm[];
+    X x(fsm, dk, dv);
+    const int tid = (int)threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const SpanStart start = span_start<SS_BK, SS_THREADS>(p, lengths);
+    if (blockIdx.x == 0)
+        for (int b = tid; b < p.B; b += SS_THREADS)
+            if (lengths[b] < p.T_q || lengths[b] > p.T_max) record_status(status, kStatusBadLength);
+    SpanWalk<SS_BK> walk(p, lengths, start);
+    SpanPiece q;
+    const int64_t groups_p = p.T_p > 0 ? (int64_t)p.h_kv * p.nrbp : 0;
+    while (walk.next(q)) {
+        const int r0 = q.rb * X::BQ;
+        const int nr = min(X::BQ, (q.prefix ? p.B * p.rows : p.rows) - r0);
+        // batch, head and new token of row r of the block
+        auto where = [&](int r, int& b, int& head, int& t) {
+            int rr = r0 + r;
+            b = q.b;
+            if (q.prefix) {
+                b = rr / p.rows;
+                rr -= b * p.rows;
+            }
+            head = q.g * p.per + rr / p.T_q;
+            t = rr % p.T_q;
+        };
+        __syncthreads();  // the previous piece's tiles are no longer read
+        x.load_q([&](int r) -> const T* {
+            if (r >= nr) return nullptr;
+            int b, head, t;
+            where(r, b, head, t);
+            return Q + ((int64_t)b * p.T_q + t) * ldq + (int64_t)head * dk;
+        }, vec);
+        x.reset();
+        const T* Kb = q.prefix ? Kp + (int64_t)q.g * dk : K + (int64_t)q.b * p.T_max * ldk + (int64_t)q.g * dk;
+        const T* Vb = q.prefix ? Vp + (int64_t)q.g * dv : V + (int64_t)q.b * p.T_max * ldv + (int64_t)q.g * dv;
+        const int64_t lk = q.prefix ? ldkp : ldk, lv = q.prefix ? ldvp : ldv;
+        for (int i = q.i0; i < q.i1; ++i) {
+            int k0, n;
+            span_tile<SS_BK>(q.v, i, k0, n);
+            __syncthreads();
+            x.load_kv(Kb + k0 * lk, lk, Vb + k0 * lv, lv, n, vec);
+            __syncthreads();
+            x.step(n, scale_log2,
+                   [&](int r, int j) {
+                       return q.prefix || span_visible(p, q.v.L - p.T_q + (r0 + r) % p.T_q, k0 + j);
+                   },
+                   [&](int r, int j, float s) {
+                       if (scores != nullptr && r < nr)
+                           scores[(((int64_t)q.b * p.h_kv + q.g) * p.rows + r0 + r) * p.T_max + k0 + j] = s;
+                   });
+        }
+        const bool direct = p.T_p == 0 && q.whole();
+        const int64_t slot = rec.row(q.prefix, groups_p, q.group, (int)blockIdx.x);
+#pragma unroll
+        for (int r = 0; r < RQ; ++r) {
+            const int rr = ty * RQ + r;
+            if (rr >= nr) continue;
+            if (tx == 0 && (!direct || scores != nullptr)) rec.ml[slot + rr] = make_float2(x.m[r], x.l[r]);
+            float* part = rec.o + (slot + rr) * dv;
+            int b, head, t;
+            where(rr, b, head, t);
+            T* out = O + ((int64_t)b * p.T_q + t) * ldo + (int64_t)head * dv;
+            const float inv = 1.f / x.l[r];
+#pragma unroll
+            for (int u = 0; u < 4 * CV; ++u) {
+                const int e = (u >> 2) * 64 + tx * 4 + (u & 3);
+                if (e >= dv) continue;
+                if (direct)
+                    out[e] = (T)(x.o[r][u] * inv);
+                else
+                    part[e] = x.o[r][u];
+            }
+        }
+    }
+}
+
+}  // namespace
+
+int span_simt_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+template <typename E>
+static cudaError_t launch_window(const E* Q, int64_t ldq, const E* K, int64_t ldk, const E* V,
+                              int64_t ldv, const E* G, int64_t ldg, E* O, int64_t ldo, int B, int h,
+                              int h_kv, int T, int d_k, int d_v, int window, int sinks,
+                              const int32_t* kv_lengths, int* status, cudaStream_t stream) {
+    auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+    const bool vec = al(Q) && al(K) && al(V) && ldq % 4 == 0 && ldk % 4 == 0 && ldv % 4 == 0 && d_k % 4 == 0 && d_v % 4 == 0;
+    const float scale = (float)(1.4426950408889634 / sqrt((double)d_k));
+    const bool small = (int64_t)B * h * ((T + 63) / 64) < 256;  // 32-row blocks where 64-row ones leave SMs idle
+    const int cv = (d_v + 63) / 64;
+    auto launch = [&](auto kernel, size_t smem, int bq) {
+        cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (err != cudaSuccess) return err;
+        kernel<<<dim3((unsigned)(B * h), (unsigned)((T + bq - 1) / bq)), SS_THREADS, smem, stream>>>(
+            Q, ldq, K, ldk, V, ldv, G, ldg, O, ldo, h, h_kv, T, d_k, d_v, window, sinks, kv_lengths, scale, vec,
+            status);
+        return cudaGetLastError();
+    };
+#define MHA_WS(RQ, CV) \
+    if ((small ? 2 : 4) == RQ && cv == CV) \
+        return launch(window_simt_kernel<E, RQ, CV>, SimtTile<E, RQ, CV>::smem_bytes(d_k), 16 * RQ);
+    MHA_WS(2, 1) MHA_WS(2, 2) MHA_WS(2, 3) MHA_WS(2, 4) MHA_WS(4, 1) MHA_WS(4, 2) MHA_WS(4, 3) MHA_WS(4, 4)
+#undef MHA_WS
+    return cudaErrorInvalidValue;
+}
+
+template <typename E>
+static cudaError_t launch_span(const SpanShape& p, const SpanRecords& rec, int bm, const E* Q, int64_t ldq,
+                            const E* K, int64_t ldk, const E* V, int64_t ldv, const E* Kp,
+                            int64_t ldkp, const E* Vp, int64_t ldvp, E* O, int64_t ldo, int d_k, int d_v,
+                            const int32_t* lengths, float* scores, int num_sms, int* grid, int* status,
+                            cudaStream_t stream) {
+    auto al = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
+    const bool vec = al(Q) && al(K) && al(V) && ldq % 4 == 0 && ldk % 4 == 0 && ldv % 4 == 0 && d_k % 4 == 0 &&
+                     d_v % 4 == 0 && (p.T_p == 0 || (al(Kp) && al(Vp) && ldkp % 4 == 0 && ldvp % 4 == 0));
+    const float scale = (float)(1.4426950408889634 / sqrt((double)d_k));
+    const int cv = (d_v + 63) / 64;
+    auto launch = [&](auto kernel, size_t smem) {
+        cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (err != cudaSuccess) return err;
+        *grid = 2 * num_sms < kSpanMaxCtas ? 2 * num_sms : kSpanMaxCtas;
+        kernel<<<dim3((unsigned)*grid), SS_THREADS, smem, stream>>>(p, rec, Q, ldq, K, ldk, V, ldv, Kp, ldkp, Vp,
+                                                                   ldvp, O, ldo, d_k, d_v, lengths, scores, scale,
+                                                                   vec, status);
+        return cudaGetLastError();
+    };
+#define MHA_SS(RQ, CV) \
+    if (bm == 16 * RQ && cv == CV) return launch(span_simt_kernel<E, RQ, CV>, SimtTile<E, RQ, CV>::smem_bytes(d_k));
+    MHA_SS(1, 1) MHA_SS(1, 2) MHA_SS(1, 3) MHA_SS(1, 4) MHA_SS(2, 1) MHA_SS(2, 2) MHA_SS(2, 3) MHA_SS(2, 4)
+    MHA_SS(4, 1) MHA_SS(4, 2) MHA_SS(4, 3) MHA_SS(4, 4)
+#undef MHA_SS
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_window_f32(const float* Q, int64_t ldq, const float* K, int64_t ldk, const float* V,
+                              int64_t ldv, const float* G, int64_t ldg, float* O, int64_t ldo, int B, int h,
+                              int h_kv, int T, int d_k, int d_v, int window, int sinks,
+                              const int32_t* kv_lengths, int* status, cudaStream_t stream) {
+    return launch_window(Q, ldq, K, ldk, V, ldv, G, ldg, O, ldo, B, h, h_kv, T, d_k, d_v, window, sinks, kv_lengths,
+                         status, stream);
+}
+
+cudaError_t launch_window_bf16(const void* Q, int64_t ldq, const void* K, int64_t ldk, const void* V,
+                               int64_t ldv, const void* G, int64_t ldg, void* O, int64_t ldo, int B, int h,
+                               int h_kv, int T, int d, int window, int sinks, const int32_t* kv_lengths,
+                               int, int* status, cudaStream_t stream) {
+    auto f = [](const void* x) { return static_cast<const __nv_bfloat16*>(x); };
+    return launch_window(f(Q), ldq, f(K), ldk, f(V), ldv, f(G), ldg, static_cast<__nv_bfloat16*>(O), ldo, B, h, h_kv, T,
+                         d, d, window, sinks, kv_lengths, status, stream);
+}
+
+cudaError_t launch_span_f32(const SpanShape& p, const SpanRecords& rec, int bm, const float* Q, int64_t ldq,
+                            const float* K, int64_t ldk, const float* V, int64_t ldv, const float* Kp,
+                            int64_t ldkp, const float* Vp, int64_t ldvp, float* O, int64_t ldo, int d_k, int d_v,
+                            const int32_t* lengths, float* scores, int num_sms, int* grid, int* status,
+                            cudaStream_t stream) {
+    return launch_span(p, rec, bm, Q, ldq, K, ldk, V, ldv, Kp, ldkp, Vp, ldvp, O, ldo, d_k, d_v, lengths, scores,
+                       num_sms, grid, status, stream);
+}
+
+cudaError_t launch_span_bf16(const SpanShape& p, const SpanRecords& rec, int bm, const void* Q, int64_t ldq,
+                             const void* K, int64_t ldk, const void* V, int64_t ldv, const void* Kp, int64_t ldkp,
+                             const void* Vp, int64_t ldvp, void* O, int64_t ldo, int d, const int32_t* lengths,
+                             float* scores, int num_sms, int* grid, int* status, cudaStream_t stream) {
+    auto f = [](const void* x) { return static_cast<const __nv_bfloat16*>(x); };
+    return launch_span(p, rec, bm, f(Q), ldq, f(K), ldk, f(V), ldv, f(Kp), ldkp, f(Vp), ldvp,
+                       static_cast<__nv_bfloat16*>(O), ldo, d, d, lengths, scores, num_sms, grid, status, stream);
+}
+
+}  // namespace mha

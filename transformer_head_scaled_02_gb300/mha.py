@@ -50,6 +50,8 @@ class Mha:
         self.handle = _lib.mha_create_ex(D, h, self.h_kv, d_k, self.d_v, int(self.gated),
                                          _DTYPES[dtype])
         self._ws: Optional[torch.Tensor] = None
+        self._ws_captured = False
+        self._kept_ws: list = []
 
     @property
     def proj_width(self) -> int:
@@ -70,8 +72,13 @@ class Mha:
     def ensure_workspace(self, B: int, T_q: int, T_kv: int, need: Optional[int] = None) -> torch.Tensor:
         need = self.workspace_size(B, T_q, T_kv) if need is None else need
         if self._ws is None or self._ws.numel() < need:
+            if self._ws_captured:  # a captured graph still launches into the one it was captured with
+                self._kept_ws.append(self._ws)
+                self._ws_captured = False
             self._ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
             _lib.mha_set_workspace(self.handle, self._ws.data_ptr(), self._ws.numel())
+        if not self._ws_captured and torch.cuda.is_current_stream_capturing():
+            self._ws_captured = True
         return self._ws
 
     def status(self) -> int:
@@ -92,9 +99,16 @@ class Mha:
                 W_o: torch.Tensor, b_o: Optional[torch.Tensor], X_kv: Optional[torch.Tensor] = None,
                 causal: bool = False, kv_lengths: Optional[torch.Tensor] = None,
                 out: Optional[torch.Tensor] = None,
-                residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+                residual: Optional[torch.Tensor] = None, window: Optional[int] = None,
+                sinks: int = 0) -> torch.Tensor:
+        """The whole layer.  With ``window`` (self-attention, causal=True): row i sees only the last
+        ``window`` keys and the first ``sinks`` of its sequence (see attention_window)."""
         B, T_q, D = X_q.shape
         T_kv = T_q if X_kv is None else X_kv.shape[1]
+        if window is None and sinks:
+            raise ValueError("sinks need a window")
+        if window is not None and (X_kv is not None or not causal):
+            raise ValueError("a window needs causal self-attention")
         ncols = self.proj_width
         self._check("X_q", X_q, (B, T_q, self.D))
         self._check("X_kv", X_kv, None if X_kv is None else (B, T_kv, self.D))
@@ -110,6 +124,11 @@ class Mha:
         self._check("out", out, (B, T_q, self.D))
         self._check("residual", residual, None if residual is None else (B, T_q, self.D))
         self.ensure_workspace(B, T_q, T_kv)
+        if window is not None:
+            _lib.mha_forward_window(self.handle, _ptr(X_q), B, T_q, _ptr(W_qkv), _ptr(b_qkv), _ptr(W_o),
+                                    _ptr(b_o), window, sinks, _ptr(kv_lengths), _ptr(residual),
+                                    _ptr(out), _stream())
+            return out
         _lib.mha_forward_ex(self.handle, _ptr(X_q), _ptr(X_kv), B, T_q, T_kv, _ptr(W_qkv),
                             _ptr(b_qkv), _ptr(W_o), _ptr(b_o), causal, _ptr(kv_lengths),
                             _ptr(residual), _ptr(out), _stream())
@@ -267,3 +286,152 @@ class Mha:
                         K_cache.stride(1), _ptr(V_cache), V_cache.stride(1), _ptr(cache_lengths),
                         _ptr(out), out.stride(1), _stream())
         return out
+
+    # ------------------------------------------------------------ long contexts
+    def _rows(self, name: str, t: torch.Tensor, B: int, T: int, width: int) -> int:
+        """Check a (B, T, width) view whose rows lie one stride apart throughout; returns the stride."""
+        if tuple(t.shape) != (B, T, width):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(B, T, width)}")
+        s0, s1, s2 = t.stride()
+        ld = s0 if T == 1 and B > 1 else s1
+        if t.dtype != self.dtype or s2 != 1 or (B > 1 and T > 1 and s0 != T * s1):
+            raise ValueError(f"{name} must be a (B,T,*) {self.dtype} view with contiguous rows and "
+                             "batches")
+        # a single row (or an empty view) has no second one: any stride of at least a row will do
+        return ld if B * T > 1 else max(ld, width)
+
+    def _device(self, first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
+        """All on one CUDA device, the current one; returns its current stream."""
+        dev = first.device
+        if dev.type != "cuda" or any(t is not None and t.device != dev for t in others):
+            raise ValueError("all tensors must be on one CUDA device")
+        if dev.index != torch.cuda.current_device():
+            raise ValueError(f"the tensors are on {dev}, which is not the current device")
+        return torch.cuda.current_stream(dev).cuda_stream
+
+    @staticmethod
+    def _ints(name: str, t: torch.Tensor, B: int) -> int:
+        if t.dtype != torch.int32 or t.shape != (B,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA int32 tensor of length {B}")
+        return t.data_ptr()
+
+    @staticmethod
+    def _weights(name: str, t: torch.Tensor, shape) -> int:
+        if t.dtype != torch.float32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA float32 tensor of shape {tuple(shape)}")
+        return t.data_ptr()
+
+    def attention_window(self, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, window: int,
+                         sinks: int = 0, kv_lengths: Optional[torch.Tensor] = None,
+                         out: Optional[torch.Tensor] = None,
+                         G: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Causal sliding-window attention over (B, T, width) views: row i sees key j iff j <= i,
+        j < L_b and (i - j < window or j < sinks); rows that see nothing (padding only) are zero.
+        Heads, gate and views as in attention().  Returns Ocat (B, T, h*d_v)."""
+        B, T, _ = Q.shape
+        ldq = self._rows("Q", Q, B, T, self.h * self.d_k)
+        ldk = self._rows("K", K, B, T, self.h_kv * self.d_k)
+        ldv = self._rows("V", V, B, T, self.h_kv * self.d_v)
+        if out is None:
+            out = torch.empty((B, T, self.h * self.d_v), dtype=self.dtype, device=Q.device)
+        ldo = self._rows("out", out, B, T, self.h * self.d_v)
+        ldg = 0 if G is None else self._rows("G", G, B, T, self.h * self.d_v)
+        lens = None if kv_lengths is None else self._ints("kv_lengths", kv_lengths, B)
+        stream = self._device(Q, K, V, out, G, kv_lengths)
+        _lib.mha_attention_window(self.handle, B, T, Q.data_ptr(), ldq, K.data_ptr(), ldk, V.data_ptr(),
+                                  ldv, _ptr(G), ldg, window, sinks, lens, out.data_ptr(), ldo, stream)
+        return out
+
+    def _cache_step(self, Q, K_cache, V_cache, cache_lengths, out, T_prefix, weights, *others):
+        """Checks and workspace that the cache steps share: (out, the arguments they have in common)."""
+        B, T_q, _ = Q.shape
+        T_max = K_cache.shape[1]
+        ldq = self._rows("Q", Q, B, T_q, self.h * self.d_k)
+        ldk = self._rows("K_cache", K_cache, B, T_max, self.h_kv * self.d_k)
+        ldv = self._rows("V_cache", V_cache, B, T_max, self.h_kv * self.d_v)
+        if out is None:
+            out = torch.empty((B, T_q, self.h * self.d_v), dtype=self.dtype, device=Q.device)
+        ldo = self._rows("out", out, B, T_q, self.h * self.d_v)
+        lens = self._ints("cache_lengths", cache_lengths, B)
+        stream = self._device(Q, K_cache, V_cache, cache_lengths, out, *others)
+        self.ensure_workspace(B, T_q, T_max, need=_lib.mha_cache_step_workspace_size(
+            self.handle, B, T_q, T_prefix, T_max, weights))
+        cache = (Q.data_ptr(), ldq, K_cache.data_ptr(), ldk, V_cache.data_ptr(), ldv)
+        return out, (B, T_q, T_max), cache, lens, (out.data_ptr(), ldo, stream)
+
+    def decode_window(self, Q: torch.Tensor, K_cache: torch.Tensor, V_cache: torch.Tensor,
+                      cache_lengths: torch.Tensor, window: int, sinks: int = 0,
+                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """decode() under a sliding window: the new token at position p of its cache sees keys j <= p
+        with p - j < window or j < sinks, and only those are read."""
+        out, sizes, cache, lens, tail = self._cache_step(Q, K_cache, V_cache, cache_lengths, out, 0, 0)
+        _lib.mha_decode_window(self.handle, *sizes, *cache, window, sinks, lens, *tail)
+        return out
+
+    def decode_shared(self, Q: torch.Tensor, K_prefix: torch.Tensor, V_prefix: torch.Tensor,
+                      K_cache: torch.Tensor, V_cache: torch.Tensor, cache_lengths: torch.Tensor,
+                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """One decode step of a batch that shares its first tokens: K_prefix (T_prefix, h_kv*d_k view)
+        and V_prefix (T_prefix, h_kv*d_v view) are stored and read once for the whole batch; the
+        caches and cache_lengths hold each sequence's own tokens after them, the new ones included."""
+        T_p = K_prefix.shape[0]
+        ldkp = self._rows("K_prefix", K_prefix.unsqueeze(0), 1, T_p, self.h_kv * self.d_k)
+        ldvp = self._rows("V_prefix", V_prefix.unsqueeze(0), 1, T_p, self.h_kv * self.d_v)
+        out, (B, T_q, T_max), cache, lens, tail = self._cache_step(
+            Q, K_cache, V_cache, cache_lengths, out, T_p, 0, K_prefix, V_prefix)
+        _lib.mha_decode_shared(self.handle, B, T_q, T_p, K_prefix.data_ptr(), ldkp, V_prefix.data_ptr(),
+                               ldvp, T_max, *cache, lens, *tail)
+        return out
+
+    def decode_weights(self, Q: torch.Tensor, K_cache: torch.Tensor, V_cache: torch.Tensor,
+                       cache_lengths: torch.Tensor, weights: torch.Tensor,
+                       out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """decode() that also adds, to ``weights`` (float32 (B, h_kv, T_max)), the softmax weight each
+        cached token receives from the step, summed over its group's query heads and the new tokens;
+        the new tokens' own entries are written, not added to."""
+        w = self._weights("weights", weights, (Q.shape[0], self.h_kv, K_cache.shape[1]))
+        out, sizes, cache, lens, tail = self._cache_step(Q, K_cache, V_cache, cache_lengths, out, 0, 1,
+                                                         weights)
+        _lib.mha_decode_weights(self.handle, *sizes, *cache, lens, w, *tail)
+        return out
+
+    def evict(self, K_cache: torch.Tensor, V_cache: torch.Tensor, cache_lengths: torch.Tensor,
+              weights: torch.Tensor, keep: int, recent: int, K_out: Optional[torch.Tensor] = None,
+              V_out: Optional[torch.Tensor] = None, weights_out: Optional[torch.Tensor] = None,
+              lengths_out: Optional[torch.Tensor] = None):
+        """Cut every sequence to at most ``keep`` tokens per K/V head: the last ``recent`` and the
+        earlier ones of largest ``weights`` (decode_weights accumulates them), in their order.  The
+        outputs may be new buffers of T_out >= keep rows (the default: exactly keep, rows past the new
+        length unset) or, all three, the inputs themselves (in place).  Returns (K_out, V_out,
+        lengths_out, weights_out, kept): kept (int32 (B, h_kv, keep)) holds the kept tokens' indices,
+        then -1."""
+        B, T_max, _ = K_cache.shape
+        wk, wv = self.h_kv * self.d_k, self.h_kv * self.d_v
+        ldk = self._rows("K_cache", K_cache, B, T_max, wk)
+        ldv = self._rows("V_cache", V_cache, B, T_max, wv)
+        w = self._weights("weights", weights, (B, self.h_kv, T_max))
+        lens = self._ints("cache_lengths", cache_lengths, B)
+        if keep < 1:
+            raise ValueError("keep must be at least 1")
+        dev = K_cache.device
+        T_out = keep if K_out is None else K_out.shape[1]
+        if K_out is None:
+            K_out = torch.empty((B, T_out, wk), dtype=self.dtype, device=dev)
+        if V_out is None:
+            V_out = torch.empty((B, T_out, wv), dtype=self.dtype, device=dev)
+        if weights_out is None:
+            weights_out = torch.empty((B, self.h_kv, T_out), dtype=torch.float32, device=dev)
+        if lengths_out is None:
+            lengths_out = torch.empty_like(cache_lengths)
+        kept = torch.empty((B, self.h_kv, keep), dtype=torch.int32, device=dev)
+        ldko = self._rows("K_out", K_out, B, T_out, wk)
+        ldvo = self._rows("V_out", V_out, B, T_out, wv)
+        wo = self._weights("weights_out", weights_out, (B, self.h_kv, T_out))
+        lo = self._ints("lengths_out", lengths_out, B)
+        stream = self._device(K_cache, V_cache, cache_lengths, weights, K_out, V_out, weights_out, lengths_out)
+        if self._ws is None:
+            self.ensure_workspace(0, 0, 0, need=256)  # the status word
+        _lib.mha_cache_evict(self.handle, B, T_max, keep, recent, K_cache.data_ptr(), ldk,
+                             V_cache.data_ptr(), ldv, lens, w, T_out, K_out.data_ptr(), ldko,
+                             V_out.data_ptr(), ldvo, wo, kept.data_ptr(), lo, stream)
+        return K_out, V_out, lengths_out, weights_out, kept
