@@ -4,14 +4,20 @@
 // The query rows that share cached keys form groups: one per (batch, K/V head, row block) over the
 // batch's own cache, and, with a shared prefix, one per (K/V head, row block) over the prefix, whose
 // rows are those of the whole batch.  A group's visible keys are at most two ranges, the sinks
-// [0, s) and the window [lo, L), each cut into tiles.  All groups' tiles in order form one
-// sequence, which D = min(G, N) of the G CTAs divide evenly: CTA c takes tiles [N c / D, N (c + 1) / D),
-// so ragged lengths and group counts that do not divide the SMs leave no CTA idle.  A CTA's run
-// crosses group borders; each crossing starts a piece.  A piece that holds a whole group writes its
-// output itself; the others leave (maximum, sum, weighted values) records that the merge joins:
+// [0, s) and the window [lo, L), each cut into tiles.
+//
+// The CTAs work in gangs of H: the member CTAs of a gang walk the same tiles of H neighbouring lanes
+// (K/V head, row block) side by side.  A cached token's rows of all heads lie side by side, so what a
+// gang reads at a time is whole pieces of DRAM pages: 32 sequences of 16 heads with d = 128 ran at 54% of
+// the copy bandwidth without gangs (each CTA somewhere else, 256 bytes at a time).  The tiles of
+// all batches and lane blocks in order form one sequence of N, which D = min(gangs, N) gangs divide
+// evenly: gang c takes tiles [N c / D, N (c + 1) / D), so ragged lengths and group counts that do not
+// divide the SMs leave no CTA idle.  A gang's run crosses group borders; each crossing starts a piece.
+// A piece that holds a whole group writes its output itself; the others leave (maximum, sum, weighted
+// values) records that the merge joins:
 //   O = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p,  M = max_p m_p   (scores in base 2).
-// Record slot of a piece: CTA index + group index.  Both only grow along the sequence and one of
-// them does at every piece, so slots are distinct.
+// Record slot of a piece: (gang + block index in the sequence) H + member.  Gang and block only grow
+// along the sequence and one of them does at every piece, so slots are distinct.
 #pragma once
 
 #include <stdint.h>
@@ -32,7 +38,18 @@ struct SpanShape {
     int nrbp;    // row blocks of the B * rows rows over the prefix
     int window;  // <= T_max; T_max: no window
     int sinks;
+    int gang;    // H: divides h_kv * nrb and h_kv * nrbp
+
+    __host__ __device__ int blocks_c() const { return h_kv * nrb / gang; }   // lane blocks of a batch
+    __host__ __device__ int blocks_p() const { return h_kv * nrbp / gang; }  // of the prefix
 };
+
+// The largest gang that leaves at most 3% of the CTAs without one.
+inline int span_gang(const SpanShape& p, int ctas) {
+    for (int H = p.h_kv * p.nrb; H > 1; --H)
+        if (p.h_kv * p.nrb % H == 0 && p.h_kv * p.nrbp % H == 0 && ctas / H * H * 100 >= ctas * 97) return H;
+    return 1;
+}
 
 // The visible keys of a batch with L cached tokens: [0, s_keys) and [lo, L); nt tiles in all (0 for
 // an invalid length).
@@ -78,41 +95,99 @@ __host__ __device__ inline int span_prefix_tiles(const SpanShape& p) {
     return (p.T_p + TILE - 1) / TILE;
 }
 
-// CTAs that share N tiles when G are launched: each of them holds at least one.
-__host__ __device__ inline int64_t span_parts(int64_t N, int G) { return N < G ? N : G; }
+// Gangs that share N tiles when G are launched: each of them holds at least one.
+__host__ __device__ inline int span_parts(int N, int G) { return N < G ? N : G; }
 
-// CTAs [c0, c1] that hold tiles [t0, t1) of N when a grid of G divides them.
-__device__ __forceinline__ void span_ctas(int64_t N, int G, int64_t t0, int64_t t1, int& c0, int& c1) {
+// Gangs [c0, c1] that hold tiles [t0, t1) of N when G divide them.
+__device__ __forceinline__ void span_gangs(int N, int G, int t0, int t1, int& c0, int& c1) {
     const int64_t D = span_parts(N, G);
     c0 = (int)(((t0 + 1) * D - 1) / N);
     c1 = (int)((t1 * D - 1) / N);
 }
 
-// Where a CTA starts in the tile sequence.
+// Tiles of one lane's sequence if every batch had the longest cache (the host checks that they fit 32
+// bits and launches no more gangs).
+template <int TILE>
+inline int64_t span_most_tiles(const SpanShape& p) {
+    const int64_t all = ((int64_t)p.T_max + TILE - 1) / TILE;
+    const int64_t win = ((int64_t)p.sinks + TILE - 1) / TILE + ((int64_t)p.window + p.T_q - 1 + TILE - 1) / TILE;
+    return (int64_t)span_prefix_tiles<TILE>(p) * p.blocks_p() + (int64_t)p.B * p.blocks_c() * (all < win ? all : win);
+}
+
+// Where a gang starts in the tile sequence.
 struct SpanStart {
-    int64_t N;       // tiles in all
-    int64_t t0, t1;  // this CTA's tiles
-    int b;           // batch that holds the CTA's first tile past the prefix
-    int64_t off;     // first tile of that batch's groups
+    int N;       // tiles in all
+    int t0, t1;  // this gang's tiles
+    int b;       // batch that holds the gang's first tile past the prefix
+    int off;     // first tile of that batch's lane blocks
 };
+
+// The sequence as seen from its prefix sums over the batches: all lanes of a warp call it and get N, the
+// batch that holds tile want(N) (of the batches' own tiles) and that batch's first tile.  A lane sums a
+// run of consecutive batches; loads only, no block-wide step.
+template <int TILE, typename F>
+__device__ __forceinline__ void span_find(const SpanShape& p, const int32_t* lengths, F want, int& N, int& b, int& off) {
+    const int lane = (int)threadIdx.x & 31;
+    const int run = (p.B + 31) / 32, i0 = lane * run, i1 = min(p.B, i0 + run);
+    const int npt = span_prefix_tiles<TILE>(p) * p.blocks_p();
+    int sum = 0;
+    for (int i = i0; i < i1; ++i) sum += span_view<TILE>(p, lengths[i]).nt * p.blocks_c();
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+    }
+    N = npt + __shfl_sync(0xffffffffu, inc, 31);
+    const int t = want(N);
+    int before = npt + inc - sum, found = 0;
+    const bool mine = before <= t && t < before + sum;
+    if (mine)
+        for (int i = i0; i < i1; ++i) {
+            const int n = span_view<TILE>(p, lengths[i]).nt * p.blocks_c();
+            if (t < before + n) {
+                found = i;
+                break;
+            }
+            before += n;
+        }
+    const unsigned who = __ballot_sync(0xffffffffu, mine);
+    const int src = who ? __ffs(who) - 1 : 0;
+    b = __shfl_sync(0xffffffffu, found, src);
+    off = __shfl_sync(0xffffffffu, before, src);
+}
+
+// This gang's share of the sequence; all lanes of a warp call it.
+template <int TILE>
+__device__ __forceinline__ SpanStart span_start(const SpanShape& p, const int32_t* lengths) {
+    const int gangs = (int)gridDim.x / p.gang, c = (int)blockIdx.x / p.gang;
+    const int npt = span_prefix_tiles<TILE>(p) * p.blocks_p();
+    SpanStart s;
+    span_find<TILE>(p, lengths, [&](int N) {
+        const int D = span_parts(N, gangs);
+        s.t0 = c < D ? (int)((int64_t)N * c / D) : N;
+        s.t1 = c < D ? (int)((int64_t)N * (c + 1) / D) : N;
+        return max(s.t0, npt);
+    }, s.N, s.b, s.off);
+    return s;
+}
 
 // One contiguous run of tiles within one group.
 struct SpanPiece {
     bool prefix;
     int b, g, rb;
-    int64_t group;  // index among all groups
-    int i0, i1;     // tiles [i0, i1) of the group
-    SpanView v;     // the batch's view (prefix: L = T_p, one range)
+    int block;   // lane block's index in the sequence
+    int i0, i1;  // tiles [i0, i1) of the group
+    SpanView v;  // the batch's view (prefix: L = T_p, one range)
     __device__ bool whole() const { return i0 == 0 && i1 == v.nt; }
 };
 
-// Walks a CTA's pieces in order.
+// Walks a gang's pieces in order.
 template <int TILE>
 struct SpanWalk {
     const SpanShape& p;
     const int32_t* lengths;
-    int64_t t, t1, off;
-    int b;
+    int t, t1, off, b;
 
     __device__ SpanWalk(const SpanShape& p_, const int32_t* lengths_, const SpanStart& s)
         : p(p_), lengths(lengths_), t(s.t0), t1(s.t1), off(s.off), b(s.b) {}
@@ -120,125 +195,41 @@ struct SpanWalk {
     __device__ bool next(SpanPiece& q) {
         if (t >= t1) return false;
         const int np = span_prefix_tiles<TILE>(p);
-        const int64_t npt = (int64_t)np * p.h_kv * p.nrbp;
-        int64_t in;  // tile within the group
-        if (t < npt) {
+        const int member = (int)blockIdx.x % p.gang;
+        int in;  // tile within the group
+        int lane;
+        if (t < np * p.blocks_p()) {
             q.prefix = true;
-            q.group = t / np;
-            in = t - q.group * np;
+            q.block = t / np;
+            in = t - q.block * np;
             q.b = 0;
-            q.g = (int)(q.group / p.nrbp);
-            q.rb = (int)(q.group - (int64_t)q.g * p.nrbp);
+            lane = q.block * p.gang + member;
+            q.g = lane / p.nrbp;
+            q.rb = lane - q.g * p.nrbp;
             q.v.L = p.T_p;
             q.v.s_keys = q.v.lo = q.v.nst = 0;
             q.v.nt = np;
         } else {
             q.prefix = false;
             q.v = span_view<TILE>(p, lengths[b]);
-            while (t >= off + (int64_t)q.v.nt * p.h_kv * p.nrb) {  // the next batch (some hold no tile)
-                off += (int64_t)q.v.nt * p.h_kv * p.nrb;
+            while (t - off >= q.v.nt * p.blocks_c()) {  // the next batch (some hold no tile)
+                off += q.v.nt * p.blocks_c();
                 ++b;
                 q.v = span_view<TILE>(p, lengths[b]);
             }
-            const int gr = (int)((t - off) / q.v.nt);
-            in = t - off - (int64_t)gr * q.v.nt;
+            const int bl = (t - off) / q.v.nt;
+            in = t - off - bl * q.v.nt;
             q.b = b;
-            q.g = gr / p.nrb;
-            q.rb = gr - q.g * p.nrb;
-            q.group = (int64_t)p.h_kv * p.nrbp + (int64_t)b * p.h_kv * p.nrb + gr;
+            lane = bl * p.gang + member;
+            q.g = lane / p.nrb;
+            q.rb = lane - q.g * p.nrb;
+            q.block = p.blocks_p() + b * p.blocks_c() + bl;
         }
-        q.i0 = (int)in;
-        const int64_t left = t1 - t;
-        q.i1 = left < q.v.nt - in ? (int)(in + left) : q.v.nt;
+        q.i0 = in;
+        q.i1 = t1 - t < q.v.nt - in ? in + t1 - t : q.v.nt;
         t += q.i1 - q.i0;
         return true;
     }
 };
-
-// First tile of batch b's groups and the number of tiles in all; every thread of the block (of
-// THREADS) calls it and gets the answer.
-template <int TILE, int THREADS>
-__device__ inline void span_offset(const SpanShape& p, const int32_t* lengths, int b, int64_t& off,
-                                   int64_t& total) {
-    const int64_t npt = (int64_t)span_prefix_tiles<TILE>(p) * p.h_kv * p.nrbp;
-    int64_t below = 0, all = 0;
-    for (int i = (int)threadIdx.x; i < p.B; i += THREADS) {
-        const int64_t n = (int64_t)span_view<TILE>(p, lengths[i]).nt * p.h_kv * p.nrb;
-        all += n;
-        if (i < b) below += n;
-    }
-    __shared__ int64_t part[2][THREADS / 32];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        below += __shfl_xor_sync(0xffffffffu, below, o);
-        all += __shfl_xor_sync(0xffffffffu, all, o);
-    }
-    if ((threadIdx.x & 31) == 0) {
-        part[0][threadIdx.x >> 5] = below;
-        part[1][threadIdx.x >> 5] = all;
-    }
-    __syncthreads();
-    off = total = npt;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) {
-        off += part[0][w];
-        total += part[1][w];
-    }
-    __syncthreads();
-}
-
-// This CTA's share of the sequence; every thread of the block calls it.
-template <int TILE, int THREADS>
-__device__ inline SpanStart span_start(const SpanShape& p, const int32_t* lengths) {
-    __shared__ int64_t part[THREADS / 32];
-    __shared__ int64_t base_s;
-    __shared__ int found_b;
-    __shared__ int64_t found_off;
-    const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t npt = (int64_t)span_prefix_tiles<TILE>(p) * p.h_kv * p.nrbp;
-    SpanStart s;
-    int64_t unused;
-    span_offset<TILE, THREADS>(p, lengths, 0, unused, s.N);
-    const int64_t D = span_parts(s.N, (int)gridDim.x), c = min((int64_t)blockIdx.x, D);
-    s.t0 = D > 0 ? s.N * c / D : 0;
-    s.t1 = c < D ? s.N * (c + 1) / D : s.t0;
-    const int64_t want = s.t0 > npt ? s.t0 : npt;  // the batch in which the own-cache tiles start
-    if (tid == 0) {
-        found_b = 0;
-        found_off = npt;
-        base_s = npt;
-    }
-    __syncthreads();
-    for (int i0 = 0; i0 < p.B; i0 += THREADS) {
-        const int i = i0 + tid;
-        const int64_t n = i < p.B ? (int64_t)span_view<TILE>(p, lengths[i]).nt * p.h_kv * p.nrb : 0;
-        int64_t inc = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += u;
-        }
-        if (lane == 31) part[warp] = inc;
-        __syncthreads();
-        int64_t before = base_s + inc - n;
-        int64_t sum = 0;
-#pragma unroll
-        for (int w = 0; w < THREADS / 32; ++w) {
-            if (w < warp) before += part[w];
-            sum += part[w];
-        }
-        if (n > 0 && before <= want && want < before + n) {
-            found_b = i;
-            found_off = before;
-        }
-        __syncthreads();
-        if (tid == 0) base_s += sum;
-        __syncthreads();
-    }
-    s.b = found_b;
-    s.off = found_off;
-    return s;
-}
-
 
 }  // namespace mha

@@ -13,9 +13,9 @@ using namespace mha;
 
 namespace {
 
-// Query rows of a row block: the smallest of 16, 32 and 64 that holds the rows (a thread of the
-// CUDA-core kernel owns 1, 2 or 4 of them).
-int row_block(const mha_s*, int64_t rows) { return span_simt_rows(rows); }
+// Query rows of a row block: a tensor-core tile for bf16; for fp32 the smallest of 16, 32 and 64 that
+// holds the rows (a thread of the CUDA-core kernel owns 1, 2 or 4 of them).
+int row_block(const mha_s* m, int64_t rows) { return m->dtype == MHA_BF16 ? 128 : span_simt_rows(rows); }
 
 SpanShape span_shape(const mha_s* m, int B, int T_q, int T_max, int T_p, int window, int sinks, int* bm) {
     SpanShape p;
@@ -33,6 +33,7 @@ SpanShape span_shape(const mha_s* m, int B, int T_q, int T_max, int T_p, int win
     p.nrbp = T_p > 0 ? (int)((rows_p + *bm - 1) / *bm) : 0;
     p.window = window < T_max ? window : T_max;
     p.sinks = sinks < T_max ? sinks : T_max;
+    p.gang = 1;
     return p;
 }
 
@@ -98,7 +99,7 @@ mha_status run_cache_step(mha_s* m, const CacheStep& a, cudaStream_t stream) {
     if (overlaps(a.O, obytes, a.weights, wbytes)) return MHA_ERR_INVALID_ARG;
 
     int bm;
-    const SpanShape p = span_shape(m, a.B, a.T_q, a.T_max, a.T_p, a.window, a.sinks, &bm);
+    SpanShape p = span_shape(m, a.B, a.T_q, a.T_max, a.T_p, a.window, a.sinks, &bm);
     const SpanLayout w = span_layout(p, m->dv, bm, a.weights != nullptr);
     if (m->ws == nullptr || m->ws_bytes < kStatusBytes + w.total) return MHA_ERR_WORKSPACE;
     uint8_t* ws = static_cast<uint8_t*>(m->ws) + kStatusBytes;
@@ -113,19 +114,25 @@ mha_status run_cache_step(mha_s* m, const CacheStep& a, cudaStream_t stream) {
     int sms = 0;
     const mha_status st = query_sms(&sms);
     if (st != MHA_OK) return st;
-    int grid = 0;
+    // one CTA per SM holds the tensor-core kernel's tiles, two the CUDA-core kernel's
+    int ctas = m->dtype == MHA_F32 ? 2 * sms : sms;
+    if (ctas > kSpanMaxCtas) ctas = kSpanMaxCtas;
+    p.gang = span_gang(p, ctas);
+    const int64_t most = m->dtype == MHA_F32 ? span_most_tiles<64>(p) : span_most_tiles<128>(p);
+    if (most > INT32_MAX) return MHA_ERR_UNSUPPORTED;
+    const int gangs = most < ctas / p.gang ? (int)most : ctas / p.gang;
     cudaError_t err;
     if (m->dtype == MHA_F32) {
         auto f = [](const void* x) { return static_cast<const float*>(x); };
         err = launch_span_f32(p, rec, bm, f(a.Q), a.ldq, f(a.K), a.ldk, f(a.V), a.ldv, f(a.Kp), a.ldkp, f(a.Vp),
-                              a.ldvp, static_cast<float*>(a.O), a.ldo, m->dk, m->dv, a.lengths, scores, sms, &grid,
+                              a.ldvp, static_cast<float*>(a.O), a.ldo, m->dk, m->dv, a.lengths, scores, gangs,
                               status_ptr(m), stream);
     } else {
-        err = launch_span_bf16(p, rec, bm, a.Q, a.ldq, a.K, a.ldk, a.V, a.ldv, a.Kp, a.ldkp, a.Vp, a.ldvp, a.O, a.ldo,
-                               m->dk, a.lengths, scores, sms, &grid, status_ptr(m), stream);
+        err = launch_span_bf16(p, rec, a.Q, a.ldq, a.K, a.ldk, a.V, a.ldv, a.Kp, a.ldkp, a.Vp, a.ldvp, a.O, a.ldo,
+                               m->dk, a.lengths, scores, gangs, status_ptr(m), stream);
     }
     if (err != cudaSuccess) return MHA_ERR_CUDA;
-    err = launch_span_merge(m->dtype, p, rec, bm, grid, a.O, a.ldo, a.lengths, scores, a.weights, stream);
+    err = launch_span_merge(m->dtype, p, rec, bm, gangs, a.O, a.ldo, a.lengths, scores, a.weights, stream);
     return err == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
 }
 

@@ -19,22 +19,40 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// The record rows of query row r of a group: pieces of CTAs c0 .. c1, one row apart per slot.
+// The record rows of query row r of a lane's group: the pieces of gangs c0 .. c1, one slot row apart.
 struct RowRecords {
     int64_t first, step;
     int n;
 };
 
-template <int TILE>
-__device__ __forceinline__ RowRecords row_records(const SpanRecords& rec, bool prefix, int64_t groups_p,
-                                                  int64_t group, int64_t t0, int nt, int64_t N, int G, int r) {
+// lane: (K/V head, row block) of the prefix or of a batch whose lane blocks start at tile `off` and index
+// `block0`; nt tiles a group.
+__device__ __forceinline__ RowRecords row_records(const SpanShape& p, const SpanRecords& rec, bool prefix, int lane,
+                                                  int off, int block0, int nt, int N, int gangs, int r) {
+    const int bl = lane / p.gang, member = lane - bl * p.gang;
+    const int t0 = off + bl * nt;
     int c0, c1;
-    span_ctas(N, G, t0, t0 + nt, c0, c1);
+    span_gangs(N, gangs, t0, t0 + nt, c0, c1);
     RowRecords x;
-    x.first = rec.row(prefix, groups_p, group, c0) + r;
-    x.step = prefix ? rec.rps_p : rec.rps_c;
+    x.first = rec.row(p, prefix, block0 + bl, c0, member) + r;
+    x.step = (int64_t)p.gang * (prefix ? rec.rps_p : rec.rps_c);
     x.n = c1 - c0 + 1;
     return x;
+}
+
+// The number of tiles N and the first tile of batch b's lane blocks (b has a valid length).
+template <int TILE>
+__device__ __forceinline__ void first_tile(const SpanShape& p, const int32_t* lengths, int b, int& N, int& off) {
+    const int lane = (int)threadIdx.x & 31;
+    const int npt = span_prefix_tiles<TILE>(p) * p.blocks_p();
+    int below = 0, all = 0;
+    for (int i = lane; i < p.B; i += 32) {
+        const int n = span_view<TILE>(p, __ldcg(lengths + i)).nt * p.blocks_c();
+        all += n;
+        if (i < b) below += n;
+    }
+    N = npt + __reduce_add_sync(0xffffffffu, all);
+    off = npt + __reduce_add_sync(0xffffffffu, below);
 }
 
 // Blocks [0, B * heads * T_q): one output row each, thread = output column.  The blocks after them
@@ -43,38 +61,38 @@ __device__ __forceinline__ RowRecords row_records(const SpanRecords& rec, bool p
 // tokens' entries start here (they have no earlier weight), those past the length stay as they are.
 template <typename T, int TILE, bool WEIGHTS>
 __global__ void __launch_bounds__(SM_THREADS)
-    span_merge_kernel(const SpanShape p, const SpanRecords rec, int bm, int G, T* __restrict__ O, int64_t ldo,
+    span_merge_kernel(const SpanShape p, const SpanRecords rec, int bm, int gangs, T* __restrict__ O, int64_t ldo,
                       const int32_t* __restrict__ lengths, const float* __restrict__ scores,
                       float* __restrict__ weights) {
-    grid_dependency_wait();  // the records come from the previous kernel
-    grid_launch_dependents();
+    // The piece kernel lets this one start once its own wait for earlier work is over, so the lengths can
+    // be read at once (from L2: nothing older may be served); the records it is still writing cannot.
     const int tid = (int)threadIdx.x;
     const int heads = p.per * p.h_kv, out_rows = p.B * heads * p.T_q;
-    const int64_t groups_p = p.T_p > 0 ? (int64_t)p.h_kv * p.nrbp : 0;
-    if (!WEIGHTS || (int)blockIdx.x < out_rows) {
+        if (!WEIGHTS || (int)blockIdx.x < out_rows) {
         const int row = (int)blockIdx.x;  // (b * heads + head) * T_q + t
         const int t = row % p.T_q, bh = row / p.T_q, b = bh / heads, head = bh - b * heads;
         T* out = O + ((int64_t)b * p.T_q + t) * ldo + (int64_t)head * rec.dv;
         const int g = head / p.per, rr = (head - g * p.per) * p.T_q + t;
-        const SpanView v = span_view<TILE>(p, lengths[b]);
+        const SpanView v = span_view<TILE>(p, __ldcg(lengths + b));
         if (v.nt == 0) {  // invalid length
+            grid_dependency_wait();
+            grid_launch_dependents();
             for (int e = tid; e < rec.dv; e += SM_THREADS) out[e] = from_f32<T>(NAN);
             return;
         }
-        int64_t off, N;
-        span_offset<TILE, SM_THREADS>(p, lengths, b, off, N);
-        const int gr = g * p.nrb + rr / bm;
+        int N, off;
+        first_tile<TILE>(p, lengths, b, N, off);
+        const int block0 = p.blocks_p() + b * p.blocks_c();
         RowRecords src[2];
-        src[0] = row_records<TILE>(rec, false, groups_p, groups_p + (int64_t)b * p.h_kv * p.nrb + gr,
-                                   off + (int64_t)gr * v.nt, v.nt, N, G, rr % bm);
+        src[0] = row_records(p, rec, false, g * p.nrb + rr / bm, off, block0, v.nt, N, gangs, rr % bm);
         src[1].n = 0;
         if (p.T_p > 0) {
             const int rp = b * p.rows + rr, np = span_prefix_tiles<TILE>(p);
-            const int gp = g * p.nrbp + rp / bm;
-            src[1] = row_records<TILE>(rec, true, groups_p, gp, (int64_t)gp * np, np, N, G, rp % bm);
-        } else if (src[0].n == 1) {
-            return;  // one piece held the whole group and wrote the row
+            src[1] = row_records(p, rec, true, g * p.nrbp + rp / bm, 0, 0, np, N, gangs, rp % bm);
         }
+        grid_dependency_wait();
+        grid_launch_dependents();
+        if (p.T_p == 0 && src[0].n == 1) return;  // one piece held the whole group and wrote the row
         float M = -INFINITY;
         for (int s = 0; s < 2; ++s)
             for (int c = 0; c < src[s].n; ++c) M = fmaxf(M, rec.ml[src[s].first + c * src[s].step].x);
@@ -100,18 +118,19 @@ __global__ void __launch_bounds__(SM_THREADS)
         const int i = (int)blockIdx.x - out_rows;
         const int bg = i / chunks, k0 = (i - bg * chunks) * SM_KEYS;
         const int b = bg / p.h_kv, g = bg - b * p.h_kv;
-        const SpanView v = span_view<TILE>(p, lengths[b]);
+        const SpanView v = span_view<TILE>(p, __ldcg(lengths + b));
+        int N, off;
+        first_tile<TILE>(p, lengths, b, N, off);
+        grid_dependency_wait();
+        grid_launch_dependents();
         if (v.nt == 0 || k0 >= v.L) return;
-        int64_t off, N;
-        span_offset<TILE, SM_THREADS>(p, lengths, b, off, N);
         float w[SM_KEYS / SM_THREADS] = {};
         for (int r0 = 0; r0 < p.rows; r0 += SM_THREADS) {
             __syncthreads();
             const int rr = r0 + tid;
             if (rr < p.rows) {
-                const int gr = g * p.nrb + rr / bm;
-                const RowRecords x = row_records<TILE>(rec, false, groups_p, groups_p + (int64_t)b * p.h_kv * p.nrb + gr,
-                                                       off + (int64_t)gr * v.nt, v.nt, N, G, rr % bm);
+                const RowRecords x = row_records(p, rec, false, g * p.nrb + rr / bm, off,
+                                                 p.blocks_p() + b * p.blocks_c(), v.nt, N, gangs, rr % bm);
                 float M = -INFINITY, l = 0.f;
                 for (int c = 0; c < x.n; ++c) M = fmaxf(M, rec.ml[x.first + c * x.step].x);
                 for (int c = 0; c < x.n; ++c) {
@@ -122,13 +141,13 @@ __global__ void __launch_bounds__(SM_THREADS)
             }
             __syncthreads();
             const int nr = min(SM_THREADS, p.rows - r0);
-            const float* s = scores + ((int64_t)bg * p.rows + r0) * p.T_max + k0;
+            const float* s = scores + ((int64_t)bg * p.rows + r0) * score_ld(p) + k0;
             for (int r = 0; r < nr; ++r) {
                 const float2 ml = row_ml[r];
 #pragma unroll
                 for (int u = 0; u < SM_KEYS / SM_THREADS; ++u) {
                     const int j = tid + u * SM_THREADS;
-                    if (k0 + j < v.L) w[u] = fmaf(exp2f(s[(int64_t)r * p.T_max + j] - ml.x), ml.y, w[u]);
+                    if (k0 + j < v.L) w[u] = fmaf(exp2f(s[(int64_t)r * score_ld(p) + j] - ml.x), ml.y, w[u]);
                 }
             }
         }
@@ -143,24 +162,24 @@ __global__ void __launch_bounds__(SM_THREADS)
 }
 
 template <typename T, int TILE>
-cudaError_t merge(const SpanShape& p, const SpanRecords& rec, int bm, int G, void* O, int64_t ldo,
+cudaError_t merge(const SpanShape& p, const SpanRecords& rec, int bm, int gangs, void* O, int64_t ldo,
                   const int32_t* lengths, const float* scores, float* weights, cudaStream_t stream) {
     const int64_t out_rows = (int64_t)p.B * p.per * p.h_kv * p.T_q;
     const int64_t blocks =
         out_rows + (weights != nullptr ? (int64_t)p.B * p.h_kv * ((p.T_max + SM_KEYS - 1) / SM_KEYS) : 0);
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     auto kernel = weights != nullptr ? span_merge_kernel<T, TILE, true> : span_merge_kernel<T, TILE, false>;
-    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(SM_THREADS), 0, stream, p, rec, bm, G,
+    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(SM_THREADS), 0, stream, p, rec, bm, gangs,
                       static_cast<T*>(O), ldo, lengths, scores, weights);
 }
 
 }  // namespace
 
-cudaError_t launch_span_merge(mha_dtype dtype, const SpanShape& p, const SpanRecords& rec, int bm, int G, void* O,
+cudaError_t launch_span_merge(mha_dtype dtype, const SpanShape& p, const SpanRecords& rec, int bm, int gangs, void* O,
                               int64_t ldo, const int32_t* lengths, const float* scores, float* weights,
                               cudaStream_t stream) {
-    if (dtype == MHA_F32) return merge<float, 64>(p, rec, bm, G, O, ldo, lengths, scores, weights, stream);
-    return merge<__nv_bfloat16, 64>(p, rec, bm, G, O, ldo, lengths, scores, weights, stream);
+    if (dtype == MHA_F32) return merge<float, 64>(p, rec, bm, gangs, O, ldo, lengths, scores, weights, stream);
+    return merge<__nv_bfloat16, 128>(p, rec, bm, gangs, O, ldo, lengths, scores, weights, stream);
 }
 
 }  // namespace mha

@@ -17,10 +17,15 @@ struct SpanRecords {
     int64_t base_c;    // first record row of the cache groups
     int dv;
 
-    __host__ __device__ int64_t row(bool prefix, int64_t groups_p, int64_t group, int cta) const {
-        return prefix ? (cta + group) * rps_p : base_c + (cta + group - groups_p) * rps_c;
+    // Record row of the first query row of a piece: lane block `block` (see SpanPiece), a gang's member.
+    __host__ __device__ int64_t row(const SpanShape& p, bool prefix, int block, int gang, int member) const {
+        const int64_t slot = (int64_t)(gang + block - (prefix ? 0 : p.blocks_p())) * p.gang + member;
+        return prefix ? slot * rps_p : base_c + slot * rps_c;
     }
 };
+
+// Row stride of the scores: 16-byte rows.
+__host__ __device__ inline int64_t score_ld(const SpanShape& p) { return ((int64_t)p.T_max + 3) & ~(int64_t)3; }
 
 struct SpanLayout {
     size_t ml_off, o_off, s_off, total;  // bytes from the workspace area's start
@@ -41,7 +46,7 @@ inline SpanLayout span_layout(const SpanShape& p, int dv, int bm, bool scores) {
     w.ml_off = 0;
     w.o_off = up(rec * sizeof(float2));
     w.s_off = w.o_off + up(rec * (size_t)dv * sizeof(float));
-    w.total = w.s_off + (scores ? up((size_t)p.B * p.h_kv * p.rows * p.T_max * sizeof(float)) : 0);
+    w.total = w.s_off + (scores ? up((size_t)p.B * p.h_kv * p.rows * (size_t)score_ld(p) * sizeof(float)) : 0);
     return w;
 }
 

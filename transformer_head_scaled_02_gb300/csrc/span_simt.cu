@@ -248,13 +248,14 @@ __global__ void __launch_bounds__(SS_THREADS)
     extern __shared__ __align__(16) float fsm[];
     X x(fsm, dk, dv);
     const int tid = (int)threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const SpanStart start = span_start<SS_BK, SS_THREADS>(p, lengths);
+    grid_dependency_wait();  // lengths, queries and caches may come from the previous kernel
+    grid_launch_dependents();
+    const SpanStart start = span_start<SS_BK>(p, lengths);
     if (blockIdx.x == 0)
         for (int b = tid; b < p.B; b += SS_THREADS)
             if (lengths[b] < p.T_q || lengths[b] > p.T_max) record_status(status, kStatusBadLength);
     SpanWalk<SS_BK> walk(p, lengths, start);
     SpanPiece q;
-    const int64_t groups_p = p.T_p > 0 ? (int64_t)p.h_kv * p.nrbp : 0;
     while (walk.next(q)) {
         const int r0 = q.rb * X::BQ;
         const int nr = min(X::BQ, (q.prefix ? p.B * p.rows : p.rows) - r0);
@@ -292,11 +293,11 @@ __global__ void __launch_bounds__(SS_THREADS)
                    },
                    [&](int r, int j, float s) {
                        if (scores != nullptr && r < nr)
-                           scores[(((int64_t)q.b * p.h_kv + q.g) * p.rows + r0 + r) * p.T_max + k0 + j] = s;
+                           scores[(((int64_t)q.b * p.h_kv + q.g) * p.rows + r0 + r) * score_ld(p) + k0 + j] = s;
                    });
         }
         const bool direct = p.T_p == 0 && q.whole();
-        const int64_t slot = rec.row(q.prefix, groups_p, q.group, (int)blockIdx.x);
+        const int64_t slot = rec.row(p, q.prefix, q.block, (int)blockIdx.x / p.gang, (int)blockIdx.x % p.gang);
 #pragma unroll
         for (int r = 0; r < RQ; ++r) {
             const int rr = ty * RQ + r;
@@ -354,7 +355,7 @@ template <typename E>
 static cudaError_t launch_span(const SpanShape& p, const SpanRecords& rec, int bm, const E* Q, int64_t ldq,
                             const E* K, int64_t ldk, const E* V, int64_t ldv, const E* Kp,
                             int64_t ldkp, const E* Vp, int64_t ldvp, E* O, int64_t ldo, int d_k, int d_v,
-                            const int32_t* lengths, float* scores, int num_sms, int* grid, int* status,
+                            const int32_t* lengths, float* scores, int gangs, int* status,
                             cudaStream_t stream) {
     auto al = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
     const bool vec = al(Q) && al(K) && al(V) && ldq % 4 == 0 && ldk % 4 == 0 && ldv % 4 == 0 && d_k % 4 == 0 &&
@@ -364,11 +365,8 @@ static cudaError_t launch_span(const SpanShape& p, const SpanRecords& rec, int b
     auto launch = [&](auto kernel, size_t smem) {
         cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (err != cudaSuccess) return err;
-        *grid = 2 * num_sms < kSpanMaxCtas ? 2 * num_sms : kSpanMaxCtas;
-        kernel<<<dim3((unsigned)*grid), SS_THREADS, smem, stream>>>(p, rec, Q, ldq, K, ldk, V, ldv, Kp, ldkp, Vp,
-                                                                   ldvp, O, ldo, d_k, d_v, lengths, scores, scale,
-                                                                   vec, status);
-        return cudaGetLastError();
+        return launch_pdl(kernel, dim3((unsigned)(gangs * p.gang)), dim3(SS_THREADS), smem, stream, p, rec, Q, ldq, K,
+                          ldk, V, ldv, Kp, ldkp, Vp, ldvp, O, ldo, d_k, d_v, lengths, scores, scale, vec, status);
     };
 #define MHA_SS(RQ, CV) \
     if (bm == 16 * RQ && cv == CV) return launch(span_simt_kernel<E, RQ, CV>, SimtTile<E, RQ, CV>::smem_bytes(d_k));
@@ -398,19 +396,10 @@ cudaError_t launch_window_bf16(const void* Q, int64_t ldq, const void* K, int64_
 cudaError_t launch_span_f32(const SpanShape& p, const SpanRecords& rec, int bm, const float* Q, int64_t ldq,
                             const float* K, int64_t ldk, const float* V, int64_t ldv, const float* Kp,
                             int64_t ldkp, const float* Vp, int64_t ldvp, float* O, int64_t ldo, int d_k, int d_v,
-                            const int32_t* lengths, float* scores, int num_sms, int* grid, int* status,
+                            const int32_t* lengths, float* scores, int gangs, int* status,
                             cudaStream_t stream) {
     return launch_span(p, rec, bm, Q, ldq, K, ldk, V, ldv, Kp, ldkp, Vp, ldvp, O, ldo, d_k, d_v, lengths, scores,
-                       num_sms, grid, status, stream);
-}
-
-cudaError_t launch_span_bf16(const SpanShape& p, const SpanRecords& rec, int bm, const void* Q, int64_t ldq,
-                             const void* K, int64_t ldk, const void* V, int64_t ldv, const void* Kp, int64_t ldkp,
-                             const void* Vp, int64_t ldvp, void* O, int64_t ldo, int d, const int32_t* lengths,
-                             float* scores, int num_sms, int* grid, int* status, cudaStream_t stream) {
-    auto f = [](const void* x) { return static_cast<const __nv_bfloat16*>(x); };
-    return launch_span(p, rec, bm, f(Q), ldq, f(K), ldk, f(V), ldv, f(Kp), ldkp, f(Vp), ldvp,
-                       static_cast<__nv_bfloat16*>(O), ldo, d, d, lengths, scores, num_sms, grid, status, stream);
+                       gangs, status, stream);
 }
 
 }  // namespace mha
