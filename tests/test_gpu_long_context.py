@@ -522,6 +522,17 @@ def test_evict_orders(kind, in_place):
     _evict_case(layer, "bf16", B, T, h_kv, 64, 64, [T, 1500], w, keep, recent, 9, in_place=in_place)
 
 
+@pytest.mark.parametrize("T", [16384, 17000, 50000, 70001])
+@pytest.mark.parametrize("ties", [False, True])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_long(T, ties, in_place):
+    """Caches longer than one scan of the selection, and longer than shared memory holds."""
+    rng = np.random.default_rng(T)
+    w = rng.integers(0, 3, (2, 1, T)).astype(float) if ties else rng.random((2, 1, T))
+    layer = _layer("f32", 1, 4, 1)
+    _evict_case(layer, "f32", 2, T, 1, 4, 4, [T, T - 333], w, T - 1000 if ties else T // 3, 77, 13, in_place=in_place)
+
+
 @pytest.mark.parametrize("in_place", [False, True])
 def test_evict_views_of_one_buffer_and_invalid_lengths(in_place):
     layer = _layer("bf16", 4, 64, 4)

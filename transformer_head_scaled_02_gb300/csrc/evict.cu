@@ -3,12 +3,12 @@
 // index), then move their K, V and weight rows together in their order.
 //
 //   evict_select_kernel   one block per (batch, K/V head).  The weights as order-preserving 32-bit
-//                         keys; the keep - recent largest are found by radix selection (8 bits at a
-//                         time: a histogram of the keys that agree with the digits fixed so far, one
-//                         private histogram per warp because most weights share their first digits),
-//                         which gives the smallest kept key and how many tokens equal to it are kept;
-//                         a pass in index order then numbers the kept tokens (ballots and warp
-//                         totals).  Reads the weights six times, from L2 after the first.
+//                         keys, in shared memory where they fit, so that they are read once; the
+//                         keep - recent largest are found by radix selection (digits of 11, 11 and 10
+//                         bits: a histogram of the keys that agree with the digits fixed so far), which
+//                         gives the smallest kept key and how many tokens equal to it are kept; two
+//                         counts in index order (ballots, one block-wide scan each) then number the
+//                         kept tokens.  Bound by latency: a few block-wide steps per block.
 //   evict_move_kernel     row copies, bound by HBM: kept rows are read and written once.
 #include <math.h>
 
@@ -18,8 +18,14 @@
 namespace mha {
 namespace {
 
-constexpr int EV_THREADS = 1024;
+constexpr int EV_THREADS = 512;
 constexpr int EV_WARPS = EV_THREADS / 32;
+constexpr int EV_BINS = 2048;
+// Tokens per scan: every warp counts 32 at a time, EV_STEPS times.
+constexpr int EV_STEPS = 32;
+constexpr int EV_SCAN = EV_THREADS * EV_STEPS;
+// Tokens whose keys fit shared memory beside the histogram and the counts.
+constexpr int EV_SMEM_TOKENS = 48 * 1024;
 
 // Ascending keys for ascending weights; NaN below everything, -0 equal to +0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -28,14 +34,42 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
+// Exclusive sum over the block of one value per thread; total: the whole sum.  Two barriers.
+__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
+    const int lane = (int)threadIdx.x & 31, warp = (int)threadIdx.x >> 5;
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+    }
+    if (lane == 31) warp_sums[warp] = inc;
+    __syncthreads();
+    const int s = lane < EV_WARPS ? warp_sums[lane] : 0;
+    int ws = s;
+#pragma unroll
+    for (int o = 1; o < EV_WARPS; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, ws, o);
+        if (lane >= o) ws += u;
+    }
+    total = __shfl_sync(0xffffffffu, ws, EV_WARPS - 1);
+    const int before = __shfl_sync(0xffffffffu, ws - s, warp);
+    __syncthreads();
+    return before + inc - v;
+}
+
+// KEYS: the keys fit shared memory (T_max <= EV_SMEM_TOKENS); otherwise every pass reads the weights.
+template <bool KEYS>
 __global__ void __launch_bounds__(EV_THREADS)
     evict_select_kernel(int T_max, int h_kv, int keep, int recent, const int32_t* __restrict__ lengths,
                         const float* weights, int32_t* __restrict__ kept, float* weights_out, int T_out,
                         int* status) {
-    __shared__ uint32_t hist[EV_WARPS][256];
-    __shared__ uint32_t total[256];
-    __shared__ uint32_t digit_s, need_s;
-    __shared__ int warp_eq[EV_WARPS], warp_keep[EV_WARPS];
+    extern __shared__ uint32_t keys_s[];
+    __shared__ int hist[EV_BINS];
+    __shared__ int warp_sums[EV_WARPS];
+    __shared__ int digit_s, need_s, count_s;
+    __shared__ int16_t counts[EV_STEPS * EV_WARPS];  // of 32 tokens each
+    __shared__ int base[EV_STEPS * EV_WARPS];
     grid_dependency_wait();
     grid_launch_dependents();
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -57,85 +91,107 @@ __global__ void __launch_bounds__(EV_THREADS)
         return;
     }
     const int n_early = L - recent;  // > keep - recent >= 0
-    uint32_t need = (uint32_t)(keep - recent), prefix = 0u;
-    // radix selection: prefix holds the digits fixed so far, need the rank left within them
-    for (int shift = 24; shift >= 0 && need > 0; shift -= 8) {
-        for (int i = tid; i < EV_WARPS * 256; i += EV_THREADS) (&hist[0][0])[i] = 0u;
+    if constexpr (KEYS) {
+        for (int j = tid; j < n_early; j += EV_THREADS) keys_s[j] = weight_key(w[j]);
         __syncthreads();
-        const uint32_t fixed = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-        for (int j = tid; j < n_early; j += EV_THREADS) {
-            const uint32_t k = weight_key(w[j]);
-            if ((k & fixed) == prefix) atomicAdd(&hist[warp][(k >> shift) & 255u], 1u);
-        }
-        __syncthreads();
-        if (tid < 256) {
-            uint32_t s = 0;
-#pragma unroll
-            for (int q = 0; q < EV_WARPS; ++q) s += hist[q][tid];
-            total[tid] = s;
-        }
-        __syncthreads();
-        if (warp == 0) {
-            // lane l: digits 255 - 8 l down to 248 - 8 l; the digit where the running count reaches need
-            uint32_t c[8], sum = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                c[i] = total[255 - 8 * lane - i];
-                sum += c[i];
-            }
-            uint32_t inc = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += u;
-            }
-            uint32_t before = inc - sum;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (before < need && need <= before + c[i]) {
-                    digit_s = (uint32_t)(255 - 8 * lane - i);
-                    need_s = need - before;
-                }
-                before += c[i];
-            }
-        }
-        __syncthreads();
-        prefix |= digit_s << shift;
-        need = need_s;
     }
-    // tokens above `prefix` are kept, and the first `need` of those equal to it (none if keep == recent)
+    auto key = [&](int j) { return KEYS ? keys_s[j] : weight_key(w[j]); };
+    // radix selection: `prefix` holds the digits fixed so far, `need` how many of the keys that agree
+    // with them are kept, `equal` how many there are
+    int need = keep - recent, equal = 0;
+    uint32_t prefix = 0u, fixed = 0u;
+#pragma unroll 1
+    for (int shift = 21; shift >= 0 && need > 0; shift = shift == 21 ? 10 : shift == 10 ? 0 : -1) {
+        const uint32_t mask = shift == 0 ? 1023u : 2047u;
+        for (int i = tid; i < EV_BINS; i += EV_THREADS) hist[i] = 0;
+        __syncthreads();
+        for (int j = tid; j < n_early; j += EV_THREADS) {
+            const uint32_t k = key(j);
+            if ((k & fixed) == prefix) atomicAdd(&hist[(k >> shift) & mask], 1);
+        }
+        __syncthreads();
+        // thread i: digits from the top down; the digit where the running count reaches need
+        constexpr int PER = EV_BINS / EV_THREADS;
+        int c[PER], sum = 0, total;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            c[i] = hist[EV_BINS - 1 - PER * tid - i];
+            sum += c[i];
+        }
+        int before = block_scan(sum, warp_sums, total);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (before < need && need <= before + c[i]) {
+                digit_s = EV_BINS - 1 - PER * tid - i;
+                need_s = need - before;
+                count_s = c[i];
+            }
+            before += c[i];
+        }
+        __syncthreads();
+        prefix |= (uint32_t)digit_s << shift;
+        fixed |= mask << shift;
+        need = need_s;
+        equal = count_s;
+    }
+    // Tokens above `prefix` are kept and the first `need` of those equal to it (keep == recent: none).
+    // Numbering in index order, EV_SCAN tokens at a time: the ballots of 32 tokens each are counted, the
+    // counts scanned over the block, the places read back.
     const bool any = keep > recent;
     int eq_base = 0, keep_base = 0;
-    for (int j0 = 0; j0 < L; j0 += EV_THREADS) {
-        const int j = j0 + tid;
-        const float wj = j < L ? w[j] : 0.f;
-        const uint32_t k = j < n_early ? weight_key(wj) : 0u;
-        const bool eq = any && j < n_early && k == prefix;
-        const uint32_t eq_mask = __ballot_sync(0xffffffffu, eq);
-        if (lane == 0) warp_eq[warp] = __popc(eq_mask);
-        __syncthreads();
-        int eq_rank = eq_base + __popc(eq_mask & ((1u << lane) - 1u)), eq_sum = 0;
-#pragma unroll
-        for (int q = 0; q < EV_WARPS; ++q) {
-            if (q < warp) eq_rank += warp_eq[q];
-            eq_sum += warp_eq[q];
+    for (int j0 = 0; j0 < L; j0 += EV_SCAN) {
+        const int steps = min(EV_STEPS, (L - j0 + EV_THREADS - 1) / EV_THREADS);
+        // place of the first token of each 32, counting those that f says
+        auto number = [&](auto f, int& sum) {
+#pragma unroll 4
+            for (int i = 0; i < steps; ++i) {
+                const unsigned m = __ballot_sync(0xffffffffu, f(i, j0 + i * EV_THREADS + tid));
+                if (lane == 0) counts[i * EV_WARPS + warp] = (int16_t)__popc(m);
+            }
+            __syncthreads();
+            int at = tid < steps * EV_WARPS ? counts[tid] : 0;  // EV_STEPS * EV_WARPS == EV_THREADS
+            at = block_scan(at, warp_sums, sum);
+            base[tid] = at;
+            __syncthreads();
+        };
+        static_assert(EV_STEPS * EV_WARPS == EV_THREADS, "one count per thread");
+        uint32_t eq_taken = 0u;  // bit i: this thread's token of step i is equal and among the first `need`
+        if (any && need < equal) {
+            int sum;
+            auto is_eq = [&](int, int j) { return j < n_early && key(j) == prefix; };
+            number(is_eq, sum);
+            for (int i = 0; i < steps; ++i) {
+                const bool e = is_eq(i, j0 + i * EV_THREADS + tid);
+                const unsigned m = __ballot_sync(0xffffffffu, e);
+                if (e && eq_base + base[i * EV_WARPS + warp] + __popc(m & ((1u << lane) - 1u)) < need) eq_taken |= 1u << i;
+            }
+            eq_base += sum;
+            __syncthreads();  // base is about to be overwritten
+        } else if (any) {
+            eq_taken = 0xFFFFFFFFu;
         }
-        const bool take = j < L && (j >= n_early || (any && (k > prefix || (eq && eq_rank < (int)need))));
-        const uint32_t mask = __ballot_sync(0xffffffffu, take);
-        if (lane == 0) warp_keep[warp] = __popc(mask);
-        __syncthreads();
-        int at = keep_base + __popc(mask & ((1u << lane) - 1u)), sum = 0;
-#pragma unroll
-        for (int q = 0; q < EV_WARPS; ++q) {
-            if (q < warp) at += warp_keep[q];
-            sum += warp_keep[q];
+        auto taken = [&](int i, int j) {
+            if (j >= L) return false;
+            if (j >= n_early) return true;
+            const uint32_t k = key(j);
+            return any && (k > prefix || (k == prefix && ((eq_taken >> i) & 1u)));
+        };
+        int sum;
+        number(taken, sum);
+        // in place: a token's place is at most its index, every weight up to j0 has been read, and
+        // those of a step are read by all before any of that step's is written
+        for (int i = 0; i < steps; ++i) {
+            const int j = j0 + i * EV_THREADS + tid;
+            const bool t = taken(i, j);
+            const float wj = j < L ? w[j] : 0.f;
+            const unsigned m = __ballot_sync(0xffffffffu, t);
+            __syncthreads();
+            if (t) {
+                const int at = keep_base + base[i * EV_WARPS + warp] + __popc(m & ((1u << lane) - 1u));
+                out[at] = j;
+                w_out[at] = wj;
+            }
         }
-        // in place: at <= j, and every entry up to this block of tokens has been read
-        if (take) {
-            out[at] = j;
-            w_out[at] = wj;
-        }
-        eq_base += eq_sum;
         keep_base += sum;
         __syncthreads();
     }
@@ -244,12 +300,14 @@ cudaError_t move(const MoveSide& k, const MoveSide& v, int B, int T_max, int T_o
                           dim3((unsigned)(h_kv * ((widest + MV_SLICE - 1) / MV_SLICE)), (unsigned)B, 2),
                           dim3(MV_THREADS), 0, stream, k, v, T_max, h_kv, keep, kept, new_lengths);
     }
-    // about 64 KB of a side's rows per block
-    const int64_t row_bytes = (int64_t)k.head_bytes * h_kv;
-    int rpb = (int)(65536 / (row_bytes > 65536 ? 65536 : row_bytes));
-    if (rpb > keep) rpb = keep;
+    // up to 32 KB of a side's rows per block (every thread keeps MV_ROUNDS pieces in flight), less where
+    // that would leave SMs without a block
+    const int64_t row_bytes = (int64_t)(k.head_bytes > v.head_bytes ? k.head_bytes : v.head_bytes) * h_kv;
+    int64_t rpb = 32768 / (row_bytes > 32768 ? 32768 : row_bytes);
+    const int64_t spread = ((int64_t)keep * B * 2 + 1023) / 1024;
+    if (rpb > spread) rpb = spread < 1 ? 1 : spread;
     return launch_pdl(evict_move_kernel<UNIT>, dim3((unsigned)((keep + rpb - 1) / rpb), (unsigned)B, 2),
-                      dim3(MV_THREADS), 0, stream, k, v, T_max, T_out, h_kv, keep, kept, new_lengths, rpb);
+                      dim3(MV_THREADS), 0, stream, k, v, T_max, T_out, h_kv, keep, kept, new_lengths, (int)rpb);
 }
 
 }  // namespace
@@ -258,8 +316,13 @@ cudaError_t launch_evict(const void* K, int64_t ldk, const void* V, int64_t ldv,
                          int64_t ldvo, int elem, int B, int h_kv, int T_max, int T_out, int d_k, int d_v, int keep,
                          int recent, const int32_t* lengths, const float* weights, float* weights_out,
                          int32_t* kept, int32_t* new_lengths, int* status, cudaStream_t stream) {
-    cudaError_t err = launch_pdl(evict_select_kernel, dim3((unsigned)(B * h_kv)), dim3(EV_THREADS), 0, stream, T_max,
-                                 h_kv, keep, recent, lengths, weights, kept, weights_out, T_out, status);
+    const bool keys = T_max <= EV_SMEM_TOKENS;
+    auto select = keys ? evict_select_kernel<true> : evict_select_kernel<false>;
+    const size_t smem = keys ? (size_t)T_max * sizeof(uint32_t) : 0;
+    cudaError_t err = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess) return err;
+    err = launch_pdl(select, dim3((unsigned)(B * h_kv)), dim3(EV_THREADS), smem, stream, T_max, h_kv, keep, recent, lengths,
+                     weights, kept, weights_out, T_out, status);
     if (err != cudaSuccess) return err;
     const MoveSide k{static_cast<const uint8_t*>(K), static_cast<uint8_t*>(Ko), ldk * elem, ldko * elem, d_k * elem};
     const MoveSide v{static_cast<const uint8_t*>(V), static_cast<uint8_t*>(Vo), ldv * elem, ldvo * elem, d_v * elem};

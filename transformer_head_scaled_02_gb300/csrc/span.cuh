@@ -24,6 +24,11 @@
 
 namespace mha {
 
+// Ending a piece (joining its streams, writing its rows, starting the next) takes about as long as a tile:
+// every group occupies that many places more in the sequence than it has tiles, so that a gang with many
+// short groups gets fewer tiles.  Nothing is read for those places.
+constexpr int kSpanPieceCost = 1;
+
 // Largest grid of a piece kernel (bounds the record slots; the host knows no SM count when it
 // computes workspace sizes).
 constexpr int kSpanMaxCtas = 320;
@@ -55,6 +60,7 @@ inline int span_gang(const SpanShape& p, int ctas) {
 // an invalid length).
 struct SpanView {
     int L, s_keys, lo, nst, nt;
+    __host__ __device__ int places() const { return nt > 0 ? nt + kSpanPieceCost : 0; }  // in the sequence
 };
 
 template <int TILE>
@@ -95,23 +101,36 @@ __host__ __device__ inline int span_prefix_tiles(const SpanShape& p) {
     return (p.T_p + TILE - 1) / TILE;
 }
 
+// Places of the sequence that the prefix's groups take.
+template <int TILE>
+__host__ __device__ inline int span_prefix_places(const SpanShape& p) {
+    return p.T_p > 0 ? (span_prefix_tiles<TILE>(p) + kSpanPieceCost) * p.blocks_p() : 0;
+}
+
 // Gangs that share N tiles when G are launched: each of them holds at least one.
 __host__ __device__ inline int span_parts(int N, int G) { return N < G ? N : G; }
 
-// Gangs [c0, c1] that hold tiles [t0, t1) of N when G divide them.
-__device__ __forceinline__ void span_gangs(int N, int G, int t0, int t1, int& c0, int& c1) {
-    const int64_t D = span_parts(N, G);
-    c0 = (int)(((t0 + 1) * D - 1) / N);
-    c1 = (int)((t1 * D - 1) / N);
+// a * b / c, in 32 bits where the product fits (a 64-bit division costs several hundred cycles)
+__device__ __forceinline__ int span_muldiv(int a, int b, int add, int c) {
+    if (a < (1 << 21) && b <= 1024) return (int)(((unsigned)a * (unsigned)b + (unsigned)add) / (unsigned)c);
+    return (int)(((int64_t)a * b + add) / c);
 }
 
-// Tiles of one lane's sequence if every batch had the longest cache (the host checks that they fit 32
-// bits and launches no more gangs).
+// Gangs [c0, c1] that hold places [t0, t1) of N when G divide them.
+__device__ __forceinline__ void span_gangs(int N, int G, int t0, int t1, int& c0, int& c1) {
+    const int D = span_parts(N, G);
+    c0 = span_muldiv(t0, D, D - 1, N);  // ((t0 + 1) D - 1) / N
+    c1 = span_muldiv(t1, D, -1, N);
+}
+
+// Places of the sequence if every batch had the longest cache (the host checks that they fit 32 bits and
+// launches no more gangs).
 template <int TILE>
-inline int64_t span_most_tiles(const SpanShape& p) {
+inline int64_t span_most_places(const SpanShape& p) {
     const int64_t all = ((int64_t)p.T_max + TILE - 1) / TILE;
     const int64_t win = ((int64_t)p.sinks + TILE - 1) / TILE + ((int64_t)p.window + p.T_q - 1 + TILE - 1) / TILE;
-    return (int64_t)span_prefix_tiles<TILE>(p) * p.blocks_p() + (int64_t)p.B * p.blocks_c() * (all < win ? all : win);
+    const int64_t pre = p.T_p > 0 ? ((int64_t)span_prefix_tiles<TILE>(p) + kSpanPieceCost) * p.blocks_p() : 0;
+    return pre + (int64_t)p.B * p.blocks_c() * ((all < win ? all : win) + kSpanPieceCost);
 }
 
 // Where a gang starts in the tile sequence.
@@ -129,9 +148,9 @@ template <int TILE, typename F>
 __device__ __forceinline__ void span_find(const SpanShape& p, const int32_t* lengths, F want, int& N, int& b, int& off) {
     const int lane = (int)threadIdx.x & 31;
     const int run = (p.B + 31) / 32, i0 = lane * run, i1 = min(p.B, i0 + run);
-    const int npt = span_prefix_tiles<TILE>(p) * p.blocks_p();
+    const int npt = span_prefix_places<TILE>(p);
     int sum = 0;
-    for (int i = i0; i < i1; ++i) sum += span_view<TILE>(p, lengths[i]).nt * p.blocks_c();
+    for (int i = i0; i < i1; ++i) sum += span_view<TILE>(p, lengths[i]).places() * p.blocks_c();
     int inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -144,7 +163,7 @@ __device__ __forceinline__ void span_find(const SpanShape& p, const int32_t* len
     const bool mine = before <= t && t < before + sum;
     if (mine)
         for (int i = i0; i < i1; ++i) {
-            const int n = span_view<TILE>(p, lengths[i]).nt * p.blocks_c();
+            const int n = span_view<TILE>(p, lengths[i]).places() * p.blocks_c();
             if (t < before + n) {
                 found = i;
                 break;
@@ -161,12 +180,12 @@ __device__ __forceinline__ void span_find(const SpanShape& p, const int32_t* len
 template <int TILE>
 __device__ __forceinline__ SpanStart span_start(const SpanShape& p, const int32_t* lengths) {
     const int gangs = (int)gridDim.x / p.gang, c = (int)blockIdx.x / p.gang;
-    const int npt = span_prefix_tiles<TILE>(p) * p.blocks_p();
+    const int npt = span_prefix_places<TILE>(p);
     SpanStart s;
     span_find<TILE>(p, lengths, [&](int N) {
         const int D = span_parts(N, gangs);
-        s.t0 = c < D ? (int)((int64_t)N * c / D) : N;
-        s.t1 = c < D ? (int)((int64_t)N * (c + 1) / D) : N;
+        s.t0 = c < D ? span_muldiv(N, c, 0, D) : N;
+        s.t1 = c < D ? span_muldiv(N, c + 1, 0, D) : N;
         return max(s.t0, npt);
     }, s.N, s.b, s.off);
     return s;
@@ -182,53 +201,72 @@ struct SpanPiece {
     __device__ bool whole() const { return i0 == 0 && i1 == v.nt; }
 };
 
-// Walks a gang's pieces in order.
+// Walks a gang's pieces in order.  Divisions only at the start: afterwards the walk steps from group to
+// group.
 template <int TILE>
 struct SpanWalk {
     const SpanShape& p;
     const int32_t* lengths;
-    int t, t1, off, b;
+    int left;   // places left
+    int in;     // next place within the current group
+    int bl;     // current lane block within its batch (or within the prefix)
+    int b;      // current batch; -1: the prefix
+    int first;  // first batch after the prefix
+    SpanView v;
 
     __device__ SpanWalk(const SpanShape& p_, const int32_t* lengths_, const SpanStart& s)
-        : p(p_), lengths(lengths_), t(s.t0), t1(s.t1), off(s.off), b(s.b) {}
-
-    __device__ bool next(SpanPiece& q) {
-        if (t >= t1) return false;
-        const int np = span_prefix_tiles<TILE>(p);
-        const int member = (int)blockIdx.x % p.gang;
-        int in;  // tile within the group
-        int lane;
-        if (t < np * p.blocks_p()) {
-            q.prefix = true;
-            q.block = t / np;
-            in = t - q.block * np;
-            q.b = 0;
-            lane = q.block * p.gang + member;
-            q.g = lane / p.nrbp;
-            q.rb = lane - q.g * p.nrbp;
-            q.v.L = p.T_p;
-            q.v.s_keys = q.v.lo = q.v.nst = 0;
-            q.v.nt = np;
+        : p(p_), lengths(lengths_), left(s.t1 - s.t0), in(0), bl(0), b(s.b), first(s.b) {
+        if (left <= 0) return;
+        const int npt = span_prefix_places<TILE>(p);
+        int at = s.t0 - s.off;  // within the batch's groups
+        if (s.t0 < npt) {
+            at = s.t0;
+            b = -1;
+            prefix_view();
         } else {
-            q.prefix = false;
-            q.v = span_view<TILE>(p, lengths[b]);
-            while (t - off >= q.v.nt * p.blocks_c()) {  // the next batch (some hold no tile)
-                off += q.v.nt * p.blocks_c();
-                ++b;
-                q.v = span_view<TILE>(p, lengths[b]);
-            }
-            const int bl = (t - off) / q.v.nt;
-            in = t - off - bl * q.v.nt;
-            q.b = b;
-            lane = bl * p.gang + member;
-            q.g = lane / p.nrb;
-            q.rb = lane - q.g * p.nrb;
-            q.block = p.blocks_p() + b * p.blocks_c() + bl;
+            v = span_view<TILE>(p, lengths[b]);
         }
-        q.i0 = in;
-        q.i1 = t1 - t < q.v.nt - in ? in + t1 - t : q.v.nt;
-        t += q.i1 - q.i0;
-        return true;
+        bl = at / v.places();
+        in = at - bl * v.places();
+    }
+
+    __device__ void prefix_view() {
+        v.L = p.T_p;
+        v.s_keys = v.lo = v.nst = 0;
+        v.nt = span_prefix_tiles<TILE>(p);
+    }
+
+    __device__ void next_batch() {
+        bl = 0;
+        b = b < 0 ? first : b + 1;
+        v = span_view<TILE>(p, lengths[b]);
+    }
+
+    // The next piece, or false (and q as it was) at the end.
+    __device__ bool next(SpanPiece& q) {
+        while (left > 0) {
+            if (in == v.places()) {  // the next group; batches without a tile are passed over
+                in = 0;
+                ++bl;
+                if (bl == (b < 0 ? p.blocks_p() : p.blocks_c())) next_batch();
+                while (v.nt == 0) next_batch();
+            }
+            const int i0 = in, end = min(v.places(), in + left);
+            left -= end - in;
+            in = end;
+            if (i0 >= v.nt) continue;
+            q.prefix = b < 0;
+            q.v = v;
+            q.i0 = i0;
+            q.i1 = min(v.nt, end);
+            q.b = b < 0 ? 0 : b;
+            const int lane = bl * p.gang + (int)blockIdx.x % p.gang, nrb = b < 0 ? p.nrbp : p.nrb;
+            q.g = nrb == 1 ? lane : lane / nrb;
+            q.rb = nrb == 1 ? 0 : lane - q.g * nrb;
+            q.block = b < 0 ? bl : p.blocks_p() + b * p.blocks_c() + bl;
+            return true;
+        }
+        return false;
     }
 };
 

@@ -118,21 +118,21 @@ mha_status run_cache_step(mha_s* m, const CacheStep& a, cudaStream_t stream) {
     int ctas = m->dtype == MHA_F32 ? 2 * sms : sms;
     if (ctas > kSpanMaxCtas) ctas = kSpanMaxCtas;
     p.gang = span_gang(p, ctas);
-    const int64_t most = m->dtype == MHA_F32 ? span_most_tiles<64>(p) : span_most_tiles<128>(p);
+    const int64_t most = m->dtype == MHA_F32 ? span_most_places<64>(p) : span_most_places<128>(p);
     if (most > INT32_MAX) return MHA_ERR_UNSUPPORTED;
     const int gangs = most < ctas / p.gang ? (int)most : ctas / p.gang;
     cudaError_t err;
     if (m->dtype == MHA_F32) {
         auto f = [](const void* x) { return static_cast<const float*>(x); };
+        float* O = static_cast<float*>(a.O);
         err = launch_span_f32(p, rec, bm, f(a.Q), a.ldq, f(a.K), a.ldk, f(a.V), a.ldv, f(a.Kp), a.ldkp, f(a.Vp),
-                              a.ldvp, static_cast<float*>(a.O), a.ldo, m->dk, m->dv, a.lengths, scores, gangs,
-                              status_ptr(m), stream);
+                              a.ldvp, O, a.ldo, m->dk, m->dv, a.lengths, scores, gangs, status_ptr(m), stream);
+        if (err == cudaSuccess)
+            err = launch_span_merge(p, rec, bm, gangs, O, a.ldo, a.lengths, scores, a.weights, stream);
     } else {
         err = launch_span_bf16(p, rec, a.Q, a.ldq, a.K, a.ldk, a.V, a.ldv, a.Kp, a.ldkp, a.Vp, a.ldvp, a.O, a.ldo,
-                               m->dk, a.lengths, scores, gangs, status_ptr(m), stream);
+                               m->dk, a.lengths, scores, a.weights, gangs, status_ptr(m), stream);
     }
-    if (err != cudaSuccess) return MHA_ERR_CUDA;
-    err = launch_span_merge(m->dtype, p, rec, bm, gangs, a.O, a.ldo, a.lengths, scores, a.weights, stream);
     return err == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
 }
 

@@ -52,6 +52,7 @@ class Mha:
         self._ws: Optional[torch.Tensor] = None
         self._ws_captured = False
         self._kept_ws: list = []
+        self._step_bytes: dict = {}  # workspace bytes of the cache steps, by their sizes
 
     @property
     def proj_width(self) -> int:
@@ -290,24 +291,28 @@ class Mha:
     # ------------------------------------------------------------ long contexts
     def _rows(self, name: str, t: torch.Tensor, B: int, T: int, width: int) -> int:
         """Check a (B, T, width) view whose rows lie one stride apart throughout; returns the stride."""
-        if tuple(t.shape) != (B, T, width):
+        if t.shape != (B, T, width):
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(B, T, width)}")
         s0, s1, s2 = t.stride()
-        ld = s0 if T == 1 and B > 1 else s1
         if t.dtype != self.dtype or s2 != 1 or (B > 1 and T > 1 and s0 != T * s1):
             raise ValueError(f"{name} must be a (B,T,*) {self.dtype} view with contiguous rows and "
                              "batches")
-        # a single row (or an empty view) has no second one: any stride of at least a row will do
-        return ld if B * T > 1 else max(ld, width)
+        if B * T > 1:
+            return s0 if T == 1 else s1
+        return max(s1, width)  # one row (or none): any stride of at least a row will do
 
-    def _device(self, first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
+    @staticmethod
+    def _device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
         """All on one CUDA device, the current one; returns its current stream."""
-        dev = first.device
-        if dev.type != "cuda" or any(t is not None and t.device != dev for t in others):
-            raise ValueError("all tensors must be on one CUDA device")
-        if dev.index != torch.cuda.current_device():
-            raise ValueError(f"the tensors are on {dev}, which is not the current device")
-        return torch.cuda.current_stream(dev).cuda_stream
+        dev = first.get_device()
+        if dev < 0:
+            raise ValueError("the tensors must be on a CUDA device")
+        for t in others:
+            if t is not None and t.get_device() != dev:
+                raise ValueError("all tensors must be on one CUDA device")
+        if dev != torch._C._cuda_getDevice():
+            raise ValueError(f"the tensors are on cuda:{dev}, which is not the current device")
+        return torch._C._cuda_getCurrentRawStream(dev)
 
     @staticmethod
     def _ints(name: str, t: torch.Tensor, B: int) -> int:
@@ -354,8 +359,12 @@ class Mha:
         ldo = self._rows("out", out, B, T_q, self.h * self.d_v)
         lens = self._ints("cache_lengths", cache_lengths, B)
         stream = self._device(Q, K_cache, V_cache, cache_lengths, out, *others)
-        self.ensure_workspace(B, T_q, T_max, need=_lib.mha_cache_step_workspace_size(
-            self.handle, B, T_q, T_prefix, T_max, weights))
+        key = (B, T_q, T_prefix, T_max, weights)
+        need = self._step_bytes.get(key)
+        if need is None:
+            need = _lib.mha_cache_step_workspace_size(self.handle, *key)
+            self._step_bytes[key] = need
+        self.ensure_workspace(B, T_q, T_max, need=need)
         cache = (Q.data_ptr(), ldq, K_cache.data_ptr(), ldk, V_cache.data_ptr(), ldv)
         return out, (B, T_q, T_max), cache, lens, (out.data_ptr(), ldo, stream)
 
