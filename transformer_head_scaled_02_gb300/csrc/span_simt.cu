@@ -22,7 +22,7 @@ constexpr int SS_BK = 64;
 constexpr int SS_THREADS = 256;
 constexpr int SS_PS = SS_BK + 4;  // row stride of P
 
-template <typename T, int RQ, int CV>
+template <int RQ, int CV>
 struct SimtTile {
     static constexpr int BQ = 16 * RQ;
     static constexpr int VS = 64 * CV;
@@ -55,11 +55,9 @@ struct SimtTile {
     }
 
     // 4 consecutive elements of a row, zeros past n
-    static __device__ float4 load4(const T* p, int n, bool vec) {
-        if constexpr (sizeof(T) == 4) {
-            if (vec && n >= 4) return __ldg(reinterpret_cast<const float4*>(p));
-        }
-        return make_float4(n > 0 ? (float)p[0] : 0.f, n > 1 ? (float)p[1] : 0.f, n > 2 ? (float)p[2] : 0.f, n > 3 ? (float)p[3] : 0.f);
+    static __device__ float4 load4(const float* p, int n, bool vec) {
+        if (vec && n >= 4) return __ldg(reinterpret_cast<const float4*>(p));
+        return make_float4(n > 0 ? p[0] : 0.f, n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f, n > 3 ? p[3] : 0.f);
     }
 
     // Row r of the query tile is at row(r), nullptr for rows that do not exist (zeros).
@@ -68,14 +66,14 @@ struct SimtTile {
         const int n4 = dk4 / 4;
         for (int i = (int)threadIdx.x; i < BQ * n4; i += SS_THREADS) {
             const int r = i / n4, e = (i - r * n4) * 4;
-            const T* p = row(r);
+            const float* p = row(r);
             *reinterpret_cast<float4*>(&Qs[r * ks + e]) =
                 p != nullptr ? load4(p + e, dk - e, vec) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
     }
 
     // n keys (rows past n are zero: whatever lies there never reaches a product)
-    __device__ void load_kv(const T* K, int64_t ldk, const T* V, int64_t ldv, int n, bool vec) {
+    __device__ void load_kv(const float* K, int64_t ldk, const float* V, int64_t ldv, int n, bool vec) {
         const int k4 = dk4 / 4;
         for (int i = (int)threadIdx.x; i < SS_BK * k4; i += SS_THREADS) {
             const int j = i / k4, e = (i - j * k4) * 4;
@@ -173,34 +171,34 @@ struct SimtTile {
 
 // One block = BQ query rows of one (batch, head): the sinks below the rows' windows, then the keys
 // from the first row's window to the last row.
-template <typename T, int RQ, int CV>
+template <int RQ, int CV>
 __global__ void __launch_bounds__(SS_THREADS)
-    window_simt_kernel(const T* __restrict__ Q, int64_t ldq, const T* __restrict__ K, int64_t ldk,
-                       const T* __restrict__ V, int64_t ldv, const T* __restrict__ G, int64_t ldg,
-                       T* __restrict__ O, int64_t ldo, int h, int h_kv, int T_, int dk, int dv,
+    window_simt_kernel(const float* __restrict__ Q, int64_t ldq, const float* __restrict__ K, int64_t ldk,
+                       const float* __restrict__ V, int64_t ldv, const float* __restrict__ G, int64_t ldg,
+                       float* __restrict__ O, int64_t ldo, int h, int h_kv, int T, int dk, int dv,
                        int window, int sinks, const int32_t* __restrict__ kv_lengths, float scale_log2,
                        bool vec, int* status) {
-    using X = SimtTile<T, RQ, CV>;
+    using X = SimtTile<RQ, CV>;
     extern __shared__ __align__(16) float fsm[];
     X x(fsm, dk, dv);
     const int tid = (int)threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int b = (int)blockIdx.x / h, head = (int)blockIdx.x - b * h;
     const int kvh = head / (h / h_kv);
     const int q0 = (int)blockIdx.y * X::BQ;
-    const int L = kv_lengths != nullptr ? kv_lengths[b] : T_;
-    const int64_t row0 = (int64_t)b * T_ + q0;
-    if (L < 1 || L > T_) {
+    const int L = kv_lengths != nullptr ? kv_lengths[b] : T;
+    const int64_t row0 = (int64_t)b * T + q0;
+    if (L < 1 || L > T) {
         if (tid == 0) record_status(status, kStatusBadLength);
         for (int i = tid; i < X::BQ * dv; i += SS_THREADS) {
             const int r = i / dv;
-            if (q0 + r < T_) O[(row0 + r) * ldo + (int64_t)head * dv + (i - r * dv)] = (T)NAN;
+            if (q0 + r < T) O[(row0 + r) * ldo + (int64_t)head * dv + (i - r * dv)] = NAN;
         }
         return;
     }
-    x.load_q([&](int r) { return q0 + r < T_ ? Q + (row0 + r) * ldq + (int64_t)head * dk : nullptr; }, vec);
+    x.load_q([&](int r) { return q0 + r < T ? Q + (row0 + r) * ldq + (int64_t)head * dk : nullptr; }, vec);
     x.reset();
-    const T* Kb = K + (int64_t)b * T_ * ldk + (int64_t)kvh * dk;
-    const T* Vb = V + (int64_t)b * T_ * ldv + (int64_t)kvh * dv;
+    const float* Kb = K + (int64_t)b * T * ldk + (int64_t)kvh * dk;
+    const float* Vb = V + (int64_t)b * T * ldv + (int64_t)kvh * dv;
     const int end = min(L, q0 + X::BQ);
     int lo = max(0, q0 - window + 1);
     int s_end = min(sinks, L);  // sinks below the windows
@@ -223,28 +221,28 @@ __global__ void __launch_bounds__(SS_THREADS)
 #pragma unroll
     for (int r = 0; r < RQ; ++r) {
         const int t = ty * RQ + r;
-        if (q0 + t >= T_) continue;
+        if (q0 + t >= T) continue;
         const float inv = x.l[r] > 0.f ? 1.f / x.l[r] : 0.f;  // nothing visible: zeros
 #pragma unroll
         for (int u = 0; u < 4 * CV; ++u) {
             const int e = (u >> 2) * 64 + tx * 4 + (u & 3);
             if (e >= dv) continue;
             float y = x.o[r][u] * inv;
-            if (G != nullptr) y *= 1.f / (1.f + expf(-(float)G[(row0 + t) * ldg + (int64_t)head * dv + e]));
-            O[(row0 + t) * ldo + (int64_t)head * dv + e] = (T)y;
+            if (G != nullptr) y *= 1.f / (1.f + expf(-G[(row0 + t) * ldg + (int64_t)head * dv + e]));
+            O[(row0 + t) * ldo + (int64_t)head * dv + e] = y;
         }
     }
 }
 
-template <typename T, int RQ, int CV>
+template <int RQ, int CV>
 __global__ void __launch_bounds__(SS_THREADS)
-    span_simt_kernel(const SpanShape p, const SpanRecords rec, const T* __restrict__ Q, int64_t ldq,
-                     const T* __restrict__ K, int64_t ldk, const T* __restrict__ V, int64_t ldv,
-                     const T* __restrict__ Kp, int64_t ldkp, const T* __restrict__ Vp, int64_t ldvp,
-                     T* __restrict__ O, int64_t ldo, int dk, int dv,
+    span_simt_kernel(const SpanShape p, const SpanRecords rec, const float* __restrict__ Q, int64_t ldq,
+                     const float* __restrict__ K, int64_t ldk, const float* __restrict__ V, int64_t ldv,
+                     const float* __restrict__ Kp, int64_t ldkp, const float* __restrict__ Vp, int64_t ldvp,
+                     float* __restrict__ O, int64_t ldo, int dk, int dv,
                      const int32_t* __restrict__ lengths, float* __restrict__ scores, float scale_log2,
                      bool vec, int* status) {
-    using X = SimtTile<T, RQ, CV>;
+    using X = SimtTile<RQ, CV>;
     extern __shared__ __align__(16) float fsm[];
     X x(fsm, dk, dv);
     const int tid = (int)threadIdx.x, tx = tid & 15, ty = tid >> 4;
@@ -271,15 +269,15 @@ __global__ void __launch_bounds__(SS_THREADS)
             t = rr % p.T_q;
         };
         __syncthreads();  // the previous piece's tiles are no longer read
-        x.load_q([&](int r) -> const T* {
+        x.load_q([&](int r) -> const float* {
             if (r >= nr) return nullptr;
             int b, head, t;
             where(r, b, head, t);
             return Q + ((int64_t)b * p.T_q + t) * ldq + (int64_t)head * dk;
         }, vec);
         x.reset();
-        const T* Kb = q.prefix ? Kp + (int64_t)q.g * dk : K + (int64_t)q.b * p.T_max * ldk + (int64_t)q.g * dk;
-        const T* Vb = q.prefix ? Vp + (int64_t)q.g * dv : V + (int64_t)q.b * p.T_max * ldv + (int64_t)q.g * dv;
+        const float* Kb = q.prefix ? Kp + (int64_t)q.g * dk : K + (int64_t)q.b * p.T_max * ldk + (int64_t)q.g * dk;
+        const float* Vb = q.prefix ? Vp + (int64_t)q.g * dv : V + (int64_t)q.b * p.T_max * ldv + (int64_t)q.g * dv;
         const int64_t lk = q.prefix ? ldkp : ldk, lv = q.prefix ? ldvp : ldv;
         for (int i = q.i0; i < q.i1; ++i) {
             int k0, n;
@@ -303,19 +301,18 @@ __global__ void __launch_bounds__(SS_THREADS)
             const int rr = ty * RQ + r;
             if (rr >= nr) continue;
             if (tx == 0 && (!direct || scores != nullptr)) rec.ml[slot + rr] = make_float2(x.m[r], x.l[r]);
-            float* part = rec.o + (slot + rr) * dv;
-            int b, head, t;
-            where(rr, b, head, t);
-            T* out = O + ((int64_t)b * p.T_q + t) * ldo + (int64_t)head * dv;
-            const float inv = 1.f / x.l[r];
+            float* out = rec.o + (slot + rr) * dv;
+            float inv = 1.f;
+            if (direct) {
+                int b, head, t;
+                where(rr, b, head, t);
+                out = O + ((int64_t)b * p.T_q + t) * ldo + (int64_t)head * dv;
+                inv = 1.f / x.l[r];
+            }
 #pragma unroll
             for (int u = 0; u < 4 * CV; ++u) {
                 const int e = (u >> 2) * 64 + tx * 4 + (u & 3);
-                if (e >= dv) continue;
-                if (direct)
-                    out[e] = (T)(x.o[r][u] * inv);
-                else
-                    part[e] = x.o[r][u];
+                if (e < dv) out[e] = x.o[r][u] * inv;
             }
         }
     }
@@ -325,9 +322,8 @@ __global__ void __launch_bounds__(SS_THREADS)
 
 int span_simt_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
-template <typename E>
-static cudaError_t launch_window(const E* Q, int64_t ldq, const E* K, int64_t ldk, const E* V,
-                              int64_t ldv, const E* G, int64_t ldg, E* O, int64_t ldo, int B, int h,
+cudaError_t launch_window_f32(const float* Q, int64_t ldq, const float* K, int64_t ldk, const float* V,
+                              int64_t ldv, const float* G, int64_t ldg, float* O, int64_t ldo, int B, int h,
                               int h_kv, int T, int d_k, int d_v, int window, int sinks,
                               const int32_t* kv_lengths, int* status, cudaStream_t stream) {
     auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
@@ -345,16 +341,15 @@ static cudaError_t launch_window(const E* Q, int64_t ldq, const E* K, int64_t ld
     };
 #define MHA_WS(RQ, CV) \
     if ((small ? 2 : 4) == RQ && cv == CV) \
-        return launch(window_simt_kernel<E, RQ, CV>, SimtTile<E, RQ, CV>::smem_bytes(d_k), 16 * RQ);
+        return launch(window_simt_kernel<RQ, CV>, SimtTile<RQ, CV>::smem_bytes(d_k), 16 * RQ);
     MHA_WS(2, 1) MHA_WS(2, 2) MHA_WS(2, 3) MHA_WS(2, 4) MHA_WS(4, 1) MHA_WS(4, 2) MHA_WS(4, 3) MHA_WS(4, 4)
 #undef MHA_WS
     return cudaErrorInvalidValue;
 }
 
-template <typename E>
-static cudaError_t launch_span(const SpanShape& p, const SpanRecords& rec, int bm, const E* Q, int64_t ldq,
-                            const E* K, int64_t ldk, const E* V, int64_t ldv, const E* Kp,
-                            int64_t ldkp, const E* Vp, int64_t ldvp, E* O, int64_t ldo, int d_k, int d_v,
+cudaError_t launch_span_f32(const SpanShape& p, const SpanRecords& rec, int bm, const float* Q, int64_t ldq,
+                            const float* K, int64_t ldk, const float* V, int64_t ldv, const float* Kp,
+                            int64_t ldkp, const float* Vp, int64_t ldvp, float* O, int64_t ldo, int d_k, int d_v,
                             const int32_t* lengths, float* scores, int gangs, int* status,
                             cudaStream_t stream) {
     auto al = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
@@ -369,37 +364,11 @@ static cudaError_t launch_span(const SpanShape& p, const SpanRecords& rec, int b
                           ldk, V, ldv, Kp, ldkp, Vp, ldvp, O, ldo, d_k, d_v, lengths, scores, scale, vec, status);
     };
 #define MHA_SS(RQ, CV) \
-    if (bm == 16 * RQ && cv == CV) return launch(span_simt_kernel<E, RQ, CV>, SimtTile<E, RQ, CV>::smem_bytes(d_k));
+    if (bm == 16 * RQ && cv == CV) return launch(span_simt_kernel<RQ, CV>, SimtTile<RQ, CV>::smem_bytes(d_k));
     MHA_SS(1, 1) MHA_SS(1, 2) MHA_SS(1, 3) MHA_SS(1, 4) MHA_SS(2, 1) MHA_SS(2, 2) MHA_SS(2, 3) MHA_SS(2, 4)
     MHA_SS(4, 1) MHA_SS(4, 2) MHA_SS(4, 3) MHA_SS(4, 4)
 #undef MHA_SS
     return cudaErrorInvalidValue;
-}
-
-cudaError_t launch_window_f32(const float* Q, int64_t ldq, const float* K, int64_t ldk, const float* V,
-                              int64_t ldv, const float* G, int64_t ldg, float* O, int64_t ldo, int B, int h,
-                              int h_kv, int T, int d_k, int d_v, int window, int sinks,
-                              const int32_t* kv_lengths, int* status, cudaStream_t stream) {
-    return launch_window(Q, ldq, K, ldk, V, ldv, G, ldg, O, ldo, B, h, h_kv, T, d_k, d_v, window, sinks, kv_lengths,
-                         status, stream);
-}
-
-cudaError_t launch_window_bf16(const void* Q, int64_t ldq, const void* K, int64_t ldk, const void* V,
-                               int64_t ldv, const void* G, int64_t ldg, void* O, int64_t ldo, int B, int h,
-                               int h_kv, int T, int d, int window, int sinks, const int32_t* kv_lengths,
-                               int, int* status, cudaStream_t stream) {
-    auto f = [](const void* x) { return static_cast<const __nv_bfloat16*>(x); };
-    return launch_window(f(Q), ldq, f(K), ldk, f(V), ldv, f(G), ldg, static_cast<__nv_bfloat16*>(O), ldo, B, h, h_kv, T,
-                         d, d, window, sinks, kv_lengths, status, stream);
-}
-
-cudaError_t launch_span_f32(const SpanShape& p, const SpanRecords& rec, int bm, const float* Q, int64_t ldq,
-                            const float* K, int64_t ldk, const float* V, int64_t ldv, const float* Kp,
-                            int64_t ldkp, const float* Vp, int64_t ldvp, float* O, int64_t ldo, int d_k, int d_v,
-                            const int32_t* lengths, float* scores, int gangs, int* status,
-                            cudaStream_t stream) {
-    return launch_span(p, rec, bm, Q, ldq, K, ldk, V, ldv, Kp, ldkp, Vp, ldvp, O, ldo, d_k, d_v, lengths, scores,
-                       gangs, status, stream);
 }
 
 }  // namespace mha
