@@ -126,21 +126,21 @@ cudaError_t launch_window_bf16(const void* Q, int64_t ldq, const void* K, int64_
                                int h_kv, int T, int d, int window, int sinks, const int32_t* kv_lengths,
                                int num_sms, int* status, cudaStream_t stream);
 
-// A cache step (span.cuh) by `gangs` gangs of p.gang CTAs each.  scores (nullable): room for the base-2
+// A cache step (span.cuh) by `ctas` CTAs.  scores (nullable): room for the base-2
 // scores of every query row, [B][h_kv][rows][score_ld]; weights (nullable, with scores): the accumulated
-// attention weights.  bf16: one launch, status the first word of the status block.  fp32: the pieces, which
-// launch_span_merge then joins (bm: query rows of a row block).
+// attention weights.  bf16: one launch, status the first of four words of the status block.  fp32: the units, which
+// launch_span_merge then joins.
 int span_simt_rows(int64_t rows);  // row block of launch_span_f32: 16, 32 or 64
-cudaError_t launch_span_f32(const SpanShape& p, const SpanRecords& rec, int bm, const float* Q, int64_t ldq,
+cudaError_t launch_span_f32(const SpanShape& p, const SpanRecords& rec, const float* Q, int64_t ldq,
                             const float* K, int64_t ldk, const float* V, int64_t ldv, const float* Kp,
                             int64_t ldkp, const float* Vp, int64_t ldvp, float* O, int64_t ldo, int d_k, int d_v,
-                            const int32_t* lengths, float* scores, int gangs, int* status,
+                            const int32_t* lengths, float* scores, int ctas, int* status,
                             cudaStream_t stream);
 cudaError_t launch_span_bf16(const SpanShape& p, const SpanRecords& rec, const void* Q, int64_t ldq, const void* K,
                              int64_t ldk, const void* V, int64_t ldv, const void* Kp, int64_t ldkp, const void* Vp,
                              int64_t ldvp, void* O, int64_t ldo, int d, const int32_t* lengths, float* scores,
-                             float* weights, int gangs, int* status, cudaStream_t stream);
-cudaError_t launch_span_merge(const SpanShape& p, const SpanRecords& rec, int bm, int gangs, float* O, int64_t ldo,
+                             float* weights, int ctas, int* status, cudaStream_t stream);
+cudaError_t launch_span_merge(const SpanShape& p, const SpanRecords& rec, int ctas, float* O, int64_t ldo,
                               const int32_t* lengths, const float* scores, float* weights, cudaStream_t stream);
 
 // Selection and row moves of mha_cache_evict (in place when K == Ko).

@@ -1,37 +1,30 @@
-// span.cuh -- how the cache operators (windowed, shared-prefix and weight-accumulating decode
-// steps) cut their work, shared by the kernels that compute the pieces and those that join them.
+// span.cuh -- how the cache operators (windowed, shared-prefix and weight-accumulating decode steps) cut
+// their work, shared by the kernels that compute the units and those that join them.
 //
-// The query rows that share cached keys form groups: one per (batch, K/V head, row block) over the
-// batch's own cache, and, with a shared prefix, one per (K/V head, row block) over the prefix, whose
-// rows are those of the whole batch.  A group's visible keys are at most two ranges, the sinks
-// [0, s) and the window [lo, L), each cut into tiles.
-//
-// The CTAs work in gangs of H: the member CTAs of a gang walk the same tiles of H neighbouring lanes
-// (K/V head, row block) side by side.  A cached token's rows of all heads lie side by side, so what a
-// gang reads at a time is whole pieces of DRAM pages: 32 sequences of 16 heads with d = 128 ran at 54% of
-// the copy bandwidth without gangs (each CTA somewhere else, 256 bytes at a time).  The tiles of
-// all batches and lane blocks in order form one sequence of N, which D = min(gangs, N) gangs divide
-// evenly: gang c takes tiles [N c / D, N (c + 1) / D), so ragged lengths and group counts that do not
-// divide the SMs leave no CTA idle.  A gang's run crosses group borders; each crossing starts a piece.
-// A piece that holds a whole group writes its output itself; the others leave (maximum, sum, weighted
-// values) records that the merge joins:
-//   O = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p,  M = max_p m_p   (scores in base 2).
-// Record slot of a piece: (gang + block index in the sequence) H + member.  Gang and block only grow
-// along the sequence and one of them does at every piece, so slots are distinct.
+// The query rows that share cached keys form groups: one per (batch, lane) over the batch's own cache,
+// and, with a shared prefix, one per lane over the prefix, whose rows are those of the whole batch; a lane is
+// a (K/V head, block of at most bm query rows).  A group's visible keys are at most two ranges, the sinks
+// [0, s) and the window [lo, L), each cut into tiles.  A unit is U consecutive tiles of one group (Up of a
+// prefix group): the CTAs take units one after another, so ragged lengths, group counts that do not
+// divide the SMs and SMs that are slower than others leave none idle (an even cut made beforehand left the
+// first CTA idle for a fifth of a step).  Units are numbered prefix first, then by batch, chunk and lane,
+// lanes fastest: a cached token's rows of all heads lie side by side, and units taken at about the same
+// time read whole pieces of DRAM pages.  U is chosen so that every CTA gets about kSpanUnits units, but no
+// unit's record of its rows costs more than a few percent of the unit.  A unit that holds a whole
+// group writes its output itself; the others leave a record per row (maximum, sum, weighted values), and
+// the join adds them in order:
+//   O = sum_u 2^(m_u - M) o_u / sum_u 2^(m_u - M) l_u,  M = max_u m_u   (scores in base 2).
+// Everything follows from the lengths alone, not from which CTA took what.
 #pragma once
 
 #include <stdint.h>
 
 namespace mha {
 
-// Ending a piece (joining its streams, writing its rows, starting the next) takes about as long as a tile:
-// every group occupies that many places more in the sequence than it has tiles, so that a gang with many
-// short groups gets fewer tiles.  Nothing is read for those places.
-constexpr int kSpanPieceCost = 1;
-
-// Largest grid of a piece kernel (bounds the record slots; the host knows no SM count when it
-// computes workspace sizes).
+// Largest grid of the unit kernels (bounds the records; the host knows no SM count when it computes
+// workspace sizes), and units per CTA to aim for.
 constexpr int kSpanMaxCtas = 320;
+constexpr int kSpanUnits = 10;
 
 struct SpanShape {
     int B, h_kv;
@@ -41,26 +34,23 @@ struct SpanShape {
     int nrb;     // row blocks of such a group
     int T_p;     // shared prefix tokens (0: none)
     int nrbp;    // row blocks of the B * rows rows over the prefix
+    int bm;      // rows of a row block
     int window;  // <= T_max; T_max: no window
     int sinks;
-    int gang;    // H: divides h_kv * nrb and h_kv * nrbp
 
-    __host__ __device__ int blocks_c() const { return h_kv * nrb / gang; }   // lane blocks of a batch
-    __host__ __device__ int blocks_p() const { return h_kv * nrbp / gang; }  // of the prefix
+    __host__ __device__ int lanes_c() const { return h_kv * nrb; }
+    __host__ __device__ int lanes_p() const { return h_kv * nrbp; }
+    // rows of a record; fewest tiles of a unit whose records stay cheap beside its tiles
+    __host__ __device__ int rps_c() const { return rows < bm ? rows : bm; }
+    __host__ __device__ int rps_p() const { return (int64_t)B * rows < bm ? B * rows : bm; }
+    __host__ __device__ int least_c() const { return (rps_c() + 15) / 16; }
+    __host__ __device__ int least_p() const { return (rps_p() + 15) / 16; }
 };
 
-// The largest gang that leaves at most 3% of the CTAs without one.
-inline int span_gang(const SpanShape& p, int ctas) {
-    for (int H = p.h_kv * p.nrb; H > 1; --H)
-        if (p.h_kv * p.nrb % H == 0 && p.h_kv * p.nrbp % H == 0 && ctas / H * H * 100 >= ctas * 97) return H;
-    return 1;
-}
-
-// The visible keys of a batch with L cached tokens: [0, s_keys) and [lo, L); nt tiles in all (0 for
-// an invalid length).
+// The visible keys of a batch with L cached tokens: [0, s_keys) and [lo, L); nst sink tiles, nt tiles in all
+// (0 for an invalid length).
 struct SpanView {
     int L, s_keys, lo, nst, nt;
-    __host__ __device__ int places() const { return nt > 0 ? nt + kSpanPieceCost : 0; }  // in the sequence
 };
 
 template <int TILE>
@@ -101,173 +91,132 @@ __host__ __device__ inline int span_prefix_tiles(const SpanShape& p) {
     return (p.T_p + TILE - 1) / TILE;
 }
 
-// Places of the sequence that the prefix's groups take.
+// Most tiles of all groups together (the host checks that they fit 32 bits and launches no more CTAs).
 template <int TILE>
-__host__ __device__ inline int span_prefix_places(const SpanShape& p) {
-    return p.T_p > 0 ? (span_prefix_tiles<TILE>(p) + kSpanPieceCost) * p.blocks_p() : 0;
-}
-
-// Gangs that share N tiles when G are launched: each of them holds at least one.
-__host__ __device__ inline int span_parts(int N, int G) { return N < G ? N : G; }
-
-// a * b / c, in 32 bits where the product fits (a 64-bit division costs several hundred cycles)
-__device__ __forceinline__ int span_muldiv(int a, int b, int add, int c) {
-    if (a < (1 << 21) && b <= 1024) return (int)(((unsigned)a * (unsigned)b + (unsigned)add) / (unsigned)c);
-    return (int)(((int64_t)a * b + add) / c);
-}
-
-// Gangs [c0, c1] that hold places [t0, t1) of N when G divide them.
-__device__ __forceinline__ void span_gangs(int N, int G, int t0, int t1, int& c0, int& c1) {
-    const int D = span_parts(N, G);
-    c0 = span_muldiv(t0, D, D - 1, N);  // ((t0 + 1) D - 1) / N
-    c1 = span_muldiv(t1, D, -1, N);
-}
-
-// Places of the sequence if every batch had the longest cache (the host checks that they fit 32 bits and
-// launches no more gangs).
-template <int TILE>
-inline int64_t span_most_places(const SpanShape& p) {
+inline int64_t span_most_tiles(const SpanShape& p) {
     const int64_t all = ((int64_t)p.T_max + TILE - 1) / TILE;
     const int64_t win = ((int64_t)p.sinks + TILE - 1) / TILE + ((int64_t)p.window + p.T_q - 1 + TILE - 1) / TILE;
-    const int64_t pre = p.T_p > 0 ? ((int64_t)span_prefix_tiles<TILE>(p) + kSpanPieceCost) * p.blocks_p() : 0;
-    return pre + (int64_t)p.B * p.blocks_c() * ((all < win ? all : win) + kSpanPieceCost);
+    return (int64_t)span_prefix_tiles<TILE>(p) * p.lanes_p() + (int64_t)p.B * p.lanes_c() * (all < win ? all : win);
 }
 
-// Where a gang starts in the tile sequence.
-struct SpanStart {
-    int N;       // tiles in all
-    int t0, t1;  // this gang's tiles
-    int b;       // batch that holds the gang's first tile past the prefix
-    int off;     // first tile of that batch's lane blocks
+// Most records (units) of the prefix and of the caches, for any lengths and any grid up to kSpanMaxCtas:
+// U tiles a unit, U at least total / (kSpanUnits * CTAs), leave at most that many units and a rest per group.
+template <int TILE>
+inline void span_most_units(const SpanShape& p, int64_t& units_p, int64_t& units_c) {
+    const int64_t cap = (int64_t)kSpanUnits * kSpanMaxCtas;
+    const int64_t np = span_prefix_tiles<TILE>(p), nt = ((int64_t)p.T_max + TILE - 1) / TILE + 1;
+    const int64_t lp = p.lanes_p(), lc = (int64_t)p.B * p.lanes_c();
+    const int64_t ap = (np + p.least_p() - 1) / p.least_p() * lp, ac = (nt + p.least_c() - 1) / p.least_c() * lc;
+    units_p = ap < cap + lp ? ap : cap + lp;
+    units_c = ac < cap + lc ? ac : cap + lc;
+}
+
+// The cut, from the lengths; and one lane's part of its prefix sums over the batches.
+struct SpanPlan {
+    int U, Up;   // tiles of a unit
+    int np;      // units of the prefix
+    int N;       // units in all
 };
 
-// The sequence as seen from its prefix sums over the batches: all lanes of a warp call it and get N, the
-// batch that holds tile want(N) (of the batches' own tiles) and that batch's first tile.  A lane sums a
-// run of consecutive batches; loads only, no block-wide step.
-template <int TILE, typename F>
-__device__ __forceinline__ void span_find(const SpanShape& p, const int32_t* lengths, F want, int& N, int& b, int& off) {
+struct SpanSums {
+    int i0, i1;       // this lane's batches
+    int before, sum;  // first unit of batch i0, units of the lane's batches
+};
+
+// All lanes of a warp call it; ctas: the grid of the unit kernel.
+template <int TILE>
+__device__ inline SpanPlan span_plan(const SpanShape& p, const int32_t* lengths, int ctas, SpanSums& s) {
     const int lane = (int)threadIdx.x & 31;
-    const int run = (p.B + 31) / 32, i0 = lane * run, i1 = min(p.B, i0 + run);
-    const int npt = span_prefix_places<TILE>(p);
-    int sum = 0;
-    for (int i = i0; i < i1; ++i) sum += span_view<TILE>(p, lengths[i]).places() * p.blocks_c();
-    int inc = sum;
+    const int run = (p.B + 31) / 32;
+    s.i0 = min(p.B, lane * run);
+    s.i1 = min(p.B, s.i0 + run);
+    int tiles = 0;
+    for (int i = s.i0; i < s.i1; ++i) tiles += span_view<TILE>(p, __ldcg(lengths + i)).nt;
+    const int np = span_prefix_tiles<TILE>(p);
+    const unsigned total = __reduce_add_sync(0xffffffffu, (unsigned)tiles) * (unsigned)p.lanes_c() + (unsigned)(np * p.lanes_p());
+    const unsigned target = (unsigned)(kSpanUnits * ctas);
+    SpanPlan q;
+    q.U = max(p.least_c(), (int)((total + target - 1) / target));
+    q.U = max(q.U, 1);
+    q.Up = max(max(q.U, p.least_p()), (np * p.lanes_p() + ctas - 1) / ctas);
+    q.np = p.T_p > 0 ? (np + q.Up - 1) / q.Up * p.lanes_p() : 0;
+    s.sum = 0;
+    for (int i = s.i0; i < s.i1; ++i) s.sum += (span_view<TILE>(p, __ldcg(lengths + i)).nt + q.U - 1) / q.U * p.lanes_c();
+    int inc = s.sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += u;
     }
-    N = npt + __shfl_sync(0xffffffffu, inc, 31);
-    const int t = want(N);
-    int before = npt + inc - sum, found = 0;
-    const bool mine = before <= t && t < before + sum;
-    if (mine)
-        for (int i = i0; i < i1; ++i) {
-            const int n = span_view<TILE>(p, lengths[i]).places() * p.blocks_c();
-            if (t < before + n) {
-                found = i;
-                break;
-            }
-            before += n;
-        }
-    const unsigned who = __ballot_sync(0xffffffffu, mine);
-    const int src = who ? __ffs(who) - 1 : 0;
-    b = __shfl_sync(0xffffffffu, found, src);
-    off = __shfl_sync(0xffffffffu, before, src);
+    s.before = q.np + inc - s.sum;
+    q.N = q.np + __shfl_sync(0xffffffffu, inc, 31);
+    return q;
 }
 
-// This gang's share of the sequence; all lanes of a warp call it.
+// First unit of batch b (all lanes of a warp; b the same in all).
 template <int TILE>
-__device__ __forceinline__ SpanStart span_start(const SpanShape& p, const int32_t* lengths) {
-    const int gangs = (int)gridDim.x / p.gang, c = (int)blockIdx.x / p.gang;
-    const int npt = span_prefix_places<TILE>(p);
-    SpanStart s;
-    span_find<TILE>(p, lengths, [&](int N) {
-        const int D = span_parts(N, gangs);
-        s.t0 = c < D ? span_muldiv(N, c, 0, D) : N;
-        s.t1 = c < D ? span_muldiv(N, c + 1, 0, D) : N;
-        return max(s.t0, npt);
-    }, s.N, s.b, s.off);
-    return s;
+__device__ __forceinline__ int span_first_unit(const SpanShape& p, const int32_t* lengths, const SpanPlan& q, const SpanSums& s,
+                                               int b) {
+    int at = 0;
+    const bool mine = s.i0 <= b && b < s.i1;
+    if (mine) {
+        at = s.before;
+        for (int i = s.i0; i < b; ++i) at += (span_view<TILE>(p, __ldcg(lengths + i)).nt + q.U - 1) / q.U * p.lanes_c();
+    }
+    return __shfl_sync(0xffffffffu, at, __ffs(__ballot_sync(0xffffffffu, mine)) - 1);
 }
 
-// One contiguous run of tiles within one group.
-struct SpanPiece {
-    bool prefix;
+struct SpanUnit {
+    int unit;        // -1: no more
+    int prefix;
     int b, g, rb;
-    int block;   // lane block's index in the sequence
-    int i0, i1;  // tiles [i0, i1) of the group
-    SpanView v;  // the batch's view (prefix: L = T_p, one range)
+    int i0, i1;      // tiles [i0, i1) of the group
+    SpanView v;      // the batch's view (prefix: L = T_p, one range)
     __device__ bool whole() const { return i0 == 0 && i1 == v.nt; }
 };
 
-// Walks a gang's pieces in order.  Divisions only at the start: afterwards the walk steps from group to
-// group.
+// Unit u < N (all lanes of a warp; every lane gets it).
 template <int TILE>
-struct SpanWalk {
-    const SpanShape& p;
-    const int32_t* lengths;
-    int left;   // places left
-    int in;     // next place within the current group
-    int bl;     // current lane block within its batch (or within the prefix)
-    int b;      // current batch; -1: the prefix
-    int first;  // first batch after the prefix
-    SpanView v;
-
-    __device__ SpanWalk(const SpanShape& p_, const int32_t* lengths_, const SpanStart& s)
-        : p(p_), lengths(lengths_), left(s.t1 - s.t0), in(0), bl(0), b(s.b), first(s.b) {
-        if (left <= 0) return;
-        const int npt = span_prefix_places<TILE>(p);
-        int at = s.t0 - s.off;  // within the batch's groups
-        if (s.t0 < npt) {
-            at = s.t0;
-            b = -1;
-            prefix_view();
-        } else {
-            v = span_view<TILE>(p, lengths[b]);
-        }
-        bl = at / v.places();
-        in = at - bl * v.places();
-    }
-
-    __device__ void prefix_view() {
-        v.L = p.T_p;
-        v.s_keys = v.lo = v.nst = 0;
-        v.nt = span_prefix_tiles<TILE>(p);
-    }
-
-    __device__ void next_batch() {
-        bl = 0;
-        b = b < 0 ? first : b + 1;
-        v = span_view<TILE>(p, lengths[b]);
-    }
-
-    // The next piece, or false (and q as it was) at the end.
-    __device__ bool next(SpanPiece& q) {
-        while (left > 0) {
-            if (in == v.places()) {  // the next group; batches without a tile are passed over
-                in = 0;
-                ++bl;
-                if (bl == (b < 0 ? p.blocks_p() : p.blocks_c())) next_batch();
-                while (v.nt == 0) next_batch();
+__device__ inline SpanUnit span_unit(const SpanShape& p, const int32_t* lengths, const SpanPlan& q, const SpanSums& s, int u) {
+    SpanUnit x;
+    x.unit = u;
+    int k, lane_i, U, nrb;
+    if (u < q.np) {
+        x.prefix = 1;
+        x.b = 0;
+        x.v.L = p.T_p;
+        x.v.s_keys = x.v.lo = x.v.nst = 0;
+        x.v.nt = span_prefix_tiles<TILE>(p);
+        k = u / p.lanes_p();
+        lane_i = u - k * p.lanes_p();
+        U = q.Up;
+        nrb = p.nrbp;
+    } else {
+        x.prefix = 0;
+        int b = 0, at = 0;
+        const bool mine = s.before <= u && u < s.before + s.sum;
+        if (mine) {
+            at = s.before;
+            for (b = s.i0;; ++b) {
+                const int n = (span_view<TILE>(p, __ldcg(lengths + b)).nt + q.U - 1) / q.U * p.lanes_c();
+                if (u < at + n) break;
+                at += n;
             }
-            const int i0 = in, end = min(v.places(), in + left);
-            left -= end - in;
-            in = end;
-            if (i0 >= v.nt) continue;
-            q.prefix = b < 0;
-            q.v = v;
-            q.i0 = i0;
-            q.i1 = min(v.nt, end);
-            q.b = b < 0 ? 0 : b;
-            const int lane = bl * p.gang + (int)blockIdx.x % p.gang, nrb = b < 0 ? p.nrbp : p.nrb;
-            q.g = nrb == 1 ? lane : lane / nrb;
-            q.rb = nrb == 1 ? 0 : lane - q.g * nrb;
-            q.block = b < 0 ? bl : p.blocks_p() + b * p.blocks_c() + bl;
-            return true;
         }
-        return false;
+        const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+        x.b = __shfl_sync(0xffffffffu, b, src);
+        at = __shfl_sync(0xffffffffu, at, src);
+        x.v = span_view<TILE>(p, __ldcg(lengths + x.b));
+        k = (u - at) / p.lanes_c();
+        lane_i = u - at - k * p.lanes_c();
+        U = q.U;
+        nrb = p.nrb;
     }
-};
+    x.g = lane_i / nrb;
+    x.rb = lane_i - x.g * nrb;
+    x.i0 = k * U;
+    x.i1 = min(x.v.nt, x.i0 + U);
+    return x;
+}
 
 }  // namespace mha

@@ -17,7 +17,7 @@ namespace {
 // holds the rows (a thread of the CUDA-core kernel owns 1, 2 or 4 of them).
 int row_block(const mha_s* m, int64_t rows) { return m->dtype == MHA_BF16 ? 128 : span_simt_rows(rows); }
 
-SpanShape span_shape(const mha_s* m, int B, int T_q, int T_max, int T_p, int window, int sinks, int* bm) {
+SpanShape span_shape(const mha_s* m, int B, int T_q, int T_max, int T_p, int window, int sinks) {
     SpanShape p;
     p.B = B;
     p.h_kv = m->h_kv;
@@ -28,13 +28,16 @@ SpanShape span_shape(const mha_s* m, int B, int T_q, int T_max, int T_p, int win
     p.T_p = T_p;
     // a prefix's rows are those of the whole batch
     const int64_t rows_p = (int64_t)B * p.rows;
-    *bm = row_block(m, T_p > 0 ? rows_p : p.rows);
-    p.nrb = (p.rows + *bm - 1) / *bm;
-    p.nrbp = T_p > 0 ? (int)((rows_p + *bm - 1) / *bm) : 0;
+    p.bm = row_block(m, T_p > 0 ? rows_p : p.rows);
+    p.nrb = (p.rows + p.bm - 1) / p.bm;
+    p.nrbp = T_p > 0 ? (int)((rows_p + p.bm - 1) / p.bm) : 0;
     p.window = window < T_max ? window : T_max;
     p.sinks = sinks < T_max ? sinks : T_max;
-    p.gang = 1;
     return p;
+}
+
+SpanLayout layout(const mha_s* m, const SpanShape& p, bool scores) {
+    return m->dtype == MHA_F32 ? span_layout<64>(p, m->dv, scores) : span_layout<128>(p, m->dv, scores);
 }
 
 // Bytes from the first to the last element of `rows` rows of `width` elements.
@@ -98,16 +101,13 @@ mha_status run_cache_step(mha_s* m, const CacheStep& a, cudaStream_t stream) {
         if (overlaps(a.O, obytes, x.p, x.n) || overlaps(a.weights, wbytes, x.p, x.n)) return MHA_ERR_INVALID_ARG;
     if (overlaps(a.O, obytes, a.weights, wbytes)) return MHA_ERR_INVALID_ARG;
 
-    int bm;
-    SpanShape p = span_shape(m, a.B, a.T_q, a.T_max, a.T_p, a.window, a.sinks, &bm);
-    const SpanLayout w = span_layout(p, m->dv, bm, a.weights != nullptr);
+    const SpanShape p = span_shape(m, a.B, a.T_q, a.T_max, a.T_p, a.window, a.sinks);
+    const SpanLayout w = layout(m, p, a.weights != nullptr);
     if (m->ws == nullptr || m->ws_bytes < kStatusBytes + w.total) return MHA_ERR_WORKSPACE;
     uint8_t* ws = static_cast<uint8_t*>(m->ws) + kStatusBytes;
     SpanRecords rec;
     rec.ml = reinterpret_cast<float2*>(ws + w.ml_off);
     rec.o = reinterpret_cast<float*>(ws + w.o_off);
-    rec.rps_p = w.rps_p;
-    rec.rps_c = w.rps_c;
     rec.base_c = w.base_c;
     rec.dv = m->dv;
     float* scores = a.weights != nullptr ? reinterpret_cast<float*>(ws + w.s_off) : nullptr;
@@ -117,21 +117,20 @@ mha_status run_cache_step(mha_s* m, const CacheStep& a, cudaStream_t stream) {
     // one CTA per SM holds the tensor-core kernel's tiles, two the CUDA-core kernel's
     int ctas = m->dtype == MHA_F32 ? 2 * sms : sms;
     if (ctas > kSpanMaxCtas) ctas = kSpanMaxCtas;
-    p.gang = span_gang(p, ctas);
-    const int64_t most = m->dtype == MHA_F32 ? span_most_places<64>(p) : span_most_places<128>(p);
+    const int64_t most = m->dtype == MHA_F32 ? span_most_tiles<64>(p) : span_most_tiles<128>(p);
     if (most > INT32_MAX) return MHA_ERR_UNSUPPORTED;
-    const int gangs = most < ctas / p.gang ? (int)most : ctas / p.gang;
+    if (most < ctas) ctas = (int)most;
     cudaError_t err;
     if (m->dtype == MHA_F32) {
         auto f = [](const void* x) { return static_cast<const float*>(x); };
         float* O = static_cast<float*>(a.O);
-        err = launch_span_f32(p, rec, bm, f(a.Q), a.ldq, f(a.K), a.ldk, f(a.V), a.ldv, f(a.Kp), a.ldkp, f(a.Vp),
-                              a.ldvp, O, a.ldo, m->dk, m->dv, a.lengths, scores, gangs, status_ptr(m), stream);
+        err = launch_span_f32(p, rec, f(a.Q), a.ldq, f(a.K), a.ldk, f(a.V), a.ldv, f(a.Kp), a.ldkp, f(a.Vp),
+                              a.ldvp, O, a.ldo, m->dk, m->dv, a.lengths, scores, ctas, status_ptr(m), stream);
         if (err == cudaSuccess)
-            err = launch_span_merge(p, rec, bm, gangs, O, a.ldo, a.lengths, scores, a.weights, stream);
+            err = launch_span_merge(p, rec, ctas, O, a.ldo, a.lengths, scores, a.weights, stream);
     } else {
         err = launch_span_bf16(p, rec, a.Q, a.ldq, a.K, a.ldk, a.V, a.ldv, a.Kp, a.ldkp, a.Vp, a.ldvp, a.O, a.ldo,
-                               m->dk, a.lengths, scores, a.weights, gangs, status_ptr(m), stream);
+                               m->dk, a.lengths, scores, a.weights, ctas, status_ptr(m), stream);
     }
     return err == cudaSuccess ? MHA_OK : MHA_ERR_CUDA;
 }
@@ -207,9 +206,7 @@ mha_status mha_forward_window(mha_t handle, const void* X, int B, int T, const v
 size_t mha_cache_step_workspace_size(mha_t handle, int B, int T_q, int T_prefix, int T_max, int weights) {
     if (handle == nullptr || !step_sizes_ok(handle, B, T_q, T_prefix, T_max)) return 0;
     if (B == 0 || T_q == 0 || T_max == 0) return kStatusBytes;
-    int bm;
-    const SpanShape p = span_shape(handle, B, T_q, T_max, T_prefix, T_max, 0, &bm);
-    return kStatusBytes + span_layout(p, handle->dv, bm, weights != 0).total;
+    return kStatusBytes + layout(handle, span_shape(handle, B, T_q, T_max, T_prefix, T_max, 0), weights != 0).total;
 }
 
 mha_status mha_decode_window(mha_t handle, int B, int T_q, int T_max, const void* Q, int64_t ldq, const void* K_cache,

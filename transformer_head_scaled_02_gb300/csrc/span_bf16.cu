@@ -2,33 +2,34 @@
 // prefix and weight-accumulating decode steps (span.cuh).
 //
 // Bound by HBM for the few query rows of a decode step: every visible cached key and value is read once,
-// 4 d bytes per token and K/V head.  A persistent CTA per SM takes an even run of 128-key tiles from the
-// sequence of all groups (span.cuh); its TMA ring, MMAs and softmax run on across the borders between
-// pieces, so neither ragged lengths nor many short windows leave the memory system idle.
+// 4 d bytes per token and K/V head.  Persistent CTAs, one per SM, take units of 128-key tiles (span.cuh) from a
+// counter; the TMA ring, the MMAs and the softmax run on across the borders between units.
 //
-// The up to 128 query rows of a piece form one tile (rows past them hold whatever lies in shared memory:
+// The up to 128 query rows of a unit form one tile (rows past them hold whatever lies in shared memory:
 // each row's results depend on that row alone).  Alternate key tiles go to two streams, each with its own
 // softmax warpgroup, running reference maximum, sum and output accumulator, so that one stream's
-// exponentials run under the other's MMAs; a piece's end joins the two.  Tiles that end early (sinks,
-// ends of caches) are loaded in boxes of 16 rows and multiplied with as few columns and steps.
+// exponentials run under the other's MMAs; a unit's end joins the two.  Tiles that end early (sinks,
+// ends of caches) are loaded in boxes of 16 rows.
 //
 // When a CTA is through, it waits for the others (a cooperative launch, so all of them run; the wait gives
-// up after a second like every other) and then joins its share of the rows that several pieces hold, and
+// up after a second like every other) and then joins its share of the rows that several units hold, and
 // of the attention weights.  As a kernel of its own that took 12 to 16 us of a step: its blocks find no
-// room until these CTAs end, and the next step's CTAs none until they are gone.
+// room until these CTAs end, and the next step's CTAs none until they are gone.  Code that runs once per
+// CTA is kept short throughout: it is fetched from L2 every time.
 //
 // Tensor memory (512 columns): S_t at 128 t (P_t overwrites its first 64 columns), O_t at 256 + HD t.
-// Warp roles (384 threads): warp 0 TMA; warp 1 TMEM owner and MMA issuer, in the order S(0), S(1), then
-// O += P(j) V(j), S(j + 2) for j = 0, 1, ... (MMAs of one thread execute in issue order, so S(j + 2) may
-// overwrite the P(j) columns); warps 2-3 gather the next piece's query rows; warps 4-7 softmax of stream 0
-// and the pieces' ends, warps 8-11 softmax of stream 1 (thread = query row).
+// Warp roles (384 threads): warp 0 TMA; warp 1 TMEM owner and MMA issuer (from the whole warp, see
+// tc_issue.cuh), in the order S(0), S(1), then O += P(j) V(j), S(j + 2) for j = 0, 1, ... (MMAs of one thread
+// execute in issue order, so S(j + 2) may overwrite the P(j) columns); warp 2 gathers the next units' query
+// rows; warp 3 takes units and hands them to the others through a ring in shared memory; warps 4-7 softmax
+// of stream 0, warps 8-11 of stream 1 (thread = query row), and each stream's warps half of a unit's end.
 #include <math.h>
 
 #include <atomic>
 
 #include "internal.h"
-#include "ptx.cuh"
-#include "span_join.cuh"
+#include "span_records.cuh"
+#include "tc_issue.cuh"
 
 namespace mha {
 namespace {
@@ -36,6 +37,7 @@ namespace {
 constexpr int SP_THREADS = 384;
 constexpr int SP_TK = 128;   // keys per tile
 constexpr int SP_BOX = 16;   // rows of a box of a tile that ends early
+constexpr int SP_RING = 4;   // units in flight
 // Registers per thread after the split: warps 0-3, and the softmax warps (whose score row, packed
 // weights and an output chunk want 200).  The sum fits the 168 per thread of the launch.
 constexpr int SP_REGS = 168;  // at launch
@@ -49,24 +51,27 @@ struct SpCfg {
     static constexpr int CHUNK = 128 * 128;        // 128 rows x 64 bf16
     static constexpr int TILE = CH * CHUNK;
     static constexpr int STAGES = HD == 128 ? 3 : 6;
-    static constexpr int SMEM = TILE + 2 * STAGES * TILE + 1024 + 1024 + 1024;  // + row sums, barriers, alignment
+    static constexpr int SMEM = TILE + 2 * STAGES * TILE + 3072;  // + row sums, barriers, units
     static constexpr uint32_t O_COL = 256;
 };
 static_assert(SpCfg<128>::SMEM <= 232448 && SpCfg<64>::SMEM <= 232448, "span smem budget");
 
 // What follows the tiles in shared memory.
 struct SpTail {
-    float2 ml1[128];  // stream 1's (reference, sum) per row at a piece's end
+    float2 ml[2][128];  // each stream's (reference, sum) per row at a unit's end
     uint64_t kfull[6], kempty[6], vfull[6], vempty[6];
-    uint64_t qfull[2], qfree[2], sfull[2], pfull[2];
-    uint64_t odone, ofree, ml, drain;
+    uint64_t qfull[2], qfree[2], sfull[2], pfull[2], ufull[SP_RING], uempty[SP_RING];
+    uint64_t odone, ofree, mlfull, drain;
+    SpanUnit units[SP_RING];
+    int nr[SP_RING];  // query rows of the unit
+    SpanPlan plan;
     uint32_t tmem;
     int abort_flag, joined;
 };
-static_assert(sizeof(SpTail) <= 2048, "span tail");
+static_assert(sizeof(SpTail) <= 3072, "span tail");
 
 struct SpMaps {
-    CUtensorMap k, v, k16, v16, kp, vp, kp16, vp16;
+    CUtensorMap k, k16, v, v16, kp, kp16, vp, vp16;
 };
 
 // One row of a score tile from TMEM (warp-collective).
@@ -86,8 +91,8 @@ __device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&v)[8]) {
                  : "memory");
 }
 
-// One thread of every CTA of a cooperative grid: waits until all have arrived.  The two words behind the
-// status word (arrivals, generation) are as they were when it is over, so nothing has to clear them
+// One thread of every CTA of a cooperative grid: waits until all have arrived.  The words behind the status
+// word (arrivals, generation, units taken) are as they were when it is over, so nothing has to clear them
 // between launches; a CTA arrives whatever happened to it before.
 __device__ __forceinline__ bool span_grid_barrier(int* status, int ctas) {
     unsigned* arrived = reinterpret_cast<unsigned*>(status) + 1;
@@ -96,6 +101,7 @@ __device__ __forceinline__ bool span_grid_barrier(int* status, int ctas) {
     __threadfence();
     if (atomicAdd(arrived, 1u) == (unsigned)ctas - 1u) {
         *arrived = 0u;
+        status[3] = 0;
         __threadfence();
         *generation = g + 1u;
         return true;
@@ -118,13 +124,12 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
                      int* status) {
     using C = SpCfg<HD>;
     constexpr int S = C::STAGES;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;
-    const uint32_t sQ = base;
+    // (the tiles' swizzle wants 1024 bytes; there is no room to align by hand)
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t sQ = smem_u32(smem_raw);
     const uint32_t sK = sQ + C::TILE;
     const uint32_t sV = sK + S * C::TILE;
-    SpTail* tail = reinterpret_cast<SpTail*>(smem_raw + (base - raw) + C::TILE * (1 + 2 * S));
+    SpTail* tail = reinterpret_cast<SpTail*>(smem_raw + C::TILE * (1 + 2 * S));
     volatile int* abort_flag = &tail->abort_flag;
     auto bar = [](uint64_t& b) { return smem_u32(&b); };
 
@@ -139,14 +144,18 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
             mbar_init(bar(tail->vempty[s]), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(tail->qfull[i]), 64);
+            mbar_init(bar(tail->qfull[i]), 32);
             mbar_init(bar(tail->qfree[i]), 1);
             mbar_init(bar(tail->sfull[i]), 1);
             mbar_init(bar(tail->pfull[i]), 4);
         }
+        for (int i = 0; i < SP_RING; ++i) {
+            mbar_init(bar(tail->ufull[i]), 1);
+            mbar_init(bar(tail->uempty[i]), 11);  // TMA, MMA, gather and the eight softmax warps
+        }
         mbar_init(bar(tail->odone), 1);
-        mbar_init(bar(tail->ofree), 4);
-        mbar_init(bar(tail->ml), 4);
+        mbar_init(bar(tail->ofree), 8);
+        mbar_init(bar(tail->mlfull), 8);
         mbar_init(bar(tail->drain), 1);
         tail->abort_flag = 0;
         fence_mbar_init();
@@ -156,29 +165,26 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
         tmem_relinquish();
     }
     grid_launch_dependents();
-    const SpanStart start = span_start<SP_TK>(p, lengths);
-    if (blockIdx.x == 0)
-        for (int b = (int)threadIdx.x; b < p.B; b += SP_THREADS)
-            if (lengths[b] < p.T_q || lengths[b] > p.T_max) record_status(status, kStatusBadLength);
-    SpanPiece q;
-    // query rows of a piece, and where row r of it lies
-    auto n_rows = [&](const SpanPiece& x) { return min(128, (x.prefix ? p.B * p.rows : p.rows) - x.rb * 128); };
-    auto where = [&](const SpanPiece& x, int r, int& b, int& head, int& t) {
+    // The i-th unit of this CTA, once it is there; its slot is released after the last look at it.
+    auto unit_ready = [&](int i) { return mbar_wait(bar(tail->ufull[i % SP_RING]), (uint32_t)(i / SP_RING) & 1u, abort_flag, status); };
+    auto unit_done = [&](int i) { mbar_arrive(bar(tail->uempty[i % SP_RING])); };
+    // where query row r of a unit lies
+    auto where = [&](const SpanUnit& x, int r, int& b, int& head, int& t) {
         int rr = x.rb * 128 + r;
         b = x.b;
         if (x.prefix) {
             b = rr / p.rows;
             rr -= b * p.rows;
         }
-        const int hg = rr / p.T_q;
+        const int hg = p.T_q == 1 ? rr : rr / p.T_q;
         head = x.g * p.per + hg;
         t = rr - hg * p.T_q;
     };
-    // The query tile is two buffers of 64 rows: a piece of at most 64 rows takes them in turn, a larger one
-    // both.  uses[i]: pieces that have had buffer i.
+    // The query tile is two buffers of 64 rows: a unit of at most 64 rows takes them in turn, a larger one
+    // both.  uses[i]: units that have had buffer i.
     struct QueryBuffers {
         int uses[2] = {0, 0}, turn = 0;
-        // first and last buffer of the next piece
+        // first and last buffer of the next unit
         __device__ int first(int nr) const { return nr > 64 ? 0 : turn; }
         __device__ int last(int nr) const { return nr > 64 ? 1 : turn; }
         __device__ void take(int nr) {
@@ -191,75 +197,6 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
             }
         }
     };
-    // One warp copies query rows [r0, r0 + 32) of a piece of nr rows, 128-byte swizzled like a TMA box: a
-    // lane finds one row, a step copies 32 / U rows of U 16-byte units.
-    auto gather = [&](const SpanPiece& x, int nr, int buf, int r0) {
-        constexpr int U = HD / 8, PER = 32 / U;
-        int b, head, t;
-        where(x, min(r0 + lane, nr - 1), b, head, t);
-        const int64_t off = ((int64_t)b * p.T_q + t) * ldq + (int64_t)head * HD;
-        const int u = lane & (U - 1), c = u >> 3;
-#pragma unroll 4
-        for (int i = 0; i < 32 && r0 + i < nr; i += PER) {
-            const int r = r0 + i + lane / U;
-            const int64_t o = __shfl_sync(0xffffffffu, off, i + lane / U);
-            if (r < nr) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(Q + o + u * 8));
-                st_shared_v4(sQ + (uint32_t)(buf * 64 * 128 + c * C::CHUNK + r * 128) + ((uint32_t)((u & 7) ^ (r & 7)) << 4),
-                             v.x, v.y, v.z, v.w);
-            }
-        }
-        fence_proxy_async_smem();
-    };
-    // warp 0, lane 0: tiles through the ring.  nk, nv: K and V tiles issued
-    SpanWalk<SP_TK> walk(p, lengths, start);
-    SpanPiece qt;
-    int i_t = 0, nk = 0, nv = 0;
-    bool ok = true;
-    qt.i1 = 0;
-    auto next_t = [&]() {
-        if (!walk.next(qt)) return false;
-        i_t = qt.i0;
-        return true;
-    };
-    auto load_tile = [&]() {
-        int key0, n;
-        span_tile<SP_TK>(qt.v, i_t, key0, n);
-        ++i_t;
-        const int boxes = n > SP_TK - SP_BOX ? 0 : (n + SP_BOX - 1) / SP_BOX;
-        const uint32_t bytes = boxes ? (uint32_t)boxes * SP_BOX * 128 * C::CH : (uint32_t)C::TILE;
-        const int st = nk % S;
-        const uint32_t ph = ((uint32_t)(nk / S) & 1u) ^ 1u;
-        auto load = [&](uint32_t dst, const CUtensorMap* m, const CUtensorMap* m16, uint32_t full) {
-            mbar_arrive_expect_tx(full, bytes);
-#pragma unroll
-            for (int c = 0; c < C::CH; ++c) {
-                if (boxes == 0) tma_load_3d(dst + c * C::CHUNK, m, qt.g * HD + c * 64, key0, qt.b, full);
-                for (int x = 0; x < boxes; ++x)
-                    tma_load_3d(dst + c * C::CHUNK + x * SP_BOX * 128, m16, qt.g * HD + c * 64, key0 + x * SP_BOX, qt.b, full);
-            }
-        };
-        ok = mbar_wait(bar(tail->kempty[st]), ph, abort_flag, status);
-        if (!ok) return;
-        load(sK + st * C::TILE, qt.prefix ? &maps.kp : &maps.k, qt.prefix ? &maps.kp16 : &maps.k16, bar(tail->kfull[st]));
-        ++nk;
-        ok = mbar_wait(bar(tail->vempty[st]), ph, abort_flag, status);
-        if (!ok) return;
-        load(sV + st * C::TILE, qt.prefix ? &maps.vp : &maps.v, qt.prefix ? &maps.vp16 : &maps.v16, bar(tail->vfull[st]));
-        ++nv;
-    };
-    if (warp == 0) {
-        // the ring's first fill needs nobody else (this thread set the barriers up): before the block meets
-        if (lane == 0)
-            while (nk < S && (i_t < qt.i1 || next_t())) load_tile();
-    } else if (warp >= 4 && warp < 8) {  // the first piece's rows
-        SpanWalk<SP_TK> first = walk;
-        if (first.next(q)) {
-            const int nr = n_rows(q);
-            if ((warp - 4) * 32 < nr) gather(q, nr, 0, (warp - 4) * 32);
-        }
-    }
-    __syncwarp();  // the block's barrier has to see whole warps
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -269,102 +206,193 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
       setmaxnreg_dec<SP_REGS_CTRL>();
       if (warp == 0) {
         if (lane == 0) {
-            // ---------------- TMA: K and V tiles
-            while (ok && (i_t < qt.i1 || next_t())) load_tile();
+            // ---------------- TMA: K and V tiles.  nk, nv: issued
+            int nk = 0, nv = 0;
+            bool ok = true;
+            for (int i = 0; ok && unit_ready(i); ++i) {
+                const SpanUnit q = tail->units[i % SP_RING];
+                if (q.unit < 0) break;
+                const CUtensorMap* mk = q.prefix ? &maps.kp : &maps.k;
+                const CUtensorMap* mv = q.prefix ? &maps.vp : &maps.v;
+                for (int j = q.i0; j < q.i1; ++j) {
+                    int key0, n;
+                    span_tile<SP_TK>(q.v, j, key0, n);
+                    const int boxes = n > SP_TK - SP_BOX ? 0 : (n + SP_BOX - 1) / SP_BOX;
+                    const uint32_t bytes = boxes ? (uint32_t)boxes * SP_BOX * 128 * C::CH : (uint32_t)C::TILE;
+                    const int st = nk % S;
+                    const uint32_t ph = ((uint32_t)(nk / S) & 1u) ^ 1u;
+                    auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t full) {
+                        mbar_arrive_expect_tx(full, bytes);
+#pragma unroll
+                        for (int c = 0; c < C::CH; ++c) {
+                            if (boxes == 0) tma_load_3d(dst + c * C::CHUNK, m, q.g * HD + c * 64, key0, q.b, full);
+                            for (int x = 0; x < boxes; ++x)  // the map with boxes of 16 rows follows the whole one
+                                tma_load_3d(dst + c * C::CHUNK + x * SP_BOX * 128, m + 1, q.g * HD + c * 64, key0 + x * SP_BOX, q.b, full);
+                        }
+                    };
+                    ok = mbar_wait(bar(tail->kempty[st]), ph, abort_flag, status);
+                    if (!ok) break;
+                    load(sK + st * C::TILE, mk, bar(tail->kfull[st]));
+                    ++nk;
+                    ok = mbar_wait(bar(tail->vempty[st]), ph, abort_flag, status);
+                    if (!ok) break;
+                    load(sV + st * C::TILE, mv, bar(tail->vfull[st]));
+                    ++nv;
+                }
+                unit_done(i);
+            }
             // every load issued lands before the CTA exits
             for (int i = nk > S ? nk - S : 0; i < nk; ++i) drain_wait_a(bar(tail->kfull[i % S]), (uint32_t)(i / S) & 1u);
             for (int i = nv > S ? nv - S : 0; i < nv; ++i) drain_wait_a(bar(tail->vfull[i % S]), (uint32_t)(i / S) & 1u);
         }
       } else if (warp == 1) {
-        if (lane == 0) {
-            // ---------------- MMA issuer.  js, jp: score and value products issued so far
-            const uint64_t qdesc0 = sdesc_sw128(sQ, 16, 1024);
-            const uint64_t kdesc0 = sdesc_sw128(sK, 16, 1024);
-            const uint64_t vdesc0 = sdesc_sw128(sV, C::CHUNK, 1024);
-            SpanWalk<SP_TK> ahead(p, lengths, start);  // walks the score products, two tiles ahead
-            SpanPiece qs;
-            QueryBuffers qb;
-            int js = 0, piece_s = -1, i_s = 0, nr_s = 0, buf_s = 0;
-            qs.i1 = 0;
-            bool more_s = true;
-            auto cols = [&](const SpanPiece& x, int i) {  // keys of a tile in whole boxes
-                int key0, n;
-                span_tile<SP_TK>(x.v, i, key0, n);
-                return n > SP_TK - SP_BOX ? SP_TK : (n + SP_BOX - 1) / SP_BOX * SP_BOX;
-            };
-            auto issue_s = [&]() -> bool {
-                if (i_s == qs.i1) {
-                    if (!more_s || !(more_s = ahead.next(qs))) return true;
-                    i_s = qs.i0;
-                    ++piece_s;
-                    nr_s = n_rows(qs);
-                    buf_s = qb.first(nr_s);
-                    // (for the first piece too, whose rows were there before the roles parted: a warp that
-                    // gathers must not be a phase ahead of the other)
-                    for (int x = buf_s; x <= qb.last(nr_s); ++x)
-                        if (!mbar_wait(bar(tail->qfull[x]), (uint32_t)qb.uses[x] & 1u, abort_flag, status)) return false;
-                }
-                const int st = js % S;
-                if (!mbar_wait(bar(tail->kfull[st]), (uint32_t)(js / S) & 1u, abort_flag, status)) return false;
-                tc_fence_after();
-                const uint32_t idesc = idesc_bf16_f32(128, cols(qs, i_s), false, false);
-                const uint64_t kdesc = kdesc0 + (uint64_t)((st * C::TILE) >> 4);
-                const uint64_t qdesc = qdesc0 + (uint64_t)((buf_s * 64 * 128) >> 4);
-#pragma unroll
-                for (int kk = 0; kk < HD / 16; ++kk) {
-                    const uint32_t off16 = (uint32_t)(((kk >> 2) * C::CHUNK + (kk & 3) * 32) >> 4);
-                    mma_bf16_ss(tmem + 128u * (js & 1), qdesc + off16, kdesc + off16, idesc, kk > 0 ? 1u : 0u);
-                }
-                tc_commit(bar(tail->sfull[js & 1]));
-                tc_commit(bar(tail->kempty[st]));
-                ++js;
-                if (++i_s == qs.i1) {
-                    for (int x = buf_s; x <= qb.last(nr_s); ++x) tc_commit(bar(tail->qfree[x]));
-                    qb.take(nr_s);
-                }
-                return true;
-            };
-            bool ok = issue_s() && issue_s();
-            int jp = 0;
-            for (int piece = 0; ok && walk.next(q); ++piece) {
-                // the piece before has been read out of O
-                if (piece > 0) ok = mbar_wait(bar(tail->ofree), (uint32_t)(piece - 1) & 1u, abort_flag, status);
-                for (int i = q.i0; i < q.i1 && ok; ++i) {
-                    const int st = jp % S, t = jp & 1;
-                    ok = mbar_wait(bar(tail->vfull[st]), (uint32_t)(jp / S) & 1u, abort_flag, status) &&
-                         mbar_wait(bar(tail->pfull[t]), (uint32_t)(jp >> 1) & 1u, abort_flag, status);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t idesc = idesc_bf16_f32(128, HD, false, true);
-                    const uint64_t vdesc = vdesc0 + (uint64_t)((st * C::TILE) >> 4);
-                    const int steps = cols(q, i) / 16;
-                    const bool first = i - q.i0 < 2;  // of its stream
-                    for (int kk = 0; kk < steps; ++kk)
-                        mma_bf16_ts(tmem + C::O_COL + HD * t, tmem + 128u * t + kk * 8,
-                                    vdesc + (uint64_t)((kk * 2048) >> 4), idesc, (!first || kk > 0) ? 1u : 0u);
-                    tc_commit(bar(tail->vempty[st]));
-                    if (i + 1 == q.i1) tc_commit(bar(tail->odone));
-                    ++jp;
-                    ok = issue_s();
-                }
-            }
-            tc_commit(bar(tail->drain));
-            drain_wait_a(bar(tail->drain), 0);
-        }
-      } else {
-        // ---------------- the next pieces' query rows, into the buffers as they become free
+        // ---------------- MMA issuer.  js, jp: score and value products issued so far
+        const uint32_t el = elect_lane();
+        const uint64_t qdesc0 = sdesc_sw128(sQ, 16, 1024);
+        const uint64_t kdesc0 = sdesc_sw128(sK, 16, 1024);
+        const uint64_t vdesc0 = sdesc_sw128(sV, C::CHUNK, 1024);
+        constexpr uint32_t idesc_s = idesc_bf16_f32(128, SP_TK, false, false);
+        constexpr uint32_t idesc_o = idesc_bf16_f32(128, HD, false, true);
         QueryBuffers qb;
-        bool ok = true;
-        for (int piece = 0; ok && walk.next(q); ++piece) {
-            const int nr = n_rows(q), buf = qb.first(nr), end = qb.last(nr);
-            if (piece > 0) {
-                for (int x = buf; x <= end && ok; ++x)
-                    if (qb.uses[x] > 0) ok = mbar_wait(bar(tail->qfree[x]), (uint32_t)(qb.uses[x] - 1) & 1u, abort_flag, status);
-                if (!ok) break;
-                for (int r0 = (warp - 2) * 32; r0 < nr; r0 += 64) gather(q, nr, buf, r0);
+        int js = 0, us = -1, left_s = 0, nr_s = 0, buf_s = 0;  // us: the unit of the score products, left_s tiles of it
+        bool more_s = true;
+        // the next score product, if there is one
+        auto issue_s = [&]() -> bool {
+            if (left_s == 0) {
+                if (!more_s) return true;
+                if (!__all_sync(0xffffffffu, unit_ready(us + 1))) return false;
+                const SpanUnit& x = tail->units[(us + 1) % SP_RING];
+                if (x.unit < 0) {
+                    more_s = false;
+                    return true;
+                }
+                ++us;
+                left_s = x.i1 - x.i0;
+                nr_s = tail->nr[us % SP_RING];
+                buf_s = qb.first(nr_s);
+                for (int i = buf_s; i <= qb.last(nr_s); ++i)
+                    if (!warp_wait(bar(tail->qfull[i]), (uint32_t)qb.uses[i] & 1u, abort_flag, status)) return false;
             }
+            const int st = js % S;
+            if (!warp_wait(bar(tail->kfull[st]), (uint32_t)(js / S) & 1u, abort_flag, status)) return false;
+            tc_fence_after();
+            const uint64_t kdesc = kdesc0 + (uint64_t)((st * C::TILE) >> 4);
+            const uint64_t qdesc = qdesc0 + (uint64_t)((buf_s * 64 * 128) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < HD / 16; ++kk) {
+                const uint32_t off16 = (uint32_t)(((kk >> 2) * C::CHUNK + (kk & 3) * 32) >> 4);
+                mma_bf16_ss_elect(el, tmem + 128u * (js & 1), qdesc + off16, kdesc + off16, idesc_s, kk > 0 ? 1u : 0u);
+            }
+            tc_commit_elect(el, bar(tail->sfull[js & 1]));
+            tc_commit_elect(el, bar(tail->kempty[st]));
+            ++js;
+            if (--left_s == 0) {
+                for (int i = buf_s; i <= qb.last(nr_s); ++i) tc_commit_elect(el, bar(tail->qfree[i]));
+                qb.take(nr_s);
+            }
+            return true;
+        };
+        bool ok = issue_s() && issue_s();
+        int jp = 0;
+        for (int i = 0; ok; ++i) {
+            ok = __all_sync(0xffffffffu, unit_ready(i));
+            if (!ok || tail->units[i % SP_RING].unit < 0) break;
+            const int i0 = tail->units[i % SP_RING].i0, nt = tail->units[i % SP_RING].i1 - i0;
+            const SpanView v = tail->units[i % SP_RING].v;
+            // the unit before has been read out of O
+            if (i > 0) ok = warp_wait(bar(tail->ofree), (uint32_t)(i - 1) & 1u, abort_flag, status);
+            for (int k = 0; k < nt && ok; ++k) {
+                const int st = jp % S, t = jp & 1;
+                ok = warp_wait(bar(tail->vfull[st]), (uint32_t)(jp / S) & 1u, abort_flag, status) &&
+                     warp_wait(bar(tail->pfull[t]), (uint32_t)(jp >> 1) & 1u, abort_flag, status);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t vdesc = vdesc0 + (uint64_t)((st * C::TILE) >> 4);
+                int key0, n;  // values past the tile's end were not loaded: no steps over them
+                span_tile<SP_TK>(v, i0 + k, key0, n);
+#pragma unroll
+                for (int kk = 0; kk < SP_TK / 16; ++kk)
+                    if (16 * kk < n)
+                        mma_bf16_ts_elect(el, tmem + C::O_COL + HD * t, tmem + 128u * t + kk * 8, vdesc + (uint64_t)((kk * 2048) >> 4),
+                                          idesc_o, (k >= 2 || kk > 0) ? 1u : 0u);
+                tc_commit_elect(el, bar(tail->vempty[st]));
+                if (k + 1 == nt) tc_commit_elect(el, bar(tail->odone));
+                ++jp;
+                ok = issue_s();
+            }
+            __syncwarp();
+            if (ok && lane == 0) unit_done(i);
+        }
+        tc_commit_elect(el, bar(tail->drain));
+        drain_wait_a(bar(tail->drain), 0);
+      } else if (warp == 2) {
+        // ---------------- query rows, 128-byte swizzled like a TMA box, into the buffers as they become
+        // free.  A lane finds one row of 32, a step copies 32 / U rows of U 16-byte units.
+        QueryBuffers qb;
+        for (int i = 0; __all_sync(0xffffffffu, unit_ready(i)); ++i) {
+            const SpanUnit q = tail->units[i % SP_RING];
+            const int nr = tail->nr[i % SP_RING];
+            __syncwarp();
+            if (q.unit < 0) break;
+            if (lane == 0) unit_done(i);
+            const int buf = qb.first(nr), end = qb.last(nr);
+            bool ok = true;
+            for (int x = buf; x <= end && ok; ++x)
+                if (qb.uses[x] > 0) ok = warp_wait(bar(tail->qfree[x]), (uint32_t)(qb.uses[x] - 1) & 1u, abort_flag, status);
+            if (!ok) break;
+            constexpr int U = HD / 8, PER = 32 / U;
+            const int u = lane & (U - 1), c = u >> 3;
+#pragma unroll 1
+            for (int r0 = 0; r0 < nr; r0 += 32) {
+                int b, head, t;
+                where(q, min(r0 + lane, nr - 1), b, head, t);
+                const int64_t off = ((int64_t)b * p.T_q + t) * ldq + (int64_t)head * HD;
+#pragma unroll 1
+                for (int s = 0; s < 32 && r0 + s < nr; s += 8 * PER) {  // eight loads under way
+                    uint4 v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int from = (s + e * PER + lane / U) & 31;
+                        const int64_t o = __shfl_sync(0xffffffffu, off, from);
+                        if (s + e * PER < 32) v[e] = __ldg(reinterpret_cast<const uint4*>(Q + o + u * 8));  // (rows past nr: the last one)
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = r0 + s + e * PER + lane / U;
+                        if (s + e * PER < 32 && r < nr)
+                            st_shared_v4(sQ + (uint32_t)(buf * 64 * 128 + c * C::CHUNK + r * 128) + ((uint32_t)((u & 7) ^ (r & 7)) << 4),
+                                         v[e].x, v[e].y, v[e].z, v[e].w);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
             for (int x = buf; x <= end; ++x) mbar_arrive(bar(tail->qfull[x]));
             qb.take(nr);
+        }
+      } else {
+        // ---------------- units: the first is this CTA's, the others come from the counter
+        if (blockIdx.x == 0)
+            for (int b = lane; b < p.B; b += 32)
+                if (lengths[b] < p.T_q || lengths[b] > p.T_max) record_status(status, kStatusBadLength);
+        SpanSums sums;
+        const SpanPlan plan = span_plan<SP_TK>(p, lengths, (int)gridDim.x, sums);
+        if (lane == 0) tail->plan = plan;
+        int u = (int)blockIdx.x;
+        for (int i = 0;; ++i) {
+            SpanUnit x;
+            x.unit = -1;
+            x.prefix = x.rb = 0;
+            if (u < plan.N) x = span_unit<SP_TK>(p, lengths, plan, sums, u);
+            if (i >= SP_RING && !warp_wait(bar(tail->uempty[i % SP_RING]), (uint32_t)(i / SP_RING - 1) & 1u, abort_flag, status)) break;
+            if (lane == 0) {
+                tail->units[i % SP_RING] = x;
+                tail->nr[i % SP_RING] = min(128, (x.prefix ? p.B * p.rows : p.rows) - x.rb * 128);
+                mbar_arrive(bar(tail->ufull[i % SP_RING]));
+            }
+            if (x.unit < 0) break;
+            int next = 0;
+            if (lane == 0) next = atomicAdd(status + 3, 1);
+            u = (int)gridDim.x + __shfl_sync(0xffffffffu, next, 0);
         }
       }
       // the tensor memory goes back once the softmax warps have read it
@@ -376,15 +404,20 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
       }
     } else {
         setmaxnreg_inc<SP_REGS_SOFTMAX>();
-        // ---------------- softmax of stream t; stream 0's warps also end the pieces
+        // ---------------- softmax of stream t
         const int t = (warp - 4) >> 2, quarter = warp & 3;
         const int r = quarter * 32 + lane;
         const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t s_col = trow + 128u * t, o_col = trow + C::O_COL + HD * t;
-        int j = 0;  // tiles before this piece
+        int j = 0;  // tiles before this unit
         bool ok = true;
-        for (int piece = 0; ok && walk.next(q); ++piece) {
-            const int nr = n_rows(q), nt = q.i1 - q.i0;
+        for (int iu = 0; ok; ++iu) {
+            if (!__all_sync(0xffffffffu, unit_ready(iu))) break;
+            const SpanUnit q = tail->units[iu % SP_RING];
+            const int nr = tail->nr[iu % SP_RING], nt = q.i1 - q.i0;
+            __syncwarp();
+            if (q.unit < 0) break;
+            if (lane == 0) unit_done(iu);
             const bool active = quarter * 32 < nr, real = r < nr;
             int rb_, head, tok;
             where(q, real ? r : 0, rb_, head, tok);
@@ -495,40 +528,41 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
                 if (lane == 0) mbar_arrive(bar(tail->pfull[t]));
             }
             if (!ok) break;
-            // ---------------- the piece's end
-            if (t == 1) {
-                // the piece before has read ml1
-                if (piece > 0 && !__all_sync(0xffffffffu, mbar_wait(bar(tail->ofree), (uint32_t)(piece - 1) & 1u, abort_flag, status))) {
+            // ---------------- the unit's end
+            // each stream's warps join half of the columns
+            {
+                // (the sums of the unit before have been read)
+                if (iu > 0 && !__all_sync(0xffffffffu, mbar_wait(bar(tail->ofree), (uint32_t)(iu - 1) & 1u, abort_flag, status))) {
                     ok = false;
                     break;
                 }
-                tail->ml1[r] = make_float2(m, l);
+                tail->ml[t][r] = make_float2(m, l);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(tail->ml));
-            } else {
-                if (!__all_sync(0xffffffffu, mbar_wait(bar(tail->odone), (uint32_t)piece & 1u, abort_flag, status) &&
-                                                 mbar_wait(bar(tail->ml), (uint32_t)piece & 1u, abort_flag, status))) {
+                if (lane == 0) mbar_arrive(bar(tail->mlfull));
+                if (!__all_sync(0xffffffffu, mbar_wait(bar(tail->odone), (uint32_t)iu & 1u, abort_flag, status) &&
+                                                 mbar_wait(bar(tail->mlfull), (uint32_t)iu & 1u, abort_flag, status))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 if (active) {
-                    const float2 ml1 = tail->ml1[r];
-                    const float M = fmaxf(m, ml1.x);
-                    // the first tile of the piece went to stream j & 1
+                    const float2 ml0 = tail->ml[0][r], ml1 = tail->ml[1][r];
+                    const float M = fmaxf(ml0.x, ml1.x);
+                    // the first tile of the unit went to stream j & 1
                     const bool has0 = nt > 1 || (j & 1) == 0, has1 = nt > 1 || (j & 1) == 1;
-                    const float w0 = m == -INFINITY ? 0.f : ex2_approx(m - M);
+                    const float w0 = ml0.x == -INFINITY ? 0.f : ex2_approx(ml0.x - M);
                     const float w1 = ml1.x == -INFINITY ? 0.f : ex2_approx(ml1.x - M);
-                    const float sum = w0 * l + w1 * ml1.y;
+                    const float sum = w0 * ml0.y + w1 * ml1.y;
                     const bool direct = p.T_p == 0 && q.whole();
-                    const int64_t row = rec.row(p, q.prefix, q.block, (int)blockIdx.x / p.gang, (int)blockIdx.x % p.gang) + r;
-                    if (real && (!direct || scores != nullptr)) rec.ml[row] = make_float2(M, sum);
+                    const int64_t row = rec.row(p, q.unit, tail->plan.np) + r;
+                    if (t == 0 && real && (!direct || scores != nullptr)) rec.ml[row] = make_float2(M, sum);
                     const float inv = 1.f / sum;
                     __nv_bfloat16* out = O + ((int64_t)rb_ * p.T_q + tok) * ldo + (int64_t)head * HD;
                     float* part = rec.o + row * HD;
                     const bool wide = ((reinterpret_cast<uintptr_t>(O) | (uintptr_t)(ldo * 2)) & 31u) == 0;
 #pragma unroll
-                    for (int cc = 0; cc < HD / 32; ++cc) {
+                    for (int c2 = 0; c2 < HD / 64; ++c2) {
+                        const int cc = t * (HD / 64) + c2;
                         float f[32];
 #pragma unroll
                         for (int e = 0; e < 32; ++e) f[e] = 0.f;
@@ -580,122 +614,143 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
         tc_fence_before();
         __threadfence();  // the records, before this CTA counts as arrived
         named_barrier_sync(1, SP_THREADS);
-        // ---------------- all pieces are done: join
-        // (by the softmax warps: they have the registers)
-        constexpr int JOIN = 256, JOIN_WARPS = JOIN / 32;
+        // ---------------- all units are done: join (the softmax warps: they have the registers).  What does
+        // not need the records is worked out before the others have arrived.
+        constexpr int JOIN = 256, JOIN_WARPS = JOIN / 32, E = HD / 32;  // E columns per lane
         const int jw = warp - 4;
+        SpanSums sums;
+        const SpanPlan plan = span_plan<SP_TK>(p, lengths, (int)gridDim.x, sums);
+        const int heads = p.per * p.h_kv, out_rows = p.B * heads * p.T_q;
+        // rows in turn to the CTAs, whose warps share a row's records, where there are few rows; to the
+        // warps otherwise
+        const bool few = out_rows <= (int)gridDim.x;
+        int row = few ? (int)blockIdx.x : (int)blockIdx.x * JOIN_WARPS + jw;
+        __nv_bfloat16* out = nullptr;
+        RowRecords src;
+        auto find_row = [&]() {
+            if (row >= out_rows) return;
+            const int bh = p.T_q == 1 ? row : row / p.T_q, t = row - bh * p.T_q, b = bh / heads, head = bh - b * heads;
+            const SpanView v = span_view<SP_TK>(p, __ldcg(lengths + b));
+            const int g = head / p.per;
+            out = O + ((int64_t)b * p.T_q + t) * ldo + (int64_t)head * HD + lane * E;
+            src = row_records<SP_TK>(p, rec, plan, span_first_unit<SP_TK>(p, lengths, plan, sums, b), v.nt, b, g,
+                                     (head - g * p.per) * p.T_q + t);
+            if (v.nt == 0) src.n[0] = src.n[1] = 0;  // invalid length
+        };
+        find_row();
         if (jw == 0 && lane == 0) tail->joined = span_grid_barrier(status, (int)gridDim.x) ? 1 : 0;
         named_barrier_sync(2, JOIN);
         if (!tail->joined) return;
-        const int gangs = (int)gridDim.x / p.gang;
-        const int heads = p.per * p.h_kv, out_rows = p.B * heads * p.T_q;
-        {
-            // rows in turn to the CTAs, whose warps share a row's records, where there are few rows; to the
-            // warps otherwise
-            const bool few = out_rows <= (int)gridDim.x;
-            float* sums = reinterpret_cast<float*>(smem_raw + (base - raw));  // [warp][column]
-            for (int row = few ? (int)blockIdx.x : (int)blockIdx.x * JOIN_WARPS + jw; row < out_rows;
-                 row += few ? (int)gridDim.x : (int)gridDim.x * JOIN_WARPS) {
-                const int t = row % p.T_q, bh = row / p.T_q, b = bh / heads, head = bh - b * heads, g = head / p.per;
-                const SpanView v = span_view<SP_TK>(p, lengths[b]);
-                constexpr int E = HD / 32;  // columns per lane
-                __nv_bfloat16* out = O + ((int64_t)b * p.T_q + t) * ldo + (int64_t)head * HD + lane * E;
-                float o[E] = {}, l = 1.f;
-                bool write = true;
-                if (v.nt == 0) {  // invalid length
-    #pragma unroll
-                    for (int e = 0; e < E; ++e) o[e] = NAN;
-                    write = !few || jw == 0;
-                } else {
-                    int N, off;
-                    first_tile<SP_TK>(p, lengths, b, N, off);
-                    RowRecords src[2];
-                    row_sources<SP_TK>(p, rec, 128, gangs, v, b, g, (head - g * p.per) * p.T_q + t, N, off, src);
-                    if (p.T_p == 0 && src[0].n == 1) continue;  // one piece held the whole group and wrote the row
-                    const float2 ml = row_sum(rec, src);
-                    l = ml.y;
-    #pragma unroll 4
-                    for (int c = few ? jw : 0; c < src[0].n + src[1].n; c += few ? JOIN_WARPS : 1) {
-                        const int64_t k = c < src[0].n ? src[0].first + c * src[0].step : src[1].first + (c - src[0].n) * src[1].step;
-                        const float m = __ldcg(rec.ml + k).x;
-                        const float w = m == -INFINITY ? 0.f : ex2_approx(m - ml.x);
-                        float x[E];
-                        if constexpr (E == 4) {
-                            const float4 y = __ldcg(reinterpret_cast<const float4*>(rec.o + k * HD) + lane);
-                            x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
-                        } else {
-                            const float2 y = __ldcg(reinterpret_cast<const float2*>(rec.o + k * HD) + lane);
-                            x[0] = y.x; x[1] = y.y;
-                        }
-    #pragma unroll
-                        for (int e = 0; e < E; ++e) o[e] = fmaf(w, x[e], o[e]);
+        float* part = reinterpret_cast<float*>(smem_raw);  // [warp][column]
+        for (; row < out_rows; row += few ? (int)gridDim.x : (int)gridDim.x * JOIN_WARPS, find_row()) {
+            const int n = src.count();
+            if (n == 1) continue;  // one unit held the whole group and wrote the row
+            float o[E], l = 1.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = n == 0 ? NAN : 0.f;
+            if (n > 0) {
+                // records two at a time; a lane's columns of one are 16 (8) bytes
+                float M = -INFINITY;
+                for (int c = lane; c < n; c += 32) M = fmaxf(M, __ldcg(rec.ml + src.at(c)).x);
+#pragma unroll
+                for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+                l = 0.f;
+#pragma unroll 4
+                for (int c = few ? jw : 0; c < n; c += few ? JOIN_WARPS : 1) {
+                    const int64_t k = src.at(c);
+                    const float2 ml = __ldcg(rec.ml + k);
+                    float x[E];
+                    if constexpr (E == 4) {
+                        const float4 y = __ldcg(reinterpret_cast<const float4*>(rec.o + k * HD) + lane);
+                        x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+                    } else {
+                        const float2 y = __ldcg(reinterpret_cast<const float2*>(rec.o + k * HD) + lane);
+                        x[0] = y.x; x[1] = y.y;
                     }
-                    if (few) {
-    #pragma unroll
-                        for (int e = 0; e < E; ++e) sums[jw * HD + lane * E + e] = o[e];
-                        named_barrier_sync(2, JOIN);
-                        write = jw == 0;
-                        if (write)
-    #pragma unroll
-                            for (int e = 0; e < E; ++e) {
-                                float y = 0.f;
-                                for (int w = 0; w < JOIN_WARPS; ++w) y += sums[w * HD + lane * E + e];
-                                o[e] = y;
-                            }
-                        named_barrier_sync(2, JOIN);
+                    const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+                    l = fmaf(w, ml.y, l);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[e] = fmaf(w, x[e], o[e]);
+                }
+                if (few) {
+                    float* mine = part + jw * (HD + 4);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) mine[lane * E + e] = o[e];
+                    if (lane == 0) mine[HD] = l;
+                    named_barrier_sync(2, JOIN);
+                    l = 0.f;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[e] = 0.f;
+                    for (int w = 0; w < JOIN_WARPS; ++w) {
+                        l += part[w * (HD + 4) + HD];
+#pragma unroll
+                        for (int e = 0; e < E; ++e) o[e] += part[w * (HD + 4) + lane * E + e];
                     }
+                    named_barrier_sync(2, JOIN);
                 }
-                if (write) {
-                    const float inv = 1.f / l;
-    #pragma unroll
-                    for (int e = 0; e < E; e += 2)
-                        *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
-                }
+            }
+            if (!few || jw == 0) {
+                const float inv = 1.f / l;
+#pragma unroll
+                for (int e = 0; e < E; e += 2)
+                    *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
             }
         }
         if (weights != nullptr) {
-            // a token's weight is the sum over the query rows of 2^(s - M) / l, in row order.  A warp takes 256
-            // tokens of one (batch, K/V head) at a time.
-            constexpr int PER = 8, KEYS = 32 * PER;
+            // a token's weight is the sum over the query rows of 2^(s - M) / l, in row order.  A warp takes 512
+            // tokens of one (batch, K/V head) at a time, a lane the sums of one row.
+            constexpr int PER = 16, KEYS = 32 * PER;
             const int chunks = (p.T_max + KEYS - 1) / KEYS;
             const int64_t tasks = (int64_t)p.B * p.h_kv * chunks;
+            const int64_t ld = score_ld(p);
             for (int64_t task = (int64_t)blockIdx.x * JOIN_WARPS + jw; task < tasks; task += (int64_t)gridDim.x * JOIN_WARPS) {
                 const int bg = (int)(task / chunks), k0 = (int)(task - (int64_t)bg * chunks) * KEYS;
                 const int b = bg / p.h_kv, g = bg - b * p.h_kv;
-                const SpanView v = span_view<SP_TK>(p, lengths[b]);
+                const SpanView v = span_view<SP_TK>(p, __ldcg(lengths + b));
                 if (v.nt == 0 || k0 >= v.L) continue;
-                int N, off;
-                first_tile<SP_TK>(p, lengths, b, N, off);
-                float w[PER] = {}, old[PER];
-                float* out = weights + (int64_t)bg * p.T_max + k0 + lane;
-                // the new tokens' entries start here, the others grow
-    #pragma unroll
-                for (int u = 0; u < PER; ++u) old[u] = k0 + lane + 32 * u < v.L - p.T_q ? out[32 * u] : 0.f;
+                const int unit0 = span_first_unit<SP_TK>(p, lengths, plan, sums, b);
+                // this lane's keys; those past the length read the last one's scores and are dropped
+                int key[PER];
+#pragma unroll
+                for (int u = 0; u < PER; ++u) key[u] = min(k0 + lane + 32 * u, v.L - 1);
+                float w[PER] = {};
                 for (int r0 = 0; r0 < p.rows; r0 += 32) {
                     const int nr = min(32, p.rows - r0);
-                    float M = 0.f, il = 0.f;  // of row r0 + lane
-                    for (int r = 0; r < nr; ++r) {
-                        RowRecords src[2];
-                        row_sources<SP_TK>(p, rec, 128, gangs, v, b, g, r0 + r, N, off, src);
-                        const float2 ml = row_sum(rec, src);
-                        if (lane == r) {
-                            M = ml.x;
-                            il = 1.f / ml.y;
+                    const RowRecords x = row_records<SP_TK>(p, rec, plan, unit0, v.nt, b, g, r0 + min(lane, nr - 1));
+                    float M = -INFINITY, l = 0.f;  // of row r0 + lane
+#pragma unroll 8
+                    for (int c = 0; c < x.count(); ++c) M = fmaxf(M, __ldcg(rec.ml + x.at(c)).x);
+#pragma unroll 8
+                    for (int c = 0; c < x.count(); ++c) {
+                        const float2 ml = __ldcg(rec.ml + x.at(c));
+                        l = fmaf(ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M), ml.y, l);
+                    }
+                    const float il = 1.f / l;
+                    const float* s = scores + ((int64_t)bg * p.rows + r0) * ld;
+#pragma unroll 1
+                    for (int r = 0; r < nr; r += 2, s += 2 * ld) {
+                        float sv[2][PER];
+#pragma unroll
+                        for (int u = 0; u < PER; ++u) sv[0][u] = __ldcg(s + key[u]);
+                        const bool two = r + 1 < nr;
+#pragma unroll
+                        for (int u = 0; u < PER; ++u) sv[1][u] = two ? __ldcg(s + ld + key[u]) : -INFINITY;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float m = __shfl_sync(0xffffffffu, M, min(r + i, nr - 1)), f = __shfl_sync(0xffffffffu, il, min(r + i, nr - 1));
+#pragma unroll
+                            for (int u = 0; u < PER; ++u) w[u] = fmaf(ex2_approx(sv[i][u] - m), f, w[u]);
                         }
                     }
-                    const float* s = scores + ((int64_t)bg * p.rows + r0) * score_ld(p) + k0 + lane;
-    #pragma unroll 2
-                    for (int r = 0; r < nr; ++r) {
-                        const float m = __shfl_sync(0xffffffffu, M, r), f = __shfl_sync(0xffffffffu, il, r);
-    #pragma unroll
-                        for (int u = 0; u < PER; ++u)
-                            if (k0 + lane + 32 * u < v.L)
-                                w[u] = fmaf(exp2f(__ldcg(s + (int64_t)r * score_ld(p) + 32 * u) - m), f, w[u]);
-                    }
                 }
-    #pragma unroll
+                float* to = weights + (int64_t)bg * p.T_max + k0 + lane;
+                float old[PER];
+                // the new tokens' entries start here, the others grow
+#pragma unroll
+                for (int u = 0; u < PER; ++u) old[u] = k0 + lane + 32 * u < v.L - p.T_q ? to[32 * u] : 0.f;
+#pragma unroll
                 for (int u = 0; u < PER; ++u)
-                    if (k0 + lane + 32 * u < v.L) out[32 * u] = old[u] + w[u];
+                    if (k0 + lane + 32 * u < v.L) to[32 * u] = old[u] + w[u];
             }
         }
     }
@@ -704,7 +759,7 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
 template <int HD>
 cudaError_t launch(const SpanShape& p, const SpanRecords& rec, const void* Q, int64_t ldq, const void* K, int64_t ldk,
                    const void* V, int64_t ldv, const void* Kp, int64_t ldkp, const void* Vp, int64_t ldvp, void* O,
-                   int64_t ldo, const int32_t* lengths, float* scores, float* weights, int gangs, int* status,
+                   int64_t ldo, const int32_t* lengths, float* scores, float* weights, int ctas, int* status,
                    cudaStream_t stream) {
     using C = SpCfg<HD>;
     SpMaps maps;
@@ -740,7 +795,7 @@ cudaError_t launch(const SpanShape& p, const SpanRecords& rec, const void* Q, in
     // Cooperative, and not started early behind the previous kernel: its CTAs wait for one another, so
     // they have to be placed together.
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(gangs * p.gang));
+    cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(SP_THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = stream;
@@ -759,13 +814,13 @@ cudaError_t launch(const SpanShape& p, const SpanRecords& rec, const void* Q, in
 cudaError_t launch_span_bf16(const SpanShape& p, const SpanRecords& rec, const void* Q, int64_t ldq, const void* K,
                              int64_t ldk, const void* V, int64_t ldv, const void* Kp, int64_t ldkp, const void* Vp,
                              int64_t ldvp, void* O, int64_t ldo, int d, const int32_t* lengths, float* scores,
-                             float* weights, int gangs, int* status, cudaStream_t stream) {
+                             float* weights, int ctas, int* status, cudaStream_t stream) {
     if (d == 64)
         return launch<64>(p, rec, Q, ldq, K, ldk, V, ldv, Kp, ldkp, Vp, ldvp, O, ldo, lengths, scores,
-                          weights, gangs, status, stream);
+                          weights, ctas, status, stream);
     if (d == 128)
         return launch<128>(p, rec, Q, ldq, K, ldk, V, ldv, Kp, ldkp, Vp, ldvp, O, ldo, lengths, scores,
-                           weights, gangs, status, stream);
+                           weights, ctas, status, stream);
     return cudaErrorInvalidValue;
 }
 

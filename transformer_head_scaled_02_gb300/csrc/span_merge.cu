@@ -1,10 +1,10 @@
-// span_merge.cu -- joins the pieces of the fp32 cache steps (span_simt.cu): the output rows of groups that
-// several CTAs (or a prefix and a cache) share, and the attention weights per cached token.
+// span_merge.cu -- joins the units of the fp32 cache steps (span_simt.cu): the output rows of groups of
+// several units (or of a prefix and a cache), and the attention weights per cached token.
 #include <math.h>
 
 #include "internal.h"
 #include "ptx.cuh"
-#include "span_join.cuh"
+#include "span_records.cuh"
 
 namespace mha {
 namespace {
@@ -22,35 +22,34 @@ constexpr int SM_KEYS = 1024;  // cached tokens per block of the weight sums
 // decode step are few, so everything that does not need the records is done before the wait for them.
 template <bool WEIGHTS>
 __global__ void __launch_bounds__(SM_THREADS)
-    span_merge_kernel(const SpanShape p, const SpanRecords rec, int bm, int gangs, float* __restrict__ O, int64_t ldo,
+    span_merge_kernel(const SpanShape p, const SpanRecords rec, int ctas, float* __restrict__ O, int64_t ldo,
                       const int32_t* __restrict__ lengths, const float* __restrict__ scores,
                       float* __restrict__ weights) {
-    // The piece kernel lets this one start once its own wait for earlier work is over, so the lengths can
+    // The unit kernel lets this one start once its own wait for earlier work is over, so the lengths can
     // be read at once (from L2: nothing older may be served); the records it is still writing cannot.
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int heads = p.per * p.h_kv, out_rows = p.B * heads * p.T_q;
+    SpanSums sums;
+    const SpanPlan plan = span_plan<SM_TILE>(p, lengths, ctas, sums);
     if (!WEIGHTS || (int)blockIdx.x < out_rows) {
         const int row = (int)blockIdx.x;  // (b * heads + head) * T_q + t
         const int t = row % p.T_q, bh = row / p.T_q, b = bh / heads, head = bh - b * heads;
         float* out = O + ((int64_t)b * p.T_q + t) * ldo + (int64_t)head * rec.dv;
         const int g = head / p.per, rr = (head - g * p.per) * p.T_q + t;
         const SpanView v = span_view<SM_TILE>(p, __ldcg(lengths + b));
-        int N, off;
-        first_tile<SM_TILE>(p, lengths, b, N, off);
-        RowRecords src[2];
-        if (v.nt > 0) row_sources<SM_TILE>(p, rec, bm, gangs, v, b, g, rr, N, off, src);
+        const RowRecords src = row_records<SM_TILE>(p, rec, plan, span_first_unit<SM_TILE>(p, lengths, plan, sums, b), v.nt, b, g, rr);
         grid_dependency_wait();
         grid_launch_dependents();
         if (v.nt == 0) {  // invalid length
             for (int e = tid; e < rec.dv; e += SM_THREADS) out[e] = NAN;
             return;
         }
-        if (p.T_p == 0 && src[0].n == 1) return;  // one piece held the whole group and wrote the row
+        if (src.count() == 1) return;  // one unit held the whole group and wrote the row
         __shared__ float part[SM_WARPS][256];
         const float2 ml = row_sum(rec, src);
         float o[8] = {};  // d_v <= 256
-        for (int c = warp; c < src[0].n + src[1].n; c += SM_WARPS) {
-            const int64_t k = c < src[0].n ? src[0].first + c * src[0].step : src[1].first + (c - src[0].n) * src[1].step;
+        for (int c = warp; c < src.count(); c += SM_WARPS) {
+            const int64_t k = src.at(c);
             const float m = rec.ml[k].x;
             const float w = m == -INFINITY ? 0.f : exp2f(m - ml.x);
 #pragma unroll
@@ -76,8 +75,7 @@ __global__ void __launch_bounds__(SM_THREADS)
         const int bg = i / chunks, k0 = (i - bg * chunks) * SM_KEYS;
         const int b = bg / p.h_kv, g = bg - b * p.h_kv;
         const SpanView v = span_view<SM_TILE>(p, __ldcg(lengths + b));
-        int N, off;
-        first_tile<SM_TILE>(p, lengths, b, N, off);
+        const int unit0 = span_first_unit<SM_TILE>(p, lengths, plan, sums, b);
         grid_dependency_wait();
         grid_launch_dependents();
         if (v.nt == 0 || k0 >= v.L) return;
@@ -87,9 +85,7 @@ __global__ void __launch_bounds__(SM_THREADS)
             __syncthreads();
             for (int r = warp; r < nr; r += SM_WARPS) {
                 const int rr = r0 + r;
-                RowRecords src[2];
-                row_sources<SM_TILE>(p, rec, bm, gangs, v, b, g, rr, N, off, src);
-                const float2 ml = row_sum(rec, src);
+                const float2 ml = row_sum(rec, row_records<SM_TILE>(p, rec, plan, unit0, v.nt, b, g, rr));
                 if (lane == 0) row_ml[r] = make_float2(ml.x, 1.f / ml.y);
             }
             __syncthreads();
@@ -116,14 +112,14 @@ __global__ void __launch_bounds__(SM_THREADS)
 
 }  // namespace
 
-cudaError_t launch_span_merge(const SpanShape& p, const SpanRecords& rec, int bm, int gangs, float* O, int64_t ldo,
+cudaError_t launch_span_merge(const SpanShape& p, const SpanRecords& rec, int ctas, float* O, int64_t ldo,
                               const int32_t* lengths, const float* scores, float* weights, cudaStream_t stream) {
     const int64_t out_rows = (int64_t)p.B * p.per * p.h_kv * p.T_q;
     const int64_t blocks =
         out_rows + (weights != nullptr ? (int64_t)p.B * p.h_kv * ((p.T_max + SM_KEYS - 1) / SM_KEYS) : 0);
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     auto kernel = weights != nullptr ? span_merge_kernel<true> : span_merge_kernel<false>;
-    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(SM_THREADS), 0, stream, p, rec, bm, gangs, O, ldo, lengths,
+    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(SM_THREADS), 0, stream, p, rec, ctas, O, ldo, lengths,
                       scores, weights);
 }
 

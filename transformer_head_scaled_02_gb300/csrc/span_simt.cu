@@ -1,6 +1,6 @@
 // span_simt.cu -- the windowed attention and the cache operators on CUDA cores (fp32 layers):
 //   window_simt_kernel  causal sliding-window attention with sinks over whole sequences
-//   span_simt_kernel    the pieces of span.cuh: windowed, shared-prefix and weight-accumulating
+//   span_simt_kernel    the units of span.cuh: windowed, shared-prefix and weight-accumulating
 //                       decode steps
 // Both form score tiles of BQ = 16 RQ query rows x 64 keys as small matrix products in full fp32
 // (256 threads: thread (tx, ty) owns rows RQ ty.. and keys tx + 16 c), keep the online softmax in
@@ -248,13 +248,13 @@ __global__ void __launch_bounds__(SS_THREADS)
     const int tid = (int)threadIdx.x, tx = tid & 15, ty = tid >> 4;
     grid_dependency_wait();  // lengths, queries and caches may come from the previous kernel
     grid_launch_dependents();
-    const SpanStart start = span_start<SS_BK>(p, lengths);
+    SpanSums sums;
+    const SpanPlan plan = span_plan<SS_BK>(p, lengths, (int)gridDim.x, sums);
     if (blockIdx.x == 0)
         for (int b = tid; b < p.B; b += SS_THREADS)
             if (lengths[b] < p.T_q || lengths[b] > p.T_max) record_status(status, kStatusBadLength);
-    SpanWalk<SS_BK> walk(p, lengths, start);
-    SpanPiece q;
-    while (walk.next(q)) {
+    for (int u = (int)blockIdx.x; u < plan.N; u += (int)gridDim.x) {
+        const SpanUnit q = span_unit<SS_BK>(p, lengths, plan, sums, u);
         const int r0 = q.rb * X::BQ;
         const int nr = min(X::BQ, (q.prefix ? p.B * p.rows : p.rows) - r0);
         // batch, head and new token of row r of the block
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(SS_THREADS)
             head = q.g * p.per + rr / p.T_q;
             t = rr % p.T_q;
         };
-        __syncthreads();  // the previous piece's tiles are no longer read
+        __syncthreads();  // the previous unit's tiles are no longer read
         x.load_q([&](int r) -> const float* {
             if (r >= nr) return nullptr;
             int b, head, t;
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(SS_THREADS)
                    });
         }
         const bool direct = p.T_p == 0 && q.whole();
-        const int64_t slot = rec.row(p, q.prefix, q.block, (int)blockIdx.x / p.gang, (int)blockIdx.x % p.gang);
+        const int64_t slot = rec.row(p, q.unit, plan.np);
 #pragma unroll
         for (int r = 0; r < RQ; ++r) {
             const int rr = ty * RQ + r;
@@ -347,10 +347,10 @@ cudaError_t launch_window_f32(const float* Q, int64_t ldq, const float* K, int64
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_span_f32(const SpanShape& p, const SpanRecords& rec, int bm, const float* Q, int64_t ldq,
+cudaError_t launch_span_f32(const SpanShape& p, const SpanRecords& rec, const float* Q, int64_t ldq,
                             const float* K, int64_t ldk, const float* V, int64_t ldv, const float* Kp,
                             int64_t ldkp, const float* Vp, int64_t ldvp, float* O, int64_t ldo, int d_k, int d_v,
-                            const int32_t* lengths, float* scores, int gangs, int* status,
+                            const int32_t* lengths, float* scores, int ctas, int* status,
                             cudaStream_t stream) {
     auto al = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
     const bool vec = al(Q) && al(K) && al(V) && ldq % 4 == 0 && ldk % 4 == 0 && ldv % 4 == 0 && d_k % 4 == 0 &&
@@ -360,11 +360,11 @@ cudaError_t launch_span_f32(const SpanShape& p, const SpanRecords& rec, int bm, 
     auto launch = [&](auto kernel, size_t smem) {
         cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (err != cudaSuccess) return err;
-        return launch_pdl(kernel, dim3((unsigned)(gangs * p.gang)), dim3(SS_THREADS), smem, stream, p, rec, Q, ldq, K,
+        return launch_pdl(kernel, dim3((unsigned)ctas), dim3(SS_THREADS), smem, stream, p, rec, Q, ldq, K,
                           ldk, V, ldv, Kp, ldkp, Vp, ldvp, O, ldo, d_k, d_v, lengths, scores, scale, vec, status);
     };
 #define MHA_SS(RQ, CV) \
-    if (bm == 16 * RQ && cv == CV) return launch(span_simt_kernel<RQ, CV>, SimtTile<RQ, CV>::smem_bytes(d_k));
+    if (p.bm == 16 * RQ && cv == CV) return launch(span_simt_kernel<RQ, CV>, SimtTile<RQ, CV>::smem_bytes(d_k));
     MHA_SS(1, 1) MHA_SS(1, 2) MHA_SS(1, 3) MHA_SS(1, 4) MHA_SS(2, 1) MHA_SS(2, 2) MHA_SS(2, 3) MHA_SS(2, 4)
     MHA_SS(4, 1) MHA_SS(4, 2) MHA_SS(4, 3) MHA_SS(4, 4)
 #undef MHA_SS
