@@ -67,6 +67,7 @@ struct SpTail {
     SpanPlan plan;
     uint32_t tmem;
     int abort_flag, joined;
+    unsigned generation;
 };
 static_assert(sizeof(SpTail) <= 3072, "span tail");
 
@@ -91,29 +92,34 @@ __device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&v)[8]) {
                  : "memory");
 }
 
-// One thread of every CTA of a cooperative grid: waits until all have arrived.  The words behind the status
-// word (arrivals, generation, units taken) are as they were when it is over, so nothing has to clear them
-// between launches; a CTA arrives whatever happened to it before.
-__device__ __forceinline__ bool span_grid_barrier(int* status, int ctas) {
-    unsigned* arrived = reinterpret_cast<unsigned*>(status) + 1;
-    volatile unsigned* generation = reinterpret_cast<unsigned*>(status) + 2;
-    const unsigned g = *generation;
-    __threadfence();
-    if (atomicAdd(arrived, 1u) == (unsigned)ctas - 1u) {
-        *arrived = 0u;
+// One thread of every CTA of a cooperative grid: waits until all have arrived; g: the generation word as it
+// was when the CTA began.  The words behind the status word (arrivals, generation, units taken) are as they
+// were when it is over, so nothing has to clear them between launches; a CTA arrives whatever happened to
+// it before.
+__device__ __forceinline__ unsigned span_generation(const int* status) {
+    unsigned g;
+    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(g) : "l"(status + 2) : "memory");
+    return g;
+}
+
+__device__ __forceinline__ bool span_grid_barrier(int* status, int ctas, unsigned g) {
+    unsigned before, now;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(status + 1) : "memory");
+    if (before == (unsigned)ctas - 1u) {
+        status[1] = 0;
         status[3] = 0;
-        __threadfence();
-        *generation = g + 1u;
+        asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(status + 2), "r"(g + 1u) : "memory");
         return true;
     }
     const uint64_t t0 = globaltimer_ns();
-    while (*generation == g)
+    for (;;) {
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(now) : "l"(status + 2) : "memory");
+        if (now != g) return true;
         if (globaltimer_ns() - t0 > kWaitLimitNs) {
             record_status(status, kStatusTimeout);
             return false;
         }
-    __threadfence();
-    return true;
+    }
 }
 
 template <int HD>
@@ -158,6 +164,7 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
         mbar_init(bar(tail->mlfull), 8);
         mbar_init(bar(tail->drain), 1);
         tail->abort_flag = 0;
+        tail->generation = span_generation(status);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -612,7 +619,6 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
         }
         __syncwarp();
         tc_fence_before();
-        __threadfence();  // the records, before this CTA counts as arrived
         named_barrier_sync(1, SP_THREADS);
         // ---------------- all units are done: join (the softmax warps: they have the registers).  What does
         // not need the records is worked out before the others have arrived.
@@ -638,7 +644,8 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
             if (v.nt == 0) src.n[0] = src.n[1] = 0;  // invalid length
         };
         find_row();
-        if (jw == 0 && lane == 0) tail->joined = span_grid_barrier(status, (int)gridDim.x) ? 1 : 0;
+        // (the records of all this CTA's warps are behind the block barrier above)
+        if (jw == 0 && lane == 0) tail->joined = span_grid_barrier(status, (int)gridDim.x, tail->generation) ? 1 : 0;
         named_barrier_sync(2, JOIN);
         if (!tail->joined) return;
         float* part = reinterpret_cast<float*>(smem_raw);  // [warp][column]
@@ -649,11 +656,8 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
 #pragma unroll
             for (int e = 0; e < E; ++e) o[e] = n == 0 ? NAN : 0.f;
             if (n > 0) {
-                // records two at a time; a lane's columns of one are 16 (8) bytes
+                // one pass, the sums following the running maximum
                 float M = -INFINITY;
-                for (int c = lane; c < n; c += 32) M = fmaxf(M, __ldcg(rec.ml + src.at(c)).x);
-#pragma unroll
-                for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
                 l = 0.f;
 #pragma unroll 4
                 for (int c = few ? jw : 0; c < n; c += few ? JOIN_WARPS : 1) {
@@ -667,24 +671,31 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
                         const float2 y = __ldcg(reinterpret_cast<const float2*>(rec.o + k * HD) + lane);
                         x[0] = y.x; x[1] = y.y;
                     }
-                    const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
-                    l = fmaf(w, ml.y, l);
+                    const float m = fmaxf(M, ml.x);
+                    const float f = M == -INFINITY ? 0.f : ex2_approx(M - m), w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
+                    l = fmaf(w, ml.y, l * f);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) o[e] = fmaf(w, x[e], o[e]);
+                    for (int e = 0; e < E; ++e) o[e] = fmaf(w, x[e], o[e] * f);
+                    M = m;
                 }
                 if (few) {
                     float* mine = part + jw * (HD + 4);
 #pragma unroll
                     for (int e = 0; e < E; ++e) mine[lane * E + e] = o[e];
-                    if (lane == 0) mine[HD] = l;
+                    if (lane == 0) mine[HD] = l, mine[HD + 1] = M;
                     named_barrier_sync(2, JOIN);
                     l = 0.f;
 #pragma unroll
                     for (int e = 0; e < E; ++e) o[e] = 0.f;
-                    for (int w = 0; w < JOIN_WARPS; ++w) {
-                        l += part[w * (HD + 4) + HD];
 #pragma unroll
-                        for (int e = 0; e < E; ++e) o[e] += part[w * (HD + 4) + lane * E + e];
+                    for (int w = 0; w < JOIN_WARPS; ++w) M = fmaxf(M, part[w * (HD + 4) + HD + 1]);
+#pragma unroll
+                    for (int w = 0; w < JOIN_WARPS; ++w) {
+                        const float* his = part + w * (HD + 4);
+                        const float f = his[HD + 1] == -INFINITY ? 0.f : ex2_approx(his[HD + 1] - M);
+                        l = fmaf(f, his[HD], l);
+#pragma unroll
+                        for (int e = 0; e < E; ++e) o[e] = fmaf(f, his[lane * E + e], o[e]);
                     }
                     named_barrier_sync(2, JOIN);
                 }
