@@ -130,12 +130,16 @@ cudaError_t launch_window_bf16(const void* Q, int64_t ldq, const void* K, int64_
 // scores of every query row, [B][h_kv][rows][score_ld]; weights (nullable, with scores): the accumulated
 // attention weights.  bf16: one launch, status the first of four words of the status block.  fp32: the units, which
 // launch_span_merge then joins.
-int span_simt_rows(int64_t rows);  // row block of launch_span_f32: 16, 32 or 64
-cudaError_t launch_span_f32(const SpanShape& p, const SpanRecords& rec, const float* Q, int64_t ldq,
-                            const float* K, int64_t ldk, const float* V, int64_t ldv, const float* Kp,
-                            int64_t ldkp, const float* Vp, int64_t ldvp, float* O, int64_t ldo, int d_k, int d_v,
-                            const int32_t* lengths, float* scores, int ctas, int* status,
-                            cudaStream_t stream);
+// prefix_units, cache_units: the units that the call computes.
+cudaError_t launch_span_f32(const SpanShape& p, const SpanRecords& rec, const float* Q, int64_t ldq, const float* K,
+                            int64_t ldk, const float* V, int64_t ldv, const float* Kp, int64_t ldkp, const float* Vp,
+                            int64_t ldvp, float* O, int64_t ldo, int d_k, int d_v, const int32_t* lengths, float* scores,
+                            bool prefix_units, bool cache_units, int ctas, int* status, cudaStream_t stream);
+int span_few_rows(int d_k, int d_v);
+cudaError_t launch_span_few(const SpanShape& p, const SpanRecords& rec, const float* Q, int64_t ldq, const float* K,
+                            int64_t ldk, const float* V, int64_t ldv, const float* Kp, int64_t ldkp, const float* Vp,
+                            int64_t ldvp, float* O, int64_t ldo, int d_k, int d_v, const int32_t* lengths, float* scores,
+                            bool prefix_units, bool cache_units, int ctas, int* status, cudaStream_t stream);
 cudaError_t launch_span_bf16(const SpanShape& p, const SpanRecords& rec, const void* Q, int64_t ldq, const void* K,
                              int64_t ldk, const void* V, int64_t ldv, const void* Kp, int64_t ldkp, const void* Vp,
                              int64_t ldvp, void* O, int64_t ldo, int d, const int32_t* lengths, float* scores,

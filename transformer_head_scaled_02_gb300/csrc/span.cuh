@@ -3,14 +3,15 @@
 //
 // The query rows that share cached keys form groups: one per (batch, lane) over the batch's own cache,
 // and, with a shared prefix, one per lane over the prefix, whose rows are those of the whole batch; a lane is
-// a (K/V head, block of at most bm query rows).  A group's visible keys are at most two ranges, the sinks
+// a (K/V head, block of query rows).  A group's visible keys are at most two ranges, the sinks
 // [0, s) and the window [lo, L), each cut into tiles.  A unit is U consecutive tiles of one group (Up of a
 // prefix group): the CTAs take units one after another, so ragged lengths, group counts that do not
 // divide the SMs and SMs that are slower than others leave none idle (an even cut made beforehand left the
 // first CTA idle for a fifth of a step).  Units are numbered prefix first, then by batch, chunk and lane,
 // lanes fastest: a cached token's rows of all heads lie side by side, and units taken at about the same
-// time read whole pieces of DRAM pages.  U is chosen so that every CTA gets about kSpanUnits units, but no
-// unit's record of its rows costs more than a few percent of the unit.  A unit that holds a whole
+// time read whole pieces of DRAM pages.  U is chosen so that every CTA gets about `aim` units, but no
+// unit's record of its rows costs more than a few percent of the unit; Up so that every CTA gets at most about one
+// of the prefix.  A unit that holds a whole
 // group writes its output itself; the others leave a record per row (maximum, sum, weighted values), and
 // the join adds them in order:
 //   O = sum_u 2^(m_u - M) o_u / sum_u 2^(m_u - M) l_u,  M = max_u m_u   (scores in base 2).
@@ -22,7 +23,7 @@
 namespace mha {
 
 // Largest grid of the unit kernels (bounds the records; the host knows no SM count when it computes
-// workspace sizes), and units per CTA to aim for.
+// workspace sizes), and most units per CTA to aim for.
 constexpr int kSpanMaxCtas = 320;
 constexpr int kSpanUnits = 10;
 
@@ -34,15 +35,17 @@ struct SpanShape {
     int nrb;     // row blocks of such a group
     int T_p;     // shared prefix tokens (0: none)
     int nrbp;    // row blocks of the B * rows rows over the prefix
-    int bm;      // rows of a row block
+    int bm_c, bm_p;  // rows of a row block of a cache and of the prefix
+    int aim;     // units per CTA to aim for, at most kSpanUnits
+    int step;    // tiles that a CTA of the caches' kernel works on at a time: larger units are multiples of it
     int window;  // <= T_max; T_max: no window
     int sinks;
 
     __host__ __device__ int lanes_c() const { return h_kv * nrb; }
     __host__ __device__ int lanes_p() const { return h_kv * nrbp; }
     // rows of a record; fewest tiles of a unit whose records stay cheap beside its tiles
-    __host__ __device__ int rps_c() const { return rows < bm ? rows : bm; }
-    __host__ __device__ int rps_p() const { return (int64_t)B * rows < bm ? B * rows : bm; }
+    __host__ __device__ int rps_c() const { return rows < bm_c ? rows : bm_c; }
+    __host__ __device__ int rps_p() const { return (int64_t)B * rows < bm_p ? B * rows : bm_p; }
     __host__ __device__ int least_c() const { return (rps_c() + 15) / 16; }
     __host__ __device__ int least_p() const { return (rps_p() + 15) / 16; }
 };
@@ -134,10 +137,11 @@ __device__ inline SpanPlan span_plan(const SpanShape& p, const int32_t* lengths,
     for (int i = s.i0; i < s.i1; ++i) tiles += span_view<TILE>(p, __ldcg(lengths + i)).nt;
     const int np = span_prefix_tiles<TILE>(p);
     const unsigned total = __reduce_add_sync(0xffffffffu, (unsigned)tiles) * (unsigned)p.lanes_c() + (unsigned)(np * p.lanes_p());
-    const unsigned target = (unsigned)(kSpanUnits * ctas);
+    const unsigned target = (unsigned)(p.aim * ctas);
     SpanPlan q;
     q.U = max(p.least_c(), (int)((total + target - 1) / target));
     q.U = max(q.U, 1);
+    if (q.U > p.step / 2) q.U = (q.U + p.step - 1) / p.step * p.step;
     q.Up = max(max(q.U, p.least_p()), (np * p.lanes_p() + ctas - 1) / ctas);
     q.np = p.T_p > 0 ? (np + q.Up - 1) / q.Up * p.lanes_p() : 0;
     s.sum = 0;

@@ -13,9 +13,18 @@ using namespace mha;
 
 namespace {
 
-// Query rows of a row block: a tensor-core tile for bf16; for fp32 the smallest of 16, 32 and 64 that
-// holds the rows (a thread of the CUDA-core kernel owns 1, 2 or 4 of them).
-int row_block(const mha_s* m, int64_t rows) { return m->dtype == MHA_BF16 ? 128 : span_simt_rows(rows); }
+
+// Query rows of a row block: a tensor-core tile for bf16; for fp32 what a block of the few-row kernel holds
+// if it holds them all, else the smallest of 16, 32 and 64 that does (a thread of span_simt.cu's kernel owns
+// 1, 2 or 4 of them).  Measured both ways, 16 caches of 4096 tokens, 4 K/V heads, few rows | tiles: d = 64, 1
+// row 41 | 151 us, 8 rows 74 | 154; d = 128, 4 rows 68 | 273; d = 256, 2 rows 243 | 798.  Two caches of 1000:
+// 10 | 13, 17 | 14, 14 | 18, 19 | 28.  With 10 rows of d = 64 in two blocks of 8 instead of one of 16, 3 caches
+// of 300 visible tokens took 17 us instead of 12.
+int row_block(const mha_s* m, int64_t rows) {
+    if (m->dtype == MHA_BF16) return 128;
+    if (rows <= span_few_rows(m->dk, m->dv)) return span_few_rows(m->dk, m->dv);
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
 
 SpanShape span_shape(const mha_s* m, int B, int T_q, int T_max, int T_p, int window, int sinks) {
     SpanShape p;
@@ -28,9 +37,13 @@ SpanShape span_shape(const mha_s* m, int B, int T_q, int T_max, int T_p, int win
     p.T_p = T_p;
     // a prefix's rows are those of the whole batch
     const int64_t rows_p = (int64_t)B * p.rows;
-    p.bm = row_block(m, T_p > 0 ? rows_p : p.rows);
-    p.nrb = (p.rows + p.bm - 1) / p.bm;
-    p.nrbp = T_p > 0 ? (int)((rows_p + p.bm - 1) / p.bm) : 0;
+    p.bm_c = row_block(m, p.rows);
+    p.bm_p = row_block(m, rows_p);
+    p.nrb = (p.rows + p.bm_c - 1) / p.bm_c;
+    p.nrbp = T_p > 0 ? (int)((rows_p + p.bm_p - 1) / p.bm_p) : 0;
+    const bool few = p.bm_c < 16;
+    p.aim = few ? 1 : kSpanUnits;  // few rows: its units are long (1, 2 and 4 of them: 41, 46 and 50 us as above)
+    p.step = few ? 4 : 1;
     p.window = window < T_max ? window : T_max;
     p.sinks = sinks < T_max ? sinks : T_max;
     return p;
@@ -124,8 +137,19 @@ mha_status run_cache_step(mha_s* m, const CacheStep& a, cudaStream_t stream) {
     if (m->dtype == MHA_F32) {
         auto f = [](const void* x) { return static_cast<const float*>(x); };
         float* O = static_cast<float*>(a.O);
-        err = launch_span_f32(p, rec, f(a.Q), a.ldq, f(a.K), a.ldk, f(a.V), a.ldv, f(a.Kp), a.ldkp, f(a.Vp),
-                              a.ldvp, O, a.ldo, m->dk, m->dv, a.lengths, scores, ctas, status_ptr(m), stream);
+        // each kind of unit in the row blocks made for its rows: one launch if they are the same
+        auto units = [&](bool prefix, bool cache) {
+            const int bm = cache ? p.bm_c : p.bm_p;
+            auto launch = bm < 16 ? launch_span_few : launch_span_f32;
+            return launch(p, rec, f(a.Q), a.ldq, f(a.K), a.ldk, f(a.V), a.ldv, f(a.Kp), a.ldkp, f(a.Vp), a.ldvp, O, a.ldo,
+                          m->dk, m->dv, a.lengths, scores, prefix, cache, ctas, status_ptr(m), stream);
+        };
+        if (p.T_p == 0 || p.bm_p == p.bm_c) {
+            err = units(true, true);
+        } else {
+            err = units(true, false);
+            if (err == cudaSuccess) err = units(false, true);
+        }
         if (err == cudaSuccess)
             err = launch_span_merge(p, rec, ctas, O, a.ldo, a.lengths, scores, a.weights, stream);
     } else {

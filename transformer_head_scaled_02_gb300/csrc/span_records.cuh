@@ -62,16 +62,16 @@ template <int TILE>
 __device__ __forceinline__ RowRecords row_records(const SpanShape& p, const SpanRecords& rec, const SpanPlan& q, int unit0, int nt,
                                                   int b, int g, int rr) {
     RowRecords x;
-    const int rb = p.nrb == 1 ? 0 : rr / p.bm;
+    const int rb = p.nrb == 1 ? 0 : rr / p.bm_c;
     x.n[0] = (nt + q.U - 1) / q.U;
-    x.first[0] = rec.row(p, unit0 + g * p.nrb + rb, q.np) + (rr - rb * p.bm);
+    x.first[0] = rec.row(p, unit0 + g * p.nrb + rb, q.np) + (rr - rb * p.bm_c);
     x.step[0] = (int64_t)p.lanes_c() * p.rps_c();
     x.n[1] = 0;
     x.first[1] = x.step[1] = 0;
     if (p.T_p > 0) {
-        const int rp = b * p.rows + rr, rbp = rp / p.bm;
+        const int rp = b * p.rows + rr, rbp = rp / p.bm_p;
         x.n[1] = q.np / p.lanes_p();
-        x.first[1] = rec.row(p, g * p.nrbp + rbp, q.np) + (rp - rbp * p.bm);
+        x.first[1] = rec.row(p, g * p.nrbp + rbp, q.np) + (rp - rbp * p.bm_p);
         x.step[1] = (int64_t)p.lanes_p() * p.rps_p();
     }
     return x;

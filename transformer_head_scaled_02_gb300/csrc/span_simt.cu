@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(SS_THREADS)
                      const float* __restrict__ Kp, int64_t ldkp, const float* __restrict__ Vp, int64_t ldvp,
                      float* __restrict__ O, int64_t ldo, int dk, int dv,
                      const int32_t* __restrict__ lengths, float* __restrict__ scores, float scale_log2,
-                     bool vec, int* status) {
+                     bool vec, int prefix_units, int cache_units, int* status) {
     using X = SimtTile<RQ, CV>;
     extern __shared__ __align__(16) float fsm[];
     X x(fsm, dk, dv);
@@ -253,7 +253,8 @@ __global__ void __launch_bounds__(SS_THREADS)
     if (blockIdx.x == 0)
         for (int b = tid; b < p.B; b += SS_THREADS)
             if (lengths[b] < p.T_q || lengths[b] > p.T_max) record_status(status, kStatusBadLength);
-    for (int u = (int)blockIdx.x; u < plan.N; u += (int)gridDim.x) {
+    const int end = cache_units ? plan.N : plan.np;
+    for (int u = (prefix_units ? 0 : plan.np) + (int)blockIdx.x; u < end; u += (int)gridDim.x) {
         const SpanUnit q = span_unit<SS_BK>(p, lengths, plan, sums, u);
         const int r0 = q.rb * X::BQ;
         const int nr = min(X::BQ, (q.prefix ? p.B * p.rows : p.rows) - r0);
@@ -320,8 +321,6 @@ __global__ void __launch_bounds__(SS_THREADS)
 
 }  // namespace
 
-int span_simt_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
-
 cudaError_t launch_window_f32(const float* Q, int64_t ldq, const float* K, int64_t ldk, const float* V,
                               int64_t ldv, const float* G, int64_t ldg, float* O, int64_t ldo, int B, int h,
                               int h_kv, int T, int d_k, int d_v, int window, int sinks,
@@ -347,11 +346,10 @@ cudaError_t launch_window_f32(const float* Q, int64_t ldq, const float* K, int64
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_span_f32(const SpanShape& p, const SpanRecords& rec, const float* Q, int64_t ldq,
-                            const float* K, int64_t ldk, const float* V, int64_t ldv, const float* Kp,
-                            int64_t ldkp, const float* Vp, int64_t ldvp, float* O, int64_t ldo, int d_k, int d_v,
-                            const int32_t* lengths, float* scores, int ctas, int* status,
-                            cudaStream_t stream) {
+cudaError_t launch_span_f32(const SpanShape& p, const SpanRecords& rec, const float* Q, int64_t ldq, const float* K,
+                            int64_t ldk, const float* V, int64_t ldv, const float* Kp, int64_t ldkp, const float* Vp,
+                            int64_t ldvp, float* O, int64_t ldo, int d_k, int d_v, const int32_t* lengths, float* scores,
+                            bool prefix_units, bool cache_units, int ctas, int* status, cudaStream_t stream) {
     auto al = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
     const bool vec = al(Q) && al(K) && al(V) && ldq % 4 == 0 && ldk % 4 == 0 && ldv % 4 == 0 && d_k % 4 == 0 &&
                      d_v % 4 == 0 && (p.T_p == 0 || (al(Kp) && al(Vp) && ldkp % 4 == 0 && ldvp % 4 == 0));
@@ -361,10 +359,12 @@ cudaError_t launch_span_f32(const SpanShape& p, const SpanRecords& rec, const fl
         cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (err != cudaSuccess) return err;
         return launch_pdl(kernel, dim3((unsigned)ctas), dim3(SS_THREADS), smem, stream, p, rec, Q, ldq, K,
-                          ldk, V, ldv, Kp, ldkp, Vp, ldvp, O, ldo, d_k, d_v, lengths, scores, scale, vec, status);
+                          ldk, V, ldv, Kp, ldkp, Vp, ldvp, O, ldo, d_k, d_v, lengths, scores, scale, vec,
+                          prefix_units ? 1 : 0, cache_units ? 1 : 0, status);
     };
+    const int bm = cache_units ? p.bm_c : p.bm_p;
 #define MHA_SS(RQ, CV) \
-    if (p.bm == 16 * RQ && cv == CV) return launch(span_simt_kernel<RQ, CV>, SimtTile<RQ, CV>::smem_bytes(d_k));
+    if (bm == 16 * RQ && cv == CV) return launch(span_simt_kernel<RQ, CV>, SimtTile<RQ, CV>::smem_bytes(d_k));
     MHA_SS(1, 1) MHA_SS(1, 2) MHA_SS(1, 3) MHA_SS(1, 4) MHA_SS(2, 1) MHA_SS(2, 2) MHA_SS(2, 3) MHA_SS(2, 4)
     MHA_SS(4, 1) MHA_SS(4, 2) MHA_SS(4, 3) MHA_SS(4, 4)
 #undef MHA_SS
