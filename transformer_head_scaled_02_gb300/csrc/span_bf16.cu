@@ -472,23 +472,6 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
                         }
                         tmem_wait_st();
                     }
-                    if (scores != nullptr && !q.prefix) {
-                        // (the loads are warp-wide; a group's padding rows store nothing, keys past the end
-                        // are masked and lie in the row's padding)
-                        float4* out = reinterpret_cast<float4*>(
-                            scores + (((int64_t)q.b * p.h_kv + q.g) * p.rows + q.rb * 128 + (real ? r : 0)) * score_ld(p) + key0);
-#pragma unroll 1
-                        for (int c = 0; c < n; c += 32) {
-                            uint32_t sr[32];
-                            tmem_ld32(s_col + c, sr);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int u = 0; u < 32; u += 4)
-                                if (real && c + u < n)
-                                    out[(c + u) / 4] = make_float4(__uint_as_float(sr[u]) * scale_log2, __uint_as_float(sr[u + 1]) * scale_log2,
-                                                                   __uint_as_float(sr[u + 2]) * scale_log2, __uint_as_float(sr[u + 3]) * scale_log2);
-                        }
-                    }
                     // any reference m gives the same O / l as long as P stays finite: keep it until a row's
                     // sum passes 2^64 (or is not finite: m = -inf), then take the tile's maximum and redo
                     uint32_t pk[64];
@@ -497,6 +480,14 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
                     for (;;) {
                         float x[128];
                         load_scores(s_col, x);
+                        if (scores != nullptr && real && !q.prefix) {
+                            // (keys past the end are masked and lie in the row's padding)
+                            float4* out = reinterpret_cast<float4*>(
+                                scores + (((int64_t)q.b * p.h_kv + q.g) * p.rows + q.rb * 128 + r) * score_ld(p) + key0);
+#pragma unroll
+                            for (int c = 0; c < SP_TK; c += 4)
+                                if (c < n) out[c / 4] = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
+                        }
                         if (renew) {
                             const float m_new = fmaxf(m, row_max(x) * scale_log2);
                             alpha = m_new == -INFINITY ? 1.f : ex2_approx(m - m_new);  // 0 when m leaves -inf
@@ -708,13 +699,13 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
             }
         }
         if (weights != nullptr) {
-            // a token's weight is the sum over the query rows of 2^(s - M) / l, in row order.  A warp takes 512
-            // tokens of one (batch, K/V head) at a time, a lane the sums of one row.
+            // a token's weight is the sum over the query rows of 2^(c s - M) / l, in row order.  A warp takes 512
+            // tokens of one (batch, K/V head) at a time, from the last CTA on (the first have rows to join).
             constexpr int PER = 16, KEYS = 32 * PER;
             const int chunks = (p.T_max + KEYS - 1) / KEYS;
             const int64_t tasks = (int64_t)p.B * p.h_kv * chunks;
             const int64_t ld = score_ld(p);
-            for (int64_t task = (int64_t)blockIdx.x * JOIN_WARPS + jw; task < tasks; task += (int64_t)gridDim.x * JOIN_WARPS) {
+            for (int64_t task = (int64_t)jw * gridDim.x + (gridDim.x - 1 - blockIdx.x); task < tasks; task += (int64_t)gridDim.x * JOIN_WARPS) {
                 const int bg = (int)(task / chunks), k0 = (int)(task - (int64_t)bg * chunks) * KEYS;
                 const int b = bg / p.h_kv, g = bg - b * p.h_kv;
                 const SpanView v = span_view<SP_TK>(p, __ldcg(lengths + b));
@@ -727,14 +718,24 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
                 float w[PER] = {};
                 for (int r0 = 0; r0 < p.rows; r0 += 32) {
                     const int nr = min(32, p.rows - r0);
-                    const RowRecords x = row_records<SP_TK>(p, rec, plan, unit0, v.nt, b, g, r0 + min(lane, nr - 1));
-                    float M = -INFINITY, l = 0.f;  // of row r0 + lane
+                    // the sums of row r0 + (lane mod span), its records shared by 32 / span lanes
+                    const int span = nr == 1 ? 1 : 1 << (32 - __clz(nr - 1));
+                    const RowRecords x = row_records<SP_TK>(p, rec, plan, unit0, v.nt, b, g, r0 + min(lane & (span - 1), nr - 1));
+                    float M = -INFINITY, l = 0.f;
+                    auto add = [&](float m2, float l2) {
+                        const float m = fmaxf(M, m2);
+                        const float f = M == -INFINITY ? 0.f : ex2_approx(M - m), f2 = m2 == -INFINITY ? 0.f : ex2_approx(m2 - m);
+                        l = fmaf(f2, l2, l * f);
+                        M = m;
+                    };
 #pragma unroll 8
-                    for (int c = 0; c < x.count(); ++c) M = fmaxf(M, __ldcg(rec.ml + x.at(c)).x);
-#pragma unroll 8
-                    for (int c = 0; c < x.count(); ++c) {
+                    for (int c = lane / span; c < x.count(); c += 32 / span) {
                         const float2 ml = __ldcg(rec.ml + x.at(c));
-                        l = fmaf(ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M), ml.y, l);
+                        add(ml.x, ml.y);
+                    }
+                    for (int o = span; o < 32; o <<= 1) {
+                        const float m2 = __shfl_xor_sync(0xffffffffu, M, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+                        add(m2, l2);
                     }
                     const float il = 1.f / l;
                     const float* s = scores + ((int64_t)bg * p.rows + r0) * ld;
@@ -750,7 +751,7 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
                         for (int i = 0; i < 2; ++i) {
                             const float m = __shfl_sync(0xffffffffu, M, min(r + i, nr - 1)), f = __shfl_sync(0xffffffffu, il, min(r + i, nr - 1));
 #pragma unroll
-                            for (int u = 0; u < PER; ++u) w[u] = fmaf(ex2_approx(sv[i][u] - m), f, w[u]);
+                            for (int u = 0; u < PER; ++u) w[u] = fmaf(ex2_approx(fmaf(sv[i][u], scale_log2, -m)), f, w[u]);
                         }
                     }
                 }
