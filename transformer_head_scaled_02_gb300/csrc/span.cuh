@@ -123,8 +123,15 @@ struct SpanPlan {
 
 struct SpanSums {
     int i0, i1;       // this lane's batches
+    int L0;           // length of batch i0: up to 32 batches, lengths are read once
     int before, sum;  // first unit of batch i0, units of the lane's batches
+    __device__ __forceinline__ int length(const int32_t* lengths, int i) const { return i == i0 ? L0 : __ldcg(lengths + i); }
 };
+
+template <int TILE>
+__device__ __forceinline__ int span_units(const SpanShape& p, const SpanPlan& q, int L) {
+    return (span_view<TILE>(p, L).nt + q.U - 1) / q.U * p.lanes_c();
+}
 
 // All lanes of a warp call it; ctas: the grid of the unit kernel.
 template <int TILE>
@@ -133,8 +140,9 @@ __device__ inline SpanPlan span_plan(const SpanShape& p, const int32_t* lengths,
     const int run = (p.B + 31) / 32;
     s.i0 = min(p.B, lane * run);
     s.i1 = min(p.B, s.i0 + run);
+    s.L0 = s.i0 < s.i1 ? __ldcg(lengths + s.i0) : 0;
     int tiles = 0;
-    for (int i = s.i0; i < s.i1; ++i) tiles += span_view<TILE>(p, __ldcg(lengths + i)).nt;
+    for (int i = s.i0; i < s.i1; ++i) tiles += span_view<TILE>(p, s.length(lengths, i)).nt;
     const int np = span_prefix_tiles<TILE>(p);
     const unsigned total = __reduce_add_sync(0xffffffffu, (unsigned)tiles) * (unsigned)p.lanes_c() + (unsigned)(np * p.lanes_p());
     const unsigned target = (unsigned)(p.aim * ctas);
@@ -145,7 +153,7 @@ __device__ inline SpanPlan span_plan(const SpanShape& p, const int32_t* lengths,
     q.Up = max(max(q.U, p.least_p()), (np * p.lanes_p() + ctas - 1) / ctas);
     q.np = p.T_p > 0 ? (np + q.Up - 1) / q.Up * p.lanes_p() : 0;
     s.sum = 0;
-    for (int i = s.i0; i < s.i1; ++i) s.sum += (span_view<TILE>(p, __ldcg(lengths + i)).nt + q.U - 1) / q.U * p.lanes_c();
+    for (int i = s.i0; i < s.i1; ++i) s.sum += span_units<TILE>(p, q, s.length(lengths, i));
     int inc = s.sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -157,17 +165,20 @@ __device__ inline SpanPlan span_plan(const SpanShape& p, const int32_t* lengths,
     return q;
 }
 
-// First unit of batch b (all lanes of a warp; b the same in all).
+// First unit and length of batch b (all lanes of a warp; b the same in all).
 template <int TILE>
 __device__ __forceinline__ int span_first_unit(const SpanShape& p, const int32_t* lengths, const SpanPlan& q, const SpanSums& s,
-                                               int b) {
-    int at = 0;
+                                               int b, int& L) {
+    int at = 0, len = 0;
     const bool mine = s.i0 <= b && b < s.i1;
     if (mine) {
         at = s.before;
-        for (int i = s.i0; i < b; ++i) at += (span_view<TILE>(p, __ldcg(lengths + i)).nt + q.U - 1) / q.U * p.lanes_c();
+        for (int i = s.i0; i < b; ++i) at += span_units<TILE>(p, q, s.length(lengths, i));
+        len = s.length(lengths, b);
     }
-    return __shfl_sync(0xffffffffu, at, __ffs(__ballot_sync(0xffffffffu, mine)) - 1);
+    const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+    L = __shfl_sync(0xffffffffu, len, src);
+    return __shfl_sync(0xffffffffu, at, src);
 }
 
 struct SpanUnit {
@@ -197,12 +208,13 @@ __device__ inline SpanUnit span_unit(const SpanShape& p, const int32_t* lengths,
         nrb = p.nrbp;
     } else {
         x.prefix = 0;
-        int b = 0, at = 0;
+        int b = 0, at = 0, len = 0;
         const bool mine = s.before <= u && u < s.before + s.sum;
         if (mine) {
             at = s.before;
             for (b = s.i0;; ++b) {
-                const int n = (span_view<TILE>(p, __ldcg(lengths + b)).nt + q.U - 1) / q.U * p.lanes_c();
+                len = s.length(lengths, b);
+                const int n = span_units<TILE>(p, q, len);
                 if (u < at + n) break;
                 at += n;
             }
@@ -210,7 +222,7 @@ __device__ inline SpanUnit span_unit(const SpanShape& p, const int32_t* lengths,
         const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
         x.b = __shfl_sync(0xffffffffu, b, src);
         at = __shfl_sync(0xffffffffu, at, src);
-        x.v = span_view<TILE>(p, __ldcg(lengths + x.b));
+        x.v = span_view<TILE>(p, __shfl_sync(0xffffffffu, len, src));
         k = (u - at) / p.lanes_c();
         lane_i = u - at - k * p.lanes_c();
         U = q.U;

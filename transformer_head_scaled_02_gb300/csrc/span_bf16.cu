@@ -627,11 +627,12 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
         auto find_row = [&]() {
             if (row >= out_rows) return;
             const int bh = p.T_q == 1 ? row : row / p.T_q, t = row - bh * p.T_q, b = bh / heads, head = bh - b * heads;
-            const SpanView v = span_view<SP_TK>(p, __ldcg(lengths + b));
+            int L;
+            const int unit0 = span_first_unit<SP_TK>(p, lengths, plan, sums, b, L);
+            const SpanView v = span_view<SP_TK>(p, L);
             const int g = head / p.per;
             out = O + ((int64_t)b * p.T_q + t) * ldo + (int64_t)head * HD + lane * E;
-            src = row_records<SP_TK>(p, rec, plan, span_first_unit<SP_TK>(p, lengths, plan, sums, b), v.nt, b, g,
-                                     (head - g * p.per) * p.T_q + t);
+            src = row_records<SP_TK>(p, rec, plan, unit0, v.nt, b, g, (head - g * p.per) * p.T_q + t);
             if (v.nt == 0) src.n[0] = src.n[1] = 0;  // invalid length
         };
         find_row();
@@ -708,9 +709,10 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
             for (int64_t task = (int64_t)jw * gridDim.x + (gridDim.x - 1 - blockIdx.x); task < tasks; task += (int64_t)gridDim.x * JOIN_WARPS) {
                 const int bg = (int)(task / chunks), k0 = (int)(task - (int64_t)bg * chunks) * KEYS;
                 const int b = bg / p.h_kv, g = bg - b * p.h_kv;
-                const SpanView v = span_view<SP_TK>(p, __ldcg(lengths + b));
+                int L;
+                const int unit0 = span_first_unit<SP_TK>(p, lengths, plan, sums, b, L);
+                const SpanView v = span_view<SP_TK>(p, L);
                 if (v.nt == 0 || k0 >= v.L) continue;
-                const int unit0 = span_first_unit<SP_TK>(p, lengths, plan, sums, b);
                 // this lane's keys; those past the length read the last one's scores and are dropped
                 int key[PER];
 #pragma unroll

@@ -36,8 +36,10 @@ __global__ void __launch_bounds__(SM_THREADS)
         const int t = row % p.T_q, bh = row / p.T_q, b = bh / heads, head = bh - b * heads;
         float* out = O + ((int64_t)b * p.T_q + t) * ldo + (int64_t)head * rec.dv;
         const int g = head / p.per, rr = (head - g * p.per) * p.T_q + t;
-        const SpanView v = span_view<SM_TILE>(p, __ldcg(lengths + b));
-        const RowRecords src = row_records<SM_TILE>(p, rec, plan, span_first_unit<SM_TILE>(p, lengths, plan, sums, b), v.nt, b, g, rr);
+        int L;
+        const int unit0 = span_first_unit<SM_TILE>(p, lengths, plan, sums, b, L);
+        const SpanView v = span_view<SM_TILE>(p, L);
+        const RowRecords src = row_records<SM_TILE>(p, rec, plan, unit0, v.nt, b, g, rr);
         grid_dependency_wait();
         grid_launch_dependents();
         if (v.nt == 0) {  // invalid length
@@ -74,8 +76,9 @@ __global__ void __launch_bounds__(SM_THREADS)
         const int i = (int)blockIdx.x - out_rows;
         const int bg = i / chunks, k0 = (i - bg * chunks) * SM_KEYS;
         const int b = bg / p.h_kv, g = bg - b * p.h_kv;
-        const SpanView v = span_view<SM_TILE>(p, __ldcg(lengths + b));
-        const int unit0 = span_first_unit<SM_TILE>(p, lengths, plan, sums, b);
+        int L;
+        const int unit0 = span_first_unit<SM_TILE>(p, lengths, plan, sums, b, L);
+        const SpanView v = span_view<SM_TILE>(p, L);
         grid_dependency_wait();
         grid_launch_dependents();
         if (v.nt == 0 || k0 >= v.L) return;
