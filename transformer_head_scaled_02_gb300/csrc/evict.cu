@@ -91,10 +91,6 @@ __global__ void __launch_bounds__(EV_THREADS)
         return;
     }
     const int n_early = L - recent;  // > keep - recent >= 0
-    if constexpr (KEYS) {
-        for (int j = tid; j < n_early; j += EV_THREADS) keys_s[j] = weight_key(w[j]);
-        __syncthreads();
-    }
     auto key = [&](int j) { return KEYS ? keys_s[j] : weight_key(w[j]); };
     // radix selection: `prefix` holds the digits fixed so far, `need` how many of the keys that agree
     // with them are kept, `equal` how many there are
@@ -105,9 +101,19 @@ __global__ void __launch_bounds__(EV_THREADS)
         const uint32_t mask = shift == 0 ? 1023u : 2047u;
         for (int i = tid; i < EV_BINS; i += EV_THREADS) hist[i] = 0;
         __syncthreads();
-        for (int j = tid; j < n_early; j += EV_THREADS) {
-            const uint32_t k = key(j);
-            if ((k & fixed) == prefix) atomicAdd(&hist[(k >> shift) & mask], 1);
+        if (!KEYS || shift == 21) {  // from the weights
+#pragma unroll 4
+            for (int j = tid; j < n_early; j += EV_THREADS) {
+                const uint32_t k = weight_key(w[j]);
+                if constexpr (KEYS) keys_s[j] = k;
+                if ((k & fixed) == prefix) atomicAdd(&hist[(k >> shift) & mask], 1);
+            }
+        } else {
+#pragma unroll 4
+            for (int j = tid; j < n_early; j += EV_THREADS) {
+                const uint32_t k = keys_s[j];
+                if ((k & fixed) == prefix) atomicAdd(&hist[(k >> shift) & mask], 1);
+            }
         }
         __syncthreads();
         // thread i: digits from the top down; the digit where the running count reaches need
@@ -141,11 +147,15 @@ __global__ void __launch_bounds__(EV_THREADS)
     int eq_base = 0, keep_base = 0;
     for (int j0 = 0; j0 < L; j0 += EV_SCAN) {
         const int steps = min(EV_STEPS, (L - j0 + EV_THREADS - 1) / EV_THREADS);
-        // place of the first token of each 32, counting those that f says
+        // places of the first token of each 32, counting those that f says; bit i of the result: what f says of
+        // this thread's token of step i
         auto number = [&](auto f, int& sum) {
+            uint32_t mine = 0u;
 #pragma unroll 4
             for (int i = 0; i < steps; ++i) {
-                const unsigned m = __ballot_sync(0xffffffffu, f(i, j0 + i * EV_THREADS + tid));
+                const bool is = f(i, j0 + i * EV_THREADS + tid);
+                const unsigned m = __ballot_sync(0xffffffffu, is);
+                mine |= is ? 1u << i : 0u;
                 if (lane == 0) counts[i * EV_WARPS + warp] = (int16_t)__popc(m);
             }
             __syncthreads();
@@ -153,15 +163,15 @@ __global__ void __launch_bounds__(EV_THREADS)
             at = block_scan(at, warp_sums, sum);
             base[tid] = at;
             __syncthreads();
+            return mine;
         };
         static_assert(EV_STEPS * EV_WARPS == EV_THREADS, "one count per thread");
         uint32_t eq_taken = 0u;  // bit i: this thread's token of step i is equal and among the first `need`
         if (any && need < equal) {
             int sum;
-            auto is_eq = [&](int, int j) { return j < n_early && key(j) == prefix; };
-            number(is_eq, sum);
+            const uint32_t eq = number([&](int, int j) { return j < n_early && key(j) == prefix; }, sum);
             for (int i = 0; i < steps; ++i) {
-                const bool e = is_eq(i, j0 + i * EV_THREADS + tid);
+                const bool e = (eq >> i) & 1u;
                 const unsigned m = __ballot_sync(0xffffffffu, e);
                 if (e && eq_base + base[i * EV_WARPS + warp] + __popc(m & ((1u << lane) - 1u)) < need) eq_taken |= 1u << i;
             }
@@ -177,19 +187,25 @@ __global__ void __launch_bounds__(EV_THREADS)
             return any && (k > prefix || (k == prefix && ((eq_taken >> i) & 1u)));
         };
         int sum;
-        number(taken, sum);
+        const uint32_t mine = number(taken, sum);
         // in place: a token's place is at most its index, every weight up to j0 has been read, and
-        // those of a step are read by all before any of that step's is written
-        for (int i = 0; i < steps; ++i) {
-            const int j = j0 + i * EV_THREADS + tid;
-            const bool t = taken(i, j);
-            const float wj = j < L ? w[j] : 0.f;
-            const unsigned m = __ballot_sync(0xffffffffu, t);
+        // those of some steps are read by all before any of theirs is written
+        constexpr int AT_ONCE = 8;
+        for (int i0 = 0; i0 < steps; i0 += AT_ONCE) {
+            float wj[AT_ONCE];
+#pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i)
+                if ((mine >> (i0 + i)) & 1u) wj[i] = w[j0 + (i0 + i) * EV_THREADS + tid];
             __syncthreads();
-            if (t) {
-                const int at = keep_base + base[i * EV_WARPS + warp] + __popc(m & ((1u << lane) - 1u));
-                out[at] = j;
-                w_out[at] = wj;
+#pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i) {
+                const bool t = (mine >> (i0 + i)) & 1u;
+                const unsigned m = __ballot_sync(0xffffffffu, t);
+                if (t) {
+                    const int at = keep_base + base[(i0 + i) * EV_WARPS + warp] + __popc(m & ((1u << lane) - 1u));
+                    out[at] = j0 + (i0 + i) * EV_THREADS + tid;
+                    w_out[at] = wj[i];
+                }
             }
         }
         keep_base += sum;

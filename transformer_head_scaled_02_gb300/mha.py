@@ -301,6 +301,15 @@ class Mha:
             return s0 if T == 1 else s1
         return max(s1, width)  # one row (or none): any stride of at least a row will do
 
+    def _prefix(self, name: str, t: torch.Tensor, T: int, width: int) -> int:
+        """_rows for the (T, width) view of a shared prefix."""
+        if t.shape != (T, width):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, width)}")
+        s0, s1 = t.stride()
+        if t.dtype != self.dtype or s1 != 1:
+            raise ValueError(f"{name} must be a (T,*) {self.dtype} view with contiguous rows")
+        return s0 if T > 1 else max(s0, width)
+
     @staticmethod
     def _device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
         """All on one CUDA device, the current one; returns its current stream."""
@@ -384,8 +393,8 @@ class Mha:
         and V_prefix (T_prefix, h_kv*d_v view) are stored and read once for the whole batch; the
         caches and cache_lengths hold each sequence's own tokens after them, the new ones included."""
         T_p = K_prefix.shape[0]
-        ldkp = self._rows("K_prefix", K_prefix.unsqueeze(0), 1, T_p, self.h_kv * self.d_k)
-        ldvp = self._rows("V_prefix", V_prefix.unsqueeze(0), 1, T_p, self.h_kv * self.d_v)
+        ldkp = self._prefix("K_prefix", K_prefix, T_p, self.h_kv * self.d_k)
+        ldvp = self._prefix("V_prefix", V_prefix, T_p, self.h_kv * self.d_v)
         out, (B, T_q, T_max), cache, lens, tail = self._cache_step(
             Q, K_cache, V_cache, cache_lengths, out, T_p, 0, K_prefix, V_prefix)
         _lib.mha_decode_shared(self.handle, B, T_q, T_p, K_prefix.data_ptr(), ldkp, V_prefix.data_ptr(),
