@@ -8,7 +8,14 @@
 // threads sharing the rows, by shuffles), stage P in shared memory and add P V to RQ x 4 CV outputs
 // per thread.  Q, K and V tiles are row-major in shared memory with rows padded by 4 floats: global
 // loads are coalesced 16-byte pieces and the 16-byte reads of a product step (8 keys a quarter
-// warp apart by d_k + 4 floats) touch every bank once.
+// warp apart by d_k + 4 floats) touch every bank once.  One K and one V tile: the next K comes in behind
+// the score product, the next V behind the value product, each under the other half of the work.
+//
+// Bound by the issue of FMAs and the waits between the halves (two blocks an SM).  Measured with asynchronous
+// copies and packed score products | with plain loads of both tiles before a step: window of 256 over 2 x 8
+// heads x 2048 rows, d = 64 98 | 112 us (36 % of the FMA rate), d = 128 218 | 306, d = 256 360 | 548; weights
+// of 16 caches of 4096 tokens, 4 K/V heads, 20 rows of d = 64 180 | 227, 64 rows of d = 128 611 | 759; but one
+// or two tiles a block (64 rows of d = 64 over a prefix of 4096) 59 | 51.
 #include <math.h>
 
 #include "internal.h"
@@ -21,6 +28,16 @@ namespace {
 constexpr int SS_BK = 64;
 constexpr int SS_THREADS = 256;
 constexpr int SS_PS = SS_BK + 4;  // row stride of P
+
+// 16 bytes, or 16 zero bytes, to shared memory.
+__device__ __forceinline__ void cp_async16(float* dst, const float* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 template <int RQ, int CV>
 struct SimtTile {
@@ -72,55 +89,101 @@ struct SimtTile {
         }
     }
 
-    // n keys (rows past n are zero: whatever lies there never reaches a product)
-    __device__ void load_kv(const float* K, int64_t ldk, const float* V, int64_t ldv, int n, bool vec) {
-        const int k4 = dk4 / 4;
-        for (int i = (int)threadIdx.x; i < SS_BK * k4; i += SS_THREADS) {
-            const int j = i / k4, e = (i - j * k4) * 4;
-            *reinterpret_cast<float4*>(&Ks[j * ks + e]) =
-                j < n ? load4(K + j * ldk + e, dk - e, vec) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        for (int i = (int)threadIdx.x; i < SS_BK * (VS / 4); i += SS_THREADS) {
-            const int j = i / (VS / 4), e = (i - j * (VS / 4)) * 4;
-            *reinterpret_cast<float4*>(&Vs[j * VS + e]) =
-                j < n && e < dv ? load4(V + j * ldv + e, dv - e, vec) : make_float4(0.f, 0.f, 0.f, 0.f);
+    // n rows of a key or value tile, zeros past them and past `width` (whatever lies there never reaches a
+    // product): asynchronous copies where 16-byte pieces are aligned.
+    static __device__ void load_rows(float* dst, int stride, int cols, const float* src, int64_t ld, int n, int width, bool vec) {
+        const int tx = (int)threadIdx.x & 15, ty = (int)threadIdx.x >> 4;
+        for (int e = 4 * tx; e < cols; e += 64)
+#pragma unroll
+            for (int i = 0; i < SS_BK / 16; ++i) {
+                const int j = ty + 16 * i;
+                const bool in = j < n && e < width;
+                float* to = dst + j * stride + e;
+                if (vec)
+                    cp_async16(to, in ? src + j * ld + e : src, in ? 16 : 0);
+                else
+                    *reinterpret_cast<float4*>(to) = in ? load4(src + j * ld + e, width - e, false) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+    }
+
+    __device__ void load_k(const float* K, int64_t ld, int n, bool vec) { load_rows(Ks, ks, dk4, K, ld, n, dk, vec); }
+    __device__ void load_v(const float* V, int64_t ld, int n, bool vec) { load_rows(Vs, VS, VS, V, ld, n, dv, vec); }
+
+    // All key tiles of a range: tile(i, k0, n) gives their keys [k0, k0 + n); visible(row in block, key) and
+    // score(row in block, key, s), which sees every masked base-2 score.  The next keys are on their way
+    // during the softmax and the value product, the next values during the score product.
+    template <class T, class F, class G>
+    __device__ void run(int i0, int i1, T tile, const float* K, int64_t ldk, const float* V, int64_t ldv, bool vec,
+                        float scale_log2, F visible, G score) {
+        int k0, n;
+        tile(i0, k0, n);
+        __syncthreads();  // the tiles of the last range are no longer read
+        load_k(K + k0 * ldk, ldk, n, vec);
+        cp_async_commit();
+        load_v(V + k0 * ldv, ldv, n, vec);
+        cp_async_commit();
+        for (int i = i0; i < i1; ++i) {
+            int next_k0 = 0, next_n = 0;
+            if (i + 1 < i1) tile(i + 1, next_k0, next_n);
+            cp_async_wait<1>();
+            __syncthreads();
+            uint64_t sc2[RQ][4];
+            products(sc2);
+            __syncthreads();
+            if (next_n > 0) load_k(K + next_k0 * ldk, ldk, next_n, vec);
+            cp_async_commit();
+            softmax(sc2, n, scale_log2, [&](int r, int j) { return visible(r, k0 + j); }, [&](int r, int j, float v) { score(r, k0 + j, v); });
+            cp_async_wait<1>();
+            __syncthreads();
+            values(n);
+            if (next_n > 0) {
+                __syncthreads();
+                load_v(V + next_k0 * ldv, ldv, next_n, vec);
+            }
+            cp_async_commit();
+            k0 = next_k0;
+            n = next_n;
         }
     }
 
-    // One key tile: visible(row in block, key in tile); score(row in block, key in tile, s) sees
-    // every masked base-2 score.  The caller synchronises before and after.
-    template <class F, class G>
-    __device__ void step(int n, float scale_log2, F visible, G score) {
+    // Scores of a tile before their scale, as sums over the even and the odd elements (packed products: half
+    // the instructions).
+    __device__ void products(uint64_t (&sc)[RQ][4]) {
         const int tx = (int)threadIdx.x & 15, ty = (int)threadIdx.x >> 4;
-        float sc[RQ][4];
 #pragma unroll
         for (int r = 0; r < RQ; ++r)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) sc[r][c] = 0.f;
+            for (int c = 0; c < 4; ++c) sc[r][c] = 0ull;
 #pragma unroll 2
         for (int e = 0; e < dk4; e += 4) {
-            float4 q[RQ], k[4];
+            ulonglong2 q[RQ], k[4];
 #pragma unroll
-            for (int r = 0; r < RQ; ++r) q[r] = *reinterpret_cast<const float4*>(&Qs[(ty * RQ + r) * ks + e]);
+            for (int r = 0; r < RQ; ++r) q[r] = *reinterpret_cast<const ulonglong2*>(&Qs[(ty * RQ + r) * ks + e]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) k[c] = *reinterpret_cast<const float4*>(&Ks[(tx + 16 * c) * ks + e]);
+            for (int c = 0; c < 4; ++c) k[c] = *reinterpret_cast<const ulonglong2*>(&Ks[(tx + 16 * c) * ks + e]);
 #pragma unroll
             for (int r = 0; r < RQ; ++r)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    sc[r][c] = fmaf(q[r].x, k[c].x, sc[r][c]);
-                    sc[r][c] = fmaf(q[r].y, k[c].y, sc[r][c]);
-                    sc[r][c] = fmaf(q[r].z, k[c].z, sc[r][c]);
-                    sc[r][c] = fmaf(q[r].w, k[c].w, sc[r][c]);
+                    sc[r][c] = fma2(q[r].x, k[c].x, sc[r][c]);
+                    sc[r][c] = fma2(q[r].y, k[c].y, sc[r][c]);
                 }
         }
+    }
+
+    template <class F, class G>
+    __device__ void softmax(const uint64_t (&sc2)[RQ][4], int n, float scale_log2, F visible, G score) {
+        const int tx = (int)threadIdx.x & 15, ty = (int)threadIdx.x >> 4;
+        float sc[RQ][4];
 #pragma unroll
         for (int r = 0; r < RQ; ++r) {
             float tmax = -INFINITY;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int j = tx + 16 * c;
-                sc[r][c] = j < n && visible(ty * RQ + r, j) ? sc[r][c] * scale_log2 : -INFINITY;
+                float even, odd;
+                unpack2(sc2[r][c], even, odd);
+                sc[r][c] = j < n && visible(ty * RQ + r, j) ? (even + odd) * scale_log2 : -INFINITY;
                 if (j < n) score(ty * RQ + r, j, sc[r][c]);
                 tmax = fmaxf(tmax, sc[r][c]);
             }
@@ -144,6 +207,10 @@ struct SimtTile {
             for (int c = 0; c < 4; ++c) Ps[(ty * RQ + r) * SS_PS + tx + 16 * c] = sc[r][c];
         }
         __syncwarp();  // a row's P is written and read by the same half warp
+    }
+
+    __device__ void values(int n) {
+        const int tx = (int)threadIdx.x & 15, ty = (int)threadIdx.x >> 4;
         const int n4 = (n + 3) & ~3;  // rows past n are zero on both sides
         for (int j = 0; j < n4; j += 4) {
             float p[RQ][4];
@@ -172,7 +239,7 @@ struct SimtTile {
 // One block = BQ query rows of one (batch, head): the sinks below the rows' windows, then the keys
 // from the first row's window to the last row.
 template <int RQ, int CV>
-__global__ void __launch_bounds__(SS_THREADS)
+__global__ void __launch_bounds__(SS_THREADS, CV <= 2 ? 2 : 1)
     window_simt_kernel(const float* __restrict__ Q, int64_t ldq, const float* __restrict__ K, int64_t ldk,
                        const float* __restrict__ V, int64_t ldv, const float* __restrict__ G, int64_t ldg,
                        float* __restrict__ O, int64_t ldo, int h, int h_kv, int T, int dk, int dv,
@@ -203,21 +270,19 @@ __global__ void __launch_bounds__(SS_THREADS)
     int lo = max(0, q0 - window + 1);
     int s_end = min(sinks, L);  // sinks below the windows
     if (s_end >= lo) s_end = lo = 0;
-    for (int part = 0; part < 2; ++part) {
-        const int k_end = part == 0 ? s_end : end;
-        for (int k0 = part == 0 ? 0 : lo; k0 < k_end; k0 += SS_BK) {
-            const int n = min(SS_BK, k_end - k0);
-            __syncthreads();  // the previous tile is no longer read
-            x.load_kv(Kb + k0 * ldk, ldk, Vb + k0 * ldv, ldv, n, vec);
-            __syncthreads();
-            x.step(n, scale_log2,
-                   [&](int r, int j) {
-                       const int i = q0 + r, key = k0 + j;
-                       return key <= i && (i - key < window || key < sinks);
-                   },
-                   [](int, int, float) {});
-        }
-    }
+    const int nst = (s_end + SS_BK - 1) / SS_BK, nt = nst + (max(0, end - lo) + SS_BK - 1) / SS_BK;
+    if (nt > 0)
+        x.run(0, nt,
+              [&](int i, int& k0, int& n) {
+                  k0 = i < nst ? i * SS_BK : lo + (i - nst) * SS_BK;
+                  n = min(SS_BK, (i < nst ? s_end : end) - k0);
+              },
+              Kb, ldk, Vb, ldv, vec, scale_log2,
+              [&](int r, int key) {
+                  const int i = q0 + r;
+                  return key <= i && (i - key < window || key < sinks);
+              },
+              [](int, int, float) {});
 #pragma unroll
     for (int r = 0; r < RQ; ++r) {
         const int t = ty * RQ + r;
@@ -235,7 +300,7 @@ __global__ void __launch_bounds__(SS_THREADS)
 }
 
 template <int RQ, int CV>
-__global__ void __launch_bounds__(SS_THREADS)
+__global__ void __launch_bounds__(SS_THREADS, CV <= 2 ? 2 : 1)
     span_simt_kernel(const SpanShape p, const SpanRecords rec, const float* __restrict__ Q, int64_t ldq,
                      const float* __restrict__ K, int64_t ldk, const float* __restrict__ V, int64_t ldv,
                      const float* __restrict__ Kp, int64_t ldkp, const float* __restrict__ Vp, int64_t ldvp,
@@ -280,21 +345,11 @@ __global__ void __launch_bounds__(SS_THREADS)
         const float* Kb = q.prefix ? Kp + (int64_t)q.g * dk : K + (int64_t)q.b * p.T_max * ldk + (int64_t)q.g * dk;
         const float* Vb = q.prefix ? Vp + (int64_t)q.g * dv : V + (int64_t)q.b * p.T_max * ldv + (int64_t)q.g * dv;
         const int64_t lk = q.prefix ? ldkp : ldk, lv = q.prefix ? ldvp : ldv;
-        for (int i = q.i0; i < q.i1; ++i) {
-            int k0, n;
-            span_tile<SS_BK>(q.v, i, k0, n);
-            __syncthreads();
-            x.load_kv(Kb + k0 * lk, lk, Vb + k0 * lv, lv, n, vec);
-            __syncthreads();
-            x.step(n, scale_log2,
-                   [&](int r, int j) {
-                       return q.prefix || span_visible(p, q.v.L - p.T_q + (r0 + r) % p.T_q, k0 + j);
-                   },
-                   [&](int r, int j, float s) {
-                       if (scores != nullptr && r < nr)
-                           scores[(((int64_t)q.b * p.h_kv + q.g) * p.rows + r0 + r) * score_ld(p) + k0 + j] = s;
-                   });
-        }
+        x.run(q.i0, q.i1, [&](int i, int& k0, int& n) { span_tile<SS_BK>(q.v, i, k0, n); }, Kb, lk, Vb, lv, vec, scale_log2,
+              [&](int r, int key) { return q.prefix || span_visible(p, q.v.L - p.T_q + (r0 + r) % p.T_q, key); },
+              [&](int r, int key, float s) {
+                  if (scores != nullptr && r < nr) scores[(((int64_t)q.b * p.h_kv + q.g) * p.rows + r0 + r) * score_ld(p) + key] = s;
+              });
         const bool direct = p.T_p == 0 && q.whole();
         const int64_t slot = rec.row(p, q.unit, plan.np);
 #pragma unroll
