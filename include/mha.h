@@ -382,7 +382,9 @@ size_t mha_cache_step_workspace_size(mha_t handle, int B, int T_q, int T_prefix,
  * those keys: a step costs the same at every cache length.  window >= 1, sinks >= 0; other arguments
  * as for mha_decode.  O must not overlap an input.
  * Both dtypes need a workspace of mha_cache_step_workspace_size(B, T_q, 0, T_max, 0) bytes
- * (MHA_ERR_WORKSPACE otherwise).  Two launches.
+ * (MHA_ERR_WORKSPACE otherwise).  bf16: one cooperative launch of a CTA per SM, so it starts once other
+ * streams' kernels have left every SM; fp32: two launches.  A call whose status is MHA_ERR_TIMEOUT may leave
+ * the workspace's counters mid-way: attach it again (mha_set_workspace) before the next.
  */
 mha_status mha_decode_window(mha_t handle, int B, int T_q, int T_max, const void* Q, int64_t ldq,
                              const void* K_cache, int64_t ldk, const void* V_cache, int64_t ldv, int window,
@@ -397,7 +399,8 @@ mha_status mha_decode_window(mha_t handle, int B, int T_q, int T_max, const void
  *   K_cache, V_cache, cache_lengths  each sequence's own tokens after the prefix, as for mha_decode:
  *             L_b of them, the T_q new ones included
  * New token t sees the whole prefix and its own cache rows j <= L_b - T_q + t.  O must not overlap an
- * input.  Workspace: mha_cache_step_workspace_size(B, T_q, T_prefix, T_max, 0).  Two launches.
+ * input.  Workspace: mha_cache_step_workspace_size(B, T_q, T_prefix, T_max, 0).  Launches
+ * and status as for mha_decode_window (fp32: up to three).
  */
 mha_status mha_decode_shared(mha_t handle, int B, int T_q, int T_prefix, const void* K_prefix, int64_t ldkp,
                              const void* V_prefix, int64_t ldvp, int T_max, const void* Q, int64_t ldq,
@@ -412,7 +415,8 @@ mha_status mha_decode_shared(mha_t handle, int B, int T_q, int T_prefix, const v
  *            own entries (j >= L_b - T_q) have no history and are written, not added to; entries at or
  *            past L_b, and those of a batch with an invalid length, stay as they are.
  * O is mha_decode's.  The sums are made in a fixed order.  weights and O must not overlap an input or
- * each other.  Workspace: mha_cache_step_workspace_size(B, T_q, 0, T_max, 1).  Two launches.
+ * each other.  Workspace: mha_cache_step_workspace_size(B, T_q, 0, T_max, 1).  Launches
+ * and status as for mha_decode_window.
  */
 mha_status mha_decode_weights(mha_t handle, int B, int T_q, int T_max, const void* Q, int64_t ldq,
                               const void* K_cache, int64_t ldk, const void* V_cache, int64_t ldv,

@@ -17,8 +17,8 @@ namespace {
 // Query rows of a row block: a tensor-core tile for bf16; for fp32 what a block of the few-row kernel holds
 // if it holds them all, else the smallest of 16, 32 and 64 that does (a thread of span_simt.cu's kernel owns
 // 1, 2 or 4 of them).  Measured both ways, 16 caches of 4096 tokens, 4 K/V heads, few rows | tiles: d = 64, 1
-// row 41 | 151 us, 8 rows 74 | 154; d = 128, 4 rows 68 | 273; d = 256, 2 rows 243 | 798.  Two caches of 1000:
-// 10 | 13, 17 | 14, 14 | 18, 19 | 28.  With 10 rows of d = 64 in two blocks of 8 instead of one of 16, 3 caches
+// row 40 | 106 us, 8 rows 75 | 107; d = 128, 4 rows 67 | 172; d = 256, 2 rows 243 | 356.  Two caches of 1000:
+// 10 | 12, 17 | 12, 14 | 16, 21 | 22.  With 10 rows of d = 64 in two blocks of 8 instead of one of 16, 3 caches
 // of 300 visible tokens took 17 us instead of 12.
 int row_block(const mha_s* m, int64_t rows) {
     if (m->dtype == MHA_BF16) return 128;
@@ -42,7 +42,8 @@ SpanShape span_shape(const mha_s* m, int B, int T_q, int T_max, int T_p, int win
     p.nrb = (p.rows + p.bm_c - 1) / p.bm_c;
     p.nrbp = T_p > 0 ? (int)((rows_p + p.bm_p - 1) / p.bm_p) : 0;
     const bool few = p.bm_c < 16;
-    p.aim = few ? 1 : kSpanUnits;  // few rows: its units are long (1, 2 and 4 of them: 41, 46 and 50 us as above)
+    p.aim = few ? 1 : kSpanUnits;  // few rows: its units are long (1, 2 and 4 of them: 41, 46 and 50 us of the
+                                   // first case above)
     p.step = few ? 4 : 1;
     p.window = window < T_max ? window : T_max;
     p.sinks = sinks < T_max ? sinks : T_max;

@@ -11,7 +11,8 @@
 // same work took twice as long.
 //
 // Bound by HBM latency: a warp has 8 KB in flight and waits for K before V.  16 caches of 4096 tokens, 4 K/V
-// heads: d = 64 41 us (134 MB, 49 % of the measured copy rate), d = 128 67 us (60 %), d = 256 243 us (33 %).
+// heads, one row: d = 64 40 us (134 MB, 50 % of the measured copy rate; in tiles, span_simt.cu, 106), d = 128
+// 63 us (64 %; 170), d = 256 242 us (33 %; 356).
 #include <math.h>
 
 #include "internal.h"

@@ -13,6 +13,12 @@
 // window, come last and even out the CTAs (numbered the other way, 16 heads of 16384 rows took 219 us with
 // the tensor pipes of the SMs busy for 51 to 70 % of the time).
 //
+// Measured: 16 heads x 16384 rows, d = 128, window 2048: 205 us, 65 % of the measured bf16 rate (260 GF: only the
+// visible pairs count), bound by the chain score product, softmax, value product of each query tile with two
+// in flight.  4 x 16 heads x 2048 rows, d = 64, window 256: 35 us; most of its tiles are cut by a mask and a
+// CTA has three items.  P in columns of its own (d = 64 has room) took 45 us where this took 41, masks kept in
+// registers no less than in the scores.
+//
 // Tensor memory (512 columns): S_t at 128 t (P_t overwrites its first 64 columns), O_t at 256 + HD t, for
 // query tile t.  Warp roles (384 threads): warp 0 TMA of K and V; warp 1 TMEM owner and MMA issuer: for
 // each key tile J of the items in order and each query tile t that sees it, O_t += P_t V_J and then

@@ -331,8 +331,8 @@ class Mha:
 
     @staticmethod
     def _weights(name: str, t: torch.Tensor, shape) -> int:
-        if t.dtype != torch.float32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA float32 tensor of shape {tuple(shape)}")
+        if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA float32 tensor of shape {shape}")
         return t.data_ptr()
 
     def attention_window(self, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, window: int,
@@ -440,7 +440,7 @@ class Mha:
         if weights_out is None:
             weights_out = torch.empty((B, self.h_kv, T_out), dtype=torch.float32, device=dev)
         if lengths_out is None:
-            lengths_out = torch.empty_like(cache_lengths)
+            lengths_out = torch.empty(B, dtype=torch.int32, device=dev)
         kept = torch.empty((B, self.h_kv, keep), dtype=torch.int32, device=dev)
         ldko = self._rows("K_out", K_out, B, T_out, wk)
         ldvo = self._rows("V_out", V_out, B, T_out, wv)
