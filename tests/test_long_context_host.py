@@ -158,6 +158,24 @@ def test_python_refusals(lib):
             f()
 
 
+def test_sizes_past_32_bits_are_refused(lib):
+    """ctypes would cut them to 32 bits."""
+    torch = pytest.importorskip("torch")
+    from transformer_head_scaled_02_gb300 import Mha
+    layer = Mha(256, 4, 64, dtype=torch.bfloat16, h_kv=2, device="cpu")
+    q, k = torch.zeros((2, 1, 256), dtype=torch.bfloat16), torch.zeros((2, 10, 128), dtype=torch.bfloat16)
+    x, lens = torch.zeros((2, 10, 256), dtype=torch.bfloat16), torch.ones(2, dtype=torch.int32)
+    w = torch.zeros((2, 2, 10))
+    wq, wo = torch.zeros((256, 512), dtype=torch.bfloat16), torch.zeros((256, 256), dtype=torch.bfloat16)
+    big = 2 ** 32 + 5
+    for f in (lambda: layer.decode_window(q, k, k, lens, big), lambda: layer.decode_window(q, k, k, lens, 4, big),
+              lambda: layer.attention_window(x, k, k, big), lambda: layer.attention_window(x, k, k, 4, -big),
+              lambda: layer.forward(x, wq, None, wo, None, causal=True, window=big),
+              lambda: layer.evict(k, k, lens, w, 4, big), lambda: layer.evict(k, k, lens, w, big, 0)):
+        with pytest.raises(ValueError, match="out of range"):
+            f()
+
+
 # ------------------------------------------------------------------ the oracle's pins
 
 def test_oracle_agrees_with_the_c_oracle():

@@ -110,6 +110,9 @@ class Mha:
             raise ValueError("sinks need a window")
         if window is not None and (X_kv is not None or not causal):
             raise ValueError("a window needs causal self-attention")
+        if window is not None:
+            self._int32("window", window, 1)
+            self._int32("sinks", sinks, 0)
         ncols = self.proj_width
         self._check("X_q", X_q, (B, T_q, self.D))
         self._check("X_kv", X_kv, None if X_kv is None else (B, T_kv, self.D))
@@ -324,6 +327,13 @@ class Mha:
         return torch._C._cuda_getCurrentRawStream(dev)
 
     @staticmethod
+    def _int32(name: str, x: int, least: int) -> int:
+        """A size as a C int (ctypes would cut it to 32 bits)."""
+        if not least <= x <= 0x7FFFFFFF:
+            raise ValueError(f"{name} = {x} is out of range")
+        return x
+
+    @staticmethod
     def _ints(name: str, t: torch.Tensor, B: int) -> int:
         if t.dtype != torch.int32 or t.shape != (B,) or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous CUDA int32 tensor of length {B}")
@@ -343,6 +353,8 @@ class Mha:
         j < L_b and (i - j < window or j < sinks); rows that see nothing (padding only) are zero.
         Heads, gate and views as in attention().  Returns Ocat (B, T, h*d_v)."""
         B, T, _ = Q.shape
+        self._int32("window", window, 1)
+        self._int32("sinks", sinks, 0)
         ldq = self._rows("Q", Q, B, T, self.h * self.d_k)
         ldk = self._rows("K", K, B, T, self.h_kv * self.d_k)
         ldv = self._rows("V", V, B, T, self.h_kv * self.d_v)
@@ -382,6 +394,8 @@ class Mha:
                       out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """decode() under a sliding window: the new token at position p of its cache sees keys j <= p
         with p - j < window or j < sinks, and only those are read."""
+        self._int32("window", window, 1)
+        self._int32("sinks", sinks, 0)
         out, sizes, cache, lens, tail = self._cache_step(Q, K_cache, V_cache, cache_lengths, out, 0, 0)
         _lib.mha_decode_window(self.handle, *sizes, *cache, window, sinks, lens, *tail)
         return out
@@ -429,8 +443,8 @@ class Mha:
         ldv = self._rows("V_cache", V_cache, B, T_max, wv)
         w = self._weights("weights", weights, (B, self.h_kv, T_max))
         lens = self._ints("cache_lengths", cache_lengths, B)
-        if keep < 1:
-            raise ValueError("keep must be at least 1")
+        self._int32("keep", keep, 1)
+        self._int32("recent", recent, 0)
         dev = K_cache.device
         T_out = keep if K_out is None else K_out.shape[1]
         if K_out is None:
