@@ -660,3 +660,94 @@ def test_on_another_stream(dtype, d):
     torch.cuda.synchronize()
     for o in outs[0] + outs[1]:
         _check(to_host(o), ref, A, dtype, "streams")
+
+
+# Few query rows per K/V head in fp32 (they take a kernel of their own): every number of rows and width
+# that it holds, and one more row.
+FEW_SHAPES = [
+    # d, d_v, h, h_kv, T_q
+    (64, 64, 4, 4, 1), (64, 60, 8, 4, 2), (61, 64, 4, 4, 1), (32, 64, 8, 1, 1), (64, 64, 9, 1, 1),
+    (128, 128, 4, 4, 1), (128, 96, 4, 2, 2), (66, 65, 4, 4, 2), (100, 100, 5, 1, 1),
+    (256, 256, 2, 2, 1), (200, 256, 4, 2, 1), (130, 255, 2, 2, 2), (256, 192, 3, 1, 1)]
+
+
+@pytest.mark.parametrize("d,dv,h,h_kv,Tq", FEW_SHAPES)
+def test_few_rows_f32(d, dv, h, h_kv, Tq):
+    B, Tmax, Tp = 3, 700, 150
+    lengths = [700, Tq, 261]
+    Q, K, V = _cache(400 + d + dv, "f32", B, Tq, Tmax, h, h_kv, d, dv)
+    Kp, Vp = _rand((Tp, h_kv * d), 401, "f32"), _rand((Tp, h_kv * dv), 402, "f32")
+    Kn, Vn = _garbage(K, V, lengths)
+    t = [to_device(x, "f32") for x in (Q, Kn, Vn)]
+    layer = _layer("f32", h, d, h_kv, dv)
+    for window, sinks in ((200, 5), (64, 0), (1, 0)):
+        ref, A, _ = lc.decode(Q, K, V, h, lengths, h_kv, window, sinks)
+        _check(to_host(layer.decode_window(*t, _lens(lengths), window, sinks)), ref, A, "f32", "few rows, window")
+    # the prefix's rows are the batch's: another kernel than the caches' where those are many
+    ref, A, _ = lc.decode(Q, K, V, h, lengths, h_kv, K_prefix=Kp, V_prefix=Vp)
+    _check(to_host(layer.decode_shared(t[0], to_device(Kp, "f32"), to_device(Vp, "f32"), *t[1:], _lens(lengths))),
+           ref, A, "f32", "few rows, shared")
+    w0 = np.abs(_rand((B, h_kv, Tmax), 403, "f32"))
+    w = to_device(w0, "f32")
+    ref, A, W = lc.decode(Q, K, V, h, lengths, h_kv, weights=w0)
+    _check(to_host(layer.decode_weights(*t, _lens(lengths), w)), ref, A, "f32", "few rows, weights")
+    for b, L in enumerate(lengths):
+        _check_weights(to_host(w)[b, :, :L], W[b, :, :L], "few rows, weights")
+    assert layer.status() == 0
+
+
+@pytest.mark.parametrize("Tq", [1, 9])
+def test_offsets_past_32_bits_f32(Tq):
+    h = h_kv = 16
+    d, B, Tmax = 64, 5, 850_000
+    K = torch.empty((B, Tmax, h_kv * d), device="cuda")
+    V = torch.empty_like(K)
+    assert K.numel() > 2 ** 32
+    n = 300
+    lengths = [n, n, n, n, Tmax]
+    Q = _rand((B, Tq, h * d), 110, "f32")
+    kb, vb = _rand((n, h_kv * d), 111, "f32"), _rand((n, h_kv * d), 112, "f32")
+    for b in range(4):
+        K[b, :n], V[b, :n] = to_device(kb, "f32"), to_device(vb, "f32")
+    K[4, Tmax - n:], V[4, Tmax - n:] = to_device(kb, "f32"), to_device(vb, "f32")
+    layer = _layer("f32", h, d, h_kv)
+    W = n - Tq + 1  # the first new token's window begins with the filled rows
+    got = to_host(layer.decode_window(to_device(Q, "f32"), K, V, _lens(lengths), W, 0))
+    ref, A, _ = lc.decode(Q, np.broadcast_to(kb, (B, n, h * d)), np.broadcast_to(vb, (B, n, h * d)), h, [n] * B, h_kv, W, 0)
+    _check(got, ref, A, "f32", "past 32 bits")
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("f32", 64)])
+def test_two_graphs_share_a_workspace(dtype, d):
+    """Graphs of different sizes captured from one layer, replayed in turn with eager calls between them."""
+    h, h_kv = 8, 2
+    layer = _layer(dtype, h, d, h_kv)
+    cases = []
+    for i, (B, Tmax, lengths) in enumerate(((1, 1500, [1500]), (7, 400, [400, 3, 77, 128, 399, 1, 200]))):
+        Q, K, V = _cache(500 + 10 * i, dtype, B, 1, Tmax, h, h_kv, d, d)
+        t = [to_device(x, dtype) for x in (Q, K, V)]
+        w0 = np.zeros((B, h_kv, Tmax), dtype=np.float32)
+        ref, A, W = lc.decode(Q, K, V, h, lengths, h_kv, weights=w0)
+        out = torch.zeros((B, 1, h * d), dtype=torch_dtype(dtype), device="cuda")
+        cases.append((t, _lens(lengths), lengths, to_device(w0, "f32"), out, ref, A, W))
+    for t, lens, _, w, out, *_ in cases[::-1]:
+        layer.decode_weights(*t, lens, w, out=out)
+    torch.cuda.synchronize()
+    graphs = []
+    for t, lens, _, w, out, *_ in cases:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            layer.decode_weights(*t, lens, w, out=out)
+        graphs.append(g)
+    for turn in range(3):
+        for i in (0, 1, 1, 0):
+            t, lens, lengths, w, out, ref, A, W = cases[i]
+            w.zero_()
+            out.zero_()
+            graphs[i].replay()
+            _check(to_host(out), ref, A, dtype, "graph")
+            for b, L in enumerate(lengths):
+                _check_weights(to_host(w)[b, :, :L], W[b, :, :L], "graph")
+            t, lens, _, w, out, ref, A, _ = cases[1 - i]
+            _check(to_host(layer.decode_weights(*t, lens, w)), ref, A, dtype, "eager between graphs")
+    assert layer.status() == 0

@@ -59,7 +59,7 @@ struct SpCfg {
     static constexpr int CHUNK = 128 * 128;        // 128 rows x 64 bf16
     static constexpr int TILE = CH * CHUNK;
     static constexpr int STAGES = HD == 128 ? 3 : 6;
-    static constexpr int SMEM = TILE + 2 * STAGES * TILE + 3072;  // + row sums, barriers, units
+    static constexpr int SMEM = TILE + 2 * STAGES * TILE + 3 * 1024;  // + row sums, barriers, units
     static constexpr uint32_t O_COL = 256;
 };
 static_assert(SpCfg<128>::SMEM <= 232448 && SpCfg<64>::SMEM <= 232448, "span smem budget");
