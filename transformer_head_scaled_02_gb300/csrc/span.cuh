@@ -142,6 +142,7 @@ __device__ inline SpanPlan span_plan(const SpanShape& p, const int32_t* lengths,
     s.i1 = min(p.B, s.i0 + run);
     s.L0 = s.i0 < s.i1 ? __ldcg(lengths + s.i0) : 0;
     int tiles = 0;
+#pragma unroll 1
     for (int i = s.i0; i < s.i1; ++i) tiles += span_view<TILE>(p, s.length(lengths, i)).nt;
     const int np = span_prefix_tiles<TILE>(p);
     const unsigned total = __reduce_add_sync(0xffffffffu, (unsigned)tiles) * (unsigned)p.lanes_c() + (unsigned)(np * p.lanes_p());
@@ -153,6 +154,7 @@ __device__ inline SpanPlan span_plan(const SpanShape& p, const int32_t* lengths,
     q.Up = max(max(q.U, p.least_p()), (np * p.lanes_p() + ctas - 1) / ctas);
     q.np = p.T_p > 0 ? (np + q.Up - 1) / q.Up * p.lanes_p() : 0;
     s.sum = 0;
+#pragma unroll 1
     for (int i = s.i0; i < s.i1; ++i) s.sum += span_units<TILE>(p, q, s.length(lengths, i));
     int inc = s.sum;
 #pragma unroll
@@ -173,6 +175,7 @@ __device__ __forceinline__ int span_first_unit(const SpanShape& p, const int32_t
     const bool mine = s.i0 <= b && b < s.i1;
     if (mine) {
         at = s.before;
+#pragma unroll 1
         for (int i = s.i0; i < b; ++i) at += span_units<TILE>(p, q, s.length(lengths, i));
         len = s.length(lengths, b);
     }
@@ -212,6 +215,7 @@ __device__ inline SpanUnit span_unit(const SpanShape& p, const int32_t* lengths,
         const bool mine = s.before <= u && u < s.before + s.sum;
         if (mine) {
             at = s.before;
+#pragma unroll 1
             for (b = s.i0;; ++b) {
                 len = s.length(lengths, b);
                 const int n = span_units<TILE>(p, q, len);

@@ -224,35 +224,36 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
             // ---------------- TMA: K and V tiles.  nk, nv: issued
             int nk = 0, nv = 0;
             bool ok = true;
+#pragma unroll 1
             for (int i = 0; ok && unit_ready(i); ++i) {
-                const SpanUnit q = tail->units[i % SP_RING];
+                const SpanUnit& q = tail->units[i % SP_RING];
                 if (q.unit < 0) break;
-                const CUtensorMap* mk = q.prefix ? &maps.kp : &maps.k;
-                const CUtensorMap* mv = q.prefix ? &maps.vp : &maps.v;
-                for (int j = q.i0; j < q.i1; ++j) {
+                const CUtensorMap* maps_k = q.prefix ? &maps.kp : &maps.k;  // the values' follow: k, k16, v, v16
+                const int i1 = q.i1;
+#pragma unroll 1
+                for (int j2 = 2 * q.i0; j2 < 2 * i1; ++j2) {  // a tile's keys, then its values
                     int key0, n;
-                    span_tile<SP_TK>(q.v, j, key0, n);
-                    const int boxes = n > SP_TK - SP_BOX ? 0 : (n + SP_BOX - 1) / SP_BOX;
-                    const uint32_t bytes = boxes ? (uint32_t)boxes * SP_BOX * 128 * C::CH : (uint32_t)C::TILE;
-                    const int st = nk % S;
-                    const uint32_t ph = ((uint32_t)(nk / S) & 1u) ^ 1u;
-                    auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t full) {
-                        mbar_arrive_expect_tx(full, bytes);
+                    span_tile<SP_TK>(q.v, j2 >> 1, key0, n);
+                    const bool val = j2 & 1;
+                    const int st = nv % S;
+                    const uint32_t full = bar(val ? tail->vfull[st] : tail->kfull[st]);
+                    ok = mbar_wait(bar(val ? tail->vempty[st] : tail->kempty[st]), ((uint32_t)(nv / S) & 1u) ^ 1u, abort_flag, status);
+                    if (!ok) break;
+                    const CUtensorMap* m = maps_k + (val ? 2 : 0);
+                    const uint32_t dst = (val ? sV : sK) + st * C::TILE;
+                    // the map with boxes of 16 rows follows the whole one
+                    const int rows = n > SP_TK - SP_BOX ? SP_TK : SP_BOX, loads = rows == SP_TK ? 1 : (n + SP_BOX - 1) / SP_BOX;
+                    mbar_arrive_expect_tx(full, (uint32_t)(loads * rows) * 128 * C::CH);
+#pragma unroll 1
+                    for (int x = 0; x < loads; ++x)
 #pragma unroll
-                        for (int c = 0; c < C::CH; ++c) {
-                            if (boxes == 0) tma_load_3d(dst + c * C::CHUNK, m, q.g * HD + c * 64, key0, q.b, full);
-                            for (int x = 0; x < boxes; ++x)  // the map with boxes of 16 rows follows the whole one
-                                tma_load_3d(dst + c * C::CHUNK + x * SP_BOX * 128, m + 1, q.g * HD + c * 64, key0 + x * SP_BOX, q.b, full);
-                        }
-                    };
-                    ok = mbar_wait(bar(tail->kempty[st]), ph, abort_flag, status);
-                    if (!ok) break;
-                    load(sK + st * C::TILE, mk, bar(tail->kfull[st]));
-                    ++nk;
-                    ok = mbar_wait(bar(tail->vempty[st]), ph, abort_flag, status);
-                    if (!ok) break;
-                    load(sV + st * C::TILE, mv, bar(tail->vfull[st]));
-                    ++nv;
+                        for (int c = 0; c < C::CH; ++c)
+                            tma_load_3d(dst + c * C::CHUNK + x * SP_BOX * 128, rows == SP_TK ? m : m + 1, q.g * HD + c * 64, key0 + x * SP_BOX,
+                                        q.b, full);
+                    if (val)
+                        ++nv;
+                    else
+                        ++nk;
                 }
                 unit_done(i);
             }
@@ -307,16 +308,29 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
             }
             return true;
         };
-        bool ok = issue_s() && issue_s();
+        bool ok = true;
         int jp = 0;
-        for (int i = 0; ok; ++i) {
-            ok = __all_sync(0xffffffffu, unit_ready(i));
-            if (!ok || tail->units[i % SP_RING].unit < 0) break;
-            const int i0 = tail->units[i % SP_RING].i0, nt = tail->units[i % SP_RING].i1 - i0;
-            const SpanView v = tail->units[i % SP_RING].v;
+#pragma unroll 1
+        for (int i = -1; ok; ++i) {
+            // (unit -1: the first two score products, by the one copy of their code)
+            int i0 = 0, nt = 2;
+            SpanView v = {};
+            if (i >= 0) {
+                ok = __all_sync(0xffffffffu, unit_ready(i));
+                const SpanUnit& x = tail->units[i % SP_RING];
+                if (!ok || x.unit < 0) break;
+                i0 = x.i0;
+                nt = x.i1 - i0;
+                v = x.v;
+            }
             // the unit before has been read out of O
             if (i > 0) ok = warp_wait(bar(tail->ofree), (uint32_t)(i - 1) & 1u, abort_flag, status);
+#pragma unroll 1
             for (int k = 0; k < nt && ok; ++k) {
+                if (i < 0) {
+                    ok = issue_s();
+                    continue;
+                }
                 const int st = jp % S, t = jp & 1;
                 ok = warp_wait(bar(tail->vfull[st]), (uint32_t)(jp / S) & 1u, abort_flag, status) &&
                      warp_wait(bar(tail->pfull[t]), (uint32_t)(jp >> 1) & 1u, abort_flag, status);
@@ -336,7 +350,7 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
                 ok = issue_s();
             }
             __syncwarp();
-            if (ok && lane == 0) unit_done(i);
+            if (ok && lane == 0 && i >= 0) unit_done(i);
         }
         tc_commit_elect(el, bar(tail->drain));
         drain_wait_a(bar(tail->drain), 0);
@@ -565,8 +579,7 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
                     const float inv = 1.f / sum;
                     __nv_bfloat16* out = O + ((int64_t)rb_ * p.T_q + tok) * ldo + (int64_t)head * HD;
                     float* part = rec.o + row * HD;
-                    const bool wide = ((reinterpret_cast<uintptr_t>(O) | (uintptr_t)(ldo * 2)) & 31u) == 0;
-#pragma unroll
+#pragma unroll 1
                     for (int c2 = 0; c2 < HD / 64; ++c2) {
                         const int cc = t * (HD / 64) + c2;
                         float f[32];
@@ -588,17 +601,10 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
                         }
                         if (real && direct) {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 16) {
-                                uint32_t y[8];
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) y[i] = pack_bf16x2(f[e + 2 * i] * inv, f[e + 2 * i + 1] * inv);
-                                if (wide)
-                                    st_global_v8(out + cc * 32 + e, y);
-                                else {
-                                    *reinterpret_cast<uint4*>(out + cc * 32 + e) = make_uint4(y[0], y[1], y[2], y[3]);
-                                    *reinterpret_cast<uint4*>(out + cc * 32 + e + 8) = make_uint4(y[4], y[5], y[6], y[7]);
-                                }
-                            }
+                            for (int e = 0; e < 32; e += 8)
+                                *reinterpret_cast<uint4*>(out + cc * 32 + e) =
+                                    make_uint4(pack_bf16x2(f[e] * inv, f[e + 1] * inv), pack_bf16x2(f[e + 2] * inv, f[e + 3] * inv),
+                                               pack_bf16x2(f[e + 4] * inv, f[e + 5] * inv), pack_bf16x2(f[e + 6] * inv, f[e + 7] * inv));
                         } else if (real) {
 #pragma unroll
                             for (int e = 0; e < 32; e += 8) {
