@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
     volatile int* abort_flag = &tail->abort_flag;
     auto bar = [](uint64_t& b) { return smem_u32(&b); };
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&maps.k);
         tma_prefetch_desc(&maps.v);
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
     }
     grid_launch_dependents();
     // The i-th unit of this CTA, once it is there; its slot is released after the last look at it.
-    auto unit_ready = [&](int i) { return mbar_wait(bar(tail->ufull[i % SP_RING]), (uint32_t)(i / SP_RING) & 1u, abort_flag, status); };
+    auto unit_ready = [&](int i) { return lean_wait(bar(tail->ufull[i % SP_RING]), (uint32_t)(i / SP_RING) & 1u, abort_flag, status); };
     auto unit_done = [&](int i) { mbar_arrive(bar(tail->uempty[i % SP_RING])); };
     // where query row r of a unit lies
     auto where = [&](const SpanUnit& x, int r, int& b, int& head, int& t) {
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
                     const bool val = j2 & 1;
                     const int st = nv % S;
                     const uint32_t full = bar(val ? tail->vfull[st] : tail->kfull[st]);
-                    ok = mbar_wait(bar(val ? tail->vempty[st] : tail->kempty[st]), ((uint32_t)(nv / S) & 1u) ^ 1u, abort_flag, status);
+                    ok = lean_wait(bar(val ? tail->vempty[st] : tail->kempty[st]), ((uint32_t)(nv / S) & 1u) ^ 1u, abort_flag, status);
                     if (!ok) break;
                     const CUtensorMap* m = maps_k + (val ? 2 : 0);
                     const uint32_t dst = (val ? sV : sK) + st * C::TILE;
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
         }
       } else if (warp == 1) {
         // ---------------- MMA issuer.  js, jp: score and value products issued so far
-        const uint32_t el = elect_lane();
+        const uint32_t el = elect_lane(), tm = uniform(tmem);
         const uint64_t qdesc0 = sdesc_sw128(sQ, 16, 1024);
         const uint64_t kdesc0 = sdesc_sw128(sK, 16, 1024);
         const uint64_t vdesc0 = sdesc_sw128(sV, C::CHUNK, 1024);
@@ -278,14 +278,15 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
                 if (!more_s) return true;
                 if (!__all_sync(0xffffffffu, unit_ready(us + 1))) return false;
                 const SpanUnit& x = tail->units[(us + 1) % SP_RING];
-                if (x.unit < 0) {
+                if (uniform(x.unit) < 0) {
                     more_s = false;
                     return true;
                 }
                 ++us;
-                left_s = x.i1 - x.i0;
-                nr_s = tail->nr[us % SP_RING];
+                left_s = uniform(x.i1 - x.i0);
+                nr_s = uniform(tail->nr[us % SP_RING]);
                 buf_s = qb.first(nr_s);
+#pragma unroll 1
                 for (int i = buf_s; i <= qb.last(nr_s); ++i)
                     if (!warp_wait(bar(tail->qfull[i]), (uint32_t)qb.uses[i] & 1u, abort_flag, status)) return false;
             }
@@ -297,12 +298,13 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
 #pragma unroll
             for (int kk = 0; kk < HD / 16; ++kk) {
                 const uint32_t off16 = (uint32_t)(((kk >> 2) * C::CHUNK + (kk & 3) * 32) >> 4);
-                mma_bf16_ss_elect(el, tmem + 128u * (js & 1), qdesc + off16, kdesc + off16, idesc_s, kk > 0 ? 1u : 0u);
+                mma_bf16_ss_elect(el, tm + 128u * (js & 1), qdesc + off16, kdesc + off16, idesc_s, kk > 0 ? 1u : 0u);
             }
             tc_commit_elect(el, bar(tail->sfull[js & 1]));
             tc_commit_elect(el, bar(tail->kempty[st]));
             ++js;
             if (--left_s == 0) {
+#pragma unroll 1
                 for (int i = buf_s; i <= qb.last(nr_s); ++i) tc_commit_elect(el, bar(tail->qfree[i]));
                 qb.take(nr_s);
             }
@@ -318,9 +320,9 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
             if (i >= 0) {
                 ok = __all_sync(0xffffffffu, unit_ready(i));
                 const SpanUnit& x = tail->units[i % SP_RING];
-                if (!ok || x.unit < 0) break;
+                if (!ok || uniform(x.unit) < 0) break;
                 i0 = x.i0;
-                nt = x.i1 - i0;
+                nt = uniform(x.i1 - i0);
                 v = x.v;
             }
             // the unit before has been read out of O
@@ -337,13 +339,20 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t vdesc = vdesc0 + (uint64_t)((st * C::TILE) >> 4);
-                int key0, n;  // values past the tile's end were not loaded: no steps over them
+                int key0, n;
                 span_tile<SP_TK>(v, i0 + k, key0, n);
+                n = uniform(n);
+                if (n > SP_TK - SP_BOX) {
 #pragma unroll
-                for (int kk = 0; kk < SP_TK / 16; ++kk)
-                    if (16 * kk < n)
-                        mma_bf16_ts_elect(el, tmem + C::O_COL + HD * t, tmem + 128u * t + kk * 8, vdesc + (uint64_t)((kk * 2048) >> 4),
-                                          idesc_o, (k >= 2 || kk > 0) ? 1u : 0u);
+                    for (int kk = 0; kk < SP_TK / 16; ++kk)
+                        mma_bf16_ts_elect(el, tm + C::O_COL + HD * t, tm + 128u * t + kk * 8, vdesc + (uint64_t)((kk * 2048) >> 4), idesc_o,
+                                          (k >= 2 || kk > 0) ? 1u : 0u);
+                } else {  // values past the tile's end were not loaded: no steps over them
+#pragma unroll 1
+                    for (int kk = 0; 16 * kk < n; ++kk)
+                        mma_bf16_ts_elect(el, tm + C::O_COL + HD * t, tm + 128u * t + kk * 8, vdesc + (uint64_t)((kk * 2048) >> 4), idesc_o,
+                                          (k >= 2 || kk > 0) ? 1u : 0u);
+                }
                 tc_commit_elect(el, bar(tail->vempty[st]));
                 if (k + 1 == nt) tc_commit_elect(el, bar(tail->odone));
                 ++jp;
@@ -366,6 +375,7 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
             if (lane == 0) unit_done(i);
             const int buf = qb.first(nr), end = qb.last(nr);
             bool ok = true;
+#pragma unroll 1
             for (int x = buf; x <= end && ok; ++x)
                 if (qb.uses[x] > 0) ok = warp_wait(bar(tail->qfree[x]), (uint32_t)(qb.uses[x] - 1) & 1u, abort_flag, status);
             if (!ok) break;
@@ -395,6 +405,7 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
                 }
             }
             fence_proxy_async_smem();
+#pragma unroll 1
             for (int x = buf; x <= end; ++x) mbar_arrive(bar(tail->qfull[x]));
             qb.take(nr);
         }
@@ -453,7 +464,7 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
             const int pos = q.v.L - p.T_q + tok;
             float m = -INFINITY, l = 0.f;
             for (int k = (j ^ t) & 1; k < nt; k += 2) {
-                if (!__all_sync(0xffffffffu, mbar_wait(bar(tail->sfull[t]), (uint32_t)((j + k) >> 1) & 1u, abort_flag, status))) {
+                if (!__all_sync(0xffffffffu, lean_wait(bar(tail->sfull[t]), (uint32_t)((j + k) >> 1) & 1u, abort_flag, status))) {
                     ok = false;
                     break;
                 }
@@ -464,11 +475,12 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
                     // rows past the end may hold anything: zero the V rows the product would multiply by
                     // P = 0 (a NaN there would survive it)
                     const int st = (j + k) % S;
-                    if (!__all_sync(0xffffffffu, mbar_wait(bar(tail->vfull[st]), (uint32_t)((j + k) / S) & 1u, abort_flag, status))) {
+                    if (!__all_sync(0xffffffffu, lean_wait(bar(tail->vfull[st]), (uint32_t)((j + k) / S) & 1u, abort_flag, status))) {
                         ok = false;
                         break;
                     }
                     const int rows = (n + SP_BOX - 1) / SP_BOX * SP_BOX - n;
+#pragma unroll 1
                     for (int z = quarter * 32 + lane; z < rows * C::CH * 8; z += 128) {
                         const int row = n + z / (C::CH * 8), cu = z % (C::CH * 8);
                         st_shared_v4(sV + st * C::TILE + (uint32_t)((cu >> 3) * C::CHUNK + row * 128 + ((cu & 7) << 4)), 0u, 0u, 0u, 0u);
@@ -552,15 +564,15 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
             // each stream's warps join half of the columns
             {
                 // (the sums of the unit before have been read)
-                if (iu > 0 && !__all_sync(0xffffffffu, mbar_wait(bar(tail->ofree), (uint32_t)(iu - 1) & 1u, abort_flag, status))) {
+                if (iu > 0 && !__all_sync(0xffffffffu, lean_wait(bar(tail->ofree), (uint32_t)(iu - 1) & 1u, abort_flag, status))) {
                     ok = false;
                     break;
                 }
                 tail->ml[t][r] = make_float2(m, l);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(tail->mlfull));
-                if (!__all_sync(0xffffffffu, mbar_wait(bar(tail->odone), (uint32_t)iu & 1u, abort_flag, status) &&
-                                                 mbar_wait(bar(tail->mlfull), (uint32_t)iu & 1u, abort_flag, status))) {
+                if (!__all_sync(0xffffffffu, lean_wait(bar(tail->odone), (uint32_t)iu & 1u, abort_flag, status) &&
+                                                 lean_wait(bar(tail->mlfull), (uint32_t)iu & 1u, abort_flag, status))) {
                     ok = false;
                     break;
                 }

@@ -21,9 +21,35 @@ __device__ __forceinline__ uint32_t elect_lane() {
     return e;
 }
 
-// mbar_wait with an outcome that is the same in all lanes.
+// The same value in all lanes, as the compiler knows it: operands of MMAs computed from such values need no
+// search for a common one.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// mbar_wait in less code (32 bits of the clock; giving up after another's abort records the status once more,
+// which keeps the first): a kernel with thirty waits holds it thirty times between the instructions that run
+// all the time, and the instruction cache is what its roles share.
+__device__ __forceinline__ uint32_t globaltimer_lo() {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+}
+
+__device__ __forceinline__ bool lean_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint32_t t0 = globaltimer_lo();
+    while (!mbar_try_wait_sleep(bar, parity, 100000u))
+        if (*abort_flag || globaltimer_lo() - t0 > (uint32_t)kWaitLimitNs) {
+            *abort_flag = 1;
+            record_status(status, kStatusTimeout);
+            return false;
+        }
+    return true;
+}
+
+// A wait with an outcome that is the same in all lanes.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
+    return __all_sync(0xffffffffu, lean_wait(bar, parity, abort_flag, status));
 }
 
 __device__ __forceinline__ void mma_bf16_ss_elect(uint32_t elected, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,

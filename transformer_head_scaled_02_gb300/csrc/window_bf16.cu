@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(WN_THREADS, 1)
     WnTail* tail = reinterpret_cast<WnTail*>(smem_raw + (base - raw) + C::TILE * (2 + SK + SV));
     volatile int* abort_flag = &tail->abort_flag;
     auto bar = [](uint64_t& b) { return smem_u32(&b); };
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < SK; ++s) {
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(WN_THREADS, 1)
     grid_dependency_wait();  // Q, K, V and the lengths may come from the previous kernel
     grid_launch_dependents();
     // The i-th item, once it is there; afterwards its slot is released.
-    auto item_ready = [&](int i) { return mbar_wait(bar(tail->ifull[i % WN_RING]), (uint32_t)(i / WN_RING) & 1u, abort_flag, status); };
+    auto item_ready = [&](int i) { return lean_wait(bar(tail->ifull[i % WN_RING]), (uint32_t)(i / WN_RING) & 1u, abort_flag, status); };
     auto item_done = [&](int i) { mbar_arrive(bar(tail->iempty[i % WN_RING])); };
 
     if (warp < 4) {
@@ -224,14 +224,14 @@ __global__ void __launch_bounds__(WN_THREADS, 1)
                 for (int j = 0; j < it.tiles; ++j) {
                     const int key0 = j < it.nst ? 128 * j : it.kA + 128 * (j - it.nst);
                     const int sk = nk % SK, sv = nv % SV;
-                    ok = mbar_wait(bar(tail->kempty[sk]), ((uint32_t)(nk / SK) & 1u) ^ 1u, abort_flag, status);
+                    ok = lean_wait(bar(tail->kempty[sk]), ((uint32_t)(nk / SK) & 1u) ^ 1u, abort_flag, status);
                     if (!ok) break;
                     mbar_arrive_expect_tx(bar(tail->kfull[sk]), C::TILE);
 #pragma unroll
                     for (int c = 0; c < C::CH; ++c)
                         tma_load_3d(sK + sk * C::TILE + c * C::CHUNK, &maps.k, col + c * 64, key0, it.b, bar(tail->kfull[sk]));
                     ++nk;
-                    ok = mbar_wait(bar(tail->vempty[sv]), ((uint32_t)(nv / SV) & 1u) ^ 1u, abort_flag, status);
+                    ok = lean_wait(bar(tail->vempty[sv]), ((uint32_t)(nv / SV) & 1u) ^ 1u, abort_flag, status);
                     if (!ok) break;
                     mbar_arrive_expect_tx(bar(tail->vfull[sv]), C::TILE);
 #pragma unroll
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(WN_THREADS, 1)
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     if (!ok || it.end[t] == 0) continue;
-                    if (nq[t] > 0) ok = mbar_wait(bar(tail->qempty[t]), (uint32_t)(nq[t] - 1) & 1u, abort_flag, status);
+                    if (nq[t] > 0) ok = lean_wait(bar(tail->qempty[t]), (uint32_t)(nq[t] - 1) & 1u, abort_flag, status);
                     if (!ok) continue;
                     mbar_arrive_expect_tx(bar(tail->qfull[t]), C::TILE);
 #pragma unroll
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(WN_THREADS, 1)
             int64_t k = blockIdx.x;
             for (int i = 0;; ++i, k += gridDim.x) {
                 if (i >= WN_RING &&
-                    !mbar_wait(bar(tail->iempty[i % WN_RING]), (uint32_t)(i / WN_RING - 1) & 1u, abort_flag, status))
+                    !lean_wait(bar(tail->iempty[i % WN_RING]), (uint32_t)(i / WN_RING - 1) & 1u, abort_flag, status))
                     break;
                 if (k < a.items) {
                     const WnItem x = wn_item(a, k);
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(WN_THREADS, 1)
             bool first = true;
             for (int j = 0; j < it.tiles && ok; ++j) {
                 if (!wn_visits(j, it.nst, first_t, end_t)) continue;
-                if (!__all_sync(0xffffffffu, mbar_wait(bar(tail->sfull[t]), (uint32_t)nj & 1u, abort_flag, status))) {
+                if (!__all_sync(0xffffffffu, lean_wait(bar(tail->sfull[t]), (uint32_t)nj & 1u, abort_flag, status))) {
                     ok = false;
                     break;
                 }
@@ -528,11 +528,12 @@ __global__ void __launch_bounds__(WN_THREADS, 1)
                     // P = 0 (a NaN there would survive it).  Both query tiles' warps do, each before its own
                     // product.
                     const int st = (J + j) % SV;
-                    if (!__all_sync(0xffffffffu, mbar_wait(bar(tail->vfull[st]), (uint32_t)((J + j) / SV) & 1u, abort_flag, status))) {
+                    if (!__all_sync(0xffffffffu, lean_wait(bar(tail->vfull[st]), (uint32_t)((J + j) / SV) & 1u, abort_flag, status))) {
                         ok = false;
                         break;
                     }
                     const int from = it.L - key0;
+#pragma unroll 1
                     for (int z = r; z < (128 - from) * C::CH * 8; z += 128) {
                         const int vr = from + z / (C::CH * 8), cu = z % (C::CH * 8);
                         st_shared_v4(sV + st * C::TILE + (uint32_t)((cu >> 3) * C::CHUNK + vr * 128 + ((cu & 7) << 4)), 0u, 0u, 0u, 0u);
@@ -547,7 +548,7 @@ __global__ void __launch_bounds__(WN_THREADS, 1)
             }
             J += it.tiles;
             if (!ok) break;
-            if (!__all_sync(0xffffffffu, mbar_wait(bar(tail->odone[t]), (uint32_t)no & 1u, abort_flag, status))) {
+            if (!__all_sync(0xffffffffu, lean_wait(bar(tail->odone[t]), (uint32_t)no & 1u, abort_flag, status))) {
                 ok = false;
                 break;
             }
