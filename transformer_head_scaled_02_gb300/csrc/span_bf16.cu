@@ -648,26 +648,29 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
         // warps otherwise
         const bool few = out_rows <= (int)gridDim.x;
         int row = few ? (int)blockIdx.x : (int)blockIdx.x * JOIN_WARPS + jw;
-        __nv_bfloat16* out = nullptr;
-        RowRecords src;
-        auto find_row = [&]() {
-            if (row >= out_rows) return;
-            const int bh = p.T_q == 1 ? row : row / p.T_q, t = row - bh * p.T_q, b = bh / heads, head = bh - b * heads;
-            int L;
-            const int unit0 = span_first_unit<SP_TK>(p, lengths, plan, sums, b, L);
-            const SpanView v = span_view<SP_TK>(p, L);
-            const int g = head / p.per;
-            out = O + ((int64_t)b * p.T_q + t) * ldo + (int64_t)head * HD + lane * E;
-            src = row_records<SP_TK>(p, rec, plan, unit0, v.nt, b, g, (head - g * p.per) * p.T_q + t);
-            if (v.nt == 0) src.n[0] = src.n[1] = 0;  // invalid length
-        };
-        find_row();
-        // (the records of all this CTA's warps are behind the block barrier above)
-        if (jw == 0 && lane == 0) tail->joined = span_grid_barrier(status, (int)gridDim.x, tail->generation) ? 1 : 0;
-        named_barrier_sync(2, JOIN);
-        if (!tail->joined) return;
         float* part = reinterpret_cast<float*>(smem_raw);  // [warp][column]
-        for (; row < out_rows; row += few ? (int)gridDim.x : (int)gridDim.x * JOIN_WARPS, find_row()) {
+#pragma unroll 1
+        for (bool waited = false;; row += few ? (int)gridDim.x : (int)gridDim.x * JOIN_WARPS) {
+            __nv_bfloat16* out = nullptr;
+            RowRecords src;
+            if (row < out_rows) {
+                const int bh = p.T_q == 1 ? row : row / p.T_q, t = row - bh * p.T_q, b = bh / heads, head = bh - b * heads;
+                int L;
+                const int unit0 = span_first_unit<SP_TK>(p, lengths, plan, sums, b, L);
+                const SpanView v = span_view<SP_TK>(p, L);
+                const int g = head / p.per;
+                out = O + ((int64_t)b * p.T_q + t) * ldo + (int64_t)head * HD + lane * E;
+                src = row_records<SP_TK>(p, rec, plan, unit0, v.nt, b, g, (head - g * p.per) * p.T_q + t);
+                if (v.nt == 0) src.n[0] = src.n[1] = 0;  // invalid length
+            }
+            if (!waited) {
+                waited = true;
+                // (the records of all this CTA's warps are behind the block barrier above)
+                if (jw == 0 && lane == 0) tail->joined = span_grid_barrier(status, (int)gridDim.x, tail->generation) ? 1 : 0;
+                named_barrier_sync(2, JOIN);
+                if (!tail->joined) return;
+            }
+            if (row >= out_rows) break;
             const int n = src.count();
             if (n == 1) continue;  // one unit held the whole group and wrote the row
             float o[E], l = 1.f;
