@@ -9,7 +9,7 @@
 // divide the SMs and SMs that are slower than others leave none idle (an even cut made beforehand left the
 // first CTA idle for a fifth of a step).  Units are numbered prefix first, then by batch, chunk and lane,
 // lanes fastest: a cached token's rows of all heads lie side by side, and units taken at about the same
-// time read whole pieces of DRAM pages.  U is chosen so that every CTA gets about `aim` units, but no
+// time read whole pieces of DRAM pages.  U is chosen so that every CTA gets 6 to 16 units, but no
 // unit's record of its rows costs more than a few percent of the unit; Up so that every CTA gets at most about one
 // of the prefix.  A unit that holds a whole
 // group writes its output itself; the others leave a record per row (maximum, sum, weighted values), and
@@ -25,7 +25,7 @@ namespace mha {
 // Largest grid of the unit kernels (bounds the records; the host knows no SM count when it computes
 // workspace sizes), and most units per CTA to aim for.
 constexpr int kSpanMaxCtas = 320;
-constexpr int kSpanUnits = 10;
+constexpr int kSpanUnits = 16;
 
 struct SpanShape {
     int B, h_kv;
@@ -36,7 +36,7 @@ struct SpanShape {
     int T_p;     // shared prefix tokens (0: none)
     int nrbp;    // row blocks of the B * rows rows over the prefix
     int bm_c, bm_p;  // rows of a row block of a cache and of the prefix
-    int aim;     // units per CTA to aim for, at most kSpanUnits
+    int aim;     // units per CTA to aim for, at most kSpanUnits; 0: by the number of tiles
     int step;    // tiles that a CTA of the caches' kernel works on at a time: larger units are multiples of it
     int window;  // <= T_max; T_max: no window
     int sinks;
@@ -146,7 +146,11 @@ __device__ inline SpanPlan span_plan(const SpanShape& p, const int32_t* lengths,
     for (int i = s.i0; i < s.i1; ++i) tiles += span_view<TILE>(p, s.length(lengths, i)).nt;
     const int np = span_prefix_tiles<TILE>(p);
     const unsigned total = __reduce_add_sync(0xffffffffu, (unsigned)tiles) * (unsigned)p.lanes_c() + (unsigned)(np * p.lanes_p());
-    const unsigned target = (unsigned)(p.aim * ctas);
+    // With many tiles short units at the end even out the CTAs; with few, a unit's own cost counts.  Units per
+    // CTA 6 | 10 | 14 | 20, us: 20 tiles a CTA 39 | 43 | 43 | 60, 40 tiles 72 | 73 | 76 | 81, 160 tiles 238 | 233 |
+    // 232 | 232.
+    const unsigned aim = p.aim > 0 ? (unsigned)p.aim : min((unsigned)kSpanUnits, max(6u, total / (6u * (unsigned)ctas)));
+    const unsigned target = aim * (unsigned)ctas;
     SpanPlan q;
     q.U = max(p.least_c(), (int)((total + target - 1) / target));
     q.U = max(q.U, 1);

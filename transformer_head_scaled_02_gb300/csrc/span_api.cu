@@ -42,7 +42,7 @@ SpanShape span_shape(const mha_s* m, int B, int T_q, int T_max, int T_p, int win
     p.nrb = (p.rows + p.bm_c - 1) / p.bm_c;
     p.nrbp = T_p > 0 ? (int)((rows_p + p.bm_p - 1) / p.bm_p) : 0;
     const bool few = p.bm_c < 16;
-    p.aim = few ? 1 : kSpanUnits;  // few rows: its units are long (1, 2 and 4 of them: 41, 46 and 50 us of the
+    p.aim = few ? 1 : 0;  // few rows: its units are long (1, 2 and 4 of them: 41, 46 and 50 us of the
                                    // first case above)
     p.step = few ? 4 : 1;
     p.window = window < T_max ? window : T_max;
