@@ -341,7 +341,8 @@ __global__ void __launch_bounds__(WN_THREADS, 1)
                     nx_tiles = nx.tiles;
                     nx_nst = nx.nst;
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) nx_first[t] = nx.first[t], nx_end[t] = nx.end[t];
+                    for (int t = 0; t < 2; ++t)  // (the end mark has a count of tiles only)
+                        if (nx_tiles > 0) nx_first[t] = nx.first[t], nx_end[t] = nx.end[t];
                 }
                 for (int j = 0; j < tiles && ok; ++j, ++J) {
                     const bool lastj = j + 1 == tiles;
@@ -364,13 +365,12 @@ __global__ void __launch_bounds__(WN_THREADS, 1)
                             fresh[t] = false;
                             if (j + 1 == end[t]) tc_commit_elect(el, bar(tail->odone[t]));
                         }
-                        // this query tile's scores of the next tile
-                        if (lastj) {
-                            if (nx_tiles > 0 && wn_visits(0, nx_nst, nx_first[t], nx_end[t])) ok = ok && issue_s(t, J + 1, true, nx_end[t] == 1);
-                        } else if (wn_visits(j + 1, nst, first[t], end[t])) {
-                            // (the first one, if this query tile passed over the tiles before)
-                            ok = ok && issue_s(t, J + 1, nst == 0 && j + 1 == first[t], j + 2 == end[t]);
-                        }
+                        // this query tile's scores of the next tile, the next item's first one included (a new
+                        // query tile also if this one passed over the tiles before)
+                        const int jn = lastj ? 0 : j + 1, nst_n = lastj ? nx_nst : nst;
+                        const int first_n = lastj ? nx_first[t] : first[t], end_n = lastj ? nx_end[t] : end[t];
+                        if (wn_visits(jn, nst_n, first_n, end_n))
+                            ok = ok && issue_s(t, J + 1, jn == (nst_n > 0 ? 0 : first_n), jn + 1 == end_n);
                     }
                     if (!ok) break;
                     tc_commit_elect(el, bar(tail->vempty[st]));
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(WN_THREADS, 1)
                 // nothing visible to the whole tile: zeros (padding), NaN for an invalid length
                 const uint32_t z = it.bad ? 0x7FC07FC0u : 0u;
                 if (store)
-#pragma unroll
+#pragma unroll 1
                     for (int e = 0; e < HD; e += 8) *reinterpret_cast<uint4*>(out + e) = make_uint4(z, z, z, z);
                 J += it.tiles;
                 continue;
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(WN_THREADS, 1)
             tc_fence_after();
             const float inv = l > 0.f ? 1.f / l : 0.f;  // a row that sees nothing (padding): zeros
             const __nv_bfloat16* g = GATE ? gate + ((int64_t)it.b * a.T + row) * ldg + (int64_t)it.head * HD : nullptr;
-#pragma unroll
+#pragma unroll 1
             for (int cc = 0; cc < HD; cc += 32) {
                 uint32_t o[32];
                 tmem_ld32(o_col + cc, o);
