@@ -17,13 +17,13 @@
 // room until these CTAs end, and the next step's CTAs none until they are gone.  Code that runs once per
 // CTA is kept short throughout: it is fetched from L2 every time.
 //
-// Measured: 32 caches of up to 8192 tokens, 16 K/V heads of d = 128, window 4096 (1.08 GB) 174 to 181 us, 89 to
-// 93 % of the measured copy rate; 4 K/V heads with weights (409 MB) 99 us, 62 %; 64 caches of up to 1024 tokens
-// behind a prefix of 32768, 4 query heads each on 4 K/V heads, 68 us; one cache of 1004 visible tokens 12 us.
-// Short units cost most beside HBM: between two units a stream waits for the last value product and reads the
-// sums, about 2 us.  (Putting a unit's end behind the next unit's first softmax made every tile's softmax
-// slower, 97 us instead of 84 without weights.)  Boxes of 32 rows, 5, 16 and 24 units per CTA and masks in
-// registers were slower, too.
+// Measured: 32 caches of up to 8192 tokens, 16 K/V heads of d = 128, window 4096 (1.08 GB) 167 us, 96 % of the
+// measured copy rate; 4 K/V heads with weights (409 MB) 84 us, 73 %; 64 caches of up to 1024 tokens behind a
+// prefix of 32768, 4 query heads each on 4 K/V heads, 62 us; one cache of 1004 visible tokens 12 us.  Short units
+// cost most beside HBM: between two units a stream waits for the last value product and reads the sums, about
+// 2 us.  The roles' loops share the instruction cache: with several copies of the score product and of the
+// tile loads the same four took 177, 99, 68 and 12 us.  Slower, too: a unit's end behind the next unit's first
+// softmax, few query rows twice in the tile for the two streams to run on two warp schedulers, boxes of 32 rows.
 //
 // Tensor memory (512 columns): S_t at 128 t (P_t overwrites its first 64 columns), O_t at 256 + HD t.
 // Warp roles (384 threads): warp 0 TMA; warp 1 TMEM owner and MMA issuer (from the whole warp, see

@@ -10,12 +10,12 @@
 // end (reading the accumulator, the gate, the stores) lies under the next one's loads and products.
 //
 // Items are numbered from the last rows of all sequences to the first: those, which see less than a
-// window, come last and even out the CTAs (numbered the other way, 16 heads of 16384 rows took 219 us with
-// the tensor pipes of the SMs busy for 51 to 70 % of the time).
+// window, come last and even out the CTAs (numbered the other way, 16 heads of 16384 rows took 219 us for
+// 205, with the tensor pipes of the SMs busy for 51 to 70 % of the time).
 //
-// Measured: 16 heads x 16384 rows, d = 128, window 2048: 205 us, 65 % of the measured bf16 rate (260 GF: only the
+// Measured: 16 heads x 16384 rows, d = 128, window 2048: 192 us, 69 % of the measured bf16 rate (260 GF: only the
 // visible pairs count), bound by the chain score product, softmax, value product of each query tile with two
-// in flight.  4 x 16 heads x 2048 rows, d = 64, window 256: 35 us; most of its tiles are cut by a mask and a
+// in flight.  4 x 16 heads x 2048 rows, d = 64, window 256: 32 us; most of its tiles are cut by a mask and a
 // CTA has three items.  P in columns of its own (d = 64 has room) took 45 us where this took 41, masks kept in
 // registers no less than in the scores.
 //
