@@ -13,7 +13,8 @@
 //
 // Bound by the issue of FMAs and the waits between the halves (two blocks an SM).  Measured with asynchronous
 // copies and packed score products | with plain loads of both tiles before a step: window of 256 over 2 x 8
-// heads x 2048 rows, d = 64 98 | 112 us (36 % of the FMA rate), d = 128 218 | 306, d = 256 360 | 548; weights
+// heads x 2048 rows, d = 64 98 | 112 us (36 % of the FMA rate), d = 128 218 (200 in 32-row blocks) | 306, d = 256
+// 360 | 548; weights
 // of 16 caches of 4096 tokens, 4 K/V heads, 20 rows of d = 64 180 | 227, 64 rows of d = 128 611 | 759; but one
 // or two tiles a block (64 rows of d = 64 over a prefix of 4096) 59 | 51.
 #include <math.h>
@@ -239,7 +240,7 @@ struct SimtTile {
 // One block = BQ query rows of one (batch, head): the sinks below the rows' windows, then the keys
 // from the first row's window to the last row.
 template <int RQ, int CV>
-__global__ void __launch_bounds__(SS_THREADS, CV <= 2 ? 2 : 1)
+__global__ void __launch_bounds__(SS_THREADS, RQ <= 2 ? (CV == 1 ? 4 : CV == 2 ? 3 : 2) : CV <= 2 ? 2 : 1)
     window_simt_kernel(const float* __restrict__ Q, int64_t ldq, const float* __restrict__ K, int64_t ldk,
                        const float* __restrict__ V, int64_t ldv, const float* __restrict__ G, int64_t ldg,
                        float* __restrict__ O, int64_t ldo, int h, int h_kv, int T, int dk, int dv,
@@ -383,8 +384,13 @@ cudaError_t launch_window_f32(const float* Q, int64_t ldq, const float* K, int64
     auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
     const bool vec = al(Q) && al(K) && al(V) && ldq % 4 == 0 && ldk % 4 == 0 && ldv % 4 == 0 && d_k % 4 == 0 && d_v % 4 == 0;
     const float scale = (float)(1.4426950408889634 / sqrt((double)d_k));
-    const bool small = (int64_t)B * h * ((T + 63) / 64) < 256;  // 32-row blocks where 64-row ones leave SMs idle
     const int cv = (d_v + 63) / 64;
+    // 32-row blocks where 64-row ones leave SMs idle, and where an SM holds one block of 64 rows but three of 32:
+    // 2 x 8 heads x 2048 rows of d = 128, window 64 | 256 | 1024: 90 | 200 | 542 us, in 64-row blocks 109 | 218 | 541
+    // (d = 64 44 | 105 | 291 for 45 | 98 | 256, d = 80 156 for 141 under 256; d = 256 198 | 436 | 1155 for
+    // 181 | 360 | 888)
+    const bool one = cv <= 2 && SimtTile<4, 2>::smem_bytes(d_k) > 113 * 1024;
+    const bool small = (int64_t)B * h * ((T + 63) / 64) < 256 || one;
     auto launch = [&](auto kernel, size_t smem, int bq) {
         cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (err != cudaSuccess) return err;
