@@ -77,7 +77,7 @@ struct SpTail {
     int abort_flag, joined;
     unsigned generation;
 };
-static_assert(sizeof(SpTail) <= 3072, "span tail");
+static_assert(sizeof(SpTail) <= 3 * 1024, "span tail");
 
 struct SpMaps {
     CUtensorMap k, k16, v, v16, kp, kp16, vp, vp16;
