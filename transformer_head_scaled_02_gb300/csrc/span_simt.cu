@@ -14,9 +14,9 @@
 // Bound by the issue of FMAs and the waits between the halves (two blocks an SM).  Measured with asynchronous
 // copies and packed score products | with plain loads of both tiles before a step: window of 256 over 2 x 8
 // heads x 2048 rows, d = 64 98 | 112 us (36 % of the FMA rate), d = 128 218 (200 in 32-row blocks) | 306, d = 256
-// 360 | 548; weights
-// of 16 caches of 4096 tokens, 4 K/V heads, 20 rows of d = 64 180 | 227, 64 rows of d = 128 611 | 759; but one
-// or two tiles a block (64 rows of d = 64 over a prefix of 4096) 59 | 51.
+// 360 | 548; weights of 16 caches of 4096 tokens, 4 K/V heads, 20 rows of d = 64 180 | 227, 64 rows of d = 128
+// 611 | 759; but one or two tiles a block (64 rows of d = 64 over a prefix of 4096) 59 | 51.  Packed value products
+// as well, with P twice in shared memory, took 102 | 98 at d = 64, 204 | 200 at d = 128 and 343 | 360 at d = 256.
 #include <math.h>
 
 #include "internal.h"
@@ -385,7 +385,7 @@ cudaError_t launch_window_f32(const float* Q, int64_t ldq, const float* K, int64
     const bool vec = al(Q) && al(K) && al(V) && ldq % 4 == 0 && ldk % 4 == 0 && ldv % 4 == 0 && d_k % 4 == 0 && d_v % 4 == 0;
     const float scale = (float)(1.4426950408889634 / sqrt((double)d_k));
     const int cv = (d_v + 63) / 64;
-    // 32-row blocks where 64-row ones leave SMs idle, and where an SM holds one block of 64 rows but three of 32:
+    // 32-row blocks where 64-row ones leave SMs idle, and where an SM holds one block of 64 rows but two of 32:
     // 2 x 8 heads x 2048 rows of d = 128, window 64 | 256 | 1024: 90 | 200 | 542 us, in 64-row blocks 109 | 218 | 541
     // (d = 64 44 | 105 | 291 for 45 | 98 | 256, d = 80 156 for 141 under 256; d = 256 198 | 436 | 1155 for
     // 181 | 360 | 888)
