@@ -17,6 +17,8 @@
 // 360 | 548; weights of 16 caches of 4096 tokens, 4 K/V heads, 20 rows of d = 64 180 | 227, 64 rows of d = 128
 // 611 | 759; but one or two tiles a block (64 rows of d = 64 over a prefix of 4096) 59 | 51.  Packed value products
 // as well, with P twice in shared memory, took 102 | 98 at d = 64, 204 | 200 at d = 128 and 343 | 360 at d = 256.
+// The windows' blocks go from the last rows to the first: under a window of 2048 the same heads of d = 64 take 276
+// us, from the first to the last 367 (256: 95 | 98).
 #include <math.h>
 
 #include "internal.h"
@@ -252,7 +254,7 @@ __global__ void __launch_bounds__(SS_THREADS, RQ <= 2 ? (CV == 1 ? 4 : CV == 2 ?
     const int tid = (int)threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int b = (int)blockIdx.x / h, head = (int)blockIdx.x - b * h;
     const int kvh = head / (h / h_kv);
-    const int q0 = (int)blockIdx.y * X::BQ;
+    const int q0 = (int)(gridDim.y - 1 - blockIdx.y) * X::BQ;  // the last rows, which see the most keys, first
     const int L = kv_lengths != nullptr ? kv_lengths[b] : T;
     const int64_t row0 = (int64_t)b * T + q0;
     if (L < 1 || L > T) {
