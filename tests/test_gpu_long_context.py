@@ -751,3 +751,31 @@ def test_two_graphs_share_a_workspace(dtype, d):
             t, lens, _, w, out, ref, A, _ = cases[1 - i]
             _check(to_host(layer.decode_weights(*t, lens, w)), ref, A, dtype, "eager between graphs")
     assert layer.status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_captured_status_word_outlives_a_larger_workspace(dtype):
+    """attention_window and evict need the workspace for its status word only: one that a graph of them was
+    captured with stays theirs when a larger call replaces it."""
+    h, h_kv, d, B, T = 4, 2, 64, 2, 100
+    for op in ("window", "evict"):
+        layer = _layer(dtype, h, d, h_kv)
+        Q, K, V = (to_device(x, dtype) for x in _cache(600, dtype, B, T, T, h, h_kv, d, d))
+        lens, w = _lens([T, T + 1]), torch.ones((B, h_kv, T), device="cuda")  # the second is invalid
+
+        def call():
+            if op == "window":
+                return layer.attention_window(Q, K, V, 10, kv_lengths=lens)
+            return layer.evict(K, V, lens, w, 10, 2)
+        layer.ensure_workspace(0, 0, 0, need=256)
+        call()
+        assert layer.status() == 6
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        old = layer._ws
+        layer.ensure_workspace(0, 0, 0, need=1 << 20)
+        assert layer._ws is not old and any(x is old for x in layer._kept_ws)
+        g.replay()
+        torch.cuda.synchronize()
+        assert int(old[:4].view(torch.int32).item()) == 6 and layer.status() == 0

@@ -364,6 +364,8 @@ class Mha:
         ldg = 0 if G is None else self._rows("G", G, B, T, self.h * self.d_v)
         lens = None if kv_lengths is None else self._ints("kv_lengths", kv_lengths, B)
         stream = self._device(Q, K, V, out, G, kv_lengths)
+        if self._ws is not None:
+            self.ensure_workspace(0, 0, 0, need=256)  # its status word is the kernel's, a captured one's too
         _lib.mha_attention_window(self.handle, B, T, Q.data_ptr(), ldq, K.data_ptr(), ldk, V.data_ptr(),
                                   ldv, _ptr(G), ldg, window, sinks, lens, out.data_ptr(), ldo, stream)
         return out
@@ -454,15 +456,14 @@ class Mha:
         if weights_out is None:
             weights_out = torch.empty((B, self.h_kv, T_out), dtype=torch.float32, device=dev)
         if lengths_out is None:
-            lengths_out = torch.empty(B, dtype=torch.int32, device=dev)
-        kept = torch.empty((B, self.h_kv, keep), dtype=torch.int32, device=dev)
+            lengths_out = torch.empty_like(cache_lengths)
+        kept = cache_lengths.new_empty((B, self.h_kv, keep))
         ldko = self._rows("K_out", K_out, B, T_out, wk)
         ldvo = self._rows("V_out", V_out, B, T_out, wv)
         wo = self._weights("weights_out", weights_out, (B, self.h_kv, T_out))
         lo = self._ints("lengths_out", lengths_out, B)
         stream = self._device(K_cache, V_cache, cache_lengths, weights, K_out, V_out, weights_out, lengths_out)
-        if self._ws is None:
-            self.ensure_workspace(0, 0, 0, need=256)  # the status word
+        self.ensure_workspace(0, 0, 0, need=256)  # the status word
         _lib.mha_cache_evict(self.handle, B, T_max, keep, recent, K_cache.data_ptr(), ldk,
                              V_cache.data_ptr(), ldv, lens, w, T_out, K_out.data_ptr(), ldko,
                              V_out.data_ptr(), ldvo, wo, kept.data_ptr(), lo, stream)
