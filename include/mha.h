@@ -111,13 +111,25 @@ size_t mha_workspace_size(mha_t handle, int B, int T_q, int T_kv);
 
 /*
  * mha_set_workspace -- attach caller-owned device memory (256-byte aligned,
- * `bytes` long) to the handle, and zero its status block (a synchronous
- * cudaMemset of 256 bytes).  The memory must stay valid while calls using
+ * `bytes` long) to the handle, and zero its 256-byte status block: the status
+ * word, and counters that calls leave at zero for the next one, so nothing else
+ * may write there while it is attached.  The zeros follow the work queued on the
+ * legacy default stream and are in place on return; other streams must have no
+ * work pending on the memory.  The memory must stay valid while calls using
  * the handle are in flight.  NULL detaches.  The first attach also creates the
  * two copy streams and the events mha_forward_host uses, on the current device
  * (MHA_ERR_CUDA if that fails); they live until mha_destroy.
  */
 mha_status mha_set_workspace(mha_t handle, void* dev_ptr, size_t bytes);
+
+/*
+ * mha_set_workspace_on -- mha_set_workspace whose zeros are queued on `stream`,
+ * behind the work that is already there, without waiting: the handle's next calls
+ * must be on that stream or ordered behind it.  If `stream` is being captured the
+ * zeros come with the graph's replays, and only calls of that graph may use the
+ * workspace until another one is attached.
+ */
+mha_status mha_set_workspace_on(mha_t handle, void* dev_ptr, size_t bytes, void* stream);
 
 /*
  * mha_forward -- Y = MultiHead(X_q, X_kv) for the whole batch.

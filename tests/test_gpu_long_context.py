@@ -779,3 +779,91 @@ def test_captured_status_word_outlives_a_larger_workspace(dtype):
         g.replay()
         torch.cuda.synchronize()
         assert int(old[:4].view(torch.int32).item()) == 6 and layer.status() == 0
+
+
+# ------------------------------------------------------------------ workspaces
+
+def _busy(ms=30.0):
+    """About that many milliseconds of ordinary work on the current stream (a product of 8192^3 takes more
+    than half a millisecond)."""
+    a = torch.zeros((8192, 8192), dtype=torch.bfloat16, device="cuda")
+    for _ in range(int(ms / 0.55)):
+        a = a @ a
+
+
+def _step_cases(dtype, d, seed, h=8, h_kv=2):
+    """A small and a larger batch for decode_weights: tensors, lengths, and the 64-bit results."""
+    cases = []
+    for i, (B, Tmax, lengths) in enumerate(((2, 700, [700, 391]), (6, 2000, [2000, 1, 1333, 640, 129, 1999]))):
+        Q, K, V = _cache(seed + 10 * i, dtype, B, 1, Tmax, h, h_kv, d, d)
+        t = [to_device(x, dtype) for x in (Q, K, V)]
+        w0 = np.zeros((B, h_kv, Tmax), dtype=np.float32)
+        ref, A, W = lc.decode(Q, K, V, h, lengths, h_kv, weights=w0)
+        cases.append((t, _lens(lengths), lengths, to_device(w0, "f32"), ref, A, W))
+    return cases
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("f32", 32)])
+def test_workspace_of_a_side_stream_under_a_busy_default_stream(dtype, d):
+    """The first and a larger step on a side stream, in memory that still has writes pending there, while the
+    default stream is busy: each starts from a zeroed status block."""
+    h, h_kv = 8, 2
+    cases = _step_cases(dtype, d, 700)
+    layer = _layer(dtype, h, d, h_kv)
+    sizes = [_lib.mha_cache_step_workspace_size(layer.handle, len(c[2]), 1, 0, c[0][1].shape[1], 1) for c in cases]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        _busy(1.0)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    _busy()
+    with torch.cuda.stream(side):
+        dirty = []
+        for c, n in zip(cases, sizes):
+            out = torch.empty((len(c[2]), 1, h * d), dtype=torch_dtype(dtype), device="cuda")
+            _busy(2.0)
+            x = torch.full((n,), 1, dtype=torch.uint8, device="cuda")  # counters of 0x01010101
+            dirty.append(x.data_ptr())
+            del x
+            layer.decode_weights(*c[0], c[1], c[3], out=out)
+            assert layer._ws.data_ptr() == dirty[-1]                   # or this tests nothing
+            c[0].append(out)
+        status = layer.status()
+    assert status == 0
+    torch.cuda.synchronize()
+    for t, _, lengths, w, ref, A, W in cases:
+        _check(to_host(t[3]), ref, A, dtype, "side stream")
+        for b, n in enumerate(lengths):
+            _check_weights(to_host(w)[b, :, :n], W[b, :, :n], "side stream")
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("f32", 32)])
+def test_workspace_attached_under_capture(dtype, d):
+    """A layer whose first steps are captured: eager steps before the first replay, then replays, then eager
+    steps again, all from the same workspace."""
+    h, h_kv = 8, 2
+    cases = _step_cases(dtype, d, 750)
+    warm = _layer(dtype, h, d, h_kv)
+    for t, lens, _, w, *_ in cases:
+        warm.decode_weights(*t, lens, w)
+    torch.cuda.synchronize()
+    layer = _layer(dtype, h, d, h_kv)
+    outs = [torch.zeros((len(c[2]), 1, h * d), dtype=torch_dtype(dtype), device="cuda") for c in cases]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        # a temporary of the graph where its pool may hand out memory again
+        torch.full((1 << 22,), 1, dtype=torch.uint8, device="cuda")
+        for (t, lens, _, w, *_), out in zip(cases, outs):
+            layer.decode_weights(*t, lens, w, out=out)
+    for turn in range(3):
+        for (t, lens, lengths, w, ref, A, W), out in zip(cases, outs):
+            w.zero_()
+            _check(to_host(layer.decode_weights(*t, lens, w)), ref, A, dtype, "eager")
+            out.zero_()
+            w.zero_()
+        g.replay()
+        for (t, lens, lengths, w, ref, A, W), out in zip(cases, outs):
+            _check(to_host(out), ref, A, dtype, "replayed")
+            for b, n in enumerate(lengths):
+                _check_weights(to_host(w)[b, :, :n], W[b, :, :n], "replayed")
+    assert layer.status() == 0

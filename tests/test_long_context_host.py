@@ -214,3 +214,47 @@ def test_oracle_evict():
     assert lc.evict(w, [6], 5, 1) == [[[0, 1, 3, 4, 5]]]
     assert lc.evict(w, [5], 1, 0) == [[[0]]]
     assert lc.evict(w, [8], 1, 0) == [[None]]
+
+
+# ------------------------------------------------------------------ workspaces
+
+def test_set_workspace_on_refusals(handles):
+    def call(h="bf", ptr=FAKE, n=4096, stream=None):
+        return L.mha_set_workspace_on(None if h is None else handles[h], ptr, n, stream, check=False)
+    for kw in (dict(h=None), dict(ptr=FAKE + 128), dict(n=255), dict(n=0)):
+        assert call(**kw) == L.MHA_ERR_INVALID_ARG, kw
+    assert call(ptr=None, n=0) == L.MHA_OK                   # detaches
+
+
+def test_workspace_is_zeroed_in_the_order_of_the_calls_stream(lib, monkeypatch):
+    """The status block holds the cache steps' counters: its zeros have to come before the call that follows
+    the attach, which on another stream they need not.  Memory of a capture stays with captured calls."""
+    torch = pytest.importorskip("torch")
+    from transformer_head_scaled_02_gb300 import Mha, mha
+    calls, now = [], [False]
+    monkeypatch.setattr(mha, "_stream", lambda: 55)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: now[0])
+    monkeypatch.setattr(L, "mha_set_workspace", lambda *a: calls.append(("unordered",)))
+    monkeypatch.setattr(L, "mha_set_workspace_on", lambda h, p, n, stream: calls.append((p, n, stream)), raising=False)
+    layer = Mha(256, 4, 64, dtype=torch.bfloat16, device="cpu")
+
+    def ensure(need, capturing=False):
+        now[0] = capturing
+        ws, n = layer._ws, len(calls)
+        got = layer.ensure_workspace(1, 1, 1, need=need)
+        assert got.numel() >= need and got is layer._ws
+        if got is not ws:
+            assert calls[n:] == [(got.data_ptr(), got.numel(), 55)]
+        else:
+            assert len(calls) == n
+        return got
+    a = ensure(1000)
+    assert ensure(500) is a and ensure(1000, True) is a      # captured: outlives its replacement
+    b = ensure(5000)
+    assert b is not a and layer._kept_ws == [a]
+    c = ensure(9000, True)                                   # the graph's memory
+    c.fill_(1)
+    assert ensure(9000, True) is c and (c[4:256] == 0).all() and c[0] == 1 and c[256] == 1
+    d = ensure(100)
+    assert d is not c and any(x is c for x in layer._kept_ws)
+    assert ensure(100, True) is d

@@ -36,6 +36,7 @@ _SIGNATURES = {
     "mha_destroy": (None, [_vp]),
     "mha_workspace_size": (_sz, [_vp, _i, _i, _i]),
     "mha_set_workspace": (_i, [_vp, _vp, _sz]),
+    "mha_set_workspace_on": (_i, [_vp, _vp, _sz, _vp]),
     "mha_forward": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp]),
     "mha_forward_checked": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp]),
     "mha_forward_ex": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp]),
@@ -138,6 +139,11 @@ def mha_workspace_size(handle: int, B: int, T_q: int, T_kv: int) -> int:
 
 def mha_set_workspace(handle: int, dev_ptr: int, nbytes: int) -> int:
     return _check("mha_set_workspace", load().mha_set_workspace(handle, dev_ptr, nbytes))
+
+
+def mha_set_workspace_on(handle: int, dev_ptr: int, nbytes: int, stream: int, check: bool = True) -> int:
+    code = load().mha_set_workspace_on(handle, dev_ptr, nbytes, stream)
+    return _check("mha_set_workspace_on", code) if check else code
 
 
 def mha_forward(handle, X_q, X_kv, B, T_q, T_kv, W_qkv, b_qkv, W_o, b_o, causal, kv_lengths,

@@ -289,6 +289,17 @@ size_t mha_workspace_size(mha_t handle, int B, int T_q, int T_kv) {
 }
 
 mha_status mha_set_workspace(mha_t handle, void* dev_ptr, size_t bytes) {
+    mha_status st = mha_set_workspace_on(handle, dev_ptr, bytes, nullptr);
+    if (st != MHA_OK || dev_ptr == nullptr) return st;
+    // a capture that this thread has begun on another stream does not concern the wait
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (cudaStreamSynchronize(nullptr) != cudaSuccess) st = MHA_ERR_CUDA;
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    return st;
+}
+
+mha_status mha_set_workspace_on(mha_t handle, void* dev_ptr, size_t bytes, void* stream) {
     if (handle == nullptr) return MHA_ERR_INVALID_ARG;
     if (dev_ptr == nullptr) {
         handle->ws = nullptr;
@@ -297,7 +308,10 @@ mha_status mha_set_workspace(mha_t handle, void* dev_ptr, size_t bytes) {
     }
     if ((reinterpret_cast<uintptr_t>(dev_ptr) & 255u) != 0 || bytes < kStatusBytes)
         return MHA_ERR_INVALID_ARG;
-    if (cudaMemset(dev_ptr, 0, kStatusBytes) != cudaSuccess) return MHA_ERR_CUDA;
+    // In the order of the stream the kernels will run on: the counters of the block decide what a cache
+    // step computes, and zeros on any other stream need not be there before it.
+    if (cudaMemsetAsync(dev_ptr, 0, kStatusBytes, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return MHA_ERR_CUDA;
     if (handle->aux_dev < 0) {
         const mha_status st = create_aux(handle);
         if (st != MHA_OK) return st;

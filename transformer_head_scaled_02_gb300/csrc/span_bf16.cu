@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
             SpanUnit x;
             x.unit = -1;
             x.prefix = x.rb = 0;
-            if (u < plan.N) x = span_unit<SP_TK>(p, lengths, plan, sums, u);
+            if ((unsigned)u < (unsigned)plan.N) x = span_unit<SP_TK>(p, lengths, plan, sums, u);  // (whatever the counter held)
             if (i >= SP_RING && !warp_wait(bar(tail->uempty[i % SP_RING]), (uint32_t)(i / SP_RING - 1) & 1u, abort_flag, status)) break;
             if (lane == 0) {
                 tail->units[i % SP_RING] = x;

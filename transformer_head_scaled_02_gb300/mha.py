@@ -51,6 +51,7 @@ class Mha:
                                          _DTYPES[dtype])
         self._ws: Optional[torch.Tensor] = None
         self._ws_captured = False
+        self._ws_of_graph = False
         self._kept_ws: list = []
         self._step_bytes: dict = {}  # workspace bytes of the cache steps, by their sizes
 
@@ -72,14 +73,24 @@ class Mha:
 
     def ensure_workspace(self, B: int, T_q: int, T_kv: int, need: Optional[int] = None) -> torch.Tensor:
         need = self.workspace_size(B, T_q, T_kv) if need is None else need
-        if self._ws is None or self._ws.numel() < need:
+        capturing = torch.cuda.is_current_stream_capturing()
+        if self._ws is None or self._ws.numel() < need or (self._ws_of_graph and not capturing):
             if self._ws_captured:  # a captured graph still launches into the one it was captured with
                 self._kept_ws.append(self._ws)
-                self._ws_captured = False
-            self._ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
-            _lib.mha_set_workspace(self.handle, self._ws.data_ptr(), self._ws.numel())
-        if not self._ws_captured and torch.cuda.is_current_stream_capturing():
+            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
+            # its status block, with the counters of the cache steps, is zeroed in the order of the
+            # current stream: that is where the memory comes from and where the call goes
+            _lib.mha_set_workspace_on(self.handle, ws.data_ptr(), ws.numel(), _stream())
+            self._ws = ws
+            # under capture the memory is the graph's and the zeros come with its replays: eager calls
+            # get a workspace of their own
+            self._ws_captured = self._ws_of_graph = capturing
+        elif capturing:
             self._ws_captured = True
+            if self._ws_of_graph:
+                # this may be another graph of the pool, whose memory they all write to: the counters
+                # start from zero in every call
+                self._ws[4:256].zero_()
         return self._ws
 
     def status(self) -> int:
