@@ -867,3 +867,32 @@ def test_workspace_attached_under_capture(dtype, d):
             for b, n in enumerate(lengths):
                 _check_weights(to_host(w)[b, :, :n], W[b, :, :n], "replayed")
     assert layer.status() == 0
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("f32", 32)])
+def test_replaced_workspace_stays_until_its_steps_are_through(dtype, d):
+    """A step on a side stream with a workspace of the default stream, then a larger one there: the memory of the
+    first must not be given to a tensor of the default stream before the step has run."""
+    h, h_kv = 8, 2
+    cases = _step_cases(dtype, d, 800)
+    layer = _layer(dtype, h, d, h_kv)
+    (t, lens, _, w, *_), (t2, lens2, _, w2, *_) = cases
+    layer.decode_weights(*t, lens, w)
+    w.zero_()
+    torch.cuda.synchronize()
+    old, n = layer._ws.data_ptr(), layer._ws.numel()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        outs = [torch.empty((len(c[2]), 1, h * d), dtype=torch_dtype(dtype), device="cuda") for c in cases]
+        _busy()
+        layer.decode_weights(*t, lens, w, out=outs[0])
+        layer.decode_weights(*t2, lens2, w2, out=outs[1])
+    assert layer._ws.data_ptr() != old
+    taken = [torch.full((n,), 1, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    assert not any(x.data_ptr() <= old < x.data_ptr() + n for x in taken)
+    torch.cuda.synchronize()
+    for (_, _, lengths, w, ref, A, W), out in zip(cases, outs):
+        _check(to_host(out), ref, A, dtype, "replaced workspace")
+        for b, m in enumerate(lengths):
+            _check_weights(to_host(w)[b, :, :m], W[b, :, :m], "replaced workspace")
+    assert layer.status() == 0

@@ -258,3 +258,25 @@ def test_workspace_is_zeroed_in_the_order_of_the_calls_stream(lib, monkeypatch):
     d = ensure(100)
     assert d is not c and any(x is c for x in layer._kept_ws)
     assert ensure(100, True) is d
+
+
+def test_workspace_used_on_another_stream_is_recorded_there(lib, monkeypatch):
+    """Its memory must not go to another owner while calls on that stream are under way."""
+    torch = pytest.importorskip("torch")
+    from transformer_head_scaled_02_gb300 import Mha, mha
+    now, recorded = [1], []
+    monkeypatch.setattr(mha, "_stream", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: now[0])
+    monkeypatch.setattr(L, "mha_set_workspace_on", lambda *a: 0)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append((t.data_ptr(), s)), raising=False)
+    layer = Mha(256, 4, 64, dtype=torch.bfloat16, device="cpu")
+    a = layer.ensure_workspace(1, 1, 1, need=1000).data_ptr()
+    for now[0] in (1, 2, 1, 2, 3):
+        layer.ensure_workspace(1, 1, 1, need=1000)
+    assert recorded == [(a, 2), (a, 3)]
+    old = layer._ws                                          # (keeps its address from being given out again)
+    layer.ensure_workspace(1, 1, 1, need=5000)               # on 3: its own
+    now[0] = 1
+    layer.ensure_workspace(1, 1, 1, need=5000)
+    assert recorded[2:] == [(layer._ws.data_ptr(), 1)] and old is not layer._ws

@@ -21,7 +21,7 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 class Mha:
@@ -52,6 +52,7 @@ class Mha:
         self._ws: Optional[torch.Tensor] = None
         self._ws_captured = False
         self._ws_of_graph = False
+        self._ws_streams: set = set()  # streams that the allocator knows to use the workspace
         self._kept_ws: list = []
         self._step_bytes: dict = {}  # workspace bytes of the cache steps, by their sizes
 
@@ -85,12 +86,17 @@ class Mha:
             # under capture the memory is the graph's and the zeros come with its replays: eager calls
             # get a workspace of their own
             self._ws_captured = self._ws_of_graph = capturing
+            self._ws_streams = {_stream()}
         elif capturing:
             self._ws_captured = True
             if self._ws_of_graph:
                 # this may be another graph of the pool, whose memory they all write to: the counters
                 # start from zero in every call
                 self._ws[4:256].zero_()
+        elif _stream() not in self._ws_streams:
+            # calls on this stream may still be under way when a larger workspace replaces it
+            self._ws.record_stream(torch.cuda.current_stream())
+            self._ws_streams.add(_stream())
         return self._ws
 
     def status(self) -> int:
