@@ -578,10 +578,12 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
                 }
                 tc_fence_after();
                 if (active) {
-                    const float2 ml0 = tail->ml[0][r], ml1 = tail->ml[1][r];
+                    // in the order of the unit's tiles, the first of which went to stream j & 1: which one that
+                    // is depends on what this CTA took before, and must not show in the sums
+                    const int s0 = j & 1;
+                    const float2 ml0 = tail->ml[s0][r], ml1 = tail->ml[s0 ^ 1][r];
                     const float M = fmaxf(ml0.x, ml1.x);
-                    // the first tile of the unit went to stream j & 1
-                    const bool has0 = nt > 1 || (j & 1) == 0, has1 = nt > 1 || (j & 1) == 1;
+                    const uint32_t o0 = trow + C::O_COL + HD * s0, o1 = trow + C::O_COL + HD * (s0 ^ 1);
                     const float w0 = ml0.x == -INFINITY ? 0.f : ex2_approx(ml0.x - M);
                     const float w1 = ml1.x == -INFINITY ? 0.f : ex2_approx(ml1.x - M);
                     const float sum = w0 * ml0.y + w1 * ml1.y;
@@ -595,18 +597,16 @@ __global__ void __launch_bounds__(SP_THREADS, 1)
                     for (int c2 = 0; c2 < HD / 64; ++c2) {
                         const int cc = t * (HD / 64) + c2;
                         float f[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) f[e] = 0.f;
-                        if (has0) {
+                        {
                             uint32_t a[32];
-                            tmem_ld32(trow + C::O_COL + cc * 32, a);
+                            tmem_ld32(o0 + cc * 32, a);
                             tmem_wait_ld();
 #pragma unroll
                             for (int e = 0; e < 32; ++e) f[e] = w0 * __uint_as_float(a[e]);
                         }
-                        if (has1) {
+                        if (nt > 1) {
                             uint32_t a[32];
-                            tmem_ld32(trow + C::O_COL + HD + cc * 32, a);
+                            tmem_ld32(o1 + cc * 32, a);
                             tmem_wait_ld();
 #pragma unroll
                             for (int e = 0; e < 32; ++e) f[e] = fmaf(w1, __uint_as_float(a[e]), f[e]);
