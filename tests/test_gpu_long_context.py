@@ -934,3 +934,84 @@ def test_results_do_not_depend_on_the_schedule(d, step):
         side.synchronize()
     assert differ == 0
     assert layer.status() == 0
+
+
+def _non_finite_queries(Q, d):
+    """Rows of head 0 that hold a NaN, an infinity of either sign, or one that makes every score -inf (the keys'
+    first element is positive); the row numbers."""
+    rows = {3: (1, np.nan), 40: (1, np.inf), 41: (1, -np.inf), 100: (0, -np.inf), 150: (0, np.inf), 0: (0, -np.inf),
+            199: (0, -np.inf)}
+    for i, (e, x) in rows.items():
+        Q[:, i, e] = x
+    return sorted(rows)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("f32", 16), ("f32", 200)])
+@pytest.mark.parametrize("window,sinks", [(1000, 0), (30, 0), (30, 3), (1, 0), (130, 140)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_window_non_finite_queries(dtype, d, window, sinks, gated):
+    """A query row that is not finite gives NaN in its head, as in attention(); zeros are for padding rows that
+    see no key, whatever their queries hold.  The other rows and heads are as without it."""
+    h, h_kv, B, T = 2, 1, 2, 230
+    lengths = [230, 120]
+    Q, K, V = (_rand((B, T, n * d), s, dtype) for s, n in ((11, h), (12, h_kv), (13, h_kv)))
+    G = _rand((B, T, h * d), 14, dtype) if gated else None
+    K[..., 0] = np.abs(K[..., 0]) + 0.25                     # (exact enough: rounded again below)
+    if dtype == "bf16":
+        K = wl.bf16_to_f32(wl.bf16_bits(np.ascontiguousarray(K, dtype=np.float32)))
+    ref, A = lc.attention_window(Q, K, V, h, window, sinks, h_kv, lengths, G)
+    Qn = Q.copy()
+    rows = _non_finite_queries(Qn, d)
+    layer = _layer(dtype, h, d, h_kv, gated=gated)
+    t = [to_device(x, dtype) for x in (Qn, K, V)]
+    tg = to_device(G, dtype)
+    got = to_host(layer.attention_window(*t, window, sinks, kv_lengths=_lens(lengths), G=tg))
+    i, j = np.arange(T)[:, None], np.arange(T)
+    for b, L in enumerate(lengths):
+        sees = ((j <= i) & (j < L) & ((i - j < window) | (j < sinks))).any(1)
+        want_nan = np.zeros((T, h), bool)
+        want_nan[rows, 0] = sees[rows]
+        nan = np.isnan(got[b]).reshape(T, h, d)
+        assert (nan.all(-1) == want_nan).all() and (nan.any(-1) == want_nan).all()
+        assert (got[b][~sees] == 0).all()
+        keep = ~np.repeat(want_nan, d, -1)
+        _check(np.where(keep, got[b], 0), np.where(keep, ref[b], 0), np.where(keep, A[b], 0), dtype, "beside NaN rows")
+    if window >= T:
+        # the batch without padding rows: attention() the same
+        full = to_host(layer.attention(*t, causal=True, kv_lengths=_lens(lengths), G=tg))
+        assert (np.isnan(full[0]) == np.isnan(got[0])).all()
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("f32", 16), ("f32", 200)])
+@pytest.mark.parametrize("step", ["window", "shared", "weights"])
+@pytest.mark.parametrize("Tq", [1, 9])
+def test_steps_non_finite_queries(dtype, d, step, Tq):
+    """The same for the cache steps, which have no rows that see nothing."""
+    h, h_kv, B, Tmax = 4, 2, 5, 700
+    lengths = [700, Tq, 300, 129, 512]
+    Q, K, V = _cache(900, dtype, B, Tq, Tmax, h, h_kv, d, d)
+    K[..., ::d] = np.abs(K[..., ::d]) + 0.25
+    if dtype == "bf16":
+        K = wl.bf16_to_f32(wl.bf16_bits(np.ascontiguousarray(K, dtype=np.float32)))
+    kw = dict(window=333, sinks=4) if step == "window" else dict(K_prefix=K[0], V_prefix=V[0]) if step == "shared" else {}
+    ref, A, _ = lc.decode(Q, K, V, h, lengths, h_kv, **kw)
+    bad = {(0, 0, 0): np.nan, (1, 0, 3): -np.inf, (2, Tq - 1, 1): -np.inf, (3, 0, 2): np.inf}
+    for (b, t, i), x in bad.items():
+        Q[b, t, i * d] = x
+    layer = _layer(dtype, h, d, h_kv)
+    t = [to_device(x, dtype) for x in (Q, K, V)]
+    if step == "window":
+        got = layer.decode_window(*t, _lens(lengths), 333, 4)
+    elif step == "shared":
+        got = layer.decode_shared(t[0], t[1][0], t[2][0], t[1], t[2], _lens(lengths))
+    else:
+        got = layer.decode_weights(*t, _lens(lengths), torch.zeros((B, h_kv, Tmax), device="cuda"))
+    got = to_host(got)
+    want = np.zeros((B, Tq, h), bool)
+    for b, n, i in bad:
+        want[b, n, i] = True
+    nan = np.isnan(got).reshape(B, Tq, h, d)
+    assert (nan.all(-1) == want).all() and (nan.any(-1) == want).all()
+    keep = ~np.repeat(want, d, -1)
+    _check(np.where(keep, got, 0), np.where(keep, ref, 0), np.where(keep, A, 0), dtype, "beside NaN rows")
+    assert layer.status() == 0

@@ -290,7 +290,10 @@ __global__ void __launch_bounds__(SS_THREADS, RQ <= 2 ? (CV == 1 ? 4 : CV == 2 ?
     for (int r = 0; r < RQ; ++r) {
         const int t = ty * RQ + r;
         if (q0 + t >= T) continue;
-        const float inv = x.l[r] > 0.f ? 1.f / x.l[r] : 0.f;  // nothing visible: zeros
+        // zeros where the mask leaves nothing, which only the mask can tell: a row whose scores are all NaN or
+        // -inf has no weights either and is NaN
+        const bool sees = q0 + t - L + 1 < window || sinks > 0;
+        const float inv = sees ? 1.f / x.l[r] : 0.f;
 #pragma unroll
         for (int u = 0; u < 4 * CV; ++u) {
             const int e = (u >> 2) * 64 + tx * 4 + (u & 3);

@@ -554,7 +554,10 @@ __global__ void __launch_bounds__(WN_THREADS, 1)
             }
             ++no;
             tc_fence_after();
-            const float inv = l > 0.f ? 1.f / l : 0.f;  // a row that sees nothing (padding): zeros
+            // zeros where the mask leaves nothing (a padding row), which only the mask can tell: a row whose scores
+            // are all NaN or -inf has no weights either and is NaN
+            const bool sees = row - it.L + 1 < a.window || a.sinks > 0;
+            const float inv = sees ? 1.f / l : 0.f;
             const __nv_bfloat16* g = GATE ? gate + ((int64_t)it.b * a.T + row) * ldg + (int64_t)it.head * HD : nullptr;
 #pragma unroll 1
             for (int cc = 0; cc < HD; cc += 32) {
