@@ -395,8 +395,8 @@ size_t mha_cache_step_workspace_size(mha_t handle, int B, int T_q, int T_prefix,
  * as for mha_decode.  O must not overlap an input.
  * Both dtypes need a workspace of mha_cache_step_workspace_size(B, T_q, 0, T_max, 0) bytes
  * (MHA_ERR_WORKSPACE otherwise).  bf16: one cooperative launch of a CTA per SM, so it starts once other
- * streams' kernels have left every SM; fp32: two launches.  A call whose status is MHA_ERR_TIMEOUT may leave
- * the workspace's counters mid-way: attach it again (mha_set_workspace) before the next.
+ * streams' kernels have left every SM; fp32: two launches.  A call that ran into MHA_ERR_TIMEOUT may leave the
+ * workspace's counters mid-way: read the status (mha_get_status resets them), or attach it again, before the next.
  */
 mha_status mha_decode_window(mha_t handle, int B, int T_q, int T_max, const void* Q, int64_t ldq,
                              const void* K_cache, int64_t ldk, const void* V_cache, int64_t ldv, int window,
@@ -462,7 +462,8 @@ mha_status mha_cache_evict(mha_t handle, int B, int T_max, int keep, int recent,
 /*
  * mha_get_status -- copy the device status word of the attached workspace to
  * *status_out (an mha_status: MHA_OK, MHA_ERR_TIMEOUT or MHA_ERR_BAD_LENGTH;
- * the first error recorded wins) and reset it to MHA_OK.  Synchronises
+ * the first error recorded wins) and zero the status block, which resets it to
+ * MHA_OK and clears what a timed-out call may have left.  Synchronises
  * `stream`.  Returns MHA_ERR_WORKSPACE if no workspace is attached.
  */
 mha_status mha_get_status(mha_t handle, int32_t* status_out, void* stream);

@@ -1015,3 +1015,24 @@ def test_steps_non_finite_queries(dtype, d, step, Tq):
     keep = ~np.repeat(want, d, -1)
     _check(np.where(keep, got, 0), np.where(keep, ref, 0), np.where(keep, A, 0), dtype, "beside NaN rows")
     assert layer.status() == 0
+
+
+@pytest.mark.parametrize("code", [_lib.MHA_ERR_TIMEOUT, _lib.MHA_ERR_BAD_LENGTH])
+@pytest.mark.parametrize("d", [64, 128])
+def test_status_resets_what_a_timed_out_step_left(code, d):
+    """Arrivals, generation and unit counter as an aborted step leaves them (written here by the host; the status
+    may be that of an earlier error): reading the status makes the workspace whole again."""
+    h, h_kv = 8, 2
+    cases = _step_cases("bf16", d, 850)
+    layer = _layer("bf16", h, d, h_kv)
+    for t, lens, _, w, *_ in cases:
+        layer.decode_weights(*t, lens, w)
+    assert layer.status() == 0
+    layer._ws[:16].view(torch.int32).copy_(torch.tensor([code, 77, 5, 901], dtype=torch.int32))
+    assert layer.status() == code
+    for t, lens, lengths, w, ref, A, W in cases:
+        w.zero_()
+        _check(to_host(layer.decode_weights(*t, lens, w)), ref, A, "bf16", "after an error")
+        for b, n in enumerate(lengths):
+            _check_weights(to_host(w)[b, :, :n], W[b, :, :n], "after an error")
+    assert layer.status() == 0

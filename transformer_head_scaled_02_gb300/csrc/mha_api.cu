@@ -699,7 +699,8 @@ mha_status mha_get_status(mha_t handle, int32_t* status_out, void* stream) {
     int32_t v = 0;
     if (cudaMemcpyAsync(&v, handle->ws, sizeof(v), cudaMemcpyDeviceToHost, cs) != cudaSuccess)
         return MHA_ERR_CUDA;
-    if (cudaMemsetAsync(handle->ws, 0, sizeof(v), cs) != cudaSuccess) return MHA_ERR_CUDA;
+    // the whole block: a step that timed out (behind another error, perhaps) leaves the counters mid-way
+    if (cudaMemsetAsync(handle->ws, 0, kStatusBytes, cs) != cudaSuccess) return MHA_ERR_CUDA;
     if (cudaStreamSynchronize(cs) != cudaSuccess) return MHA_ERR_CUDA;
     *status_out = v;
     return MHA_OK;

@@ -100,7 +100,8 @@ class Mha:
         return self._ws
 
     def status(self) -> int:
-        """Read and clear the device status word (synchronises the current stream)."""
+        """Read and clear the device status word, and reset what a step that timed out may have left in
+        the workspace's counters (synchronises the current stream)."""
         return _lib.mha_get_status(self.handle, _stream())
 
     # ------------------------------------------------------------ checks
