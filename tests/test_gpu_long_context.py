@@ -936,6 +936,63 @@ def test_results_do_not_depend_on_the_schedule(d, step):
     assert layer.status() == 0
 
 
+# Two layers of one kernel instantiation that need different amounts of shared memory.
+THREAD_CASES = {
+    # operator: (d_k, d_v, tokens) of the smaller and of the larger layer
+    "evict": ((4, 4, 9000), (4, 4, 45000)), "attention_window": ((16, 48, 40), (256, 48, 40)),
+    "decode_window": ((16, 48, 40), (256, 48, 40)), "attention": ((16, 48, 40), (256, 48, 40)),
+    "decode": ((16, 48, 40), (256, 256, 40))}
+
+
+@pytest.mark.parametrize("op", THREAD_CASES)
+def test_layers_of_different_sizes_in_two_threads(op, monkeypatch):
+    """Each host thread has a layer and a stream of its own: what one launches must not change the shared-memory
+    limit that the other's launch of the same kernel needs."""
+    import threading
+    entry = {"evict": "mha_cache_evict", "attention": "mha_attention_ex"}.get(op, f"mha_{op}")
+    real, taken = getattr(_lib, entry), []
+    monkeypatch.setattr(_lib, entry, lambda *a: taken.append(a) or real(*a))
+    jobs, keep = [], []
+    for d, dv, T in THREAD_CASES[op]:
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            layer = _layer("f32", 1, d, 1, dv)
+            Q, K, V = (torch.zeros((1, T, n), device="cuda") for n in (d, d, dv))
+            q = torch.zeros((1, 20, d), device="cuda")
+            if op == "evict":
+                lens, w = _lens([50]), torch.zeros((1, 1, T), device="cuda")
+                out = layer.evict(K, V, lens, w, 100, 10)
+            elif op == "attention_window":
+                lens, w, out = None, None, layer.attention_window(Q, K, V, 8)
+            elif op == "attention":
+                lens, w, out = None, None, layer.attention(Q, K, V, causal=True)
+            else:
+                lens, w = _lens([T]), torch.zeros((1, 20, dv), device="cuda")
+                out = layer.decode_window(q, K, V, lens, 8, out=w) if op == "decode_window" else \
+                    layer.decode(q, K, V, lens, out=w)
+        keep.append((layer, Q, q, K, V, lens, w, out))
+        jobs.append((taken[-1], stream))
+    torch.cuda.synchronize()
+    failed, start = [], threading.Barrier(2)
+
+    def work(args, stream):
+        start.wait()
+        try:
+            for i in range(10000):   # the C entry by itself: no interpreter lock is held in it
+                real(*args)
+                if i % 500 == 0:
+                    stream.synchronize()
+        except Exception as e:  # noqa: BLE001 (reported below)
+            failed.append(e)
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+
+
 def _non_finite_queries(Q, d):
     """Rows of head 0 that hold a NaN, an infinity of either sign, or one that makes every score -inf (the keys'
     first element is positive); the row numbers."""

@@ -342,8 +342,10 @@ cudaError_t launch_evict(const void* K, int64_t ldk, const void* V, int64_t ldv,
     auto select = keys ? evict_select_kernel<true> : evict_select_kernel<false>;
     const size_t smem = keys ? (size_t)T_max * sizeof(uint32_t) : 0;
     cudaError_t err = cudaSuccess;
-    if (smem > 32 * 1024)  // with the static 11 KB past what a launch gets unasked
-        err = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // past what a launch gets unasked (with the static 11 KB).  The limit belongs to the process, where another
+    // thread may be launching a larger selection: always the largest
+    if (smem > 32 * 1024)
+        err = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, EV_SMEM_TOKENS * (int)sizeof(uint32_t));
     if (err != cudaSuccess) return err;
     err = launch_pdl(select, dim3((unsigned)(B * h_kv)), dim3(EV_THREADS), smem, stream, T_max, h_kv, keep, recent, lengths,
                      weights, kept, weights_out, T_out, status);

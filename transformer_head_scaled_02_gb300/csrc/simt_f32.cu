@@ -509,12 +509,18 @@ cudaError_t launch_attn_f32_tiled(const float* Q, int64_t ldq, const float* K, i
                                   int d_v, int causal, const int32_t* kv_lengths, int* status,
                                   cudaStream_t stream) {
     constexpr int BQ = ft_bq(RQ);
-    const int dk4 = (d_k + 3) & ~3;
-    const size_t smem = sizeof(float) * ((size_t)dk4 * (BQ + FT_PAD) + (size_t)dk4 * (FT_BK + FT_PAD) +
-                                         (size_t)FT_BK * 64 * CV + (size_t)BQ * (FT_BK + FT_PAD));
-    if (smem > 232448) return cudaErrorInvalidValue;
+    auto bytes = [](int dk4) constexpr {
+        return sizeof(float) * ((size_t)dk4 * (BQ + FT_PAD) + (size_t)dk4 * (FT_BK + FT_PAD) + (size_t)FT_BK * 64 * CV +
+                                (size_t)BQ * (FT_BK + FT_PAD));
+    };
+    // The shared-memory limit belongs to the process, where another thread may be launching the kernel for
+    // wider heads: always the largest.
+    constexpr size_t most = bytes(256);
+    static_assert(most <= 232448, "tiles fit shared memory");
+    const size_t smem = bytes((d_k + 3) & ~3);
+    if (smem > most) return cudaErrorInvalidValue;
     auto kernel = attn_f32_tiled_kernel<RQ, CV>;
-    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (err != cudaSuccess) return err;
     const float scale = (float)(1.0 / sqrt((double)d_k));
     const dim3 grid((unsigned)(B * h), (unsigned)((T_q + BQ - 1) / BQ));
@@ -593,9 +599,11 @@ cudaError_t launch_attn_f32(const float* Q, int64_t ldq, const float* K, int64_t
 #undef MHA_FT
     }
     // the decode step (a few new rows over a long cache): 16-row blocks
-    const size_t smem = sizeof(float) * (size_t)(FA_BQ * d_k + FA_BKEY * (d_k + 1) + FA_BKEY * d_v);
-    cudaError_t err = cudaFuncSetAttribute(attn_f32_kernel,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    auto bytes = [](int dk, int dv) constexpr { return sizeof(float) * (size_t)(FA_BQ * dk + FA_BKEY * (dk + 1) + FA_BKEY * dv); };
+    constexpr size_t most = bytes(256, 256);  // (as for the tiles)
+    const size_t smem = bytes(d_k, d_v);
+    if (smem > most) return cudaErrorInvalidValue;
+    cudaError_t err = cudaFuncSetAttribute(attn_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (err != cudaSuccess) return err;
     const float scale = (float)(1.0 / sqrt((double)d_k));
     const dim3 grid((unsigned)(B * h), (unsigned)((T_q + FA_BQ - 1) / FA_BQ));

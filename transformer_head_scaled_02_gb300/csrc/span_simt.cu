@@ -30,6 +30,7 @@ namespace {
 
 constexpr int SS_BK = 64;
 constexpr int SS_THREADS = 256;
+constexpr int SS_DK = 256;  // widest d_k
 constexpr int SS_PS = SS_BK + 4;  // row stride of P
 
 // 16 bytes, or 16 zero bytes, to shared memory.
@@ -51,7 +52,7 @@ struct SimtTile {
     int dk, dk4, dv;
     float m[RQ], l[RQ], o[RQ][4 * CV];
 
-    static size_t smem_bytes(int dk) {
+    static constexpr size_t smem_bytes(int dk) {
         const size_t ks = (size_t)((dk + 3) & ~3) + 4;
         return sizeof(float) * (BQ * ks + SS_BK * ks + (size_t)SS_BK * VS + (size_t)BQ * SS_PS);
     }
@@ -239,6 +240,8 @@ struct SimtTile {
     }
 };
 
+static_assert(SimtTile<4, 4>::smem_bytes(SS_DK) <= 232448, "tiles fit shared memory");
+
 // One block = BQ query rows of one (batch, head): the sinks below the rows' windows, then the keys
 // from the first row's window to the last row.
 template <int RQ, int CV>
@@ -396,8 +399,9 @@ cudaError_t launch_window_f32(const float* Q, int64_t ldq, const float* K, int64
     // 181 | 360 | 888)
     const bool one = cv <= 2 && SimtTile<4, 2>::smem_bytes(d_k) > 113 * 1024;
     const bool small = (int64_t)B * h * ((T + 63) / 64) < 256 || one;
-    auto launch = [&](auto kernel, size_t smem, int bq) {
-        cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // most: what the kernel may ever need.  The limit belongs to the process, so every launch sets the same
+    auto launch = [&](auto kernel, size_t smem, size_t most, int bq) {
+        cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
         if (err != cudaSuccess) return err;
         kernel<<<dim3((unsigned)(B * h), (unsigned)((T + bq - 1) / bq)), SS_THREADS, smem, stream>>>(
             Q, ldq, K, ldk, V, ldv, G, ldg, O, ldo, h, h_kv, T, d_k, d_v, window, sinks, kv_lengths, scale, vec,
@@ -406,7 +410,8 @@ cudaError_t launch_window_f32(const float* Q, int64_t ldq, const float* K, int64
     };
 #define MHA_WS(RQ, CV) \
     if ((small ? 2 : 4) == RQ && cv == CV) \
-        return launch(window_simt_kernel<RQ, CV>, SimtTile<RQ, CV>::smem_bytes(d_k), 16 * RQ);
+        return launch(window_simt_kernel<RQ, CV>, SimtTile<RQ, CV>::smem_bytes(d_k), SimtTile<RQ, CV>::smem_bytes(SS_DK), \
+                      16 * RQ);
     MHA_WS(2, 1) MHA_WS(2, 2) MHA_WS(2, 3) MHA_WS(2, 4) MHA_WS(4, 1) MHA_WS(4, 2) MHA_WS(4, 3) MHA_WS(4, 4)
 #undef MHA_WS
     return cudaErrorInvalidValue;
@@ -421,8 +426,8 @@ cudaError_t launch_span_f32(const SpanShape& p, const SpanRecords& rec, const fl
                      d_v % 4 == 0 && (p.T_p == 0 || (al(Kp) && al(Vp) && ldkp % 4 == 0 && ldvp % 4 == 0));
     const float scale = (float)(1.4426950408889634 / sqrt((double)d_k));
     const int cv = (d_v + 63) / 64;
-    auto launch = [&](auto kernel, size_t smem) {
-        cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    auto launch = [&](auto kernel, size_t smem, size_t most) {  // most: as for the windows
+        cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
         if (err != cudaSuccess) return err;
         return launch_pdl(kernel, dim3((unsigned)ctas), dim3(SS_THREADS), smem, stream, p, rec, Q, ldq, K,
                           ldk, V, ldv, Kp, ldkp, Vp, ldvp, O, ldo, d_k, d_v, lengths, scores, scale, vec,
@@ -430,7 +435,8 @@ cudaError_t launch_span_f32(const SpanShape& p, const SpanRecords& rec, const fl
     };
     const int bm = cache_units ? p.bm_c : p.bm_p;
 #define MHA_SS(RQ, CV) \
-    if (bm == 16 * RQ && cv == CV) return launch(span_simt_kernel<RQ, CV>, SimtTile<RQ, CV>::smem_bytes(d_k));
+    if (bm == 16 * RQ && cv == CV) \
+        return launch(span_simt_kernel<RQ, CV>, SimtTile<RQ, CV>::smem_bytes(d_k), SimtTile<RQ, CV>::smem_bytes(SS_DK));
     MHA_SS(1, 1) MHA_SS(1, 2) MHA_SS(1, 3) MHA_SS(1, 4) MHA_SS(2, 1) MHA_SS(2, 2) MHA_SS(2, 3) MHA_SS(2, 4)
     MHA_SS(4, 1) MHA_SS(4, 2) MHA_SS(4, 3) MHA_SS(4, 4)
 #undef MHA_SS
