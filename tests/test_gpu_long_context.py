@@ -541,6 +541,24 @@ def test_evict_views_of_one_buffer_and_invalid_lengths(in_place):
     assert layer.status() == _lib.MHA_ERR_BAD_LENGTH
 
 
+def test_evict_budget_whose_indices_pass_32_bits():
+    """h_kv * keep beyond 2^31: the kept tokens' indices of the last head lie past every 32-bit offset."""
+    h_kv, T, L = 17, 100, 60
+    keep = 2 ** 27 + 5
+    layer = _layer("f32", h_kv, 1, h_kv, 1)
+    K, V = (to_device(_rand((1, T, h_kv), s, "f32"), "f32") for s in (21, 22))
+    w = to_device(_rand((1, h_kv, T), 23, "f32"), "f32")
+    Ko, Vo = (torch.full((1, keep, h_kv), 5.0, device="cuda") for _ in range(2))
+    wo = torch.full((1, h_kv, keep), 5.0, device="cuda")
+    _, _, lo, _, kept = layer.evict(K, V, _lens([L]), w, keep, 7, K_out=Ko, V_out=Vo, weights_out=wo)
+    assert h_kv * keep > 2 ** 31 and kept.shape == (1, h_kv, keep) and lo.tolist() == [L]
+    assert (kept[0, :, :L] == torch.arange(L, device="cuda")).all() and (kept[0, :, L:] == -1).all()
+    for got, src in ((Ko, K), (Vo, V)):
+        assert torch.equal(got[:, :L], src[:, :L]) and (got[:, L:] == 5).all()
+    assert torch.equal(wo[..., :L], w[..., :L]) and (wo[..., L:] == 5).all()
+    assert layer.status() == 0
+
+
 # ------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("f32", 32)])

@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(MV_THREADS)
             to[r] = -1;
             if (u < total) {
                 const int row = u / upr, c = u - row * upr, g = c / uph;
-                const int from = at[g * keep + i0 + row];
+                const int from = at[(int64_t)g * keep + i0 + row];
                 if (from >= 0) {
                     to[r] = ((int64_t)b * T_out + i0 + row) * s.ld_dst + (int64_t)c * sizeof(UNIT);
                     x[r] = *reinterpret_cast<const UNIT*>(s.src + ((int64_t)b * T_max + from) * s.ld_src + (int64_t)c * sizeof(UNIT));
