@@ -116,6 +116,52 @@ def test_evict_refusals(handles):
     assert call(B=0) == L.MHA_OK
 
 
+def test_row_counts_next_to_32_bits_are_refused(lib):
+    """The kernels step past the last row in 32 bits.  One head of one element: such sizes fit a GPU's memory."""
+    most, G = 2 ** 31 - 2 ** 16, 1 << 38
+    one, many = L.mha_create(1, 1, 1, 1, L.MHA_F32), L.mha_create(1 << 12, 1 << 12, 1, 1, L.MHA_F32)
+    bad = L.MHA_ERR_INVALID_ARG
+    try:
+        def step(name, h=one, T_q=1, T_max=100, ld=1, **kw):
+            a = dict(B=1, T_q=T_q, T_max=T_max, Q=FAKE, ldq=ld, K_cache=FAKE + G, ldk=ld, V_cache=FAKE + 2 * G, ldv=ld,
+                     cache_lengths=FAKE + 8 * G, O=FAKE + 3 * G, ldo=ld, stream=None)
+            a.update(kw)
+            return getattr(L, f"mha_decode_{name}")(h, check=False, **a)
+
+        def window(T):
+            return L.mha_attention_window(one, 1, T, FAKE, 1, FAKE + G, 1, FAKE + 2 * G, 1, None, 0, 8, 0, None, FAKE + 3 * G,
+                                          1, None, check=False)
+
+        def evict(T_max, keep, T_out):
+            return L.mha_cache_evict(one, 1, T_max, keep, 0, FAKE, 1, FAKE + G, 1, FAKE + 8 * G, FAKE + 2 * G, T_out,
+                                     FAKE + 3 * G, 1, FAKE + 4 * G, 1, FAKE + 5 * G, FAKE + 6 * G, FAKE + 7 * G, None,
+                                     check=False)
+        prefix = dict(K_prefix=FAKE + 4 * G, ldkp=1, V_prefix=FAKE + 5 * G, ldvp=1)
+        for n in (most + 1, 2 ** 31 - 1):
+            assert step("window", T_max=n, window=5, sinks=0) == bad
+            assert step("weights", T_max=n, weights=FAKE + 6 * G) == bad
+            assert step("shared", T_max=n, T_prefix=5, **prefix) == bad
+            assert step("shared", T_prefix=n, **prefix) == bad
+            assert window(n) == bad
+            assert evict(n, 10, 10) == bad and evict(100, 10, n) == bad and evict(100, n, n) == bad
+            assert L.mha_cache_step_workspace_size(one, 1, 1, 0, n, 0) == 0
+            assert L.mha_cache_step_workspace_size(one, 1, 1, n, 100, 0) == 0
+        # query rows: 2^12 heads of 2^19 new tokens
+        assert step("window", many, T_q=1 << 19, T_max=1 << 19, ld=1 << 12, window=5, sinks=0) == bad
+        wide = L.mha_create(1, (1 << 23) + 1, 256, 1, L.MHA_F32)
+        n = ((1 << 23) + 1) * 256
+        assert L.mha_cache_evict(wide, 1, 1, 1, 0, FAKE, n, FAKE + G, n, FAKE + 8 * G, FAKE + 2 * G, 1, FAKE + 3 * G, n,
+                                 FAKE + 4 * G, n, FAKE + 5 * G, FAKE + 6 * G, FAKE + 7 * G, None, check=False) == bad
+        L.mha_destroy(wide)
+        # the largest are taken (no workspace is attached)
+        assert step("window", T_max=most, window=5, sinks=0) == L.MHA_ERR_WORKSPACE
+        assert step("shared", T_prefix=most, **prefix) == L.MHA_ERR_WORKSPACE
+        assert window(most) == L.MHA_ERR_UNSUPPORTED         # fp32 windows end at 2097120 tokens
+    finally:
+        L.mha_destroy(one)
+        L.mha_destroy(many)
+
+
 def test_workspace_sizes(handles):
     f = L.mha_cache_step_workspace_size
     assert f(None, 1, 1, 0, 1, 0) == 0 and f(handles["bf"], -1, 1, 0, 1, 0) == 0 and f(handles["bf"], 1, 1, -1, 1, 0) == 0

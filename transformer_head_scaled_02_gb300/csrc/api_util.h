@@ -15,6 +15,10 @@ namespace mha {
 
 constexpr size_t kStatusBytes = 256;
 
+// Most rows (tokens of all batches, query rows) of a long-context call: its kernels count them in 32 bits
+// and step past the last one by up to a scan or a grid.
+constexpr int64_t kMostRows = INT32_MAX - 65535;
+
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

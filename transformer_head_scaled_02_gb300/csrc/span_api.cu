@@ -81,8 +81,8 @@ struct CacheStep {
 
 // Sizes that every cache step shares (the int32 row arithmetic of the kernels).
 bool step_sizes_ok(const mha_s* m, int B, int T_q, int T_p, int T_max) {
-    return B >= 0 && T_q >= 0 && T_p >= 0 && T_max >= 0 && (int64_t)B * T_max <= INT32_MAX &&
-           (int64_t)B * m->h * T_q <= INT32_MAX;
+    return B >= 0 && T_q >= 0 && T_p >= 0 && T_max >= 0 && T_p <= kMostRows && (int64_t)B * T_max <= kMostRows &&
+           (int64_t)B * m->h * T_q <= kMostRows;
 }
 
 mha_status run_cache_step(mha_s* m, const CacheStep& a, cudaStream_t stream) {
@@ -170,7 +170,7 @@ mha_status mha_attention_window(mha_t handle, int B, int T, const void* Q, int64
     const mha_s* m = handle;
     if (m == nullptr) return MHA_ERR_INVALID_ARG;
     if (B < 0 || T < 0 || window < 1 || sinks < 0) return MHA_ERR_INVALID_ARG;
-    if ((int64_t)B * T > INT32_MAX || (int64_t)B * m->h > INT32_MAX) return MHA_ERR_INVALID_ARG;
+    if ((int64_t)B * T > kMostRows || (int64_t)B * m->h > INT32_MAX) return MHA_ERR_INVALID_ARG;
     const mha_status sup = shape_supported(m);
     if (sup != MHA_OK) return sup;
     if (B == 0 || T == 0) return MHA_OK;
@@ -267,7 +267,7 @@ mha_status mha_cache_evict(mha_t handle, int B, int T_max, int keep, int recent,
     const mha_s* m = handle;
     if (m == nullptr) return MHA_ERR_INVALID_ARG;
     if (B < 0 || T_max < 0 || keep < 1 || recent < 0 || recent > keep || T_out < keep) return MHA_ERR_INVALID_ARG;
-    if ((int64_t)B * T_max > INT32_MAX || (int64_t)B * T_out > INT32_MAX || (int64_t)B * m->h_kv > INT32_MAX)
+    if ((int64_t)B * T_max > kMostRows || (int64_t)B * T_out > kMostRows || (int64_t)B * m->h_kv > INT32_MAX)
         return MHA_ERR_INVALID_ARG;
     const mha_status sup = shape_supported(m);
     if (sup != MHA_OK) return sup;
@@ -275,6 +275,7 @@ mha_status mha_cache_evict(mha_t handle, int B, int T_max, int keep, int recent,
     if (B == 0) return MHA_OK;
     if (T_max == 0) return MHA_ERR_INVALID_ARG;
     const Widths wd = widths(m);
+    if (wd.k > kMostRows || wd.v > kMostRows) return MHA_ERR_INVALID_ARG;  // the moves count a row's pieces
     if (cache_lengths == nullptr || weights == nullptr || weights_out == nullptr || kept == nullptr ||
         new_lengths == nullptr)
         return MHA_ERR_INVALID_ARG;
