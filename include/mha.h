@@ -353,8 +353,8 @@ mha_status mha_decode(mha_t handle, int B, int T_q, int T_max, const void* Q, in
 
 /*
  * Long-context operators.  K and V rows of cached or valid tokens (j < L_b) must be finite; rows at or
- * past L_b may hold anything and reach no output.  Sizes: B * T, B * T_max, B * T_out, T_prefix, B * h * T_q and
- * the width of an evicted row are at most 2^31 - 65536 (MHA_ERR_INVALID_ARG otherwise).
+ * past L_b may hold anything and reach no output.  Sizes: B * T, B * T_max, B * T_out, T_prefix and B * h * T_q
+ * are at most 2^31 - 65536 (MHA_ERR_INVALID_ARG otherwise).
  *
  * mha_attention_window -- causal sliding-window attention with sinks for all heads: row i of a sequence
  * sees key j iff j <= i, j < L_b and (i - j < window or j < sinks), so the work grows with T * window

@@ -275,7 +275,6 @@ mha_status mha_cache_evict(mha_t handle, int B, int T_max, int keep, int recent,
     if (B == 0) return MHA_OK;
     if (T_max == 0) return MHA_ERR_INVALID_ARG;
     const Widths wd = widths(m);
-    if (wd.k > kMostRows || wd.v > kMostRows) return MHA_ERR_INVALID_ARG;  // the moves count a row's pieces
     if (cache_lengths == nullptr || weights == nullptr || weights_out == nullptr || kept == nullptr ||
         new_lengths == nullptr)
         return MHA_ERR_INVALID_ARG;
