@@ -148,6 +148,13 @@ def test_row_counts_next_to_32_bits_are_refused(lib):
             assert L.mha_cache_step_workspace_size(one, 1, 1, n, 100, 0) == 0
         # query rows: 2^12 heads of 2^19 new tokens
         assert step("window", many, T_q=1 << 19, T_max=1 << 19, ld=1 << 12, window=5, sinks=0) == bad
+        # the layer refuses what its attention refuses before the projection is launched
+        f = dict(X=FAKE, W_qkv=FAKE + G, b_qkv=None, W_o=FAKE + 2 * G, b_o=None, window=8, sinks=0, kv_lengths=None,
+                 residual=None, out=FAKE + 3 * G, stream=None, check=False)
+        assert most < 2048 * 1048560 < 2 ** 31
+        assert L.mha_forward_window(one, B=2048, T=1048560, **f) == bad
+        assert L.mha_forward_window(one, B=1, T=2097121, **f) == L.MHA_ERR_UNSUPPORTED
+        assert L.mha_forward_window(one, B=2047, T=1048560, **f) == L.MHA_ERR_WORKSPACE
         # the largest are taken (no workspace is attached)
         assert step("window", T_max=most, window=5, sinks=0) == L.MHA_ERR_WORKSPACE
         assert step("shared", T_prefix=most, **prefix) == L.MHA_ERR_WORKSPACE

@@ -69,6 +69,17 @@ mha_status shape_supported(const mha_s* m) {
     return m->dk <= 256 && m->dv <= 256 ? MHA_OK : MHA_ERR_UNSUPPORTED;
 }
 
+// What a window's sizes are refused for, before the layer's projections as well as before the attention.
+mha_status window_supported(const mha_s* m, int B, int T, int window, int sinks) {
+    if (B < 0 || T < 0 || window < 1 || sinks < 0) return MHA_ERR_INVALID_ARG;
+    if ((int64_t)B * T > kMostRows || (int64_t)B * m->h > INT32_MAX) return MHA_ERR_INVALID_ARG;
+    const mha_status sup = shape_supported(m);
+    if (sup != MHA_OK) return sup;
+    const bool fits = m->dtype == MHA_F32 ? ((int64_t)T + 31) / 32 <= 65535
+                                          : (int64_t)B * m->h * (((int64_t)T + 127) / 128) <= INT32_MAX;
+    return fits ? MHA_OK : MHA_ERR_UNSUPPORTED;
+}
+
 struct CacheStep {
     int B, T_q, T_max, T_p, window, sinks;
     const void *Q, *K, *V, *Kp, *Vp;
@@ -169,9 +180,7 @@ mha_status mha_attention_window(mha_t handle, int B, int T, const void* Q, int64
                                 const int32_t* kv_lengths, void* O, int64_t ldo, void* stream) {
     const mha_s* m = handle;
     if (m == nullptr) return MHA_ERR_INVALID_ARG;
-    if (B < 0 || T < 0 || window < 1 || sinks < 0) return MHA_ERR_INVALID_ARG;
-    if ((int64_t)B * T > kMostRows || (int64_t)B * m->h > INT32_MAX) return MHA_ERR_INVALID_ARG;
-    const mha_status sup = shape_supported(m);
+    const mha_status sup = window_supported(m, B, T, window, sinks);
     if (sup != MHA_OK) return sup;
     if (B == 0 || T == 0) return MHA_OK;
     const Widths wd = widths(m);
@@ -189,12 +198,10 @@ mha_status mha_attention_window(mha_t handle, int B, int T, const void* Q, int64
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     cudaError_t err;
     if (m->dtype == MHA_F32) {
-        if ((T + 31) / 32 > 65535) return MHA_ERR_UNSUPPORTED;
         auto f = [](const void* x) { return static_cast<const float*>(x); };
         err = launch_window_f32(f(Q), ldq, f(K), ldk, f(V), ldv, f(G), ldg, static_cast<float*>(O), ldo, B, m->h,
                                 m->h_kv, T, m->dk, m->dv, window, sinks, kv_lengths, status_ptr(m), cs);
     } else {
-        if ((int64_t)B * m->h * ((T + 127) / 128) > INT32_MAX) return MHA_ERR_UNSUPPORTED;
         int sms = 0;
         const mha_status st = query_sms(&sms);
         if (st != MHA_OK) return st;
@@ -208,8 +215,10 @@ mha_status mha_forward_window(mha_t handle, const void* X, int B, int T, const v
                               const void* W_o, const void* b_o, int window, int sinks, const int32_t* kv_lengths,
                               const void* residual, void* out, void* stream) {
     const mha_s* m = handle;
-    if (window < 1 || sinks < 0) return MHA_ERR_INVALID_ARG;
-    mha_status st = check_forward(m, X, nullptr, B, T, T, W_qkv, b_qkv, W_o, b_o, 1, residual, out);
+    if (m == nullptr) return MHA_ERR_INVALID_ARG;
+    mha_status st = window_supported(m, B, T, window, sinks);
+    if (st != MHA_OK) return st;
+    st = check_forward(m, X, nullptr, B, T, T, W_qkv, b_qkv, W_o, b_o, 1, residual, out);
     if (st != MHA_OK) return st;
     if (B == 0 || T == 0) return MHA_OK;
     const WsLayout w = ws_layout(m, B, T, T);
