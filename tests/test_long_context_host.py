@@ -148,6 +148,12 @@ def test_row_counts_next_to_32_bits_are_refused(lib):
             assert L.mha_cache_step_workspace_size(one, 1, 1, n, 100, 0) == 0
         # query rows: 2^12 heads of 2^19 new tokens
         assert step("window", many, T_q=1 << 19, T_max=1 << 19, ld=1 << 12, window=5, sinks=0) == bad
+        # a step whose join would need more blocks than a grid has, before its units are launched
+        heads = L.mha_create(1, 1 << 11, 1, 1, L.MHA_F32)
+        B = (1 << 20) - 40
+        assert step("weights", heads, B=B, T_max=1, ld=1 << 11, weights=FAKE + 6 * G) == L.MHA_ERR_UNSUPPORTED
+        assert step("window", heads, B=B, T_max=1, ld=1 << 11, window=5, sinks=0) == L.MHA_ERR_WORKSPACE
+        L.mha_destroy(heads)
         # the layer refuses what its attention refuses before the projection is launched
         f = dict(X=FAKE, W_qkv=FAKE + G, b_qkv=None, W_o=FAKE + 2 * G, b_o=None, window=8, sinks=0, kv_lengths=None,
                  residual=None, out=FAKE + 3 * G, stream=None, check=False)

@@ -144,6 +144,7 @@ cudaError_t launch_span_bf16(const SpanShape& p, const SpanRecords& rec, const v
                              int64_t ldk, const void* V, int64_t ldv, const void* Kp, int64_t ldkp, const void* Vp,
                              int64_t ldvp, void* O, int64_t ldo, int d, const int32_t* lengths, float* scores,
                              float* weights, int ctas, int* status, cudaStream_t stream);
+int64_t span_merge_blocks(const SpanShape& p, bool weights);
 cudaError_t launch_span_merge(const SpanShape& p, const SpanRecords& rec, int ctas, float* O, int64_t ldo,
                               const int32_t* lengths, const float* scores, float* weights, cudaStream_t stream);
 

@@ -127,6 +127,9 @@ mha_status run_cache_step(mha_s* m, const CacheStep& a, cudaStream_t stream) {
     if (overlaps(a.O, obytes, a.weights, wbytes)) return MHA_ERR_INVALID_ARG;
 
     const SpanShape p = span_shape(m, a.B, a.T_q, a.T_max, a.T_p, a.window, a.sinks);
+    const int64_t most = m->dtype == MHA_F32 ? span_most_tiles<64>(p) : span_most_tiles<128>(p);
+    if (most > INT32_MAX || (m->dtype == MHA_F32 && span_merge_blocks(p, a.weights != nullptr) > INT32_MAX))
+        return MHA_ERR_UNSUPPORTED;
     const SpanLayout w = layout(m, p, a.weights != nullptr);
     if (m->ws == nullptr || m->ws_bytes < kStatusBytes + w.total) return MHA_ERR_WORKSPACE;
     uint8_t* ws = static_cast<uint8_t*>(m->ws) + kStatusBytes;
@@ -142,8 +145,6 @@ mha_status run_cache_step(mha_s* m, const CacheStep& a, cudaStream_t stream) {
     // one CTA per SM holds the tensor-core kernel's tiles, two the CUDA-core kernel's
     int ctas = m->dtype == MHA_F32 ? 2 * sms : sms;
     if (ctas > kSpanMaxCtas) ctas = kSpanMaxCtas;
-    const int64_t most = m->dtype == MHA_F32 ? span_most_tiles<64>(p) : span_most_tiles<128>(p);
-    if (most > INT32_MAX) return MHA_ERR_UNSUPPORTED;
     if (most < ctas) ctas = (int)most;
     cudaError_t err;
     if (m->dtype == MHA_F32) {

@@ -115,12 +115,14 @@ __global__ void __launch_bounds__(SM_THREADS)
 
 }  // namespace
 
+int64_t span_merge_blocks(const SpanShape& p, bool weights) {
+    const int64_t out_rows = (int64_t)p.B * p.per * p.h_kv * p.T_q;
+    return out_rows + (weights ? (int64_t)p.B * p.h_kv * ((p.T_max + SM_KEYS - 1) / SM_KEYS) : 0);
+}
+
 cudaError_t launch_span_merge(const SpanShape& p, const SpanRecords& rec, int ctas, float* O, int64_t ldo,
                               const int32_t* lengths, const float* scores, float* weights, cudaStream_t stream) {
-    const int64_t out_rows = (int64_t)p.B * p.per * p.h_kv * p.T_q;
-    const int64_t blocks =
-        out_rows + (weights != nullptr ? (int64_t)p.B * p.h_kv * ((p.T_max + SM_KEYS - 1) / SM_KEYS) : 0);
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    const int64_t blocks = span_merge_blocks(p, weights != nullptr);  // (the caller has checked that they are a grid)
     auto kernel = weights != nullptr ? span_merge_kernel<true> : span_merge_kernel<false>;
     return launch_pdl(kernel, dim3((unsigned)blocks), dim3(SM_THREADS), 0, stream, p, rec, ctas, O, ldo, lengths,
                       scores, weights);
