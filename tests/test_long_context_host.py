@@ -334,3 +334,13 @@ def test_workspace_used_on_another_stream_is_recorded_there(lib, monkeypatch):
     now[0] = 1
     layer.ensure_workspace(1, 1, 1, need=5000)
     assert recorded[2:] == [(layer._ws.data_ptr(), 1)] and old is not layer._ws
+
+
+def test_remembered_workspace_sizes_are_bounded(lib):
+    torch = pytest.importorskip("torch")
+    from transformer_head_scaled_02_gb300 import Mha
+    layer = Mha(256, 4, 64, dtype=torch.bfloat16, h_kv=2, device="cpu")
+    for again in range(2):
+        for Tp in range(1000):
+            assert layer._step_need(3, 1, 64 * Tp, 500, 0) == L.mha_cache_step_workspace_size(layer.handle, 3, 1, 64 * Tp, 500, 0)
+    assert len(layer._step_bytes) <= 64

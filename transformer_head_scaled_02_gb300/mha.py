@@ -388,6 +388,15 @@ class Mha:
                                   ldv, _ptr(G), ldg, window, sinks, lens, out.data_ptr(), ldo, stream)
         return out
 
+    def _step_need(self, *sizes: int) -> int:
+        """mha_cache_step_workspace_size, remembered for the sizes at hand."""
+        need = self._step_bytes.get(sizes)
+        if need is None:
+            if len(self._step_bytes) >= 64:  # (a prefix length that varies would fill it without end)
+                self._step_bytes.clear()
+            need = self._step_bytes[sizes] = _lib.mha_cache_step_workspace_size(self.handle, *sizes)
+        return need
+
     def _cache_step(self, Q, K_cache, V_cache, cache_lengths, out, T_prefix, weights, *others):
         """Checks and workspace that the cache steps share: (out, the arguments they have in common)."""
         B, T_q, _ = Q.shape
@@ -400,11 +409,7 @@ class Mha:
         ldo = self._rows("out", out, B, T_q, self.h * self.d_v)
         lens = self._ints("cache_lengths", cache_lengths, B)
         stream = self._device(Q, K_cache, V_cache, cache_lengths, out, *others)
-        key = (B, T_q, T_prefix, T_max, weights)
-        need = self._step_bytes.get(key)
-        if need is None:
-            need = _lib.mha_cache_step_workspace_size(self.handle, *key)
-            self._step_bytes[key] = need
+        need = self._step_need(B, T_q, T_prefix, T_max, weights)
         self.ensure_workspace(B, T_q, T_max, need=need)
         cache = (Q.data_ptr(), ldq, K_cache.data_ptr(), ldk, V_cache.data_ptr(), ldv)
         return out, (B, T_q, T_max), cache, lens, (out.data_ptr(), ldo, stream)
