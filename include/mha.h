@@ -125,11 +125,19 @@ mha_status mha_set_workspace(mha_t handle, void* dev_ptr, size_t bytes);
 /*
  * mha_set_workspace_on -- mha_set_workspace whose zeros are queued on `stream`,
  * behind the work that is already there, without waiting: the handle's next calls
- * must be on that stream or ordered behind it.  If `stream` is being captured the
- * zeros come with the graph's replays, and only calls of that graph may use the
- * workspace until another one is attached.
+ * must be on that stream or ordered behind it.  MHA_ERR_INVALID_ARG if `stream` is
+ * being captured: the zeros would come with the graph's replays instead of now.
  */
 mha_status mha_set_workspace_on(mha_t handle, void* dev_ptr, size_t bytes, void* stream);
+
+/*
+ * mha_exchange_capture_mode -- cudaThreadExchangeStreamCaptureMode of this library's CUDA
+ * runtime: which CUDA calls the calling thread may make while a stream is being captured
+ * (0 global, 1 thread-local, 2 relaxed).  *mode is the new mode and receives the old one.
+ * For a caller that has to allocate a workspace, and to wait for its zeros on another
+ * stream, in the middle of a capture.
+ */
+mha_status mha_exchange_capture_mode(int32_t* mode);
 
 /*
  * mha_forward -- Y = MultiHead(X_q, X_kv) for the whole batch.

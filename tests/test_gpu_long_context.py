@@ -873,10 +873,12 @@ def test_workspace_attached_under_capture(dtype, d):
         torch.full((1 << 22,), 1, dtype=torch.uint8, device="cuda")
         for (t, lens, _, w, *_), out in zip(cases, outs):
             layer.decode_weights(*t, lens, w, out=out)
+    ws = layer._ws
     for turn in range(3):
         for (t, lens, lengths, w, ref, A, W), out in zip(cases, outs):
             w.zero_()
             _check(to_host(layer.decode_weights(*t, lens, w)), ref, A, dtype, "eager")
+            assert layer._ws is ws
             out.zero_()
             w.zero_()
         g.replay()
@@ -1110,4 +1112,31 @@ def test_status_resets_what_a_timed_out_step_left(code, d):
         _check(to_host(layer.decode_weights(*t, lens, w)), ref, A, "bf16", "after an error")
         for b, n in enumerate(lengths):
             _check_weights(to_host(w)[b, :, :n], W[b, :, :n], "after an error")
+    assert layer.status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_status_of_replays_is_kept(dtype):
+    """An error of one replay is there to read after later ones, in a workspace attached under capture too."""
+    h, h_kv, d, B, T = 4, 2, 64, 2, 300
+    Q, K, V = _cache(950, dtype, B, 1, T, h, h_kv, d, d)
+    t, lens = [to_device(x, dtype) for x in (Q, K, V)], _lens([T, 100])
+    _layer(dtype, h, d, h_kv).decode_window(*t, lens, 50)
+    torch.cuda.synchronize()
+    for _ in range(40):  # from whichever of torch's streams comes next, the capture's own among them
+        layer = _layer(dtype, h, d, h_kv)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            torch.full((1 << 22,), 1, dtype=torch.uint8, device="cuda")  # a temporary, where its pool may hand out memory
+            out = layer.decode_window(*t, lens, 50)
+    ref, A, _ = lc.decode(Q, K, V, h, [T, 100], h_kv, 50)
+    for bad in (False, True, False, False):
+        lens.copy_(_lens([T, T + 1 if bad else 100]))
+        g.replay()
+        got = to_host(out)
+        assert np.isnan(got[1]).all() == bad
+        _check(got[:1], ref[:1], A[:1], dtype, "replayed")
+    assert layer.status() == _lib.MHA_ERR_BAD_LENGTH and layer.status() == 0
+    g.replay()
+    _check(to_host(out), ref, A, dtype, "replayed")
     assert layer.status() == 0

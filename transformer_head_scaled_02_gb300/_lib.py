@@ -25,6 +25,8 @@ MHA_ERR_CUDA = 4
 MHA_ERR_TIMEOUT = 5
 MHA_ERR_BAD_LENGTH = 6
 
+CAPTURE_RELAXED = 2  # mha_exchange_capture_mode
+
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _i64 = ctypes.c_int64
@@ -37,6 +39,7 @@ _SIGNATURES = {
     "mha_workspace_size": (_sz, [_vp, _i, _i, _i]),
     "mha_set_workspace": (_i, [_vp, _vp, _sz]),
     "mha_set_workspace_on": (_i, [_vp, _vp, _sz, _vp]),
+    "mha_exchange_capture_mode": (_i, [ctypes.POINTER(ctypes.c_int32)]),
     "mha_forward": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp]),
     "mha_forward_checked": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp]),
     "mha_forward_ex": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp]),
@@ -144,6 +147,12 @@ def mha_set_workspace(handle: int, dev_ptr: int, nbytes: int) -> int:
 def mha_set_workspace_on(handle: int, dev_ptr: int, nbytes: int, stream: int, check: bool = True) -> int:
     code = load().mha_set_workspace_on(handle, dev_ptr, nbytes, stream)
     return _check("mha_set_workspace_on", code) if check else code
+
+
+def mha_exchange_capture_mode(mode: int) -> int:
+    v = ctypes.c_int32(mode)
+    _check("mha_exchange_capture_mode", load().mha_exchange_capture_mode(ctypes.byref(v)))
+    return v.value
 
 
 def mha_forward(handle, X_q, X_kv, B, T_q, T_kv, W_qkv, b_qkv, W_o, b_o, causal, kv_lengths,

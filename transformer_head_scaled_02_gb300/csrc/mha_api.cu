@@ -299,6 +299,16 @@ mha_status mha_set_workspace(mha_t handle, void* dev_ptr, size_t bytes) {
     return st;
 }
 
+mha_status mha_exchange_capture_mode(int32_t* mode) {
+    if (mode == nullptr || *mode < 0 || *mode > 2) return MHA_ERR_INVALID_ARG;
+    cudaStreamCaptureMode m = *mode == 0   ? cudaStreamCaptureModeGlobal
+                              : *mode == 1 ? cudaStreamCaptureModeThreadLocal
+                                           : cudaStreamCaptureModeRelaxed;
+    if (cudaThreadExchangeStreamCaptureMode(&m) != cudaSuccess) return MHA_ERR_CUDA;
+    *mode = m == cudaStreamCaptureModeGlobal ? 0 : m == cudaStreamCaptureModeThreadLocal ? 1 : 2;
+    return MHA_OK;
+}
+
 mha_status mha_set_workspace_on(mha_t handle, void* dev_ptr, size_t bytes, void* stream) {
     if (handle == nullptr) return MHA_ERR_INVALID_ARG;
     if (dev_ptr == nullptr) {
@@ -308,10 +318,13 @@ mha_status mha_set_workspace_on(mha_t handle, void* dev_ptr, size_t bytes, void*
     }
     if ((reinterpret_cast<uintptr_t>(dev_ptr) & 255u) != 0 || bytes < kStatusBytes)
         return MHA_ERR_INVALID_ARG;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(cs, &capture) != cudaSuccess) return MHA_ERR_CUDA;
+    if (capture != cudaStreamCaptureStatusNone) return MHA_ERR_INVALID_ARG;
     // In the order of the stream the kernels will run on: the counters of the block decide what a cache
     // step computes, and zeros on any other stream need not be there before it.
-    if (cudaMemsetAsync(dev_ptr, 0, kStatusBytes, static_cast<cudaStream_t>(stream)) != cudaSuccess)
-        return MHA_ERR_CUDA;
+    if (cudaMemsetAsync(dev_ptr, 0, kStatusBytes, cs) != cudaSuccess) return MHA_ERR_CUDA;
     if (handle->aux_dev < 0) {
         const mha_status st = create_aux(handle);
         if (st != MHA_OK) return st;

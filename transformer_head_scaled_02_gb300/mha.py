@@ -51,7 +51,6 @@ class Mha:
                                          _DTYPES[dtype])
         self._ws: Optional[torch.Tensor] = None
         self._ws_captured = False
-        self._ws_of_graph = False
         self._ws_streams: set = set()  # streams that the allocator knows to use the workspace
         self._kept_ws: list = []
         self._step_bytes: dict = {}  # workspace bytes of the cache steps, by their sizes
@@ -75,29 +74,46 @@ class Mha:
     def ensure_workspace(self, B: int, T_q: int, T_kv: int, need: Optional[int] = None) -> torch.Tensor:
         need = self.workspace_size(B, T_q, T_kv) if need is None else need
         capturing = torch.cuda.is_current_stream_capturing()
-        if self._ws is None or self._ws.numel() < need or (self._ws_of_graph and not capturing):
+        if self._ws is None or self._ws.numel() < need:
             if self._ws_captured:  # a captured graph still launches into the one it was captured with
                 self._kept_ws.append(self._ws)
-            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
-            # its status block, with the counters of the cache steps, is zeroed in the order of the
-            # current stream: that is where the memory comes from and where the call goes
-            _lib.mha_set_workspace_on(self.handle, ws.data_ptr(), ws.numel(), _stream())
-            self._ws = ws
-            # under capture the memory is the graph's and the zeros come with its replays: eager calls
-            # get a workspace of their own
-            self._ws_captured = self._ws_of_graph = capturing
-            self._ws_streams = {_stream()}
-        elif capturing:
+                self._ws_captured = False
+            self._ws, home = (self._new_workspace_in_capture if capturing else self._new_workspace)(max(need, 256))
+            self._ws_streams = {home}
+        if capturing:
             self._ws_captured = True
-            if self._ws_of_graph:
-                # this may be another graph of the pool, whose memory they all write to: the counters
-                # start from zero in every call
-                self._ws[4:256].zero_()
         elif _stream() not in self._ws_streams:
             # calls on this stream may still be under way when a larger workspace replaces it
             self._ws.record_stream(torch.cuda.current_stream())
             self._ws_streams.add(_stream())
         return self._ws
+
+    def _new_workspace(self, nbytes: int):
+        """A workspace, attached, and the stream it belongs to: the current one, in whose order its status
+        block (with the counters of the cache steps) is zeroed, as the memory comes from there and the call
+        goes there."""
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        _lib.mha_set_workspace_on(self.handle, ws.data_ptr(), nbytes, _stream())
+        return ws, _stream()
+
+    def _new_workspace_in_capture(self, nbytes: int):
+        """The same while a graph is being captured: neither the memory nor the zeros may be the graph's.  It
+        writes its temporaries over memory of its own at every replay, and eager calls may come before the
+        first.  So both come from another stream, and the zeros are waited for."""
+        mode = _lib.mha_exchange_capture_mode(_lib.CAPTURE_RELAXED)
+        try:
+            while True:  # torch gives out a few streams in turn, those under capture among them
+                side = torch.cuda.Stream()
+                with torch.cuda.stream(side):
+                    if torch.cuda.is_current_stream_capturing():
+                        continue
+                    ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+                    _lib.mha_set_workspace_on(self.handle, ws.data_ptr(), nbytes, side.cuda_stream)
+                break
+            side.synchronize()
+        finally:
+            _lib.mha_exchange_capture_mode(mode)
+        return ws, side.cuda_stream
 
     def status(self) -> int:
         """Read and clear the device status word, and reset what a step that timed out may have left in
