@@ -459,7 +459,8 @@ mha_status mha_decode_weights(mha_t handle, int B, int T_q, int T_max, const voi
  *   new_lengths    device int32[B]: min(L_b, keep); may be cache_lengths
  * 1 <= keep, 0 <= recent <= keep.  With recent >= T_q the next decode steps' rule that the new tokens
  * are the last ones holds.  K and V may be column views of one buffer.  Needs no workspace (one that is
- * attached receives the status).  bf16: B <= 65535, d_k == d_v in {64, 128}, strides multiples of 8 and
+ * attached receives the status).  B <= 65535; into new buffers h_kv * keep < 2^32 (MHA_ERR_UNSUPPORTED
+ * otherwise).  bf16: d_k == d_v in {64, 128}, strides multiples of 8 and
  * 16-byte aligned pointers.  Two launches.
  */
 mha_status mha_cache_evict(mha_t handle, int B, int T_max, int keep, int recent, const void* K_cache,

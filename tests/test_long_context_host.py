@@ -148,6 +148,12 @@ def test_row_counts_next_to_32_bits_are_refused(lib):
             assert L.mha_cache_step_workspace_size(one, 1, 1, n, 100, 0) == 0
         # query rows: 2^12 heads of 2^19 new tokens
         assert step("window", many, T_q=1 << 19, T_max=1 << 19, ld=1 << 12, window=5, sinks=0) == bad
+        # indices of kept tokens past 2^32: into new buffers only
+        wide = dict(cache_lengths=FAKE + 8 * G, T_out=1 << 20, ldko=1 << 12, ldvo=1 << 12, kept=FAKE + 6 * G,
+                    new_lengths=FAKE + 7 * G, stream=None, check=False)
+        assert L.mha_cache_evict(many, 1, 100, 1 << 20, 0, FAKE, 1 << 12, FAKE + G, 1 << 12, weights=FAKE + 2 * G,
+                                 K_out=FAKE + 3 * G, V_out=FAKE + 4 * G, weights_out=FAKE + 5 * G,
+                                 **wide) == L.MHA_ERR_UNSUPPORTED
         # a step whose join would need more blocks than a grid has, before its units are launched
         heads = L.mha_create(1, 1 << 11, 1, 1, L.MHA_F32)
         B = (1 << 20) - 40

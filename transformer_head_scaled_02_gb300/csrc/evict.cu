@@ -256,7 +256,9 @@ __global__ void __launch_bounds__(MV_THREADS)
             to[r] = -1;
             if (u < total) {
                 const int row = u / upr, c = u - row * upr, g = c / uph;
-                const int from = at[(int64_t)g * keep + i0 + row];
+                // (unsigned: h_kv * keep may pass 2^31, but not 2^32, which the host checks; a 64-bit product takes
+                // the kernel from 64 to 67 registers, from four blocks an SM to three, and 211 us to 233)
+                const int from = at[(uint32_t)g * (uint32_t)keep + (uint32_t)(i0 + row)];
                 if (from >= 0) {
                     to[r] = ((int64_t)b * T_out + i0 + row) * s.ld_dst + (int64_t)c * sizeof(UNIT);
                     x[r] = *reinterpret_cast<const UNIT*>(s.src + ((int64_t)b * T_max + from) * s.ld_src + (int64_t)c * sizeof(UNIT));

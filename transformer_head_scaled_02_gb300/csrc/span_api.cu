@@ -298,6 +298,7 @@ mha_status mha_cache_evict(mha_t handle, int B, int T_max, int keep, int recent,
         if (V_out != V_cache || weights_out != weights || T_out != T_max || ldko != ldk || ldvo != ldv)
             return MHA_ERR_INVALID_ARG;
     }
+    if (!in_place && (int64_t)m->h_kv * keep > UINT32_MAX) return MHA_ERR_UNSUPPORTED;
     const int64_t ni = (int64_t)B * T_max, no = (int64_t)B * T_out;
     struct Span {
         const void* p;
