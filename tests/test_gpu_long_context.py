@@ -541,6 +541,32 @@ def test_evict_views_of_one_buffer_and_invalid_lengths(in_place):
     assert layer.status() == _lib.MHA_ERR_BAD_LENGTH
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("f32", 6)])
+@pytest.mark.parametrize("shared", ["outputs", "all"])
+def test_evict_into_column_views(dtype, d, shared):
+    """K_out and V_out as columns of one buffer, or of the buffer that the caches are columns of."""
+    h_kv, B, T, keep, recent = 2, 3, 500, 120, 20
+    w_, lengths = h_kv * d, [500, 119, 301]
+    buf = to_device(_rand((B, T, 4 * w_), 31, dtype), dtype)
+    K, V = buf[..., :w_], buf[..., w_:2 * w_]
+    out = buf if shared == "all" else torch.full((B, keep + 9, 4 * w_), 5.0, dtype=torch_dtype(dtype), device="cuda")
+    Ko, Vo = out[..., 2 * w_:3 * w_], out[..., 3 * w_:]
+    before, src = to_host(out), to_host(buf)
+    w = np.random.default_rng(3).random((B, h_kv, T)).astype(np.float32)
+    layer = _layer(dtype, h_kv, d, h_kv)
+    wo = torch.zeros((B, h_kv, out.shape[1]), device="cuda")
+    layer.evict(K, V, _lens(lengths), torch.tensor(w, device="cuda"), keep, recent, K_out=Ko, V_out=Vo, weights_out=wo)
+    ref, got = lc.evict(w, lengths, keep, recent), to_host(out)
+    for b, g in itertools.product(range(B), range(h_kv)):
+        n, at = len(ref[b][g]), ref[b][g]
+        for i in range(2):
+            c = slice((2 + i) * w_ + g * d, (2 + i) * w_ + (g + 1) * d)
+            f = slice(i * w_ + g * d, i * w_ + (g + 1) * d)
+            assert (got[b, :n, c] == src[b, at, f]).all() and (got[b, n:, c] == before[b, n:, c]).all()
+    assert (got[..., :2 * w_] == before[..., :2 * w_]).all()
+    assert layer.status() == 0
+
+
 def test_evict_budget_whose_indices_pass_32_bits():
     """h_kv * keep beyond 2^31: the kept tokens' indices of the last head lie past every 32-bit offset."""
     h_kv, T, L = 17, 100, 60
