@@ -142,7 +142,8 @@ mha_status run_cache_step(mha_s* m, const CacheStep& a, cudaStream_t stream) {
     int sms = 0;
     const mha_status st = query_sms(&sms);
     if (st != MHA_OK) return st;
-    // one CTA per SM holds the tensor-core kernel's tiles, two the CUDA-core kernel's
+    // one CTA per SM holds the tensor-core kernel's tiles, two mostly the CUDA-core tiles (span_simt.cu); of the
+    // few-row kernel and of 64-row tiles at d = 128 an SM holds one, and the second takes its turn
     int ctas = m->dtype == MHA_F32 ? 2 * sms : sms;
     if (ctas > kSpanMaxCtas) ctas = kSpanMaxCtas;
     if (most < ctas) ctas = (int)most;

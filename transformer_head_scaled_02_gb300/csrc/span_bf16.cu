@@ -17,12 +17,16 @@
 // room until these CTAs end, and the next step's CTAs none until they are gone.  Code that runs once per
 // CTA is kept short throughout: it is fetched from L2 every time.
 //
-// Measured: 32 caches of up to 8192 tokens, 16 K/V heads of d = 128, window 4096 (1.08 GB) 167 us, 96 % of the
-// measured copy rate; 4 K/V heads with weights (409 MB) 84 us, 73 %; 64 caches of up to 1024 tokens behind a
-// prefix of 32768, 4 query heads each on 4 K/V heads, 62 us; one cache of 1004 visible tokens 12 us.  Short units
+// The softmax weights are rounded to bf16 for the value product, as the tensor cores take them, by at most 2^-8
+// of themselves; the row sums are of the fp32 values, and records, joins and accumulated weights stay fp32.
+//
+// Measured in a captured graph | in a loop of calls: 32 caches of up to 8192 tokens, 16 K/V heads of d = 128,
+// window 4096 (1.08 GB) 167 | 169 us, 96 | 95 % of the measured copy rate; 4 K/V heads with weights (409 MB)
+// 84 | 89 us, 73 | 69 %; 64 caches of up to 1024 tokens behind a prefix of 32768, 4 query heads each on 4 K/V
+// heads, 62 | 65 us; one cache of 1004 visible tokens 12 | 14 us.  Short units
 // cost most beside HBM: between two units a stream waits for the last value product and reads the sums, about
 // 2 us.  The roles' loops share the instruction cache: with several copies of the score product and of the
-// tile loads the same four took 177, 99, 68 and 12 us.  Slower, too: a unit's end behind the next unit's first
+// tile loads the same four took 177, 99, 68 and 12 us in a graph.  Slower, too: a unit's end behind the next unit's first
 // softmax, few query rows twice in the tile for the two streams to run on two warp schedulers, boxes of 32 rows.
 //
 // Tensor memory (512 columns): S_t at 128 t (P_t overwrites its first 64 columns), O_t at 256 + HD t.

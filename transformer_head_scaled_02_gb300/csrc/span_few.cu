@@ -1,7 +1,7 @@
 // span_few.cu -- the units of the fp32 cache steps (span.cuh) with few query rows: bound by HBM, so keys and
 // values go straight from global memory to registers, once, in pieces of 16 bytes.
 //
-// A block is one unit; its 8 warps take 32 keys at a time in turn, each with its own running maximum, sum and
+// A block takes a unit at a time; its 8 warps take 32 keys at a time in turn, each with its own running maximum, sum and
 // values, joined at the unit's end.  16 lanes hold a key (4 of its elements per lane and chunk of 64), so a warp
 // reads two keys with one load.  A row's 16 partial products per lane meet by halving: in each of four steps a
 // lane hands over the half of its keys that the other half of the lanes ends up with, 15 shuffles for
@@ -10,7 +10,8 @@
 // Units are multiples of 4 tiles where there are enough keys, so that no warp idles: with 2 tiles a unit the
 // same work took twice as long.
 //
-// Bound by HBM latency: a warp has 8 KB in flight and waits for K before V.  16 caches of 4096 tokens, 4 K/V
+// Bound by HBM latency: 179 to 255 registers leave one block an SM, whose warps have 8 KB in flight each and wait
+// for K before V.  16 caches of 4096 tokens, 4 K/V
 // heads, one row: d = 64 40 us (134 MB, 50 % of the measured copy rate; in tiles, span_simt.cu, 106), d = 128
 // 63 us (64 %; 170), d = 256 242 us (33 %; 356).
 #include <math.h>

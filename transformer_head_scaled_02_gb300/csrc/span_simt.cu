@@ -11,7 +11,8 @@
 // warp apart by d_k + 4 floats) touch every bank once.  One K and one V tile: the next K comes in behind
 // the score product, the next V behind the value product, each under the other half of the work.
 //
-// Bound by the issue of FMAs and the waits between the halves (two blocks an SM).  Measured with asynchronous
+// Bound by the issue of FMAs and the waits between the halves (two blocks an SM, one where shared memory holds no
+// more: 64 rows of d = 128).  Measured with asynchronous
 // copies and packed score products | with plain loads of both tiles before a step: window of 256 over 2 x 8
 // heads x 2048 rows, d = 64 98 | 112 us (36 % of the FMA rate), d = 128 218 (200 in 32-row blocks) | 306, d = 256
 // 360 | 548; weights of 16 caches of 4096 tokens, 4 K/V heads, 20 rows of d = 64 180 | 227, 64 rows of d = 128

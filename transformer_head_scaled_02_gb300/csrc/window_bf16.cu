@@ -13,8 +13,11 @@
 // window, come last and even out the CTAs (numbered the other way, 16 heads of 16384 rows took 219 us for
 // 205, with the tensor pipes of the SMs busy for 51 to 70 % of the time).
 //
-// Measured: 16 heads x 16384 rows, d = 128, window 2048: 192 us, 69 % of the measured bf16 rate (260 GF: only the
-// visible pairs count), bound by the chain score product, softmax, value product of each query tile with two
+// P is rounded to bf16 for the value product, as the tensor cores take it, by at most 2^-8 of itself; the row sums
+// are of the fp32 values.
+//
+// Measured: 16 heads x 16384 rows, d = 128, window 2048: 192 to 200 us in a captured graph, 66 to 69 % of the measured
+// bf16 rate (260 GF: only the visible pairs count), 208 us in a loop of calls; bound by the chain score product, softmax, value product of each query tile with two
 // in flight.  4 x 16 heads x 2048 rows, d = 64, window 256: 32 us; most of its tiles are cut by a mask and a
 // CTA has three items.  P in columns of its own (d = 64 has room) took 45 us where this took 41, masks kept in
 // registers no less than in the scores.
