@@ -1166,3 +1166,45 @@ def test_status_of_replays_is_kept(dtype):
     g.replay()
     _check(to_host(out), ref, A, dtype, "replayed")
     assert layer.status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("op", ["attention", "linear", "linear_segments", "linear_pair"])
+def test_single_steps_hold_the_status_word(dtype, op):
+    """The layer's single steps use an attached workspace's status word: a captured one stays theirs, and the
+    allocator knows of the stream."""
+    h, d, B, T = 4, 64, 2, 128
+    layer = _layer(dtype, h, d, h)
+    x = [to_device(_rand((B, T, h * d), s, dtype), dtype) for s in (51, 52, 53)]
+    W, rows = to_device(_rand((h * d, h * d), 54, dtype), dtype), x[0].view(B * T, h * d)
+    lens = _lens([T, T + 1])  # the second is invalid
+
+    def call():
+        if op == "attention":
+            return layer.attention(*x, kv_lengths=lens)
+        if op == "linear":
+            return layer.linear(rows, W)
+        if op == "linear_segments":
+            return layer.linear_segments(rows, W, None, _lens_ok, T)
+        return layer.linear_pair(rows, W, None, rows, W, None)
+    _lens_ok = _lens([T, 50])
+    call()                                                   # none attached: no status, no workspace
+    assert layer._ws is None
+    layer.ensure_workspace(0, 0, 0, need=256)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    assert side.cuda_stream in layer._ws_streams
+    torch.cuda.synchronize()
+    assert layer.status() == (_lib.MHA_ERR_BAD_LENGTH if op == "attention" else 0)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    old = layer._ws
+    layer.ensure_workspace(0, 0, 0, need=1 << 20)
+    assert layer._ws is not old and any(w is old for w in layer._kept_ws)
+    g.replay()
+    torch.cuda.synchronize()
+    assert int(old[:4].view(torch.int32).item()) == (_lib.MHA_ERR_BAD_LENGTH if op == "attention" else 0)
+    assert layer.status() == 0

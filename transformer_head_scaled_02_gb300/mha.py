@@ -115,6 +115,12 @@ class Mha:
             _lib.mha_exchange_capture_mode(mode)
         return ws, side.cuda_stream
 
+    def _hold_status(self) -> None:
+        """For calls that use an attached workspace for its status word alone: it has to outlive them, and the
+        graphs that they are captured in, too."""
+        if self._ws is not None:
+            self.ensure_workspace(0, 0, 0, need=256)
+
     def status(self) -> int:
         """Read and clear the device status word, and reset what a step that timed out may have left in
         the workspace's counters (synchronises the current stream)."""
@@ -222,6 +228,7 @@ class Mha:
             if not t.is_cuda or t.dtype != self.dtype or t.stride(1) != 1:
                 raise ValueError(f"{name} must be a row-major {self.dtype} CUDA matrix")
         self._check("bias", bias, None if bias is None else (N,))
+        self._hold_status()
         _lib.mha_linear_ex(self.handle, _ptr(A), A.stride(0), M, K, _ptr(W), W.stride(0), N,
                            _ptr(bias), _ptr(residual), 0 if residual is None else residual.stride(0),
                            _ptr(out), out.stride(0), _stream())
@@ -243,6 +250,7 @@ class Mha:
         self._check("bias", bias, None if bias is None else (N,))
         if seg_len.dtype != torch.int32 or not seg_len.is_cuda:
             raise ValueError("seg_len must be a CUDA int32 tensor")
+        self._hold_status()
         _lib.mha_linear_segments(self.handle, _ptr(A), A.stride(0), M, K, _ptr(W), W.stride(0), N,
                                  _ptr(bias), _ptr(seg_len), seg_rows, _ptr(out), out.stride(0),
                                  _stream())
@@ -272,6 +280,7 @@ class Mha:
         self._check("bias2", bias2, None if bias2 is None else (N2,))
         if seg_len is not None and (seg_len.dtype != torch.int32 or not seg_len.is_cuda):
             raise ValueError("seg_len must be a CUDA int32 tensor")
+        self._hold_status()
         _lib.mha_linear_pair(self.handle, _ptr(A), A.stride(0), M, _ptr(W), W.stride(0), N, _ptr(bias),
                              _ptr(seg_len), seg_rows, _ptr(out), out.stride(0), _ptr(A2), A2.stride(0),
                              M2, _ptr(W2), W2.stride(0), N2, _ptr(bias2), _ptr(out2), out2.stride(0), K,
@@ -297,6 +306,7 @@ class Mha:
             out = torch.empty((B, T_q, self.h * self.d_v), dtype=self.dtype, device=Q.device)
         if kv_lengths is not None and (kv_lengths.dtype != torch.int32 or not kv_lengths.is_cuda):
             raise ValueError("kv_lengths must be a CUDA int32 tensor")
+        self._hold_status()
         _lib.mha_attention_ex(self.handle, B, T_q, T_kv, _ptr(Q), Q.stride(1), _ptr(K), K.stride(1),
                               _ptr(V), V.stride(1), _ptr(G), 0 if G is None else G.stride(1), causal,
                               _ptr(kv_lengths), _ptr(out), out.stride(1), _stream())
@@ -398,8 +408,7 @@ class Mha:
         ldg = 0 if G is None else self._rows("G", G, B, T, self.h * self.d_v)
         lens = None if kv_lengths is None else self._ints("kv_lengths", kv_lengths, B)
         stream = self._device(Q, K, V, out, G, kv_lengths)
-        if self._ws is not None:
-            self.ensure_workspace(0, 0, 0, need=256)  # its status word is the kernel's, a captured one's too
+        self._hold_status()
         _lib.mha_attention_window(self.handle, B, T, Q.data_ptr(), ldq, K.data_ptr(), ldk, V.data_ptr(),
                                   ldv, _ptr(G), ldg, window, sinks, lens, out.data_ptr(), ldo, stream)
         return out
