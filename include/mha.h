@@ -470,6 +470,71 @@ mha_status mha_cache_evict(mha_t handle, int B, int T_max, int keep, int recent,
                            void* stream);
 
 /*
+ * Quantised key/value caches.  Decoding reads the whole cache (mha_decode), so a cache of 4 or 8 bits a value is
+ * as much faster to attend over as it is smaller.  Per (batch, K/V head, token) it holds the codes of the head's
+ * d channels and, for each group of 64 channels (the last of a head may be shorter), a step s and a lowest value
+ * m, both bf16; with n = 2^bits - 1:
+ *   m     the largest bf16 not above the group's minimum (bf16 inputs: the minimum itself)
+ *   s     the smallest bf16 with n s >= maximum - m, at least 2^-126
+ *   code  (x - m) / s rounded to the nearest whole number, ties to even; it stands for s code + m
+ * which is within s / 2 of x.  The codes are those of the real numbers: they do not depend on the machine's
+ * rounding.  A group with a value that is not finite in bf16 (NaN, infinite, or an fp32 value above 3.39e38) holds
+ * NaN and reads back as NaN; attention that sees such a token gives NaN.
+ *
+ * A cache is one device buffer of mha_quant_cache_size bytes, 256-byte aligned, with four parts at the byte offsets
+ * that call gives, each row-major: key codes (B, h_kv, T_max, row bytes), key parameters (B, h_kv, T_max, groups, 2)
+ * bf16 [s, m], then the same two of the values.  A row's codes are padded to 32 channels; 4 bits: channel 2i in the
+ * low half of byte i, channel 2i + 1 in the high half.  T_max is a multiple of 16.  It needs no initial contents:
+ * tokens at or past a length may hold anything and reach no output.
+ *
+ * For all calls: bits is 4 or 8; B * T_max, B * T_new, B * T_out and B * h * T_q are at most 2^31 - 65536 and
+ * B * h_kv below 2^31; dtype, shape and alignment rules as for the long-context operators.
+ *
+ * mha_quant_cache_size -- bytes of a cache for B sequences of up to T_max tokens; offsets: NULL, or size_t[4] that
+ * receives the parts' offsets.  0 for an invalid handle or size.  Makes no CUDA call.
+ */
+size_t mha_quant_cache_size(mha_t handle, int bits, int B, int T_max, size_t* offsets);
+
+/*
+ * mha_quant_write -- quantise new tokens' keys and values into the cache.
+ *   K, V           rows (B, T_new) of strides ldk, ldv, heads as for mha_decode's caches
+ *   cache_lengths  device int32[B]: L_b, the new tokens included, as the decode step after it wants it
+ *   counts         device int32[B] or NULL (every n_b = T_new): the first n_b rows of batch b become its tokens
+ *                  L_b - n_b .. L_b - 1; other tokens of the cache stay as they are
+ * A batch whose L_b or n_b does not satisfy 0 <= n_b <= T_new and n_b <= L_b <= T_max is not touched, and
+ * MHA_ERR_BAD_LENGTH is recorded (in an attached workspace's status word; none is needed).  The cache must not
+ * overlap an input.  One launch.  MHA_ERR_UNSUPPORTED for h_kv * ceil(d / 64) above 524272.
+ */
+mha_status mha_quant_write(mha_t handle, int bits, int B, int T_max, void* cache, int T_new, const void* K, int64_t ldk,
+                           const void* V, int64_t ldv, const int32_t* cache_lengths, const int32_t* counts,
+                           void* stream);
+
+/*
+ * mha_quant_read -- the reverse: rows 0 .. n_b - 1 of batch b of K and V (B, T_out) receive the values that its
+ * tokens L_b - n_b .. L_b - 1 stand for, rounded once to the handle's dtype; rows past n_b stay as they are.
+ * counts == NULL: every n_b = T_out.  counts == cache_lengths reads whole sequences.  K and V may be column views of
+ * one buffer but must not overlap each other, the cache or the lengths.  Other rules as for mha_quant_write.
+ */
+mha_status mha_quant_read(mha_t handle, int bits, int B, int T_max, const void* cache, int T_out, void* K, int64_t ldk,
+                          void* V, int64_t ldv, const int32_t* cache_lengths, const int32_t* counts, void* stream);
+
+/*
+ * mha_decode_quant_workspace_size -- bytes of workspace mha_decode_quant needs: the 256-byte status block and the
+ * partial results of the split over the cache.  0 for an invalid handle or size.
+ */
+size_t mha_decode_quant_workspace_size(mha_t handle, int B, int T_q, int T_max);
+
+/*
+ * mha_decode_quant -- mha_decode over a quantised cache: new token t sees cached tokens j <= L_b - T_q + t, and the
+ * keys and values are those that the codes stand for, s code + m, without further rounding.  Q, O, cache_lengths as
+ * for mha_decode (an L_b outside [T_q, T_max] makes that batch's rows NaN and records MHA_ERR_BAD_LENGTH).  O must
+ * not overlap an input.  Needs a workspace of mha_decode_quant_workspace_size(B, T_q, T_max) bytes.  One or two
+ * launches; results do not depend on the order in which the GPU runs them.
+ */
+mha_status mha_decode_quant(mha_t handle, int bits, int B, int T_q, int T_max, const void* Q, int64_t ldq,
+                            const void* cache, const int32_t* cache_lengths, void* O, int64_t ldo, void* stream);
+
+/*
  * mha_get_status -- copy the device status word of the attached workspace to
  * *status_out (an mha_status: MHA_OK, MHA_ERR_TIMEOUT or MHA_ERR_BAD_LENGTH;
  * the first error recorded wins) and zero the status block, which resets it to

@@ -9,11 +9,11 @@ library is missing, loading it raises ImportError.
 ``workloads`` (seeded synthetic inputs) imports neither torch nor the library.
 """
 
-__all__ = ["Mha", "workloads"]
+__all__ = ["Mha", "QuantCache", "workloads"]
 
 
 def __getattr__(name):
-    if name == "Mha":
-        from .mha import Mha
-        return Mha
+    if name in ("Mha", "QuantCache"):
+        from . import mha
+        return getattr(mha, name)
     raise AttributeError(name)

@@ -69,6 +69,11 @@ _SIGNATURES = {
                                 _vp]),
     "mha_cache_evict": (_i, [_vp, _i, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _vp, _i, _vp, _i64, _vp,
                              _i64, _vp, _vp, _vp, _vp]),
+    "mha_quant_cache_size": (_sz, [_vp, _i, _i, _i, ctypes.POINTER(_sz)]),
+    "mha_quant_write": (_i, [_vp, _i, _i, _i, _vp, _i, _vp, _i64, _vp, _i64, _vp, _vp, _vp]),
+    "mha_quant_read": (_i, [_vp, _i, _i, _i, _vp, _i, _vp, _i64, _vp, _i64, _vp, _vp, _vp]),
+    "mha_decode_quant_workspace_size": (_sz, [_vp, _i, _i, _i]),
+    "mha_decode_quant": (_i, [_vp, _i, _i, _i, _i, _vp, _i64, _vp, _vp, _vp, _i64, _vp]),
     "mha_get_status": (_i, [_vp, ctypes.POINTER(ctypes.c_int32), _vp]),
     "mha_forward_static_workspace": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp,
                                           _vp, _vp, _vp]),
@@ -289,6 +294,36 @@ def mha_cache_evict(handle, B, T_max, keep, recent, K_cache, ldk, V_cache, ldv, 
                                   cache_lengths, weights, T_out, K_out, ldko, V_out, ldvo, weights_out,
                                   kept, new_lengths, stream)
     return _check("mha_cache_evict", code) if check else code
+
+
+def mha_quant_cache_size(handle: int, bits: int, B: int, T_max: int):
+    """(bytes, byte offsets of the keys' codes and parameters and the values'); bytes is 0 for invalid sizes."""
+    off = (_sz * 4)()
+    return int(load().mha_quant_cache_size(handle, bits, B, T_max, off)), tuple(off)
+
+
+def mha_quant_write(handle, bits, B, T_max, cache, T_new, K, ldk, V, ldv, cache_lengths, counts, stream,
+                    check: bool = True) -> int:
+    code = load().mha_quant_write(handle, bits, B, T_max, cache, T_new, K, ldk, V, ldv, cache_lengths, counts,
+                                  stream)
+    return _check("mha_quant_write", code) if check else code
+
+
+def mha_quant_read(handle, bits, B, T_max, cache, T_out, K, ldk, V, ldv, cache_lengths, counts, stream,
+                   check: bool = True) -> int:
+    code = load().mha_quant_read(handle, bits, B, T_max, cache, T_out, K, ldk, V, ldv, cache_lengths, counts,
+                                 stream)
+    return _check("mha_quant_read", code) if check else code
+
+
+def mha_decode_quant_workspace_size(handle: int, B: int, T_q: int, T_max: int) -> int:
+    return int(load().mha_decode_quant_workspace_size(handle, B, T_q, T_max))
+
+
+def mha_decode_quant(handle, bits, B, T_q, T_max, Q, ldq, cache, cache_lengths, O, ldo, stream,
+                     check: bool = True) -> int:
+    code = load().mha_decode_quant(handle, bits, B, T_q, T_max, Q, ldq, cache, cache_lengths, O, ldo, stream)
+    return _check("mha_decode_quant", code) if check else code
 
 
 def mha_get_status(handle: int, stream: int) -> int:

@@ -154,4 +154,21 @@ cudaError_t launch_evict(const void* K, int64_t ldk, const void* V, int64_t ldv,
                          int recent, const int32_t* lengths, const float* weights, float* weights_out,
                          int32_t* kept, int32_t* new_lengths, int* status, cudaStream_t stream);
 
+struct QuantPlane;  // quant.cuh
+struct QuantStep;
+
+// mha_quant_write (write) and mha_quant_read; quant_copy_fits: is there a grid for so many heads?
+bool quant_copy_fits(const QuantPlane& pk, const QuantPlane& pv, int h_kv);
+cudaError_t launch_quant_copy(bool write, bool f32, int bits, const QuantPlane& pk, const QuantPlane& pv, void* K,
+                              int64_t ldk, void* V, int64_t ldv, int B, int T, int T_max, int h_kv,
+                              const int32_t* lengths, const int32_t* counts, int* status, cudaStream_t stream);
+
+// mha_decode_quant: how a step is cut, the bytes of its records (part), and its launches.
+QuantStep quant_step_shape(int B, int h, int h_kv, int T_q, int T_max);
+size_t quant_step_bytes(const QuantStep& s, int dv);
+bool quant_step_fits(const QuantStep& s);
+cudaError_t launch_quant_decode(const QuantStep& s, bool f32, int bits, const QuantPlane& pk, const QuantPlane& pv,
+                                const void* Q, int64_t ldq, void* O, int64_t ldo, const int32_t* lengths, float* part,
+                                int* status, cudaStream_t stream);
+
 }  // namespace mha

@@ -417,9 +417,13 @@ class Mha:
         """mha_cache_step_workspace_size, remembered for the sizes at hand."""
         need = self._step_bytes.get(sizes)
         if need is None:
-            if len(self._step_bytes) >= 64:  # (a prefix length that varies would fill it without end)
-                self._step_bytes.clear()
-            need = self._step_bytes[sizes] = _lib.mha_cache_step_workspace_size(self.handle, *sizes)
+            need = self._step_need_put(sizes, _lib.mha_cache_step_workspace_size(self.handle, *sizes))
+        return need
+
+    def _step_need_put(self, sizes: tuple, need: int) -> int:
+        if len(self._step_bytes) >= 64:  # (a prefix length that varies would fill it without end)
+            self._step_bytes.clear()
+        self._step_bytes[sizes] = need
         return need
 
     def _cache_step(self, Q, K_cache, V_cache, cache_lengths, out, T_prefix, weights, *others):
@@ -516,3 +520,102 @@ class Mha:
                              V_cache.data_ptr(), ldv, lens, w, T_out, K_out.data_ptr(), ldko,
                              V_out.data_ptr(), ldvo, wo, kept.data_ptr(), lo, stream)
         return K_out, V_out, lengths_out, weights_out, kept
+
+    # ------------------------------------------------------------ quantised caches
+    def quant_cache(self, B: int, T_max: int, bits: int = 4) -> "QuantCache":
+        """A cache of ``bits`` (4 or 8) bits a value for B sequences of up to T_max tokens, T_max rounded up to a
+        multiple of 16.  Its contents are unset: quant_write fills it, decode_quant attends over it."""
+        return QuantCache(self, B, T_max, bits)
+
+    def _quant_check(self, cache: "QuantCache", lengths: torch.Tensor, counts: Optional[torch.Tensor]):
+        if cache.heads != (self.h_kv, self.d_k, self.d_v):
+            raise ValueError(f"the cache holds (heads, d_k, d_v) {cache.heads}, expected "
+                             f"{(self.h_kv, self.d_k, self.d_v)}")
+        return (self._ints("cache_lengths", lengths, cache.B),
+                None if counts is None else self._ints("counts", counts, cache.B))
+
+    def quant_write(self, cache: "QuantCache", K: torch.Tensor, V: torch.Tensor, cache_lengths: torch.Tensor,
+                    counts: Optional[torch.Tensor] = None) -> "QuantCache":
+        """Quantise the keys K (B, T_new, h_kv*d_k view) and values V (B, T_new, h_kv*d_v view) of new tokens into
+        the cache.  cache_lengths (int32, B) count the cached tokens including the new ones, as decode_quant wants
+        them; counts (int32, B; default: T_new) how many rows of each sequence are tokens: the first n_b rows
+        become tokens L_b - n_b .. L_b - 1."""
+        lens, n = self._quant_check(cache, cache_lengths, counts)
+        T = K.shape[1]
+        ldk = self._rows("K", K, cache.B, T, self.h_kv * self.d_k)
+        ldv = self._rows("V", V, cache.B, T, self.h_kv * self.d_v)
+        stream = self._device(K, V, cache.data, cache_lengths, counts)
+        self.ensure_workspace(0, 0, 0, need=256)  # the status word
+        _lib.mha_quant_write(self.handle, *cache.args, T, K.data_ptr(), ldk, V.data_ptr(), ldv, lens, n, stream)
+        return cache
+
+    def quant_read(self, cache: "QuantCache", cache_lengths: torch.Tensor, counts: Optional[torch.Tensor] = None,
+                   T_out: Optional[int] = None, K_out: Optional[torch.Tensor] = None,
+                   V_out: Optional[torch.Tensor] = None):
+        """The values that each sequence's last n_b tokens (counts; default: T_out of them) stand for, in rows
+        0 .. n_b - 1 of K_out (B, T_out, h_kv*d_k view) and V_out (B, T_out, h_kv*d_v view); rows past n_b of
+        given outputs stay, of new ones are unset.  T_out defaults to the cache's T_max or the given outputs' rows.
+        counts=cache_lengths reads whole sequences.  Returns (K_out, V_out)."""
+        lens, n = self._quant_check(cache, cache_lengths, counts)
+        B, wk, wv = cache.B, self.h_kv * self.d_k, self.h_kv * self.d_v
+        if T_out is None:
+            T_out = K_out.shape[1] if K_out is not None else V_out.shape[1] if V_out is not None else cache.T_max
+        if K_out is None:
+            K_out = torch.empty((B, T_out, wk), dtype=self.dtype, device=cache.data.device)
+        if V_out is None:
+            V_out = torch.empty((B, T_out, wv), dtype=self.dtype, device=cache.data.device)
+        ldk = self._rows("K_out", K_out, B, T_out, wk)
+        ldv = self._rows("V_out", V_out, B, T_out, wv)
+        stream = self._device(cache.data, K_out, V_out, cache_lengths, counts)
+        self.ensure_workspace(0, 0, 0, need=256)  # the status word
+        _lib.mha_quant_read(self.handle, *cache.args, T_out, K_out.data_ptr(), ldk, V_out.data_ptr(), ldv, lens, n,
+                            stream)
+        return K_out, V_out
+
+    def decode_quant(self, Q: torch.Tensor, cache: "QuantCache", cache_lengths: torch.Tensor,
+                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """decode() over a quantised cache: the keys and values are those that the codes stand for."""
+        lens, _ = self._quant_check(cache, cache_lengths, None)
+        B, T_q, _ = Q.shape
+        ldq = self._rows("Q", Q, cache.B, T_q, self.h * self.d_k)
+        if out is None:
+            out = torch.empty((B, T_q, self.h * self.d_v), dtype=self.dtype, device=Q.device)
+        ldo = self._rows("out", out, B, T_q, self.h * self.d_v)
+        stream = self._device(Q, cache.data, cache_lengths, out)
+        sizes = ("quant", B, T_q, cache.T_max)
+        need = self._step_bytes.get(sizes)
+        if need is None:
+            need = self._step_need_put(sizes, _lib.mha_decode_quant_workspace_size(self.handle, *sizes[1:]))
+        self.ensure_workspace(B, T_q, cache.T_max, need=need)
+        bits, B, T_max, ptr = cache.args
+        _lib.mha_decode_quant(self.handle, bits, B, T_q, T_max, Q.data_ptr(), ldq, ptr, lens, out.data_ptr(), ldo,
+                              stream)
+        return out
+
+
+class QuantCache:
+    """A quantised key/value cache of one layer (Mha.quant_cache): ``data`` is its one buffer, the other tensors
+    are views of it.  K_codes, V_codes (B, h_kv, T_max, row bytes) uint8 hold the codes (4 bits: channel 2i in the
+    low half of byte i; rows padded to 32 channels), K_params, V_params (B, h_kv, T_max, groups, 2) bf16 the step s
+    and lowest value m of each group of 64 channels: a code c stands for s c + m.  Buffers of any origin will do:
+    fill the views and decode."""
+
+    def __init__(self, layer: Mha, B: int, T_max: int, bits: int = 4):
+        if bits not in (4, 8):
+            raise ValueError("bits must be 4 or 8")
+        layer._int32("B", B, 0)
+        layer._int32("T_max", T_max, 0)
+        T_max = layer._int32("T_max", (T_max + 15) // 16 * 16, 0)
+        nbytes, off = _lib.mha_quant_cache_size(layer.handle, bits, B, T_max)
+        if nbytes == 0 and B * T_max > 0:
+            raise ValueError(f"no cache of {B} x {T_max} tokens: sizes out of range")
+        self.B, self.T_max, self.bits = B, T_max, bits
+        self.heads = (layer.h_kv, layer.d_k, layer.d_v)
+        self.data = torch.empty(nbytes, dtype=torch.uint8, device=layer.device)
+        self.args = (bits, B, T_max, self.data.data_ptr())  # of every C call
+        views = []
+        for d, c, p in ((layer.d_k, off[0], off[1]), (layer.d_v, off[2], off[3])):
+            row, groups, n = (d + 31) // 32 * 4 * bits, (d + 63) // 64, B * layer.h_kv * T_max
+            views.append(self.data[c:c + n * row].view(B, layer.h_kv, T_max, row))
+            views.append(self.data[p:p + n * groups * 4].view(torch.bfloat16).view(B, layer.h_kv, T_max, groups, 2))
+        self.K_codes, self.K_params, self.V_codes, self.V_params = views
