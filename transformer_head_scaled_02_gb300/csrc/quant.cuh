@@ -40,14 +40,108 @@ __device__ __forceinline__ QuantRows quant_rows(int L, int n, int most, int T_ma
 __device__ __forceinline__ float quant_step(uint32_t p) { return __uint_as_float(p << 16); }
 __device__ __forceinline__ float quant_lowest(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
 
-// How a decode step is cut (host and device compute the same).  The query rows that share a cached head are taken
-// `rb` at a time; each batch's tokens are cut into at most `splits` equal parts of whole 64s.
+// ------------------------------------------------------------------ how a decode step is cut
+//
+// The query rows that share a cached head are taken `rb` at a time: a group is (batch, K/V head, block of rows), and
+// its visible tokens are cut into quanta of kQuantum.  All quanta of all groups, numbered by batch, head, block and
+// token, are dealt out evenly: CTA c of C <= N takes those from c N / C to (c + 1) N / C, whatever the lengths are.  A
+// CTA therefore has pieces of at most two groups that others share, its first and its last, and leaves records of those
+// (per row: m, l and the values, scores in base 2); groups that it has alone it finishes.  The join adds a group's
+// records in the order of its tokens.  Which CTA has what follows from the lengths and C alone.
+
+constexpr int kQuantum = 128;      // tokens
+constexpr int kQuantMaxCtas = 640; // largest grid, for the size of the workspace
+
 struct QuantStep {
     int B, h_kv, per, T_q, T_max;
-    int rows;    // per * T_q: query rows of a cached head
-    int rb, nrb; // rows of a row block; row blocks
-    int splits;
-    __host__ __device__ int part(int L) const { return ((L + splits - 1) / splits + 63) / 64 * 64; }
+    int rows;     // per * T_q: query rows of a cached head
+    int rb, nrb;  // rows of a row block; row blocks
+    int ctas;     // grid: C is this, or the number of quanta if that is less
+    int dv;
+    __host__ __device__ int lanes() const { return h_kv * nrb; }   // groups of a batch
+    __host__ __device__ int record() const { return dv + 2; }      // floats
+    // Record of a row of a CTA's first (which = 0: it began in another CTA) or last group.
+    __host__ __device__ int64_t slot(int cta, int which, int row) const { return ((int64_t)(2 * cta + which) * rb + row) * record(); }
 };
+
+#ifdef __CUDACC__
+
+__device__ __forceinline__ int quant_quanta(const QuantStep& s, int L) {
+    return L < s.T_q || L > s.T_max ? 0 : (L + kQuantum - 1) / kQuantum;
+}
+
+// A lane's part of the prefix sums over the batches; N quanta in all.
+struct QuantPlan {
+    int i0, i1, L0, before, sum, N, C;
+    __device__ __forceinline__ int length(const int32_t* lengths, int i) const { return i == i0 ? L0 : __ldcg(lengths + i); }
+    // First quantum of a CTA.
+    __device__ __forceinline__ int first(int cta) const { return cta < C ? (int)((int64_t)cta * N / C) : N; }
+    // The CTA that has a quantum.
+    __device__ __forceinline__ int owner(int q) const { return (int)((((int64_t)q + 1) * C - 1) / N); }
+};
+
+// All lanes of a warp call it, and the next two.
+__device__ __forceinline__ QuantPlan quant_plan(const QuantStep& s, const int32_t* lengths) {
+    const int lane = (int)threadIdx.x & 31, run = (s.B + 31) / 32;
+    QuantPlan p;
+    p.i0 = min(s.B, lane * run);
+    p.i1 = min(s.B, p.i0 + run);
+    p.L0 = p.i0 < p.i1 ? __ldcg(lengths + p.i0) : 0;
+    p.sum = 0;
+#pragma unroll 1
+    for (int i = p.i0; i < p.i1; ++i) p.sum += quant_quanta(s, p.length(lengths, i));
+    p.sum *= s.lanes();
+    int inc = p.sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+    }
+    p.before = inc - p.sum;
+    p.N = __shfl_sync(0xffffffffu, inc, 31);
+    p.C = min(s.ctas, p.N);
+    return p;
+}
+
+// The piece of a group that begins at quantum q of a CTA whose quanta end at `end`.
+struct QuantPiece {
+    int b, lane;   // batch; head * nrb + block
+    int L;
+    int q0, q1;    // quanta [q0, q1) of the group
+    int next;      // quantum behind the piece
+    int nq;        // quanta of the group
+    __device__ __forceinline__ int k0() const { return q0 * kQuantum; }
+    __device__ __forceinline__ int k1() const { return min(L, q1 * kQuantum); }
+    __device__ __forceinline__ bool whole() const { return q0 == 0 && q1 == nq; }
+};
+
+__device__ __forceinline__ QuantPiece quant_piece(const QuantStep& s, const int32_t* lengths, const QuantPlan& p, int q, int end) {
+    int b = 0, at = 0, len = 0;
+    const bool mine = p.before <= q && q < p.before + p.sum;
+    if (mine) {
+        at = p.before;
+#pragma unroll 1
+        for (b = p.i0;; ++b) {
+            len = p.length(lengths, b);
+            const int n = quant_quanta(s, len) * s.lanes();
+            if (q < at + n) break;
+            at += n;
+        }
+    }
+    const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+    QuantPiece x;
+    x.b = __shfl_sync(0xffffffffu, b, src);
+    at = __shfl_sync(0xffffffffu, at, src);
+    x.L = __shfl_sync(0xffffffffu, len, src);
+    x.nq = (x.L + kQuantum - 1) / kQuantum;
+    x.lane = (q - at) / x.nq;
+    const int start = at + x.lane * x.nq;
+    x.q0 = q - start;
+    x.q1 = min(x.nq, end - start);
+    x.next = start + x.q1;
+    return x;
+}
+
+#endif
 
 }  // namespace mha

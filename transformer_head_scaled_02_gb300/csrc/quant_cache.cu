@@ -130,9 +130,9 @@ __device__ __forceinline__ void store8(float* p, int n, const float (&x)[8]) {
 }
 
 // This thread's channels of its u-th group: head, channel in the head, how many of the eight exist.
-struct QuantPiece {
+struct QuantEight {
     int head, sub, c0, n;
-    __device__ __forceinline__ QuantPiece(const QuantPlane& p, int h_kv, int chunk, int u) {
+    __device__ __forceinline__ QuantEight(const QuantPlane& p, int h_kv, int chunk, int u) {
         const int lane = (int)threadIdx.x & 31, gi = chunk * QC_GROUPS + 4 * u + (lane >> 3);
         head = p.groups == 1 ? gi : gi / p.groups;
         sub = gi - head * p.groups;
@@ -159,13 +159,13 @@ __global__ void __launch_bounds__(QC_THREADS)
     float x[QC_RUN][8];
 #pragma unroll
     for (int u = 0; u < QC_RUN; ++u) {
-        const QuantPiece a(p, h_kv, chunk, u);
+        const QuantEight a(p, h_kv, chunk, u);
         load8<VEC>(src + (int64_t)a.head * p.d + a.c0, a.n, x[u]);
     }
     const int lane = (int)threadIdx.x & 31;
 #pragma unroll
     for (int u = 0; u < QC_RUN; ++u) {
-        const QuantPiece a(p, h_kv, chunk, u);
+        const QuantEight a(p, h_kv, chunk, u);
         float lo = INFINITY, hi = -INFINITY;
         bool fine = true;
 #pragma unroll
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(QC_THREADS)
     uint32_t par[QC_RUN];
 #pragma unroll
     for (int u = 0; u < QC_RUN; ++u) {
-        const QuantPiece a(p, h_kv, chunk, u);
+        const QuantEight a(p, h_kv, chunk, u);
         const int64_t at = ((int64_t)b * h_kv + a.head) * T_max + token;
         c[u] = make_uint2(0u, 0u);
         par[u] = 0;
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(QC_THREADS)
     }
 #pragma unroll
     for (int u = 0; u < QC_RUN; ++u) {
-        const QuantPiece a(p, h_kv, chunk, u);
+        const QuantEight a(p, h_kv, chunk, u);
         const float s = quant_step(par[u]), m = quant_lowest(par[u]);
         float x[8];
 #pragma unroll

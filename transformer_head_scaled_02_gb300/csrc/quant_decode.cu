@@ -12,6 +12,7 @@
 #include "internal.h"
 #include "ptx.cuh"
 #include "quant.cuh"
+#include "quant_meet.cuh"
 
 namespace mha {
 namespace {
@@ -22,8 +23,6 @@ constexpr int QD_ROWS = 4;
 
 __device__ __forceinline__ float elem(const float* p) { return *p; }
 __device__ __forceinline__ float elem(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void put(float* p, float x) { *p = x; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
 // Eight codes of a row as fp32.
 template <int BITS>
@@ -51,187 +50,199 @@ __global__ void __launch_bounds__(QD_THREADS)
     const int dpk = (pk.d + 31) & ~31, dpv = (pv.d + 31) & ~31;
     float* q = sm;
     float* qs = q + R * dpk;
-    float* own = qs + R * pk.groups + warp * R * (dpv + 32);
+    float* all = qs + R * pk.groups;
+    float* own = all + warp * R * (dpv + 32);
     grid_dependency_wait();
     grid_launch_dependents();
-    int i = (int)blockIdx.x;
-    const int rb = i % s.nrb;
-    i /= s.nrb;
-    const int split = i % s.splits;
-    i /= s.splits;
-    const int g = i % s.h_kv, b = i / s.h_kv;
-    const int L = lengths[b], r0 = rb * R, nr = min(R, s.rows - r0);
-    auto out_row = [&](int r, int& head, int& t) {
-        head = g * s.per + (r0 + r) / s.T_q;
-        t = (r0 + r) % s.T_q;
-        return O + ((int64_t)b * s.T_q + t) * ldo + (int64_t)head * pv.d;
-    };
-    if (L < s.T_q || L > s.T_max) {
-        if (split == 0) {
-            if (tid == 0) record_status(status, kStatusBadLength);
-            int head, t;
-            for (int r = 0; r < nr; ++r)
-                for (int e = tid; e < pv.d; e += QD_THREADS) put(out_row(r, head, t) + e, NAN);
+    const QuantPlan plan = quant_plan(s, lengths);
+    quant_invalid<QD_THREADS>(s, lengths, O, ldo, status);
+    const int end = plan.first((int)blockIdx.x + 1);
+    for (int at = plan.first((int)blockIdx.x); at < end;) {
+        const QuantPiece z = quant_piece(s, lengths, plan, at, end);
+        at = z.next;
+        const int b = z.b, g = z.lane / s.nrb, L = z.L, k0 = z.k0(), k1 = z.k1();
+        const int r0 = (z.lane - g * s.nrb) * R, nr = min(R, s.rows - r0);
+        __syncthreads();  // the piece before is written
+        for (int e = tid; e < R * dpk; e += QD_THREADS) {
+            const int r = e / dpk, c = e - r * dpk, rr = r0 + min(r, nr - 1);
+            q[e] = c < pk.d ? scale_log2 * elem(Q + ((int64_t)b * s.T_q + rr % s.T_q) * ldq + (int64_t)(g * s.per + rr / s.T_q) * pk.d + c) : 0.f;
         }
-        return;
-    }
-    const int span = s.part(L), k0 = split * span, k1 = min(L, k0 + span);
-    if (k0 >= k1) return;
-    for (int e = tid; e < R * dpk; e += QD_THREADS) {
-        const int r = e / dpk, c = e - r * dpk, rr = r0 + min(r, nr - 1);
-        q[e] = c < pk.d ? scale_log2 * elem(Q + ((int64_t)b * s.T_q + rr % s.T_q) * ldq + (int64_t)(g * s.per + rr / s.T_q) * pk.d + c) : 0.f;
-    }
-    __syncthreads();
-    for (int e = tid; e < R * pk.groups; e += QD_THREADS) {
-        const int r = e / pk.groups, c0 = (e - r * pk.groups) * kQuantGroup;
-        float x = 0.f;
-        for (int c = c0; c < min(dpk, c0 + kQuantGroup); ++c) x += q[r * dpk + c];
-        qs[e] = x;
-    }
-    __syncthreads();
-    const int64_t head_row = ((int64_t)b * s.h_kv + g) * s.T_max;
-    const uint8_t* kc = pk.codes + head_row * pk.row;
-    const uint32_t* kp = pk.params + head_row * pk.groups;
-    const uint8_t* vc = pv.codes + head_row * pv.row;
-    const uint32_t* vp = pv.params + head_row * pv.groups;
-    // values: `width` lanes hold a token's channels, 32 / width tokens at a time
-    const int width = dpv <= 32 ? 4 : dpv <= 64 ? 8 : dpv <= 128 ? 16 : 32, c0 = 8 * (lane % width), sub = lane / width;
-    const bool has = c0 < dpv;
-    float m[R], l[R], o[R][8];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        m[r] = -INFINITY;
-        l[r] = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[r][e] = 0.f;
-    }
-    for (int key0 = k0 + 32 * warp; key0 < k1; key0 += 32 * QD_WARPS) {
-        const int key = key0 + lane;
-        float x[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) x[r] = 0.f;
-        if (key < k1)
-            for (int G = 0; G < pk.groups; ++G) {
-                float dot[R];
-#pragma unroll
-                for (int r = 0; r < R; ++r) dot[r] = 0.f;
-                for (int c = G * kQuantGroup; c < min(dpk, (G + 1) * kQuantGroup); c += 8) {
-                    float v[8];
-                    codes8<BITS>(kc + (int64_t)key * pk.row + c * BITS / 8, v);
-#pragma unroll
-                    for (int r = 0; r < R; ++r)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) dot[r] = fmaf(q[r * dpk + c + e], v[e], dot[r]);
-                }
-                const uint32_t par = __ldg(kp + (int64_t)key * pk.groups + G);
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-                    x[r] = fmaf(quant_step(par), dot[r], fmaf(quant_lowest(par), qs[r * pk.groups + G], x[r]));
-            }
-        __syncwarp();
+        __syncthreads();
+        for (int e = tid; e < R * pk.groups; e += QD_THREADS) {
+            const int r = e / pk.groups, c0 = (e - r * pk.groups) * kQuantGroup;
+            float x = 0.f;
+            for (int c = c0; c < min(dpk, c0 + kQuantGroup); ++c) x += q[r * dpk + c];
+            qs[e] = x;
+        }
+        __syncthreads();
+        const int64_t head_row = ((int64_t)b * s.h_kv + g) * s.T_max;
+        const uint8_t* kc = pk.codes + head_row * pk.row;
+        const uint32_t* kp = pk.params + head_row * pk.groups;
+        const uint8_t* vc = pv.codes + head_row * pv.row;
+        const uint32_t* vp = pv.params + head_row * pv.groups;
+        // values: `width` lanes hold a token's channels, 32 / width tokens at a time
+        const int width = dpv <= 32 ? 4 : dpv <= 64 ? 8 : dpv <= 128 ? 16 : 32, c0 = 8 * (lane % width), sub = lane / width;
+        const bool has = c0 < dpv;
+        float m[R], l[R], o[R][8];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int pos = L - s.T_q + (r0 + min(r, nr - 1)) % s.T_q;
-            if (key >= k1 || key > pos) x[r] = -INFINITY;
-            float top = x[r];
+            m[r] = -INFINITY;
+            l[r] = 0.f;
 #pragma unroll
-            for (int w = 16; w >= 1; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-            if (top > m[r]) {
-                const float f = exp2f(m[r] - top);
-                l[r] *= f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[r][e] *= f;
-                m[r] = top;
-            }
-            const float p = x[r] == -INFINITY ? 0.f : exp2f(x[r] - m[r]);  // (NaN stays NaN)
-            l[r] += p;
-            own[r * 32 + lane] = p;
+            for (int e = 0; e < 8; ++e) o[r][e] = 0.f;
         }
-        __syncwarp();
-        for (int j = sub; j < min(32, k1 - key0); j += 32 / width) {
-            if (!has) continue;
-            float v[8];
-            codes8<BITS>(vc + (int64_t)(key0 + j) * pv.row + c0 * BITS / 8, v);
-            const uint32_t par = __ldg(vp + (int64_t)(key0 + j) * pv.groups + c0 / kQuantGroup);
-            const float vs = quant_step(par), vm = quant_lowest(par);
+        for (int key0 = k0 + 32 * warp; key0 < k1; key0 += 32 * QD_WARPS) {
+            const int key = key0 + lane;
+            float x[R];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e], vs, vm);
+            for (int r = 0; r < R; ++r) x[r] = 0.f;
+            if (key < k1)
+                for (int G = 0; G < pk.groups; ++G) {
+                    float dot[R];
+#pragma unroll
+                    for (int r = 0; r < R; ++r) dot[r] = 0.f;
+                    for (int c = G * kQuantGroup; c < min(dpk, (G + 1) * kQuantGroup); c += 8) {
+                        float v[8];
+                        codes8<BITS>(kc + (int64_t)key * pk.row + c * BITS / 8, v);
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) dot[r] = fmaf(q[r * dpk + c + e], v[e], dot[r]);
+                    }
+                    const uint32_t par = __ldg(kp + (int64_t)key * pk.groups + G);
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        x[r] = fmaf(quant_step(par), dot[r], fmaf(quant_lowest(par), qs[r * pk.groups + G], x[r]));
+                }
+            __syncwarp();
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const float p = own[r * 32 + j];
+                const int pos = L - s.T_q + (r0 + min(r, nr - 1)) % s.T_q;
+                if (key >= k1 || key > pos) x[r] = -INFINITY;
+                float top = x[r];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[r][e] = fmaf(p, v[e], o[r][e]);
+                for (int w = 16; w >= 1; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+                if (top > m[r]) {
+                    const float f = exp2f(m[r] - top);
+                    l[r] *= f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[r][e] *= f;
+                    m[r] = top;
+                }
+                const float p = x[r] == -INFINITY ? 0.f : exp2f(x[r] - m[r]);  // (NaN stays NaN)
+                l[r] += p;
+                own[r * 32 + lane] = p;
             }
+            __syncwarp();
+            for (int j = sub; j < min(32, k1 - key0); j += 32 / width) {
+                if (!has) continue;
+                float v[8];
+                codes8<BITS>(vc + (int64_t)(key0 + j) * pv.row + c0 * BITS / 8, v);
+                const uint32_t par = __ldg(vp + (int64_t)(key0 + j) * pv.groups + c0 / kQuantGroup);
+                const float vs = quant_step(par), vm = quant_lowest(par);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e], vs, vm);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float p = own[r * 32 + j];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[r][e] = fmaf(p, v[e], o[r][e]);
+                }
+            }
+            __syncwarp();
         }
-        __syncwarp();
-    }
-    // the warps' results meet
+        // the warps' results meet
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+        for (int r = 0; r < R; ++r) {
 #pragma unroll
-        for (int w = 16; w >= 1; w >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], w);
+            for (int w = 16; w >= 1; w >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            for (int w = width; w < 32; w <<= 1) o[r][e] += __shfl_xor_sync(0xffffffffu, o[r][e], w);
-        float* to = own + r * (dpv + 32);
-        if (lane == 0) to[dpv] = m[r], to[dpv + 1] = l[r];
-        if (has && sub == 0)
+            for (int e = 0; e < 8; ++e)
+                for (int w = width; w < 32; w <<= 1) o[r][e] += __shfl_xor_sync(0xffffffffu, o[r][e], w);
+            float* to = own + r * (dpv + 32);
+            if (lane == 0) to[dpv] = m[r], to[dpv + 1] = l[r];
+            if (has && sub == 0)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) to[c0 + e] = o[r][e];
-    }
-    __syncthreads();
-    const bool whole = span >= L;
-    const float* all = qs + R * pk.groups;
-    for (int e = tid; e < nr * pv.d; e += QD_THREADS) {
-        const int r = e / pv.d, c = e - r * pv.d;
-        float M = -INFINITY, sum = 0.f, x = 0.f;
-#pragma unroll
-        for (int w = 0; w < QD_WARPS; ++w) M = fmaxf(M, all[(w * R + r) * (dpv + 32) + dpv]);
-#pragma unroll
-        for (int w = 0; w < QD_WARPS; ++w) {
-            const float* a = all + (w * R + r) * (dpv + 32);
-            const float f = a[dpv] == -INFINITY ? 0.f : exp2f(a[dpv] - M);
-            sum = a[dpv + 1] == 0.f ? sum : fmaf(f, a[dpv + 1], sum);
-            x = fmaf(f, a[c], x);
+                for (int e = 0; e < 8; ++e) to[c0 + e] = o[r][e];
         }
-        int head, t;
-        T* out = out_row(r, head, t);
-        if (whole) {
-            put(out + c, x / sum);
-        } else {
-            float* rec = part + ((((int64_t)b * s.h_kv * s.per + head) * s.T_q + t) * s.splits + split) * (pv.d + 2);
-            rec[2 + c] = x;
-            if (c == 0) rec[0] = M, rec[1] = sum;
+        __syncthreads();
+        for (int e = tid; e < nr * pv.d; e += QD_THREADS) {
+            const int r = e / pv.d, c = e - r * pv.d;
+            const float* a = all + r * (dpv + 32);
+            quant_meet<QD_WARPS>(s, z, a + c, a + dpv, R * (dpv + 32), g, r0, r, c, O, ldo, part);
         }
     }
 }
 
-// The join: one output row per block.
+// The join: one output row per block.  The records' maxima and sums are read side by side, then the values, a slice of
+// the records per QJ_THREADS / 64 of the threads.
+constexpr int QJ_THREADS = 256;
+
 template <typename T>
-__global__ void __launch_bounds__(128)
-    quant_join_kernel(const QuantStep s, const float* __restrict__ part, T* __restrict__ O, int64_t ldo, int dv,
+__global__ void __launch_bounds__(QJ_THREADS)
+    quant_join_kernel(const QuantStep s, const float* __restrict__ part, T* __restrict__ O, int64_t ldo,
                       const int32_t* __restrict__ lengths) {
+    __shared__ float f[kQuantMaxCtas], top[QJ_THREADS / 32], sum[QJ_THREADS / 32], y[QJ_THREADS];
+    const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int heads = s.h_kv * s.per, row = (int)blockIdx.x;
     const int t = row % s.T_q, bh = row / s.T_q, b = bh / heads, head = bh - b * heads;
+    const int g = head / s.per, rr = (head - g * s.per) * s.T_q + t, block = rr / s.rb, r = rr - block * s.rb;
+    // The kernel before lets this one start once its own wait for earlier work is over: the lengths can be read (from
+    // L2), its records not yet.
+    const QuantPlan p = quant_plan(s, lengths);
+    int at = 0, len = 0;
+    const bool mine = p.i0 <= b && b < p.i1;
+    if (mine) {
+        at = p.before;
+#pragma unroll 1
+        for (int i = p.i0; i < b; ++i) at += quant_quanta(s, p.length(lengths, i)) * s.lanes();
+        len = p.length(lengths, b);
+    }
+    const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+    const int nq = quant_quanta(s, __shfl_sync(0xffffffffu, len, src));
+    const int first = __shfl_sync(0xffffffffu, at, src) + (g * s.nrb + block) * nq;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int L = lengths[b];
-    if (L < s.T_q || L > s.T_max) return;  // written as NaN already
-    const int span = s.part(L), n = (L + span - 1) / span;
+    if (nq == 0) return;  // an invalid length: written as NaN already
+    const int c0 = p.owner(first), n = p.owner(first + nq - 1) - c0 + 1;
     if (n == 1) return;
-    const float* rec = part + (int64_t)row * s.splits * (dv + 2);
-    float M = -INFINITY;
-    for (int c = 0; c < n; ++c) M = fmaxf(M, rec[(int64_t)c * (dv + 2)]);
-    for (int e = (int)threadIdx.x; e < dv; e += 128) {
-        float sum = 0.f, x = 0.f;
-        for (int c = 0; c < n; ++c) {
-            const float* a = rec + (int64_t)c * (dv + 2);
-            const float f = a[0] == -INFINITY ? 0.f : exp2f(a[0] - M);
-            sum = fmaf(f, a[1], sum);
-            x = fmaf(f, a[2 + e], x);
-        }
-        put(O + ((int64_t)b * s.T_q + t) * ldo + (int64_t)head * dv + e, x / sum);
+    // record c of the group: of the first CTA its last group, of the others their first
+    auto record = [&](int c) { return part + s.slot(c0 + c, c == 0 ? 1 : 0, r); };
+    float M = -INFINITY, l = 0.f;
+    for (int c = tid; c < n; c += QJ_THREADS) {
+        const float m = __ldcg(record(c));
+        f[c] = m;
+        M = fmaxf(M, m);
     }
+#pragma unroll
+    for (int w = 16; w >= 1; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+    if (lane == 0) top[warp] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < QJ_THREADS / 32; ++w) M = fmaxf(M, top[w]);
+    for (int c = tid; c < n; c += QJ_THREADS) {
+        f[c] = f[c] == -INFINITY ? 0.f : exp2f(f[c] - M);
+        l = fmaf(f[c], __ldcg(record(c) + 1), l);
+    }
+#pragma unroll
+    for (int w = 16; w >= 1; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+    if (lane == 0) sum[warp] = l;
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < QJ_THREADS / 32; ++w) l += sum[w];
+    // width threads hold the columns, QJ_THREADS / width slices of the records
+    const int width = s.dv <= 64 ? 64 : s.dv <= 128 ? 128 : 256, e = tid % width;
+    float x = 0.f;
+    if (e < s.dv) {
+#pragma unroll 8
+        for (int c = tid / width; c < n; c += QJ_THREADS / width) x = fmaf(f[c], __ldcg(record(c) + 2 + e), x);
+    }
+    y[tid] = x;
+    __syncthreads();
+    if (tid >= s.dv) return;
+    for (int w = tid + width; w < QJ_THREADS; w += width) x += y[w];
+    quant_put(O + ((int64_t)b * s.T_q + t) * ldo + (int64_t)head * s.dv + e, x / l);
 }
 
 size_t qd_smem(const QuantPlane& pk, const QuantPlane& pv) {
@@ -241,9 +252,9 @@ size_t qd_smem(const QuantPlane& pk, const QuantPlane& pv) {
 
 }  // namespace
 
-// Rows of a block, and parts of a cache: enough of them to fill the GPU a few times over, none shorter than 256
-// tokens.  Independent of the GPU, so that the workspace's size is.
-QuantStep quant_step_shape(int B, int h, int h_kv, int T_q, int T_max) {
+// Rows of a block by the kernel that serves the head size; CTAs: as many as the GPU holds at a time, but no more than
+// there may be quanta.
+QuantStep quant_step_shape(bool f32, int d_k, int d_v, int B, int h, int h_kv, int T_q, int T_max, int sms) {
     QuantStep s;
     s.B = B;
     s.h_kv = h_kv;
@@ -251,48 +262,52 @@ QuantStep quant_step_shape(int B, int h, int h_kv, int T_q, int T_max) {
     s.T_q = T_q;
     s.T_max = T_max;
     s.rows = s.per * T_q;
-    s.rb = QD_ROWS;
+    s.dv = d_v;
+    const bool mma = quant_mma_serves(d_k, d_v);
+    s.rb = mma ? quant_mma_rows(f32, d_k, s.rows) : QD_ROWS;
     s.nrb = (s.rows + s.rb - 1) / s.rb;
-    const int64_t groups = (int64_t)B * h_kv * s.nrb;
-    int64_t splits = (1024 + groups - 1) / groups;
-    const int64_t most = ((int64_t)T_max + 255) / 256;
-    if (splits > most) splits = most;
-    s.splits = splits < 1 ? 1 : (int)splits;
+    int64_t ctas = (int64_t)sms * (mma ? quant_mma_ctas(f32, d_k, s.rb) : 2);
+    const int64_t most = quant_most_quanta(s);
+    if (ctas > kQuantMaxCtas) ctas = kQuantMaxCtas;
+    if (ctas > most) ctas = most;
+    s.ctas = ctas < 1 ? 1 : (int)ctas;
     return s;
 }
 
-size_t quant_step_bytes(const QuantStep& s, int dv) {
-    return s.splits == 1 ? 0 : sizeof(float) * (size_t)s.B * s.h_kv * s.rows * s.splits * (size_t)(dv + 2);
+int64_t quant_most_quanta(const QuantStep& s) { return (int64_t)s.B * s.h_kv * s.nrb * ((s.T_max + kQuantum - 1) / kQuantum); }
+
+// For any number of SMs.
+size_t quant_step_bytes(const QuantStep& s) {
+    const int64_t most = quant_most_quanta(s);
+    const int64_t ctas = most < kQuantMaxCtas ? most : kQuantMaxCtas;
+    return sizeof(float) * 2 * (size_t)ctas * s.rb * s.record();
 }
 
-bool quant_step_fits(const QuantStep& s) {
-    return (int64_t)s.B * s.h_kv * s.nrb * s.splits <= INT32_MAX && (int64_t)s.B * s.h_kv * s.rows <= INT32_MAX;
-}
+bool quant_step_fits(const QuantStep& s) { return quant_most_quanta(s) <= INT32_MAX && (int64_t)s.B * s.h_kv * s.rows <= INT32_MAX; }
 
 cudaError_t launch_quant_decode(const QuantStep& s, bool f32, int bits, const QuantPlane& pk, const QuantPlane& pv,
                                 const void* Q, int64_t ldq, void* O, int64_t ldo, const int32_t* lengths, float* part,
                                 int* status, cudaStream_t stream) {
     const float scale = (float)(1.4426950408889634 / sqrt((double)pk.d));
-    const dim3 grid((unsigned)((int64_t)s.B * s.h_kv * s.nrb * s.splits));
-    const size_t smem = qd_smem(pk, pv);
-    auto go = [&](auto* x, auto kernel, auto join) {
+    auto go = [&](auto* x, auto kernel) {
         using T = std::remove_pointer_t<decltype(x)>;
-        cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 << 10);
-        if (err != cudaSuccess) return err;
-        err = launch_pdl(kernel, grid, dim3(QD_THREADS), smem, stream, s, pk, pv, static_cast<const T*>(Q), ldq,
-                         static_cast<T*>(O), ldo, lengths, scale, part, status);
-        if (err != cudaSuccess || s.splits == 1) return err;
-        return launch_pdl(join, dim3((unsigned)((int64_t)s.B * s.h_kv * s.rows)), dim3(128), 0, stream, s,
-                          static_cast<const float*>(part), static_cast<T*>(O), ldo, pv.d, lengths);
+        cudaError_t err;
+        if (quant_mma_serves(pk.d, pv.d)) {
+            err = launch_quant_mma(s, f32, bits, pk, pv, Q, ldq, O, ldo, lengths, part, status, stream);
+        } else {
+            err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 << 10);
+            if (err != cudaSuccess) return err;
+            err = launch_pdl(kernel, dim3((unsigned)s.ctas), dim3(QD_THREADS), qd_smem(pk, pv), stream, s, pk, pv,
+                             static_cast<const T*>(Q), ldq, static_cast<T*>(O), ldo, lengths, scale, part, status);
+        }
+        if (err != cudaSuccess || s.T_max <= kQuantum) return err;  // (groups of one quantum are never shared)
+        return launch_pdl(quant_join_kernel<T>, dim3((unsigned)((int64_t)s.B * s.h_kv * s.rows)), dim3(QJ_THREADS), 0, stream, s,
+                          static_cast<const float*>(part), static_cast<T*>(O), ldo, lengths);
     };
-    if (f32) {
-        float* x = nullptr;
-        return bits == 4 ? go(x, quant_decode_kernel<float, 4>, quant_join_kernel<float>)
-                         : go(x, quant_decode_kernel<float, 8>, quant_join_kernel<float>);
-    }
-    __nv_bfloat16* x = nullptr;
-    return bits == 4 ? go(x, quant_decode_kernel<__nv_bfloat16, 4>, quant_join_kernel<__nv_bfloat16>)
-                     : go(x, quant_decode_kernel<__nv_bfloat16, 8>, quant_join_kernel<__nv_bfloat16>);
+    if (f32) return bits == 4 ? go(static_cast<float*>(nullptr), quant_decode_kernel<float, 4>)
+                              : go(static_cast<float*>(nullptr), quant_decode_kernel<float, 8>);
+    return bits == 4 ? go(static_cast<__nv_bfloat16*>(nullptr), quant_decode_kernel<__nv_bfloat16, 4>)
+                     : go(static_cast<__nv_bfloat16*>(nullptr), quant_decode_kernel<__nv_bfloat16, 8>);
 }
 
 }  // namespace mha
