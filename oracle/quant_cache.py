@@ -79,10 +79,9 @@ def values(codes, params):
     return codes * p[..., 0] + p[..., 1]
 
 
-def spread(codes, params, bits):
-    """s |code - middle|: what the parts of a value that a kernel rounds amount to."""
-    p = np.repeat(params, GROUP, axis=-2)[..., :codes.shape[-1], 0]
-    return p * np.abs(codes - 2 ** (bits - 1))
+def spread(codes, params):
+    """s code: the part of a value that meets a rounded weight in a kernel (the other, m, is added in fp32)."""
+    return codes * np.repeat(params, GROUP, axis=-2)[..., :codes.shape[-1], 0]
 
 
 def heads(x, n):
@@ -91,13 +90,13 @@ def heads(x, n):
     return np.moveaxis(x.reshape(x.shape[0], x.shape[1], n, -1), 2, 1)
 
 
-def decode(Q, codes_k, params_k, codes_v, params_v, h, lengths, bits):
+def decode(Q, codes_k, params_k, codes_v, params_v, h, lengths):
     """One decode step over a cache (codes (B, h_kv, T, d), params (B, h_kv, T, groups, 2)): (O, A, S) with
     A = sum of weight * |v| and S = sum of weight * spread, which bound O's rounding."""
     Q = np.asarray(Q, np.float64)
     B, Tq, _ = Q.shape
     h_kv, T = codes_k.shape[1], codes_k.shape[2]
-    K, V, W = values(codes_k, params_k), values(codes_v, params_v), spread(codes_v, params_v, bits)
+    K, V, W = values(codes_k, params_k), values(codes_v, params_v), spread(codes_v, params_v)
     dk, dv = K.shape[-1], V.shape[-1]
     O, A, S = (np.zeros((B, Tq, h * dv)) for _ in range(3))
     for b in range(B):

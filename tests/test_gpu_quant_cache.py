@@ -5,11 +5,13 @@ Codes, steps and lowest values are those of the real numbers and are compared fo
 s code + m rounded once to fp32 (equal), or to bf16 (half a step, 2^-8 of the value, and 2^-24 for the sum in fp32).
 
 Tolerances of the decode step.  fp32: the normwise 1e-5 every fp32 parity test uses.  bf16 outputs, element by
-element: the output is rounded once, by at most 2^-8 |o|; the products of softmax weight and step may be rounded to
-16 bits of at least 11 significant ones before they meet the codes less their middle, which is off by at most
-2^-11 sum_j w_j s_j |code_j - middle| = 2^-11 S; everything else is fp32 and bounded by 1e-4 A, A = sum_j w_j |v_j|
-(scores of a few units, off by at most (d + 8) 2^-23 sum |q||k| / sqrt(d) each), and 1e-4 S for values that are
-small beside the two parts, step times code and lowest value, that they are the sum of.
+element: the output is rounded once, by at most 2^-8 |o|.  A value is s code + m; the products w s of softmax weight
+and step are rounded to fp16, each by at most 2^-11 of itself (11 significant bits), before they meet the codes:
+|sum_j fl(w_j s_j) code_j - sum_j w_j s_j code_j| <= 2^-11 sum_j w_j s_j code_j = 2^-11 S, whatever the m are, as
+those meet w in fp32.  (A bound with the codes' distance from their middle in S's place, which these tests first had,
+holds only for a kernel that takes the middle off the codes before the product: with code = middle it would be 0.)
+Everything else is fp32 and bounded by 1e-4 A, A = sum_j w_j |v_j| (scores of a few units, off by at most (d + 8)
+2^-23 sum |q||k| / sqrt(d) each), and 1e-4 S for values that are small beside the two parts they are the sum of.
 """
 import numpy as np
 import pytest
@@ -255,7 +257,7 @@ def _check(got, ref, A, S, dtype, what=""):
 
 def _step(layer, cache, held, Q, lengths, dtype, what=""):
     got = to_host(layer.decode_quant(to_device(Q, dtype), cache, _ints(lengths)))
-    O, A, S = qc.decode(Q, *held, layer.h, lengths, cache.bits)
+    O, A, S = qc.decode(Q, *held, layer.h, lengths)
     _check(got, O, A, S, dtype, what)
     return got
 
@@ -317,7 +319,7 @@ def test_decode_large_scores_and_scales(dtype, d, bits):
         layer.quant_write(cache, to_device(k, dtype), to_device(v, dtype), _ints([T]))
         held = _held(cache, "K") + _held(cache, "V")
         got = to_host(layer.decode_quant(to_device(q, dtype), cache, _ints([T])))
-        O, A, S = qc.decode(q, *held, h, [T], bits)
+        O, A, S = qc.decode(q, *held, h, [T])
         assert np.isfinite(got).all()
         # a score sums d products of q and the parts s code and m of a key, which may cancel
         Kv, p = qc.values(held[0], held[1]), np.repeat(held[1], 64, -2)[..., :d, :]
@@ -343,7 +345,7 @@ def test_decode_invalid_lengths():
         got = to_host(big)
         assert (got[..., :8] == 7).all() and (got[..., 8 + 4 * d:] == 7).all()
         got = got[..., 8:8 + 4 * d]
-        O, A, S = qc.decode(Q, *held, 4, lengths, 4)
+        O, A, S = qc.decode(Q, *held, 4, lengths)
         for b in range(6):
             if 2 <= lengths[b] <= cache.T_max:
                 _check(got[b], O[b], A[b], S[b], dtype)
@@ -361,7 +363,7 @@ def test_decode_views_and_results_that_repeat(dtype, d):
     t = to_device(x, dtype)[..., 16:16 + h * d]
     lengths = [3000, 77, 1501]
     first = layer.decode_quant(t, cache, _ints(lengths))
-    O, A, S = qc.decode(x[..., 16:16 + h * d], *held, h, lengths, 4)
+    O, A, S = qc.decode(x[..., 16:16 + h * d], *held, h, lengths)
     _check(to_host(first), O, A, S, dtype)
     for _ in range(5):
         assert torch.equal(layer.decode_quant(t, cache, _ints(lengths)), first)
@@ -403,7 +405,7 @@ def test_offsets_past_32_bits(dtype, d):
     cache.V_params[:-1, :, 0].zero_()
     out = to_host(layer.decode_quant(q, cache, lens)[-1:])
     pad = [np.concatenate((np.zeros(x.shape[:2] + (at,) + x.shape[3:]), x[:, :, :n]), 2) for x in held]
-    O, A, S = qc.decode(Q, *pad, 16, [T_max], 4)
+    O, A, S = qc.decode(Q, *pad, 16, [T_max])
     _check(out, O, A, S, dtype, "past 32 bits")
 
 
@@ -441,7 +443,7 @@ def test_generation(dtype, d, h, h_kv, bits):
                 side[b] = [np.concatenate((old, y[b]), 1) for old, y in zip(side[b], new)]
         for b in range(B):
             held = [y[None] for y in want[0][b] + want[1][b]]
-            O, A, S = qc.decode(to_host(p[b:b + 1, :, :cut[0]]), *held, h, [lengths[b]], bits)
+            O, A, S = qc.decode(to_host(p[b:b + 1, :, :cut[0]]), *held, h, [lengths[b]])
             _check(got[b:b + 1], O, A, S, dtype, f"step {step}")
     assert layer.status() == 0
     Ko, Vo = layer.quant_read(cache, lens, lens, K_out=torch.zeros((B, 400, h_kv * d), dtype=torch_dtype(dtype), device="cuda"),
@@ -481,7 +483,7 @@ def test_captured_steps_share_a_workspace(dtype, d):
                 g.replay()
                 got = to_host(s["out"])
                 held = _held(cache, "K") + _held(cache, "V")
-                O, A, S = qc.decode(to_host(s["q"]), *held, h, lengths, 4)
+                O, A, S = qc.decode(to_host(s["q"]), *held, h, lengths)
                 _check(got, O, A, S, dtype, f"replay {round_}")
                 eager = layer.decode_quant(s["q"], cache, s["len"])
                 assert torch.equal(eager, s["out"])

@@ -1,28 +1,28 @@
 // quant_mma.cu -- a decode step over a quantised cache (quant.cuh) for heads of 64 and 128 channels, on the tensor
 // cores: the codes themselves are the matrix operands.
 //
-// A code less its middle z (8 or 128) is a whole number that fp16 holds exactly, so with steps s, middles
-// c = m + z s, and 64-channel groups G
-//   score_j = sum_G s_jG (q_G . (code_jG - z)) + c_jG (sum of q_G)
-//   o       = sum_j (p_j s_jG) (code_j - z) + sum_j p_j c_jG
-// the two products are exact but for the 16-bit forms of q and of p s; sums, softmax and the c terms are fp32.  q is
-// scaled by a power of two so that fp16 holds it: exactly for bf16 layers, as high and low part for fp32 layers
-// (2^-25 of the row's largest element); likewise p s, against a running power of two: 11 bits for bf16 layers, high
-// and low part for fp32 ones.
+// A code in a 16-bit half whose other bits are zero is an fp16 number as it stands, a subnormal one: code 2^-24 exactly
+// in the low bits, up to code 2^-18 further up the fraction.  So with steps s, lowest values m and 64-channel groups G
+//   score_j = sum_G s_jG (q_G . code_jG) + m_jG (sum of q_G)
+//   o       = sum_j (p_j s_jG) code_j + sum_j p_j m_jG
+// need no more unpacking than masks, and the two products are exact but for the 16-bit forms of q and of p s; sums,
+// softmax and the m terms are fp32.  q is scaled by a power of two so that fp16 holds it: exactly for bf16 layers, as
+// high and low part for fp32 layers (22 bits); likewise p s, against a running power of two: 11 bits for bf16 layers,
+// high and low part for fp32 ones.
 //
 // The cached tokens are the M side of both products (16 at a time) and the query rows the N side (8 or 16), so a few
 // rows waste no tensor work and the exponentials spread over all lanes.  Which channel or token is which k of a
-// product is free as long as both operands agree: it is chosen so that operands come out of the packed words with one
-// mask-and-or for two elements.  0x6400 | code is the fp16 number 1024 + code; a nibble in place reads 1024 + 16 code.
+// product is free as long as both operands agree: it is chosen so that one mask takes two elements out of a word.
 //   scores:  A = keys [token][channel], lane (gid, tig) holds 16 channels of a group of tokens gid and gid + 8
 //   values:  A = values transposed [channel][token], the words of two tokens interleaved by a byte permutation;
 //            B = p s, which the scores' layout becomes by transposing 8 x 8 pieces (movmatrix)
 // mma.sync feeds operands from registers, where the unpacked codes are; tcgen05 would take them through shared
 // memory, written and read once more per element.
 //
-// Each warp streams its own tokens through its own ring of bulk copies (a head's codes lie in one piece), so warps
-// wait for nothing but their data; they meet at the end of their part of the cache.  The reference maximum moves only
-// when a score exceeds it by 2^8, which one vote per 16 tokens finds.
+// Stages of tokens come by bulk copies (a head's codes lie in one piece) into a ring; each warp takes a run of a
+// stage's 16-token blocks with its own maximum, sum and values, and the last warp to finish a stage asks for the next
+// one in its place.  (A ring per warp cost 200 instructions per stage and warp instead of some 30.)  Warps meet at the
+// end of a piece.  The reference maximum moves only when a score exceeds it by 2^8, which one vote per block finds.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -37,31 +37,37 @@ namespace mha {
 namespace {
 
 constexpr int QM_WARPS = 8;
+constexpr float kNone = -3e38f;  // the reference of a row that has seen nothing: below every score, finite
 constexpr int QM_THREADS = 32 * QM_WARPS;
 
 template <int BITS, int D, int TERMS, int NT>
 struct QmCfg {
     static constexpr int G = D / kQuantGroup;
     static constexpr int ROW = D * BITS / 8;
-    static constexpr int TOK = 16384 / (D * BITS);            // tokens of a stage: 4 KB of codes
+    static constexpr int TOK = 131072 / (D * BITS);           // tokens of a stage: 32 KB of codes
     static constexpr int STAGE = 2 * TOK * (ROW + 4 * G);     // key codes, value codes, key and value parameters
     static constexpr int CTAS = NT * TERMS * G > 2 ? 1 : 2;   // of an SM (registers)
     static constexpr int STAGES = CTAS == 1 ? 4 : 2;
-    static constexpr int RING = STAGES * STAGE;
     static constexpr int ROWS = 8 * NT;
     static constexpr int REC = D + 4;                         // floats of a row's result: values, m, l
-    static constexpr int RES = QM_WARPS * RING;               // the warps' results
+    static constexpr int RES = STAGES * STAGE;                // the warps' results
     static constexpr int BARS = RES + QM_WARPS * ROWS * REC * 4;
-    static constexpr int SMEM = BARS + 8 * QM_WARPS * STAGES + 16;
-    static constexpr float Z = BITS == 4 ? 8.f : 128.f;
-    static_assert(TOK % 16 == 0, "stages are whole products");
+    static constexpr int SMEM = BARS + 16 * STAGES + 48;      // barriers, counts of the warps done, QmNext, abort flag
+    static_assert(TOK % kQuantum == 0, "a stage's tokens are dealt out evenly");
     static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
+// Where the next stage to be copied begins.
+struct QmNext {
+    int64_t row;       // the piece's head in the cache
+    int at, from, to;  // quantum behind the piece; what is left of it
+    int issued;        // stages so far
+};
+
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -77,57 +83,53 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 
 __device__ __forceinline__ float2 half2_floats(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
 
-// (w & mask) | 0x64006400
-template <uint32_t MASK>
-__device__ __forceinline__ uint32_t pick(uint32_t w) {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "n"(MASK), "r"(0x64006400u));
-    return r;
+// Codes of a word as fp16 pairs, two at a time.  The two are 16 bits apart:
+// nibbles i and i + 4, or bytes i and i + 2, in x[i].  bf16 layers take them where they are, which is cheapest;
+// fp32 layers move them to the top of the fraction, as the tensor core adds products by their exponents, which
+// subnormal numbers' leading zeros do not lower: 7 bits lost show in fp32 (1.4e-5 of an output) but not in bf16.
+template <int BITS, int TERMS>
+__device__ __forceinline__ void codes_of(uint32_t w, uint32_t (&x)[BITS == 4 ? 4 : 2]) {
+    if constexpr (BITS == 4 && TERMS == 1) {
+        x[0] = w & 0x000f000fu;
+        x[1] = w & 0x00f000f0u;
+        x[2] = w >> 8 & 0x000f000fu;
+        x[3] = w >> 8 & 0x00f000f0u;
+    } else if constexpr (BITS == 4) {
+        x[0] = w << 6 & 0x03c003c0u;
+        x[1] = w << 2 & 0x03c003c0u;
+        x[2] = w >> 2 & 0x03c003c0u;
+        x[3] = w >> 6 & 0x03c003c0u;
+    } else if constexpr (TERMS == 1) {
+        x[0] = w & 0x00ff00ffu;
+        x[1] = w >> 8 & 0x00ff00ffu;
+    } else {
+        x[0] = w << 2 & 0x03fc03fcu;
+        x[1] = w >> 6 & 0x03fc03fcu;
+    }
 }
 
-__device__ __forceinline__ uint32_t sub2(uint32_t x, uint32_t c) {  // fp16 pairs
-    uint32_t r;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(c));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t fma2h(uint32_t x, uint32_t a, uint32_t c) {
-    uint32_t r;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(a), "r"(c));
-    return r;
-}
-
-// Nibbles 0 and 4, or 1 and 5, of a word less 8, as fp16 pairs.
-__device__ __forceinline__ uint32_t even_codes(uint32_t w) { return sub2(pick<0x000f000fu>(w), 0x64086408u); }  // 1032
-__device__ __forceinline__ uint32_t odd_codes(uint32_t w) {
-    return fma2h(pick<0x00f000f0u>(w), 0x2c002c00u, 0xd480d480u);  // (1024 + 16 code) / 16 - 72
-}
-// Two bytes less 128; sel places them.
-__device__ __forceinline__ uint32_t byte_codes(uint32_t w, uint32_t sel) {
-    return sub2(__byte_perm(w, 0x64646464u, sel), 0x64806480u);  // 1152
+// What a code counts in even (h = 0) and odd (h = 1) places.
+template <int BITS, int TERMS>
+__device__ __forceinline__ constexpr float unit(int h) {
+    constexpr float u = 5.9604644775390625e-8f;  // 2^-24
+    return TERMS == 1 ? (BITS == 4 && h == 1 ? 16.f * u : u) : BITS == 4 ? 64.f * u : 4.f * u;
 }
 
 // 16 of a row's channels in a group (keys), as the A operands of the group's four products for one token: x[c][0] its
 // k = 2 tig, 2 tig + 1, x[c][1] its k = 2 tig + 8, 2 tig + 9.  The channels behind them: q_channel().
-template <int BITS>
+template <int BITS, int TERMS>
 __device__ __forceinline__ void key_operands(uint32_t addr, uint32_t (&x)[4][2]) {
-    if constexpr (BITS == 4) {
-        uint32_t w[2];
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+    uint32_t w[BITS / 2];
+    if constexpr (BITS == 4) asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+    else asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            x[2 * i][0] = even_codes(w[i]);
-            x[2 * i][1] = odd_codes(w[i]);
-            x[2 * i + 1][0] = even_codes(w[i] >> 8);
-            x[2 * i + 1][1] = odd_codes(w[i] >> 8);
-        }
-    } else {
-        uint32_t w[4];
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+    for (int i = 0; i < BITS / 2; ++i) {
+        uint32_t y[BITS == 4 ? 4 : 2];
+        codes_of<BITS, TERMS>(w[i], y);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[i][0] = byte_codes(w[i], 0x4140);
-            x[i][1] = byte_codes(w[i], 0x4342);
+        for (int c = 0; c < 8 / BITS; ++c) {
+            x[i * 8 / BITS + c][0] = y[2 * c];
+            x[i * 8 / BITS + c][1] = y[2 * c + 1];
         }
     }
 }
@@ -135,34 +137,30 @@ __device__ __forceinline__ void key_operands(uint32_t addr, uint32_t (&x)[4][2])
 // Channel (of this lane's 16 of a group) behind half h, element e of product c.
 template <int BITS>
 __device__ __forceinline__ constexpr int q_channel(int c, int h, int e) {
-    return BITS == 4 ? 8 * (c >> 1) + 2 * (c & 1) + h + 4 * e : 4 * c + 2 * h + e;
+    return BITS == 4 ? 8 * (c >> 1) + 2 * (c & 1) + h + 4 * e : 4 * c + h + 2 * e;
 }
 
 // Eight of a row's channels in a group (values) of two tokens a, b, as the A operands of the group's four products:
 // x[t][0] channel 2 t of both tokens, x[t][1] channel 2 t + 1.
-template <int BITS>
+template <int BITS, int TERMS>
 __device__ __forceinline__ void value_operands(uint32_t addr_a, uint32_t addr_b, uint32_t (&x)[4][2]) {
+    uint32_t a[BITS / 4], b[BITS / 4];
     if constexpr (BITS == 4) {
-        uint32_t a, b;
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(a) : "r"(addr_a));
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(b) : "r"(addr_b));
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t w = __byte_perm(a, b, i == 0 ? 0x5410 : 0x7632);
-            x[2 * i][0] = even_codes(w);
-            x[2 * i][1] = odd_codes(w);
-            x[2 * i + 1][0] = even_codes(w >> 8);
-            x[2 * i + 1][1] = odd_codes(w >> 8);
-        }
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(a[0]) : "r"(addr_a));
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(b[0]) : "r"(addr_b));
     } else {
-        uint32_t a[2], b[2];
         asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(a[0]), "=r"(a[1]) : "r"(addr_a));
         asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(b[0]), "=r"(b[1]) : "r"(addr_b));
+    }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t w = __byte_perm(a[i >> 1], b[i >> 1], (i & 1) ? 0x7362 : 0x5140);  // bytes a0 b0 a1 b1
-            x[i][0] = byte_codes(w, 0x4140);
-            x[i][1] = byte_codes(w, 0x4342);
+    for (int i = 0; i < BITS / 2; ++i) {
+        const uint32_t w = __byte_perm(a[i / 2], b[i / 2], (i & 1) ? 0x7632 : 0x5410);  // half of a, half of b
+        uint32_t y[BITS == 4 ? 4 : 2];
+        codes_of<BITS, TERMS>(w, y);
+#pragma unroll
+        for (int c = 0; c < 8 / BITS; ++c) {
+            x[i * 8 / BITS + c][0] = y[2 * c];
+            x[i * 8 / BITS + c][1] = y[2 * c + 1];
         }
     }
 }
@@ -188,53 +186,55 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT>::CTAS)
     constexpr int G = C::G;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5, gid = lane >> 2, tig = lane & 3;
-    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * C::RING);
-    const uint32_t bars = smem_u32(smem) + (uint32_t)(C::BARS + 8 * warp * C::STAGES);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::BARS + 8 * QM_WARPS * C::STAGES);
-    if (lane == 0)
-        for (int i = 0; i < C::STAGES; ++i) mbar_init(bars + 8u * i, 1);
-    if (tid == 0) *abort_flag = 0;
-    fence_mbar_init();
+    const uint32_t ring = smem_u32(smem), bars = ring + C::BARS;
+    uint32_t* done = reinterpret_cast<uint32_t*>(smem + C::BARS + 8 * C::STAGES);
+    QmNext* next = reinterpret_cast<QmNext*>(smem + C::BARS + 16 * C::STAGES);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(next + 1);
+    if (tid == 0) {
+        for (int i = 0; i < C::STAGES; ++i) {
+            mbar_init(bars + 8u * i, 1);
+            done[i] = 0;
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
     __syncthreads();
     grid_dependency_wait();
     grid_launch_dependents();
 
     const QuantPlan plan = quant_plan(s, lengths);
     const int end = plan.first((int)blockIdx.x + 1);
-    // Two places in this CTA's quanta: where copies are asked for, up to STAGES ahead, and where they are used, piece
-    // by piece.  A warp has a run of each piece's 16-token blocks.
-    auto run = [&](const QuantPiece& z, int& from, int& to) {
-        const int n = (z.k1() - z.k0() + 15) / 16;
-        from = z.k0() + (warp * n / QM_WARPS) * 16;
-        to = min(z.k1(), z.k0() + ((warp + 1) * n / QM_WARPS) * 16);
-    };
-    int issued = 0;      // stages asked for
-    int f_at = plan.first((int)blockIdx.x), f_from = 0, f_to = 0;
-    int64_t f_row = 0;   // the piece's head in the cache
-    auto fetch = [&]() {
-        while (f_from >= f_to) {
-            if (f_at >= end) return;
-            const QuantPiece z = quant_piece(s, lengths, plan, f_at, end);
-            f_at = z.next;
-            f_row = ((int64_t)z.b * s.h_kv + z.lane / s.nrb) * s.T_max;
-            run(z, f_from, f_to);
+    // One warp at a time asks for the next stage (all its lanes call this): at first warp 0, then whichever is the last
+    // to have used the stage whose place it takes.
+    auto fetch = [&](QmNext& x) {
+        while (x.from >= x.to) {
+            if (x.at >= end) return;
+            const QuantPiece z = quant_piece(s, lengths, plan, x.at, end);
+            x.at = z.next;
+            x.row = ((int64_t)z.b * s.h_kv + z.lane / s.nrb) * s.T_max;
+            x.from = z.k0();
+            x.to = z.k1();
         }
-        // whole sixteens: caches hold multiples of them
-        const uint32_t tok = (uint32_t)min(C::TOK, (f_to - f_from + 15) & ~15);
         if (lane == 0) {
-            const uint32_t at = ring + (uint32_t)(issued % C::STAGES * C::STAGE), bar = bars + 8u * (uint32_t)(issued % C::STAGES);
-            const int64_t r = f_row + f_from;
+            // whole sixteens: caches hold multiples of them
+            const uint32_t tok = (uint32_t)min(C::TOK, (x.to - x.from + 15) & ~15);
+            const uint32_t at = ring + (uint32_t)(x.issued % C::STAGES * C::STAGE), bar = bars + 8u * (uint32_t)(x.issued % C::STAGES);
+            const int64_t r = x.row + x.from;
             mbar_arrive_expect_tx(bar, 2u * tok * (C::ROW + 4 * G));
             bulk_load(at, pk.codes + r * C::ROW, tok * C::ROW, bar);
             bulk_load(at + 2 * C::TOK * C::ROW, pk.params + r * G, tok * 4 * G, bar);
             bulk_load(at + C::TOK * C::ROW, pv.codes + r * C::ROW, tok * C::ROW, bar);
             bulk_load(at + 2 * C::TOK * C::ROW + C::TOK * 4 * G, pv.params + r * G, tok * 4 * G, bar);
         }
-        f_from += C::TOK;
-        ++issued;
+        x.from += C::TOK;
+        ++x.issued;
     };
+    if (warp == 0) {
+        QmNext x{0, plan.first((int)blockIdx.x), 0, 0, 0};
 #pragma unroll 1
-    for (int n = 0; n < C::STAGES; ++n) fetch();
+        for (int n = 0; n < C::STAGES; ++n) fetch(x);
+        if (lane == 0) *next = x;
+    }
     quant_invalid<QM_THREADS>(s, lengths, O, ldo, status);
 
     bool ok = true;
@@ -246,11 +246,11 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT>::CTAS)
     const int b = z.b, g = z.lane / s.nrb, L = z.L;
     const int r0 = (z.lane - g * s.nrb) * C::ROWS, nr = min(C::ROWS, s.rows - r0);
 
-    // queries: row gid of each eight as B operands, and what the lane's score columns 2 tig, 2 tig + 1 need of theirs
+    // queries: row gid of each eight as B operands, and what the lane's score columns 2 tig, 2 tig + 1 need of theirs.
+    // y rs is a score.
     uint32_t qf[TERMS][NT][G][4][2];
     float qs[NT][G][2], rs[NT][2];
-    int lim[NT][2];  // tokens before this one are visible
-    int lim_min = L;
+    const int lim_min = L - s.T_q + 1;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int rr = r0 + min(8 * nt + gid, nr - 1), head = g * s.per + rr / s.T_q, t = rr % s.T_q;
@@ -265,8 +265,8 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT>::CTAS)
             }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // the largest element to [16, 32); zero, infinite and tiny rows as far as powers of two go
-        const int e2 = top > 0.f && top < INFINITY ? max(-100, min(100, 4 - exponent(top))) : 0;
+        // the largest element to [2^13, 2^14); zero, infinite and tiny rows as far as powers of two go
+        const int e2 = top > 0.f && top < INFINITY ? max(-80, min(100, 13 - exponent(top))) : 0;
         const float f = power2(e2);
         float sum[G];
 #pragma unroll
@@ -276,35 +276,35 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT>::CTAS)
             for (int c = 0; c < 4; ++c)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float x0 = f * x[u][q_channel<BITS>(c, h, 0)], x1 = f * x[u][q_channel<BITS>(c, h, 1)];
+                    const float fh = f * (unit<BITS, TERMS>(0) / unit<BITS, TERMS>(h));
+                    const float x0 = fh * x[u][q_channel<BITS>(c, h, 0)], x1 = fh * x[u][q_channel<BITS>(c, h, 1)];
                     qf[0][nt][u][c][h] = half2_bits(x0, x1);
                     if constexpr (TERMS == 2) {
-                        const float2 hi = half2_floats(qf[0][nt][u][c][h]);
-                        qf[TERMS - 1][nt][u][c][h] = half2_bits(x0 - hi.x, x1 - hi.y);
+                        const float2 high = half2_floats(qf[0][nt][u][c][h]);
+                        qf[TERMS - 1][nt][u][c][h] = half2_bits(x0 - high.x, x1 - high.y);
                     }
-                    sum[u] += x0 + x1;
+                    sum[u] = fmaf(unit<BITS, TERMS>(h), x0 + x1, sum[u]);
                 }
             sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], 1);
             sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], 2);
         }
-        const float back = scale_log2 * power2(-e2);
+        const float back = scale_log2 / unit<BITS, TERMS>(0) * power2(-e2);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int from = 4 * (2 * tig + e);
 #pragma unroll
             for (int u = 0; u < G; ++u) qs[nt][u][e] = __shfl_sync(0xffffffffu, sum[u], from);
             rs[nt][e] = __shfl_sync(0xffffffffu, back, from);
-            lim[nt][e] = L - s.T_q + __shfl_sync(0xffffffffu, t, from) + 1;
         }
-        lim_min = min(lim_min, L - s.T_q + 1);
     }
 
     float o[NT][G][4][4], om[NT][G][2], m[NT][2], l[NT][2];
+    float far[NT][2];  // the y that moves the reference m: (m + 8) / rs
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            m[nt][e] = -INFINITY;
+            m[nt][e] = far[nt][e] = kNone;
             l[nt][e] = 0.f;
 #pragma unroll
             for (int u = 0; u < G; ++u) {
@@ -316,43 +316,43 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT>::CTAS)
     float vs = power2(100);  // p s is held as p s vs
     const int pa = gid ^ (gid >> 1 & 1);                          // this lane's key token, and its second at + 8: the
     const int va = 2 * tig ^ (tig & 1), vb = (2 * tig + 1) ^ (tig & 1);  // order in which neither load meets itself in a bank
-    int from, to;
-    run(z, from, to);
 #pragma unroll 1
-    for (int t_stage = from; t_stage < to && ok; t_stage += C::TOK) {
-        const uint32_t bar = bars + 8u * (uint32_t)(used % C::STAGES);
-        if (!__all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)(used / C::STAGES) & 1u, abort_flag, status))) {
+    for (int t_stage = z.k0(); t_stage < z.k1() && ok; t_stage += C::TOK) {
+        const uint32_t slot = (uint32_t)(used % C::STAGES);
+        if (!__all_sync(0xffffffffu, mbar_wait(bars + 8u * slot, (uint32_t)(used / C::STAGES) & 1u, abort_flag, status))) {
             ok = false;
             break;
         }
-        const uint32_t at = ring + (uint32_t)(used % C::STAGES * C::STAGE);
+        const uint32_t at = ring + slot * C::STAGE;
+        // the stage's 16-token blocks, a run of them for each warp
+        const int blocks = min(C::TOK / 16, (z.k1() - t_stage + 15) / 16);
 #pragma unroll 1
-        for (int sub = 0; sub < C::TOK && t_stage + sub < to; sub += 16) {
+        for (int sub = warp * blocks / QM_WARPS * 16; sub < (warp + 1) * blocks / QM_WARPS * 16; sub += 16) {
             const int t0 = t_stage + sub;
             const bool edge = t0 + 16 > lim_min;  // some row does not see all of the 16
             const uint32_t kc = at + (uint32_t)(sub * C::ROW), vc = kc + C::TOK * C::ROW;
             const uint32_t kp = at + 2 * C::TOK * C::ROW + (uint32_t)(sub * 4 * G), vp = kp + C::TOK * 4 * G;
             // scores
-            float x[NT][4];
+            float y[NT][4];
             {
                 float acc[NT][G][4];
 #pragma unroll
                 for (int u = 0; u < G; ++u) {
                     uint32_t ka[4][2], kb[4][2];
                     const uint32_t col = (uint32_t)((u * kQuantGroup + 16 * tig) * BITS / 8);
-                    key_operands<BITS>(kc + (uint32_t)(pa * C::ROW) + col, ka);
-                    key_operands<BITS>(kc + (uint32_t)((pa + 8) * C::ROW) + col, kb);
+                    key_operands<BITS, TERMS>(kc + (uint32_t)(pa * C::ROW) + col, ka);
+                    key_operands<BITS, TERMS>(kc + (uint32_t)((pa + 8) * C::ROW) + col, kb);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[nt][u][e] = 0.f;
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             const uint32_t a[4] = {ka[c][0], kb[c][0], ka[c][1], kb[c][1]};
 #pragma unroll
-                            for (int w = 0; w < TERMS; ++w) mma_f16(acc[nt][u], a, qf[w][nt][u][c][0], qf[w][nt][u][c][1]);
+                            for (int w = 0; w < TERMS; ++w) {
+                                if (c == 0 && w == 0) acc[nt][u][0] = acc[nt][u][1] = acc[nt][u][2] = acc[nt][u][3] = 0.f;
+                                mma_f16(acc[nt][u], a, qf[w][nt][u][c][0], qf[w][nt][u][c][1]);
+                            }
                         }
-                    }
                 }
                 uint32_t p0[G], p1[G];
                 token_params<G>(kp + (uint32_t)(pa * 4 * G), p0);
@@ -361,62 +361,75 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT>::CTAS)
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float y = 0.f;
 #pragma unroll
                         for (int u = 0; u < G; ++u) {
-                            const float ks = quant_step(e < 2 ? p0[u] : p1[u]);
-                            const float kz = fmaf(C::Z, ks, quant_lowest(e < 2 ? p0[u] : p1[u]));
-                            y = fmaf(ks, acc[nt][u][e], fmaf(kz, qs[nt][u][e & 1], y));
+                            const uint32_t par = e < 2 ? p0[u] : p1[u];
+                            const float low = quant_lowest(par) * qs[nt][u][e & 1];
+                            y[nt][e] = fmaf(quant_step(par), acc[nt][u][e], u == 0 ? low : y[nt][e] + low);
                         }
-                        x[nt][e] = y * rs[nt][e & 1];
                     }
             }
-            uint32_t q0[G], q1[G];
-            token_params<G>(vp + (uint32_t)(pa * 4 * G), q0);
-            token_params<G>(vp + (uint32_t)((pa + 8) * 4 * G), q1);
+            uint32_t v0[G], v1[G];
+            token_params<G>(vp + (uint32_t)(pa * 4 * G), v0);
+            token_params<G>(vp + (uint32_t)((pa + 8) * 4 * G), v1);
             if (edge) {  // tokens at or past the length hold anything
                 const int ta = t0 + pa, tb = ta + 8;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if ((e < 2 ? ta : tb) >= lim[nt][e & 1]) x[nt][e] = -INFINITY;
+                    for (int e = 0; e < 2; ++e) {
+                        const int t = (r0 + min(8 * nt + 2 * tig + e, nr - 1)) % s.T_q;  // sees tokens below lim_min + t
+                        if (ta >= lim_min + t) y[nt][e] = -INFINITY;
+                        if (tb >= lim_min + t) y[nt][e + 2] = -INFINITY;
+                    }
 #pragma unroll
                 for (int u = 0; u < G; ++u) {
-                    if (ta >= L) q0[u] = 0;
-                    if (tb >= L) q1[u] = 0;
+                    if (ta >= L) v0[u] = 0;
+                    if (tb >= L) v1[u] = 0;
                 }
             }
             // references
-            float vmax = 0.f;
-            bool move = false;
+            float ws[2][G], vmax = 0.f;
 #pragma unroll
-            for (int u = 0; u < G; ++u) vmax = fmaxf(vmax, fmaxf(quant_step(q0[u]), quant_step(q1[u])));
-            move = vmax * vs > 128.f;
+            for (int u = 0; u < G; ++u) {
+                ws[0][u] = quant_step(v0[u]) * vs;
+                ws[1][u] = quant_step(v1[u]) * vs;
+                vmax = fmax3(vmax, ws[0][u], ws[1][u]);
+            }
+            bool move = vmax > 128.f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) move = move || fmaxf(x[nt][e], x[nt][e + 2]) > m[nt][e] + 8.f;
+                for (int e = 0; e < 2; ++e) move = move || fmaxf(y[nt][e], y[nt][e + 2]) > far[nt][e];
             if (__any_sync(0xffffffffu, move)) {
+                float step = 0.f, r = 1.f;
 #pragma unroll
-                for (int w = 16; w >= 4; w >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, w));
-                float r = 1.f;
-                if (vmax * vs > 128.f) {
-                    const float now = power2(max(-126, 5 - exponent(vmax)));
+                for (int u = 0; u < G; ++u) step = fmax3(step, quant_step(v0[u]), quant_step(v1[u]));
+#pragma unroll
+                for (int w = 16; w >= 4; w >>= 1) step = fmaxf(step, __shfl_xor_sync(0xffffffffu, step, w));
+                if (step * vs > 128.f) {  // to [32, 64)
+                    const float now = power2(max(-126, 5 - exponent(step)));
                     r = now / vs;
                     vs = now;
+#pragma unroll
+                    for (int u = 0; u < G; ++u) {
+                        ws[0][u] = quant_step(v0[u]) * vs;
+                        ws[1][u] = quant_step(v1[u]) * vs;
+                    }
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float top = fmaxf(x[nt][e], x[nt][e + 2]);
+                        float top = fmaxf(y[nt][e], y[nt][e + 2]);
 #pragma unroll
                         for (int w = 16; w >= 4; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
                         float f = 1.f;
-                        if (top > m[nt][e]) {
-                            f = ex2_approx(m[nt][e] - top);
-                            m[nt][e] = top;
+                        const float now = top * rs[nt][e];
+                        if (now > m[nt][e]) {
+                            f = ex2_approx(m[nt][e] - now);
+                            m[nt][e] = now;
+                            far[nt][e] = top + 8.f / rs[nt][e];
                         }
                         l[nt][e] *= f;
 #pragma unroll
@@ -436,15 +449,15 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT>::CTAS)
             for (int nt = 0; nt < NT; ++nt) {
                 float p[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) p[e] = ex2_approx(x[nt][e] - (m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1]));
+                for (int e = 0; e < 4; ++e) p[e] = ex2_approx(fmaf(y[nt][e], rs[nt][e & 1], -m[nt][e & 1]));
                 l[nt][0] += p[0] + p[2];
                 l[nt][1] += p[1] + p[3];
 #pragma unroll
                 for (int u = 0; u < G; ++u) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint32_t par = h == 0 ? q0[u] : q1[u];
-                        const float st = quant_step(par), z = fmaf(C::Z, st, quant_lowest(par)), w = st * vs;
+                        const uint32_t par = h == 0 ? v0[u] : v1[u];
+                        const float z = quant_lowest(par), w = ws[h][u];
                         om[nt][u][0] = fmaf(p[2 * h], z, om[nt][u][0]);
                         om[nt][u][1] = fmaf(p[2 * h + 1], z, om[nt][u][1]);
                         const float w0 = p[2 * h] * w, w1 = p[2 * h + 1] * w;
@@ -462,8 +475,8 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT>::CTAS)
             for (int u = 0; u < G; ++u) {
                 uint32_t xa[4][2], xb[4][2];
                 const uint32_t col = (uint32_t)((u * kQuantGroup + 8 * gid) * BITS / 8);
-                value_operands<BITS>(vc + (uint32_t)(va * C::ROW) + col, vc + (uint32_t)(vb * C::ROW) + col, xa);
-                value_operands<BITS>(vc + (uint32_t)((va + 8) * C::ROW) + col, vc + (uint32_t)((vb + 8) * C::ROW) + col, xb);
+                value_operands<BITS, TERMS>(vc + (uint32_t)(va * C::ROW) + col, vc + (uint32_t)(vb * C::ROW) + col, xa);
+                value_operands<BITS, TERMS>(vc + (uint32_t)((va + 8) * C::ROW) + col, vc + (uint32_t)((vb + 8) * C::ROW) + col, xb);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const uint32_t a[4] = {xa[c][0], xa[c][1], xb[c][0], xb[c][1]};
@@ -474,9 +487,20 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT>::CTAS)
                 }
             }
         }
-        __syncwarp();  // the stage is read
         ++used;
-        fetch();
+        uint32_t last = 0;
+        __syncwarp();  // the stage is read
+        if (lane == 0) {
+            __threadfence_block();
+            last = atomicAdd(done + slot, 1u) % QM_WARPS == QM_WARPS - 1;
+            __threadfence_block();
+        }
+        if (__shfl_sync(0xffffffffu, last, 0)) {
+            QmNext x = *next;
+            fetch(x);
+            __syncwarp();
+            if (lane == 0) *next = x;
+        }
     }
 
     // this warp's result: rows of D values, m, l
@@ -498,7 +522,8 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT>::CTAS)
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     *reinterpret_cast<float2*>(row + u * kQuantGroup + 8 * gid + 2 * c) =
-                        make_float2(fmaf(o[nt][u][c][e], inv, om[nt][u][e]), fmaf(o[nt][u][c][e + 2], inv, om[nt][u][e]));
+                        make_float2(fmaf(o[nt][u][c][e], inv / unit<BITS, TERMS>(0), om[nt][u][e]),
+                                    fmaf(o[nt][u][c][e + 2], inv / unit<BITS, TERMS>(1), om[nt][u][e]));
             if (gid == 0) *reinterpret_cast<float2*>(row + D) = make_float2(m[nt][e], l[nt][e]);
         }
     __syncthreads();
@@ -509,8 +534,8 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT>::CTAS)
     }
     __syncthreads();
     }
-    if (!ok && lane == 0)  // a copy did not arrive: wait for those in flight, and leave
-        for (int k = used; k < issued; ++k)
+    if (*abort_flag && tid == 0)  // a copy did not arrive: wait for those in flight, and leave
+        for (int k = max(0, next->issued - C::STAGES); k < next->issued; ++k)
             drain_wait_a(bars + 8u * (uint32_t)(k % C::STAGES), (uint32_t)(k / C::STAGES) & 1u);
 }
 
