@@ -321,10 +321,10 @@ def test_decode_large_scores_and_scales(dtype, d, bits):
         got = to_host(layer.decode_quant(to_device(q, dtype), cache, _ints([T])))
         O, A, S = qc.decode(q, *held, h, [T])
         assert np.isfinite(got).all()
-        # a score sums d products of q and the parts s code and m of a key, which may cancel
+        # (rows past T are unset memory) a score sums d products of q and the parts s code and m of a key, which may cancel
         Kv, p = qc.values(held[0], held[1]), np.repeat(held[1], 64, -2)[..., :d, :]
         parts = np.abs(p[..., 1]) + p[..., 0] * (2 ** bits - 1)
-        s = np.max(np.abs(qc.heads(q, h)[0]) @ np.moveaxis(parts[0], -1, -2)) / np.sqrt(d)
+        s = np.max(np.abs(qc.heads(q, h)[0]) @ np.moveaxis(parts[0, :, :T], -1, -2)) / np.sqrt(d)
         w = 2 * s * (d + 8) * 2.0 ** -23
         rounding = 2.0 ** -8 * np.abs(O) + 2.0 ** -11 * S if dtype == "bf16" else 0.0
         assert (np.abs(got - O) <= rounding + (w + 1e-5) * (A + S)).all(), (np.abs(got - O) / (A + S)).max()
