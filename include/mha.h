@@ -479,7 +479,7 @@ mha_status mha_cache_evict(mha_t handle, int B, int T_max, int keep, int recent,
  *   code  (x - m) / s rounded to the nearest whole number, ties to even; it stands for s code + m
  * which is within s / 2 of x.  The codes are those of the real numbers: they do not depend on the machine's
  * rounding.  A group with a value that is not finite in bf16 (NaN, infinite, or an fp32 value above 3.39e38) holds
- * NaN and reads back as NaN; attention that sees such a token gives NaN.
+ * NaN and reads back as NaN; a decode step over a length that includes such a token may give NaN in every row.
  *
  * A cache is one device buffer of mha_quant_cache_size bytes, 256-byte aligned, with four parts at the byte offsets
  * that call gives, each row-major: key codes (B, h_kv, T_max, row bytes), key parameters (B, h_kv, T_max, groups, 2)
@@ -503,7 +503,8 @@ size_t mha_quant_cache_size(mha_t handle, int bits, int B, int T_max, size_t* of
  *                  L_b - n_b .. L_b - 1; other tokens of the cache stay as they are
  * A batch whose L_b or n_b does not satisfy 0 <= n_b <= T_new and n_b <= L_b <= T_max is not touched, and
  * MHA_ERR_BAD_LENGTH is recorded (in an attached workspace's status word; none is needed).  The cache must not
- * overlap an input.  One launch.  MHA_ERR_UNSUPPORTED for h_kv * ceil(d / 64) above 524272.
+ * overlap an input.  One launch.  MHA_ERR_UNSUPPORTED for B * T_new * h_kv beyond 2^31 and more, which no GPU's memory
+ * holds.
  */
 mha_status mha_quant_write(mha_t handle, int bits, int B, int T_max, void* cache, int T_new, const void* K, int64_t ldk,
                            const void* V, int64_t ldv, const int32_t* cache_lengths, const int32_t* counts,

@@ -69,7 +69,8 @@ def test_copy_refusals(handles, call_of):
         assert call(**kw) == bad, kw
     assert call("odd", ldk=96, ldv=96) == L.MHA_ERR_UNSUPPORTED
     assert call("wide", ldk=600, ldv=600) == L.MHA_ERR_UNSUPPORTED
-    assert call("many", B=1, T_max=16, ldk=600000, ldv=600000, **{T: 1}) == L.MHA_ERR_UNSUPPORTED
+    assert call("many", B=1, T_max=1 << 17, ldk=600000, ldv=600000, V=FAKE + (1 << 43), cache=FAKE + (1 << 44),
+                cache_lengths=FAKE + (1 << 45), counts=None, **{T: 1 << 17}) == L.MHA_ERR_UNSUPPORTED
     assert call(B=0) == L.MHA_OK and call(**{T: 0}) == L.MHA_OK
 
 

@@ -24,19 +24,6 @@ struct QuantPlane {
 __host__ __device__ inline int quant_row_bytes(int d, int bits) { return (d + 31) / 32 * 4 * bits; }
 __host__ __device__ inline int quant_groups(int d) { return (d + kQuantGroup - 1) / kQuantGroup; }
 
-// The cache tokens [first, first + n) that rows 0 .. n - 1 of batch b stand for.
-struct QuantRows {
-    int first, n;
-    bool valid;
-};
-__device__ __forceinline__ QuantRows quant_rows(int L, int n, int most, int T_max) {
-    QuantRows r;
-    r.valid = n >= 0 && n <= most && n <= L && L <= T_max;
-    r.n = n;
-    r.first = L - n;
-    return r;
-}
-
 __device__ __forceinline__ float quant_step(uint32_t p) { return __uint_as_float(p << 16); }
 __device__ __forceinline__ float quant_lowest(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
 

@@ -9,9 +9,13 @@
 // depend on how a machine rounds on the way.  A group with a value that is not finite in bf16 gets NaN for s and m
 // and reads back as NaN.
 //
-// Eight lanes hold a group, eight channels each (16 bytes of bf16); a warp takes 16 groups of one token's keys or
-// values, all loads first.  Both directions are bound by HBM.
+// A warp takes a run of tokens of one head's keys or values: 8 lanes a group, 8 channels a lane (16 bytes of bf16, 4
+// or 8 of codes), so codes move in whole pieces and keys in rows of a head; all loads first.  Neighbouring warps have
+// neighbouring heads.
+#include <cuda_bf16.h>
 #include <math.h>
+
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -22,24 +26,56 @@ namespace {
 
 constexpr int QC_THREADS = 256;
 constexpr int QC_WARPS = QC_THREADS / 32;
-constexpr int QC_RUN = 4;                // groups per eight lanes
-constexpr int QC_GROUPS = 4 * QC_RUN;    // groups per warp
+constexpr int QC_WRITE = 4, QC_READ = 8;  // loads of a lane in flight
 constexpr float kBf16Max = 3.3895313892515355e38f;
 
-// Which of a call's rows a warp has: token of the cache, batch; false: none.
-__device__ __forceinline__ bool quant_warp_row(int B, int T, int T_max, const int32_t* lengths, const int32_t* counts,
-                                               int* status, int64_t& row, int& b, int& token) {
-    row = (int64_t)blockIdx.x * QC_WARPS + (threadIdx.x >> 5);
-    if (row >= (int64_t)B * T) return false;
-    b = (int)row / T;
-    const int i = (int)row - b * T;
-    const QuantRows r = quant_rows(lengths[b], counts != nullptr ? counts[b] : T, T, T_max);
-    if (!r.valid) {
-        if (i == 0 && blockIdx.y == 0 && (threadIdx.x & 31) == 0) record_status(status, kStatusBadLength);
+// A call's rows, and how the warps take them: a unit is (batch, `run` x tokens-of-a-warp tokens, head of K or V).
+struct QuantCopy {
+    QuantPlane pk, pv;
+    int64_t ldk, ldv;
+    int B, T, T_max, h_kv;
+    int lanes;        // of a token: 8, 16 or 32
+    unsigned tiles;   // units of a head and sequence
+    unsigned units;
+    const int32_t *lengths, *counts;
+    int* status;
+};
+
+// This lane's part of a unit.
+struct QuantUnit {
+    QuantPlane p;
+    bool values;
+    int b, head;
+    int row, rows;     // first of its rows of the call, and how many the batch has
+    int token;         // of the first row
+    int step;          // rows from one item to the next
+    int sub, c0, n;    // group, first channel, how many of the eight exist
+    __device__ __forceinline__ bool has(int i) const { return row + i * step < rows; }
+};
+
+template <int RUN>
+__device__ __forceinline__ bool quant_unit(const QuantCopy& c, QuantUnit& u) {
+    const unsigned id = blockIdx.x * QC_WARPS + (threadIdx.x >> 5);
+    if (id >= c.units) return false;
+    const unsigned v = id / (2u * c.h_kv), hv = id - v * (2u * c.h_kv), b = v / c.tiles, tile = v - b * c.tiles;
+    u.b = (int)b;
+    u.values = hv >= (unsigned)c.h_kv;
+    u.head = (int)hv - (u.values ? c.h_kv : 0);
+    u.p = u.values ? c.pv : c.pk;
+    const int L = __ldg(c.lengths + b), n = c.counts != nullptr ? __ldg(c.counts + b) : c.T;
+    if (n < 0 || n > c.T || n > L || L > c.T_max) {
+        if (tile == 0 && hv == 0 && (threadIdx.x & 31) == 0) record_status(c.status, kStatusBadLength);
         return false;
     }
-    token = r.first + i;
-    return i < r.n;
+    const int lane = (int)threadIdx.x & 31, in = lane & (c.lanes - 1);
+    u.step = 32 / c.lanes;
+    u.row = (int)tile * RUN * u.step + lane / c.lanes;
+    u.rows = n;
+    u.token = L - n + u.row;
+    u.sub = in >> 3;
+    u.c0 = 8 * in;
+    u.n = max(0, min(8, u.p.d - u.c0));
+    return (int)tile * RUN * u.step < n;
 }
 
 // x to bf16 (as fp32), towards minus infinity.
@@ -55,21 +91,20 @@ __device__ __forceinline__ void two_diff(float a, float b, float& s, float& e) {
     e = __fsub_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fadd_rn(b, bb));
 }
 
-// The smallest bf16 s >= 2^-126 with n s >= hi - m.  n s is exact in fp32.
-__device__ __forceinline__ float group_step(float hi, float m, float n) {
+// The smallest bf16 s >= 2^-126 with N s >= hi - m.  t is below (hi - m) / N by 2^-21 of it, give or take 2^-22, so the
+// step is the first or the second bf16 above t; N s is exact in fp32, and so is its difference from a number near it.
+template <int N>
+__device__ __forceinline__ float group_step(float hi, float m) {
     float a, e;
     two_diff(hi, m, a, e);
-    // from below: a / n less up to 2 units in the last place of bf16, cut; at most 4 units above lies the step
-    float s = __uint_as_float(__float_as_uint(__fmul_rn(__fdiv_rn(a, n), 0.9921875f)) & 0xffff0000u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (__fsub_rn(__fmul_rn(n, s), a) < e) s = __uint_as_float(__float_as_uint(s) + 0x10000u);
-    return fmaxf(s, 1.17549435e-38f);
+    const float t = __fmul_rn(a, (float)((1.0 - 1.0 / 2097152) / N));
+    float s = __uint_as_float((__float_as_uint(t) & 0xffff0000u) + 0x10000u);
+    if (__fsub_rn(__fmul_rn((float)N, s), a) < e) s = __uint_as_float(__float_as_uint(s) + 0x10000u);
+    return a > 0.f ? fmaxf(s, 1.17549435e-38f) : 1.17549435e-38f;
 }
 
-// The code of x: q is (x - m) / s to within 2^-14.
-__device__ __noinline__ int code_at_border(float x, float m, float s, float q) {
-    const float k = floorf(q);
+// The code of an x whose (x - m) / s is next to k + 1/2.
+__device__ __forceinline__ int code_at_border(float x, float m, float s, float k) {
     float a, e;
     two_diff(x, m, a, e);
     // both terms are exact: (k + 1/2) s has at most 17 bits, and a is near it
@@ -78,49 +113,205 @@ __device__ __noinline__ int code_at_border(float x, float m, float s, float q) {
     return over > 0.f ? c + 1 : over < 0.f ? c : c + (c & 1);
 }
 
-__device__ __forceinline__ int code_of(float x, float m, float s, float inv) {
-    const float q = __fmul_rn(__fsub_rn(x, m), inv);  // off by at most 255 * 3 * 2^-24
-    const float r = rintf(q);
-    if (fabsf(q - r) > 0.5f - 6.1e-5f) return code_at_border(x, m, s, q);
-    return (int)r;
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t bmin2(uint32_t a, uint32_t b) {  // bf16 pairs, NaN wins
+    uint32_t d;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// Eight channels of a lane as they come from memory, and their minimum and maximum over the group's eight lanes (NaN if
+// any is).  Maxima are minima of the negated.
+template <typename T, bool VEC>
+struct Eight;
+
 template <bool VEC>
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, int n, float (&x)[8]) {
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (n > 0) v = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+struct Eight<__nv_bfloat16, VEC> {  // groups are whole
+    uint4 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, bool any, int) {
+        v = any ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
     }
-}
+    __device__ __forceinline__ void range(int, float& lo, float& hi) const {
+        constexpr uint32_t neg = 0x80008000u;
+        uint32_t a = bmin2(bmin2(v.x, v.y), bmin2(v.z, v.w));
+        uint32_t b = bmin2(bmin2(v.x ^ neg, v.y ^ neg), bmin2(v.z ^ neg, v.w ^ neg));
+        // (minimum, -maximum) side by side
+        a = bmin2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+#pragma unroll
+        for (int w = 1; w < 8; w <<= 1) a = bmin2(a, __shfl_xor_sync(0xffffffffu, a, w));
+        lo = __uint_as_float(a << 16);
+        hi = -__uint_as_float(a & 0xffff0000u);
+    }
+    // the least magnitude of the lane's values
+    __device__ __forceinline__ float least() const {
+        constexpr uint32_t mag = 0x7fff7fffu;
+        const uint32_t a = bmin2(bmin2(v.x & mag, v.y & mag), bmin2(v.z & mag, v.w & mag));
+        return fminf(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+    }
+    __device__ __forceinline__ void values(float (&x)[8]) const {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
 
 template <bool VEC>
-__device__ __forceinline__ void load8(const float* p, int n, float (&x)[8]) {
-    if constexpr (VEC) {  // n is 0, 4 or 8
-        const float4 a = n > 0 ? __ldg(reinterpret_cast<const float4*>(p)) : make_float4(0.f, 0.f, 0.f, 0.f);
-        const float4 b = n > 4 ? __ldg(reinterpret_cast<const float4*>(p) + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+struct Eight<float, VEC> {
+    float x[8];
+    __device__ __forceinline__ void load(const float* p, bool any, int n) {
+        if constexpr (VEC) {  // n is 0, 4 or 8
+            const float4 a = any && n > 0 ? __ldg(reinterpret_cast<const float4*>(p)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 b = any && n > 4 ? __ldg(reinterpret_cast<const float4*>(p) + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+            x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = any && i < n ? __ldg(p + i) : 0.f;
+        }
+    }
+    __device__ __forceinline__ void range(int n, float& lo, float& hi) const {
+        lo = hi = INFINITY;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) {
+                lo = min_nan(lo, x[i]);
+                hi = min_nan(hi, -x[i]);
+            }
+#pragma unroll
+        for (int w = 1; w < 8; w <<= 1) {
+            lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, w));
+            hi = min_nan(hi, __shfl_xor_sync(0xffffffffu, hi, w));
+        }
+        hi = -hi;
+    }
+    __device__ __forceinline__ float least() const { return 0.f; }
+    __device__ __forceinline__ void values(float (&y)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = x[i];
+    }
+};
+
+// Codes of eight channels (n of them exist), and the group's parameters.
+//
+// q = (x - m) / s in fp32, to about half a unit in its last place: a product with 1 / s, and its remainder's.  Exact
+// quotients, k + 1/2 among them, come out exact, and adding 1.5 * 2^23 rounds to the nearest whole number, ties to even.
+// What is left are quotients so near to k + 1/2 that q may be on its wrong side.  Those of bf16 values need an x - m of
+// more than 20 bits, for which some value (`least`) or m has to be far smaller than the range; with fp32 values any
+// near one is looked at.  They are settled by exact differences.
+template <int BITS, bool F32>
+__device__ __forceinline__ uint32_t eight_codes(float (&x)[8], int n, float lo, float hi, float least, uint32_t (&c)[BITS / 4]) {
+    constexpr int N = (1 << BITS) - 1;
+    constexpr float magic = 12582912.f;  // 1.5 * 2^23
+    constexpr float near = BITS == 4 ? 0.5f - 1.f / 262144 : 0.5f - 1.f / 16384;  // q is off by 2^-20, 2^-16
+    c[0] = 0;
+    if constexpr (BITS == 8) c[1] = 0;
+    if (!(lo >= -kBf16Max && hi <= kBf16Max)) return 0x7fff7fffu;  // NaN
+    float m = bf16_down(lo), f = 1.f;
+    if (hi - m > 3.4e38f) {  // differences would overflow: in halves, which changes no code
+        f = 0.5f;
+        m *= f;
+        hi *= f;
+        least *= f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= f;
+    }
+    const float s = group_step<N>(hi, m);
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    const uint64_t m2 = pack2(-m, -m), inv2 = pack2(inv, inv), step2 = pack2(-s, -s), magic2 = pack2(magic, magic);
+    const uint64_t minus2 = pack2(-1.f, -1.f);
+    float far = 0.f;
+    uint32_t k[8];
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const uint64_t a = add2(pack2(x[i], x[i + 1]), m2), q0 = mul2(a, inv2);
+        const uint64_t q = fma2(fma2(q0, step2, a), inv2, q0), y = add2(q, magic2);
+        float y0, y1, d0, d1;
+        unpack2(y, y0, y1);
+        unpack2(add2(q, fma2(y, minus2, magic2)), d0, d1);
+        far = fmax3(far, fabsf(d0), fabsf(d1));
+        k[i] = __float_as_uint(y0);
+        k[i + 1] = __float_as_uint(y1);
+    }
+    if (far > near && (F32 || fminf(least, fabsf(m)) < (hi - m) * (1.f / 4096))) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float r = __uint_as_float(k[i]) - magic, q = (x[i] - m) * inv, down = q < r ? r - 1.f : r;
+            if (fabsf(q - down - 0.5f) < 1.f / 4096) k[i] = 0x4b400000u + code_at_border(x[i], m, s, down);
+        }
+    }
+    // (the low bits of the sums with 1.5 * 2^23 are the codes)
+    if constexpr (F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) c[i * BITS / 32] += (k[i] - 0x4b400000u) << (i * BITS % 32);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = i < n ? __ldg(p + i) : 0.f;
+        for (int i = 0; i < 8; ++i) c[i * BITS / 32] += k[i] << (i * BITS % 32);
+        constexpr uint32_t all = 0x4b400000u * (BITS == 4 ? 0x11111111u : 0x01010101u);
+        c[0] -= all;
+        if constexpr (BITS == 8) c[1] -= all;
+    }
+    return __float_as_uint(s / f) >> 16 | (__float_as_uint(m / f) & 0xffff0000u);
+}
+
+template <typename T, int BITS, bool VEC>
+__global__ void __launch_bounds__(QC_THREADS)
+    quant_write_kernel(const QuantCopy a, const T* __restrict__ K, const T* __restrict__ V) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    QuantUnit u;
+    if (!quant_unit<QC_WRITE>(a, u)) return;
+    const int64_t ld = u.values ? a.ldv : a.ldk;
+    const T* src = (u.values ? V : K) + ((int64_t)u.b * a.T + u.row) * ld + (int64_t)u.head * u.p.d + u.c0;
+    Eight<T, VEC> in[QC_WRITE];
+#pragma unroll
+    for (int i = 0; i < QC_WRITE; ++i) in[i].load(src + i * u.step * ld, u.has(i) && u.n > 0, u.n);
+    const int64_t head = ((int64_t)u.b * a.h_kv + u.head) * a.T_max;
+    uint8_t* codes = u.p.codes + (head + u.token) * u.p.row + u.c0 * BITS / 8;
+    uint32_t* params = u.p.params + (head + u.token) * u.p.groups + u.sub;
+    const bool store = u.c0 * BITS / 8 < u.p.row, first = (u.c0 & (kQuantGroup - 1)) == 0 && u.sub < u.p.groups;
+#pragma unroll
+    for (int i = 0; i < QC_WRITE; ++i) {
+        float lo, hi, x[8];
+        in[i].range(u.n, lo, hi);
+        if (!u.has(i)) continue;
+        in[i].values(x);
+        uint32_t c[BITS / 4];
+        const uint32_t par = eight_codes<BITS, std::is_same_v<T, float>>(x, u.n, lo, hi, in[i].least(), c);
+        if (store) {
+            uint8_t* to = codes + i * u.step * u.p.row;
+            if constexpr (BITS == 4) *reinterpret_cast<uint32_t*>(to) = c[0];
+            else *reinterpret_cast<uint2*>(to) = make_uint2(c[0], c[1]);
+        }
+        if (first) params[i * u.step * u.p.groups] = par;
     }
 }
 
 template <bool VEC>
-__device__ __forceinline__ void store8(__nv_bfloat16* p, int n, const float (&x)[8]) {
-    if (n > 0)
-        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                                                  pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ void store8(__nv_bfloat16* p, int, const float (&x)[8]) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                                              pack_bf16x2(x[6], x[7]));
 }
 
 template <bool VEC>
 __device__ __forceinline__ void store8(float* p, int n, const float (&x)[8]) {
     if constexpr (VEC) {
-        if (n > 0) *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
         if (n > 4) *(reinterpret_cast<float4*>(p) + 1) = make_float4(x[4], x[5], x[6], x[7]);
     } else {
 #pragma unroll
@@ -129,131 +320,57 @@ __device__ __forceinline__ void store8(float* p, int n, const float (&x)[8]) {
     }
 }
 
-// This thread's channels of its u-th group: head, channel in the head, how many of the eight exist.
-struct QuantEight {
-    int head, sub, c0, n;
-    __device__ __forceinline__ QuantEight(const QuantPlane& p, int h_kv, int chunk, int u) {
-        const int lane = (int)threadIdx.x & 31, gi = chunk * QC_GROUPS + 4 * u + (lane >> 3);
-        head = p.groups == 1 ? gi : gi / p.groups;
-        sub = gi - head * p.groups;
-        c0 = sub * kQuantGroup + 8 * (lane & 7);
-        n = head < h_kv ? max(0, min(8, p.d - c0)) : 0;
-    }
-};
-
 template <typename T, int BITS, bool VEC>
 __global__ void __launch_bounds__(QC_THREADS)
-    quant_write_kernel(const QuantPlane pk, const QuantPlane pv, const T* __restrict__ K, int64_t ldk,
-                       const T* __restrict__ V, int64_t ldv, int B, int T_new, int T_max, int h_kv, int k_chunks,
-                       const int32_t* __restrict__ lengths, const int32_t* __restrict__ counts, int* status) {
-    constexpr int N = (1 << BITS) - 1;
+    quant_read_kernel(const QuantCopy a, T* __restrict__ K, T* __restrict__ V) {
     grid_dependency_wait();
     grid_launch_dependents();
-    int64_t row;
-    int b, token;
-    if (!quant_warp_row(B, T_new, T_max, lengths, counts, status, row, b, token)) return;
-    const bool values = (int)blockIdx.y >= k_chunks;
-    const QuantPlane p = values ? pv : pk;
-    const int chunk = (int)blockIdx.y - (values ? k_chunks : 0);
-    const T* src = values ? V + row * ldv : K + row * ldk;
-    float x[QC_RUN][8];
+    QuantUnit u;
+    if (!quant_unit<QC_READ>(a, u) || u.n <= 0) return;
+    const int64_t ld = u.values ? a.ldv : a.ldk;
+    T* dst = (u.values ? V : K) + ((int64_t)u.b * a.T + u.row) * ld + (int64_t)u.head * u.p.d + u.c0;
+    const int64_t head = ((int64_t)u.b * a.h_kv + u.head) * a.T_max;
+    const uint8_t* codes = u.p.codes + (head + u.token) * u.p.row + u.c0 * BITS / 8;
+    const uint32_t* params = u.p.params + (head + u.token) * u.p.groups + u.sub;
+    uint32_t c[QC_READ][BITS / 4], par[QC_READ];
 #pragma unroll
-    for (int u = 0; u < QC_RUN; ++u) {
-        const QuantEight a(p, h_kv, chunk, u);
-        load8<VEC>(src + (int64_t)a.head * p.d + a.c0, a.n, x[u]);
-    }
-    const int lane = (int)threadIdx.x & 31;
-#pragma unroll
-    for (int u = 0; u < QC_RUN; ++u) {
-        const QuantEight a(p, h_kv, chunk, u);
-        float lo = INFINITY, hi = -INFINITY;
-        bool fine = true;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < a.n) {
-                lo = fminf(lo, x[u][i]);
-                hi = fmaxf(hi, x[u][i]);
-                fine = fine && fabsf(x[u][i]) <= kBf16Max;
-            }
-#pragma unroll
-        for (int w = 1; w < 8; w <<= 1) {
-            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, w));
-            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, w));
+    for (int i = 0; i < QC_READ; ++i) {
+        if (!u.has(i)) continue;
+        const uint8_t* from = codes + i * u.step * u.p.row;
+        if constexpr (BITS == 4) {
+            c[i][0] = __ldg(reinterpret_cast<const uint32_t*>(from));
+        } else {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(from));
+            c[i][0] = w.x;
+            c[i][1] = w.y;
         }
-        const uint32_t good = __ballot_sync(0xffffffffu, fine) >> (lane & 24) & 0xffu;
-        if (a.head >= h_kv) continue;
-        uint32_t par = 0x7fff7fffu;  // NaN
-        uint32_t c[BITS == 4 ? 1 : 2] = {};
-        if (good == 0xffu) {
-            float m = bf16_down(lo), f = 1.f;
-            if (hi - m > 3.4e38f) {  // differences would overflow: in halves, which changes no code
-                f = 0.5f;
-                m *= f;
-                hi *= f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[u][i] *= f;
-            }
-            const float s = group_step(hi, m, (float)N), inv = __fdiv_rn(1.f, s);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < a.n) c[i * BITS / 32] |= (uint32_t)min(code_of(x[u][i], m, s, inv), N) << (i * BITS % 32);
-            par = __float_as_uint(s / f) >> 16 | (__float_as_uint(m / f) & 0xffff0000u);
-        }
-        const int64_t at = ((int64_t)b * h_kv + a.head) * T_max + token;
-        if (a.c0 * BITS / 8 < p.row) {
-            uint8_t* out = p.codes + at * p.row + a.c0 * BITS / 8;
-            if constexpr (BITS == 4) *reinterpret_cast<uint32_t*>(out) = c[0];
-            else *reinterpret_cast<uint2*>(out) = make_uint2(c[0], c[1]);
-        }
-        if ((lane & 7) == 0) p.params[at * p.groups + a.sub] = par;
-    }
-}
-
-template <typename T, int BITS, bool VEC>
-__global__ void __launch_bounds__(QC_THREADS)
-    quant_read_kernel(const QuantPlane pk, const QuantPlane pv, T* __restrict__ K, int64_t ldk, T* __restrict__ V,
-                      int64_t ldv, int B, int T_out, int T_max, int h_kv, int k_chunks,
-                      const int32_t* __restrict__ lengths, const int32_t* __restrict__ counts, int* status) {
-    grid_dependency_wait();
-    grid_launch_dependents();
-    int64_t row;
-    int b, token;
-    if (!quant_warp_row(B, T_out, T_max, lengths, counts, status, row, b, token)) return;
-    const bool values = (int)blockIdx.y >= k_chunks;
-    const QuantPlane p = values ? pv : pk;
-    const int chunk = (int)blockIdx.y - (values ? k_chunks : 0);
-    T* dst = values ? V + row * ldv : K + row * ldk;
-    uint2 c[QC_RUN];
-    uint32_t par[QC_RUN];
-#pragma unroll
-    for (int u = 0; u < QC_RUN; ++u) {
-        const QuantEight a(p, h_kv, chunk, u);
-        const int64_t at = ((int64_t)b * h_kv + a.head) * T_max + token;
-        c[u] = make_uint2(0u, 0u);
-        par[u] = 0;
-        if (a.n > 0) {
-            const uint8_t* in = p.codes + at * p.row + a.c0 * BITS / 8;
-            if constexpr (BITS == 4) c[u].x = __ldg(reinterpret_cast<const uint32_t*>(in));
-            else c[u] = __ldg(reinterpret_cast<const uint2*>(in));
-            par[u] = __ldg(p.params + at * p.groups + a.sub);
-        }
+        par[i] = __ldg(params + i * u.step * u.p.groups);
     }
 #pragma unroll
-    for (int u = 0; u < QC_RUN; ++u) {
-        const QuantEight a(p, h_kv, chunk, u);
-        const float s = quant_step(par[u]), m = quant_lowest(par[u]);
+    for (int i = 0; i < QC_READ; ++i) {
+        if (!u.has(i)) continue;
+        const float s = quant_step(par[i]), m = quant_lowest(par[i]);
+        const uint64_t s2 = pack2(s, s), m2 = pack2(m, m), base2 = pack2(-8388608.f, -8388608.f);
+        // bytes as fp32 numbers of 2^23 and more
+        uint32_t by[2];
+        if constexpr (BITS == 4) by[0] = c[i][0] & 0x0f0f0f0fu, by[1] = c[i][0] >> 4 & 0x0f0f0f0fu;
+        else by[0] = c[i][0], by[1] = c[i][1];
         float x[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t w = i * BITS < 32 ? c[u].x : c[u].y;
-            x[i] = fmaf((float)(w >> (i * BITS % 32) & ((1 << BITS) - 1)), s, m);  // s code is exact
+        for (int j = 0; j < 8; j += 2) {
+            uint32_t f0, f1;
+            if constexpr (BITS == 4) {
+                f0 = __byte_perm(by[0], 0x4b000000u, 0x7440 | (j / 2));
+                f1 = __byte_perm(by[1], 0x4b000000u, 0x7440 | (j / 2));
+            } else {
+                f0 = __byte_perm(by[j / 4], 0x4b000000u, 0x7440 | (j & 3));
+                f1 = __byte_perm(by[j / 4], 0x4b000000u, 0x7440 | ((j + 1) & 3));
+            }
+            const uint64_t code = add2(pack2(__uint_as_float(f0), __uint_as_float(f1)), base2);
+            unpack2(fma2(code, s2, m2), x[j], x[j + 1]);  // s code is exact
         }
-        store8<VEC>(dst + (int64_t)a.head * p.d + a.c0, a.n, x);
+        store8<VEC>(dst + i * u.step * ld, u.n, x);
     }
-}
-
-int chunks(const QuantPlane& p, int h_kv) {
-    return (int)(((int64_t)h_kv * p.groups + QC_GROUPS - 1) / QC_GROUPS);
 }
 
 bool vec_ok(const QuantPlane& p, const void* x, int64_t ld) {
@@ -262,23 +379,46 @@ bool vec_ok(const QuantPlane& p, const void* x, int64_t ld) {
 
 }  // namespace
 
-bool quant_copy_fits(const QuantPlane& pk, const QuantPlane& pv, int h_kv) {
-    return (int64_t)h_kv * pk.groups <= (int64_t)32767 * QC_GROUPS && (int64_t)h_kv * pv.groups <= (int64_t)32767 * QC_GROUPS;
+// Units of a call; 0: more than a grid takes.
+unsigned quant_copy_units(bool write, const QuantPlane& pk, const QuantPlane& pv, int B, int T, int h_kv, int* lanes, unsigned* tiles) {
+    const int groups = pk.groups > pv.groups ? pk.groups : pv.groups;
+    *lanes = groups == 1 ? 8 : groups == 2 ? 16 : 32;
+    const int tokens = 32 / *lanes * (write ? QC_WRITE : QC_READ);
+    *tiles = (unsigned)(((int64_t)T + tokens - 1) / tokens);
+    const double units = (double)B * *tiles * 2.0 * h_kv;
+    return units > (double)INT32_MAX ? 0u : (unsigned)units;
+}
+
+bool quant_copy_fits(bool write, const QuantPlane& pk, const QuantPlane& pv, int B, int T, int h_kv) {
+    int lanes;
+    unsigned tiles;
+    return quant_copy_units(write, pk, pv, B, T, h_kv, &lanes, &tiles) > 0;
 }
 
 cudaError_t launch_quant_copy(bool write, bool f32, int bits, const QuantPlane& pk, const QuantPlane& pv, void* K,
                               int64_t ldk, void* V, int64_t ldv, int B, int T, int T_max, int h_kv,
                               const int32_t* lengths, const int32_t* counts, int* status, cudaStream_t stream) {
-    const int kc = chunks(pk, h_kv), vc = chunks(pv, h_kv);
-    const dim3 grid((unsigned)(((int64_t)B * T + QC_WARPS - 1) / QC_WARPS), (unsigned)(kc + vc));
+    QuantCopy a;
+    a.pk = pk;
+    a.pv = pv;
+    a.ldk = ldk;
+    a.ldv = ldv;
+    a.B = B;
+    a.T = T;
+    a.T_max = T_max;
+    a.h_kv = h_kv;
+    a.units = quant_copy_units(write, pk, pv, B, T, h_kv, &a.lanes, &a.tiles);
+    if (a.units == 0) return cudaErrorInvalidValue;
+    a.lengths = lengths;
+    a.counts = counts;
+    a.status = status;
+    const dim3 grid((a.units + QC_WARPS - 1) / QC_WARPS);
     const bool vec = !f32 || (vec_ok(pk, K, ldk) && vec_ok(pv, V, ldv));
     auto go = [&](auto* x, auto kw, auto kr) {
         using T_ = std::remove_pointer_t<decltype(x)>;
         if (write)
-            return launch_pdl(kw, grid, dim3(QC_THREADS), 0, stream, pk, pv, static_cast<const T_*>(K), ldk,
-                              static_cast<const T_*>(V), ldv, B, T, T_max, h_kv, kc, lengths, counts, status);
-        return launch_pdl(kr, grid, dim3(QC_THREADS), 0, stream, pk, pv, static_cast<T_*>(K), ldk, static_cast<T_*>(V), ldv,
-                          B, T, T_max, h_kv, kc, lengths, counts, status);
+            return launch_pdl(kw, grid, dim3(QC_THREADS), 0, stream, a, static_cast<const T_*>(K), static_cast<const T_*>(V));
+        return launch_pdl(kr, grid, dim3(QC_THREADS), 0, stream, a, static_cast<T_*>(K), static_cast<T_*>(V));
     };
 #define MHA_QC(T, BITS, VEC) return go(static_cast<T*>(nullptr), quant_write_kernel<T, BITS, VEC>, quant_read_kernel<T, BITS, VEC>)
     if (!f32) {
