@@ -158,7 +158,7 @@ struct QuantPlane;  // quant.cuh
 struct QuantStep;
 
 // mha_quant_write (write) and mha_quant_read; quant_copy_fits: is there a grid for so much?
-bool quant_copy_fits(bool write, const QuantPlane& pk, const QuantPlane& pv, int B, int T, int h_kv);
+bool quant_copy_fits(bool write, bool f32, const QuantPlane& pk, const QuantPlane& pv, int B, int T, int h_kv);
 cudaError_t launch_quant_copy(bool write, bool f32, int bits, const QuantPlane& pk, const QuantPlane& pv, void* K,
                               int64_t ldk, void* V, int64_t ldv, int B, int T, int T_max, int h_kv,
                               const int32_t* lengths, const int32_t* counts, int* status, cudaStream_t stream);

@@ -87,7 +87,7 @@ mha_status copy(mha_s* m, bool write, int bits, int B, int T_max, const void* ca
             if (ldk != ldv || col < wd.k * (int64_t)s || col + wd.v * (int64_t)s > ld) return MHA_ERR_INVALID_ARG;
         }
     }
-    if (!quant_copy_fits(write, c.k, c.v, B, T, m->h_kv)) return MHA_ERR_UNSUPPORTED;
+    if (!quant_copy_fits(write, m->dtype == MHA_F32, c.k, c.v, B, T, m->h_kv)) return MHA_ERR_UNSUPPORTED;
     const cudaError_t err = launch_quant_copy(write, m->dtype == MHA_F32, bits, c.k, c.v, const_cast<void*>(K), ldk,
                                               const_cast<void*>(V), ldv, B, T, T_max, m->h_kv, lengths, counts,
                                               status_ptr(m), static_cast<cudaStream_t>(stream));

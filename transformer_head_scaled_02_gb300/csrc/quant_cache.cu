@@ -26,8 +26,25 @@ namespace {
 
 constexpr int QC_THREADS = 256;
 constexpr int QC_WARPS = QC_THREADS / 32;
-constexpr int QC_WRITE = 4, QC_READ = 8;  // loads of a lane in flight
+// Items (8 channels) of a lane: many where there is work for every SM, few for calls whose warps would be too few.  Few |
+// many, us: 3 x 1001 tokens of 8 heads of 64 in fp32 and 8 bits, written 4.8 | 5.8, read 5.3 | 7.8; 4 x 2048 of 16 heads
+// in bf16 and 4 bits, written 13.2 | 10.1, read 8.2 | 6.1.
+constexpr int kFewItems = 2;
+template <typename T>
+constexpr int kWriteItems = sizeof(T) == 2 ? 8 : 4;
+constexpr int kReadItems = 8;
+constexpr unsigned kFewUnits = 4096;  // warps below which a call is short
 constexpr float kBf16Max = 3.3895313892515355e38f;
+
+// Division of numbers below 2^31 by a number known on the host.
+struct Divide {
+    uint32_t mul, shift, by;
+    __host__ explicit Divide(uint32_t d = 1) : shift(0), by(d) {
+        while ((1ull << shift) < d) ++shift;
+        mul = (uint32_t)(((((uint64_t)1 << shift) - d) << 32) / d + 1);  // 2^(32 + shift) / d, upwards, less 2^32
+    }
+    __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
 
 // A call's rows, and how the warps take them: a unit is (batch, `run` x tokens-of-a-warp tokens, head of K or V).
 struct QuantCopy {
@@ -35,7 +52,8 @@ struct QuantCopy {
     int64_t ldk, ldv;
     int B, T, T_max, h_kv;
     int lanes;        // of a token: 8, 16 or 32
-    unsigned tiles;   // units of a head and sequence
+    Divide tiles;     // units of a head and sequence
+    Divide heads;     // of keys and values together
     unsigned units;
     const int32_t *lengths, *counts;
     int* status;
@@ -57,7 +75,7 @@ template <int RUN>
 __device__ __forceinline__ bool quant_unit(const QuantCopy& c, QuantUnit& u) {
     const unsigned id = blockIdx.x * QC_WARPS + (threadIdx.x >> 5);
     if (id >= c.units) return false;
-    const unsigned v = id / (2u * c.h_kv), hv = id - v * (2u * c.h_kv), b = v / c.tiles, tile = v - b * c.tiles;
+    const unsigned v = c.heads(id), hv = id - v * c.heads.by, b = c.tiles(v), tile = v - b * c.tiles.by;
     u.b = (int)b;
     u.values = hv >= (unsigned)c.h_kv;
     u.head = (int)hv - (u.values ? c.h_kv : 0);
@@ -131,8 +149,14 @@ __device__ __forceinline__ uint32_t bmin2(uint32_t a, uint32_t b) {  // bf16 pai
     return d;
 }
 
-// Eight channels of a lane as they come from memory, and their minimum and maximum over the group's eight lanes (NaN if
-// any is).  Maxima are minima of the negated.
+__device__ __forceinline__ uint32_t bmax2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// Eight channels of a lane as they come from memory, their minimum and maximum (NaN if any is; maxima are minima of the
+// negated), and how these meet with other lanes'.
 template <typename T, bool VEC>
 struct Eight;
 
@@ -142,22 +166,22 @@ struct Eight<__nv_bfloat16, VEC> {  // groups are whole
     __device__ __forceinline__ void load(const __nv_bfloat16* p, bool any, int) {
         v = any ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
     }
-    __device__ __forceinline__ void range(int, float& lo, float& hi) const {
-        constexpr uint32_t neg = 0x80008000u;
-        uint32_t a = bmin2(bmin2(v.x, v.y), bmin2(v.z, v.w));
-        uint32_t b = bmin2(bmin2(v.x ^ neg, v.y ^ neg), bmin2(v.z ^ neg, v.w ^ neg));
-        // (minimum, -maximum) side by side
-        a = bmin2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
-#pragma unroll
-        for (int w = 1; w < 8; w <<= 1) a = bmin2(a, __shfl_xor_sync(0xffffffffu, a, w));
-        lo = __uint_as_float(a << 16);
-        hi = -__uint_as_float(a & 0xffff0000u);
+    using Range = uint32_t;  // (minimum, -maximum) side by side
+    __device__ __forceinline__ Range range(int) const {
+        const uint32_t a = bmin2(bmin2(v.x, v.y), bmin2(v.z, v.w));
+        const uint32_t b = bmax2(bmax2(v.x, v.y), bmax2(v.z, v.w)) ^ 0x80008000u;
+        return bmin2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
     }
-    // the least magnitude of the lane's values
-    __device__ __forceinline__ float least() const {
+    __device__ __forceinline__ static Range meet(Range a, Range b) { return bmin2(a, b); }
+    __device__ __forceinline__ static Range other(Range a, int w) { return __shfl_xor_sync(0xffffffffu, a, w); }
+    __device__ __forceinline__ static float lo(Range a) { return __uint_as_float(a << 16); }
+    __device__ __forceinline__ static float hi(Range a) { return -__uint_as_float(a & 0xffff0000u); }
+    static constexpr bool kWhole = true;
+    // the least magnitude of m and the lane's values
+    __device__ __forceinline__ float least(float m) const {
         constexpr uint32_t mag = 0x7fff7fffu;
         const uint32_t a = bmin2(bmin2(v.x & mag, v.y & mag), bmin2(v.z & mag, v.w & mag));
-        return fminf(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+        return fminf(fabsf(m), fminf(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u)));
     }
     __device__ __forceinline__ void values(float (&x)[8]) const {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -183,122 +207,177 @@ struct Eight<float, VEC> {
             for (int i = 0; i < 8; ++i) x[i] = any && i < n ? __ldg(p + i) : 0.f;
         }
     }
-    __device__ __forceinline__ void range(int n, float& lo, float& hi) const {
-        lo = hi = INFINITY;
+    using Range = float2;  // minimum, -maximum
+    __device__ __forceinline__ Range range(int n) const {
+        Range a = make_float2(INFINITY, INFINITY);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < n) {
-                lo = min_nan(lo, x[i]);
-                hi = min_nan(hi, -x[i]);
-            }
-#pragma unroll
-        for (int w = 1; w < 8; w <<= 1) {
-            lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, w));
-            hi = min_nan(hi, __shfl_xor_sync(0xffffffffu, hi, w));
-        }
-        hi = -hi;
+            if (i < n) a = make_float2(min_nan(a.x, x[i]), min_nan(a.y, -x[i]));
+        return a;
     }
-    __device__ __forceinline__ float least() const { return 0.f; }
+    __device__ __forceinline__ static Range meet(Range a, Range b) { return make_float2(min_nan(a.x, b.x), min_nan(a.y, b.y)); }
+    __device__ __forceinline__ static Range other(Range a, int w) {
+        return make_float2(__shfl_xor_sync(0xffffffffu, a.x, w), __shfl_xor_sync(0xffffffffu, a.y, w));
+    }
+    __device__ __forceinline__ static float lo(Range a) { return a.x; }
+    __device__ __forceinline__ static float hi(Range a) { return -a.y; }
+    static constexpr bool kWhole = false;
+    __device__ __forceinline__ float least(float) const { return 0.f; }
     __device__ __forceinline__ void values(float (&y)[8]) const {
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = x[i];
     }
 };
 
-// Codes of eight channels (n of them exist), and the group's parameters.
+// What a group's codes are computed with.  inv is 1 / s to a unit in its last place; NaN: no codes (a value that is not
+// finite); below zero: in halves, as differences would overflow.
+struct QuantScale {
+    float m, s, inv;
+    uint32_t params;
+};
+
+template <int N>
+__device__ __forceinline__ QuantScale group_scale(float lo, float hi) {
+    QuantScale g;
+    if (!(lo >= -kBf16Max && hi <= kBf16Max)) {
+        g.m = 0.f;
+        g.s = g.inv = NAN;
+        g.params = 0x7fff7fffu;
+        return g;
+    }
+    g.m = bf16_down(lo);
+    const bool halves = hi - g.m > 3.4e38f;
+    if (halves) {
+        g.m *= 0.5f;
+        hi *= 0.5f;
+    }
+    g.s = group_step<N>(hi, g.m);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(g.inv) : "f"(g.s));
+    const float back = halves ? 2.f : 1.f;
+    g.params = __float_as_uint(g.s * back) >> 16 | (__float_as_uint(g.m * back) & 0xffff0000u);
+    if (halves) g.inv = -g.inv;
+    return g;
+}
+
+// Codes of eight channels (n of them exist).
 //
 // q = (x - m) / s in fp32, to about half a unit in its last place: a product with 1 / s, and its remainder's.  Exact
 // quotients, k + 1/2 among them, come out exact, and adding 1.5 * 2^23 rounds to the nearest whole number, ties to even.
 // What is left are quotients so near to k + 1/2 that q may be on its wrong side.  Those of bf16 values need an x - m of
 // more than 20 bits, for which some value (`least`) or m has to be far smaller than the range; with fp32 values any
 // near one is looked at.  They are settled by exact differences.
-template <int BITS, bool F32>
-__device__ __forceinline__ uint32_t eight_codes(float (&x)[8], int n, float lo, float hi, float least, uint32_t (&c)[BITS / 4]) {
+template <int BITS, typename E>
+__device__ __forceinline__ void eight_codes(const E& in, int n, float m, float s, float inv, uint32_t (&c)[BITS / 4]) {
     constexpr int N = (1 << BITS) - 1;
     constexpr float magic = 12582912.f;  // 1.5 * 2^23
     constexpr float near = BITS == 4 ? 0.5f - 1.f / 262144 : 0.5f - 1.f / 16384;  // q is off by 2^-20, 2^-16
-    c[0] = 0;
-    if constexpr (BITS == 8) c[1] = 0;
-    if (!(lo >= -kBf16Max && hi <= kBf16Max)) return 0x7fff7fffu;  // NaN
-    float m = bf16_down(lo), f = 1.f;
-    if (hi - m > 3.4e38f) {  // differences would overflow: in halves, which changes no code
-        f = 0.5f;
-        m *= f;
-        hi *= f;
-        least *= f;
+    float x[8];
+    in.values(x);
+    if (!(inv > 0.f)) {  // NaN, or in halves, which changes no code
+        inv = -inv;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= f;
+        for (int i = 0; i < 8; ++i) x[i] *= 0.5f;
     }
-    const float s = group_step<N>(hi, m);
-    float inv;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    if constexpr (!E::kWhole)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = i < n ? x[i] : m;  // code 0
     const uint64_t m2 = pack2(-m, -m), inv2 = pack2(inv, inv), step2 = pack2(-s, -s), magic2 = pack2(magic, magic);
     const uint64_t minus2 = pack2(-1.f, -1.f);
     float far = 0.f;
-    uint32_t k[8];
+    uint64_t r2[4];  // the codes, negated, of channels i and i + 4
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-        const uint64_t a = add2(pack2(x[i], x[i + 1]), m2), q0 = mul2(a, inv2);
-        const uint64_t q = fma2(fma2(q0, step2, a), inv2, q0), y = add2(q, magic2);
-        float y0, y1, d0, d1;
-        unpack2(y, y0, y1);
-        unpack2(add2(q, fma2(y, minus2, magic2)), d0, d1);
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t a = add2(pack2(x[i], x[i + 4]), m2), q0 = mul2(a, inv2);
+        const uint64_t q = fma2(fma2(q0, step2, a), inv2, q0);
+        r2[i] = fma2(add2(q, magic2), minus2, magic2);
+        float d0, d1;
+        unpack2(add2(q, r2[i]), d0, d1);
         far = fmax3(far, fabsf(d0), fabsf(d1));
-        k[i] = __float_as_uint(y0);
-        k[i + 1] = __float_as_uint(y1);
     }
-    if (far > near && (F32 || fminf(least, fabsf(m)) < (hi - m) * (1.f / 4096))) {
+    if (far > near && in.least(m) < (float)N / 2048.f * s) {  // (N s is not below the range, or its half)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float r = __uint_as_float(k[i]) - magic, q = (x[i] - m) * inv, down = q < r ? r - 1.f : r;
-            if (fabsf(q - down - 0.5f) < 1.f / 4096) k[i] = 0x4b400000u + code_at_border(x[i], m, s, down);
+        for (int i = 0; i < 4; ++i) {
+            float r[2];
+            unpack2(r2[i], r[0], r[1]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float v = x[i + 4 * h], q = (v - m) * inv, down = q < -r[h] ? -r[h] - 1.f : -r[h];
+                if (fabsf(q - down - 0.5f) < 1.f / 4096) r[h] = -(float)code_at_border(v, m, s, down);
+            }
+            r2[i] = pack2(r[0], r[1]);
         }
     }
-    // (the low bits of the sums with 1.5 * 2^23 are the codes)
-    if constexpr (F32) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) c[i * BITS / 32] += (k[i] - 0x4b400000u) << (i * BITS % 32);
+    // side by side: sums below 2^16 with 1.5 * 2^23, whose low bits they are
+    auto put2 = [](uint64_t r, float at, uint64_t y) { return fma2(r, pack2(-at, -at), y); };
+    float y0, y1;
+    if constexpr (BITS == 4) {
+        unpack2(put2(r2[3], 4096.f, put2(r2[2], 256.f, put2(r2[1], 16.f, put2(r2[0], 1.f, magic2)))), y0, y1);
+        c[0] = __byte_perm(__float_as_uint(y0), __float_as_uint(y1), 0x5410);
     } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) c[i * BITS / 32] += k[i] << (i * BITS % 32);
-        constexpr uint32_t all = 0x4b400000u * (BITS == 4 ? 0x11111111u : 0x01010101u);
-        c[0] -= all;
-        if constexpr (BITS == 8) c[1] -= all;
+        float y2, y3;
+        unpack2(put2(r2[1], 256.f, put2(r2[0], 1.f, magic2)), y0, y1);
+        unpack2(put2(r2[3], 256.f, put2(r2[2], 1.f, magic2)), y2, y3);
+        c[0] = __byte_perm(__float_as_uint(y0), __float_as_uint(y2), 0x5410);
+        c[1] = __byte_perm(__float_as_uint(y1), __float_as_uint(y3), 0x5410);
     }
-    return __float_as_uint(s / f) >> 16 | (__float_as_uint(m / f) & 0xffff0000u);
+    if (inv != inv)
+#pragma unroll
+        for (int i = 0; i < BITS / 4; ++i) c[i] = 0;
 }
 
-template <typename T, int BITS, bool VEC>
-__global__ void __launch_bounds__(QC_THREADS)
+// The group's eight lanes share the work on its scale: the ranges of their RUN items meet by halving, after which a
+// lane has one item's range of the group, computes that item's scale and hands it out.  (With every lane computing
+// every scale an item took 171 instructions instead of about 100, and a long write 240 us instead of 150.)
+template <typename T, int BITS, bool VEC, int RUN>
+__global__ void __launch_bounds__(QC_THREADS, 4)  // (24 warps an SM instead of 32: 164 us of the long write, not 153)
     quant_write_kernel(const QuantCopy a, const T* __restrict__ K, const T* __restrict__ V) {
+    using E = Eight<T, VEC>;
     grid_dependency_wait();
     grid_launch_dependents();
     QuantUnit u;
-    if (!quant_unit<QC_WRITE>(a, u)) return;
+    if (!quant_unit<RUN>(a, u)) return;
     const int64_t ld = u.values ? a.ldv : a.ldk;
     const T* src = (u.values ? V : K) + ((int64_t)u.b * a.T + u.row) * ld + (int64_t)u.head * u.p.d + u.c0;
-    Eight<T, VEC> in[QC_WRITE];
+    E in[RUN];
 #pragma unroll
-    for (int i = 0; i < QC_WRITE; ++i) in[i].load(src + i * u.step * ld, u.has(i) && u.n > 0, u.n);
+    for (int i = 0; i < RUN; ++i, src += u.step * ld) in[i].load(src, u.has(i) && u.n > 0, u.n);
     const int64_t head = ((int64_t)u.b * a.h_kv + u.head) * a.T_max;
     uint8_t* codes = u.p.codes + (head + u.token) * u.p.row + u.c0 * BITS / 8;
     uint32_t* params = u.p.params + (head + u.token) * u.p.groups + u.sub;
-    const bool store = u.c0 * BITS / 8 < u.p.row, first = (u.c0 & (kQuantGroup - 1)) == 0 && u.sub < u.p.groups;
+    const bool store = u.c0 * BITS / 8 < u.p.row, param = u.sub < u.p.groups;
+    const int lane = (int)threadIdx.x & 31;
+    typename E::Range range[RUN];
 #pragma unroll
-    for (int i = 0; i < QC_WRITE; ++i) {
-        float lo, hi, x[8];
-        in[i].range(u.n, lo, hi);
-        if (!u.has(i)) continue;
-        in[i].values(x);
-        uint32_t c[BITS / 4];
-        const uint32_t par = eight_codes<BITS, std::is_same_v<T, float>>(x, u.n, lo, hi, in[i].least(), c);
-        if (store) {
-            uint8_t* to = codes + i * u.step * u.p.row;
-            if constexpr (BITS == 4) *reinterpret_cast<uint32_t*>(to) = c[0];
-            else *reinterpret_cast<uint2*>(to) = make_uint2(c[0], c[1]);
+    for (int i = 0; i < RUN; ++i) range[i] = in[i].range(u.n);
+    int mine = 0;  // item whose range this lane ends up with
+#pragma unroll
+    for (int w = 1, left = RUN; w < 8; w <<= 1) {
+        if (left > 1) {
+            left /= 2;
+            const bool upper = (lane & w) != 0;
+            mine += upper ? left : 0;
+#pragma unroll
+            for (int i = 0; i < left; ++i) {
+                const typename E::Range keep = upper ? range[i + left] : range[i], give = upper ? range[i] : range[i + left];
+                range[i] = E::meet(keep, E::other(give, w));
+            }
+        } else {
+            range[0] = E::meet(range[0], E::other(range[0], w));
         }
-        if (first) params[i * u.step * u.p.groups] = par;
+    }
+    const QuantScale g = group_scale<(1 << BITS) - 1>(E::lo(range[0]), E::hi(range[0]));
+    if (param && (lane & 7) < RUN && u.has(mine)) params[mine * u.step * u.p.groups] = g.params;
+#pragma unroll
+    for (int i = 0; i < RUN; ++i, codes += u.step * u.p.row) {
+        // the lane of the eight that has item i: its bits from the highest on
+        const int from = (lane & 24) | (RUN == 8 ? (i >> 2 & 1) | (i & 2) | (i << 2 & 4) : RUN == 4 ? (i >> 1 & 1) | (i << 1 & 2) : i);
+        const float m = __shfl_sync(0xffffffffu, g.m, from), s = __shfl_sync(0xffffffffu, g.s, from),
+                    inv = __shfl_sync(0xffffffffu, g.inv, from);
+        if (!u.has(i) || !store) continue;
+        uint32_t c[BITS / 4];
+        eight_codes<BITS>(in[i], u.n, m, s, inv, c);
+        if constexpr (BITS == 4) *reinterpret_cast<uint32_t*>(codes) = c[0];
+        else *reinterpret_cast<uint2*>(codes) = make_uint2(c[0], c[1]);
     }
 }
 
@@ -320,21 +399,21 @@ __device__ __forceinline__ void store8(float* p, int n, const float (&x)[8]) {
     }
 }
 
-template <typename T, int BITS, bool VEC>
+template <typename T, int BITS, bool VEC, int RUN>
 __global__ void __launch_bounds__(QC_THREADS)
     quant_read_kernel(const QuantCopy a, T* __restrict__ K, T* __restrict__ V) {
     grid_dependency_wait();
     grid_launch_dependents();
     QuantUnit u;
-    if (!quant_unit<QC_READ>(a, u) || u.n <= 0) return;
+    if (!quant_unit<RUN>(a, u) || u.n <= 0) return;
     const int64_t ld = u.values ? a.ldv : a.ldk;
     T* dst = (u.values ? V : K) + ((int64_t)u.b * a.T + u.row) * ld + (int64_t)u.head * u.p.d + u.c0;
     const int64_t head = ((int64_t)u.b * a.h_kv + u.head) * a.T_max;
     const uint8_t* codes = u.p.codes + (head + u.token) * u.p.row + u.c0 * BITS / 8;
     const uint32_t* params = u.p.params + (head + u.token) * u.p.groups + u.sub;
-    uint32_t c[QC_READ][BITS / 4], par[QC_READ];
+    uint32_t c[RUN][BITS / 4], par[RUN];
 #pragma unroll
-    for (int i = 0; i < QC_READ; ++i) {
+    for (int i = 0; i < RUN; ++i) {
         if (!u.has(i)) continue;
         const uint8_t* from = codes + i * u.step * u.p.row;
         if constexpr (BITS == 4) {
@@ -347,7 +426,7 @@ __global__ void __launch_bounds__(QC_THREADS)
         par[i] = __ldg(params + i * u.step * u.p.groups);
     }
 #pragma unroll
-    for (int i = 0; i < QC_READ; ++i) {
+    for (int i = 0; i < RUN; ++i) {
         if (!u.has(i)) continue;
         const float s = quant_step(par[i]), m = quant_lowest(par[i]);
         const uint64_t s2 = pack2(s, s), m2 = pack2(m, m), base2 = pack2(-8388608.f, -8388608.f);
@@ -379,20 +458,23 @@ bool vec_ok(const QuantPlane& p, const void* x, int64_t ld) {
 
 }  // namespace
 
-// Units of a call; 0: more than a grid takes.
-unsigned quant_copy_units(bool write, const QuantPlane& pk, const QuantPlane& pv, int B, int T, int h_kv, int* lanes, unsigned* tiles) {
+// Units of a call with `items` items a lane; 0: more than a grid takes.
+unsigned quant_copy_units(int items, const QuantPlane& pk, const QuantPlane& pv, int B, int T, int h_kv, int* lanes,
+                          unsigned* tiles) {
     const int groups = pk.groups > pv.groups ? pk.groups : pv.groups;
     *lanes = groups == 1 ? 8 : groups == 2 ? 16 : 32;
-    const int tokens = 32 / *lanes * (write ? QC_WRITE : QC_READ);
+    const int tokens = 32 / *lanes * items;
     *tiles = (unsigned)(((int64_t)T + tokens - 1) / tokens);
     const double units = (double)B * *tiles * 2.0 * h_kv;
     return units > (double)INT32_MAX ? 0u : (unsigned)units;
 }
 
-bool quant_copy_fits(bool write, const QuantPlane& pk, const QuantPlane& pv, int B, int T, int h_kv) {
+int most_items(bool write, bool f32) { return !write ? kReadItems : f32 ? kWriteItems<float> : kWriteItems<__nv_bfloat16>; }
+
+bool quant_copy_fits(bool write, bool f32, const QuantPlane& pk, const QuantPlane& pv, int B, int T, int h_kv) {
     int lanes;
     unsigned tiles;
-    return quant_copy_units(write, pk, pv, B, T, h_kv, &lanes, &tiles) > 0;
+    return quant_copy_units(most_items(write, f32), pk, pv, B, T, h_kv, &lanes, &tiles) > 0;
 }
 
 cudaError_t launch_quant_copy(bool write, bool f32, int bits, const QuantPlane& pk, const QuantPlane& pv, void* K,
@@ -407,8 +489,14 @@ cudaError_t launch_quant_copy(bool write, bool f32, int bits, const QuantPlane& 
     a.T = T;
     a.T_max = T_max;
     a.h_kv = h_kv;
-    a.units = quant_copy_units(write, pk, pv, B, T, h_kv, &a.lanes, &a.tiles);
+    unsigned tiles;
+    int items = most_items(write, f32);
+    a.units = quant_copy_units(items, pk, pv, B, T, h_kv, &a.lanes, &tiles);
+    const bool few = a.units < kFewUnits;
+    if (few) a.units = quant_copy_units(kFewItems, pk, pv, B, T, h_kv, &a.lanes, &tiles);
     if (a.units == 0) return cudaErrorInvalidValue;
+    a.tiles = Divide(tiles);
+    a.heads = Divide(2u * (unsigned)h_kv);
     a.lengths = lengths;
     a.counts = counts;
     a.status = status;
@@ -420,18 +508,20 @@ cudaError_t launch_quant_copy(bool write, bool f32, int bits, const QuantPlane& 
             return launch_pdl(kw, grid, dim3(QC_THREADS), 0, stream, a, static_cast<const T_*>(K), static_cast<const T_*>(V));
         return launch_pdl(kr, grid, dim3(QC_THREADS), 0, stream, a, static_cast<T_*>(K), static_cast<T_*>(V));
     };
-#define MHA_QC(T, BITS, VEC) return go(static_cast<T*>(nullptr), quant_write_kernel<T, BITS, VEC>, quant_read_kernel<T, BITS, VEC>)
-    if (!f32) {
-        if (bits == 4) MHA_QC(__nv_bfloat16, 4, true);
-        MHA_QC(__nv_bfloat16, 8, true);
+#define MHA_QC(T, BITS, VEC)                                                                                        \
+    if (f32 == std::is_same_v<T, float> && bits == BITS && vec == VEC) {                                              \
+        T* x = nullptr;                                                                                              \
+        return few ? go(x, quant_write_kernel<T, BITS, VEC, kFewItems>, quant_read_kernel<T, BITS, VEC, kFewItems>)    \
+                   : go(x, quant_write_kernel<T, BITS, VEC, kWriteItems<T>>, quant_read_kernel<T, BITS, VEC, kReadItems>); \
     }
-    if (vec) {
-        if (bits == 4) MHA_QC(float, 4, true);
-        MHA_QC(float, 8, true);
-    }
-    if (bits == 4) MHA_QC(float, 4, false);
-    MHA_QC(float, 8, false);
+    MHA_QC(__nv_bfloat16, 4, true)
+    MHA_QC(__nv_bfloat16, 8, true)
+    MHA_QC(float, 4, true)
+    MHA_QC(float, 8, true)
+    MHA_QC(float, 4, false)
+    MHA_QC(float, 8, false)
 #undef MHA_QC
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace mha

@@ -166,24 +166,19 @@ __global__ void __launch_bounds__(QD_THREADS)
                 for (int e = 0; e < 8; ++e) to[c0 + e] = o[r][e];
         }
         __syncthreads();
-        for (int e = tid; e < nr * pv.d; e += QD_THREADS) {
-            const int r = e / pv.d, c = e - r * pv.d;
-            const float* a = all + r * (dpv + 32);
-            quant_meet<QD_WARPS>(s, z, a + c, a + dpv, R * (dpv + 32), g, r0, r, c, O, ldo, part);
-        }
+        quant_meet<QD_WARPS>(s, z, all, R, dpv + 32, dpv, g, r0, nr, O, ldo, part);
     }
 }
 
-// The join: one output row per block.  The records' maxima and sums are read side by side, then the values, a slice of
-// the records per QJ_THREADS / 64 of the threads.
-constexpr int QJ_THREADS = 256;
-
+// The join: a block per output row.  Threads take the columns, in as many slices of the records as there are threads
+// for; a slice's maxima, sums and values are loaded together, so that a row costs about one round trip to L2, a second
+// one for every eight records of a slice, and the slices meet in shared memory.
 template <typename T>
-__global__ void __launch_bounds__(QJ_THREADS)
+__global__ void __launch_bounds__(1024)
     quant_join_kernel(const QuantStep s, const float* __restrict__ part, T* __restrict__ O, int64_t ldo,
                       const int32_t* __restrict__ lengths) {
-    __shared__ float f[kQuantMaxCtas], top[QJ_THREADS / 32], sum[QJ_THREADS / 32], y[QJ_THREADS];
-    const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ float ys[1024], ms[1024], ls[1024];
+    const int tid = (int)threadIdx.x;
     const int heads = s.h_kv * s.per, row = (int)blockIdx.x;
     const int t = row % s.T_q, bh = row / s.T_q, b = bh / heads, head = bh - b * heads;
     const int g = head / s.per, rr = (head - g * s.per) * s.T_q + t, block = rr / s.rb, r = rr - block * s.rb;
@@ -201,47 +196,53 @@ __global__ void __launch_bounds__(QJ_THREADS)
     const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
     const int nq = quant_quanta(s, __shfl_sync(0xffffffffu, len, src));
     const int first = __shfl_sync(0xffffffffu, at, src) + (g * s.nrb + block) * nq;
+    const int c0 = nq > 0 ? p.owner(first) : 0, n = nq > 0 ? p.owner(first + nq - 1) - c0 + 1 : 0;
+    const int width = s.dv <= 64 ? 64 : s.dv <= 128 ? 128 : 256, slices = (int)blockDim.x / width;
+    const int e = tid % width, slice = tid / width;
+    // record c of the group: of the first CTA its last group, of the others their first
+    const float* rec = part + s.slot(c0, 1, r);
+    const float* others = part + s.slot(c0, 0, r);
+    const int64_t stride = s.slot(1, 0, 0);
     grid_dependency_wait();
     grid_launch_dependents();
-    if (nq == 0) return;  // an invalid length: written as NaN already
-    const int c0 = p.owner(first), n = p.owner(first + nq - 1) - c0 + 1;
-    if (n == 1) return;
-    // record c of the group: of the first CTA its last group, of the others their first
-    auto record = [&](int c) { return part + s.slot(c0 + c, c == 0 ? 1 : 0, r); };
-    float M = -INFINITY, l = 0.f;
-    for (int c = tid; c < n; c += QJ_THREADS) {
-        const float m = __ldcg(record(c));
-        f[c] = m;
-        M = fmaxf(M, m);
+    if (n <= 1) return;  // an invalid length (written as NaN already), or a group that one CTA had alone
+    float M = -INFINITY, l = 0.f, x = 0.f;
+    for (int i0 = slice; i0 < n; i0 += 8 * slices) {
+        float m[8], sum[8], v[8], top = M;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = min(i0 + k * slices, n - 1);
+            const float* a = i == 0 ? rec : others + i * stride;
+            m[k] = i0 + k * slices < n ? __ldcg(a) : -INFINITY;
+            sum[k] = __ldcg(a + 1);
+            v[k] = e < s.dv ? __ldcg(a + 2 + e) : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = fmaxf(top, m[k]);
+        const float f = M == -INFINITY ? 0.f : exp2f(M - top);
+        l *= f;
+        x *= f;
+        M = top;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (m[k] != -INFINITY) {
+                const float fk = exp2f(m[k] - M);
+                l = fmaf(fk, sum[k], l);
+                x = fmaf(fk, v[k], x);
+            }
     }
-#pragma unroll
-    for (int w = 16; w >= 1; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
-    if (lane == 0) top[warp] = M;
+    ys[tid] = x;
+    ms[tid] = M;
+    ls[tid] = l;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < QJ_THREADS / 32; ++w) M = fmaxf(M, top[w]);
-    for (int c = tid; c < n; c += QJ_THREADS) {
-        f[c] = f[c] == -INFINITY ? 0.f : exp2f(f[c] - M);
-        l = fmaf(f[c], __ldcg(record(c) + 1), l);
+    if (slice > 0 || e >= s.dv) return;
+    for (int k = 1; k < slices; ++k) M = fmaxf(M, ms[k * width + e]);
+    l = x = 0.f;
+    for (int k = 0; k < slices; ++k) {
+        const float m = ms[k * width + e], f = m == -INFINITY ? 0.f : exp2f(m - M);
+        l = fmaf(f, ls[k * width + e], l);
+        x = fmaf(f, ys[k * width + e], x);
     }
-#pragma unroll
-    for (int w = 16; w >= 1; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
-    if (lane == 0) sum[warp] = l;
-    __syncthreads();
-    l = 0.f;
-#pragma unroll
-    for (int w = 0; w < QJ_THREADS / 32; ++w) l += sum[w];
-    // width threads hold the columns, QJ_THREADS / width slices of the records
-    const int width = s.dv <= 64 ? 64 : s.dv <= 128 ? 128 : 256, e = tid % width;
-    float x = 0.f;
-    if (e < s.dv) {
-#pragma unroll 8
-        for (int c = tid / width; c < n; c += QJ_THREADS / width) x = fmaf(f[c], __ldcg(record(c) + 2 + e), x);
-    }
-    y[tid] = x;
-    __syncthreads();
-    if (tid >= s.dv) return;
-    for (int w = tid + width; w < QJ_THREADS; w += width) x += y[w];
     quant_put(O + ((int64_t)b * s.T_q + t) * ldo + (int64_t)head * s.dv + e, x / l);
 }
 
@@ -301,8 +302,13 @@ cudaError_t launch_quant_decode(const QuantStep& s, bool f32, int bits, const Qu
                              static_cast<const T*>(Q), ldq, static_cast<T*>(O), ldo, lengths, scale, part, status);
         }
         if (err != cudaSuccess || s.T_max <= kQuantum) return err;  // (groups of one quantum are never shared)
-        return launch_pdl(quant_join_kernel<T>, dim3((unsigned)((int64_t)s.B * s.h_kv * s.rows)), dim3(QJ_THREADS), 0, stream, s,
-                          static_cast<const float*>(part), static_cast<T*>(O), ldo, lengths);
+        // threads: for as many slices as leave each about eight records of an evenly cut step
+        const int width = s.dv <= 64 ? 64 : s.dv <= 128 ? 128 : 256;
+        const int64_t n = s.ctas / ((int64_t)s.B * s.lanes()) + 2;
+        int threads = 256;
+        while (threads < 1024 && n > 8 * (threads / width)) threads *= 2;
+        return launch_pdl(quant_join_kernel<T>, dim3((unsigned)((int64_t)s.B * s.h_kv * s.rows)), dim3((unsigned)threads), 0,
+                          stream, s, static_cast<const float*>(part), static_cast<T*>(O), ldo, lengths);
     };
     if (f32) return bits == 4 ? go(static_cast<float*>(nullptr), quant_decode_kernel<float, 4>)
                               : go(static_cast<float*>(nullptr), quant_decode_kernel<float, 8>);

@@ -527,11 +527,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT>::CTAS)
             if (gid == 0) *reinterpret_cast<float2*>(row + D) = make_float2(m[nt][e], l[nt][e]);
         }
     __syncthreads();
-    for (int e = tid; e < nr * D; e += QM_THREADS) {
-        const int r = e / D, c = e % D;
-        const float* a = reinterpret_cast<const float*>(smem + C::RES) + r * C::REC;
-        quant_meet<QM_WARPS>(s, z, a + c, a + D, C::ROWS * C::REC, g, r0, r, c, O, ldo, part);
-    }
+    quant_meet<QM_WARPS>(s, z, reinterpret_cast<float*>(smem + C::RES), C::ROWS, C::REC, D, g, r0, nr, O, ldo, part);
     __syncthreads();
     }
     if (*abort_flag && tid == 0)  // a copy did not arrive: wait for those in flight, and leave
