@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(QD_THREADS)
                 for (int e = 0; e < 8; ++e) to[c0 + e] = o[r][e];
         }
         __syncthreads();
-        quant_meet<QD_WARPS>(s, z, all, R, dpv + 32, dpv, g, r0, nr, O, ldo, part);
+        quant_meet<QD_WARPS, QD_THREADS>(s, z, all, R, dpv + 32, dpv, g, r0, nr, O, ldo, part);
     }
 }
 

@@ -31,32 +31,32 @@ __device__ __forceinline__ void quant_invalid(const QuantStep& s, const int32_t*
     }
 }
 
-// The warps' results of a piece, [warp][row] of `stride` floats: dv values, then at ml m and l.  A group that the CTA has
-// alone is finished, another leaves a record.  All threads; the results are in place (a barrier before), and m of a row
-// becomes its factor.
-template <int WARPS, typename T>
+// A piece's ENTRIES results for each of `rows` rows (the warps', or several of a warp), [entry][row] of `stride` floats:
+// dv values, then at ml m and l.  A group that the CTA has alone is finished, another leaves a record.  All threads,
+// behind a barrier; an entry's m becomes its factor.
+template <int ENTRIES, int THREADS, typename T>
 __device__ __forceinline__ void quant_meet(const QuantStep& s, const QuantPiece& z, float* res, int rows, int stride, int ml,
                                            int g, int r0, int nr, T* O, int64_t ldo, float* part) {
     const int tid = (int)threadIdx.x;
     const bool whole = z.whole();
     const int which = z.q0 == 0 ? 1 : 0;
-    // eight lanes a row: maximum and sum of its warps
-    for (int r = tid / WARPS; r < nr; r += 32) {
-        float* a = res + ((tid % WARPS) * rows + r) * stride + ml;
-        const unsigned lanes = ((1u << WARPS) - 1) << (tid & 31 & ~(WARPS - 1));
+    // ENTRIES lanes a row: maximum and sum
+    for (int r = tid / ENTRIES; r < nr; r += THREADS / ENTRIES) {
+        float* a = res + ((tid % ENTRIES) * rows + r) * stride + ml;
+        const unsigned lanes = ((1u << ENTRIES) - 1) << (tid & 31 & ~(ENTRIES - 1));
         const float m = a[0];
         float M = m;
 #pragma unroll
-        for (int w = WARPS / 2; w >= 1; w >>= 1) M = fmaxf(M, __shfl_xor_sync(lanes, M, w));
+        for (int w = ENTRIES / 2; w >= 1; w >>= 1) M = fmaxf(M, __shfl_xor_sync(lanes, M, w));
         const float f = m == -INFINITY ? 0.f : exp2f(m - M);
         float l = f * a[1];
 #pragma unroll
-        for (int w = WARPS / 2; w >= 1; w >>= 1) l += __shfl_xor_sync(lanes, l, w);
+        for (int w = ENTRIES / 2; w >= 1; w >>= 1) l += __shfl_xor_sync(lanes, l, w);
         if (whole) {
             a[0] = f / l;  // (l is NaN, or above zero: a whole group has a visible token for every row)
         } else {
             a[0] = f;
-            if (tid % WARPS == 0) {
+            if (tid % ENTRIES == 0) {
                 float* rec = part + s.slot((int)blockIdx.x, which, r);
                 rec[0] = M;
                 rec[1] = l;
@@ -64,12 +64,12 @@ __device__ __forceinline__ void quant_meet(const QuantStep& s, const QuantPiece&
         }
     }
     __syncthreads();
-    for (int e = tid; e < nr * s.dv; e += 32 * WARPS) {
+    for (int e = tid; e < nr * s.dv; e += THREADS) {
         const int r = e / s.dv, c = e - r * s.dv;
         const float* a = res + r * stride;
         float x = 0.f;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) x = fmaf(a[w * rows * stride + ml], a[w * rows * stride + c], x);
+        for (int w = 0; w < ENTRIES; ++w) x = fmaf(a[w * rows * stride + ml], a[w * rows * stride + c], x);
         if (whole) quant_put(quant_out(s, O, ldo, z.b, g, r0 + r) + c, x);
         else part[s.slot((int)blockIdx.x, which, r) + 2 + c] = x;
     }

@@ -10,8 +10,9 @@
 // high and low part for fp32 layers (22 bits); likewise p s, against a running power of two: 11 bits for bf16 layers,
 // high and low part for fp32 ones.
 //
-// The cached tokens are the M side of both products (16 at a time) and the query rows the N side (8 or 16), so a few
-// rows waste no tensor work and the exponentials spread over all lanes.  Which channel or token is which k of a
+// The cached tokens are the M side of both products (16 at a time) and the query rows the N side (8 or 16 columns), so
+// a few rows waste no tensor work and the exponentials spread over all lanes.  Up to 4 rows leave half of the columns:
+// every other block of 16 tokens takes those, as rows of their own until the end, and two blocks share one softmax.  Which channel or token is which k of a
 // product is free as long as both operands agree: it is chosen so that one mask takes two elements out of a word.
 //   scores:  A = keys [token][channel], lane (gid, tig) holds 16 channels of a group of tokens gid and gid + 8
 //   values:  A = values transposed [channel][token], the words of two tokens interleaved by a byte permutation;
@@ -40,7 +41,7 @@ constexpr int QM_WARPS = 8;
 constexpr float kNone = -3e38f;  // the reference of a row that has seen nothing: below every score, finite
 constexpr int QM_THREADS = 32 * QM_WARPS;
 
-template <int BITS, int D, int TERMS, int NT>
+template <int BITS, int D, int TERMS, int NT, int SUB>
 struct QmCfg {
     static constexpr int G = D / kQuantGroup;
     static constexpr int ROW = D * BITS / 8;
@@ -48,11 +49,16 @@ struct QmCfg {
     static constexpr int STAGE = 2 * TOK * (ROW + 4 * G);     // key codes, value codes, key and value parameters
     static constexpr int CTAS = NT * TERMS * G > 2 ? 1 : 2;   // of an SM (registers)
     static constexpr int STAGES = CTAS == 1 ? 4 : 2;
-    static constexpr int ROWS = 8 * NT;
-    static constexpr int REC = D + 4;                         // floats of a row's result: values, m, l
+    static constexpr int COLS = 8 * NT;                       // columns of the products
+    static constexpr int ROWS = COLS / SUB;                   // query rows of a block
+    static constexpr int REC = D + 4;                         // floats of a column's result: values, m, l
     static constexpr int RES = STAGES * STAGE;                // the warps' results
-    static constexpr int BARS = RES + QM_WARPS * ROWS * REC * 4;
+    static constexpr int QF = RES + QM_WARPS * COLS * REC * 4;  // queries as operands, their sums and scales
+    static constexpr int QS = QF + TERMS * NT * G * 32 * 32;
+    static constexpr int BARS = QS + COLS * (G + 1) * 4;
     static constexpr int SMEM = BARS + 16 * STAGES + 48;      // barriers, counts of the warps done, QmNext, abort flag
+    static_assert(SUB == 1 || NT == 1, "only a few rows leave columns for a second block");
+    static_assert(BARS % 16 == 0 && SMEM <= 232448, "");
     static_assert(TOK % kQuantum == 0, "a stage's tokens are dealt out evenly");
     static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory of an SM");
 };
@@ -116,7 +122,7 @@ __device__ __forceinline__ constexpr float unit(int h) {
 }
 
 // 16 of a row's channels in a group (keys), as the A operands of the group's four products for one token: x[c][0] its
-// k = 2 tig, 2 tig + 1, x[c][1] its k = 2 tig + 8, 2 tig + 9.  The channels behind them: q_channel().
+// k = 2 tig, 2 tig + 1, x[c][1] its k = 2 tig + 8, 2 tig + 9.  Which channels these are: q_place().
 template <int BITS, int TERMS>
 __device__ __forceinline__ void key_operands(uint32_t addr, uint32_t (&x)[4][2]) {
     uint32_t w[BITS / 2];
@@ -134,10 +140,12 @@ __device__ __forceinline__ void key_operands(uint32_t addr, uint32_t (&x)[4][2])
     }
 }
 
-// Channel (of this lane's 16 of a group) behind half h, element e of product c.
+// Product c, half h (k = 2 tig, .. or 2 tig + 8, ..) and element of the pair behind channel j of a lane's 16.
 template <int BITS>
-__device__ __forceinline__ constexpr int q_channel(int c, int h, int e) {
-    return BITS == 4 ? 8 * (c >> 1) + 2 * (c & 1) + h + 4 * e : 4 * c + h + 2 * e;
+__device__ __forceinline__ void q_place(int j, int& c, int& h, int& e) {
+    h = j & 1;
+    c = BITS == 4 ? (j >> 3) * 2 + (j >> 1 & 1) : j >> 2;
+    e = BITS == 4 ? j >> 2 & 1 : j >> 1 & 1;
 }
 
 // Eight of a row's channels in a group (values) of two tokens a, b, as the A operands of the group's four products:
@@ -177,12 +185,12 @@ __device__ __forceinline__ float elem(const __nv_bfloat16* p) { return __bfloat1
 __device__ __forceinline__ float power2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126 .. 127
 __device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23 & 255u) - 127; }
 
-template <int BITS, int D, int TERMS, int NT, typename T>
-__global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT>::CTAS)
+template <int BITS, int D, int TERMS, int NT, int SUB, typename T>
+__global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CTAS)
     quant_mma_kernel(const QuantStep s, const QuantPlane pk, const QuantPlane pv, const T* __restrict__ Q, int64_t ldq,
                      T* __restrict__ O, int64_t ldo, const int32_t* __restrict__ lengths, float scale_log2,
                      float* __restrict__ part, int* status) {
-    using C = QmCfg<BITS, D, TERMS, NT>;
+    using C = QmCfg<BITS, D, TERMS, NT, SUB>;
     constexpr int G = C::G;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5, gid = lane >> 2, tig = lane & 3;
@@ -246,55 +254,76 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT>::CTAS)
     const int b = z.b, g = z.lane / s.nrb, L = z.L;
     const int r0 = (z.lane - g * s.nrb) * C::ROWS, nr = min(C::ROWS, s.rows - r0);
 
-    // queries: row gid of each eight as B operands, and what the lane's score columns 2 tig, 2 tig + 1 need of theirs.
-    // y rs is a score.
+    // queries: a warp makes a row's B operands, as the lanes will want them, its sum per group and the factor that turns
+    // a product with it into a score
+    {
+        constexpr int CPL = D / 32;  // channels of a lane
+        __half* qh = reinterpret_cast<__half*>(smem + C::QF);
+        float* qv = reinterpret_cast<float*>(smem + C::QS);
+#pragma unroll 1
+        for (int r = warp; r < C::ROWS; r += QM_WARPS) {
+            const int rr = r0 + min(r, nr - 1), hg = rr / s.T_q, t = rr - hg * s.T_q;
+            const T* src = Q + ((int64_t)b * s.T_q + t) * ldq + (int64_t)(g * s.per + hg) * D + lane * CPL;
+            float x[CPL], top = 0.f;
+#pragma unroll
+            for (int e = 0; e < CPL; ++e) {
+                x[e] = elem(src + e);
+                top = fmaxf(top, fabsf(x[e]));
+            }
+#pragma unroll
+            for (int w = 16; w >= 1; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+            // the largest element to [2^13, 2^14); zero, infinite and tiny rows as far as powers of two go
+            const int e2 = top > 0.f && top < INFINITY ? max(-80, min(100, 13 - exponent(top))) : 0;
+            const float f = power2(e2);
+            const int u = G == 1 ? 0 : lane / 16;
+            float sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < CPL; ++e) {
+                const int j = lane * CPL + e & 15, to = lane * CPL + e >> 4 & 3;  // channel of lane `to` of four
+                int c, h, half;
+                q_place<BITS>(j, c, h, half);
+                const float v = f * x[e] * (h == 0 ? 1.f : unit<BITS, TERMS>(0) / unit<BITS, TERMS>(1));
+                sum = fmaf(h == 0 ? unit<BITS, TERMS>(0) : unit<BITS, TERMS>(1), v, sum);
+                const __half hi = __float2half_rn(v), lo = __float2half_rn(v - __half2float(hi));
+#pragma unroll
+                for (int k = 0; k < SUB; ++k) {
+                    const int n = r % 8 + k * C::ROWS;  // column
+                    const int at = (((r / 8 * G + u) * 32 + 4 * n + to) * 8 + 2 * c + h) * 2 + half;
+                    qh[at] = hi;
+                    if constexpr (TERMS == 2) qh[NT * G * 512 + at] = lo;
+                }
+            }
+#pragma unroll
+            for (int w = 8; w >= 1; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+            if constexpr (G == 1) sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+#pragma unroll
+            for (int k = 0; k < SUB; ++k) {
+                if (lane % 16 == 0 && lane / 16 < G) qv[(r + k * C::ROWS) * (G + 1) + u] = sum;
+                if (lane == 0) qv[(r + k * C::ROWS) * (G + 1) + G] = scale_log2 / unit<BITS, TERMS>(0) * power2(-e2);
+            }
+        }
+    }
+    __syncthreads();
     uint32_t qf[TERMS][NT][G][4][2];
-    float qs[NT][G][2], rs[NT][2];
+    float qs[NT][G][2], rs[NT][2];  // y rs is a score
     const int lim_min = L - s.T_q + 1;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const int rr = r0 + min(8 * nt + gid, nr - 1), head = g * s.per + rr / s.T_q, t = rr % s.T_q;
-        const T* src = Q + ((int64_t)b * s.T_q + t) * ldq + (int64_t)head * D + 16 * tig;
-        float x[G][16], top = 0.f;
 #pragma unroll
-        for (int u = 0; u < G; ++u)
+        for (int w = 0; w < TERMS; ++w)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                x[u][e] = elem(src + u * kQuantGroup + e);
-                top = fmaxf(top, fabsf(x[u][e]));
+            for (int u = 0; u < G; ++u) {
+                const uint4* from = reinterpret_cast<const uint4*>(smem + C::QF) + (((w * NT + nt) * G + u) * 32 + lane) * 2;
+                const uint4 v0 = from[0], v1 = from[1];
+                qf[w][nt][u][0][0] = v0.x; qf[w][nt][u][0][1] = v0.y; qf[w][nt][u][1][0] = v0.z; qf[w][nt][u][1][1] = v0.w;
+                qf[w][nt][u][2][0] = v1.x; qf[w][nt][u][2][1] = v1.y; qf[w][nt][u][3][0] = v1.z; qf[w][nt][u][3][1] = v1.w;
             }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // the largest element to [2^13, 2^14); zero, infinite and tiny rows as far as powers of two go
-        const int e2 = top > 0.f && top < INFINITY ? max(-80, min(100, 13 - exponent(top))) : 0;
-        const float f = power2(e2);
-        float sum[G];
-#pragma unroll
-        for (int u = 0; u < G; ++u) {
-            sum[u] = 0.f;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float fh = f * (unit<BITS, TERMS>(0) / unit<BITS, TERMS>(h));
-                    const float x0 = fh * x[u][q_channel<BITS>(c, h, 0)], x1 = fh * x[u][q_channel<BITS>(c, h, 1)];
-                    qf[0][nt][u][c][h] = half2_bits(x0, x1);
-                    if constexpr (TERMS == 2) {
-                        const float2 high = half2_floats(qf[0][nt][u][c][h]);
-                        qf[TERMS - 1][nt][u][c][h] = half2_bits(x0 - high.x, x1 - high.y);
-                    }
-                    sum[u] = fmaf(unit<BITS, TERMS>(h), x0 + x1, sum[u]);
-                }
-            sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], 1);
-            sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], 2);
-        }
-        const float back = scale_log2 / unit<BITS, TERMS>(0) * power2(-e2);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int from = 4 * (2 * tig + e);
+            const float* from = reinterpret_cast<const float*>(smem + C::QS) + (8 * nt + 2 * tig + e) * (G + 1);
 #pragma unroll
-            for (int u = 0; u < G; ++u) qs[nt][u][e] = __shfl_sync(0xffffffffu, sum[u], from);
-            rs[nt][e] = __shfl_sync(0xffffffffu, back, from);
+            for (int u = 0; u < G; ++u) qs[nt][u][e] = from[u];
+            rs[nt][e] = from[G];
         }
     }
 
@@ -314,6 +343,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT>::CTAS)
             }
         }
     float vs = power2(100);  // p s is held as p s vs
+    const int block = SUB == 1 ? 0 : 2 * tig / C::ROWS;           // whose columns the lane has
     const int pa = gid ^ (gid >> 1 & 1);                          // this lane's key token, and its second at + 8: the
     const int va = 2 * tig ^ (tig & 1), vb = (2 * tig + 1) ^ (tig & 1);  // order in which neither load meets itself in a bank
 #pragma unroll 1
@@ -326,34 +356,38 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT>::CTAS)
         const uint32_t at = ring + slot * C::STAGE;
         // the stage's 16-token blocks, a run of them for each warp
         const int blocks = min(C::TOK / 16, (z.k1() - t_stage + 15) / 16);
+        const int w_end = min(z.k1(), t_stage + (warp + 1) * blocks / QM_WARPS * 16);  // the run's end
 #pragma unroll 1
-        for (int sub = warp * blocks / QM_WARPS * 16; sub < (warp + 1) * blocks / QM_WARPS * 16; sub += 16) {
+        for (int sub = warp * blocks / QM_WARPS * 16; t_stage + sub < w_end; sub += 16 * SUB) {
             const int t0 = t_stage + sub;
-            const bool edge = t0 + 16 > lim_min;  // some row does not see all of the 16
+            const bool edge = t0 + 16 * SUB > min(lim_min, w_end);  // some column does not see all of its 16
             const uint32_t kc = at + (uint32_t)(sub * C::ROW), vc = kc + C::TOK * C::ROW;
-            const uint32_t kp = at + 2 * C::TOK * C::ROW + (uint32_t)(sub * 4 * G), vp = kp + C::TOK * 4 * G;
-            // scores
+            const uint32_t kp = at + 2 * C::TOK * C::ROW + (uint32_t)((sub + 16 * block) * 4 * G), vp = kp + C::TOK * 4 * G;
+            // scores; with two blocks, columns 0 .. 3 are the first one's and columns 4 .. 7 the second one's
             float y[NT][4];
             {
                 float acc[NT][G][4];
 #pragma unroll
-                for (int u = 0; u < G; ++u) {
-                    uint32_t ka[4][2], kb[4][2];
-                    const uint32_t col = (uint32_t)((u * kQuantGroup + 16 * tig) * BITS / 8);
-                    key_operands<BITS, TERMS>(kc + (uint32_t)(pa * C::ROW) + col, ka);
-                    key_operands<BITS, TERMS>(kc + (uint32_t)((pa + 8) * C::ROW) + col, kb);
+                for (int k = 0; k < SUB; ++k)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int u = 0; u < G; ++u) {
+                        uint32_t ka[4][2], kb[4][2];
+                        const uint32_t col = (uint32_t)((u * kQuantGroup + 16 * tig) * BITS / 8);
+                        key_operands<BITS, TERMS>(kc + (uint32_t)((pa + 16 * k) * C::ROW) + col, ka);
+                        key_operands<BITS, TERMS>(kc + (uint32_t)((pa + 16 * k + 8) * C::ROW) + col, kb);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const uint32_t a[4] = {ka[c][0], kb[c][0], ka[c][1], kb[c][1]};
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                            for (int w = 0; w < TERMS; ++w) {
-                                if (c == 0 && w == 0) acc[nt][u][0] = acc[nt][u][1] = acc[nt][u][2] = acc[nt][u][3] = 0.f;
-                                mma_f16(acc[nt][u], a, qf[w][nt][u][c][0], qf[w][nt][u][c][1]);
+                            for (int c = 0; c < 4; ++c) {
+                                const uint32_t a[4] = {ka[c][0], kb[c][0], ka[c][1], kb[c][1]};
+#pragma unroll
+                                for (int w = 0; w < TERMS; ++w) mma_f16(d, a, qf[w][nt][u][c][0], qf[w][nt][u][c][1]);
                             }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[nt][u][e] = k == 0 ? d[e] : block == 0 ? acc[nt][u][e] : d[e];
                         }
-                }
+                    }
                 uint32_t p0[G], p1[G];
                 token_params<G>(kp + (uint32_t)(pa * 4 * G), p0);
                 token_params<G>(kp + (uint32_t)((pa + 8) * 4 * G), p1);
@@ -361,11 +395,12 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT>::CTAS)
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
+                        y[nt][e] = quant_lowest(e < 2 ? p0[0] : p1[0]) * qs[nt][0][e & 1];
 #pragma unroll
                         for (int u = 0; u < G; ++u) {
                             const uint32_t par = e < 2 ? p0[u] : p1[u];
-                            const float low = quant_lowest(par) * qs[nt][u][e & 1];
-                            y[nt][e] = fmaf(quant_step(par), acc[nt][u][e], u == 0 ? low : y[nt][e] + low);
+                            if (u > 0) y[nt][e] = fmaf(quant_lowest(par), qs[nt][u][e & 1], y[nt][e]);
+                            y[nt][e] = fmaf(quant_step(par), acc[nt][u][e], y[nt][e]);
                         }
                     }
             }
@@ -373,19 +408,20 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT>::CTAS)
             token_params<G>(vp + (uint32_t)(pa * 4 * G), v0);
             token_params<G>(vp + (uint32_t)((pa + 8) * 4 * G), v1);
             if (edge) {  // tokens at or past the length hold anything
-                const int ta = t0 + pa, tb = ta + 8;
+                const int ta = t0 + 16 * block + pa, tb = ta + 8;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int t = (r0 + min(8 * nt + 2 * tig + e, nr - 1)) % s.T_q;  // sees tokens below lim_min + t
-                        if (ta >= lim_min + t) y[nt][e] = -INFINITY;
-                        if (tb >= lim_min + t) y[nt][e + 2] = -INFINITY;
+                        const int r = (8 * nt + 2 * tig + e) % C::ROWS;
+                        const int lim = min(w_end, lim_min + (r0 + min(r, nr - 1)) % s.T_q);
+                        if (ta >= lim) y[nt][e] = -INFINITY;
+                        if (tb >= lim) y[nt][e + 2] = -INFINITY;
                     }
 #pragma unroll
                 for (int u = 0; u < G; ++u) {
-                    if (ta >= L) v0[u] = 0;
-                    if (tb >= L) v1[u] = 0;
+                    if (ta >= w_end) v0[u] = 0;
+                    if (tb >= w_end) v1[u] = 0;
                 }
             }
             // references
@@ -470,22 +506,30 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT>::CTAS)
                     }
                 }
             }
-            // values
+            // values: each block's tokens with its own columns
 #pragma unroll
-            for (int u = 0; u < G; ++u) {
-                uint32_t xa[4][2], xb[4][2];
-                const uint32_t col = (uint32_t)((u * kQuantGroup + 8 * gid) * BITS / 8);
-                value_operands<BITS, TERMS>(vc + (uint32_t)(va * C::ROW) + col, vc + (uint32_t)(vb * C::ROW) + col, xa);
-                value_operands<BITS, TERMS>(vc + (uint32_t)((va + 8) * C::ROW) + col, vc + (uint32_t)((vb + 8) * C::ROW) + col, xb);
+            for (int k = 0; k < SUB; ++k)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint32_t a[4] = {xa[c][0], xa[c][1], xb[c][0], xb[c][1]};
+                for (int u = 0; u < G; ++u) {
+                    uint32_t xa[4][2], xb[4][2], w2[TERMS][NT][2];
+                    const uint32_t col = (uint32_t)((u * kQuantGroup + 8 * gid) * BITS / 8), from = vc + (uint32_t)(16 * k * C::ROW) + col;
+                    value_operands<BITS, TERMS>(from + (uint32_t)(va * C::ROW), from + (uint32_t)(vb * C::ROW), xa);
+                    value_operands<BITS, TERMS>(from + (uint32_t)((va + 8) * C::ROW), from + (uint32_t)((vb + 8) * C::ROW), xb);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int w = 0; w < TERMS; ++w)
 #pragma unroll
-                        for (int w = 0; w < TERMS; ++w) mma_f16(o[nt][u][c], a, bf[w][nt][u][0], bf[w][nt][u][1]);
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) w2[w][nt][h] = SUB == 1 || gid / C::ROWS == k ? bf[w][nt][u][h] : 0u;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t a[4] = {xa[c][0], xa[c][1], xb[c][0], xb[c][1]};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int w = 0; w < TERMS; ++w) mma_f16(o[nt][u][c], a, w2[w][nt][0], w2[w][nt][1]);
+                    }
                 }
-            }
         }
         ++used;
         uint32_t last = 0;
@@ -504,7 +548,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT>::CTAS)
     }
 
     // this warp's result: rows of D values, m, l
-    float* own = reinterpret_cast<float*>(smem + C::RES) + warp * C::ROWS * C::REC;
+    float* own = reinterpret_cast<float*>(smem + C::RES) + warp * C::COLS * C::REC;
     const float inv = 1.f / vs;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -527,7 +571,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT>::CTAS)
             if (gid == 0) *reinterpret_cast<float2*>(row + D) = make_float2(m[nt][e], l[nt][e]);
         }
     __syncthreads();
-    quant_meet<QM_WARPS>(s, z, reinterpret_cast<float*>(smem + C::RES), C::ROWS, C::REC, D, g, r0, nr, O, ldo, part);
+    quant_meet<QM_WARPS * SUB, QM_THREADS>(s, z, reinterpret_cast<float*>(smem + C::RES), C::ROWS, C::REC, D, g, r0, nr, O, ldo, part);
     __syncthreads();
     }
     if (*abort_flag && tid == 0)  // a copy did not arrive: wait for those in flight, and leave
@@ -535,40 +579,53 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT>::CTAS)
             drain_wait_a(bars + 8u * (uint32_t)(k % C::STAGES), (uint32_t)(k / C::STAGES) & 1u);
 }
 
-template <int BITS, int D, int TERMS, int NT, typename T>
+template <int BITS, int D, int TERMS, int NT, int SUB, typename T>
 cudaError_t launch(const QuantStep& s, const QuantPlane& pk, const QuantPlane& pv, const void* Q, int64_t ldq, void* O,
                    int64_t ldo, const int32_t* lengths, float* part, int* status, cudaStream_t stream) {
-    using C = QmCfg<BITS, D, TERMS, NT>;
-    auto kernel = quant_mma_kernel<BITS, D, TERMS, NT, T>;
+    using C = QmCfg<BITS, D, TERMS, NT, SUB>;
+    auto kernel = quant_mma_kernel<BITS, D, TERMS, NT, SUB, T>;
     const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (err != cudaSuccess) return err;
     const float scale = (float)(1.4426950408889634 / sqrt((double)D));
-    return launch_pdl(kernel, dim3((unsigned)s.ctas), dim3(QM_THREADS), C::SMEM, stream, s,
-                      pk, pv, static_cast<const T*>(Q), ldq, static_cast<T*>(O), ldo, lengths, scale, part, status);
+    return launch_pdl(kernel, dim3((unsigned)s.ctas), dim3(QM_THREADS), C::SMEM, stream, s, pk, pv, static_cast<const T*>(Q),
+                      ldq, static_cast<T*>(O), ldo, lengths, scale, part, status);
+}
+
+// (fp32 layers of 128 channels have no room in the registers for 16 rows)
+constexpr bool most_rows_16(int terms, int d) { return !(terms == 2 && d == 128); }
+
+template <int BITS, int D, typename T, typename... A>
+cudaError_t launch_rows(int rb, A... a) {
+    constexpr int TERMS = std::is_same_v<T, float> ? 2 : 1;
+    if (rb == 4) return launch<BITS, D, TERMS, 1, 2, T>(a...);
+    if (rb == 8) return launch<BITS, D, TERMS, 1, 1, T>(a...);
+    if constexpr (most_rows_16(TERMS, D)) return launch<BITS, D, TERMS, 2, 1, T>(a...);
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
 bool quant_mma_serves(int d_k, int d_v) { return d_k == d_v && (d_k == 64 || d_k == 128); }
 
-// Query rows of a block: 16 if there are more than 8 (two sets of operands and sums beside each unpacked code).
-int quant_mma_rows(bool f32, int d, int rows) { return rows > 8 && !(f32 && d == 128) ? 16 : 8; }
+// Query rows of a block: 4, whose columns two blocks of tokens share, 8, or 16 (two sets of operands and sums beside each
+// unpacked code).
+int quant_mma_rows(bool f32, int d, int rows) { return rows <= 4 ? 4 : rows <= 8 || !most_rows_16(f32 ? 2 : 1, d) ? 8 : 16; }
 
-int quant_mma_ctas(bool f32, int d, int rb) { return (f32 ? 2 : 1) * (d / 64) * (rb / 8) > 2 ? 1 : 2; }
+int quant_mma_ctas(bool f32, int d, int rb) { return (f32 ? 2 : 1) * (d / 64) * (rb == 16 ? 2 : 1) > 2 ? 1 : 2; }
 
 cudaError_t launch_quant_mma(const QuantStep& s, bool f32, int bits, const QuantPlane& pk, const QuantPlane& pv, const void* Q,
                              int64_t ldq, void* O, int64_t ldo, const int32_t* lengths, float* part, int* status,
                              cudaStream_t stream) {
-#define MHA_QM(BITS, D, TERMS, NT, T) \
-    if (bits == BITS && pk.d == D && f32 == (TERMS == 2) && s.rb == 8 * NT) \
-        return launch<BITS, D, TERMS, NT, T>(s, pk, pv, Q, ldq, O, ldo, lengths, part, status, stream);
-    MHA_QM(4, 64, 1, 1, __nv_bfloat16) MHA_QM(4, 64, 1, 2, __nv_bfloat16) MHA_QM(4, 128, 1, 1, __nv_bfloat16)
-    MHA_QM(4, 128, 1, 2, __nv_bfloat16) MHA_QM(8, 64, 1, 1, __nv_bfloat16) MHA_QM(8, 64, 1, 2, __nv_bfloat16)
-    MHA_QM(8, 128, 1, 1, __nv_bfloat16) MHA_QM(8, 128, 1, 2, __nv_bfloat16) MHA_QM(4, 64, 2, 1, float)
-    MHA_QM(4, 64, 2, 2, float) MHA_QM(4, 128, 2, 1, float) MHA_QM(8, 64, 2, 1, float) MHA_QM(8, 64, 2, 2, float)
-    MHA_QM(8, 128, 2, 1, float)
-#undef MHA_QM
-    return cudaErrorInvalidValue;
+    auto go = [&](auto* x) {
+        using T = std::remove_pointer_t<decltype(x)>;
+        auto with = [&](auto f) { return f(s.rb, s, pk, pv, Q, ldq, O, ldo, lengths, part, status, stream); };
+        if (bits == 4)
+            return pk.d == 64 ? with([](auto rb, auto&... a) { return launch_rows<4, 64, T>(rb, a...); })
+                              : with([](auto rb, auto&... a) { return launch_rows<4, 128, T>(rb, a...); });
+        return pk.d == 64 ? with([](auto rb, auto&... a) { return launch_rows<8, 64, T>(rb, a...); })
+                          : with([](auto rb, auto&... a) { return launch_rows<8, 128, T>(rb, a...); });
+    };
+    return f32 ? go(static_cast<float*>(nullptr)) : go(static_cast<__nv_bfloat16*>(nullptr));
 }
 
 }  // namespace mha
