@@ -300,6 +300,25 @@ def test_decode_long(dtype, d, bits):
     _step(layer, cache, held, wl.random_tensor((4, 1, 4 * d), 5, dtype), lengths, dtype, "long")
 
 
+@pytest.mark.parametrize("dtype,d,h,h_kv", [("bf16", 64, 8, 4), ("bf16", 128, 4, 4), ("bf16", 64, 64, 4), ("f32", 64, 4, 4), ("f32", 48, 4, 4)])
+@pytest.mark.parametrize("B,T", [(13, 700), (40, 300), (70, 257)])
+def test_decode_many_sequences(dtype, d, h, h_kv, B, T):
+    """More groups than CTAs, and nearly as many, with lengths of every size, none at all among them: groups shared by
+    two CTAs, CTAs with many groups, batches beyond a warp's lanes."""
+    rng = np.random.default_rng(B + T)
+    lengths = [int(x) for x in rng.integers(1, T + 1, B)]
+    lengths[0], lengths[5], lengths[-1], lengths[7] = T, 1, T, 0
+    layer = _layer(dtype, h, d, h_kv)
+    cache, held = _filled(layer, 11, dtype, B, T, 4)
+    _spoil(cache, lengths)
+    Q = wl.random_tensor((B, 1, h * d), 5, dtype)
+    got = to_host(layer.decode_quant(to_device(Q, dtype), cache, _ints(lengths)))
+    O, A, S = qc.decode(Q, *held, h, lengths)
+    assert np.isnan(got[7]).all() and layer.status() == _lib.MHA_ERR_BAD_LENGTH
+    keep = np.arange(B) != 7
+    _check(got[keep], O[keep], A[keep], S[keep], dtype, "many sequences")
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("f32", 64), ("f32", 16)])
 @pytest.mark.parametrize("bits", [4, 8])
 def test_decode_large_scores_and_scales(dtype, d, bits):

@@ -35,9 +35,13 @@ __device__ __forceinline__ float quant_lowest(uint32_t p) { return __uint_as_flo
 // CTA therefore has pieces of at most two groups that others share, its first and its last, and leaves records of those
 // (per row: m, l and the values, scores in base 2); groups that it has alone it finishes.  The join adds a group's
 // records in the order of its tokens.  Which CTA has what follows from the lengths and C alone.
+//
+// Short steps of few groups give each group a cluster of kQuantCluster CTAs instead, which cut its quanta evenly among
+// themselves and join their results through distributed shared memory: one launch, no records.
 
 constexpr int kQuantum = 128;      // tokens
 constexpr int kQuantMaxCtas = 640; // largest grid, for the size of the workspace
+constexpr int kQuantCluster = 8;
 
 struct QuantStep {
     int B, h_kv, per, T_q, T_max;
@@ -45,6 +49,7 @@ struct QuantStep {
     int rb, nrb;  // rows of a row block; row blocks
     int ctas;     // grid: C is this, or the number of quanta if that is less
     int dv;
+    bool clusters;  // a cluster per group; ctas is then kQuantCluster times the groups
     __host__ __device__ int lanes() const { return h_kv * nrb; }   // groups of a batch
     __host__ __device__ int record() const { return dv + 2; }      // floats
     // Record of a row of a CTA's first (which = 0: it began in another CTA) or last group.
@@ -57,14 +62,20 @@ __device__ __forceinline__ int quant_quanta(const QuantStep& s, int L) {
     return L < s.T_q || L > s.T_max ? 0 : (L + kQuantum - 1) / kQuantum;
 }
 
-// A lane's part of the prefix sums over the batches; N quanta in all.
+// A lane's part of the prefix sums over the batches; N quanta in all, of which a CTA has `each` or one more.
 struct QuantPlan {
-    int i0, i1, L0, before, sum, N, C;
+    int i0, i1, L0, before, sum, N, C, each, rest;
+    bool bad;  // some length is invalid
     __device__ __forceinline__ int length(const int32_t* lengths, int i) const { return i == i0 ? L0 : __ldcg(lengths + i); }
-    // First quantum of a CTA.
-    __device__ __forceinline__ int first(int cta) const { return cta < C ? (int)((int64_t)cta * N / C) : N; }
+    // First quantum of a CTA: floor(cta N / C).
+    __device__ __forceinline__ int first(int cta) const { return cta < C ? cta * each + (int)((unsigned)(cta * rest) / (unsigned)C) : N; }
     // The CTA that has a quantum.
-    __device__ __forceinline__ int owner(int q) const { return (int)((((int64_t)q + 1) * C - 1) / N); }
+    __device__ __forceinline__ int owner(int q) const {
+        int c = min(C - 1, (int)((float)q * ((float)C / (float)N)));  // off by one at most
+        if (first(c) > q) --c;
+        if (first(c + 1) <= q) ++c;
+        return c;
+    }
 };
 
 // All lanes of a warp call it, and the next two.
@@ -75,8 +86,14 @@ __device__ __forceinline__ QuantPlan quant_plan(const QuantStep& s, const int32_
     p.i1 = min(s.B, p.i0 + run);
     p.L0 = p.i0 < p.i1 ? __ldcg(lengths + p.i0) : 0;
     p.sum = 0;
+    p.bad = false;
 #pragma unroll 1
-    for (int i = p.i0; i < p.i1; ++i) p.sum += quant_quanta(s, p.length(lengths, i));
+    for (int i = p.i0; i < p.i1; ++i) {
+        const int n = quant_quanta(s, p.length(lengths, i));
+        p.sum += n;
+        p.bad = p.bad || n == 0;
+    }
+    p.bad = __any_sync(0xffffffffu, p.bad);
     p.sum *= s.lanes();
     int inc = p.sum;
 #pragma unroll
@@ -86,7 +103,9 @@ __device__ __forceinline__ QuantPlan quant_plan(const QuantStep& s, const int32_
     }
     p.before = inc - p.sum;
     p.N = __shfl_sync(0xffffffffu, inc, 31);
-    p.C = min(s.ctas, p.N);
+    p.C = max(1, min(s.ctas, p.N));
+    p.each = (int)((unsigned)p.N / (unsigned)p.C);
+    p.rest = p.N - p.each * p.C;
     return p;
 }
 
@@ -126,6 +145,20 @@ __device__ __forceinline__ QuantPiece quant_piece(const QuantStep& s, const int3
     x.q0 = q - start;
     x.q1 = min(x.nq, end - start);
     x.next = start + x.q1;
+    return x;
+}
+
+// A cluster's part of its group.  q0 == q1: none (an invalid length: nq is 0).
+__device__ __forceinline__ QuantPiece quant_cluster_piece(const QuantStep& s, const int32_t* lengths) {
+    const int group = (int)blockIdx.x / kQuantCluster, rank = (int)blockIdx.x % kQuantCluster;
+    QuantPiece x;
+    x.b = group / s.lanes();
+    x.lane = group - x.b * s.lanes();
+    x.L = __ldcg(lengths + x.b);
+    x.nq = quant_quanta(s, x.L);
+    x.q0 = (int)((int64_t)x.nq * rank / kQuantCluster);
+    x.q1 = (int)((int64_t)x.nq * (rank + 1) / kQuantCluster);
+    x.next = x.q1;
     return x;
 }
 

@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(QD_THREADS)
     grid_dependency_wait();
     grid_launch_dependents();
     const QuantPlan plan = quant_plan(s, lengths);
-    quant_invalid<QD_THREADS>(s, lengths, O, ldo, status);
+    if (plan.bad) quant_invalid<QD_THREADS>(s, (int)blockIdx.x, (int)gridDim.x, lengths, O, ldo, status);
     const int end = plan.first((int)blockIdx.x + 1);
     for (int at = plan.first((int)blockIdx.x); at < end;) {
         const QuantPiece z = quant_piece(s, lengths, plan, at, end);
@@ -166,7 +166,8 @@ __global__ void __launch_bounds__(QD_THREADS)
                 for (int e = 0; e < 8; ++e) to[c0 + e] = o[r][e];
         }
         __syncthreads();
-        quant_meet<QD_WARPS, QD_THREADS>(s, z, all, R, dpv + 32, dpv, g, r0, nr, O, ldo, part);
+        quant_meet<QD_WARPS, QD_THREADS>(s, z.whole(), part + s.slot((int)blockIdx.x, z.q0 == 0 ? 1 : 0, 0), all, R, dpv + 32, dpv, b, g,
+                                         r0, nr, O, ldo);
     }
 }
 
@@ -253,6 +254,9 @@ size_t qd_smem(const QuantPlane& pk, const QuantPlane& pv) {
 
 }  // namespace
 
+// Longest caches of steps that a cluster takes per group, in quanta of a CTA: (measured below)
+constexpr int kClusterQuanta = 4;
+
 // Rows of a block by the kernel that serves the head size; CTAs: as many as the GPU holds at a time, but no more than
 // there may be quanta.
 QuantStep quant_step_shape(bool f32, int d_k, int d_v, int B, int h, int h_kv, int T_q, int T_max, int sms) {
@@ -268,9 +272,11 @@ QuantStep quant_step_shape(bool f32, int d_k, int d_v, int B, int h, int h_kv, i
     s.rb = mma ? quant_mma_rows(f32, d_k, s.rows) : QD_ROWS;
     s.nrb = (s.rows + s.rb - 1) / s.rb;
     int64_t ctas = (int64_t)sms * (mma ? quant_mma_ctas(f32, d_k, s.rb) : 2);
-    const int64_t most = quant_most_quanta(s);
+    const int64_t most = quant_most_quanta(s), groups = (int64_t)B * s.lanes();
+    s.clusters = mma && groups * kQuantCluster <= ctas && T_max <= kQuantCluster * kClusterQuanta * kQuantum && T_max > kQuantum;
     if (ctas > kQuantMaxCtas) ctas = kQuantMaxCtas;
     if (ctas > most) ctas = most;
+    if (s.clusters) ctas = groups * kQuantCluster;
     s.ctas = ctas < 1 ? 1 : (int)ctas;
     return s;
 }
@@ -301,7 +307,7 @@ cudaError_t launch_quant_decode(const QuantStep& s, bool f32, int bits, const Qu
             err = launch_pdl(kernel, dim3((unsigned)s.ctas), dim3(QD_THREADS), qd_smem(pk, pv), stream, s, pk, pv,
                              static_cast<const T*>(Q), ldq, static_cast<T*>(O), ldo, lengths, scale, part, status);
         }
-        if (err != cudaSuccess || s.T_max <= kQuantum) return err;  // (groups of one quantum are never shared)
+        if (err != cudaSuccess || s.clusters || s.T_max <= kQuantum) return err;  // (groups of one quantum are never shared)
         // threads: for as many slices as leave each about eight records of an evenly cut step
         const int width = s.dv <= 64 ? 64 : s.dv <= 128 ? 128 : 256;
         const int64_t n = s.ctas / ((int64_t)s.B * s.lanes()) + 2;

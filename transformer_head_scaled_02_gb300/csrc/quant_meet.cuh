@@ -18,10 +18,10 @@ __device__ __forceinline__ T* quant_out(const QuantStep& s, T* O, int64_t ldo, i
     return O + ((int64_t)b * s.T_q + (rr - hg * s.T_q)) * ldo + (int64_t)(g * s.per + hg) * s.dv;
 }
 
-// Batches with an invalid length: NaN rows and a status, by the CTA of the batch's number modulo the grid.
+// Batches b, b + step, .. with an invalid length: NaN rows and a status.
 template <int THREADS, typename T>
-__device__ __forceinline__ void quant_invalid(const QuantStep& s, const int32_t* lengths, T* O, int64_t ldo, int* status) {
-    for (int b = (int)blockIdx.x; b < s.B; b += (int)gridDim.x) {
+__device__ __noinline__ void quant_invalid(const QuantStep& s, int b, int step, const int32_t* lengths, T* O, int64_t ldo, int* status) {
+    for (; b < s.B; b += step) {
         const int L = __ldcg(lengths + b);
         if (L >= s.T_q && L <= s.T_max) continue;
         if (threadIdx.x == 0) record_status(status, kStatusBadLength);
@@ -32,14 +32,12 @@ __device__ __forceinline__ void quant_invalid(const QuantStep& s, const int32_t*
 }
 
 // A piece's ENTRIES results for each of `rows` rows (the warps', or several of a warp), [entry][row] of `stride` floats:
-// dv values, then at ml m and l.  A group that the CTA has alone is finished, another leaves a record.  All threads,
-// behind a barrier; an entry's m becomes its factor.
+// dv values, then at ml m and l.  Either they are finished (whole), or they become records at rec.  All threads, behind a
+// barrier; an entry's m becomes its factor.
 template <int ENTRIES, int THREADS, typename T>
-__device__ __forceinline__ void quant_meet(const QuantStep& s, const QuantPiece& z, float* res, int rows, int stride, int ml,
-                                           int g, int r0, int nr, T* O, int64_t ldo, float* part) {
+__device__ __forceinline__ void quant_meet(const QuantStep& s, bool whole, float* rec, float* res, int rows, int stride, int ml,
+                                           int b, int g, int r0, int nr, T* O, int64_t ldo) {
     const int tid = (int)threadIdx.x;
-    const bool whole = z.whole();
-    const int which = z.q0 == 0 ? 1 : 0;
     // ENTRIES lanes a row: maximum and sum
     for (int r = tid / ENTRIES; r < nr; r += THREADS / ENTRIES) {
         float* a = res + ((tid % ENTRIES) * rows + r) * stride + ml;
@@ -57,9 +55,8 @@ __device__ __forceinline__ void quant_meet(const QuantStep& s, const QuantPiece&
         } else {
             a[0] = f;
             if (tid % ENTRIES == 0) {
-                float* rec = part + s.slot((int)blockIdx.x, which, r);
-                rec[0] = M;
-                rec[1] = l;
+                rec[r * s.record()] = M;
+                rec[r * s.record() + 1] = l;
             }
         }
     }
@@ -70,8 +67,8 @@ __device__ __forceinline__ void quant_meet(const QuantStep& s, const QuantPiece&
         float x = 0.f;
 #pragma unroll
         for (int w = 0; w < ENTRIES; ++w) x = fmaf(a[w * rows * stride + ml], a[w * rows * stride + c], x);
-        if (whole) quant_put(quant_out(s, O, ldo, z.b, g, r0 + r) + c, x);
-        else part[s.slot((int)blockIdx.x, which, r) + 2 + c] = x;
+        if (whole) quant_put(quant_out(s, O, ldo, b, g, r0 + r) + c, x);
+        else rec[r * s.record() + 2 + c] = x;
     }
 }
 

@@ -210,14 +210,30 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
     grid_dependency_wait();
     grid_launch_dependents();
 
-    const QuantPlan plan = quant_plan(s, lengths);
-    const int end = plan.first((int)blockIdx.x + 1);
+    QuantPlan plan;
+    QuantPiece own;  // of a cluster's CTA
+    int begin, end;
+    if (s.clusters) {
+        own = quant_cluster_piece(s, lengths);
+        begin = own.q0;
+        end = own.q1;
+        if (own.nq == 0) {
+            if (blockIdx.x % (kQuantCluster * s.lanes()) == 0) quant_invalid<QM_THREADS>(s, own.b, s.B, lengths, O, ldo, status);
+            return;
+        }
+    } else {
+        plan = quant_plan(s, lengths);
+        begin = plan.first((int)blockIdx.x);
+        end = plan.first((int)blockIdx.x + 1);
+        if (plan.bad) quant_invalid<QM_THREADS>(s, (int)blockIdx.x, (int)gridDim.x, lengths, O, ldo, status);
+    }
+    auto piece = [&](int q) { return s.clusters ? own : quant_piece(s, lengths, plan, q, end); };
     // One warp at a time asks for the next stage (all its lanes call this): at first warp 0, then whichever is the last
     // to have used the stage whose place it takes.
     auto fetch = [&](QmNext& x) {
         while (x.from >= x.to) {
             if (x.at >= end) return;
-            const QuantPiece z = quant_piece(s, lengths, plan, x.at, end);
+            const QuantPiece z = piece(x.at);
             x.at = z.next;
             x.row = ((int64_t)z.b * s.h_kv + z.lane / s.nrb) * s.T_max;
             x.from = z.k0();
@@ -238,18 +254,17 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
         ++x.issued;
     };
     if (warp == 0) {
-        QmNext x{0, plan.first((int)blockIdx.x), 0, 0, 0};
+        QmNext x{0, begin, 0, 0, 0};
 #pragma unroll 1
         for (int n = 0; n < C::STAGES; ++n) fetch(x);
         if (lane == 0) *next = x;
     }
-    quant_invalid<QM_THREADS>(s, lengths, O, ldo, status);
 
     bool ok = true;
     int used = 0;  // stages
 #pragma unroll 1
-    for (int q_at = plan.first((int)blockIdx.x); q_at < end;) {
-    const QuantPiece z = quant_piece(s, lengths, plan, q_at, end);
+    for (int q_at = begin; q_at < end;) {
+    const QuantPiece z = piece(q_at);
     q_at = z.next;
     const int b = z.b, g = z.lane / s.nrb, L = z.L;
     const int r0 = (z.lane - g * s.nrb) * C::ROWS, nr = min(C::ROWS, s.rows - r0);
@@ -571,8 +586,38 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
             if (gid == 0) *reinterpret_cast<float2*>(row + D) = make_float2(m[nt][e], l[nt][e]);
         }
     __syncthreads();
-    quant_meet<QM_WARPS * SUB, QM_THREADS>(s, z, reinterpret_cast<float*>(smem + C::RES), C::ROWS, C::REC, D, g, r0, nr, O, ldo, part);
+    // (a cluster's CTA, which has one piece, is through with its ring)
+    float* rec = s.clusters ? reinterpret_cast<float*>(smem) : part + s.slot((int)blockIdx.x, z.q0 == 0 ? 1 : 0, 0);
+    quant_meet<QM_WARPS * SUB, QM_THREADS>(s, !s.clusters && z.whole(), rec, reinterpret_cast<float*>(smem + C::RES), C::ROWS, C::REC,
+                                           D, b, g, r0, nr, O, ldo);
     __syncthreads();
+    }
+    if (s.clusters) {  // the CTAs' records meet, an eighth of the outputs in each
+        const int g = own.lane / s.nrb, r0 = (own.lane - g * s.nrb) * C::ROWS, nr = min(C::ROWS, s.rows - r0);
+        if (begin == end)  // had nothing
+            for (int r = tid; r < nr; r += QM_THREADS) reinterpret_cast<float*>(smem)[r * (D + 2)] = kNone;
+        cluster_sync_all();
+        for (int e = (int)cluster_ctarank() * QM_THREADS + tid; e < nr * D; e += kQuantCluster * QM_THREADS) {
+            const int r = e / D, c = e % D;
+            float m[kQuantCluster], l[kQuantCluster], v[kQuantCluster], M = kNone, sum = 0.f, x = 0.f;
+#pragma unroll
+            for (int k = 0; k < kQuantCluster; ++k) {
+                const uint32_t at = mapa_shared(ring, (uint32_t)k) + (uint32_t)(r * (D + 2) * 4);
+                m[k] = ld_shared_cluster(at);
+                l[k] = ld_shared_cluster(at + 4);
+                v[k] = ld_shared_cluster(at + 8 + 4 * c);
+                M = fmaxf(M, m[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < kQuantCluster; ++k)
+                if (m[k] != kNone) {
+                    const float f = exp2f(m[k] - M);
+                    sum = fmaf(f, l[k], sum);
+                    x = fmaf(f, v[k], x);
+                }
+            quant_put(quant_out(s, O, ldo, own.b, g, r0 + r) + c, x / sum);
+        }
+        cluster_sync_all();  // no CTA leaves while its record is read
     }
     if (*abort_flag && tid == 0)  // a copy did not arrive: wait for those in flight, and leave
         for (int k = max(0, next->issued - C::STAGES); k < next->issued; ++k)
@@ -587,8 +632,8 @@ cudaError_t launch(const QuantStep& s, const QuantPlane& pk, const QuantPlane& p
     const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (err != cudaSuccess) return err;
     const float scale = (float)(1.4426950408889634 / sqrt((double)D));
-    return launch_pdl(kernel, dim3((unsigned)s.ctas), dim3(QM_THREADS), C::SMEM, stream, s, pk, pv, static_cast<const T*>(Q),
-                      ldq, static_cast<T*>(O), ldo, lengths, scale, part, status);
+    return launch_pdl_cluster(kernel, s.clusters ? kQuantCluster : 1, dim3((unsigned)s.ctas), dim3(QM_THREADS), C::SMEM, stream, s,
+                              pk, pv, static_cast<const T*>(Q), ldq, static_cast<T*>(O), ldo, lengths, scale, part, status);
 }
 
 // (fp32 layers of 128 channels have no room in the registers for 16 rows)
