@@ -20,6 +20,10 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+# (torch.cuda's own function is a Python frame more)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
+
+
 def _stream() -> int:
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
@@ -50,10 +54,12 @@ class Mha:
         self.handle = _lib.mha_create_ex(D, h, self.h_kv, d_k, self.d_v, int(self.gated),
                                          _DTYPES[dtype])
         self._ws: Optional[torch.Tensor] = None
+        self._ws_bytes = 0
         self._ws_captured = False
         self._ws_streams: set = set()  # streams that the allocator knows to use the workspace
         self._kept_ws: list = []
         self._step_bytes: dict = {}  # workspace bytes of the cache steps, by their sizes
+        self._heads = (self.h_kv, self.d_k, self.d_v)
 
     @property
     def proj_width(self) -> int:
@@ -80,6 +86,7 @@ class Mha:
                 self._ws_captured = False
             self._ws, home = (self._new_workspace_in_capture if capturing else self._new_workspace)(max(need, 256))
             self._ws_streams = {home}
+            self._ws_bytes = self._ws.numel()
         if capturing:
             self._ws_captured = True
         elif _stream() not in self._ws_streams:
@@ -338,6 +345,8 @@ class Mha:
     # ------------------------------------------------------------ long contexts
     def _rows(self, name: str, t: torch.Tensor, B: int, T: int, width: int) -> int:
         """Check a (B, T, width) view whose rows lie one stride apart throughout; returns the stride."""
+        if t.is_contiguous() and t.dtype is self.dtype and t.shape == (B, T, width):
+            return width
         if t.shape != (B, T, width):
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(B, T, width)}")
         s0, s1, s2 = t.stride()
@@ -527,12 +536,22 @@ class Mha:
         multiple of 16.  Its contents are unset: quant_write fills it, decode_quant attends over it."""
         return QuantCache(self, B, T_max, bits)
 
-    def _quant_check(self, cache: "QuantCache", lengths: torch.Tensor, counts: Optional[torch.Tensor]):
-        if cache.heads != (self.h_kv, self.d_k, self.d_v):
-            raise ValueError(f"the cache holds (heads, d_k, d_v) {cache.heads}, expected "
-                             f"{(self.h_kv, self.d_k, self.d_v)}")
-        return (self._ints("cache_lengths", lengths, cache.B),
-                None if counts is None else self._ints("counts", counts, cache.B))
+    def _quant_lens(self, cache: "QuantCache", lengths: torch.Tensor) -> int:
+        if cache.heads != self._heads:
+            raise ValueError(f"the cache holds (heads, d_k, d_v) {cache.heads}, expected {self._heads}")
+        return self._ints("cache_lengths", lengths, cache.B)
+
+    def _quant_ready(self, cache: "QuantCache", X: torch.Tensor, Y: torch.Tensor, lengths: torch.Tensor,
+                     counts: Optional[torch.Tensor], need: int) -> int:
+        """All on the cache's device, the current one, and `need` bytes of workspace there; returns its stream."""
+        dev = cache.device
+        if dev < 0 or X.get_device() != dev or Y.get_device() != dev or lengths.get_device() != dev or \
+                (counts is not None and counts.get_device() != dev) or torch._C._cuda_getDevice() != dev:
+            self._device(cache.data, X, Y, lengths, counts)  # says what is wrong
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+        if need > self._ws_bytes or stream not in self._ws_streams or _capturing():
+            self.ensure_workspace(0, 0, 0, need=need)
+        return stream
 
     def quant_write(self, cache: "QuantCache", K: torch.Tensor, V: torch.Tensor, cache_lengths: torch.Tensor,
                     counts: Optional[torch.Tensor] = None) -> "QuantCache":
@@ -540,12 +559,12 @@ class Mha:
         the cache.  cache_lengths (int32, B) count the cached tokens including the new ones, as decode_quant wants
         them; counts (int32, B; default: T_new) how many rows of each sequence are tokens: the first n_b rows
         become tokens L_b - n_b .. L_b - 1."""
-        lens, n = self._quant_check(cache, cache_lengths, counts)
+        lens = self._quant_lens(cache, cache_lengths)
+        n = None if counts is None else self._ints("counts", counts, cache.B)
         T = K.shape[1]
         ldk = self._rows("K", K, cache.B, T, self.h_kv * self.d_k)
         ldv = self._rows("V", V, cache.B, T, self.h_kv * self.d_v)
-        stream = self._device(K, V, cache.data, cache_lengths, counts)
-        self.ensure_workspace(0, 0, 0, need=256)  # the status word
+        stream = self._quant_ready(cache, K, V, cache_lengths, counts, 256)  # the status word
         _lib.mha_quant_write(self.handle, *cache.args, T, K.data_ptr(), ldk, V.data_ptr(), ldv, lens, n, stream)
         return cache
 
@@ -556,7 +575,8 @@ class Mha:
         0 .. n_b - 1 of K_out (B, T_out, h_kv*d_k view) and V_out (B, T_out, h_kv*d_v view); rows past n_b of
         given outputs stay, of new ones are unset.  T_out defaults to the cache's T_max or the given outputs' rows.
         counts=cache_lengths reads whole sequences.  Returns (K_out, V_out)."""
-        lens, n = self._quant_check(cache, cache_lengths, counts)
+        lens = self._quant_lens(cache, cache_lengths)
+        n = None if counts is None else self._ints("counts", counts, cache.B)
         B, wk, wv = cache.B, self.h_kv * self.d_k, self.h_kv * self.d_v
         if T_out is None:
             T_out = K_out.shape[1] if K_out is not None else V_out.shape[1] if V_out is not None else cache.T_max
@@ -566,8 +586,7 @@ class Mha:
             V_out = torch.empty((B, T_out, wv), dtype=self.dtype, device=cache.data.device)
         ldk = self._rows("K_out", K_out, B, T_out, wk)
         ldv = self._rows("V_out", V_out, B, T_out, wv)
-        stream = self._device(cache.data, K_out, V_out, cache_lengths, counts)
-        self.ensure_workspace(0, 0, 0, need=256)  # the status word
+        stream = self._quant_ready(cache, K_out, V_out, cache_lengths, counts, 256)  # the status word
         _lib.mha_quant_read(self.handle, *cache.args, T_out, K_out.data_ptr(), ldk, V_out.data_ptr(), ldv, lens, n,
                             stream)
         return K_out, V_out
@@ -575,19 +594,18 @@ class Mha:
     def decode_quant(self, Q: torch.Tensor, cache: "QuantCache", cache_lengths: torch.Tensor,
                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """decode() over a quantised cache: the keys and values are those that the codes stand for."""
-        lens, _ = self._quant_check(cache, cache_lengths, None)
-        B, T_q, _ = Q.shape
-        ldq = self._rows("Q", Q, cache.B, T_q, self.h * self.d_k)
+        lens = self._quant_lens(cache, cache_lengths)
+        bits, B, T_max, ptr = cache.args
+        T_q = Q.shape[1]
+        ldq = self._rows("Q", Q, B, T_q, self.h * self.d_k)
         if out is None:
             out = torch.empty((B, T_q, self.h * self.d_v), dtype=self.dtype, device=Q.device)
         ldo = self._rows("out", out, B, T_q, self.h * self.d_v)
-        stream = self._device(Q, cache.data, cache_lengths, out)
-        sizes = ("quant", B, T_q, cache.T_max)
+        sizes = ("quant", B, T_q, T_max)
         need = self._step_bytes.get(sizes)
         if need is None:
             need = self._step_need_put(sizes, _lib.mha_decode_quant_workspace_size(self.handle, *sizes[1:]))
-        self.ensure_workspace(B, T_q, cache.T_max, need=need)
-        bits, B, T_max, ptr = cache.args
+        stream = self._quant_ready(cache, Q, out, cache_lengths, None, need)
         _lib.mha_decode_quant(self.handle, bits, B, T_q, T_max, Q.data_ptr(), ldq, ptr, lens, out.data_ptr(), ldo,
                               stream)
         return out
@@ -612,6 +630,7 @@ class QuantCache:
         self.B, self.T_max, self.bits = B, T_max, bits
         self.heads = (layer.h_kv, layer.d_k, layer.d_v)
         self.data = torch.empty(nbytes, dtype=torch.uint8, device=layer.device)
+        self.device = self.data.get_device()
         self.args = (bits, B, T_max, self.data.data_ptr())  # of every C call
         views = []
         for d, c, p in ((layer.d_k, off[0], off[1]), (layer.d_v, off[2], off[3])):
