@@ -173,7 +173,7 @@ cudaError_t launch_quant_copy(bool write, bool f32, int bits, const QuantPlane& 
                               const int32_t* lengths, const int32_t* counts, int* status, cudaStream_t stream);
 
 // mha_decode_quant: how a step is cut, the bytes of its records (part), and its launches.
-QuantStep quant_step_shape(bool f32, int d_k, int d_v, int B, int h, int h_kv, int T_q, int T_max, int sms);
+QuantStep quant_step_shape(bool f32, int bits, int d_k, int d_v, int B, int h, int h_kv, int T_q, int T_max, int sms);
 int64_t quant_most_quanta(const QuantStep& s);
 size_t quant_step_bytes(const QuantStep& s);
 bool quant_step_fits(const QuantStep& s);
@@ -182,7 +182,7 @@ cudaError_t launch_quant_decode(const QuantStep& s, bool f32, int bits, const Qu
                                 int* status, cudaStream_t stream);
 // The tensor-core kernel: head sizes it serves, query rows of its blocks, CTAs that an SM holds, the launch.
 bool quant_mma_serves(int d_k, int d_v);
-int quant_mma_rows(bool f32, int d, int rows);
+int quant_mma_rows(bool f32, int bits, int d, int rows);
 int quant_mma_ctas(bool f32, int d, int rb);
 cudaError_t launch_quant_mma(const QuantStep& s, bool f32, int bits, const QuantPlane& pk, const QuantPlane& pv, const void* Q,
                              int64_t ldq, void* O, int64_t ldo, const int32_t* lengths, float* part, int* status,

@@ -27,21 +27,34 @@ __host__ __device__ inline int quant_groups(int d) { return (d + kQuantGroup - 1
 __device__ __forceinline__ float quant_step(uint32_t p) { return __uint_as_float(p << 16); }
 __device__ __forceinline__ float quant_lowest(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
 
+// Division of numbers below 2^31 by a number known on the host.
+struct Divide {
+    uint32_t mul, shift, by;
+    __host__ explicit Divide(uint32_t d = 1) : shift(0), by(d) {
+        while ((1ull << shift) < d) ++shift;
+        mul = (uint32_t)(((((uint64_t)1 << shift) - d) << 32) / d + 1);  // 2^(32 + shift) / d, upwards, less 2^32
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int operator()(uint32_t n) const { return (int)((__umulhi(n, mul) + n) >> shift); }
+#endif
+};
+
 // ------------------------------------------------------------------ how a decode step is cut
 //
 // The query rows that share a cached head are taken `rb` at a time: a group is (batch, K/V head, block of rows), and
-// its visible tokens are cut into quanta of kQuantum.  All quanta of all groups, numbered by batch, head, block and
+// its visible tokens are cut into quanta of 128, or where that would only cost a join, into one.  All quanta of all groups, numbered by batch, head, block and
 // token, are dealt out evenly: CTA c of C <= N takes those from c N / C to (c + 1) N / C, whatever the lengths are.  A
 // CTA therefore has pieces of at most two groups that others share, its first and its last, and leaves records of those
 // (per row: m, l and the values, scores in base 2); groups that it has alone it finishes.  The join adds a group's
 // records in the order of its tokens.  Which CTA has what follows from the lengths and C alone.
 //
-// Short steps of few groups give each group a cluster of kQuantCluster CTAs instead, which cut its quanta evenly among
-// themselves and join their results through distributed shared memory: one launch, no records.
+// Steps whose groups' tokens are few for a CTA give each group a cluster of 1, 2, 4 or 8 CTAs instead, which cut its quanta
+// evenly among themselves and join their results through distributed shared memory: one launch, no records.  So do steps
+// of one sequence, whose groups are equally long: `parts` clusters a group, each of which leaves one record.
 
 constexpr int kQuantum = 128;      // tokens
 constexpr int kQuantMaxCtas = 640; // largest grid, for the size of the workspace
-constexpr int kQuantCluster = 8;
+constexpr int kQuantCluster = 8;   // largest cluster
 
 struct QuantStep {
     int B, h_kv, per, T_q, T_max;
@@ -49,7 +62,12 @@ struct QuantStep {
     int rb, nrb;  // rows of a row block; row blocks
     int ctas;     // grid: C is this, or the number of quanta if that is less
     int dv;
-    bool clusters;  // a cluster per group; ctas is then kQuantCluster times the groups
+    int quantum;  // tokens of a quantum: a multiple of kQuantum
+    int cluster;  // CTAs of a cluster, each with one piece; 0: the even cut.  ctas is then cluster * parts * groups
+    int parts;    // clusters of a group
+    // divisions by T_q, nrb, lanes(), quantum, ctas and the CTAs of a group (a runtime division is some 150 cycles of
+    // a chain that a step has to wait for)
+    Divide by_T_q, by_nrb, by_lanes, by_quantum, by_ctas, by_group;
     __host__ __device__ int lanes() const { return h_kv * nrb; }   // groups of a batch
     __host__ __device__ int record() const { return dv + 2; }      // floats
     // Record of a row of a CTA's first (which = 0: it began in another CTA) or last group.
@@ -59,7 +77,7 @@ struct QuantStep {
 #ifdef __CUDACC__
 
 __device__ __forceinline__ int quant_quanta(const QuantStep& s, int L) {
-    return L < s.T_q || L > s.T_max ? 0 : (L + kQuantum - 1) / kQuantum;
+    return L < s.T_q || L > s.T_max ? 0 : s.by_quantum((uint32_t)(L + s.quantum - 1));
 }
 
 // A lane's part of the prefix sums over the batches; N quanta in all, of which a CTA has `each` or one more.
@@ -67,16 +85,26 @@ struct QuantPlan {
     int i0, i1, L0, before, sum, N, C, each, rest;
     bool bad;  // some length is invalid
     __device__ __forceinline__ int length(const int32_t* lengths, int i) const { return i == i0 ? L0 : __ldcg(lengths + i); }
-    // First quantum of a CTA: floor(cta N / C).
-    __device__ __forceinline__ int first(int cta) const { return cta < C ? cta * each + (int)((unsigned)(cta * rest) / (unsigned)C) : N; }
+    // First quantum of a CTA: floor(cta N / C); C is the grid, or N with a quantum for each.
+    __device__ __forceinline__ int first(const QuantStep& s, int cta) const {
+        return cta < C ? cta * each + s.by_ctas((uint32_t)(cta * rest)) : N;
+    }
     // The CTA that has a quantum.
-    __device__ __forceinline__ int owner(int q) const {
-        int c = min(C - 1, (int)((float)q * ((float)C / (float)N)));  // off by one at most
-        if (first(c) > q) --c;
-        if (first(c + 1) <= q) ++c;
+    __device__ __forceinline__ int owner(const QuantStep& s, int q) const {
+        int c = min(C - 1, (int)((float)q * __fdividef((float)C, (float)N)));  // off by one at most
+        if (first(s, c) > q) --c;
+        if (first(s, c + 1) <= q) ++c;
         return c;
     }
 };
+
+// a / b of a below 2^31 whose quotient is small.
+__device__ __forceinline__ int quant_quotient(int a, int b) {
+    int q = (int)__fdividef((float)a, (float)b), r = a - q * b;
+    while (r < 0) --q, r += b;
+    while (r >= b) ++q, r -= b;
+    return q;
+}
 
 // All lanes of a warp call it, and the next two.
 __device__ __forceinline__ QuantPlan quant_plan(const QuantStep& s, const int32_t* lengths) {
@@ -103,9 +131,9 @@ __device__ __forceinline__ QuantPlan quant_plan(const QuantStep& s, const int32_
     }
     p.before = inc - p.sum;
     p.N = __shfl_sync(0xffffffffu, inc, 31);
-    p.C = max(1, min(s.ctas, p.N));
-    p.each = (int)((unsigned)p.N / (unsigned)p.C);
-    p.rest = p.N - p.each * p.C;
+    p.C = min(s.ctas, p.N);
+    p.each = p.N < s.ctas ? 1 : s.by_ctas((uint32_t)p.N);
+    p.rest = p.N < s.ctas ? 0 : p.N - p.each * s.ctas;
     return p;
 }
 
@@ -116,8 +144,9 @@ struct QuantPiece {
     int q0, q1;    // quanta [q0, q1) of the group
     int next;      // quantum behind the piece
     int nq;        // quanta of the group
-    __device__ __forceinline__ int k0() const { return q0 * kQuantum; }
-    __device__ __forceinline__ int k1() const { return min(L, q1 * kQuantum); }
+    int quantum;
+    __device__ __forceinline__ int k0() const { return q0 * quantum; }
+    __device__ __forceinline__ int k1() const { return q1 == nq ? L : q1 * quantum; }
     __device__ __forceinline__ bool whole() const { return q0 == 0 && q1 == nq; }
 };
 
@@ -139,8 +168,9 @@ __device__ __forceinline__ QuantPiece quant_piece(const QuantStep& s, const int3
     x.b = __shfl_sync(0xffffffffu, b, src);
     at = __shfl_sync(0xffffffffu, at, src);
     x.L = __shfl_sync(0xffffffffu, len, src);
-    x.nq = (x.L + kQuantum - 1) / kQuantum;
-    x.lane = (q - at) / x.nq;
+    x.nq = quant_quanta(s, x.L);
+    x.quantum = s.quantum;
+    x.lane = quant_quotient(q - at, x.nq);
     const int start = at + x.lane * x.nq;
     x.q0 = q - start;
     x.q1 = min(x.nq, end - start);
@@ -148,16 +178,18 @@ __device__ __forceinline__ QuantPiece quant_piece(const QuantStep& s, const int3
     return x;
 }
 
-// A cluster's part of its group.  q0 == q1: none (an invalid length: nq is 0).
+// A cluster's CTA's piece of its group.  q0 == q1: none (an invalid length: nq is 0).
 __device__ __forceinline__ QuantPiece quant_cluster_piece(const QuantStep& s, const int32_t* lengths) {
-    const int group = (int)blockIdx.x / kQuantCluster, rank = (int)blockIdx.x % kQuantCluster;
+    const int n = s.cluster * s.parts, group = s.by_group(blockIdx.x), i = (int)blockIdx.x - group * n;
     QuantPiece x;
-    x.b = group / s.lanes();
+    x.b = s.by_lanes((uint32_t)group);
     x.lane = group - x.b * s.lanes();
     x.L = __ldcg(lengths + x.b);
     x.nq = quant_quanta(s, x.L);
-    x.q0 = (int)((int64_t)x.nq * rank / kQuantCluster);
-    x.q1 = (int)((int64_t)x.nq * (rank + 1) / kQuantCluster);
+    x.quantum = s.quantum;
+    const int each = s.by_group((uint32_t)x.nq), rest = x.nq - each * n;  // q0 = floor(i nq / n) in 32 bits
+    x.q0 = each * i + s.by_group((uint32_t)(rest * i));
+    x.q1 = each * (i + 1) + s.by_group((uint32_t)(rest * (i + 1)));
     x.next = x.q1;
     return x;
 }

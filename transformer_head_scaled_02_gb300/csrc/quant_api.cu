@@ -98,8 +98,8 @@ bool step_sizes_ok(const mha_s* m, int B, int T_q, int T_max) {
     return T_q >= 0 && (int64_t)B * m->h * T_q <= kMostRows;
 }
 
-QuantStep step_shape(const mha_s* m, int B, int T_q, int T_max, int sms) {
-    return quant_step_shape(m->dtype == MHA_F32, m->dk, m->dv, B, m->h, m->h_kv, T_q, T_max, sms);
+QuantStep step_shape(const mha_s* m, int bits, int B, int T_q, int T_max, int sms) {
+    return quant_step_shape(m->dtype == MHA_F32, bits, m->dk, m->dv, B, m->h, m->h_kv, T_q, T_max, sms);
 }
 
 }  // namespace
@@ -127,7 +127,9 @@ mha_status mha_quant_read(mha_t handle, int bits, int B, int T_max, const void* 
 size_t mha_decode_quant_workspace_size(mha_t handle, int B, int T_q, int T_max) {
     if (handle == nullptr || !cache_sizes_ok(handle, 4, B, T_max) || !step_sizes_ok(handle, B, T_q, T_max)) return 0;
     if (B == 0 || T_q == 0 || T_max == 0) return kStatusBytes;
-    return kStatusBytes + align256(quant_step_bytes(step_shape(handle, B, T_q, T_max, 1)));
+    const size_t four = quant_step_bytes(step_shape(handle, 4, B, T_q, T_max, 1)),
+                 eight = quant_step_bytes(step_shape(handle, 8, B, T_q, T_max, 1));
+    return kStatusBytes + align256(four > eight ? four : eight);
 }
 
 mha_status mha_decode_quant(mha_t handle, int bits, int B, int T_q, int T_max, const void* Q, int64_t ldq,
@@ -146,13 +148,13 @@ mha_status mha_decode_quant(mha_t handle, int bits, int B, int T_q, int T_max, c
     if (overlaps(O, ob, Q, extent(n, ldq, wd.q, s)) || overlaps(O, ob, cache, c.bytes) ||
         overlaps(O, ob, cache_lengths, (size_t)B * sizeof(int32_t)))
         return MHA_ERR_INVALID_ARG;
-    QuantStep q = step_shape(m, B, T_q, T_max, 1);
+    QuantStep q = step_shape(m, bits, B, T_q, T_max, 1);
     if (!quant_step_fits(q)) return MHA_ERR_UNSUPPORTED;
     if (m->ws == nullptr || m->ws_bytes < kStatusBytes + quant_step_bytes(q)) return MHA_ERR_WORKSPACE;
     int sms = 0;
     const mha_status st = query_sms(&sms);
     if (st != MHA_OK) return st;
-    q = step_shape(m, B, T_q, T_max, sms);
+    q = step_shape(m, bits, B, T_q, T_max, sms);
     float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(m->ws) + kStatusBytes);
     const cudaError_t err = launch_quant_decode(q, m->dtype == MHA_F32, bits, c.k, c.v, Q, ldq, O, ldo, cache_lengths, part,
                                                 status_ptr(m), static_cast<cudaStream_t>(stream));

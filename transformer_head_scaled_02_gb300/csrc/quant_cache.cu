@@ -36,16 +36,6 @@ constexpr int kReadItems = 8;
 constexpr unsigned kFewUnits = 4096;  // warps below which a call is short
 constexpr float kBf16Max = 3.3895313892515355e38f;
 
-// Division of numbers below 2^31 by a number known on the host.
-struct Divide {
-    uint32_t mul, shift, by;
-    __host__ explicit Divide(uint32_t d = 1) : shift(0), by(d) {
-        while ((1ull << shift) < d) ++shift;
-        mul = (uint32_t)(((((uint64_t)1 << shift) - d) << 32) / d + 1);  // 2^(32 + shift) / d, upwards, less 2^32
-    }
-    __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
-};
-
 // A call's rows, and how the warps take them: a unit is (batch, `run` x tokens-of-a-warp tokens, head of K or V).
 struct QuantCopy {
     QuantPlane pk, pv;

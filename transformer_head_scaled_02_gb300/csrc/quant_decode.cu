@@ -56,11 +56,11 @@ __global__ void __launch_bounds__(QD_THREADS)
     grid_launch_dependents();
     const QuantPlan plan = quant_plan(s, lengths);
     if (plan.bad) quant_invalid<QD_THREADS>(s, (int)blockIdx.x, (int)gridDim.x, lengths, O, ldo, status);
-    const int end = plan.first((int)blockIdx.x + 1);
-    for (int at = plan.first((int)blockIdx.x); at < end;) {
+    const int end = plan.first(s, (int)blockIdx.x + 1);
+    for (int at = plan.first(s, (int)blockIdx.x); at < end;) {
         const QuantPiece z = quant_piece(s, lengths, plan, at, end);
         at = z.next;
-        const int b = z.b, g = z.lane / s.nrb, L = z.L, k0 = z.k0(), k1 = z.k1();
+        const int b = z.b, g = s.by_nrb((uint32_t)z.lane), L = z.L, k0 = z.k0(), k1 = z.k1();
         const int r0 = (z.lane - g * s.nrb) * R, nr = min(R, s.rows - r0);
         __syncthreads();  // the piece before is written
         for (int e = tid; e < R * dpk; e += QD_THREADS) {
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(QD_THREADS)
                 for (int e = 0; e < 8; ++e) to[c0 + e] = o[r][e];
         }
         __syncthreads();
-        quant_meet<QD_WARPS, QD_THREADS>(s, z.whole(), part + s.slot((int)blockIdx.x, z.q0 == 0 ? 1 : 0, 0), all, R, dpv + 32, dpv, b, g,
+        quant_meet<QD_WARPS, QD_THREADS, 0>(s, z.whole(), part + s.slot((int)blockIdx.x, z.q0 == 0 ? 1 : 0, 0), all, R, dpv + 32, dpv, b, g,
                                          r0, nr, O, ldo);
     }
 }
@@ -181,29 +181,39 @@ __global__ void __launch_bounds__(1024)
     __shared__ float ys[1024], ms[1024], ls[1024];
     const int tid = (int)threadIdx.x;
     const int heads = s.h_kv * s.per, row = (int)blockIdx.x;
-    const int t = row % s.T_q, bh = row / s.T_q, b = bh / heads, head = bh - b * heads;
+    const int bh = s.by_T_q((uint32_t)row), t = row - bh * s.T_q, b = bh / heads, head = bh - b * heads;
     const int g = head / s.per, rr = (head - g * s.per) * s.T_q + t, block = rr / s.rb, r = rr - block * s.rb;
     // The kernel before lets this one start once its own wait for earlier work is over: the lengths can be read (from
     // L2), its records not yet.
-    const QuantPlan p = quant_plan(s, lengths);
-    int at = 0, len = 0;
-    const bool mine = p.i0 <= b && b < p.i1;
-    if (mine) {
-        at = p.before;
+    const float *rec, *others;  // the group's first record, and record i >= 1 at others + i * stride
+    int64_t stride;
+    int n;
+    if (s.cluster) {  // one record a cluster
+        n = quant_quanta(s, __ldcg(lengths + b)) > 0 ? s.parts : 0;
+        stride = (int64_t)s.rb * s.record();
+        rec = others = part + (int64_t)((b * s.h_kv + g) * s.nrb + block) * s.parts * stride + r * s.record();
+    } else {
+        const QuantPlan p = quant_plan(s, lengths);
+        int at = 0, len = 0;
+        const bool mine = p.i0 <= b && b < p.i1;
+        if (mine) {
+            at = p.before;
 #pragma unroll 1
-        for (int i = p.i0; i < b; ++i) at += quant_quanta(s, p.length(lengths, i)) * s.lanes();
-        len = p.length(lengths, b);
+            for (int i = p.i0; i < b; ++i) at += quant_quanta(s, p.length(lengths, i)) * s.lanes();
+            len = p.length(lengths, b);
+        }
+        const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+        const int nq = quant_quanta(s, __shfl_sync(0xffffffffu, len, src));
+        const int first = __shfl_sync(0xffffffffu, at, src) + (g * s.nrb + block) * nq;
+        const int c0 = nq > 0 ? p.owner(s, first) : 0;
+        n = nq > 0 ? p.owner(s, first + nq - 1) - c0 + 1 : 0;
+        // of the first CTA its last group, of the others their first
+        rec = part + s.slot(c0, 1, r);
+        others = part + s.slot(c0, 0, r);
+        stride = s.slot(1, 0, 0);
     }
-    const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
-    const int nq = quant_quanta(s, __shfl_sync(0xffffffffu, len, src));
-    const int first = __shfl_sync(0xffffffffu, at, src) + (g * s.nrb + block) * nq;
-    const int c0 = nq > 0 ? p.owner(first) : 0, n = nq > 0 ? p.owner(first + nq - 1) - c0 + 1 : 0;
     const int width = s.dv <= 64 ? 64 : s.dv <= 128 ? 128 : 256, slices = (int)blockDim.x / width;
     const int e = tid % width, slice = tid / width;
-    // record c of the group: of the first CTA its last group, of the others their first
-    const float* rec = part + s.slot(c0, 1, r);
-    const float* others = part + s.slot(c0, 0, r);
-    const int64_t stride = s.slot(1, 0, 0);
     grid_dependency_wait();
     grid_launch_dependents();
     if (n <= 1) return;  // an invalid length (written as NaN already), or a group that one CTA had alone
@@ -254,12 +264,22 @@ size_t qd_smem(const QuantPlane& pk, const QuantPlane& pv) {
 
 }  // namespace
 
-// Longest caches of steps that a cluster takes per group, in quanta of a CTA: (measured below)
-constexpr int kClusterQuanta = 4;
+// When a step's groups each get a cluster (us, cluster | even cut and join): 16 sequences of 1500 tokens, 16 K/V heads of
+// 64, 12 quanta a CTA 10.1 | 16.1; 8 of 2048, 16 of 128, 8 quanta 13.7 | 17.4; 32 of 8192, 4 of 128, 32 quanta 37.6 | 35.5.
+// All clusters have to run at a time: a second wave costs 5 to 6 us, a CTA's latency from its lengths to its outputs.  One
+// sequence is cut into more clusters a group from 6 quanta a CTA on: 16384 tokens, 4 heads, 16 quanta in one cluster
+// 15.9, several 11.0; 131072 tokens, 2 heads, 8 bits: even cut 25.9, clusters on all SMs 37 (they do not all fit), on 85 %
+// of them 23.3.
+constexpr int kClusterQuanta = 16;
+constexpr int kClusterQuantaOne = 6;
+
+// With more groups than CTAs: the quanta that a CTA may have more than others, where groups are not cut at all, for the
+// join and the shared groups' ends that this saves.  32 sequences of 300 tokens, 16 heads of 128, 8 bits: kQWhole us.
+constexpr int kJoinQuanta = 6;
 
 // Rows of a block by the kernel that serves the head size; CTAs: as many as the GPU holds at a time, but no more than
 // there may be quanta.
-QuantStep quant_step_shape(bool f32, int d_k, int d_v, int B, int h, int h_kv, int T_q, int T_max, int sms) {
+QuantStep quant_step_shape(bool f32, int bits, int d_k, int d_v, int B, int h, int h_kv, int T_q, int T_max, int sms) {
     QuantStep s;
     s.B = B;
     s.h_kv = h_kv;
@@ -269,15 +289,36 @@ QuantStep quant_step_shape(bool f32, int d_k, int d_v, int B, int h, int h_kv, i
     s.rows = s.per * T_q;
     s.dv = d_v;
     const bool mma = quant_mma_serves(d_k, d_v);
-    s.rb = mma ? quant_mma_rows(f32, d_k, s.rows) : QD_ROWS;
+    s.rb = mma ? quant_mma_rows(f32, bits, d_k, s.rows) : QD_ROWS;
     s.nrb = (s.rows + s.rb - 1) / s.rb;
     int64_t ctas = (int64_t)sms * (mma ? quant_mma_ctas(f32, d_k, s.rb) : 2);
     const int64_t most = quant_most_quanta(s), groups = (int64_t)B * s.lanes();
-    s.clusters = mma && groups * kQuantCluster <= ctas && T_max <= kQuantCluster * kClusterQuanta * kQuantum && T_max > kQuantum;
+    const int nq = (T_max + kQuantum - 1) / kQuantum;
     if (ctas > kQuantMaxCtas) ctas = kQuantMaxCtas;
+    s.quantum = kQuantum;
+    if (groups > ctas && (groups + ctas - 1) / ctas * nq <= groups * nq / ctas + kJoinQuanta) s.quantum = nq * kQuantum;
+    s.cluster = 0;
+    s.parts = 1;
+    if (mma) {
+        int c = kQuantCluster;  // as large as lets all groups run at a time, and no larger than there are quanta
+        while (c > 1 && (groups * c > ctas || nq < c)) c /= 2;
+        const int64_t parts = ctas * 85 / 100 / (groups * kQuantCluster);
+        if (B == 1 && parts > 1 && nq > kQuantCluster * kClusterQuantaOne) {
+            s.cluster = kQuantCluster;
+            s.parts = (int)parts;
+        } else if (groups * c <= ctas && nq <= c * kClusterQuanta) {
+            s.cluster = c;
+        }
+    }
     if (ctas > most) ctas = most;
-    if (s.clusters) ctas = groups * kQuantCluster;
+    if (s.cluster) ctas = groups * s.cluster * s.parts;
     s.ctas = ctas < 1 ? 1 : (int)ctas;
+    s.by_T_q = Divide((uint32_t)(T_q < 1 ? 1 : T_q));
+    s.by_nrb = Divide((uint32_t)(s.nrb < 1 ? 1 : s.nrb));
+    s.by_lanes = Divide((uint32_t)(s.lanes() < 1 ? 1 : s.lanes()));
+    s.by_quantum = Divide((uint32_t)s.quantum);
+    s.by_ctas = Divide((uint32_t)s.ctas);
+    s.by_group = Divide((uint32_t)(s.cluster * s.parts < 1 ? 1 : s.cluster * s.parts));
     return s;
 }
 
@@ -307,10 +348,10 @@ cudaError_t launch_quant_decode(const QuantStep& s, bool f32, int bits, const Qu
             err = launch_pdl(kernel, dim3((unsigned)s.ctas), dim3(QD_THREADS), qd_smem(pk, pv), stream, s, pk, pv,
                              static_cast<const T*>(Q), ldq, static_cast<T*>(O), ldo, lengths, scale, part, status);
         }
-        if (err != cudaSuccess || s.clusters || s.T_max <= kQuantum) return err;  // (groups of one quantum are never shared)
+        if (err != cudaSuccess || (s.cluster ? s.parts == 1 : s.T_max <= s.quantum)) return err;  // (groups of one quantum are never shared)
         // threads: for as many slices as leave each about eight records of an evenly cut step
         const int width = s.dv <= 64 ? 64 : s.dv <= 128 ? 128 : 256;
-        const int64_t n = s.ctas / ((int64_t)s.B * s.lanes()) + 2;
+        const int64_t n = s.cluster ? s.parts : s.ctas / ((int64_t)s.B * s.lanes()) + 2;
         int threads = 256;
         while (threads < 1024 && n > 8 * (threads / width)) threads *= 2;
         return launch_pdl(quant_join_kernel<T>, dim3((unsigned)((int64_t)s.B * s.h_kv * s.rows)), dim3((unsigned)threads), 0,

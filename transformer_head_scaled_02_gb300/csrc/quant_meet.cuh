@@ -14,7 +14,7 @@ __device__ __forceinline__ void quant_put(__nv_bfloat16* p, float x) { *p = __fl
 // Where row r of the block that begins at row r0 of a head's rows goes.
 template <typename T>
 __device__ __forceinline__ T* quant_out(const QuantStep& s, T* O, int64_t ldo, int b, int g, int rr) {
-    const int hg = rr / s.T_q;
+    const int hg = s.by_T_q((uint32_t)rr);
     return O + ((int64_t)b * s.T_q + (rr - hg * s.T_q)) * ldo + (int64_t)(g * s.per + hg) * s.dv;
 }
 
@@ -33,11 +33,11 @@ __device__ __noinline__ void quant_invalid(const QuantStep& s, int b, int step, 
 
 // A piece's ENTRIES results for each of `rows` rows (the warps', or several of a warp), [entry][row] of `stride` floats:
 // dv values, then at ml m and l.  Either they are finished (whole), or they become records at rec.  All threads, behind a
-// barrier; an entry's m becomes its factor.
-template <int ENTRIES, int THREADS, typename T>
+// barrier; an entry's m becomes its factor.  DV: dv if it is known.
+template <int ENTRIES, int THREADS, int DV, typename T>
 __device__ __forceinline__ void quant_meet(const QuantStep& s, bool whole, float* rec, float* res, int rows, int stride, int ml,
                                            int b, int g, int r0, int nr, T* O, int64_t ldo) {
-    const int tid = (int)threadIdx.x;
+    const int tid = (int)threadIdx.x, dv = DV > 0 ? DV : s.dv, record = dv + 2;
     // ENTRIES lanes a row: maximum and sum
     for (int r = tid / ENTRIES; r < nr; r += THREADS / ENTRIES) {
         float* a = res + ((tid % ENTRIES) * rows + r) * stride + ml;
@@ -55,20 +55,20 @@ __device__ __forceinline__ void quant_meet(const QuantStep& s, bool whole, float
         } else {
             a[0] = f;
             if (tid % ENTRIES == 0) {
-                rec[r * s.record()] = M;
-                rec[r * s.record() + 1] = l;
+                rec[r * record] = M;
+                rec[r * record + 1] = l;
             }
         }
     }
     __syncthreads();
-    for (int e = tid; e < nr * s.dv; e += THREADS) {
-        const int r = e / s.dv, c = e - r * s.dv;
+    for (int e = tid; e < nr * dv; e += THREADS) {
+        const int r = e / dv, c = e - r * dv;
         const float* a = res + r * stride;
         float x = 0.f;
 #pragma unroll
         for (int w = 0; w < ENTRIES; ++w) x = fmaf(a[w * rows * stride + ml], a[w * rows * stride + c], x);
         if (whole) quant_put(quant_out(s, O, ldo, b, g, r0 + r) + c, x);
-        else rec[r * s.record() + 2 + c] = x;
+        else rec[r * record + 2 + c] = x;
     }
 }
 

@@ -213,21 +213,21 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
     QuantPlan plan;
     QuantPiece own;  // of a cluster's CTA
     int begin, end;
-    if (s.clusters) {
+    if (s.cluster) {
         own = quant_cluster_piece(s, lengths);
         begin = own.q0;
         end = own.q1;
         if (own.nq == 0) {
-            if (blockIdx.x % (kQuantCluster * s.lanes()) == 0) quant_invalid<QM_THREADS>(s, own.b, s.B, lengths, O, ldo, status);
+            if (blockIdx.x % (unsigned)(s.cluster * s.parts * s.lanes()) == 0) quant_invalid<QM_THREADS>(s, own.b, s.B, lengths, O, ldo, status);
             return;
         }
     } else {
         plan = quant_plan(s, lengths);
-        begin = plan.first((int)blockIdx.x);
-        end = plan.first((int)blockIdx.x + 1);
+        begin = plan.first(s, (int)blockIdx.x);
+        end = plan.first(s, (int)blockIdx.x + 1);
         if (plan.bad) quant_invalid<QM_THREADS>(s, (int)blockIdx.x, (int)gridDim.x, lengths, O, ldo, status);
     }
-    auto piece = [&](int q) { return s.clusters ? own : quant_piece(s, lengths, plan, q, end); };
+    auto piece = [&](int q) { return s.cluster ? own : quant_piece(s, lengths, plan, q, end); };
     // One warp at a time asks for the next stage (all its lanes call this): at first warp 0, then whichever is the last
     // to have used the stage whose place it takes.
     auto fetch = [&](QmNext& x) {
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
             if (x.at >= end) return;
             const QuantPiece z = piece(x.at);
             x.at = z.next;
-            x.row = ((int64_t)z.b * s.h_kv + z.lane / s.nrb) * s.T_max;
+            x.row = ((int64_t)z.b * s.h_kv + s.by_nrb((uint32_t)z.lane)) * s.T_max;
             x.from = z.k0();
             x.to = z.k1();
         }
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
     for (int q_at = begin; q_at < end;) {
     const QuantPiece z = piece(q_at);
     q_at = z.next;
-    const int b = z.b, g = z.lane / s.nrb, L = z.L;
+    const int b = z.b, g = s.by_nrb((uint32_t)z.lane), L = z.L;
     const int r0 = (z.lane - g * s.nrb) * C::ROWS, nr = min(C::ROWS, s.rows - r0);
 
     // queries: a warp makes a row's B operands, as the lanes will want them, its sum per group and the factor that turns
@@ -277,14 +277,13 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
         float* qv = reinterpret_cast<float*>(smem + C::QS);
 #pragma unroll 1
         for (int r = warp; r < C::ROWS; r += QM_WARPS) {
-            const int rr = r0 + min(r, nr - 1), hg = rr / s.T_q, t = rr - hg * s.T_q;
+            const int rr = r0 + min(r, nr - 1), hg = s.by_T_q((uint32_t)rr), t = rr - hg * s.T_q;
             const T* src = Q + ((int64_t)b * s.T_q + t) * ldq + (int64_t)(g * s.per + hg) * D + lane * CPL;
             float x[CPL], top = 0.f;
 #pragma unroll
-            for (int e = 0; e < CPL; ++e) {
-                x[e] = elem(src + e);
-                top = fmaxf(top, fabsf(x[e]));
-            }
+            for (int e = 0; e < CPL; ++e) x[e] = elem(src + e);
+#pragma unroll
+            for (int e = 0; e < CPL; ++e) top = fmaxf(top, fabsf(x[e]));
 #pragma unroll
             for (int w = 16; w >= 1; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
             // the largest element to [2^13, 2^14); zero, infinite and tiny rows as far as powers of two go
@@ -429,7 +428,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int r = (8 * nt + 2 * tig + e) % C::ROWS;
-                        const int lim = min(w_end, lim_min + (r0 + min(r, nr - 1)) % s.T_q);
+                        const int rr = r0 + min(r, nr - 1), lim = min(w_end, lim_min + rr - s.by_T_q((uint32_t)rr) * s.T_q);
                         if (ta >= lim) y[nt][e] = -INFINITY;
                         if (tb >= lim) y[nt][e + 2] = -INFINITY;
                     }
@@ -587,23 +586,24 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
         }
     __syncthreads();
     // (a cluster's CTA, which has one piece, is through with its ring)
-    float* rec = s.clusters ? reinterpret_cast<float*>(smem) : part + s.slot((int)blockIdx.x, z.q0 == 0 ? 1 : 0, 0);
-    quant_meet<QM_WARPS * SUB, QM_THREADS>(s, !s.clusters && z.whole(), rec, reinterpret_cast<float*>(smem + C::RES), C::ROWS, C::REC,
+    const bool whole = s.cluster ? s.cluster * s.parts == 1 : z.whole();
+    float* rec = s.cluster > 1 ? reinterpret_cast<float*>(smem) : part + s.slot((int)blockIdx.x, z.q0 == 0 ? 1 : 0, 0);
+    quant_meet<QM_WARPS * SUB, QM_THREADS, D>(s, whole, rec, reinterpret_cast<float*>(smem + C::RES), C::ROWS, C::REC,
                                            D, b, g, r0, nr, O, ldo);
     __syncthreads();
     }
-    if (s.clusters) {  // the CTAs' records meet, an eighth of the outputs in each
-        const int g = own.lane / s.nrb, r0 = (own.lane - g * s.nrb) * C::ROWS, nr = min(C::ROWS, s.rows - r0);
+    if (s.cluster > 1) {  // the CTAs' records meet, a share of the outputs in each
+        const int g = s.by_nrb((uint32_t)own.lane), r0 = (own.lane - g * s.nrb) * C::ROWS, nr = min(C::ROWS, s.rows - r0);
         if (begin == end)  // had nothing
             for (int r = tid; r < nr; r += QM_THREADS) reinterpret_cast<float*>(smem)[r * (D + 2)] = kNone;
         cluster_sync_all();
-        for (int e = (int)cluster_ctarank() * QM_THREADS + tid; e < nr * D; e += kQuantCluster * QM_THREADS) {
+        for (int e = (int)cluster_ctarank() * QM_THREADS + tid; e < nr * D; e += s.cluster * QM_THREADS) {
             const int r = e / D, c = e % D;
             float m[kQuantCluster], l[kQuantCluster], v[kQuantCluster], M = kNone, sum = 0.f, x = 0.f;
 #pragma unroll
             for (int k = 0; k < kQuantCluster; ++k) {
-                const uint32_t at = mapa_shared(ring, (uint32_t)k) + (uint32_t)(r * (D + 2) * 4);
-                m[k] = ld_shared_cluster(at);
+                const uint32_t at = mapa_shared(ring, (uint32_t)min(k, s.cluster - 1)) + (uint32_t)(r * (D + 2) * 4);
+                m[k] = k < s.cluster ? ld_shared_cluster(at) : kNone;
                 l[k] = ld_shared_cluster(at + 4);
                 v[k] = ld_shared_cluster(at + 8 + 4 * c);
                 M = fmaxf(M, m[k]);
@@ -615,7 +615,13 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
                     sum = fmaf(f, l[k], sum);
                     x = fmaf(f, v[k], x);
                 }
-            quant_put(quant_out(s, O, ldo, own.b, g, r0 + r) + c, x / sum);
+            if (s.parts == 1) {
+                quant_put(quant_out(s, O, ldo, own.b, g, r0 + r) + c, x / sum);
+            } else {
+                float* to = part + ((int64_t)((int)blockIdx.x / s.cluster) * C::ROWS + r) * s.record();
+                to[2 + c] = x;
+                if (c == 0) to[0] = M, to[1] = sum;
+            }
         }
         cluster_sync_all();  // no CTA leaves while its record is read
     }
@@ -632,7 +638,7 @@ cudaError_t launch(const QuantStep& s, const QuantPlane& pk, const QuantPlane& p
     const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (err != cudaSuccess) return err;
     const float scale = (float)(1.4426950408889634 / sqrt((double)D));
-    return launch_pdl_cluster(kernel, s.clusters ? kQuantCluster : 1, dim3((unsigned)s.ctas), dim3(QM_THREADS), C::SMEM, stream, s,
+    return launch_pdl_cluster(kernel, s.cluster > 1 ? s.cluster : 1, dim3((unsigned)s.ctas), dim3(QM_THREADS), C::SMEM, stream, s,
                               pk, pv, static_cast<const T*>(Q), ldq, static_cast<T*>(O), ldo, lengths, scale, part, status);
 }
 
@@ -642,7 +648,8 @@ constexpr bool most_rows_16(int terms, int d) { return !(terms == 2 && d == 128)
 template <int BITS, int D, typename T, typename... A>
 cudaError_t launch_rows(int rb, A... a) {
     constexpr int TERMS = std::is_same_v<T, float> ? 2 : 1;
-    if (rb == 4) return launch<BITS, D, TERMS, 1, 2, T>(a...);
+    if constexpr (BITS * D <= 512)
+        if (rb == 4) return launch<BITS, D, TERMS, 1, 2, T>(a...);
     if (rb == 8) return launch<BITS, D, TERMS, 1, 1, T>(a...);
     if constexpr (most_rows_16(TERMS, D)) return launch<BITS, D, TERMS, 2, 1, T>(a...);
     return cudaErrorInvalidValue;
@@ -652,9 +659,12 @@ cudaError_t launch_rows(int rb, A... a) {
 
 bool quant_mma_serves(int d_k, int d_v) { return d_k == d_v && (d_k == 64 || d_k == 128); }
 
-// Query rows of a block: 4, whose columns two blocks of tokens share, 8, or 16 (two sets of operands and sums beside each
-// unpacked code).
-int quant_mma_rows(bool f32, int d, int rows) { return rows <= 4 ? 4 : rows <= 8 || !most_rows_16(f32 ? 2 : 1, d) ? 8 : 16; }
+// Query rows of a block: 4, whose columns two blocks of tokens share (a warp's part of a stage of 8 bits and 128 channels
+// is one block), 8, or 16 (two sets of operands and sums beside each unpacked code).
+int quant_mma_rows(bool f32, int bits, int d, int rows) {
+    if (rows <= 4 && bits * d <= 512) return 4;
+    return rows <= 8 || !most_rows_16(f32 ? 2 : 1, d) ? 8 : 16;
+}
 
 int quant_mma_ctas(bool f32, int d, int rb) { return (f32 ? 2 : 1) * (d / 64) * (rb == 16 ? 2 : 1) > 2 ? 1 : 2; }
 
