@@ -289,6 +289,52 @@ def test_decode_many_rows(dtype, d, h, h_kv, Tq, bits):
     _step(layer, cache, held, wl.random_tensor((3, Tq, h * d), 5, dtype), lengths, dtype, "many rows")
 
 
+@pytest.mark.parametrize("d,h,h_kv,Tq,lengths", [
+    (128, 2, 1, 130, [400, 130, 257]), (64, 4, 1, 65, [65, 700, 129]), (128, 4, 2, 200, [1500]),
+    (64, 8, 1, 100, [128, 100, 640, 127, 384]), (128, 1, 1, 256, [256, 300])])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_decode_prompt_pieces(d, h, h_kv, Tq, lengths, bits):
+    """Hundreds of query rows of a cached head: blocks of 128 rows, the last one partly filled, whole warps of it idle;
+    groups of one tile, of several, and shared by CTAs; an invalid length between them."""
+    layer = _layer("bf16", h, d, h_kv)
+    T = max(lengths)
+    cache, held = _filled(layer, d + h, "bf16", len(lengths) + 1, T, bits)
+    lengths = lengths[:1] + [Tq - 1] + lengths[1:]
+    _spoil(cache, lengths)
+    Q = wl.random_tensor((len(lengths), Tq, h * d), 5, "bf16")
+    first = layer.decode_quant(to_device(Q, "bf16"), cache, _ints(lengths))
+    assert layer.status() == _lib.MHA_ERR_BAD_LENGTH
+    got = to_host(first)
+    O, A, S = qc.decode(Q, *held, h, lengths)
+    assert np.isnan(got[1]).all()
+    keep = np.arange(len(lengths)) != 1
+    _check(got[keep], O[keep], A[keep], S[keep], "bf16", "prompt pieces")
+    again = layer.decode_quant(to_device(Q, "bf16"), cache, _ints(lengths))
+    assert torch.equal(again[torch.from_numpy(keep).cuda()], first[torch.from_numpy(keep).cuda()])
+
+
+def test_decode_prompt_pieces_large_scores_and_scales():
+    """The same with scores that rise along the keys and steps that differ by 2^40: references and scales move."""
+    d, Tq, T = 128, 256, 700
+    layer = _layer("bf16", 1, d, 1)
+    Q, K, V = (wl.random_tensor((1, n, d), 70 + i, "bf16") for i, n in enumerate((Tq, T, T)))
+    rnd = lambda x: wl.bf16_to_f32(wl.bf16_bits(x.astype(np.float32)))  # noqa: E731
+    ramp = np.linspace(0.1, 6.0, T)[None, :, None]
+    powers = 2.0 ** np.random.default_rng(3).integers(-20, 20, T)[None, :, None]
+    for q, k, v in ((Q * 4, K * ramp, V), (Q, K, V * powers), (Q * 2.0 ** 60, K * 2.0 ** -60, V * 2.0 ** 100)):
+        q, k, v = rnd(q), rnd(k), rnd(v)
+        cache = layer.quant_cache(1, T, 4)
+        layer.quant_write(cache, to_device(k, "bf16"), to_device(v, "bf16"), _ints([T]))
+        held = _held(cache, "K") + _held(cache, "V")
+        got = to_host(layer.decode_quant(to_device(q, "bf16"), cache, _ints([T])))
+        O, A, S = qc.decode(q, *held, 1, [T])
+        assert np.isfinite(got).all()
+        p = np.repeat(held[1], 64, -2)[0, :, :T]
+        s = np.max(np.abs(q[0]) @ np.moveaxis(np.abs(p[..., 1]) + p[..., 0] * 15, -1, -2)[0]) / np.sqrt(d)
+        w = 2 * s * (d + 8) * 2.0 ** -23
+        assert (np.abs(got - O) <= 2.0 ** -8 * np.abs(O) + 2.0 ** -11 * S + (w + 1e-5) * (A + S)).all()
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("f32", 64), ("f32", 48)])
 @pytest.mark.parametrize("bits", [4, 8])
 def test_decode_long(dtype, d, bits):

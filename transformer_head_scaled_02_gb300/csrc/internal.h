@@ -180,6 +180,9 @@ bool quant_step_fits(const QuantStep& s);
 cudaError_t launch_quant_decode(const QuantStep& s, bool f32, int bits, const QuantPlane& pk, const QuantPlane& pv,
                                 const void* Q, int64_t ldq, void* O, int64_t ldo, const int32_t* lengths, float* part,
                                 int* status, cudaStream_t stream);
+// Steps of many rows of bf16 layers (quant_rows.cu).
+cudaError_t launch_quant_rows(const QuantStep& s, int bits, const QuantPlane& pk, const QuantPlane& pv, const void* Q, int64_t ldq,
+                              void* O, int64_t ldo, const int32_t* lengths, float* part, int* status, cudaStream_t stream);
 // The tensor-core kernel: head sizes it serves, query rows of its blocks, CTAs that an SM holds, the launch.
 bool quant_mma_serves(int d_k, int d_v);
 int quant_mma_rows(bool f32, int bits, int d, int rows);

@@ -171,27 +171,27 @@ __global__ void __launch_bounds__(QD_THREADS)
     }
 }
 
-// The join: a block per output row.  Threads take the columns, in as many slices of the records as there are threads
-// for; a slice's maxima, sums and values are loaded together, so that a row costs about one round trip to L2, a second
-// one for every eight records of a slice, and the slices meet in shared memory.
+// The join.  A block has `run` rows of a group; its threads take (row, slice of the records, column), `width` columns and
+// `slices` slices.  A slice's maxima, sums and values are loaded together, so that a row costs about one round trip to L2
+// and one more for every eight records of a slice; slices meet in shared memory.
 template <typename T>
 __global__ void __launch_bounds__(1024)
     quant_join_kernel(const QuantStep s, const float* __restrict__ part, T* __restrict__ O, int64_t ldo,
-                      const int32_t* __restrict__ lengths) {
+                      const int32_t* __restrict__ lengths, int width, int slices, int run, int chunks) {
     __shared__ float ys[1024], ms[1024], ls[1024];
     const int tid = (int)threadIdx.x;
-    const int heads = s.h_kv * s.per, row = (int)blockIdx.x;
-    const int bh = s.by_T_q((uint32_t)row), t = row - bh * s.T_q, b = bh / heads, head = bh - b * heads;
-    const int g = head / s.per, rr = (head - g * s.per) * s.T_q + t, block = rr / s.rb, r = rr - block * s.rb;
+    const int group = (int)blockIdx.x / chunks, chunk = (int)blockIdx.x - group * chunks;
+    const int b = s.by_lanes((uint32_t)group), lane_i = group - b * s.lanes(), g = s.by_nrb((uint32_t)lane_i);
+    const int r0 = (lane_i - g * s.nrb) * s.rb, nr = min(s.rb, s.rows - r0);
     // The kernel before lets this one start once its own wait for earlier work is over: the lengths can be read (from
     // L2), its records not yet.
-    const float *rec, *others;  // the group's first record, and record i >= 1 at others + i * stride
+    const float *first, *others;  // row 0 of the group's first record, and of record i >= 1 at others + i * stride
     int64_t stride;
     int n;
     if (s.cluster) {  // one record a cluster
         n = quant_quanta(s, __ldcg(lengths + b)) > 0 ? s.parts : 0;
         stride = (int64_t)s.rb * s.record();
-        rec = others = part + (int64_t)((b * s.h_kv + g) * s.nrb + block) * s.parts * stride + r * s.record();
+        first = others = part + (int64_t)group * s.parts * stride;
     } else {
         const QuantPlan p = quant_plan(s, lengths);
         int at = 0, len = 0;
@@ -204,57 +204,65 @@ __global__ void __launch_bounds__(1024)
         }
         const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
         const int nq = quant_quanta(s, __shfl_sync(0xffffffffu, len, src));
-        const int first = __shfl_sync(0xffffffffu, at, src) + (g * s.nrb + block) * nq;
-        const int c0 = nq > 0 ? p.owner(s, first) : 0;
-        n = nq > 0 ? p.owner(s, first + nq - 1) - c0 + 1 : 0;
+        const int q0 = __shfl_sync(0xffffffffu, at, src) + lane_i * nq;
+        const int c0 = nq > 0 ? p.owner(s, q0) : 0;
+        n = nq > 0 ? p.owner(s, q0 + nq - 1) - c0 + 1 : 0;
         // of the first CTA its last group, of the others their first
-        rec = part + s.slot(c0, 1, r);
-        others = part + s.slot(c0, 0, r);
+        first = part + s.slot(c0, 1, 0);
+        others = part + s.slot(c0, 0, 0);
         stride = s.slot(1, 0, 0);
     }
-    const int width = s.dv <= 64 ? 64 : s.dv <= 128 ? 128 : 256, slices = (int)blockDim.x / width;
-    const int e = tid % width, slice = tid / width;
+    const int e = tid % width, slice = tid / width % slices, at_once = (int)blockDim.x / (width * slices);
     grid_dependency_wait();
     grid_launch_dependents();
-    if (n <= 1) return;  // an invalid length (written as NaN already), or a group that one CTA had alone
-    float M = -INFINITY, l = 0.f, x = 0.f;
-    for (int i0 = slice; i0 < n; i0 += 8 * slices) {
-        float m[8], sum[8], v[8], top = M;
+    if (n <= 1 && !s.cluster) return;  // an invalid length (written as NaN already), or a group that one CTA had alone
+    if (n == 0) return;
+#pragma unroll 1
+    for (int k0 = 0; k0 < run; k0 += at_once) {
+        const int r = chunk * run + k0 + tid / (width * slices);
+        const bool live = r < nr && k0 + tid / (width * slices) < run;
+        float M = -INFINITY, l = 0.f, x = 0.f;
+        for (int i0 = slice; live && i0 < n; i0 += 8 * slices) {
+            float m[8], sum[8], v[8], top = M;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int i = min(i0 + k * slices, n - 1);
-            const float* a = i == 0 ? rec : others + i * stride;
-            m[k] = i0 + k * slices < n ? __ldcg(a) : -INFINITY;
-            sum[k] = __ldcg(a + 1);
-            v[k] = e < s.dv ? __ldcg(a + 2 + e) : 0.f;
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) top = fmaxf(top, m[k]);
-        const float f = M == -INFINITY ? 0.f : exp2f(M - top);
-        l *= f;
-        x *= f;
-        M = top;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (m[k] != -INFINITY) {
-                const float fk = exp2f(m[k] - M);
-                l = fmaf(fk, sum[k], l);
-                x = fmaf(fk, v[k], x);
+            for (int k = 0; k < 8; ++k) {
+                const int i = min(i0 + k * slices, n - 1);
+                const float* a = (i == 0 ? first : others + i * stride) + r * s.record();
+                m[k] = i0 + k * slices < n ? __ldcg(a) : -INFINITY;
+                sum[k] = __ldcg(a + 1);
+                v[k] = e < s.dv ? __ldcg(a + 2 + e) : 0.f;
             }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) top = fmaxf(top, m[k]);
+            const float f = M == -INFINITY ? 0.f : exp2f(M - top);
+            l *= f;
+            x *= f;
+            M = top;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (m[k] != -INFINITY) {
+                    const float fk = exp2f(m[k] - M);
+                    l = fmaf(fk, sum[k], l);
+                    x = fmaf(fk, v[k], x);
+                }
+        }
+        if (slices > 1) {
+            __syncthreads();  // the rows before are read
+            ys[tid] = x;
+            ms[tid] = M;
+            ls[tid] = l;
+            __syncthreads();
+            if (slice > 0) continue;
+            for (int k = 1; k < slices; ++k) M = fmaxf(M, ms[tid + k * width]);
+            l = x = 0.f;
+            for (int k = 0; k < slices; ++k) {
+                const float m = ms[tid + k * width], f = m == -INFINITY ? 0.f : exp2f(m - M);
+                l = fmaf(f, ls[tid + k * width], l);
+                x = fmaf(f, ys[tid + k * width], x);
+            }
+        }
+        if (live && e < s.dv) quant_put(quant_out(s, O, ldo, b, g, r0 + r) + e, x / l);
     }
-    ys[tid] = x;
-    ms[tid] = M;
-    ls[tid] = l;
-    __syncthreads();
-    if (slice > 0 || e >= s.dv) return;
-    for (int k = 1; k < slices; ++k) M = fmaxf(M, ms[k * width + e]);
-    l = x = 0.f;
-    for (int k = 0; k < slices; ++k) {
-        const float m = ms[k * width + e], f = m == -INFINITY ? 0.f : exp2f(m - M);
-        l = fmaf(f, ls[k * width + e], l);
-        x = fmaf(f, ys[k * width + e], x);
-    }
-    quant_put(O + ((int64_t)b * s.T_q + t) * ldo + (int64_t)head * s.dv + e, x / l);
 }
 
 size_t qd_smem(const QuantPlane& pk, const QuantPlane& pv) {
@@ -272,10 +280,20 @@ size_t qd_smem(const QuantPlane& pk, const QuantPlane& pv) {
 // of them 23.3.
 constexpr int kClusterQuanta = 16;
 constexpr int kClusterQuantaOne = 6;
+constexpr int kClusterQuantaWide = 6;  // of CTAs that an SM holds one of: 8 of 8192, one head of 128, 32 rows, 8 quanta 24.4 | 16.9
 
 // With more groups than CTAs: the quanta that a CTA may have more than others, where groups are not cut at all, for the
 // join and the shared groups' ends that this saves.  32 sequences of 300 tokens, 16 heads of 128, 8 bits: kQWhole us.
 constexpr int kJoinQuanta = 6;
+
+// bf16 steps of at least this many rows of a cached head go to quant_rows.cu, in blocks of 128 (us, there | quant_mma.cu:
+// 2048 rows, one sequence of 8192 tokens, 4 heads of 128, 4 bits 109 | 160; 512 rows, 4 of 4096, 4 of 64 48 | 58; 128
+// rows, 8 of 8192, one of 128 42 | 31: its records are large).
+constexpr int kManyRows = 256;
+constexpr int kManyRowsBlock = 128;
+constexpr int kManyRowsCtas = 320;  // most of its CTAs: one an SM
+
+static int64_t most_ctas(const QuantStep& s) { return s.rb == kManyRowsBlock ? kManyRowsCtas : kQuantMaxCtas; }
 
 // Rows of a block by the kernel that serves the head size; CTAs: as many as the GPU holds at a time, but no more than
 // there may be quanta.
@@ -288,13 +306,13 @@ QuantStep quant_step_shape(bool f32, int bits, int d_k, int d_v, int B, int h, i
     s.T_max = T_max;
     s.rows = s.per * T_q;
     s.dv = d_v;
-    const bool mma = quant_mma_serves(d_k, d_v);
-    s.rb = mma ? quant_mma_rows(f32, bits, d_k, s.rows) : QD_ROWS;
+    const bool many = !f32 && s.rows >= kManyRows, mma = !many && quant_mma_serves(d_k, d_v);
+    s.rb = many ? kManyRowsBlock : mma ? quant_mma_rows(f32, bits, d_k, s.rows) : QD_ROWS;
     s.nrb = (s.rows + s.rb - 1) / s.rb;
-    int64_t ctas = (int64_t)sms * (mma ? quant_mma_ctas(f32, d_k, s.rb) : 2);
+    int64_t ctas = (int64_t)sms * (many ? 1 : mma ? quant_mma_ctas(f32, d_k, s.rb) : 2);
     const int64_t most = quant_most_quanta(s), groups = (int64_t)B * s.lanes();
     const int nq = (T_max + kQuantum - 1) / kQuantum;
-    if (ctas > kQuantMaxCtas) ctas = kQuantMaxCtas;
+    if (ctas > most_ctas(s)) ctas = most_ctas(s);
     s.quantum = kQuantum;
     if (groups > ctas && (groups + ctas - 1) / ctas * nq <= groups * nq / ctas + kJoinQuanta) s.quantum = nq * kQuantum;
     s.cluster = 0;
@@ -306,7 +324,7 @@ QuantStep quant_step_shape(bool f32, int bits, int d_k, int d_v, int B, int h, i
         if (B == 1 && parts > 1 && nq > kQuantCluster * kClusterQuantaOne) {
             s.cluster = kQuantCluster;
             s.parts = (int)parts;
-        } else if (groups * c <= ctas && nq <= c * kClusterQuanta) {
+        } else if (groups * c <= ctas && nq <= c * (quant_mma_ctas(f32, d_k, s.rb) == 1 ? kClusterQuantaWide : kClusterQuanta)) {
             s.cluster = c;
         }
     }
@@ -327,11 +345,13 @@ int64_t quant_most_quanta(const QuantStep& s) { return (int64_t)s.B * s.h_kv * s
 // For any number of SMs.
 size_t quant_step_bytes(const QuantStep& s) {
     const int64_t most = quant_most_quanta(s);
-    const int64_t ctas = most < kQuantMaxCtas ? most : kQuantMaxCtas;
+    const int64_t ctas = most < most_ctas(s) ? most : most_ctas(s);
     return sizeof(float) * 2 * (size_t)ctas * s.rb * s.record();
 }
 
-bool quant_step_fits(const QuantStep& s) { return quant_most_quanta(s) <= INT32_MAX && (int64_t)s.B * s.h_kv * s.rows <= INT32_MAX; }
+bool quant_step_fits(const QuantStep& s) {
+    return quant_most_quanta(s) <= INT32_MAX && (int64_t)s.B * s.h_kv * s.nrb * s.rb <= INT32_MAX;
+}
 
 cudaError_t launch_quant_decode(const QuantStep& s, bool f32, int bits, const QuantPlane& pk, const QuantPlane& pv,
                                 const void* Q, int64_t ldq, void* O, int64_t ldo, const int32_t* lengths, float* part,
@@ -340,7 +360,9 @@ cudaError_t launch_quant_decode(const QuantStep& s, bool f32, int bits, const Qu
     auto go = [&](auto* x, auto kernel) {
         using T = std::remove_pointer_t<decltype(x)>;
         cudaError_t err;
-        if (quant_mma_serves(pk.d, pv.d)) {
+        if (s.rb == kManyRowsBlock) {
+            err = launch_quant_rows(s, bits, pk, pv, Q, ldq, O, ldo, lengths, part, status, stream);
+        } else if (quant_mma_serves(pk.d, pv.d)) {
             err = launch_quant_mma(s, f32, bits, pk, pv, Q, ldq, O, ldo, lengths, part, status, stream);
         } else {
             err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 << 10);
@@ -349,13 +371,18 @@ cudaError_t launch_quant_decode(const QuantStep& s, bool f32, int bits, const Qu
                              static_cast<const T*>(Q), ldq, static_cast<T*>(O), ldo, lengths, scale, part, status);
         }
         if (err != cudaSuccess || (s.cluster ? s.parts == 1 : s.T_max <= s.quantum)) return err;  // (groups of one quantum are never shared)
-        // threads: for as many slices as leave each about eight records of an evenly cut step
+        // slices: as many as leave each about eight records of an evenly cut step; rows of a block: one, more if there
+        // are more rows than some blocks an SM
+        const int64_t groups = (int64_t)s.B * s.lanes(), n = s.cluster ? s.parts : s.ctas / groups + 2;
         const int width = s.dv <= 64 ? 64 : s.dv <= 128 ? 128 : 256;
-        const int64_t n = s.cluster ? s.parts : s.ctas / ((int64_t)s.B * s.lanes()) + 2;
-        int threads = 256;
-        while (threads < 1024 && n > 8 * (threads / width)) threads *= 2;
-        return launch_pdl(quant_join_kernel<T>, dim3((unsigned)((int64_t)s.B * s.h_kv * s.rows)), dim3((unsigned)threads), 0,
-                          stream, s, static_cast<const float*>(part), static_cast<T*>(O), ldo, lengths);
+        int slices = 1;
+        while (slices * width < 1024 && n > 8 * slices) slices *= 2;
+        const int threads = slices * width > 256 ? slices * width : 256, most = s.rows < s.rb ? s.rows : s.rb;
+        int run = threads / (width * slices);
+        while (run < most && groups * ((most + run - 1) / run) > 1024) run *= 2;
+        const int chunks = (most + run - 1) / run;
+        return launch_pdl(quant_join_kernel<T>, dim3((unsigned)(groups * chunks)), dim3((unsigned)threads), 0, stream, s,
+                          static_cast<const float*>(part), static_cast<T*>(O), ldo, lengths, width, slices, run, chunks);
     };
     if (f32) return bits == 4 ? go(static_cast<float*>(nullptr), quant_decode_kernel<float, 4>)
                               : go(static_cast<float*>(nullptr), quant_decode_kernel<float, 8>);
