@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/mha.h"
 
 // The opaque handle of include/mha.h: the layer configuration and the caller's workspace.
@@ -61,6 +63,27 @@ cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), int cluster, dim3 grid,
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, Args... args) {
     return launch_pdl_cluster(kernel, 1, grid, block, smem, stream, args...);
+}
+
+// Launch with more than 48 KB of shared memory: the kernel's limit is raised once per device (a call of its own costs a
+// tenth of a short step's host time), and again should the device's context have been destroyed since.  `done`: a static
+// of the kernel's.
+template <typename Kernel, typename Launch>
+cudaError_t launch_with_smem(Kernel kernel, int bytes, std::atomic<uint64_t>& done, Launch launch) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    const bool known = (done.load(std::memory_order_relaxed) & bit) != 0;
+    if (known) {
+        err = launch();
+        if (err != cudaErrorInvalidValue) return err;
+        (void)cudaGetLastError();
+    }
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err != cudaSuccess) return err;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return launch();
 }
 
 // Encode a bf16 tiled tensor map with 128-byte swizzle (swizzle_bytes == 0: none) and zero

@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(1024)
 
 size_t qd_smem(const QuantPlane& pk, const QuantPlane& pv) {
     const int dpk = (pk.d + 31) & ~31, dpv = (pv.d + 31) & ~31;
-    return sizeof(float) * (size_t)QD_ROWS * (dpk + pk.groups + QD_WARPS * (dpv + 32));
+    return sizeof(float) * (size_t)QD_ROWS * (dpk + pk.groups + QD_WARPS * (dpv + 32));  // at most 41 KB
 }
 
 }  // namespace
@@ -280,7 +280,7 @@ size_t qd_smem(const QuantPlane& pk, const QuantPlane& pv) {
 // of them 23.3.
 constexpr int kClusterQuanta = 16;
 constexpr int kClusterQuantaOne = 6;
-constexpr int kClusterQuantaWide = 6;  // of CTAs that an SM holds one of: 8 of 8192, one head of 128, 32 rows, 8 quanta 24.4 | 16.9
+constexpr int kClusterQuantaWide = 6;  // of CTAs that an SM holds one of: 8 of 8192, one head of 128, 32 rows, 8 quanta 24.4 | 18.4
 
 // With more groups than CTAs: the quanta that a CTA may have more than others, where groups are not cut at all, for the
 // join and the shared groups' ends that this saves.  32 sequences of 300 tokens, 16 heads of 128, 8 bits: kQWhole us.
@@ -365,8 +365,6 @@ cudaError_t launch_quant_decode(const QuantStep& s, bool f32, int bits, const Qu
         } else if (quant_mma_serves(pk.d, pv.d)) {
             err = launch_quant_mma(s, f32, bits, pk, pv, Q, ldq, O, ldo, lengths, part, status, stream);
         } else {
-            err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 << 10);
-            if (err != cudaSuccess) return err;
             err = launch_pdl(kernel, dim3((unsigned)s.ctas), dim3(QD_THREADS), qd_smem(pk, pv), stream, s, pk, pv,
                              static_cast<const T*>(Q), ldq, static_cast<T*>(O), ldo, lengths, scale, part, status);
         }

@@ -635,11 +635,12 @@ cudaError_t launch(const QuantStep& s, const QuantPlane& pk, const QuantPlane& p
                    int64_t ldo, const int32_t* lengths, float* part, int* status, cudaStream_t stream) {
     using C = QmCfg<BITS, D, TERMS, NT, SUB>;
     auto kernel = quant_mma_kernel<BITS, D, TERMS, NT, SUB, T>;
-    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (err != cudaSuccess) return err;
+    static std::atomic<uint64_t> done{0};
     const float scale = (float)(1.4426950408889634 / sqrt((double)D));
-    return launch_pdl_cluster(kernel, s.cluster > 1 ? s.cluster : 1, dim3((unsigned)s.ctas), dim3(QM_THREADS), C::SMEM, stream, s,
-                              pk, pv, static_cast<const T*>(Q), ldq, static_cast<T*>(O), ldo, lengths, scale, part, status);
+    return launch_with_smem(kernel, C::SMEM, done, [&] {
+        return launch_pdl_cluster(kernel, s.cluster > 1 ? s.cluster : 1, dim3((unsigned)s.ctas), dim3(QM_THREADS), C::SMEM, stream, s,
+                                  pk, pv, static_cast<const T*>(Q), ldq, static_cast<T*>(O), ldo, lengths, scale, part, status);
+    });
 }
 
 // (fp32 layers of 128 channels have no room in the registers for 16 rows)

@@ -527,11 +527,12 @@ template <int BITS, int D>
 cudaError_t launch(const QuantStep& s, const QuantPlane& pk, const QuantPlane& pv, const void* Q, int64_t ldq, void* O, int64_t ldo,
                    const int32_t* lengths, float* part, int* status, cudaStream_t stream) {
     using C = QrCfg<BITS, D>;
-    const cudaError_t err = cudaFuncSetAttribute(quant_rows_kernel<BITS, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (err != cudaSuccess) return err;
+    static std::atomic<uint64_t> done{0};
     const float scale = (float)(1.4426950408889634 / sqrt((double)D));
-    return launch_pdl(quant_rows_kernel<BITS, D>, dim3((unsigned)s.ctas), dim3(QR_THREADS), C::SMEM, stream, s, pk, pv,
-                      static_cast<const __nv_bfloat16*>(Q), ldq, static_cast<__nv_bfloat16*>(O), ldo, lengths, scale, part, status);
+    return launch_with_smem(quant_rows_kernel<BITS, D>, C::SMEM, done, [&] {
+        return launch_pdl(quant_rows_kernel<BITS, D>, dim3((unsigned)s.ctas), dim3(QR_THREADS), C::SMEM, stream, s, pk, pv,
+                          static_cast<const __nv_bfloat16*>(Q), ldq, static_cast<__nv_bfloat16*>(O), ldo, lengths, scale, part, status);
+    });
 }
 
 }  // namespace

@@ -13,6 +13,7 @@ import torch
 
 from . import _lib
 
+_I32 = torch.int32
 _DTYPES = {torch.float32: _lib.MHA_F32, torch.bfloat16: _lib.MHA_BF16}
 
 
@@ -22,6 +23,10 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 # (torch.cuda's own function is a Python frame more)
 _capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream() -> int:
@@ -60,6 +65,10 @@ class Mha:
         self._kept_ws: list = []
         self._step_bytes: dict = {}  # workspace bytes of the cache steps, by their sizes
         self._heads = (self.h_kv, self.d_k, self.d_v)
+        self._wq, self._wk, self._wv = self.h * self.d_k, self.h_kv * self.d_k, self.h_kv * self.d_v
+        self._wo = self.h * self.d_v
+        lib = _lib.load()
+        self._c_quant = (lib.mha_quant_write, lib.mha_quant_read, lib.mha_decode_quant)
 
     @property
     def proj_width(self) -> int:
@@ -536,19 +545,23 @@ class Mha:
         multiple of 16.  Its contents are unset: quant_write fills it, decode_quant attends over it."""
         return QuantCache(self, B, T_max, bits)
 
-    def _quant_lens(self, cache: "QuantCache", lengths: torch.Tensor) -> int:
+    # (The calls below are a short step's host time: the checks' quick forms come first, those that say what is wrong
+    # only run when one fails.)
+    def _quant_ints(self, cache: "QuantCache", name: str, t: torch.Tensor) -> int:
+        if t.dtype is _I32 and t.shape == cache.lens and t.is_contiguous() and cache.heads == self._heads:
+            return t.data_ptr()
         if cache.heads != self._heads:
             raise ValueError(f"the cache holds (heads, d_k, d_v) {cache.heads}, expected {self._heads}")
-        return self._ints("cache_lengths", lengths, cache.B)
+        return self._ints(name, t, cache.B)
 
     def _quant_ready(self, cache: "QuantCache", X: torch.Tensor, Y: torch.Tensor, lengths: torch.Tensor,
                      counts: Optional[torch.Tensor], need: int) -> int:
         """All on the cache's device, the current one, and `need` bytes of workspace there; returns its stream."""
         dev = cache.device
         if dev < 0 or X.get_device() != dev or Y.get_device() != dev or lengths.get_device() != dev or \
-                (counts is not None and counts.get_device() != dev) or torch._C._cuda_getDevice() != dev:
+                (counts is not None and counts.get_device() != dev) or _current_device() != dev:
             self._device(cache.data, X, Y, lengths, counts)  # says what is wrong
-        stream = torch._C._cuda_getCurrentRawStream(dev)
+        stream = _current_stream(dev)
         if need > self._ws_bytes or stream not in self._ws_streams or _capturing():
             self.ensure_workspace(0, 0, 0, need=need)
         return stream
@@ -559,13 +572,16 @@ class Mha:
         the cache.  cache_lengths (int32, B) count the cached tokens including the new ones, as decode_quant wants
         them; counts (int32, B; default: T_new) how many rows of each sequence are tokens: the first n_b rows
         become tokens L_b - n_b .. L_b - 1."""
-        lens = self._quant_lens(cache, cache_lengths)
-        n = None if counts is None else self._ints("counts", counts, cache.B)
+        lens = self._quant_ints(cache, "cache_lengths", cache_lengths)
+        n = None if counts is None else self._quant_ints(cache, "counts", counts)
+        bits, B, T_max, ptr = cache.args
         T = K.shape[1]
-        ldk = self._rows("K", K, cache.B, T, self.h_kv * self.d_k)
-        ldv = self._rows("V", V, cache.B, T, self.h_kv * self.d_v)
+        ldk = self._rows("K", K, B, T, self._wk)
+        ldv = self._rows("V", V, B, T, self._wv)
         stream = self._quant_ready(cache, K, V, cache_lengths, counts, 256)  # the status word
-        _lib.mha_quant_write(self.handle, *cache.args, T, K.data_ptr(), ldk, V.data_ptr(), ldv, lens, n, stream)
+        code = self._c_quant[0](self.handle, bits, B, T_max, ptr, T, K.data_ptr(), ldk, V.data_ptr(), ldv, lens, n, stream)
+        if code:
+            raise _lib.MhaError("mha_quant_write", code)
         return cache
 
     def quant_read(self, cache: "QuantCache", cache_lengths: torch.Tensor, counts: Optional[torch.Tensor] = None,
@@ -575,9 +591,10 @@ class Mha:
         0 .. n_b - 1 of K_out (B, T_out, h_kv*d_k view) and V_out (B, T_out, h_kv*d_v view); rows past n_b of
         given outputs stay, of new ones are unset.  T_out defaults to the cache's T_max or the given outputs' rows.
         counts=cache_lengths reads whole sequences.  Returns (K_out, V_out)."""
-        lens = self._quant_lens(cache, cache_lengths)
-        n = None if counts is None else self._ints("counts", counts, cache.B)
-        B, wk, wv = cache.B, self.h_kv * self.d_k, self.h_kv * self.d_v
+        lens = self._quant_ints(cache, "cache_lengths", cache_lengths)
+        n = None if counts is None else self._quant_ints(cache, "counts", counts)
+        bits, B, T_max, ptr = cache.args
+        wk, wv = self._wk, self._wv
         if T_out is None:
             T_out = K_out.shape[1] if K_out is not None else V_out.shape[1] if V_out is not None else cache.T_max
         if K_out is None:
@@ -587,27 +604,30 @@ class Mha:
         ldk = self._rows("K_out", K_out, B, T_out, wk)
         ldv = self._rows("V_out", V_out, B, T_out, wv)
         stream = self._quant_ready(cache, K_out, V_out, cache_lengths, counts, 256)  # the status word
-        _lib.mha_quant_read(self.handle, *cache.args, T_out, K_out.data_ptr(), ldk, V_out.data_ptr(), ldv, lens, n,
-                            stream)
+        code = self._c_quant[1](self.handle, bits, B, T_max, ptr, T_out, K_out.data_ptr(), ldk, V_out.data_ptr(), ldv, lens,
+                                n, stream)
+        if code:
+            raise _lib.MhaError("mha_quant_read", code)
         return K_out, V_out
 
     def decode_quant(self, Q: torch.Tensor, cache: "QuantCache", cache_lengths: torch.Tensor,
                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """decode() over a quantised cache: the keys and values are those that the codes stand for."""
-        lens = self._quant_lens(cache, cache_lengths)
+        lens = self._quant_ints(cache, "cache_lengths", cache_lengths)
         bits, B, T_max, ptr = cache.args
         T_q = Q.shape[1]
-        ldq = self._rows("Q", Q, B, T_q, self.h * self.d_k)
+        ldq = self._rows("Q", Q, B, T_q, self._wq)
         if out is None:
-            out = torch.empty((B, T_q, self.h * self.d_v), dtype=self.dtype, device=Q.device)
-        ldo = self._rows("out", out, B, T_q, self.h * self.d_v)
-        sizes = ("quant", B, T_q, T_max)
+            out = torch.empty((B, T_q, self._wo), dtype=self.dtype, device=Q.device)
+        ldo = self._rows("out", out, B, T_q, self._wo)
+        sizes = (B, T_q, T_max)
         need = self._step_bytes.get(sizes)
         if need is None:
-            need = self._step_need_put(sizes, _lib.mha_decode_quant_workspace_size(self.handle, *sizes[1:]))
+            need = self._step_need_put(sizes, _lib.mha_decode_quant_workspace_size(self.handle, *sizes))
         stream = self._quant_ready(cache, Q, out, cache_lengths, None, need)
-        _lib.mha_decode_quant(self.handle, bits, B, T_q, T_max, Q.data_ptr(), ldq, ptr, lens, out.data_ptr(), ldo,
-                              stream)
+        code = self._c_quant[2](self.handle, bits, B, T_q, T_max, Q.data_ptr(), ldq, ptr, lens, out.data_ptr(), ldo, stream)
+        if code:
+            raise _lib.MhaError("mha_decode_quant", code)
         return out
 
 
@@ -629,6 +649,7 @@ class QuantCache:
             raise ValueError(f"no cache of {B} x {T_max} tokens: sizes out of range")
         self.B, self.T_max, self.bits = B, T_max, bits
         self.heads = (layer.h_kv, layer.d_k, layer.d_v)
+        self.lens = (B,)  # shape of lengths and counts
         self.data = torch.empty(nbytes, dtype=torch.uint8, device=layer.device)
         self.device = self.data.get_device()
         self.args = (bits, B, T_max, self.data.data_ptr())  # of every C call
