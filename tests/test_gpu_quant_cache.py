@@ -396,6 +396,65 @@ def test_decode_large_scores_and_scales(dtype, d, bits):
         assert Kv.shape[-1] == d
 
 
+def _bound(q, held, h, d, bits, O, A, S, dtype):
+    """_check's bound for scores of any size: a score sums d products of q and the parts s code and m of a key, which may
+    cancel, in fp32; its weight is off by twice as much, relatively."""
+    parts = np.abs(held[1][..., 1]) + held[1][..., 0] * (2 ** bits - 1)
+    parts = np.repeat(parts, 64, -1)[..., :d]
+    per = h // parts.shape[1]
+    s = np.max(np.abs(qc.heads(q, h)) @ np.moveaxis(np.repeat(parts, per, 1), -1, -2)) / np.sqrt(d)
+    w = 2 * s * (d + 8) * 2.0 ** -23
+    return (2.0 ** -8 * np.abs(O) + 2.0 ** -11 * S if dtype == "bf16" else 0.0) + (w + 1e-5) * (A + S)
+
+
+@pytest.mark.parametrize("dtype,d,Tq", [("bf16", 64, 3), ("bf16", 128, 2), ("bf16", 64, 1), ("f32", 64, 3), ("f32", 128, 2),
+                                        ("f32", 24, 3), ("bf16", 64, 150), ("bf16", 128, 130)])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("where", ["first", "last", "spread"])
+def test_decode_values_that_matter_to_some_rows(dtype, d, Tq, bits, where):
+    """Values 2^70 times as large as the others at tokens that only the first of two heads gives any weight, and at new
+    tokens that the earlier ones do not see: the other rows' outputs are as accurate as without them."""
+    h, T = 2, 700
+    layer = _layer(dtype, h, d, 1)
+    rnd = (lambda x: wl.bf16_to_f32(wl.bf16_bits(x.astype(np.float32)))) if dtype == "bf16" else (lambda x: x.astype(np.float32))
+    Q, K, V = (wl.random_tensor((1, n, w), 80 + i, dtype) for i, (n, w) in enumerate(((Tq, h * d), (T, d), (T, d))))
+    way = np.sign(wl.random_tensor((d,), 9, "f32"))
+    Q[..., :d] = np.abs(Q[..., :d]) * way  # of the first head towards those keys, of the second one away from them
+    Q[..., d:] = -np.abs(Q[..., d:]) * way
+    at = {"first": slice(0, 3), "last": slice(T - Tq - 3, T - Tq), "spread": slice(5, T - Tq, 97)}[where]
+    K[:, at] = 60 * way
+    V[:, at] *= 2.0 ** 70
+    V[:, T - Tq + 1:] *= 2.0 ** 60
+    Q, K, V = rnd(Q), rnd(K), rnd(V)
+    cache = layer.quant_cache(1, T, bits)
+    layer.quant_write(cache, to_device(K, dtype), to_device(V, dtype), _ints([T]))
+    held = tuple(x[:, :, :T] for x in _held(cache, "K") + _held(cache, "V"))
+    got = to_host(layer.decode_quant(to_device(Q, dtype), cache, _ints([T])))
+    O, A, S = qc.decode(Q, *held, h, [T])
+    assert np.abs(O[0, 0, d:]).max() < 2 ** 10  # (the oracle: it does not see them either)
+    assert np.isfinite(got).all()
+    assert (np.abs(got - O) <= _bound(Q, held, h, d, bits, O, A, S, dtype)).all(), (np.abs(got - O) / (A + S)).max((0, 1))
+
+
+@pytest.mark.parametrize("dtype,d,Tq", [("bf16", 64, 1), ("bf16", 128, 3), ("bf16", 64, 300), ("f32", 64, 2), ("f32", 128, 1), ("f32", 20, 1)])
+def test_decode_huge_queries(dtype, d, Tq):
+    """Queries of 2^110: a row's largest score, 1e-3 or more above the next one, has all the weight."""
+    T = 400
+    layer = _layer(dtype, 1, d, 1)
+    Q = wl.random_tensor((1, Tq, d), 21, dtype) * np.float32(2.0 ** 110)
+    K, V = (wl.random_tensor((1, T, d), 22 + i, dtype) for i in range(2))
+    # the key that a row is closest to by far: its own direction, doubled
+    K[0, :Tq] = 2 * Q[0] * np.float32(2.0 ** -110)
+    cache = layer.quant_cache(1, T, 8)
+    layer.quant_write(cache, to_device(K, dtype), to_device(V, dtype), _ints([T]))
+    held = tuple(x[:, :, :T] for x in _held(cache, "K") + _held(cache, "V"))
+    x = np.sort(qc.heads(Q, 1)[0, 0].astype(np.float64) @ qc.values(*held[:2])[0, 0].T, -1)
+    assert (x[:, -1] - x[:, -2] > 1e-3 * np.abs(x).max(-1)).all()
+    got = to_host(layer.decode_quant(to_device(Q, dtype), cache, _ints([T])))
+    O, A, S = qc.decode(Q, *held, 1, [T])
+    _check(got, O, A, S, dtype, "huge queries")
+
+
 def test_decode_invalid_lengths():
     for dtype, d in (("bf16", 64), ("bf16", 128), ("f32", 64), ("f32", 24)):
         layer = _layer(dtype, 4, d, 2)

@@ -42,11 +42,12 @@ struct Divide {
 // ------------------------------------------------------------------ how a decode step is cut
 //
 // The query rows that share a cached head are taken `rb` at a time: a group is (batch, K/V head, block of rows), and
-// its visible tokens are cut into quanta of 128, or where that would only cost a join, into one.  All quanta of all groups, numbered by batch, head, block and
-// token, are dealt out evenly: CTA c of C <= N takes those from c N / C to (c + 1) N / C, whatever the lengths are.  A
-// CTA therefore has pieces of at most two groups that others share, its first and its last, and leaves records of those
-// (per row: m, l and the values, scores in base 2); groups that it has alone it finishes.  The join adds a group's
-// records in the order of its tokens.  Which CTA has what follows from the lengths and C alone.
+// its visible tokens are cut into quanta of 128, or where that would only cost a join, into one.  All quanta of all
+// groups, numbered by batch, head, block and token, are dealt out evenly: CTA c of C <= N takes those from c N / C to
+// (c + 1) N / C, whatever the lengths are.  A CTA therefore has pieces of at most two groups that others share, its first
+// and its last, and leaves records of those (per row: m, l and the values, scores in base 2); groups that it has alone it
+// finishes.  The join adds a group's records in the order of its tokens.  Which CTA has what follows from the lengths and
+// C alone.
 //
 // Steps whose groups' tokens are few for a CTA give each group a cluster of 1, 2, 4 or 8 CTAs instead, which cut its quanta
 // evenly among themselves and join their results through distributed shared memory: one launch, no records.  So do steps
@@ -77,7 +78,7 @@ struct QuantStep {
 #ifdef __CUDACC__
 
 __device__ __forceinline__ int quant_quanta(const QuantStep& s, int L) {
-    return L < s.T_q || L > s.T_max ? 0 : s.by_quantum((uint32_t)(L + s.quantum - 1));
+    return L < s.T_q || L > s.T_max ? 0 : s.by_quantum((uint32_t)(L - 1)) + 1;  // (T_q is at least 1)
 }
 
 // A lane's part of the prefix sums over the batches; N quanta in all, of which a CTA has `each` or one more.

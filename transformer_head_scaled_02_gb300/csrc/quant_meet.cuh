@@ -11,6 +11,26 @@ namespace mha {
 __device__ __forceinline__ void quant_put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void quant_put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
+__device__ __forceinline__ float quant_power2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126 .. 127
+__device__ __forceinline__ int quant_exponent(float x) { return (int)(__float_as_uint(x) >> 23 & 255u) - 127; }
+
+// A row's weights times steps, p s, are rounded to fp16 as p s vs, vs a power of two.  They fit while a step times vs is at
+// most this, as a weight is at most 2^8 (a larger one moves the row's reference); what does not, or moves it, asks for
+// the new vs where the largest p s of the tokens at hand is `need` and the row's sums so far are about to be multiplied
+// by f <= 1: to [4, 8) downwards if it is above 16, and upwards, as far as f makes room for it, if it is below 1/4.
+// (Steps differ by tokens: with [32, 64) a third of quant_rows.cu's tiles had to ask.)
+constexpr float kQuantStepMost = 255.f;
+__device__ __forceinline__ float quant_move_scale(float vs, float need, float f) {
+    const float x = need * vs;
+    if (x > 16.f || (x < 0.25f && f < 1.f)) {
+        const int now = quant_exponent(vs), most = x > 16.f ? now : max(now, min(100, now - 1 - quant_exponent(f)));
+        vs = quant_power2(max(-126, min(most, 2 - quant_exponent(need))));
+    }
+    return vs;
+}
+// to / from for two of them, times f <= 1 (which is zero where the quotient may not be finite).
+__device__ __forceinline__ float quant_rescale(float to, float from, float f) { return f * to * quant_power2(-quant_exponent(from)); }
+
 // Where row r of the block that begins at row r0 of a head's rows goes.
 template <typename T>
 __device__ __forceinline__ T* quant_out(const QuantStep& s, T* O, int64_t ldo, int b, int g, int rr) {

@@ -182,8 +182,6 @@ __device__ __forceinline__ void token_params(uint32_t addr, uint32_t (&p)[G]) {
 
 __device__ __forceinline__ float elem(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float elem(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float power2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126 .. 127
-__device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23 & 255u) - 127; }
 
 template <int BITS, int D, int TERMS, int NT, int SUB, typename T>
 __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CTAS)
@@ -286,9 +284,9 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
             for (int e = 0; e < CPL; ++e) top = fmaxf(top, fabsf(x[e]));
 #pragma unroll
             for (int w = 16; w >= 1; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-            // the largest element to [2^13, 2^14); zero, infinite and tiny rows as far as powers of two go
-            const int e2 = top > 0.f && top < INFINITY ? max(-80, min(100, 13 - exponent(top))) : 0;
-            const float f = power2(e2);
+            // the largest element to [2^13, 2^14); zero, infinite, tiny and huge (2^118) rows as far as powers of two go
+            const int e2 = top > 0.f && top < INFINITY ? max(-104, min(100, 13 - quant_exponent(top))) : 0;
+            const float f = quant_power2(e2);
             const int u = G == 1 ? 0 : lane / 16;
             float sum = 0.f;
 #pragma unroll
@@ -313,7 +311,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
 #pragma unroll
             for (int k = 0; k < SUB; ++k) {
                 if (lane % 16 == 0 && lane / 16 < G) qv[(r + k * C::ROWS) * (G + 1) + u] = sum;
-                if (lane == 0) qv[(r + k * C::ROWS) * (G + 1) + G] = scale_log2 / unit<BITS, TERMS>(0) * power2(-e2);
+                if (lane == 0) qv[(r + k * C::ROWS) * (G + 1) + G] = scale_log2 / unit<BITS, TERMS>(0) * quant_power2(-e2);
             }
         }
     }
@@ -342,12 +340,14 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
     }
 
     float o[NT][G][4][4], om[NT][G][2], m[NT][2], l[NT][2];
-    float far[NT][2];  // the y that moves the reference m: (m + 8) / rs
+    float vs[NT][2];   // p s is held as p s vs: of each column, as a token may matter to one row and not to another
+    float far[NT][2];  // the y that moves the reference m, which is a y too (a rounded score could be far from a large one)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             m[nt][e] = far[nt][e] = kNone;
+            vs[nt][e] = quant_power2(100);
             l[nt][e] = 0.f;
 #pragma unroll
             for (int u = 0; u < G; ++u) {
@@ -356,7 +356,6 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
                 for (int c = 0; c < 4; ++c) o[nt][u][c][2 * e] = o[nt][u][c][2 * e + 1] = 0.f;
             }
         }
-    float vs = power2(100);  // p s is held as p s vs
     const int block = SUB == 1 ? 0 : 2 * tig / C::ROWS;           // whose columns the lane has
     const int pa = gid ^ (gid >> 1 & 1);                          // this lane's key token, and its second at + 8: the
     const int va = 2 * tig ^ (tig & 1), vb = (2 * tig + 1) ^ (tig & 1);  // order in which neither load meets itself in a bank
@@ -439,33 +438,21 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
                 }
             }
             // references
-            float ws[2][G], vmax = 0.f;
+            float steps = 0.f;
 #pragma unroll
-            for (int u = 0; u < G; ++u) {
-                ws[0][u] = quant_step(v0[u]) * vs;
-                ws[1][u] = quant_step(v1[u]) * vs;
-                vmax = fmax3(vmax, ws[0][u], ws[1][u]);
-            }
-            bool move = vmax > 128.f;
+            for (int u = 0; u < G; ++u) steps = fmax3(steps, quant_step(v0[u]), quant_step(v1[u]));
+            bool move = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) move = move || fmaxf(y[nt][e], y[nt][e + 2]) > far[nt][e];
+                for (int e = 0; e < 2; ++e)
+                    move = move || fmaxf(y[nt][e], y[nt][e + 2]) > far[nt][e] || steps * vs[nt][e] > kQuantStepMost;
             if (__any_sync(0xffffffffu, move)) {
-                float step = 0.f, r = 1.f;
+                float step0 = 0.f, step1 = 0.f, f[NT][2], fr[NT][2], seen = 0.f;
 #pragma unroll
-                for (int u = 0; u < G; ++u) step = fmax3(step, quant_step(v0[u]), quant_step(v1[u]));
-#pragma unroll
-                for (int w = 16; w >= 4; w >>= 1) step = fmaxf(step, __shfl_xor_sync(0xffffffffu, step, w));
-                if (step * vs > 128.f) {  // to [32, 64)
-                    const float now = power2(max(-126, 5 - exponent(step)));
-                    r = now / vs;
-                    vs = now;
-#pragma unroll
-                    for (int u = 0; u < G; ++u) {
-                        ws[0][u] = quant_step(v0[u]) * vs;
-                        ws[1][u] = quant_step(v1[u]) * vs;
-                    }
+                for (int u = 0; u < G; ++u) {
+                    step0 = fmaxf(step0, quant_step(v0[u]));
+                    step1 = fmaxf(step1, quant_step(v1[u]));
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -474,24 +461,39 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
                         float top = fmaxf(y[nt][e], y[nt][e + 2]);
 #pragma unroll
                         for (int w = 16; w >= 4; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-                        float f = 1.f;
-                        const float now = top * rs[nt][e];
-                        if (now > m[nt][e]) {
-                            f = ex2_approx(m[nt][e] - now);
-                            m[nt][e] = now;
-                            far[nt][e] = top + 8.f / rs[nt][e];
+                        f[nt][e] = 1.f;
+                        if (top > m[nt][e]) {
+                            f[nt][e] = ex2_approx((m[nt][e] - top) * rs[nt][e]);
+                            m[nt][e] = top;
+                            far[nt][e] = top + __fdividef(8.f, rs[nt][e]);
                         }
-                        l[nt][e] *= f;
+                        // the column's largest p s
+                        float need = fmaxf(step0 * ex2_approx((y[nt][e] - m[nt][e]) * rs[nt][e]),
+                                           step1 * ex2_approx((y[nt][e + 2] - m[nt][e]) * rs[nt][e]));
 #pragma unroll
-                        for (int u = 0; u < G; ++u) {
-                            om[nt][u][e] *= f;
+                        for (int w = 16; w >= 4; w >>= 1) need = fmaxf(need, __shfl_xor_sync(0xffffffffu, need, w));
+                        const float to = quant_move_scale(vs[nt][e], need, f[nt][e]);
+                        fr[nt][e] = quant_rescale(to, vs[nt][e], f[nt][e]);
+                        vs[nt][e] = to;
+                        seen += l[nt][e];
+                    }
+                if (__any_sync(0xffffffffu, seen != 0.f)) {  // not at a warp's first tokens
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                o[nt][u][c][e] *= f * r;
-                                o[nt][u][c][e + 2] *= f * r;
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            l[nt][e] *= f[nt][e];
+#pragma unroll
+                            for (int u = 0; u < G; ++u) {
+                                om[nt][u][e] *= f[nt][e];
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) {
+                                    o[nt][u][c][e] *= fr[nt][e];
+                                    o[nt][u][c][e + 2] *= fr[nt][e];
+                                }
                             }
                         }
-                    }
+                }
             }
             // weights, and their products with the steps as B operands
             uint32_t bf[TERMS][NT][G][2];
@@ -499,18 +501,21 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
             for (int nt = 0; nt < NT; ++nt) {
                 float p[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) p[e] = ex2_approx(fmaf(y[nt][e], rs[nt][e & 1], -m[nt][e & 1]));
+                for (int e = 0; e < 4; ++e) p[e] = ex2_approx((y[nt][e] - m[nt][e & 1]) * rs[nt][e & 1]);
                 l[nt][0] += p[0] + p[2];
                 l[nt][1] += p[1] + p[3];
+                float pw[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) pw[e] = p[e] * vs[nt][e & 1];
 #pragma unroll
                 for (int u = 0; u < G; ++u) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t par = h == 0 ? v0[u] : v1[u];
-                        const float z = quant_lowest(par), w = ws[h][u];
+                        const float z = quant_lowest(par), w = quant_step(par);
                         om[nt][u][0] = fmaf(p[2 * h], z, om[nt][u][0]);
                         om[nt][u][1] = fmaf(p[2 * h + 1], z, om[nt][u][1]);
-                        const float w0 = p[2 * h] * w, w1 = p[2 * h + 1] * w;
+                        const float w0 = pw[2 * h] * w, w1 = pw[2 * h + 1] * w;
                         const uint32_t hi = half2_bits(w0, w1);
                         bf[0][nt][u][h] = transpose8(hi);
                         if constexpr (TERMS == 2) {
@@ -563,11 +568,11 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
 
     // this warp's result: rows of D values, m, l
     float* own = reinterpret_cast<float*>(smem + C::RES) + warp * C::COLS * C::REC;
-    const float inv = 1.f / vs;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+            const float inv = 1.f / vs[nt][e];
 #pragma unroll
             for (int w = 4; w <= 16; w <<= 1) {
                 l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], w);
@@ -582,7 +587,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
                     *reinterpret_cast<float2*>(row + u * kQuantGroup + 8 * gid + 2 * c) =
                         make_float2(fmaf(o[nt][u][c][e], inv / unit<BITS, TERMS>(0), om[nt][u][e]),
                                     fmaf(o[nt][u][c][e + 2], inv / unit<BITS, TERMS>(1), om[nt][u][e]));
-            if (gid == 0) *reinterpret_cast<float2*>(row + D) = make_float2(m[nt][e], l[nt][e]);
+            if (gid == 0) *reinterpret_cast<float2*>(row + D) = make_float2(m[nt][e] == kNone ? kNone : m[nt][e] * rs[nt][e], l[nt][e]);
         }
     __syncthreads();
     // (a cluster's CTA, which has one piece, is through with its ring)

@@ -73,9 +73,6 @@ __host__ __device__ constexpr float unit_of(int p) {
     return BITS == 4 && (p >> 1 & 1) ? 16.f * 5.9604644775390625e-8f : 5.9604644775390625e-8f;
 }
 
-__device__ __forceinline__ float power_of_2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126 .. 127
-__device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23 & 255u) - 127; }
-
 // 16 columns of tensor memory.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
@@ -185,9 +182,9 @@ __global__ void __launch_bounds__(QR_THREADS, 1)
                 const unsigned lanes = 0xffu << (lane & 24);
 #pragma unroll
                 for (int o = 4; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(lanes, top, o));
-                // the largest element to [2^13, 2^14); zero, infinite and tiny rows as far as powers of two go
-                const int e2 = top > 0.f && top < INFINITY ? max(-80, min(100, 13 - exponent_of(top))) : 0;
-                const float f = power_of_2(e2);
+                // the largest element to [2^13, 2^14); zero, infinite, tiny and huge (2^118) rows as far as powers of two go
+                const int e2 = top > 0.f && top < INFINITY ? max(-104, min(100, 13 - quant_exponent(top))) : 0;
+                const float f = quant_power2(e2);
                 float sum[G];
 #pragma unroll
                 for (int u = 0; u < G; ++u) {
@@ -215,7 +212,7 @@ __global__ void __launch_bounds__(QR_THREADS, 1)
                     float* qv = reinterpret_cast<float*>(sm + C::QS) + r * (G + 1);
 #pragma unroll
                     for (int u = 0; u < G; ++u) qv[u] = sum[u] * unit_of<BITS>(0);
-                    qv[G] = scale_log2 / unit_of<BITS>(0) * power_of_2(-e2);
+                    qv[G] = scale_log2 / unit_of<BITS>(0) * quant_power2(-e2);
                 }
             }
             fence_proxy_async_smem();
@@ -335,7 +332,7 @@ __global__ void __launch_bounds__(QR_THREADS, 1)
                 ++meets;
                 return fine;
             };
-            float qs[G], om[G], m = kRowsNone, l = 0.f, vs = power_of_2(100);
+            float qs[G], om[G], m = kRowsNone, l = 0.f, vs = quant_power2(100);
 #pragma unroll
             for (int u = 0; u < G; ++u) qs[u] = qv[u], om[u] = 0.f;
             const float rs = qv[G];
@@ -376,7 +373,7 @@ __global__ void __launch_bounds__(QR_THREADS, 1)
                 tc_fence_before();
                 mbar_arrive(s_free);
                 ok = __all_sync(0xffffffffu, mbar_wait(v_full + 8u * st, ph, abort_flag, status));  // steps of the values
-                // The reference moves when a score exceeds it by 2^8; p s is held as p s vs, against a power of two.
+                // The reference moves when a score exceeds it by 2^8; p s is held as p s vs (quant_meet.cuh).
                 float alpha = 1.f, back = 1.f;
                 bool moved = false;
                 if (!idle) {  // (both warps of a row are, or neither)
@@ -390,12 +387,24 @@ __global__ void __launch_bounds__(QR_THREADS, 1)
                         moved = true;
                     }
                     const float4 w = *reinterpret_cast<const float4*>(sm + C::TOP + (n % QR_PARAMS) * 16);
-                    const float step = fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w));
-                    if (step * vs > 128.f) {  // to [32, 64)
-                        const float now = power_of_2(max(-126, 5 - exponent_of(step)));
-                        back = now / vs;
-                        vs = now;
-                        moved = true;
+                    moved = moved || fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w)) * vs > kQuantStepMost;
+                    if (__any_sync(0xffffffffu, moved)) {  // (so says the row's other warp)
+                        const uint32_t par = base + C::VP + (uint32_t)(((n % QR_PARAMS) * 128 + c0) * 16);
+                        float need = 0.f;
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) {
+                            float s0, s1 = 0.f;  // (in order: 64 loads ahead would take the registers of y)
+                            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s0) : "r"(par + 16u * c) : "memory");
+                            if constexpr (G > 1) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s1) : "r"(par + 16u * c + 8u) : "memory");
+                            need = fmaxf(need, ex2_approx(y[c] - m) * fmaxf(s0, s1));
+                        }
+                        mine += 4 * QR_ROWS;
+                        mine[half * QR_ROWS + r] = need;
+                        if (!meet()) break;
+                        need = fmaxf(need, mine[(1 - half) * QR_ROWS + r]);
+                        const float to = quant_move_scale(vs, need, alpha);
+                        back = quant_rescale(to, vs, alpha);
+                        vs = to;
                     }
                 }
                 if (!ok) break;
@@ -406,15 +415,14 @@ __global__ void __launch_bounds__(QR_THREADS, 1)
                 tc_fence_after();
                 if (!idle) {
                     if (i > 0 && __any_sync(0xffffffffu, moved)) {  // each of the two warps half of the columns
-                        const float a = alpha * back;
-#pragma unroll
+                        #pragma unroll
                         for (int c = 0; c < D / 64; ++c) {
                             uint32_t o[32];
                             tmem_ld32(trow + C::O_COL + half * (D / 2) + 32 * c, o);
                             tmem_wait_ld();
                             reg_fence(o);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * back);
                             tmem_st32(trow + C::O_COL + half * (D / 2) + 32 * c, o);
                         }
                     }
