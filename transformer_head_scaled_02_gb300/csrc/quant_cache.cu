@@ -12,6 +12,10 @@
 // A warp takes a run of tokens of one head's keys or values: 8 lanes a group, 8 channels a lane (16 bytes of bf16, 4
 // or 8 of codes), so codes move in whole pieces and keys in rows of a head; all loads first.  Neighbouring warps have
 // neighbouring heads.
+//
+// Measured, 4 bits, heads of 128, bf16.  Reading back 32 x 8192 tokens of 4 heads: 78.3 us, 99 % of the rate of a plain
+// copy.  Writing 8 x 8192 of 16 heads: 153 us, 671 MB at 4.4 TB/s: bound by instructions (126 for eight channels,
+// issued in 70 % of all cycles), most of them the exact quotients and the packing; reading those back takes 104 us.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -317,7 +321,7 @@ __device__ __forceinline__ void eight_codes(const E& in, int n, float m, float s
 
 // The group's eight lanes share the work on its scale: the ranges of their RUN items meet by halving, after which a
 // lane has one item's range of the group, computes that item's scale and hands it out.  (With every lane computing
-// every scale an item took 171 instructions instead of about 100, and a long write 240 us instead of 150.)
+// every scale an item took 171 instructions instead of 126, and a long write 242 us instead of 153.)
 template <typename T, int BITS, bool VEC, int RUN>
 __global__ void __launch_bounds__(QC_THREADS, 4)  // (24 warps an SM instead of 32: 164 us of the long write, not 153)
     quant_write_kernel(const QuantCopy a, const T* __restrict__ K, const T* __restrict__ V) {

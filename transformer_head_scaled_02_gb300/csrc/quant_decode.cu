@@ -1,12 +1,15 @@
-// quant_decode.cu -- a decode step over a quantised cache (quant.cuh) on CUDA cores, for any head size.
+// quant_decode.cu -- a decode step over a quantised cache (quant.cuh): which kernel takes it and how it is cut, the join
+// of what several CTAs leave of a group, and the kernel for the head sizes that the tensor-core ones do not have.
 //
-// With codes c, steps s and lowest values m per group G of channels, and the query row q (log2(e)/sqrt(d) folded in):
+// Heads of 64 and 128 channels go to quant_mma.cu, bf16 steps of hundreds of query rows to quant_rows.cu; what is left
+// are fp32 layers of other head sizes, on CUDA cores.  With codes c, steps s and lowest values m per group G of channels,
+// and the query row q (log2(e)/sqrt(d) folded in):
 //   score_j = sum_G s_jG (sum_c q_c code_jc) + m_jG (sum_c q_c)          the codes are never turned into values
 //   o       = sum_j p_j (s_jG code_jc + m_jG),  p_j = 2^(score_j - M)
 // in fp32 throughout.  A CTA takes a part of one head's cached tokens for up to R query rows; its warps take 32
 // tokens at a time in turn, a lane per token for the scores and a lane per eight channels for the values, each with
-// its own running maximum, sum and values, joined at the end.  Parts leave records (maximum, sum, values), which the
-// join adds in order.
+// its own running maximum, sum and values, joined at the end.  It is bound by its two multiply-adds and one conversion
+// per code and row.
 #include <math.h>
 
 #include "internal.h"
@@ -171,7 +174,7 @@ __global__ void __launch_bounds__(QD_THREADS)
     }
 }
 
-// The join.  A block has `run` rows of a group; its threads take (row, slice of the records, column), `width` columns and
+// The join, 2 to 4 us behind the kernel before it, mostly the two round trips.  A block has `run` rows of a group; its threads take (row, slice of the records, column), `width` columns and
 // `slices` slices.  A slice's maxima, sums and values are loaded together, so that a row costs about one round trip to L2
 // and one more for every eight records of a slice; slices meet in shared memory.
 template <typename T>
@@ -273,22 +276,22 @@ size_t qd_smem(const QuantPlane& pk, const QuantPlane& pv) {
 }  // namespace
 
 // When a step's groups each get a cluster (us, cluster | even cut and join): 16 sequences of 1500 tokens, 16 K/V heads of
-// 64, 12 quanta a CTA 10.1 | 16.1; 8 of 2048, 16 of 128, 8 quanta 13.7 | 17.4; 32 of 8192, 4 of 128, 32 quanta 37.6 | 35.5.
+// 64, 12 quanta a CTA 10.4 | 16.9; 8 of 2048, 16 of 128, 8 quanta 14.9 | 19.8; 32 of 8192, 4 of 128, 32 quanta 37.6 | 35.5.
 // All clusters have to run at a time: a second wave costs 5 to 6 us, a CTA's latency from its lengths to its outputs.  One
 // sequence is cut into more clusters a group from 6 quanta a CTA on: 16384 tokens, 4 heads, 16 quanta in one cluster
-// 15.9, several 11.0; 131072 tokens, 2 heads, 8 bits: even cut 25.9, clusters on all SMs 37 (they do not all fit), on 85 %
-// of them 23.3.
+// 15.9, several 10.2, even cut 13.4; 131072 tokens, 2 heads, 8 bits: even cut 25.9, clusters on all SMs 37 (they do not all
+// fit), on 85 % of them 23.8.
 constexpr int kClusterQuanta = 16;
 constexpr int kClusterQuantaOne = 6;
 constexpr int kClusterQuantaWide = 6;  // of CTAs that an SM holds one of: 8 of 8192, one head of 128, 32 rows, 8 quanta 24.4 | 18.4
 
 // With more groups than CTAs: the quanta that a CTA may have more than others, where groups are not cut at all, for the
-// join and the shared groups' ends that this saves.  32 sequences of 300 tokens, 16 heads of 128, 8 bits: kQWhole us.
+// join and the shared groups' ends that this saves (32 sequences of 300 tokens, 16 heads of 128, 8 bits: 18.7 | 22.2 us).
 constexpr int kJoinQuanta = 6;
 
 // bf16 steps of at least this many rows of a cached head go to quant_rows.cu, in blocks of 128 (us, there | quant_mma.cu:
-// 2048 rows, one sequence of 8192 tokens, 4 heads of 128, 4 bits 109 | 160; 512 rows, 4 of 4096, 4 of 64 48 | 58; 128
-// rows, 8 of 8192, one of 128 42 | 31: its records are large).
+// 2048 rows, one sequence of 8192 tokens, 4 heads of 128, 4 bits 116 | 168; 512 rows, 4 of 4096, 4 of 64 50 | 63; 128
+// rows, 8 of 8192, one of 128 42 | 33: its records are large).
 constexpr int kManyRows = 256;
 constexpr int kManyRowsBlock = 128;
 constexpr int kManyRowsCtas = 320;  // most of its CTAs: one an SM

@@ -12,18 +12,27 @@
 //
 // The cached tokens are the M side of both products (16 at a time) and the query rows the N side (8 or 16 columns), so
 // a few rows waste no tensor work and the exponentials spread over all lanes.  Up to 4 rows leave half of the columns:
-// every other block of 16 tokens takes those, as rows of their own until the end, and two blocks share one softmax.  Which channel or token is which k of a
-// product is free as long as both operands agree: it is chosen so that one mask takes two elements out of a word.
+// every other block of 16 tokens takes those, as rows of their own until the end, and two blocks share one softmax.
+// Which channel or token is which k of a product is free as long as both operands agree: it is chosen so that one mask
+// takes two elements out of a word.
 //   scores:  A = keys [token][channel], lane (gid, tig) holds 16 channels of a group of tokens gid and gid + 8
 //   values:  A = values transposed [channel][token], the words of two tokens interleaved by a byte permutation;
 //            B = p s, which the scores' layout becomes by transposing 8 x 8 pieces (movmatrix)
-// mma.sync feeds operands from registers, where the unpacked codes are; tcgen05 would take them through shared
-// memory, written and read once more per element.
+// mma.sync feeds operands from registers, where the unpacked codes are; tcgen05 would take them through shared memory:
+// 64 KB of fp16 keys and values for 128 tokens of 128 channels, written and read once more, about 1000 cycles at 128
+// bytes a cycle, where an SM's share of HBM's rate brings their 4-bit codes in 870.
 //
 // Stages of tokens come by bulk copies (a head's codes lie in one piece) into a ring; each warp takes a run of a
 // stage's 16-token blocks with its own maximum, sum and values, and the last warp to finish a stage asks for the next
-// one in its place.  (A ring per warp cost 200 instructions per stage and warp instead of some 30.)  Warps meet at the
-// end of a piece.  The reference maximum moves only when a score exceeds it by 2^8, which one vote per block finds.
+// one in its place.  (A ring per warp cost 200 instructions per stage and warp instead of some 30; with stages of half
+// the size the first step below took 123 us instead of 99.)  Warps meet at the end of a piece.  The reference maximum
+// moves only when a score exceeds it by 2^8, which one vote per block finds.
+//
+// Measured, bf16 layers, 4 bits, heads of 128, 32 ragged sequences of up to 8192 tokens: 16 heads with one query row each
+// 95 us, 453 MB at 4.8 TB/s (copies alone take 72 us, the arithmetic alone 81: 260 instructions for 16 tokens and a
+// head, of which half the cycles issue one, with 16 warps an SM, which is all that the registers hold); 4 heads with 4
+// rows each 35.5 us, of which the join 4 and starts and ends of pieces 12.  One sequence of 4096 tokens, 4 heads of 64:
+// 6.1 us, latency.
 #include <cuda_fp16.h>
 #include <math.h>
 

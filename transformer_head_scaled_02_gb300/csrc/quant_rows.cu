@@ -15,6 +15,9 @@
 // a row, which halve its tokens and agree on its maximum through shared memory (with one thread a row its 128 scores did
 // not fit the registers, and the softmax, some 20 instructions a score, is what bounds a tile).  Warp 12: products.
 // Tiles are quanta of 128 tokens; pieces follow one another with a barrier between.
+//
+// Measured, 4 bits: 512 new tokens of one sequence of 8192, 16 query heads over 4 of 128: 116 us (quant_mma.cu 168); 128
+// new tokens of each of 4 ragged sequences of up to 4096, 16 heads over 4 of 64: 50 us (63).
 #include <cuda_fp16.h>
 #include <math.h>
 
