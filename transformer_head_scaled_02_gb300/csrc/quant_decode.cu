@@ -41,6 +41,46 @@ __device__ __forceinline__ void codes8(const uint8_t* p, float (&x)[8]) {
     }
 }
 
+// The warps' results of a piece meet, as quant_meet() of quant_meet.cuh has it for known sizes: [warp][row] of `stride`
+// floats, dv values, at ml m and l.
+template <typename T>
+__device__ __forceinline__ void meet_any(const QuantStep& s, bool whole, float* rec, float* res, int stride, int ml, int b, int g,
+                                         int r0, int nr, T* O, int64_t ldo) {
+    constexpr int ENTRIES = QD_WARPS, THREADS = QD_THREADS, rows = QD_ROWS;
+    const int tid = (int)threadIdx.x, dv = s.dv, record = dv + 2;
+    for (int r = tid / ENTRIES; r < nr; r += THREADS / ENTRIES) {
+        float* a = res + ((tid % ENTRIES) * rows + r) * stride + ml;
+        const unsigned lanes = ((1u << ENTRIES) - 1) << (tid & 31 & ~(ENTRIES - 1));
+        const float m = a[0];
+        float M = m;
+#pragma unroll
+        for (int w = ENTRIES / 2; w >= 1; w >>= 1) M = fmaxf(M, __shfl_xor_sync(lanes, M, w));
+        const float f = m == -INFINITY ? 0.f : exp2f(m - M);
+        float l = f * a[1];
+#pragma unroll
+        for (int w = ENTRIES / 2; w >= 1; w >>= 1) l += __shfl_xor_sync(lanes, l, w);
+        if (whole) {
+            a[0] = f / l;  // (l is NaN, or above zero: a whole group has a visible token for every row)
+        } else {
+            a[0] = f;
+            if (tid % ENTRIES == 0) {
+                rec[r * record] = M;
+                rec[r * record + 1] = l;
+            }
+        }
+    }
+    __syncthreads();
+    for (int e = tid; e < nr * dv; e += THREADS) {
+        const int r = e / dv, c = e - r * dv;
+        const float* a = res + r * stride;
+        float x = 0.f;
+#pragma unroll
+        for (int w = 0; w < ENTRIES; ++w) x = fmaf(a[w * rows * stride + ml], a[w * rows * stride + c], x);
+        if (whole) quant_put(quant_out(s, O, ldo, b, g, r0 + r) + c, x);
+        else rec[r * record + 2 + c] = x;
+    }
+}
+
 // dynamic shared memory: q[R][dpk], its sums qs[R][groups], and per warp p[R][32] or at the end m, l, o[dpv] per row
 template <typename T, int BITS>
 __global__ void __launch_bounds__(QD_THREADS)
@@ -169,8 +209,7 @@ __global__ void __launch_bounds__(QD_THREADS)
                 for (int e = 0; e < 8; ++e) to[c0 + e] = o[r][e];
         }
         __syncthreads();
-        quant_meet<QD_WARPS, QD_THREADS, 0>(s, z.whole(), part + s.slot((int)blockIdx.x, z.q0 == 0 ? 1 : 0, 0), all, R, dpv + 32, dpv, b, g,
-                                         r0, nr, O, ldo);
+        meet_any(s, z.whole(), part + s.slot((int)blockIdx.x, z.q0 == 0 ? 1 : 0, 0), all, dpv + 32, dpv, b, g, r0, nr, O, ldo);
     }
 }
 

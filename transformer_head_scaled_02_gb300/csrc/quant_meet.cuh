@@ -51,44 +51,75 @@ __device__ __noinline__ void quant_invalid(const QuantStep& s, int b, int step, 
     }
 }
 
-// A piece's ENTRIES results for each of `rows` rows (the warps', or several of a warp), [entry][row] of `stride` floats:
-// dv values, then at ml m and l.  Either they are finished (whole), or they become records at rec.  All threads, behind a
-// barrier; an entry's m becomes its factor.  DV: dv if it is known.
-template <int ENTRIES, int THREADS, int DV, typename T>
-__device__ __forceinline__ void quant_meet(const QuantStep& s, bool whole, float* rec, float* res, int rows, int stride, int ml,
+__device__ __forceinline__ void quant_put4(float* p, float4 x) {  // (fp32 rows may begin anywhere)
+    p[0] = x.x, p[1] = x.y, p[2] = x.z, p[3] = x.w;
+}
+__device__ __forceinline__ void quant_put4(__nv_bfloat16* p, float4 x) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+}
+
+// Where a cluster's CTAs put their records of a group: each CTA finishes dv / 2^shift columns of all rows, and has the
+// others' values of those, [CTA][row][column], and after them every CTA's (m, l), [CTA][row].  DV: dv.
+template <int ROWS, int DV>
+struct QuantShare {
+    static constexpr int BYTES = ROWS * DV * 4 + kQuantCluster * ROWS * 8;
+    uint32_t base;  // shared memory, the same in every CTA
+    int cluster, rank;
+    __device__ __forceinline__ int cols() const { return DV / cluster; }
+    __device__ __forceinline__ uint32_t value(int cta, int row, int col) const { return base + (uint32_t)(((cta * ROWS + row) * cols() + col) * 4); }
+    __device__ __forceinline__ uint32_t sums(int cta, int row) const { return base + (uint32_t)(ROWS * DV * 4 + (cta * ROWS + row) * 8); }
+};
+
+// A piece's ENTRIES results for each of ROWS rows (the warps', or several of a warp), [entry][row] of DV + 4 floats: DV
+// values, m, l and two unused.  Either they are finished (whole), or they become records at rec, or (rec null) go to the
+// cluster's CTAs.  All threads, behind a barrier; an entry's m becomes its factor.
+template <int ENTRIES, int THREADS, int DV, int ROWS, typename T>
+__device__ __forceinline__ void quant_meet(const QuantStep& s, bool whole, float* rec, const QuantShare<ROWS, DV>& share, float* res,
                                            int b, int g, int r0, int nr, T* O, int64_t ldo) {
-    const int tid = (int)threadIdx.x, dv = DV > 0 ? DV : s.dv, record = dv + 2;
+    constexpr int STRIDE = DV + 4, RECORD = DV + 2;
+    const int tid = (int)threadIdx.x;
     // ENTRIES lanes a row: maximum and sum
     for (int r = tid / ENTRIES; r < nr; r += THREADS / ENTRIES) {
-        float* a = res + ((tid % ENTRIES) * rows + r) * stride + ml;
+        float* a = res + ((tid % ENTRIES) * ROWS + r) * STRIDE + DV;
         const unsigned lanes = ((1u << ENTRIES) - 1) << (tid & 31 & ~(ENTRIES - 1));
         const float m = a[0];
         float M = m;
 #pragma unroll
         for (int w = ENTRIES / 2; w >= 1; w >>= 1) M = fmaxf(M, __shfl_xor_sync(lanes, M, w));
-        const float f = m == -INFINITY ? 0.f : exp2f(m - M);
+        const float f = exp2f(m - M);
         float l = f * a[1];
 #pragma unroll
         for (int w = ENTRIES / 2; w >= 1; w >>= 1) l += __shfl_xor_sync(lanes, l, w);
-        if (whole) {
-            a[0] = f / l;  // (l is NaN, or above zero: a whole group has a visible token for every row)
-        } else {
-            a[0] = f;
-            if (tid % ENTRIES == 0) {
-                rec[r * record] = M;
-                rec[r * record + 1] = l;
+        a[0] = whole ? f / l : f;  // (l is NaN, or above zero: a whole group has a visible token for every row)
+        if (!whole) {
+            const int i = tid % ENTRIES;
+            if (rec != nullptr) {
+                if (i == 0) *reinterpret_cast<float2*>(rec + r * RECORD) = make_float2(M, l);
+            } else if (i < share.cluster) {
+                st_shared_cluster_v2(mapa_shared(share.sums(share.rank, r), (uint32_t)i), M, l);
             }
         }
     }
     __syncthreads();
-    for (int e = tid; e < nr * dv; e += THREADS) {
-        const int r = e / dv, c = e - r * dv;
-        const float* a = res + r * stride;
-        float x = 0.f;
+    for (int e = tid; e < nr * (DV / 4); e += THREADS) {
+        const int r = e / (DV / 4), c = 4 * (e % (DV / 4));
+        const float* a = res + r * STRIDE;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < ENTRIES; ++w) x = fmaf(a[w * rows * stride + ml], a[w * rows * stride + c], x);
-        if (whole) quant_put(quant_out(s, O, ldo, b, g, r0 + r) + c, x);
-        else rec[r * record + 2 + c] = x;
+        for (int w = 0; w < ENTRIES; ++w) {
+            const float f = a[w * ROWS * STRIDE + DV];
+            const float4 v = *reinterpret_cast<const float4*>(a + w * ROWS * STRIDE + c);
+            x = make_float4(fmaf(f, v.x, x.x), fmaf(f, v.y, x.y), fmaf(f, v.z, x.z), fmaf(f, v.w, x.w));
+        }
+        if (whole) {
+            quant_put4(quant_out(s, O, ldo, b, g, r0 + r) + c, x);
+        } else if (rec != nullptr) {
+            *reinterpret_cast<float2*>(rec + r * RECORD + 2 + c) = make_float2(x.x, x.y);
+            *reinterpret_cast<float2*>(rec + r * RECORD + 4 + c) = make_float2(x.z, x.w);
+        } else {
+            const int to = c / share.cols();
+            st_shared_cluster_v4(mapa_shared(share.value(share.rank, r, c - to * share.cols()), (uint32_t)to), x);
+        }
     }
 }
 

@@ -64,10 +64,15 @@ struct QmCfg {
     static constexpr int RES = STAGES * STAGE;                // the warps' results
     static constexpr int QF = RES + QM_WARPS * COLS * REC * 4;  // queries as operands, their sums and scales
     static constexpr int QS = QF + TERMS * NT * G * 32 * 32;
-    static constexpr int BARS = QS + COLS * (G + 1) * 4;
-    static constexpr int SMEM = BARS + 16 * STAGES + 48;      // barriers, counts of the warps done, QmNext, abort flag
+    static constexpr int QEND = QS + COLS * (G + 1) * 4;
+    using Share = QuantShare<ROWS, D>;                        // of a cluster: a place of its own, or if that does not fit the
+    static constexpr int TAIL = 16 * STAGES + 48;             // one of the queries
+    static constexpr bool ROOM = CTAS * (QEND + Share::BYTES + TAIL + 1024) <= 228 * 1024;
+    static constexpr int SHARE = ROOM ? QEND : QF;
+    static constexpr int BARS = SHARE + Share::BYTES > QEND ? SHARE + Share::BYTES : QEND;
+    static constexpr int SMEM = BARS + TAIL;                  // barriers, counts of the warps done, QmNext, abort flag
     static_assert(SUB == 1 || NT == 1, "only a few rows leave columns for a second block");
-    static_assert(BARS % 16 == 0 && SMEM <= 232448, "");
+    static_assert(BARS % 16 == 0 && SHARE % 16 == 0 && SMEM <= 232448, "");
     static_assert(TOK % kQuantum == 0, "a stage's tokens are dealt out evenly");
     static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory of an SM");
 };
@@ -224,8 +229,10 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
         own = quant_cluster_piece(s, lengths);
         begin = own.q0;
         end = own.q1;
+        if (C::ROOM && s.cluster > 1) cluster_arrive_relaxed();  // this CTA's shared memory may be written
         if (own.nq == 0) {
             if (blockIdx.x % (unsigned)(s.cluster * s.parts * s.lanes()) == 0) quant_invalid<QM_THREADS>(s, own.b, s.B, lengths, O, ldo, status);
+            if (C::ROOM && s.cluster > 1) cluster_wait();
             return;
         }
     } else {
@@ -235,7 +242,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
         if (plan.bad) quant_invalid<QM_THREADS>(s, (int)blockIdx.x, (int)gridDim.x, lengths, O, ldo, status);
     }
     auto piece = [&](int q) { return s.cluster ? own : quant_piece(s, lengths, plan, q, end); };
-    // One warp at a time asks for the next stage (all its lanes call this): at first warp 0, then whichever is the last
+    // One warp at a time asks for the next stage (all its lanes call this): at first the last warp, then whichever is the last
     // to have used the stage whose place it takes.
     auto fetch = [&](QmNext& x) {
         while (x.from >= x.to) {
@@ -260,7 +267,8 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
         x.from += C::TOK;
         ++x.issued;
     };
-    if (warp == 0) {
+    auto share = [&] { return typename C::Share{ring + C::SHARE, s.cluster, s.cluster > 1 ? (int)cluster_ctarank() : 0}; };
+    if (warp == QM_WARPS - 1) {  // (the first warps have queries to see to)
         QmNext x{0, begin, 0, 0, 0};
 #pragma unroll 1
         for (int n = 0; n < C::STAGES; ++n) fetch(x);
@@ -282,7 +290,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
         constexpr int CPL = D / 32;  // channels of a lane
         __half* qh = reinterpret_cast<__half*>(smem + C::QF);
         float* qv = reinterpret_cast<float*>(smem + C::QS);
-#pragma unroll 1
+#pragma unroll
         for (int r = warp; r < C::ROWS; r += QM_WARPS) {
             const int rr = r0 + min(r, nr - 1), hg = s.by_T_q((uint32_t)rr), t = rr - hg * s.T_q;
             const T* src = Q + ((int64_t)b * s.T_q + t) * ldq + (int64_t)(g * s.per + hg) * D + lane * CPL;
@@ -347,6 +355,8 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
             rs[nt][e] = from[G];
         }
     }
+
+    if (!C::ROOM && s.cluster > 1) cluster_arrive();  // the queries' place may be written
 
     float o[NT][G][4][4], om[NT][G][2], m[NT][2], l[NT][2];
     float vs[NT][2];   // p s is held as p s vs: of each column, as a token may matter to one row and not to another
@@ -598,28 +608,37 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
                                     fmaf(o[nt][u][c][e + 2], inv / unit<BITS, TERMS>(1), om[nt][u][e]));
             if (gid == 0) *reinterpret_cast<float2*>(row + D) = make_float2(m[nt][e] == kNone ? kNone : m[nt][e] * rs[nt][e], l[nt][e]);
         }
+    if (s.cluster > 1) cluster_wait();
     __syncthreads();
-    // (a cluster's CTA, which has one piece, is through with its ring)
     const bool whole = s.cluster ? s.cluster * s.parts == 1 : z.whole();
-    float* rec = s.cluster > 1 ? reinterpret_cast<float*>(smem) : part + s.slot((int)blockIdx.x, z.q0 == 0 ? 1 : 0, 0);
-    quant_meet<QM_WARPS * SUB, QM_THREADS, D>(s, whole, rec, reinterpret_cast<float*>(smem + C::RES), C::ROWS, C::REC,
-                                           D, b, g, r0, nr, O, ldo);
+    float* rec = s.cluster > 1 ? nullptr : part + s.slot((int)blockIdx.x, z.q0 == 0 ? 1 : 0, 0);
+    quant_meet<QM_WARPS * SUB, QM_THREADS, D, C::ROWS>(s, whole, rec, share(), reinterpret_cast<float*>(smem + C::RES), b, g, r0, nr, O, ldo);
     __syncthreads();
     }
-    if (s.cluster > 1) {  // the CTAs' records meet, a share of the outputs in each
+    if (s.cluster > 1) {  // the CTAs' records have met, a share of the columns in each
         const int g = s.by_nrb((uint32_t)own.lane), r0 = (own.lane - g * s.nrb) * C::ROWS, nr = min(C::ROWS, s.rows - r0);
-        if (begin == end)  // had nothing
-            for (int r = tid; r < nr; r += QM_THREADS) reinterpret_cast<float*>(smem)[r * (D + 2)] = kNone;
+        const typename C::Share to = share();
+        if (begin == end) {  // had nothing
+            if (!C::ROOM) cluster_arrive();
+            cluster_wait();
+            for (int i = tid; i < nr * s.cluster; i += QM_THREADS) {
+                const int r = i / s.cluster;
+                st_shared_cluster_v2(mapa_shared(to.sums(to.rank, r), (uint32_t)(i - r * s.cluster)), kNone, 0.f);
+            }
+        }
         cluster_sync_all();
-        for (int e = (int)cluster_ctarank() * QM_THREADS + tid; e < nr * D; e += s.cluster * QM_THREADS) {
-            const int r = e / D, c = e % D;
+        const int cols = to.cols();
+        const uint8_t* mine = smem + C::SHARE;
+        for (int e = tid; e < nr * cols; e += QM_THREADS) {
+            const int r = e / cols, c = e - r * cols;
             float m[kQuantCluster], l[kQuantCluster], v[kQuantCluster], M = kNone, sum = 0.f, x = 0.f;
 #pragma unroll
             for (int k = 0; k < kQuantCluster; ++k) {
-                const uint32_t at = mapa_shared(ring, (uint32_t)min(k, s.cluster - 1)) + (uint32_t)(r * (D + 2) * 4);
-                m[k] = k < s.cluster ? ld_shared_cluster(at) : kNone;
-                l[k] = ld_shared_cluster(at + 4);
-                v[k] = ld_shared_cluster(at + 8 + 4 * c);
+                const int from = min(k, s.cluster - 1);
+                const float2 ml = *reinterpret_cast<const float2*>(mine + (to.sums(from, r) - to.base));
+                m[k] = k < s.cluster ? ml.x : kNone;
+                l[k] = ml.y;
+                v[k] = *reinterpret_cast<const float*>(mine + (to.value(from, r, c) - to.base));
                 M = fmaxf(M, m[k]);
             }
 #pragma unroll
@@ -630,14 +649,13 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
                     x = fmaf(f, v[k], x);
                 }
             if (s.parts == 1) {
-                quant_put(quant_out(s, O, ldo, own.b, g, r0 + r) + c, x / sum);
+                quant_put(quant_out(s, O, ldo, own.b, g, r0 + r) + to.rank * cols + c, x / sum);
             } else {
-                float* to = part + ((int64_t)((int)blockIdx.x / s.cluster) * C::ROWS + r) * s.record();
-                to[2 + c] = x;
-                if (c == 0) to[0] = M, to[1] = sum;
+                float* rec = part + ((int64_t)((int)blockIdx.x / s.cluster) * C::ROWS + r) * s.record();
+                rec[2 + to.rank * cols + c] = x;
+                if (to.rank == 0 && c == 0) rec[0] = M, rec[1] = sum;
             }
         }
-        cluster_sync_all();  // no CTA leaves while its record is read
     }
     if (*abort_flag && tid == 0)  // a copy did not arrive: wait for those in flight, and leave
         for (int k = max(0, next->issued - C::STAGES); k < next->issued; ++k)
