@@ -315,11 +315,11 @@ size_t qd_smem(const QuantPlane& pk, const QuantPlane& pv) {
 }  // namespace
 
 // When a step's groups each get a cluster (us, cluster | even cut and join): 16 sequences of 1500 tokens, 16 K/V heads of
-// 64, 12 quanta a CTA 10.4 | 16.9; 8 of 2048, 16 of 128, 8 quanta 14.9 | 19.8; 32 of 8192, 4 of 128, 32 quanta 37.6 | 35.5.
+// 64, 12 quanta a CTA 10.4 | 16.9; 8 of 2048, 16 of 128, 8 quanta 14.4 | 19.8; 32 of 8192, 4 of 128, 32 quanta 37.6 | 35.5.
 // All clusters have to run at a time: a second wave costs 5 to 6 us, a CTA's latency from its lengths to its outputs.  One
 // sequence is cut into more clusters a group from 6 quanta a CTA on: 16384 tokens, 4 heads, 16 quanta in one cluster
 // 15.9, several 10.2, even cut 13.4; 131072 tokens, 2 heads, 8 bits: even cut 25.9, clusters on all SMs 37 (they do not all
-// fit), on 85 % of them 23.8.
+// fit), on 85 % of them 22.7.
 constexpr int kClusterQuanta = 16;
 constexpr int kClusterQuantaOne = 6;
 constexpr int kClusterQuantaWide = 6;  // of CTAs that an SM holds one of: 8 of 8192, one head of 128, 32 rows, 8 quanta 24.4 | 18.4

@@ -30,9 +30,9 @@
 //
 // Measured, bf16 layers, 4 bits, heads of 128, 32 ragged sequences of up to 8192 tokens: 16 heads with one query row each
 // 95 us, 453 MB at 4.8 TB/s (copies alone take 72 us, the arithmetic alone 81: 260 instructions for 16 tokens and a
-// head, of which half the cycles issue one, with 16 warps an SM, which is all that the registers hold); 4 heads with 4
-// rows each 35.5 us, of which the join 4 and starts and ends of pieces 12.  One sequence of 4096 tokens, 4 heads of 64:
-// 6.1 us, latency.
+// head; half the cycles issue one, with 16 warps an SM, which is all that the registers hold); 4 heads with 4 rows each
+// 34.5 us, of which the join 4 and starts and ends of pieces 11.  One sequence of 4096 tokens, 4 heads of 64: 5.6 us,
+// latency; of 131072 tokens, 2 heads of 128, 8 bits: 22.7 us, HBM's rate but for its start and end.
 #include <cuda_fp16.h>
 #include <math.h>
 
