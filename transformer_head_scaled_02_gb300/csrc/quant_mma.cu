@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
     }
 
     bool ok = true;
-    int used = 0;  // stages
+    uint32_t used = 0;  // stages
 #pragma unroll 1
     for (int q_at = begin; q_at < end;) {
     const QuantPiece z = piece(q_at);
@@ -380,17 +380,17 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
     const int va = 2 * tig ^ (tig & 1), vb = (2 * tig + 1) ^ (tig & 1);  // order in which neither load meets itself in a bank
 #pragma unroll 1
     for (int t_stage = z.k0(); t_stage < z.k1() && ok; t_stage += C::TOK) {
-        const uint32_t slot = (uint32_t)(used % C::STAGES);
-        if (!__all_sync(0xffffffffu, mbar_wait(bars + 8u * slot, (uint32_t)(used / C::STAGES) & 1u, abort_flag, status))) {
+        const uint32_t slot = used % C::STAGES;
+        if (!__all_sync(0xffffffffu, mbar_wait(bars + 8u * slot, used / C::STAGES & 1u, abort_flag, status))) {
             ok = false;
             break;
         }
         const uint32_t at = ring + slot * C::STAGE;
         // the stage's 16-token blocks, a run of them for each warp
-        const int blocks = min(C::TOK / 16, (z.k1() - t_stage + 15) / 16);
-        const int w_end = min(z.k1(), t_stage + (warp + 1) * blocks / QM_WARPS * 16);  // the run's end
+        const uint32_t blocks = min((uint32_t)C::TOK / 16u, (uint32_t)(z.k1() - t_stage + 15) / 16u);
+        const int w_end = min(z.k1(), t_stage + (int)((uint32_t)(warp + 1) * blocks / QM_WARPS * 16u));  // the run's end
 #pragma unroll 1
-        for (int sub = warp * blocks / QM_WARPS * 16; t_stage + sub < w_end; sub += 16 * SUB) {
+        for (int sub = (int)((uint32_t)warp * blocks / QM_WARPS * 16u); t_stage + sub < w_end; sub += 16 * SUB) {
             const int t0 = t_stage + sub;
             const bool edge = t0 + 16 * SUB > min(lim_min, w_end);  // some column does not see all of its 16
             const uint32_t kc = at + (uint32_t)(sub * C::ROW), vc = kc + C::TOK * C::ROW;
@@ -573,9 +573,8 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
         uint32_t last = 0;
         __syncwarp();  // the stage is read
         if (lane == 0) {
-            __threadfence_block();
-            last = atomicAdd(done + slot, 1u) % QM_WARPS == QM_WARPS - 1;
-            __threadfence_block();
+            asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;" : "=r"(last) : "r"(bars + 8u * C::STAGES + 4u * slot) : "memory");
+            last = last % QM_WARPS == QM_WARPS - 1;
         }
         if (__shfl_sync(0xffffffffu, last, 0)) {
             QmNext x = *next;
