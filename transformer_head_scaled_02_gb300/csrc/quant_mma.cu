@@ -29,10 +29,10 @@
 // moves only when a score exceeds it by 2^8, which one vote per block finds.
 //
 // Measured, bf16 layers, 4 bits, heads of 128, 32 ragged sequences of up to 8192 tokens: 16 heads with one query row each
-// 95 us, 453 MB at 4.8 TB/s (copies alone take 72 us, the arithmetic alone 81: 260 instructions for 16 tokens and a
+// 94 us, 453 MB at 4.8 TB/s (copies alone take 72 us, the arithmetic alone 81: 260 instructions for 16 tokens and a
 // head; half the cycles issue one, with 16 warps an SM, which is all that the registers hold); 4 heads with 4 rows each
-// 34.5 us, of which the join 4 and starts and ends of pieces 11.  One sequence of 4096 tokens, 4 heads of 64: 5.6 us,
-// latency; of 131072 tokens, 2 heads of 128, 8 bits: 22.7 us, HBM's rate but for its start and end.
+// 34.3 us, of which the join 4 and starts and ends of pieces 11.  One sequence of 4096 tokens, 4 heads of 64: 5.5 us,
+// latency; of 131072 tokens, 2 heads of 128, 8 bits: 22.5 us, HBM's rate but for its start and end.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -253,16 +253,18 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
             x.from = z.k0();
             x.to = z.k1();
         }
-        if (lane == 0) {
-            // whole sixteens: caches hold multiples of them
-            const uint32_t tok = (uint32_t)min(C::TOK, (x.to - x.from + 15) & ~15);
-            const uint32_t at = ring + (uint32_t)(x.issued % C::STAGES * C::STAGE), bar = bars + 8u * (uint32_t)(x.issued % C::STAGES);
+        // whole sixteens: caches hold multiples of them.  Codes and parameters of keys and values: a lane each.
+        const uint32_t tok = (uint32_t)min(C::TOK, (x.to - x.from + 15) & ~15);
+        const uint32_t at = ring + (uint32_t)(x.issued % C::STAGES * C::STAGE), bar = bars + 8u * (uint32_t)(x.issued % C::STAGES);
+        if (lane == 0) mbar_arrive_expect_tx(bar, 2u * tok * (C::ROW + 4 * G));
+        __syncwarp();
+        if (lane < 4) {
+            const bool values = lane & 1, params = lane & 2;
             const int64_t r = x.row + x.from;
-            mbar_arrive_expect_tx(bar, 2u * tok * (C::ROW + 4 * G));
-            bulk_load(at, pk.codes + r * C::ROW, tok * C::ROW, bar);
-            bulk_load(at + 2 * C::TOK * C::ROW, pk.params + r * G, tok * 4 * G, bar);
-            bulk_load(at + C::TOK * C::ROW, pv.codes + r * C::ROW, tok * C::ROW, bar);
-            bulk_load(at + 2 * C::TOK * C::ROW + C::TOK * 4 * G, pv.params + r * G, tok * 4 * G, bar);
+            const uint8_t* codes = (values ? pv.codes : pk.codes) + r * C::ROW;
+            const uint32_t* pars = (values ? pv.params : pk.params) + r * G;
+            const uint32_t to = params ? at + 2 * C::TOK * C::ROW + (values ? C::TOK * 4 * G : 0) : at + (values ? C::TOK * C::ROW : 0);
+            bulk_load(to, params ? static_cast<const void*>(pars) : codes, params ? tok * 4 * G : tok * C::ROW, bar);
         }
         x.from += C::TOK;
         ++x.issued;
