@@ -289,6 +289,28 @@ def test_decode_many_rows(dtype, d, h, h_kv, Tq, bits):
     _step(layer, cache, held, wl.random_tensor((3, Tq, h * d), 5, dtype), lengths, dtype, "many rows")
 
 
+@pytest.mark.parametrize("d", [1, 31, 32, 33, 65, 80, 96, 97, 127])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("h,h_kv,Tq,lengths", [
+    (2, 2, 1, [300, 1, 129]), (4, 1, 2, [700, 2, 128, 65]), (8, 1, 2, [513, 100]), (6, 3, 2, [9000]),
+    (4, 2, 1, [3000, 20, 2999, 1, 1500, 700, 64, 2048])])
+def test_decode_fp32_head_sizes(d, bits, h, h_kv, Tq, lengths):
+    """Heads of any number of channels up to 128: rows of 32, 64, 96 and 128 of them, outputs that end inside a piece of
+    four, beside a guard band."""
+    layer = _layer("f32", h, d, h_kv)
+    T = max(lengths)
+    cache, held = _filled(layer, d + T, "f32", len(lengths), T, bits)
+    _spoil(cache, lengths)
+    Q = wl.random_tensor((len(lengths), Tq, h * d), 5, "f32")
+    big = torch.full((len(lengths), Tq, h * d + 9), 7.0, device="cuda")
+    layer.decode_quant(to_device(Q, "f32"), cache, _ints(lengths), out=big[..., 5:5 + h * d])
+    got = to_host(big)
+    assert (got[..., :5] == 7).all() and (got[..., 5 + h * d:] == 7).all()
+    O, A, S = qc.decode(Q, *held, h, lengths)
+    _check(got[..., 5:5 + h * d], O, A, S, "f32", "head sizes")
+    assert layer.status() == 0
+
+
 @pytest.mark.parametrize("d,h,h_kv,Tq,lengths", [
     (128, 2, 1, 130, [400, 130, 257]), (64, 4, 1, 65, [65, 700, 129]), (128, 4, 2, 200, [1500]),
     (64, 8, 1, 100, [128, 100, 640, 127, 384]), (128, 1, 1, 256, [256, 300])])

@@ -208,6 +208,7 @@ cudaError_t launch_quant_rows(const QuantStep& s, int bits, const QuantPlane& pk
                               void* O, int64_t ldo, const int32_t* lengths, float* part, int* status, cudaStream_t stream);
 // The tensor-core kernel: head sizes it serves, query rows of its blocks, CTAs that an SM holds, the launch.
 bool quant_mma_serves(int d_k, int d_v);
+int quant_mma_width(int d_k);
 int quant_mma_rows(bool f32, int bits, int d, int rows);
 int quant_mma_ctas(bool f32, int d, int rb);
 cudaError_t launch_quant_mma(const QuantStep& s, bool f32, int bits, const QuantPlane& pk, const QuantPlane& pv, const void* Q,

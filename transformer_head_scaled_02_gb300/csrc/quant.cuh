@@ -63,6 +63,7 @@ struct QuantStep {
     int rb, nrb;  // rows of a row block; row blocks
     int ctas;     // grid: C is this, or the number of quanta if that is less
     int dv;
+    int rec;      // values of a row's record: dv, or as many as the kernel computes
     int quantum;  // tokens of a quantum: a multiple of kQuantum
     int cluster;  // CTAs of a cluster, each with one piece; 0: the even cut.  ctas is then cluster * parts * groups
     int parts;    // clusters of a group
@@ -70,7 +71,7 @@ struct QuantStep {
     // a chain that a step has to wait for)
     Divide by_T_q, by_nrb, by_lanes, by_quantum, by_ctas, by_group;
     __host__ __device__ int lanes() const { return h_kv * nrb; }   // groups of a batch
-    __host__ __device__ int record() const { return dv + 2; }      // floats
+    __host__ __device__ int record() const { return rec + 2; }     // floats
     // Record of a row of a CTA's first (which = 0: it began in another CTA) or last group.
     __host__ __device__ int64_t slot(int cta, int which, int row) const { return ((int64_t)(2 * cta + which) * rb + row) * record(); }
 };

@@ -112,7 +112,15 @@ __device__ __forceinline__ void quant_meet(const QuantStep& s, bool whole, float
             x = make_float4(fmaf(f, v.x, x.x), fmaf(f, v.y, x.y), fmaf(f, v.z, x.z), fmaf(f, v.w, x.w));
         }
         if (whole) {
-            quant_put4(quant_out(s, O, ldo, b, g, r0 + r) + c, x);
+            T* to = quant_out(s, O, ldo, b, g, r0 + r) + c;
+            if (sizeof(T) == 2 || c + 4 <= s.dv) {
+                quant_put4(to, x);
+            } else {  // fp32 layers' heads may have fewer channels than are computed with
+                const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (c + i < s.dv) quant_put(to + i, v[i]);
+            }
         } else if (rec != nullptr) {
             *reinterpret_cast<float2*>(rec + r * RECORD + 2 + c) = make_float2(x.x, x.y);
             *reinterpret_cast<float2*>(rec + r * RECORD + 4 + c) = make_float2(x.z, x.w);

@@ -1,4 +1,4 @@
-// quant_mma.cu -- a decode step over a quantised cache (quant.cuh) for heads of 64 and 128 channels, on the tensor
+// quant_mma.cu -- a decode step over a quantised cache (quant.cuh) for heads of up to 128 channels, on the tensor
 // cores: the codes themselves are the matrix operands.
 //
 // A code in a 16-bit half whose other bits are zero is an fp16 number as it stands, a subnormal one: code 2^-24 exactly
@@ -50,10 +50,12 @@ constexpr int QM_WARPS = 8;
 constexpr float kNone = -3e38f;  // the reference of a row that has seen nothing: below every score, finite
 constexpr int QM_THREADS = 32 * QM_WARPS;
 
-template <int BITS, int D, int TERMS, int NT, int SUB>
+// D: channels that are computed with, DP: those that a row of the cache has.  (What lies behind a short row is the next
+// one's codes: finite numbers, which meet queries of zero and make values that nobody stores.)
+template <int BITS, int D, int DP, int TERMS, int NT, int SUB>
 struct QmCfg {
     static constexpr int G = D / kQuantGroup;
-    static constexpr int ROW = D * BITS / 8;
+    static constexpr int ROW = DP * BITS / 8;
     static constexpr int TOK = 131072 / (D * BITS);           // tokens of a stage: 32 KB of codes
     static constexpr int STAGE = 2 * TOK * (ROW + 4 * G);     // key codes, value codes, key and value parameters
     static constexpr int CTAS = NT * TERMS * G > 2 ? 1 : 2;   // of an SM (registers)
@@ -197,12 +199,12 @@ __device__ __forceinline__ void token_params(uint32_t addr, uint32_t (&p)[G]) {
 __device__ __forceinline__ float elem(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float elem(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
-template <int BITS, int D, int TERMS, int NT, int SUB, typename T>
-__global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CTAS)
+template <int BITS, int D, int DP, int TERMS, int NT, int SUB, typename T>
+__global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB>::CTAS)
     quant_mma_kernel(const QuantStep s, const QuantPlane pk, const QuantPlane pv, const T* __restrict__ Q, int64_t ldq,
                      T* __restrict__ O, int64_t ldo, const int32_t* __restrict__ lengths, float scale_log2,
                      float* __restrict__ part, int* status) {
-    using C = QmCfg<BITS, D, TERMS, NT, SUB>;
+    using C = QmCfg<BITS, D, DP, TERMS, NT, SUB>;
     constexpr int G = C::G;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5, gid = lane >> 2, tig = lane & 3;
@@ -295,10 +297,10 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
 #pragma unroll
         for (int r = warp; r < C::ROWS; r += QM_WARPS) {
             const int rr = r0 + min(r, nr - 1), hg = s.by_T_q((uint32_t)rr), t = rr - hg * s.T_q;
-            const T* src = Q + ((int64_t)b * s.T_q + t) * ldq + (int64_t)(g * s.per + hg) * D + lane * CPL;
+            const T* src = Q + ((int64_t)b * s.T_q + t) * ldq + (int64_t)(g * s.per + hg) * (TERMS == 1 ? D : s.dv) + lane * CPL;
             float x[CPL], top = 0.f;
 #pragma unroll
-            for (int e = 0; e < CPL; ++e) x[e] = elem(src + e);
+            for (int e = 0; e < CPL; ++e) x[e] = TERMS == 1 || lane * CPL + e < s.dv ? elem(src + e) : 0.f;
 #pragma unroll
             for (int e = 0; e < CPL; ++e) top = fmaxf(top, fabsf(x[e]));
 #pragma unroll
@@ -650,7 +652,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
                     x = fmaf(f, v[k], x);
                 }
             if (s.parts == 1) {
-                quant_put(quant_out(s, O, ldo, own.b, g, r0 + r) + to.rank * cols + c, x / sum);
+                if (TERMS == 1 || to.rank * cols + c < s.dv) quant_put(quant_out(s, O, ldo, own.b, g, r0 + r) + to.rank * cols + c, x / sum);
             } else {
                 float* rec = part + ((int64_t)((int)blockIdx.x / s.cluster) * C::ROWS + r) * s.record();
                 rec[2 + to.rank * cols + c] = x;
@@ -663,13 +665,13 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, TERMS, NT, SUB>::CT
             drain_wait_a(bars + 8u * (uint32_t)(k % C::STAGES), (uint32_t)(k / C::STAGES) & 1u);
 }
 
-template <int BITS, int D, int TERMS, int NT, int SUB, typename T>
+template <int BITS, int D, int DP, int TERMS, int NT, int SUB, typename T>
 cudaError_t launch(const QuantStep& s, const QuantPlane& pk, const QuantPlane& pv, const void* Q, int64_t ldq, void* O,
                    int64_t ldo, const int32_t* lengths, float* part, int* status, cudaStream_t stream) {
-    using C = QmCfg<BITS, D, TERMS, NT, SUB>;
-    auto kernel = quant_mma_kernel<BITS, D, TERMS, NT, SUB, T>;
+    using C = QmCfg<BITS, D, DP, TERMS, NT, SUB>;
+    auto kernel = quant_mma_kernel<BITS, D, DP, TERMS, NT, SUB, T>;
     static std::atomic<uint64_t> done{0};
-    const float scale = (float)(1.4426950408889634 / sqrt((double)D));
+    const float scale = (float)(1.4426950408889634 / sqrt((double)pk.d));
     return launch_with_smem(kernel, C::SMEM, done, [&] {
         return launch_pdl_cluster(kernel, s.cluster > 1 ? s.cluster : 1, dim3((unsigned)s.ctas), dim3(QM_THREADS), C::SMEM, stream, s,
                                   pk, pv, static_cast<const T*>(Q), ldq, static_cast<T*>(O), ldo, lengths, scale, part, status);
@@ -679,40 +681,51 @@ cudaError_t launch(const QuantStep& s, const QuantPlane& pk, const QuantPlane& p
 // (fp32 layers of 128 channels have no room in the registers for 16 rows)
 constexpr bool most_rows_16(int terms, int d) { return !(terms == 2 && d == 128); }
 
-template <int BITS, int D, typename T, typename... A>
+template <int BITS, int D, int DP, typename T, typename... A>
 cudaError_t launch_rows(int rb, A... a) {
     constexpr int TERMS = std::is_same_v<T, float> ? 2 : 1;
     if constexpr (BITS * D <= 512)
-        if (rb == 4) return launch<BITS, D, TERMS, 1, 2, T>(a...);
-    if (rb == 8) return launch<BITS, D, TERMS, 1, 1, T>(a...);
-    if constexpr (most_rows_16(TERMS, D)) return launch<BITS, D, TERMS, 2, 1, T>(a...);
+        if (rb == 4) return launch<BITS, D, DP, TERMS, 1, 2, T>(a...);
+    if (rb == 8) return launch<BITS, D, DP, TERMS, 1, 1, T>(a...);
+    if constexpr (most_rows_16(TERMS, D)) return launch<BITS, D, DP, TERMS, 2, 1, T>(a...);
     return cudaErrorInvalidValue;
+}
+
+// bf16 layers have heads of 64 and 128 channels.  fp32 ones compute short rows with 64 or 128 (16 ragged sequences of up
+// to 4096 tokens, 8 heads of 80, 8 bits: 33 us, 95 on CUDA cores).
+template <int BITS, typename T, typename... A>
+cudaError_t launch_width(int d, int rb, A... a) {
+    if constexpr (std::is_same_v<T, float>) {
+        if (d <= 32) return launch_rows<BITS, 64, 32, T>(rb, a...);
+        if (d > 64 && d <= 96) return launch_rows<BITS, 128, 96, T>(rb, a...);
+    }
+    return d <= 64 ? launch_rows<BITS, 64, 64, T>(rb, a...) : launch_rows<BITS, 128, 128, T>(rb, a...);
 }
 
 }  // namespace
 
-bool quant_mma_serves(int d_k, int d_v) { return d_k == d_v && (d_k == 64 || d_k == 128); }
+bool quant_mma_serves(int d_k, int d_v) { return d_k == d_v && d_k <= 128; }
+
+// Channels that are computed with.
+int quant_mma_width(int d) { return d <= 64 ? 64 : 128; }
 
 // Query rows of a block: 4, whose columns two blocks of tokens share (a warp's part of a stage of 8 bits and 128 channels
 // is one block), 8, or 16 (two sets of operands and sums beside each unpacked code).
-int quant_mma_rows(bool f32, int bits, int d, int rows) {
+int quant_mma_rows(bool f32, int bits, int d_k, int rows) {
+    const int d = quant_mma_width(d_k);
     if (rows <= 4 && bits * d <= 512) return 4;
     return rows <= 8 || !most_rows_16(f32 ? 2 : 1, d) ? 8 : 16;
 }
 
-int quant_mma_ctas(bool f32, int d, int rb) { return (f32 ? 2 : 1) * (d / 64) * (rb == 16 ? 2 : 1) > 2 ? 1 : 2; }
+int quant_mma_ctas(bool f32, int d_k, int rb) { return (f32 ? 2 : 1) * (quant_mma_width(d_k) / 64) * (rb == 16 ? 2 : 1) > 2 ? 1 : 2; }
 
 cudaError_t launch_quant_mma(const QuantStep& s, bool f32, int bits, const QuantPlane& pk, const QuantPlane& pv, const void* Q,
                              int64_t ldq, void* O, int64_t ldo, const int32_t* lengths, float* part, int* status,
                              cudaStream_t stream) {
     auto go = [&](auto* x) {
         using T = std::remove_pointer_t<decltype(x)>;
-        auto with = [&](auto f) { return f(s.rb, s, pk, pv, Q, ldq, O, ldo, lengths, part, status, stream); };
-        if (bits == 4)
-            return pk.d == 64 ? with([](auto rb, auto&... a) { return launch_rows<4, 64, T>(rb, a...); })
-                              : with([](auto rb, auto&... a) { return launch_rows<4, 128, T>(rb, a...); });
-        return pk.d == 64 ? with([](auto rb, auto&... a) { return launch_rows<8, 64, T>(rb, a...); })
-                          : with([](auto rb, auto&... a) { return launch_rows<8, 128, T>(rb, a...); });
+        return bits == 4 ? launch_width<4, T>(pk.d, s.rb, s, pk, pv, Q, ldq, O, ldo, lengths, part, status, stream)
+                         : launch_width<8, T>(pk.d, s.rb, s, pk, pv, Q, ldq, O, ldo, lengths, part, status, stream);
     };
     return f32 ? go(static_cast<float*>(nullptr)) : go(static_cast<__nv_bfloat16*>(nullptr));
 }
