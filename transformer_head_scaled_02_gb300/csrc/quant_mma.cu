@@ -52,19 +52,23 @@ constexpr int QM_THREADS = 32 * QM_WARPS;
 
 // D: channels that are computed with, DP: those that a row of the cache has.  (What lies behind a short row is the next
 // one's codes: finite numbers, which meet queries of zero and make values that nobody stores.)
-template <int BITS, int D, int DP, int TERMS, int NT, int SUB>
+// SPLIT: the columns are shared out to the groups as well.
+template <int BITS, int D, int DP, int TERMS, int NT, int SUB, bool SPLIT>
 struct QmCfg {
     static constexpr int G = D / kQuantGroup;
+    static constexpr int GL = SPLIT ? 1 : G;                  // groups of a column
     static constexpr int ROW = DP * BITS / 8;
     static constexpr int TOK = 131072 / (D * BITS);           // tokens of a stage: 32 KB of codes
     static constexpr int STAGE = 2 * TOK * (ROW + 4 * G);     // key codes, value codes, key and value parameters
     static constexpr int CTAS = NT * TERMS * G > 2 ? 1 : 2;   // of an SM (registers)
     static constexpr int STAGES = CTAS == 1 ? 4 : 2;
     static constexpr int COLS = 8 * NT;                       // columns of the products
-    static constexpr int ROWS = COLS / SUB;                   // query rows of a block
-    static constexpr int REC = D + 4;                         // floats of a column's result: values, m, l
+    static constexpr int COPIES = SPLIT ? SUB * G : SUB;      // of a query row among the columns
+    static constexpr int ROWS = COLS / COPIES;                // query rows of a block
+    static constexpr int RESULTS = SUB * ROWS;                // of a warp
+    static constexpr int REC = D + 4;                         // floats of a result: values, m, l
     static constexpr int RES = STAGES * STAGE;                // the warps' results
-    static constexpr int QF = RES + QM_WARPS * COLS * REC * 4;  // queries as operands, their sums and scales
+    static constexpr int QF = RES + QM_WARPS * RESULTS * REC * 4;  // queries as operands, their sums and scales
     static constexpr int QS = QF + TERMS * NT * G * 32 * 32;
     static constexpr int QEND = QS + COLS * (G + 1) * 4;
     using Share = QuantShare<ROWS, D>;                        // of a cluster: a place of its own, or if that does not fit the
@@ -74,6 +78,7 @@ struct QmCfg {
     static constexpr int BARS = SHARE + Share::BYTES > QEND ? SHARE + Share::BYTES : QEND;
     static constexpr int SMEM = BARS + TAIL;                  // barriers, counts of the warps done, QmNext, abort flag
     static_assert(SUB == 1 || NT == 1, "only a few rows leave columns for a second block");
+    static_assert(!SPLIT || (SUB == 2 && G == 2), "four sets of two columns");
     static_assert(BARS % 16 == 0 && SHARE % 16 == 0 && SMEM <= 232448, "");
     static_assert(TOK % kQuantum == 0, "a stage's tokens are dealt out evenly");
     static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory of an SM");
@@ -199,13 +204,13 @@ __device__ __forceinline__ void token_params(uint32_t addr, uint32_t (&p)[G]) {
 __device__ __forceinline__ float elem(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float elem(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
-template <int BITS, int D, int DP, int TERMS, int NT, int SUB, typename T>
-__global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB>::CTAS)
+template <int BITS, int D, int DP, int TERMS, int NT, int SUB, bool SPLIT, typename T>
+__global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB, SPLIT>::CTAS)
     quant_mma_kernel(const QuantStep s, const QuantPlane pk, const QuantPlane pv, const T* __restrict__ Q, int64_t ldq,
                      T* __restrict__ O, int64_t ldo, const int32_t* __restrict__ lengths, float scale_log2,
                      float* __restrict__ part, int* status) {
-    using C = QmCfg<BITS, D, DP, TERMS, NT, SUB>;
-    constexpr int G = C::G;
+    using C = QmCfg<BITS, D, DP, TERMS, NT, SUB, SPLIT>;
+    constexpr int G = C::G, GL = C::GL;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5, gid = lane >> 2, tig = lane & 3;
     const uint32_t ring = smem_u32(smem), bars = ring + C::BARS;
@@ -319,7 +324,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB>
                 sum = fmaf(h == 0 ? unit<BITS, TERMS>(0) : unit<BITS, TERMS>(1), v, sum);
                 const __half hi = __float2half_rn(v), lo = __float2half_rn(v - __half2float(hi));
 #pragma unroll
-                for (int k = 0; k < SUB; ++k) {
+                for (int k = 0; k < C::COPIES; ++k) {
                     const int n = r % 8 + k * C::ROWS;  // column
                     const int at = (((r / 8 * G + u) * 32 + 4 * n + to) * 8 + 2 * c + h) * 2 + half;
                     qh[at] = hi;
@@ -330,7 +335,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB>
             for (int w = 8; w >= 1; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
             if constexpr (G == 1) sum += __shfl_xor_sync(0xffffffffu, sum, 16);
 #pragma unroll
-            for (int k = 0; k < SUB; ++k) {
+            for (int k = 0; k < C::COPIES; ++k) {
                 if (lane % 16 == 0 && lane / 16 < G) qv[(r + k * C::ROWS) * (G + 1) + u] = sum;
                 if (lane == 0) qv[(r + k * C::ROWS) * (G + 1) + G] = scale_log2 / unit<BITS, TERMS>(0) * quant_power2(-e2);
             }
@@ -338,7 +343,8 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB>
     }
     __syncthreads();
     uint32_t qf[TERMS][NT][G][4][2];
-    float qs[NT][G][2], rs[NT][2];  // y rs is a score
+    const int set = SPLIT ? tig : 0, first = set % 2;  // of a lane's columns: block * 2 + group, and that group
+    float qs[NT][GL][2], rs[NT][2];  // y rs is a score
     const int lim_min = L - s.T_q + 1;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -355,14 +361,14 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB>
         for (int e = 0; e < 2; ++e) {
             const float* from = reinterpret_cast<const float*>(smem + C::QS) + (8 * nt + 2 * tig + e) * (G + 1);
 #pragma unroll
-            for (int u = 0; u < G; ++u) qs[nt][u][e] = from[u];
+            for (int u = 0; u < GL; ++u) qs[nt][u][e] = from[first + u];
             rs[nt][e] = from[G];
         }
     }
 
     if (!C::ROOM && s.cluster > 1) cluster_arrive();  // the queries' place may be written
 
-    float o[NT][G][4][4], om[NT][G][2], m[NT][2], l[NT][2];
+    float o[NT][GL][4][4], om[NT][GL][2], m[NT][2], l[NT][2];
     float vs[NT][2];   // p s is held as p s vs: of each column, as a token may matter to one row and not to another
     float far[NT][2];  // the y that moves the reference m, which is a y too (a rounded score could be far from a large one)
 #pragma unroll
@@ -373,13 +379,13 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB>
             vs[nt][e] = quant_power2(100);
             l[nt][e] = 0.f;
 #pragma unroll
-            for (int u = 0; u < G; ++u) {
+            for (int u = 0; u < GL; ++u) {
                 om[nt][u][e] = 0.f;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) o[nt][u][c][2 * e] = o[nt][u][c][2 * e + 1] = 0.f;
             }
         }
-    const int block = SUB == 1 ? 0 : 2 * tig / C::ROWS;           // whose columns the lane has
+    const int block = SUB == 1 ? 0 : SPLIT ? tig / 2 : 2 * tig / C::ROWS;  // whose columns the lane has
     const int pa = gid ^ (gid >> 1 & 1);                          // this lane's key token, and its second at + 8: the
     const int va = 2 * tig ^ (tig & 1), vb = (2 * tig + 1) ^ (tig & 1);  // order in which neither load meets itself in a bank
 #pragma unroll 1
@@ -398,11 +404,11 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB>
             const int t0 = t_stage + sub;
             const bool edge = t0 + 16 * SUB > min(lim_min, w_end);  // some column does not see all of its 16
             const uint32_t kc = at + (uint32_t)(sub * C::ROW), vc = kc + C::TOK * C::ROW;
-            const uint32_t kp = at + 2 * C::TOK * C::ROW + (uint32_t)((sub + 16 * block) * 4 * G), vp = kp + C::TOK * 4 * G;
+            const uint32_t kp = at + 2 * C::TOK * C::ROW + (uint32_t)((sub + 16 * block) * 4 * G + 4 * first), vp = kp + C::TOK * 4 * G;
             // scores; with two blocks, columns 0 .. 3 are the first one's and columns 4 .. 7 the second one's
             float y[NT][4];
             {
-                float acc[NT][G][4];
+                float acc[NT][GL][4];
 #pragma unroll
                 for (int k = 0; k < SUB; ++k)
 #pragma unroll
@@ -421,28 +427,32 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB>
                                 for (int w = 0; w < TERMS; ++w) mma_f16(d, a, qf[w][nt][u][c][0], qf[w][nt][u][c][1]);
                             }
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) acc[nt][u][e] = k == 0 ? d[e] : block == 0 ? acc[nt][u][e] : d[e];
+                            for (int e = 0; e < 4; ++e) {
+                                if constexpr (SPLIT) acc[nt][0][e] = k + u == 0 || set == 2 * k + u ? d[e] : acc[nt][0][e];
+                                else acc[nt][u][e] = k == 0 ? d[e] : block == 0 ? acc[nt][u][e] : d[e];
+                            }
                         }
                     }
-                uint32_t p0[G], p1[G];
-                token_params<G>(kp + (uint32_t)(pa * 4 * G), p0);
-                token_params<G>(kp + (uint32_t)((pa + 8) * 4 * G), p1);
+                uint32_t p0[GL], p1[GL];
+                token_params<GL>(kp + (uint32_t)(pa * 4 * G), p0);
+                token_params<GL>(kp + (uint32_t)((pa + 8) * 4 * G), p1);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         y[nt][e] = quant_lowest(e < 2 ? p0[0] : p1[0]) * qs[nt][0][e & 1];
 #pragma unroll
-                        for (int u = 0; u < G; ++u) {
+                        for (int u = 0; u < GL; ++u) {
                             const uint32_t par = e < 2 ? p0[u] : p1[u];
                             if (u > 0) y[nt][e] = fmaf(quant_lowest(par), qs[nt][u][e & 1], y[nt][e]);
                             y[nt][e] = fmaf(quant_step(par), acc[nt][u][e], y[nt][e]);
                         }
+                        if constexpr (SPLIT) y[nt][e] += __shfl_xor_sync(0xffffffffu, y[nt][e], 1);  // the other group's part
                     }
             }
-            uint32_t v0[G], v1[G];
-            token_params<G>(vp + (uint32_t)(pa * 4 * G), v0);
-            token_params<G>(vp + (uint32_t)((pa + 8) * 4 * G), v1);
+            uint32_t v0[GL], v1[GL];
+            token_params<GL>(vp + (uint32_t)(pa * 4 * G), v0);
+            token_params<GL>(vp + (uint32_t)((pa + 8) * 4 * G), v1);
             if (edge) {  // tokens at or past the length hold anything
                 const int ta = t0 + 16 * block + pa, tb = ta + 8;
 #pragma unroll
@@ -455,7 +465,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB>
                         if (tb >= lim) y[nt][e + 2] = -INFINITY;
                     }
 #pragma unroll
-                for (int u = 0; u < G; ++u) {
+                for (int u = 0; u < GL; ++u) {
                     if (ta >= w_end) v0[u] = 0;
                     if (tb >= w_end) v1[u] = 0;
                 }
@@ -463,7 +473,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB>
             // references
             float steps = 0.f;
 #pragma unroll
-            for (int u = 0; u < G; ++u) steps = fmax3(steps, quant_step(v0[u]), quant_step(v1[u]));
+            for (int u = 0; u < GL; ++u) steps = fmax3(steps, quant_step(v0[u]), quant_step(v1[u]));
             bool move = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -473,7 +483,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB>
             if (__any_sync(0xffffffffu, move)) {
                 float step0 = 0.f, step1 = 0.f, f[NT][2], fr[NT][2], seen = 0.f;
 #pragma unroll
-                for (int u = 0; u < G; ++u) {
+                for (int u = 0; u < GL; ++u) {
                     step0 = fmaxf(step0, quant_step(v0[u]));
                     step1 = fmaxf(step1, quant_step(v1[u]));
                 }
@@ -507,7 +517,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB>
                         for (int e = 0; e < 2; ++e) {
                             l[nt][e] *= f[nt][e];
 #pragma unroll
-                            for (int u = 0; u < G; ++u) {
+                            for (int u = 0; u < GL; ++u) {
                                 om[nt][u][e] *= f[nt][e];
 #pragma unroll
                                 for (int c = 0; c < 4; ++c) {
@@ -519,7 +529,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB>
                 }
             }
             // weights, and their products with the steps as B operands
-            uint32_t bf[TERMS][NT][G][2];
+            uint32_t bf[TERMS][NT][GL][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float p[4];
@@ -531,7 +541,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB>
 #pragma unroll
                 for (int e = 0; e < 4; ++e) pw[e] = p[e] * vs[nt][e & 1];
 #pragma unroll
-                for (int u = 0; u < G; ++u) {
+                for (int u = 0; u < GL; ++u) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t par = h == 0 ? v0[u] : v1[u];
@@ -562,14 +572,15 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB>
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) w2[w][nt][h] = SUB == 1 || gid / C::ROWS == k ? bf[w][nt][u][h] : 0u;
+                            for (int h = 0; h < 2; ++h)
+                                w2[w][nt][h] = SUB == 1 || gid / C::ROWS == (SPLIT ? 2 * k + u : k) ? bf[w][nt][SPLIT ? 0 : u][h] : 0u;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const uint32_t a[4] = {xa[c][0], xa[c][1], xb[c][0], xb[c][1]};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int w = 0; w < TERMS; ++w) mma_f16(o[nt][u][c], a, w2[w][nt][0], w2[w][nt][1]);
+                            for (int w = 0; w < TERMS; ++w) mma_f16(o[nt][SPLIT ? 0 : u][c], a, w2[w][nt][0], w2[w][nt][1]);
                     }
                 }
         }
@@ -589,7 +600,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB>
     }
 
     // this warp's result: rows of D values, m, l
-    float* own = reinterpret_cast<float*>(smem + C::RES) + warp * C::COLS * C::REC;
+    float* own = reinterpret_cast<float*>(smem + C::RES) + warp * C::RESULTS * C::REC;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -599,17 +610,17 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB>
             for (int w = 4; w <= 16; w <<= 1) {
                 l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], w);
 #pragma unroll
-                for (int u = 0; u < G; ++u) om[nt][u][e] += __shfl_xor_sync(0xffffffffu, om[nt][u][e], w);
+                for (int u = 0; u < GL; ++u) om[nt][u][e] += __shfl_xor_sync(0xffffffffu, om[nt][u][e], w);
             }
-            float* row = own + (8 * nt + 2 * tig + e) * C::REC;
+            float* row = own + (SPLIT ? block * C::ROWS + e : 8 * nt + 2 * tig + e) * C::REC + first * kQuantGroup;
 #pragma unroll
-            for (int u = 0; u < G; ++u)
+            for (int u = 0; u < GL; ++u)
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     *reinterpret_cast<float2*>(row + u * kQuantGroup + 8 * gid + 2 * c) =
                         make_float2(fmaf(o[nt][u][c][e], inv / unit<BITS, TERMS>(0), om[nt][u][e]),
                                     fmaf(o[nt][u][c][e + 2], inv / unit<BITS, TERMS>(1), om[nt][u][e]));
-            if (gid == 0) *reinterpret_cast<float2*>(row + D) = make_float2(m[nt][e] == kNone ? kNone : m[nt][e] * rs[nt][e], l[nt][e]);
+            if (gid == 0 && first == 0) *reinterpret_cast<float2*>(row + D) = make_float2(m[nt][e] == kNone ? kNone : m[nt][e] * rs[nt][e], l[nt][e]);
         }
     if (s.cluster > 1) cluster_wait();
     __syncthreads();
@@ -665,11 +676,11 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB>
             drain_wait_a(bars + 8u * (uint32_t)(k % C::STAGES), (uint32_t)(k / C::STAGES) & 1u);
 }
 
-template <int BITS, int D, int DP, int TERMS, int NT, int SUB, typename T>
+template <int BITS, int D, int DP, int TERMS, int NT, int SUB, bool SPLIT, typename T>
 cudaError_t launch(const QuantStep& s, const QuantPlane& pk, const QuantPlane& pv, const void* Q, int64_t ldq, void* O,
                    int64_t ldo, const int32_t* lengths, float* part, int* status, cudaStream_t stream) {
-    using C = QmCfg<BITS, D, DP, TERMS, NT, SUB>;
-    auto kernel = quant_mma_kernel<BITS, D, DP, TERMS, NT, SUB, T>;
+    using C = QmCfg<BITS, D, DP, TERMS, NT, SUB, SPLIT>;
+    auto kernel = quant_mma_kernel<BITS, D, DP, TERMS, NT, SUB, SPLIT, T>;
     static std::atomic<uint64_t> done{0};
     const float scale = (float)(1.4426950408889634 / sqrt((double)pk.d));
     return launch_with_smem(kernel, C::SMEM, done, [&] {
@@ -684,10 +695,12 @@ constexpr bool most_rows_16(int terms, int d) { return !(terms == 2 && d == 128)
 template <int BITS, int D, int DP, typename T, typename... A>
 cudaError_t launch_rows(int rb, A... a) {
     constexpr int TERMS = std::is_same_v<T, float> ? 2 : 1;
+    if constexpr (BITS * D == 512 && D == 128)
+        if (rb == 2) return launch<BITS, D, DP, TERMS, 1, 2, true, T>(a...);
     if constexpr (BITS * D <= 512)
-        if (rb == 4) return launch<BITS, D, DP, TERMS, 1, 2, T>(a...);
-    if (rb == 8) return launch<BITS, D, DP, TERMS, 1, 1, T>(a...);
-    if constexpr (most_rows_16(TERMS, D)) return launch<BITS, D, DP, TERMS, 2, 1, T>(a...);
+        if (rb == 4) return launch<BITS, D, DP, TERMS, 1, 2, false, T>(a...);
+    if (rb == 8) return launch<BITS, D, DP, TERMS, 1, 1, false, T>(a...);
+    if constexpr (most_rows_16(TERMS, D)) return launch<BITS, D, DP, TERMS, 2, 1, false, T>(a...);
     return cudaErrorInvalidValue;
 }
 
@@ -709,10 +722,11 @@ bool quant_mma_serves(int d_k, int d_v) { return d_k == d_v && d_k <= 128; }
 // Channels that are computed with.
 int quant_mma_width(int d) { return d <= 64 ? 64 : 128; }
 
-// Query rows of a block: 4, whose columns two blocks of tokens share (a warp's part of a stage of 8 bits and 128 channels
+// Query rows of a block: 2, whose columns two blocks of tokens and two groups share; 4, whose columns two blocks of tokens share (a warp's part of a stage of 8 bits and 128 channels
 // is one block), 8, or 16 (two sets of operands and sums beside each unpacked code).
 int quant_mma_rows(bool f32, int bits, int d_k, int rows) {
     const int d = quant_mma_width(d_k);
+    if (rows <= 2 && bits * d == 512 && d == 128) return 2;
     if (rows <= 4 && bits * d <= 512) return 4;
     return rows <= 8 || !most_rows_16(f32 ? 2 : 1, d) ? 8 : 16;
 }
