@@ -311,6 +311,16 @@ def test_decode_fp32_head_sizes(d, bits, h, h_kv, Tq, lengths):
     assert layer.status() == 0
 
 
+@pytest.mark.parametrize("d,h,h_kv,B,Tq,T", [(61, 64, 4, 8, 7, 5400), (64, 16, 1, 2, 1, 30000), (128, 8, 8, 2, 1, 20000),
+                                             (128, 2, 1, 2, 2, 9000), (32, 64, 16, 2, 1, 16000)])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_decode_fp32_long_means(d, h, h_kv, B, Tq, T, bits):
+    """Sums over thousands of tokens in an fp32 layer: the codes' are far larger than what they leave in the output."""
+    layer = _layer("f32", h, d, h_kv)
+    cache, held = _filled(layer, 3, "f32", B, T, bits)
+    _step(layer, cache, held, wl.random_tensor((B, Tq, h * d), 5, "f32"), [T] * B, "f32", "means")
+
+
 @pytest.mark.parametrize("d,h,h_kv,Tq,lengths", [
     (128, 2, 1, 130, [400, 130, 257]), (64, 4, 1, 65, [65, 700, 129]), (128, 4, 2, 200, [1500]),
     (64, 8, 1, 100, [128, 100, 640, 127, 384]), (128, 1, 1, 256, [256, 300])])

@@ -169,8 +169,18 @@ __device__ __forceinline__ void q_place(int j, int& c, int& h, int& e) {
     e = BITS == 4 ? j >> 2 & 1 : j >> 1 & 1;
 }
 
+// Codes as TERMS = 2 has them, in both halves, less 8 or 128.  Exact.
+__device__ __forceinline__ uint32_t sub_centre(uint32_t x) {
+    const uint32_t c = 0x02000200u;
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&c));
+    return *reinterpret_cast<const uint32_t*>(&y);
+}
+
 // Eight of a row's channels in a group (values) of two tokens a, b, as the A operands of the group's four products:
-// x[t][0] channel 2 t of both tokens, x[t][1] channel 2 t + 1.
+// x[t][0] channel 2 t of both tokens, x[t][1] channel 2 t + 1.  fp32 layers take half the range off the codes (and add it to
+// the lowest values), and add their sums over blocks outside the tensor core: it cuts off what its sums cannot hold, and
+// over thousands of tokens the sums of codes are far larger than what is left of them in the output (5400 tokens of small
+// scores: 2e-5 of the outputs with both left out, 1.3e-6 with the centre alone taken off).
 template <int BITS, int TERMS>
 __device__ __forceinline__ void value_operands(uint32_t addr_a, uint32_t addr_b, uint32_t (&x)[4][2]) {
     uint32_t a[BITS / 4], b[BITS / 4];
@@ -188,8 +198,8 @@ __device__ __forceinline__ void value_operands(uint32_t addr_a, uint32_t addr_b,
         codes_of<BITS, TERMS>(w, y);
 #pragma unroll
         for (int c = 0; c < 8 / BITS; ++c) {
-            x[i * 8 / BITS + c][0] = y[2 * c];
-            x[i * 8 / BITS + c][1] = y[2 * c + 1];
+            x[i * 8 / BITS + c][0] = TERMS == 1 ? y[2 * c] : sub_centre(y[2 * c]);
+            x[i * 8 / BITS + c][1] = TERMS == 1 ? y[2 * c + 1] : sub_centre(y[2 * c + 1]);
         }
     }
 }
@@ -545,7 +555,8 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB,
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t par = h == 0 ? v0[u] : v1[u];
-                        const float z = quant_lowest(par), w = quant_step(par);
+                        const float w = quant_step(par);
+                        const float z = TERMS == 1 ? quant_lowest(par) : fmaf(w, BITS == 4 ? 8.f : 128.f, quant_lowest(par));
                         om[nt][u][0] = fmaf(p[2 * h], z, om[nt][u][0]);
                         om[nt][u][1] = fmaf(p[2 * h + 1], z, om[nt][u][1]);
                         const float w0 = pw[2 * h] * w, w1 = pw[2 * h + 1] * w;
@@ -578,9 +589,18 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB,
                     for (int c = 0; c < 4; ++c) {
                         const uint32_t a[4] = {xa[c][0], xa[c][1], xb[c][0], xb[c][1]};
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float(&to)[4] = o[nt][SPLIT ? 0 : u][c];
+                            if constexpr (TERMS == 1) {
+                                mma_f16(to, a, w2[0][nt][0], w2[0][nt][1]);
+                            } else {  // (sums over many blocks are rounded, not cut off)
+                                float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                            for (int w = 0; w < TERMS; ++w) mma_f16(o[nt][SPLIT ? 0 : u][c], a, w2[w][nt][0], w2[w][nt][1]);
+                                for (int w = 0; w < TERMS; ++w) mma_f16(d, a, w2[w][nt][0], w2[w][nt][1]);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) to[e] += d[e];
+                            }
+                        }
                     }
                 }
         }
