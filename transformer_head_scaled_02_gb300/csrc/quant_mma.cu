@@ -29,9 +29,10 @@
 // moves only when a score exceeds it by 2^8, which one vote per block finds.
 //
 // Measured, bf16 layers, 4 bits, heads of 128, 32 ragged sequences of up to 8192 tokens: 16 heads with one query row each
-// 94 us, 453 MB at 4.8 TB/s (copies alone take 72 us, the arithmetic alone 81: 260 instructions for 16 tokens and a
-// head; half the cycles issue one, with 16 warps an SM, which is all that the registers hold); 4 heads with 4 rows each
-// 34.3 us, of which the join 4 and starts and ends of pieces 11.  One sequence of 4096 tokens, 4 heads of 64: 5.5 us,
+// 94 us, 453 MB at 4.8 TB/s.  Copies alone take 72 us; with all of them out of L2 it is the same 94: what bounds it is in
+// the SMs, where half of all cycles issue an instruction, with 16 warps, which is all that the registers hold (a tenth
+// fewer instructions, products interleaved, loads ahead or a third stage changed nothing).  4 heads with 4 rows each
+// 34.2 us, of which the join 4 and starts and ends of pieces 11.  One sequence of 4096 tokens, 4 heads of 64: 5.5 us,
 // latency; of 131072 tokens, 2 heads of 128, 8 bits: 22.5 us, HBM's rate but for its start and end.
 #include <cuda_fp16.h>
 #include <math.h>
@@ -180,7 +181,9 @@ __device__ __forceinline__ uint32_t sub_centre(uint32_t x) {
 // x[t][0] channel 2 t of both tokens, x[t][1] channel 2 t + 1.  fp32 layers take half the range off the codes (and add it to
 // the lowest values), and add their sums over blocks outside the tensor core: it cuts off what its sums cannot hold, and
 // over thousands of tokens the sums of codes are far larger than what is left of them in the output (5400 tokens of small
-// scores: 2e-5 of the outputs with both left out, 1.3e-6 with the centre alone taken off).
+// scores: 2e-5 of the outputs with both left out, 1.3e-6 with the centre alone taken off, 1e-7 with both).  bf16 layers leave
+// both out: 3e-8 of the codes' part for each 16 tokens of a warp, far below what the weights' 11 bits cost (adding outside
+// the tensor core took 1 to 3 % longer).
 template <int BITS, int TERMS>
 __device__ __forceinline__ void value_operands(uint32_t addr_a, uint32_t addr_b, uint32_t (&x)[4][2]) {
     uint32_t a[BITS / 4], b[BITS / 4];
