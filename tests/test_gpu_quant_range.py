@@ -1,0 +1,61 @@
+"""The decode step over a quantised cache at the ends of its number range, against the 64-bit definition
+(oracle/quant_cache.py).
+
+Weighted sums are held before the division by the weights' sum, in fp32: they are finite as long as
+2^8 T max |v| is below 2^128 (no weight is above 2^8), or for scores that are all alike, whose weights are 1,
+T max |v|.  Tolerances are those of test_gpu_quant_cache.py.
+"""
+import numpy as np
+import pytest
+
+import test_gpu_quant_cache as base
+from gpu_util import to_device, to_host
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+from oracle import quant_cache as qc  # noqa: E402
+from transformer_head_scaled_02_gb300 import workloads as wl  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__ as g
+    g.build_library()
+    assert torch.cuda.is_available()
+    torch.cuda.set_device(0)
+
+
+def _round(x, dtype):
+    x = np.asarray(x, np.float32)
+    return wl.bf16_to_f32(wl.bf16_bits(x)) if dtype == "bf16" else x
+
+
+def _written(layer, K, V, dtype, bits):
+    """A cache that holds the rows K and V (B, T, ..) and its contents in 64 bits."""
+    B, T = K.shape[:2]
+    cache = layer.quant_cache(B, T, bits)
+    layer.quant_write(cache, to_device(K, dtype), to_device(V, dtype), base._ints([T] * B))
+    return cache, tuple(x[:, :, :T] for x in base._held(cache, "K") + base._held(cache, "V"))
+
+
+# query heads over one cached head, new tokens: 1, 2, 4, 8, 16 rows and hundreds
+ROWS = [("bf16", 64, 1, 1), ("bf16", 64, 8, 1), ("bf16", 64, 16, 1), ("bf16", 128, 1, 1), ("bf16", 128, 4, 1), ("bf16", 128, 16, 1),
+        ("bf16", 64, 1, 256), ("bf16", 128, 2, 140), ("f32", 64, 1, 1), ("f32", 64, 16, 1), ("f32", 128, 1, 1), ("f32", 40, 3, 1)]
+
+
+@pytest.mark.parametrize("dtype,d,h,Tq", ROWS)
+@pytest.mark.parametrize("bits", [4, 8])
+def test_decode_values_near_the_top(dtype, d, h, Tq, bits):
+    """Values of 2^108 under ordinary scores, and of 2^116 under scores that are nearly alike: 300 of them, times 5 and
+    the weights, stay below 2^128."""
+    T = 300
+    layer = base._layer(dtype, h, d, 1)
+    Q, K, V = (wl.random_tensor((1, n, w), 30 + i, dtype) for i, (n, w) in enumerate(((Tq, h * d), (T, d), (T, d))))
+    assert np.abs(V).max() < 5
+    for q, v in ((Q, V * np.float32(2.0 ** 108)), (Q * np.float32(2.0 ** -12), V * np.float32(2.0 ** 116))):
+        cache, held = _written(layer, K, v, dtype, bits)
+        got = to_host(layer.decode_quant(to_device(q, dtype), cache, base._ints([T])))
+        O, A, S = qc.decode(q, *held, h, [T])
+        base._check(got, O, A, S, dtype, "values near the top")

@@ -640,9 +640,10 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB,
             for (int u = 0; u < GL; ++u)
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
+                    // (one factor after the other: vs goes down to 2^-126, and their product past fp32's range)
                     *reinterpret_cast<float2*>(row + u * kQuantGroup + 8 * gid + 2 * c) =
-                        make_float2(fmaf(o[nt][u][c][e], inv / unit<BITS, TERMS>(0), om[nt][u][e]),
-                                    fmaf(o[nt][u][c][e + 2], inv / unit<BITS, TERMS>(1), om[nt][u][e]));
+                        make_float2(fmaf(o[nt][u][c][e] * (1.f / unit<BITS, TERMS>(0)), inv, om[nt][u][e]),
+                                    fmaf(o[nt][u][c][e + 2] * (1.f / unit<BITS, TERMS>(1)), inv, om[nt][u][e]));
             if (gid == 0 && first == 0) *reinterpret_cast<float2*>(row + D) = make_float2(m[nt][e] == kNone ? kNone : m[nt][e] * rs[nt][e], l[nt][e]);
         }
     if (s.cluster > 1) cluster_wait();

@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(QR_THREADS, 1)
                 for (int u = 0; u < G; ++u) om[u] += other[1 + u];
                 // every key and value tile is used: the rows meet there, to be written as rows
                 float* row = reinterpret_cast<float*>(sm + C::K) + r * C::OUT;
-                const float inv = z.whole() ? 1.f / l : 1.f;
+                const float inv = z.whole() ? 1.f / l : 1.f, back = 1.f / vs;  // (vs goes down to 2^-126: 2^24 / vs may be infinite)
                 if (half == 0) row[0] = m, row[1] = l;
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(QR_THREADS, 1)
                     for (int e = 0; e < 32; e += 8)
 #pragma unroll
                         for (int p = 0; p < 8; ++p)
-                            row[2 + col + e + channel_of<BITS>(p)] = inv * fmaf(__uint_as_float(o[e + p]), 1.f / unit_of<BITS>(p) / vs, z0);
+                            row[2 + col + e + channel_of<BITS>(p)] = inv * fmaf(__uint_as_float(o[e + p]) * (1.f / unit_of<BITS>(p)), back, z0);
                 }
             }
         }
