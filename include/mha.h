@@ -479,7 +479,8 @@ mha_status mha_cache_evict(mha_t handle, int B, int T_max, int keep, int recent,
  *   code  (x - m) / s rounded to the nearest whole number, ties to even; it stands for s code + m
  * which is within s / 2 of x.  The codes are those of the real numbers: they do not depend on the machine's
  * rounding.  A group with a value that is not finite in bf16 (NaN, infinite, or an fp32 value above 3.39e38) holds
- * NaN and reads back as NaN; a decode step over a length that includes such a token may give NaN in every row.
+ * NaN and reads back as NaN.  In a decode step every row that sees such a token is NaN (a value's: in that group's
+ * channels), and a row of the same batch that does not see it yet may be.
  *
  * A cache is one device buffer of mha_quant_cache_size bytes, 256-byte aligned, with four parts at the byte offsets
  * that call gives, each row-major: key codes (B, h_kv, T_max, row bytes), key parameters (B, h_kv, T_max, groups, 2)

@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(1024)
                 const int i = min(i0 + k * slices, n - 1);
                 const float* a = (i == 0 ? first : others + i * stride) + r * s.record();
                 m[k] = i0 + k * slices < n ? __ldcg(a) : -INFINITY;
-                sum[k] = __ldcg(a + 1);
+                sum[k] = i0 + k * slices < n ? __ldcg(a + 1) : 0.f;
                 v[k] = e < s.dv ? __ldcg(a + 2 + e) : 0.f;
             }
 #pragma unroll
@@ -283,8 +283,8 @@ __global__ void __launch_bounds__(1024)
             M = top;
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                if (m[k] != -INFINITY) {
-                    const float fk = exp2f(m[k] - M);
+                if (sum[k] != 0.f) {  // (had something; one of NaN alone has no maximum, but a sum of NaN)
+                    const float fk = m[k] == -INFINITY ? 0.f : exp2f(m[k] - M);
                     l = fmaf(fk, sum[k], l);
                     x = fmaf(fk, v[k], x);
                 }

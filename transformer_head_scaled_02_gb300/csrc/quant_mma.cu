@@ -675,13 +675,13 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB,
                 const int from = min(k, s.cluster - 1);
                 const float2 ml = *reinterpret_cast<const float2*>(mine + (to.sums(from, r) - to.base));
                 m[k] = k < s.cluster ? ml.x : kNone;
-                l[k] = ml.y;
+                l[k] = k < s.cluster ? ml.y : 0.f;
                 v[k] = *reinterpret_cast<const float*>(mine + (to.value(from, r, c) - to.base));
                 M = fmaxf(M, m[k]);
             }
 #pragma unroll
             for (int k = 0; k < kQuantCluster; ++k)
-                if (m[k] != kNone) {
+                if (l[k] != 0.f) {  // (had something; a piece of NaN alone has no maximum, but a sum of NaN)
                     const float f = exp2f(m[k] - M);
                     sum = fmaf(f, l[k], sum);
                     x = fmaf(f, v[k], x);
