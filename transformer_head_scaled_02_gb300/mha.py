@@ -557,10 +557,10 @@ class Mha:
     def _quant_ready(self, cache: "QuantCache", X: torch.Tensor, Y: torch.Tensor, lengths: torch.Tensor,
                      counts: Optional[torch.Tensor], need: int) -> int:
         """All on the cache's device, the current one, and `need` bytes of workspace there; returns its stream."""
-        dev = cache.device
+        dev = cache._data.get_device()
         if dev < 0 or X.get_device() != dev or Y.get_device() != dev or lengths.get_device() != dev or \
                 (counts is not None and counts.get_device() != dev) or _current_device() != dev:
-            self._device(cache.data, X, Y, lengths, counts)  # says what is wrong
+            self._device(cache._data, X, Y, lengths, counts)  # says what is wrong
         stream = _current_stream(dev)
         if need > self._ws_bytes or stream not in self._ws_streams or _capturing():
             self.ensure_workspace(0, 0, 0, need=need)
@@ -574,12 +574,13 @@ class Mha:
         become tokens L_b - n_b .. L_b - 1."""
         lens = self._quant_ints(cache, "cache_lengths", cache_lengths)
         n = None if counts is None else self._quant_ints(cache, "counts", counts)
-        bits, B, T_max, ptr = cache.args
+        B, T_max, bits = cache.sizes
         T = K.shape[1]
         ldk = self._rows("K", K, B, T, self._wk)
         ldv = self._rows("V", V, B, T, self._wv)
         stream = self._quant_ready(cache, K, V, cache_lengths, counts, 256)  # the status word
-        code = self._c_quant[0](self.handle, bits, B, T_max, ptr, T, K.data_ptr(), ldk, V.data_ptr(), ldv, lens, n, stream)
+        code = self._c_quant[0](self.handle, bits, B, T_max, cache._data.data_ptr(), T, K.data_ptr(), ldk, V.data_ptr(), ldv,
+                                lens, n, stream)
         if code:
             raise _lib.MhaError("mha_quant_write", code)
         return cache
@@ -593,19 +594,19 @@ class Mha:
         counts=cache_lengths reads whole sequences.  Returns (K_out, V_out)."""
         lens = self._quant_ints(cache, "cache_lengths", cache_lengths)
         n = None if counts is None else self._quant_ints(cache, "counts", counts)
-        bits, B, T_max, ptr = cache.args
+        B, T_max, bits = cache.sizes
         wk, wv = self._wk, self._wv
         if T_out is None:
             T_out = K_out.shape[1] if K_out is not None else V_out.shape[1] if V_out is not None else cache.T_max
         if K_out is None:
-            K_out = torch.empty((B, T_out, wk), dtype=self.dtype, device=cache.data.device)
+            K_out = torch.empty((B, T_out, wk), dtype=self.dtype, device=cache._data.device)
         if V_out is None:
-            V_out = torch.empty((B, T_out, wv), dtype=self.dtype, device=cache.data.device)
+            V_out = torch.empty((B, T_out, wv), dtype=self.dtype, device=cache._data.device)
         ldk = self._rows("K_out", K_out, B, T_out, wk)
         ldv = self._rows("V_out", V_out, B, T_out, wv)
         stream = self._quant_ready(cache, K_out, V_out, cache_lengths, counts, 256)  # the status word
-        code = self._c_quant[1](self.handle, bits, B, T_max, ptr, T_out, K_out.data_ptr(), ldk, V_out.data_ptr(), ldv, lens,
-                                n, stream)
+        code = self._c_quant[1](self.handle, bits, B, T_max, cache._data.data_ptr(), T_out, K_out.data_ptr(), ldk,
+                                V_out.data_ptr(), ldv, lens, n, stream)
         if code:
             raise _lib.MhaError("mha_quant_read", code)
         return K_out, V_out
@@ -614,7 +615,7 @@ class Mha:
                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """decode() over a quantised cache: the keys and values are those that the codes stand for."""
         lens = self._quant_ints(cache, "cache_lengths", cache_lengths)
-        bits, B, T_max, ptr = cache.args
+        B, T_max, bits = cache.sizes
         T_q = Q.shape[1]
         ldq = self._rows("Q", Q, B, T_q, self._wq)
         if out is None:
@@ -625,7 +626,8 @@ class Mha:
         if need is None:
             need = self._step_need_put(sizes, _lib.mha_decode_quant_workspace_size(self.handle, *sizes))
         stream = self._quant_ready(cache, Q, out, cache_lengths, None, need)
-        code = self._c_quant[2](self.handle, bits, B, T_q, T_max, Q.data_ptr(), ldq, ptr, lens, out.data_ptr(), ldo, stream)
+        code = self._c_quant[2](self.handle, bits, B, T_q, T_max, Q.data_ptr(), ldq, cache._data.data_ptr(), lens,
+                                out.data_ptr(), ldo, stream)
         if code:
             raise _lib.MhaError("mha_decode_quant", code)
         return out
@@ -636,7 +638,7 @@ class QuantCache:
     are views of it.  K_codes, V_codes (B, h_kv, T_max, row bytes) uint8 hold the codes (4 bits: channel 2i in the
     low half of byte i; rows padded to 32 channels), K_params, V_params (B, h_kv, T_max, groups, 2) bf16 the step s
     and lowest value m of each group of 64 channels: a code c stands for s c + m.  Buffers of any origin will do:
-    fill the views and decode."""
+    fill the views and decode.  copy.deepcopy gives a cache of its own (a sequence that forks)."""
 
     def __init__(self, layer: Mha, B: int, T_max: int, bits: int = 4):
         if bits not in (4, 8):
@@ -644,18 +646,39 @@ class QuantCache:
         layer._int32("B", B, 0)
         layer._int32("T_max", T_max, 0)
         T_max = layer._int32("T_max", (T_max + 15) // 16 * 16, 0)
-        nbytes, off = _lib.mha_quant_cache_size(layer.handle, bits, B, T_max)
+        nbytes, self._off = _lib.mha_quant_cache_size(layer.handle, bits, B, T_max)
         if nbytes == 0 and B * T_max > 0:
             raise ValueError(f"no cache of {B} x {T_max} tokens: sizes out of range")
-        self.B, self.T_max, self.bits = B, T_max, bits
+        self.B, self.T_max, self.bits = self.sizes = B, T_max, bits
         self.heads = (layer.h_kv, layer.d_k, layer.d_v)
         self.lens = (B,)  # shape of lengths and counts
-        self.data = torch.empty(nbytes, dtype=torch.uint8, device=layer.device)
-        self.device = self.data.get_device()
-        self.args = (bits, B, T_max, self.data.data_ptr())  # of every C call
-        views = []
-        for d, c, p in ((layer.d_k, off[0], off[1]), (layer.d_v, off[2], off[3])):
-            row, groups, n = (d + 31) // 32 * 4 * bits, (d + 63) // 64, B * layer.h_kv * T_max
-            views.append(self.data[c:c + n * row].view(B, layer.h_kv, T_max, row))
-            views.append(self.data[p:p + n * groups * 4].view(torch.bfloat16).view(B, layer.h_kv, T_max, groups, 2))
-        self.K_codes, self.K_params, self.V_codes, self.V_params = views
+        # The buffer alone is kept: its address and the views are taken from it anew, so that they are a copy's own.
+        self._data = torch.empty(nbytes, dtype=torch.uint8, device=layer.device)
+
+    @property
+    def data(self) -> torch.Tensor:
+        return self._data
+
+    def _codes(self, d: int, at: int) -> torch.Tensor:
+        row, n = (d + 31) // 32 * 4 * self.bits, self.B * self.heads[0] * self.T_max
+        return self._data[at:at + n * row].view(self.B, self.heads[0], self.T_max, row)
+
+    def _params(self, d: int, at: int) -> torch.Tensor:
+        groups, n = (d + 63) // 64, self.B * self.heads[0] * self.T_max
+        return self._data[at:at + n * groups * 4].view(torch.bfloat16).view(self.B, self.heads[0], self.T_max, groups, 2)
+
+    @property
+    def K_codes(self) -> torch.Tensor:
+        return self._codes(self.heads[1], self._off[0])
+
+    @property
+    def K_params(self) -> torch.Tensor:
+        return self._params(self.heads[1], self._off[1])
+
+    @property
+    def V_codes(self) -> torch.Tensor:
+        return self._codes(self.heads[2], self._off[2])
+
+    @property
+    def V_params(self) -> torch.Tensor:
+        return self._params(self.heads[2], self._off[3])
