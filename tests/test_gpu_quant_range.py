@@ -59,3 +59,35 @@ def test_decode_values_near_the_top(dtype, d, h, Tq, bits):
         got = to_host(layer.decode_quant(to_device(q, dtype), cache, base._ints([T])))
         O, A, S = qc.decode(q, *held, h, [T])
         base._check(got, O, A, S, dtype, "values near the top")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode_references_that_move_slowly(dtype):
+    """Two heads of one cached head: the first one's scores rise by 9 powers of two of a weight with each quantum, so that
+    its reference always moves, and the second one's by 0.9, so that its first tokens, of values 2^30 times the others',
+    fade slowly.  The last tokens' values count in full."""
+    d, h, B, T, bits = 128, 2, 300, 8192, 8          # (a CTA has a sequence to itself, or nearly)
+    layer = base._layer(dtype, h, d, 1)
+    V = np.exp(1.5 * wl.random_tensor((1, T, d), 5, dtype))  # (most codes low)
+    V[0, :128] *= 2.0 ** 30
+    V = _round(V, dtype)
+    one, _ = _written(layer, np.zeros((1, T, d), np.float32), V, dtype, bits)
+    # keys: 9 j in channel 0, j in channel 64, j the quantum
+    one.K_codes.zero_()
+    one.K_codes[..., 0], one.K_codes[..., 64] = 9, 1
+    one.K_params.zero_()
+    one.K_params[..., 0] = (torch.arange(T, device="cuda") // 128)[:, None]
+    held = base._held(one, "K") + base._held(one, "V")
+    Q = np.zeros((1, 1, h * d), np.float32)
+    Q[..., 0] = np.sqrt(d) / np.log2(np.e)
+    Q[..., d + 64] = 0.9 * Q[..., 0]
+    Q = _round(Q, dtype)
+    cache = layer.quant_cache(B, T, bits)
+    for to, x in ((cache.K_codes, one.K_codes), (cache.K_params, one.K_params), (cache.V_codes, one.V_codes),
+                  (cache.V_params, one.V_params)):
+        to.copy_(x.expand_as(to))
+    got = to_host(layer.decode_quant(to_device(np.repeat(Q, B, 0), dtype), cache, base._ints([T] * B)))
+    O, A, S = qc.decode(Q, *held, h, [T])
+    bound = base._bound(Q, held, h, d, bits, O, A, S, dtype)
+    assert np.isfinite(got).all()
+    assert (np.abs(got - O) <= bound).all(), (np.abs(got - O) / (A + S)).max((0, 1))

@@ -17,13 +17,14 @@ __device__ __forceinline__ int quant_exponent(float x) { return (int)(__float_as
 // A row's weights times steps, p s, are rounded to fp16 as p s vs, vs a power of two.  They fit while a step times vs is at
 // most this, as a weight is at most 2^8 (a larger one moves the row's reference); what does not, or moves it, asks for
 // the new vs where the largest p s of the tokens at hand is `need` and the row's sums so far are about to be multiplied
-// by f <= 1: to [4, 8) downwards if it is above 16, and upwards, as far as f makes room for it, if it is below 1/4.
+// by f <= 1: to [4, 8) downwards if it is above 16, and upwards, by `room` powers of two at most, if it is below 1/4.
 // (Steps differ by tokens: with [32, 64) a third of quant_rows.cu's tiles had to ask.)
 constexpr float kQuantStepMost = 255.f;
-__device__ __forceinline__ float quant_move_scale(float vs, float need, float f) {
+__device__ __forceinline__ bool quant_scale_rises(float vs, float need, float f) { return need * vs < 0.25f && f < 1.f; }
+__device__ __forceinline__ float quant_move_scale(float vs, float need, float f, int room) {
     const float x = need * vs;
-    if (x > 16.f || (x < 0.25f && f < 1.f)) {
-        const int now = quant_exponent(vs), most = x > 16.f ? now : max(now, min(100, now - 1 - quant_exponent(f)));
+    if (x > 16.f || quant_scale_rises(vs, need, f)) {
+        const int now = quant_exponent(vs), most = x > 16.f ? now : max(now, min(100, now + room));
         vs = quant_power2(max(-126, min(most, 2 - quant_exponent(need))));
     }
     return vs;

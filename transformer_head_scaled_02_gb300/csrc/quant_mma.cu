@@ -518,7 +518,20 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB,
                                            step1 * ex2_approx((y[nt][e + 2] - m[nt][e]) * rs[nt][e]));
 #pragma unroll
                         for (int w = 16; w >= 4; w >>= 1) need = fmaxf(need, __shfl_xor_sync(0xffffffffu, need, w));
-                        const float to = quant_move_scale(vs[nt][e], need, f[nt][e]);
+                        // Upwards as far as the sums leave fp32 room.  (The room that f makes is not enough: one column's
+                        // reference moves whenever another's does, and rounded down to powers of two many small f make none.)
+                        int room = 0;
+                        if (__any_sync(0xffffffffu, quant_scale_rises(vs[nt][e], need, f[nt][e]))) {
+                            float most = 0.f;
+#pragma unroll
+                            for (int u = 0; u < GL; ++u)
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) most = fmax3(most, fabsf(o[nt][u][c][e]), fabsf(o[nt][u][c][e + 2]));
+#pragma unroll
+                            for (int w = 16; w >= 4; w >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, w));
+                            room = min(100, 38 - quant_exponent(most));
+                        }
+                        const float to = quant_move_scale(vs[nt][e], need, f[nt][e], room);
                         fr[nt][e] = quant_rescale(to, vs[nt][e], f[nt][e]);
                         vs[nt][e] = to;
                         seen += l[nt][e];
