@@ -91,3 +91,25 @@ def test_decode_references_that_move_slowly(dtype):
     bound = base._bound(Q, held, h, d, bits, O, A, S, dtype)
     assert np.isfinite(got).all()
     assert (np.abs(got - O) <= bound).all(), (np.abs(got - O) / (A + S)).max((0, 1))
+
+
+@pytest.mark.parametrize("dtype,d,h,Tq", [("bf16", 64, 1, 1), ("bf16", 128, 8, 1), ("bf16", 64, 16, 1), ("bf16", 128, 2, 128),
+                                          ("f32", 64, 1, 1), ("f32", 70, 1, 1)])
+def test_decode_scores_a_step_of_fp32_apart(dtype, d, h, Tq):
+    """Scores so large that fp32 holds them in steps of 4 to 16 powers of two of a weight, each quantum's a step above the
+    last one's, over values that grow: outputs are means of the values, whatever the weights' rounding."""
+    B, T, bits = 8, 4096, 8
+    layer = base._layer(dtype, h, d, 1)
+    j = np.arange(T) // 128
+    V = _round(wl.random_tensor((1, T, d), 5, dtype) * 2.0 ** (4 * (j % 4)[None, :, None]), dtype)
+    K = np.zeros((1, T, d), np.float32)
+    K[0, :, 0], K[0, :, 1] = 255, j                            # codes of a step of 1
+    cache, held = _written(layer, np.repeat(K, B, 0), np.repeat(V, B, 0), dtype, bits)
+    assert (held[1][..., 0, 0] == 1).all()
+    for power in np.arange(25.0, 29.01, 0.25):                 # of the log2 of a weight
+        Q = np.zeros((1, Tq, h * d), np.float32)
+        Q[..., 0::d] = 2.0 ** power * np.sqrt(d) / np.log2(np.e) / 255
+        Q[..., 1::d] = Q[..., 0::d] * 255 * 2.0 ** -23
+        got = to_host(layer.decode_quant(to_device(np.repeat(_round(Q, dtype), B, 0), dtype), cache, base._ints([T] * B)))
+        assert np.isfinite(got).all(), power
+        assert np.abs(got).max() <= np.abs(qc.values(*held[2:])).max() * (1 + 2.0 ** -7), power

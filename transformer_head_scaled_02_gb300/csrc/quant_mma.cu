@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB,
                         if (top > m[nt][e]) {
                             f[nt][e] = ex2_approx((m[nt][e] - top) * rs[nt][e]);
                             m[nt][e] = top;
-                            far[nt][e] = top + __fdividef(8.f, rs[nt][e]);
+                            far[nt][e] = __fadd_rd(top, __fdividef(8.f, rs[nt][e]));  // (rounded up, weights could be 2^16)
                         }
                         // the column's largest p s
                         float need = fmaxf(step0 * ex2_approx((y[nt][e] - m[nt][e]) * rs[nt][e]),

@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(QR_THREADS, 1)
                     mine[half * QR_ROWS + r] = top;
                     if (!meet()) break;
                     top = fmaxf(top, mine[(1 - half) * QR_ROWS + r]);
-                    if (top > m + 8.f) {
+                    if (top - m > 8.f) {  // (m + 8, rounded, could be 2^16 in a weight)
                         alpha = ex2_approx(m - top);
                         m = top;
                         moved = true;
