@@ -113,3 +113,18 @@ def test_decode_scores_a_step_of_fp32_apart(dtype, d, h, Tq):
         got = to_host(layer.decode_quant(to_device(np.repeat(_round(Q, dtype), B, 0), dtype), cache, base._ints([T] * B)))
         assert np.isfinite(got).all(), power
         assert np.abs(got).max() <= np.abs(qc.values(*held[2:])).max() * (1 + 2.0 ** -7), power
+
+
+@pytest.mark.parametrize("dtype,d,h,Tq", ROWS)
+@pytest.mark.parametrize("bits", [4, 8])
+def test_decode_small_queries_and_values(dtype, d, h, Tq, bits):
+    """Queries of 2^-95 and 2^-113 under keys as large as that makes ordinary scores, and values of 2^-112: no bits are lost."""
+    T = 300
+    layer = base._layer(dtype, h, d, 1)
+    Q, K, V = (wl.random_tensor((1, n, w), 30 + i, dtype) for i, (n, w) in enumerate(((Tq, h * d), (T, d), (T, d))))
+    for qk, v in ((-95, 0), (-113, 0), (0, -112)):
+        q, k, v = (x * np.float32(2.0 ** p) for x, p in ((Q, qk), (K, -qk), (V, v)))
+        cache, held = _written(layer, k, v, dtype, bits)
+        got = to_host(layer.decode_quant(to_device(q, dtype), cache, base._ints([T])))
+        O, A, S = qc.decode(q, *held, h, [T])
+        base._check(got, O, A, S, dtype, f"2^{qk}")

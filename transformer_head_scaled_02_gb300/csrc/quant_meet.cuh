@@ -20,11 +20,12 @@ __device__ __forceinline__ int quant_exponent(float x) { return (int)(__float_as
 // by f <= 1: to [4, 8) downwards if it is above 16, and upwards, by `room` powers of two at most, if it is below 1/4.
 // (Steps differ by tokens: with [32, 64) a third of quant_rows.cu's tiles had to ask.)
 constexpr float kQuantStepMost = 255.f;
+constexpr int kQuantScaleMost = 118;  // log2 of the largest vs: weights of 2^8 times it stay below 2^127
 __device__ __forceinline__ bool quant_scale_rises(float vs, float need, float f) { return need * vs < 0.25f && f < 1.f; }
 __device__ __forceinline__ float quant_move_scale(float vs, float need, float f, int room) {
     const float x = need * vs;
     if (x > 16.f || quant_scale_rises(vs, need, f)) {
-        const int now = quant_exponent(vs), most = x > 16.f ? now : max(now, min(100, now + room));
+        const int now = quant_exponent(vs), most = x > 16.f ? now : max(now, min(kQuantScaleMost, now + room));
         vs = quant_power2(max(-126, min(most, 2 - quant_exponent(need))));
     }
     return vs;

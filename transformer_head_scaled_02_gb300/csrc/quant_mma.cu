@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB,
 #pragma unroll
             for (int w = 16; w >= 1; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
             // the largest element to [2^13, 2^14); zero, infinite, tiny and huge (2^118) rows as far as powers of two go
-            const int e2 = top > 0.f && top < INFINITY ? max(-104, min(100, 13 - quant_exponent(top))) : 0;
+            const int e2 = top > 0.f && top < INFINITY ? max(-104, min(126, 13 - quant_exponent(top))) : 0;
             const float f = quant_power2(e2);
             const int u = G == 1 ? 0 : lane / 16;
             float sum = 0.f;
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB,
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             m[nt][e] = far[nt][e] = kNone;
-            vs[nt][e] = quant_power2(100);
+            vs[nt][e] = quant_power2(kQuantScaleMost);
             l[nt][e] = 0.f;
 #pragma unroll
             for (int u = 0; u < GL; ++u) {

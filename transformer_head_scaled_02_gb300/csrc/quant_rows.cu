@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(QR_THREADS, 1)
 #pragma unroll
                 for (int o = 4; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(lanes, top, o));
                 // the largest element to [2^13, 2^14); zero, infinite, tiny and huge (2^118) rows as far as powers of two go
-                const int e2 = top > 0.f && top < INFINITY ? max(-104, min(100, 13 - quant_exponent(top))) : 0;
+                const int e2 = top > 0.f && top < INFINITY ? max(-104, min(126, 13 - quant_exponent(top))) : 0;
                 const float f = quant_power2(e2);
                 float sum[G];
 #pragma unroll
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(QR_THREADS, 1)
                 ++meets;
                 return fine;
             };
-            float qs[G], om[G], m = kRowsNone, l = 0.f, vs = quant_power2(100);
+            float qs[G], om[G], m = kRowsNone, l = 0.f, vs = quant_power2(kQuantScaleMost);
 #pragma unroll
             for (int u = 0; u < G; ++u) qs[u] = qv[u], om[u] = 0.f;
             const float rs = qv[G];
