@@ -128,3 +128,24 @@ def test_decode_small_queries_and_values(dtype, d, h, Tq, bits):
         got = to_host(layer.decode_quant(to_device(q, dtype), cache, base._ints([T])))
         O, A, S = qc.decode(q, *held, h, [T])
         base._check(got, O, A, S, dtype, f"2^{qk}")
+
+
+def test_write_borders_of_the_widest_ranges():
+    """A range beyond fp32's largest number, and values of the smallest one on either side of a border between two codes."""
+    s = 1.25 * 2.0 ** 124
+    tiny = 2.0 ** -149
+    rows = []
+    for k in (6, 7):
+        x = np.zeros(64, np.float32)
+        x[:6] = -(k + 0.5) * s, (14.5 - k) * s, -tiny, tiny, 3 * tiny, -3 * tiny
+        rows.append(x)
+    x = np.stack(rows)
+    layer = base._layer("f32", 1, 64, 1)
+    cache = layer.quant_cache(1, len(x), 4)
+    t = to_device(x[None], "f32")
+    layer.quant_write(cache, t, t, base._ints([len(x)]))
+    codes, params = base._held(cache, "K")
+    for i in range(len(x)):
+        c, step, low = qc.quantise_exact(x[i], 4)
+        assert params[0, 0, i, 0, 0] == step and params[0, 0, i, 0, 1] == low
+        assert (codes[0, 0, i] == c).all(), (i, codes[0, 0, i][:8], c[:8])

@@ -270,7 +270,7 @@ __device__ __forceinline__ void eight_codes(const E& in, int n, float m, float s
     if (!(inv > 0.f)) {  // NaN, or in halves, which changes no code
         inv = -inv;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= 0.5f;
+        for (int i = 0; i < 8; ++i) x[i] = x[i] * 0.5f != 0.f ? x[i] * 0.5f : x[i];  // (the smallest number keeps its side of 0)
     }
     if constexpr (!E::kWhole)
 #pragma unroll
