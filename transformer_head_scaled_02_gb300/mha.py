@@ -590,8 +590,11 @@ class Mha:
                    V_out: Optional[torch.Tensor] = None):
         """The values that each sequence's last n_b tokens (counts; default: T_out of them) stand for, in rows
         0 .. n_b - 1 of K_out (B, T_out, h_kv*d_k view) and V_out (B, T_out, h_kv*d_v view); rows past n_b of
-        given outputs stay, of new ones are unset.  T_out defaults to the cache's T_max or the given outputs' rows.
-        counts=cache_lengths reads whole sequences.  Returns (K_out, V_out)."""
+        given outputs stay, of new ones are unset.  T_out defaults to the given outputs' rows; with neither counts,
+        T_out nor outputs, or with counts=cache_lengths, whole sequences are read, into T_max rows.  Returns
+        (K_out, V_out)."""
+        if counts is None and T_out is None and K_out is None and V_out is None:
+            counts = cache_lengths
         lens = self._quant_ints(cache, "cache_lengths", cache_lengths)
         n = None if counts is None else self._quant_ints(cache, "counts", counts)
         B, T_max, bits = cache.sizes
