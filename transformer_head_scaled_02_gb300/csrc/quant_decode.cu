@@ -25,9 +25,6 @@ constexpr int QD_THREADS = 256;
 constexpr int QD_WARPS = QD_THREADS / 32;
 constexpr int QD_ROWS = 4;
 
-__device__ __forceinline__ float elem(const float* p) { return *p; }
-__device__ __forceinline__ float elem(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-
 // Eight codes of a row as fp32.
 template <int BITS>
 __device__ __forceinline__ void codes8(const uint8_t* p, float (&x)[8]) {
@@ -44,9 +41,8 @@ __device__ __forceinline__ void codes8(const uint8_t* p, float (&x)[8]) {
 
 // The warps' results of a piece meet, as quant_meet() of quant_meet.cuh has it for known sizes: [warp][row] of `stride`
 // floats, dv values, at ml m and l.
-template <typename T>
 __device__ __forceinline__ void meet_any(const QuantStep& s, bool whole, float* rec, float* res, int stride, int ml, int b, int g,
-                                         int r0, int nr, T* O, int64_t ldo) {
+                                         int r0, int nr, float* O, int64_t ldo) {
     constexpr int ENTRIES = QD_WARPS, THREADS = QD_THREADS, rows = QD_ROWS;
     const int tid = (int)threadIdx.x, dv = s.dv, record = s.record();
     for (int r = tid / ENTRIES; r < nr; r += THREADS / ENTRIES) {
@@ -83,10 +79,10 @@ __device__ __forceinline__ void meet_any(const QuantStep& s, bool whole, float* 
 }
 
 // dynamic shared memory: q[R][dpk], its sums qs[R][groups], and per warp p[R][32] or at the end m, l, o[dpv] per row
-template <typename T, int BITS>
+template <int BITS>
 __global__ void __launch_bounds__(QD_THREADS)
-    quant_decode_kernel(const QuantStep s, const QuantPlane pk, const QuantPlane pv, const T* __restrict__ Q, int64_t ldq,
-                        T* __restrict__ O, int64_t ldo, const int32_t* __restrict__ lengths, float scale_log2,
+    quant_decode_kernel(const QuantStep s, const QuantPlane pk, const QuantPlane pv, const float* __restrict__ Q, int64_t ldq,
+                        float* __restrict__ O, int64_t ldo, const int32_t* __restrict__ lengths, float scale_log2,
                         float* __restrict__ part, int* status) {
     constexpr int R = QD_ROWS;
     extern __shared__ float sm[];
@@ -109,7 +105,7 @@ __global__ void __launch_bounds__(QD_THREADS)
         __syncthreads();  // the piece before is written
         for (int e = tid; e < R * dpk; e += QD_THREADS) {
             const int r = e / dpk, c = e - r * dpk, rr = r0 + min(r, nr - 1);
-            q[e] = c < pk.d ? scale_log2 * elem(Q + ((int64_t)b * s.T_q + rr % s.T_q) * ldq + (int64_t)(g * s.per + rr / s.T_q) * pk.d + c) : 0.f;
+            q[e] = c < pk.d ? scale_log2 * Q[((int64_t)b * s.T_q + rr % s.T_q) * ldq + (int64_t)(g * s.per + rr / s.T_q) * pk.d + c] : 0.f;
         }
         __syncthreads();
         for (int e = tid; e < R * pk.groups; e += QD_THREADS) {
@@ -400,36 +396,36 @@ bool quant_step_fits(const QuantStep& s) {
 cudaError_t launch_quant_decode(const QuantStep& s, bool f32, int bits, const QuantPlane& pk, const QuantPlane& pv,
                                 const void* Q, int64_t ldq, void* O, int64_t ldo, const int32_t* lengths, float* part,
                                 int* status, cudaStream_t stream) {
-    const float scale = (float)(1.4426950408889634 / sqrt((double)pk.d));
-    auto go = [&](auto* x, auto kernel) {
-        using T = std::remove_pointer_t<decltype(x)>;
-        cudaError_t err;
-        if (s.rb == kManyRowsBlock) {
-            err = launch_quant_rows(s, bits, pk, pv, Q, ldq, O, ldo, lengths, part, status, stream);
-        } else if (quant_mma_serves(pk.d, pv.d)) {
-            err = launch_quant_mma(s, f32, bits, pk, pv, Q, ldq, O, ldo, lengths, part, status, stream);
-        } else {
-            err = launch_pdl(kernel, dim3((unsigned)s.ctas), dim3(QD_THREADS), qd_smem(pk, pv), stream, s, pk, pv,
-                             static_cast<const T*>(Q), ldq, static_cast<T*>(O), ldo, lengths, scale, part, status);
-        }
-        if (err != cudaSuccess || (s.cluster ? s.parts == 1 : s.T_max <= s.quantum)) return err;  // (groups of one quantum are never shared)
-        // slices: as many as leave each about eight records of an evenly cut step; rows of a block: one, more if there
-        // are more rows than some blocks an SM
-        const int64_t groups = (int64_t)s.B * s.lanes(), n = s.cluster ? s.parts : s.ctas / groups + 2;
-        const int width = s.dv <= 64 ? 64 : s.dv <= 128 ? 128 : 256;
-        int slices = 1;
-        while (slices * width < 1024 && n > 8 * slices) slices *= 2;
-        const int threads = slices * width > 256 ? slices * width : 256, most = s.rows < s.rb ? s.rows : s.rb;
-        int run = threads / (width * slices);
-        while (run < most && groups * ((most + run - 1) / run) > 1024) run *= 2;
-        const int chunks = (most + run - 1) / run;
+    cudaError_t err;
+    if (s.rb == kManyRowsBlock) {
+        err = launch_quant_rows(s, bits, pk, pv, Q, ldq, O, ldo, lengths, part, status, stream);
+    } else if (quant_mma_serves(pk.d, pv.d)) {
+        err = launch_quant_mma(s, f32, bits, pk, pv, Q, ldq, O, ldo, lengths, part, status, stream);
+    } else if (f32) {
+        const float scale = (float)(1.4426950408889634 / sqrt((double)pk.d));
+        err = launch_pdl(bits == 4 ? quant_decode_kernel<4> : quant_decode_kernel<8>, dim3((unsigned)s.ctas), dim3(QD_THREADS),
+                         qd_smem(pk, pv), stream, s, pk, pv, static_cast<const float*>(Q), ldq, static_cast<float*>(O), ldo, lengths,
+                         scale, part, status);
+    } else {
+        err = cudaErrorInvalidValue;  // bf16 layers have no other heads
+    }
+    if (err != cudaSuccess || (s.cluster ? s.parts == 1 : s.T_max <= s.quantum)) return err;  // (groups of one quantum are never shared)
+    // slices: as many as leave each about eight records of an evenly cut step; rows of a block: one, more if there
+    // are more rows than some blocks an SM
+    const int64_t groups = (int64_t)s.B * s.lanes(), n = s.cluster ? s.parts : s.ctas / groups + 2;
+    const int width = s.dv <= 64 ? 64 : s.dv <= 128 ? 128 : 256;
+    int slices = 1;
+    while (slices * width < 1024 && n > 8 * slices) slices *= 2;
+    const int threads = slices * width > 256 ? slices * width : 256, most = s.rows < s.rb ? s.rows : s.rb;
+    int run = threads / (width * slices);
+    while (run < most && groups * ((most + run - 1) / run) > 1024) run *= 2;
+    const int chunks = (most + run - 1) / run;
+    auto join = [&](auto* out) {
+        using T = std::remove_pointer_t<decltype(out)>;
         return launch_pdl(quant_join_kernel<T>, dim3((unsigned)(groups * chunks)), dim3((unsigned)threads), 0, stream, s,
-                          static_cast<const float*>(part), static_cast<T*>(O), ldo, lengths, width, slices, run, chunks);
+                          static_cast<const float*>(part), out, ldo, lengths, width, slices, run, chunks);
     };
-    if (f32) return bits == 4 ? go(static_cast<float*>(nullptr), quant_decode_kernel<float, 4>)
-                              : go(static_cast<float*>(nullptr), quant_decode_kernel<float, 8>);
-    return bits == 4 ? go(static_cast<__nv_bfloat16*>(nullptr), quant_decode_kernel<__nv_bfloat16, 4>)
-                     : go(static_cast<__nv_bfloat16*>(nullptr), quant_decode_kernel<__nv_bfloat16, 8>);
+    return f32 ? join(static_cast<float*>(O)) : join(static_cast<__nv_bfloat16*>(O));
 }
 
 }  // namespace mha
