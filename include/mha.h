@@ -532,10 +532,12 @@ size_t mha_decode_quant_workspace_size(mha_t handle, int B, int T_q, int T_max);
  * for mha_decode (an L_b outside [T_q, T_max] makes that batch's rows NaN and records MHA_ERR_BAD_LENGTH).  O must
  * not overlap an input.  Needs a workspace of mha_decode_quant_workspace_size(B, T_q, T_max) bytes.  One or two
  * launches; results do not depend on the order in which the GPU runs them.  Scores, sums and the lowest values' part
- * are fp32; weighted sums are held before the division, by weights of up to 2^8 each, so that outputs are finite as long
- * as the values a row sees, in magnitude, add up to less than 2^120.  The weights' products with the steps are rounded to 11 significant bits for bf16 layers, to 22 for fp32
- * ones with d_k == d_v <= 128 (queries likewise, bf16 ones exactly; elements of 2^118 and more overflow there), as far
- * as they are not below 2^-24 of a row's largest.  MHA_ERR_UNSUPPORTED where B * h_kv * ceil(h / h_kv * T_q / 4)
+ * are fp32; weighted sums are held before the division, by weights of up to 2^8 each, so that outputs are finite as
+ * long as the values a row sees, in magnitude, add up to less than 2^120.  Products of a weight and a step are held in
+ * fp16 (bf16 layers) or as two of them (fp32 layers with d_k == d_v <= 128) against a power of two that follows the
+ * row: each is off by at most 2^-11 (2^-22) of itself, and by 2^-23 of the row's largest besides.  Queries are held
+ * likewise: bf16 ones are off by at most 2^-34 of a row's largest element, fp32 ones by 2^-22 of themselves and 2^-38
+ * of that; elements of 2^118 and more overflow.  MHA_ERR_UNSUPPORTED where B * h_kv * ceil(h / h_kv * T_q / 4)
  * * ceil(T_max / 128) may exceed 2^31.
  */
 mha_status mha_decode_quant(mha_t handle, int bits, int B, int T_q, int T_max, const void* Q, int64_t ldq,

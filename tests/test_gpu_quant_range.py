@@ -149,3 +149,42 @@ def test_write_borders_of_the_widest_ranges():
         c, step, low = qc.quantise_exact(x[i], 4)
         assert params[0, 0, i, 0, 0] == step and params[0, 0, i, 0, 1] == low
         assert (codes[0, 0, i] == c).all(), (i, codes[0, 0, i][:8], c[:8])
+
+
+@pytest.mark.parametrize("dtype,d,Tq", [("bf16", 64, 1), ("bf16", 128, 3), ("bf16", 64, 256), ("f32", 64, 1), ("f32", 128, 2)])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("alike", [True, False])
+def test_decode_one_token_far_above_many(dtype, d, Tq, bits, alike):
+    """One token of nearly all the weight before thousands of equal small ones, down to 2^-24 of it each, whose values are
+    alike (so that their products with the steps are all rounded the same way) or not.  A product is off by 2^-11 (fp32:
+    2^-22) of itself and by 2^-23 of the row's largest besides; it meets a code (fp32: less half its range)."""
+    B, T = (300, 4096) if Tq < 100 else (3, 4096)     # (a CTA has a sequence to itself, or nearly; rows: some tiles each)
+    layer = base._layer(dtype, 1, d, 1)
+    V = wl.random_tensor((1, T, d), 5, dtype)
+    if alike:
+        V[0, 1:] = V[0, 1]
+    one, _ = _written(layer, np.zeros((1, T, d), np.float32), V, dtype, bits)
+    one.K_codes.zero_()
+    one.K_params.zero_()
+    one.K_codes[0, 0, 0, 0] = 1                       # (the first token's key: 1 in channel 0; the others': 0)
+    one.K_params[0, 0, 0, :, 0] = 1
+    held = base._held(one, "K") + base._held(one, "V")
+    cache = layer.quant_cache(B, T, bits)
+    for to, x in ((cache.K_codes, one.K_codes), (cache.K_params, one.K_params), (cache.V_codes, one.V_codes),
+                  (cache.V_params, one.V_params)):
+        to.copy_(x.expand_as(to))
+    step = np.repeat(held[3][0, 0, :, :, 0], 64, -1)[:, :d]
+    code = np.abs(held[2][0, 0] - (0 if dtype == "bf16" else 2 ** (bits - 1)))
+    for power in (8, 13, 16, 19, 21, 24):
+        Q = np.zeros((1, Tq, d), np.float32)
+        Q[..., 0] = power * np.sqrt(d) / np.log2(np.e)
+        Q = _round(Q, dtype)
+        got = to_host(layer.decode_quant(to_device(np.repeat(Q, B, 0), dtype), cache, base._ints([T] * B)))
+        O, A, S = qc.decode(Q, *held, 1, [T])
+        w = np.exp(Q[0, 0, 0] / np.sqrt(d) * (np.arange(T) == 0))
+        w /= w[:T - Tq + 1].sum()                     # (the first new token sees fewest)
+        part, most = (w[:, None] * step * code).sum(0), (w[:, None] * step).max()
+        # scores are one product, off by some 2^-23 of up to 17, and sums of fp32 numbers: 2e-5
+        bound = 2.0 ** -8 * np.abs(O) + 2.0 ** -11 * S if dtype == "bf16" else 2.0 ** -22 * part
+        bound = bound + 2.0 ** -23 * most * code.sum(0) + 2e-5 * (A + S)
+        assert (np.abs(got - O) <= bound).all(), (power, (np.abs(got - O) / bound).max())

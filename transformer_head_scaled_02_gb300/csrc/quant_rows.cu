@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(QR_THREADS, 1)
                         mine[half * QR_ROWS + r] = need;
                         if (!meet()) break;
                         need = fmaxf(need, mine[(1 - half) * QR_ROWS + r]);
-                        const float to = quant_move_scale(vs, need, alpha, -1 - quant_exponent(alpha));  // (the room that alpha <= 2^-8 makes)
+                        const float to = quant_move_scale(vs, need, alpha, -quant_exponent(alpha));  // (what alpha <= 2^-8 takes away, and less than one more)
                         back = quant_rescale(to, vs, alpha);
                         vs = to;
                     }
