@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(1024)
                 const int i = min(i0 + k * slices, n - 1);
                 const float* a = (i == 0 ? first : others + i * stride) + r * s.record();
                 m[k] = i0 + k * slices < n ? __ldcg(a) : -INFINITY;
-                sum[k] = i0 + k * slices < n ? __ldcg(a + 1) : 0.f;
+                sum[k] = __ldcg(a + 1);
                 v[k] = e < s.dv ? __ldcg(a + 2 + e) : 0.f;
             }
 #pragma unroll
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(1024)
             M = top;
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                if (sum[k] != 0.f) {  // (had something; one of NaN alone has no maximum, but a sum of NaN)
+                if (m[k] != -INFINITY || sum[k] != sum[k]) {  // (a record of NaN alone has no maximum, but a sum of NaN)
                     const float fk = m[k] == -INFINITY ? 0.f : exp2f(m[k] - M);
                     l = fmaf(fk, sum[k], l);
                     x = fmaf(fk, v[k], x);

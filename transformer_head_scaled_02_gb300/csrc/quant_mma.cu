@@ -494,7 +494,8 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB,
                 for (int e = 0; e < 2; ++e)
                     move = move || fmaxf(y[nt][e], y[nt][e + 2]) > far[nt][e] || steps * vs[nt][e] > kQuantStepMost;
             if (__any_sync(0xffffffffu, move)) {
-                float step0 = 0.f, step1 = 0.f, f[NT][2], fr[NT][2], seen = 0.f;
+                float step0 = 0.f, step1 = 0.f, f[NT][2], fr[NT][2], need[NT][2], seen = 0.f;
+                bool rises = false;
 #pragma unroll
                 for (int u = 0; u < GL; ++u) {
                     step0 = fmaxf(step0, quant_step(v0[u]));
@@ -514,14 +515,21 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB,
                             far[nt][e] = __fadd_rd(top, __fdividef(8.f, rs[nt][e]));  // (rounded up, weights could be 2^16)
                         }
                         // the column's largest p s
-                        float need = fmaxf(step0 * ex2_approx((y[nt][e] - m[nt][e]) * rs[nt][e]),
-                                           step1 * ex2_approx((y[nt][e + 2] - m[nt][e]) * rs[nt][e]));
+                        need[nt][e] = fmaxf(step0 * ex2_approx((y[nt][e] - m[nt][e]) * rs[nt][e]),
+                                            step1 * ex2_approx((y[nt][e + 2] - m[nt][e]) * rs[nt][e]));
 #pragma unroll
-                        for (int w = 16; w >= 4; w >>= 1) need = fmaxf(need, __shfl_xor_sync(0xffffffffu, need, w));
-                        // Upwards as far as the sums leave fp32 room.  (The room that f makes is not enough: one column's
-                        // reference moves whenever another's does, and rounded down to powers of two many small f make none.)
-                        int room = 0;
-                        if (__any_sync(0xffffffffu, quant_scale_rises(vs[nt][e], need, f[nt][e]))) {
+                        for (int w = 16; w >= 4; w >>= 1) need[nt][e] = fmaxf(need[nt][e], __shfl_xor_sync(0xffffffffu, need[nt][e], w));
+                        rises = rises || quant_scale_rises(vs[nt][e], need[nt][e], f[nt][e]);
+                        seen += l[nt][e];
+                    }
+                // A scale rises as far as the column's sums leave fp32 room.  (The room that f makes is not enough: one column's
+                // reference moves whenever another's does, and rounded down to powers of two many small f make none.)
+                int room[NT][2] = {};
+                if (__any_sync(0xffffffffu, rises)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
                             float most = 0.f;
 #pragma unroll
                             for (int u = 0; u < GL; ++u)
@@ -529,12 +537,16 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB,
                                 for (int c = 0; c < 4; ++c) most = fmax3(most, fabsf(o[nt][u][c][e]), fabsf(o[nt][u][c][e + 2]));
 #pragma unroll
                             for (int w = 16; w >= 4; w >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, w));
-                            room = min(100, 38 - quant_exponent(most));
+                            room[nt][e] = min(100, 38 - quant_exponent(most));
                         }
-                        const float to = quant_move_scale(vs[nt][e], need, f[nt][e], room);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float to = quant_move_scale(vs[nt][e], need[nt][e], f[nt][e], room[nt][e]);
                         fr[nt][e] = quant_rescale(to, vs[nt][e], f[nt][e]);
                         vs[nt][e] = to;
-                        seen += l[nt][e];
                     }
                 if (__any_sync(0xffffffffu, seen != 0.f)) {  // not at a warp's first tokens
 #pragma unroll
@@ -635,13 +647,31 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB,
         }
     }
 
-    // this warp's result: rows of D values, m, l
+    // this warp's result: rows of D values, m, l.  2^24 / vs takes the sums back; where it would be past fp32's range (steps
+    // of 2^104 and more), the sums are multiplied by its two factors one after the other.
+    float up = 1.f / unit<BITS, TERMS>(0);
+    {
+        bool tiny = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) tiny = tiny || fminf(vs[nt][0], vs[nt][1]) < 7.8886090522101181e-31f;  // 2^-100
+        if (__any_sync(0xffffffffu, tiny)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int u = 0; u < GL; ++u)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[nt][u][c][e] *= up;
+            up = 1.f;
+        }
+    }
     float* own = reinterpret_cast<float*>(smem + C::RES) + warp * C::RESULTS * C::REC;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const float inv = 1.f / vs[nt][e];
+            const float inv = up / vs[nt][e];
 #pragma unroll
             for (int w = 4; w <= 16; w <<= 1) {
                 l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], w);
@@ -653,10 +683,9 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB,
             for (int u = 0; u < GL; ++u)
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                    // (one factor after the other: vs goes down to 2^-126, and their product past fp32's range)
                     *reinterpret_cast<float2*>(row + u * kQuantGroup + 8 * gid + 2 * c) =
-                        make_float2(fmaf(o[nt][u][c][e] * (1.f / unit<BITS, TERMS>(0)), inv, om[nt][u][e]),
-                                    fmaf(o[nt][u][c][e + 2] * (1.f / unit<BITS, TERMS>(1)), inv, om[nt][u][e]));
+                        make_float2(fmaf(o[nt][u][c][e], inv, om[nt][u][e]),
+                                    fmaf(o[nt][u][c][e + 2], inv * (unit<BITS, TERMS>(0) / unit<BITS, TERMS>(1)), om[nt][u][e]));
             if (gid == 0 && first == 0) *reinterpret_cast<float2*>(row + D) = make_float2(m[nt][e] == kNone ? kNone : m[nt][e] * rs[nt][e], l[nt][e]);
         }
     if (s.cluster > 1) cluster_wait();
@@ -688,13 +717,13 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB,
                 const int from = min(k, s.cluster - 1);
                 const float2 ml = *reinterpret_cast<const float2*>(mine + (to.sums(from, r) - to.base));
                 m[k] = k < s.cluster ? ml.x : kNone;
-                l[k] = k < s.cluster ? ml.y : 0.f;
+                l[k] = ml.y;
                 v[k] = *reinterpret_cast<const float*>(mine + (to.value(from, r, c) - to.base));
                 M = fmaxf(M, m[k]);
             }
 #pragma unroll
             for (int k = 0; k < kQuantCluster; ++k)
-                if (l[k] != 0.f) {  // (had something; a piece of NaN alone has no maximum, but a sum of NaN)
+                if (m[k] != kNone || l[k] != l[k]) {  // (a piece of NaN alone has no maximum, but a sum of NaN)
                     const float f = exp2f(m[k] - M);
                     sum = fmaf(f, l[k], sum);
                     x = fmaf(f, v[k], x);
