@@ -60,6 +60,7 @@ class Mha:
                                          _DTYPES[dtype])
         self._ws: Optional[torch.Tensor] = None
         self._ws_bytes = 0
+        self._ws_device = -1
         self._ws_captured = False
         self._ws_streams: set = set()  # streams that the allocator knows to use the workspace
         self._kept_ws: list = []
@@ -96,6 +97,9 @@ class Mha:
             self._ws, home = (self._new_workspace_in_capture if capturing else self._new_workspace)(max(need, 256))
             self._ws_streams = {home}
             self._ws_bytes = self._ws.numel()
+            self._ws_device = self._ws.get_device()
+        if 0 <= self._ws_device != torch._C._cuda_getDevice():  # (stream handles do not tell devices apart: 0 is every one's)
+            raise ValueError(f"the layer's workspace is on cuda:{self._ws_device}, which is not the current device")
         if capturing:
             self._ws_captured = True
         elif _stream() not in self._ws_streams:
@@ -562,7 +566,7 @@ class Mha:
                 (counts is not None and counts.get_device() != dev) or _current_device() != dev:
             self._device(cache._data, X, Y, lengths, counts)  # says what is wrong
         stream = _current_stream(dev)
-        if need > self._ws_bytes or stream not in self._ws_streams or _capturing():
+        if need > self._ws_bytes or stream not in self._ws_streams or dev != self._ws_device or _capturing():
             self.ensure_workspace(0, 0, 0, need=need)
         return stream
 
