@@ -116,7 +116,9 @@ size_t mha_workspace_size(mha_t handle, int B, int T_q, int T_kv);
  * may write there while it is attached.  The zeros follow the work queued on the
  * legacy default stream and are in place on return; other streams must have no
  * work pending on the memory.  The memory must stay valid while calls using
- * the handle are in flight.  NULL detaches.  The first attach also creates the
+ * the handle are in flight, and calls that need it must follow one another: they
+ * keep partial results there, so that two of them, or a graph's replay and a call,
+ * on streams that are not ordered would overwrite each other's.  NULL detaches.  The first attach also creates the
  * two copy streams and the events mha_forward_host uses, on the current device
  * (MHA_ERR_CUDA if that fails); they live until mha_destroy.
  */

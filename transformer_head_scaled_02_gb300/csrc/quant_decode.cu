@@ -10,7 +10,8 @@
 // tokens at a time in turn, a lane per token for the scores and a lane per eight channels for the values, each with
 // its own running maximum, sum and values, joined at the end.  It is bound by its two multiply-adds and one conversion
 // per code and row, and by latency before that: 5 ragged sequences of up to 1500 tokens, 16 heads of 80, 4 bits, which
-// quant_mma.cu now has: 27 us (14.7 there).
+// quant_mma.cu now has: 27 us (14.7 there).  16 of 4096, 8 heads of 64 for keys and 128 for values, 8 bits: 109 us, where 16
+// would move the bytes; a third of the cycles issue, most of the others wait for codes and parameters out of memory.
 #include <math.h>
 
 #include "internal.h"
@@ -312,22 +313,24 @@ size_t qd_smem(const QuantPlane& pk, const QuantPlane& pv) {
 }  // namespace
 
 // When a step's groups each get a cluster (us, cluster | even cut and join): 16 sequences of 1500 tokens, 16 K/V heads of
-// 64, 12 quanta a CTA 10.4 | 16.9; 8 of 2048, 16 of 128, 8 quanta 14.4 | 19.8; 32 of 8192, 4 of 128, 32 quanta 37.6 | 35.5.
+// 64, 12 quanta a CTA 10.1 | 16.7; 8 of 2048, 16 of 128, 8 quanta 14.4 | 19.5; 32 ragged of up to 8192, 4 of 128, 32 quanta
+// 35.2 | 34.1 (all of 8192: 36.3 | 39.7).
 // All clusters have to run at a time: a second wave costs 5 to 6 us, a CTA's latency from its lengths to its outputs.  One
 // sequence is cut into more clusters a group from 6 quanta a CTA on: 16384 tokens, 4 heads, 16 quanta in one cluster
-// 15.9, several 10.2, even cut 13.4; 131072 tokens, 2 heads, 8 bits: even cut 25.9, clusters on all SMs 37 (they do not all
+// 14.2, several 9.3, even cut 13.0; 131072 tokens, 2 heads, 8 bits: even cut 26.3, clusters on all SMs 37 (they do not all
 // fit), on 85 % of them 22.7.
 constexpr int kClusterQuanta = 16;
 constexpr int kClusterQuantaOne = 6;
-constexpr int kClusterQuantaWide = 6;  // of CTAs that an SM holds one of: 8 of 8192, one head of 128, 32 rows, 8 quanta 24.4 | 18.4
+constexpr int kClusterQuantaWide = 6;  // of CTAs that an SM holds one of: 8 of 8192, one head of 128, 32 rows, 8 quanta 26.4 | 20.1
 
 // With more groups than CTAs: the quanta that a CTA may have more than others, where groups are not cut at all, for the
 // join and the shared groups' ends that this saves (32 sequences of 300 tokens, 16 heads of 128, 8 bits: 18.7 | 22.2 us).
 constexpr int kJoinQuanta = 6;
 
-// bf16 steps of at least this many rows of a cached head go to quant_rows.cu, in blocks of 128 (us, there | quant_mma.cu:
-// 2048 rows, one sequence of 8192 tokens, 4 heads of 128, 4 bits 116 | 168; 512 rows, 4 of 4096, 4 of 64 50 | 63; 128
-// rows, 8 of 8192, one of 128 42 | 33: its records are large).
+// bf16 steps of at least this many rows of a cached head go to quant_rows.cu, in blocks of 128 (us, there | quant_mma.cu, 4
+// bits, of 192, 256, 384 and 512 rows.  One sequence of 8192 tokens, 4 heads of 128: 40 | 31, 40 | 37, 50 | 50, 60 | 63; 4
+// ragged of up to 4096, 4 of 64: 34 | 32, 34 | 39, 42 | 52, 50 | 64; 8 ragged of up to 8192, one of 128: 51 | 42, 55 | 54, 63 |
+// 75, 75 | 95.  Its records are large).
 constexpr int kManyRows = 256;
 constexpr int kManyRowsBlock = 128;
 constexpr int kManyRowsCtas = 320;  // most of its CTAs: one an SM

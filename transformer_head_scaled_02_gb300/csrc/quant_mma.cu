@@ -29,11 +29,11 @@
 // moves only when a score exceeds it by 2^8, which one vote per block finds.
 //
 // Measured, bf16 layers, 4 bits, heads of 128, 32 ragged sequences of up to 8192 tokens: 16 heads with one query row each
-// 94 us, 453 MB at 4.8 TB/s.  Copies alone take 72 us; with all of them out of L2 it is the same 94: what bounds it is in
+// 93 us, 453 MB at 4.9 TB/s.  Copies alone take 72 us; with all of them out of L2 it is the same 93: what bounds it is in
 // the SMs, where half of all cycles issue an instruction, with 16 warps, which is all that the registers hold (a tenth
 // fewer instructions, products interleaved, loads ahead or a third stage changed nothing).  4 heads with 4 rows each
-// 34.2 us, of which the join 4 and starts and ends of pieces 11.  One sequence of 4096 tokens, 4 heads of 64: 5.5 us,
-// latency; of 131072 tokens, 2 heads of 128, 8 bits: 22.5 us, HBM's rate but for its start and end.
+// 34.2 us, of which the join 4 and starts and ends of pieces 11.  One sequence of 4096 tokens, 4 heads of 64: 5.4 us,
+// latency; of 131072 tokens, 2 heads of 128, 8 bits: 22.6 us, HBM's rate but for its start and end.
 #include <cuda_fp16.h>
 #include <math.h>
 

@@ -13,11 +13,14 @@
 // Warps 0-3 unpack: codes from global memory, a tile ahead in registers, as fp16 into swizzled tiles of shared memory
 // (two of keys and two of values), with the tokens' steps and lowest values beside them.  Warps 4-11: softmax, two threads
 // a row, which halve its tokens and agree on its maximum through shared memory (with one thread a row its 128 scores did
-// not fit the registers, and the softmax, some 20 instructions a score, is what bounds a tile).  Warp 12: products.
-// Tiles are quanta of 128 tokens; pieces follow one another with a barrier between.
+// not fit the registers).  Warp 12: products.  Tiles are quanta of 128 tokens; pieces follow one another with a barrier
+// between.
 //
-// Measured, 4 bits: 512 new tokens of one sequence of 8192, 16 query heads over 4 of 128: 116 us (quant_mma.cu 168); 128
-// new tokens of each of 4 ragged sequences of up to 4096, 16 heads over 4 of 64: 50 us (63).
+// Measured, 4 bits: 512 new tokens of one sequence of 8192, 16 query heads over 4 of 128: 147 us, 21 of them the join,
+// 234 TFLOP/s (quant_mma.cu 218); 128 new tokens of each of 4 ragged sequences of up to 4096, 16 heads over 4 of 64: 50 us
+// (64).  Nothing is at its limit: a tile of 128 channels takes 8700 cycles, of which its instructions need 3800 to be issued
+// and the tensor core is busy for 1000.  The rest is the chain of a tile: scores, maximum, the two warps' meeting, the wait
+// for the tile before's product, exponentials, P, product.
 #include <cuda_fp16.h>
 #include <math.h>
 
