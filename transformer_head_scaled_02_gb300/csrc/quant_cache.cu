@@ -15,7 +15,7 @@
 //
 // Measured, 4 bits, heads of 128, bf16.  Reading back 32 x 8192 tokens of 4 heads: 78.3 us, 99 % of the rate of a plain
 // copy.  Writing 8 x 8192 of 16 heads: 154 us, 671 MB at 4.4 TB/s: nothing is at its limit, HBM at 66 %, the ALU at 65 %,
-// issue at 71 % (126 instructions for eight channels, most of them the exact quotients and the packing), as a warp's loads
+// issue at 70 % (126 instructions for eight channels, most of them the exact quotients and the packing), as a warp's loads
 // and its arithmetic take turns; reading those back takes 104 us.  fp32, 8 x 8192 of 16 heads of 64: written in 110 us, 612 MB
 // at 5.6 TB/s, read back in 123.
 #include <cuda_bf16.h>

@@ -53,7 +53,8 @@ constexpr int QM_THREADS = 32 * QM_WARPS;
 
 // D: channels that are computed with, DP: those that a row of the cache has.  (What lies behind a short row is the next
 // one's codes: finite numbers, which meet queries of zero and make values that nobody stores.)
-// SPLIT: the columns are shared out to the groups as well.
+// SPLIT: the columns are shared out to the groups as well.  ROUND: sums over blocks are added outside the tensor core, which
+// cuts off what its sums cannot hold, always towards zero, 3.6e-8 of a sum of codes with every product.
 template <int BITS, int D, int DP, int TERMS, int NT, int SUB, bool SPLIT>
 struct QmCfg {
     static constexpr int G = D / kQuantGroup;
@@ -179,11 +180,8 @@ __device__ __forceinline__ uint32_t sub_centre(uint32_t x) {
 
 // Eight of a row's channels in a group (values) of two tokens a, b, as the A operands of the group's four products:
 // x[t][0] channel 2 t of both tokens, x[t][1] channel 2 t + 1.  fp32 layers take half the range off the codes (and add it to
-// the lowest values), and add their sums over blocks outside the tensor core: it cuts off what its sums cannot hold, and
-// over thousands of tokens the sums of codes are far larger than what is left of them in the output (5400 tokens of small
-// scores: 2e-5 of the outputs with both left out, 1.3e-6 with the centre alone taken off, 1e-7 with both).  bf16 layers leave
-// both out: 3e-8 of the codes' part for each 16 tokens of a warp, far below what the weights' 11 bits cost (adding outside
-// the tensor core took 1 to 3 % longer).
+// the lowest values): over thousands of tokens the sums of codes are far larger than what is left of them in the output
+// (5400 tokens of small scores: 2e-5 of the outputs with neither this nor ROUND, 1.3e-6 with this alone, 1e-7 with both).
 template <int BITS, int TERMS>
 __device__ __forceinline__ void value_operands(uint32_t addr_a, uint32_t addr_b, uint32_t (&x)[4][2]) {
     uint32_t a[BITS / 4], b[BITS / 4];
@@ -217,7 +215,7 @@ __device__ __forceinline__ void token_params(uint32_t addr, uint32_t (&p)[G]) {
 __device__ __forceinline__ float elem(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float elem(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
-template <int BITS, int D, int DP, int TERMS, int NT, int SUB, bool SPLIT, typename T>
+template <int BITS, int D, int DP, int TERMS, int NT, int SUB, bool SPLIT, bool ROUND, typename T>
 __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB, SPLIT>::CTAS)
     quant_mma_kernel(const QuantStep s, const QuantPlane pk, const QuantPlane pv, const T* __restrict__ Q, int64_t ldq,
                      T* __restrict__ O, int64_t ldo, const int32_t* __restrict__ lengths, float scale_log2,
@@ -619,9 +617,9 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB,
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             float(&to)[4] = o[nt][SPLIT ? 0 : u][c];
-                            if constexpr (TERMS == 1) {
+                            if constexpr (!ROUND) {
                                 mma_f16(to, a, w2[0][nt][0], w2[0][nt][1]);
-                            } else {  // (sums over many blocks are rounded, not cut off)
+                            } else {
                                 float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                                 for (int w = 0; w < TERMS; ++w) mma_f16(d, a, w2[w][nt][0], w2[w][nt][1]);
@@ -742,17 +740,36 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB,
             drain_wait_a(bars + 8u * (uint32_t)(k % C::STAGES), (uint32_t)(k / C::STAGES) & 1u);
 }
 
+// Products that a warp's sums take, from when on bf16 layers add them outside the tensor core (fp32 layers always do).  With
+// 32 the cut is 1.2e-6 of the codes' part of an output, which is below bf16's rounding where the outputs are 1/2000 of it;
+// values around zero under even weights come to that at 65536 tokens: 512 products were off by 1.2 % there, 0.17 % so, of
+// which the outputs' own rounding is all.  It takes 1 to 3 % longer (us, within | outside, 16 heads as in the file's
+// comment 92.8 | 94.7, 4 heads of 4 rows 34.1 | 35.1).
+constexpr int kRoundProducts = 32;
+
+// The most tokens of a group that a CTA may have.
+int64_t most_tokens(const QuantStep& s) {
+    const int64_t nq = (s.T_max + kQuantum - 1) / kQuantum, all = (int64_t)s.B * s.lanes() * nq;
+    const int64_t each = s.cluster ? (nq + s.cluster * s.parts - 1) / (s.cluster * s.parts) : s.quantum > kQuantum ? nq : all / s.ctas + 1;
+    return kQuantum * (each < nq ? each : nq);
+}
+
 template <int BITS, int D, int DP, int TERMS, int NT, int SUB, bool SPLIT, typename T>
 cudaError_t launch(const QuantStep& s, const QuantPlane& pk, const QuantPlane& pv, const void* Q, int64_t ldq, void* O,
                    int64_t ldo, const int32_t* lengths, float* part, int* status, cudaStream_t stream) {
     using C = QmCfg<BITS, D, DP, TERMS, NT, SUB, SPLIT>;
-    auto kernel = quant_mma_kernel<BITS, D, DP, TERMS, NT, SUB, SPLIT, T>;
-    static std::atomic<uint64_t> done{0};
     const float scale = (float)(1.4426950408889634 / sqrt((double)pk.d));
-    return launch_with_smem(kernel, C::SMEM, done, [&] {
-        return launch_pdl_cluster(kernel, s.cluster > 1 ? s.cluster : 1, dim3((unsigned)s.ctas), dim3(QM_THREADS), C::SMEM, stream, s,
-                                  pk, pv, static_cast<const T*>(Q), ldq, static_cast<T*>(O), ldo, lengths, scale, part, status);
-    });
+    auto go = [&](auto round) {
+        auto kernel = quant_mma_kernel<BITS, D, DP, TERMS, NT, SUB, SPLIT, round.value, T>;
+        static std::atomic<uint64_t> done{0};
+        return launch_with_smem(kernel, C::SMEM, done, [&] {
+            return launch_pdl_cluster(kernel, s.cluster > 1 ? s.cluster : 1, dim3((unsigned)s.ctas), dim3(QM_THREADS), C::SMEM, stream, s,
+                                      pk, pv, static_cast<const T*>(Q), ldq, static_cast<T*>(O), ldo, lengths, scale, part, status);
+        });
+    };
+    if constexpr (TERMS == 1)
+        if (most_tokens(s) <= kRoundProducts * 16 * QM_WARPS * SUB) return go(std::false_type{});
+    return go(std::true_type{});
 }
 
 // (fp32 layers of 128 channels have no room in the registers for 16 rows)
