@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(QR_THREADS, 1)
             mbar_init(v_full + 8u * i, 128);
             mbar_init(v_empty + 8u * i, 1);
         }
-        mbar_init(s_full, 1);
+        mbar_init(s_full, 2);
         mbar_init(s_free, QR_SOFTMAX);
         mbar_init(p_full, QR_SOFTMAX);
         mbar_init(pv_done, 1);
@@ -285,6 +285,7 @@ __global__ void __launch_bounds__(QR_THREADS, 1)
                     const uint32_t st = (uint32_t)n & 1u;
                     if (!mbar_wait(k_full + 8u * st, (uint32_t)(n >> 1) & 1u, abort_flag, status)) return false;
                     if (n > 0 && !mbar_wait(s_free, (uint32_t)(n - 1) & 1u, abort_flag, status)) return false;
+                    mbar_arrive(s_full);  // the keys' parameters are there (its other arrival: the products)
                     tc_fence_after();
                     const uint64_t kd = kd0 + (uint64_t)((st * C::TILE) >> 4);
 #pragma unroll
@@ -347,8 +348,9 @@ __global__ void __launch_bounds__(QR_THREADS, 1)
             for (int i = 0; i < n_tiles && ok; ++i) {
                 const int n = n0 + i, key0 = k0 + 128 * i + c0;
                 const uint32_t st = (uint32_t)n & 1u, ph = (uint32_t)(n >> 1) & 1u;
-                ok = __all_sync(0xffffffffu, mbar_wait(s_full, (uint32_t)n & 1u, abort_flag, status) &&
-                                                 mbar_wait(k_full + 8u * st, ph, abort_flag, status));
+                // (Not k_full: the tile after the next may be there before a late warp asks, and the barrier's parity be this
+                // one's again.  Every other barrier's next phase but one waits for those who wait for this one.)
+                ok = __all_sync(0xffffffffu, mbar_wait(s_full, (uint32_t)n & 1u, abort_flag, status));
                 if (!ok) break;
                 tc_fence_after();
                 float y[64], top = -INFINITY;
