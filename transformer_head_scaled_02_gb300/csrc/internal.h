@@ -198,6 +198,7 @@ cudaError_t launch_quant_copy(bool write, bool f32, int bits, const QuantPlane& 
 // mha_decode_quant: how a step is cut, the bytes of its records (part), and its launches.
 QuantStep quant_step_shape(bool f32, int bits, int d_k, int d_v, int B, int h, int h_kv, int T_q, int T_max, int sms);
 int64_t quant_most_quanta(const QuantStep& s);
+int64_t quant_most_tokens(const QuantStep& s);  // of one group that a CTA may have
 size_t quant_step_bytes(const QuantStep& s);
 bool quant_step_fits(const QuantStep& s);
 cudaError_t launch_quant_decode(const QuantStep& s, bool f32, int bits, const QuantPlane& pk, const QuantPlane& pv,

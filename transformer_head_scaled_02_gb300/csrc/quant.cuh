@@ -56,6 +56,7 @@ struct Divide {
 constexpr int kQuantum = 128;      // tokens
 constexpr int kQuantMaxCtas = 640; // largest grid, for the size of the workspace
 constexpr int kQuantCluster = 8;   // largest cluster
+constexpr int kQuantRowsLong = 4096;  // tokens of a piece that quant_rows.cu's tensor-core sums may take
 
 struct QuantStep {
     int B, h_kv, per, T_q, T_max;

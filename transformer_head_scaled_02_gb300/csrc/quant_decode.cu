@@ -385,11 +385,19 @@ QuantStep quant_step_shape(bool f32, int bits, int d_k, int d_v, int B, int h, i
 
 int64_t quant_most_quanta(const QuantStep& s) { return (int64_t)s.B * s.h_kv * s.nrb * ((s.T_max + kQuantum - 1) / kQuantum); }
 
-// For any number of SMs.
+int64_t quant_most_tokens(const QuantStep& s) {
+    const int64_t nq = (s.T_max + kQuantum - 1) / kQuantum, ctas = s.cluster * s.parts;
+    const int64_t each = s.cluster ? (nq + ctas - 1) / ctas : s.quantum > kQuantum ? nq : quant_most_quanta(s) / s.ctas + 1;
+    return kQuantum * (each < nq ? each : nq);
+}
+
+// For any number of SMs: two records a CTA, and behind them one place for sums of blocks of many rows whose pieces may
+// be long.
 size_t quant_step_bytes(const QuantStep& s) {
     const int64_t most = quant_most_quanta(s);
     const int64_t ctas = most < most_ctas(s) ? most : most_ctas(s);
-    return sizeof(float) * 2 * (size_t)ctas * s.rb * s.record();
+    const int sums = s.rb == kManyRowsBlock && s.T_max > kQuantRowsLong ? s.dv : 0;
+    return sizeof(float) * (size_t)ctas * s.rb * (2 * s.record() + sums);
 }
 
 bool quant_step_fits(const QuantStep& s) {

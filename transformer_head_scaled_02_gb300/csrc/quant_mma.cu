@@ -747,13 +747,6 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<BITS, D, DP, TERMS, NT, SUB,
 // comment 92.8 | 94.7, 4 heads of 4 rows 34.1 | 35.1).
 constexpr int kRoundProducts = 32;
 
-// The most tokens of a group that a CTA may have.
-int64_t most_tokens(const QuantStep& s) {
-    const int64_t nq = (s.T_max + kQuantum - 1) / kQuantum, all = (int64_t)s.B * s.lanes() * nq;
-    const int64_t each = s.cluster ? (nq + s.cluster * s.parts - 1) / (s.cluster * s.parts) : s.quantum > kQuantum ? nq : all / s.ctas + 1;
-    return kQuantum * (each < nq ? each : nq);
-}
-
 template <int BITS, int D, int DP, int TERMS, int NT, int SUB, bool SPLIT, typename T>
 cudaError_t launch(const QuantStep& s, const QuantPlane& pk, const QuantPlane& pv, const void* Q, int64_t ldq, void* O,
                    int64_t ldo, const int32_t* lengths, float* part, int* status, cudaStream_t stream) {
@@ -768,7 +761,7 @@ cudaError_t launch(const QuantStep& s, const QuantPlane& pk, const QuantPlane& p
         });
     };
     if constexpr (TERMS == 1)
-        if (most_tokens(s) <= kRoundProducts * 16 * QM_WARPS * SUB) return go(std::false_type{});
+        if (quant_most_tokens(s) <= kRoundProducts * 16 * QM_WARPS * SUB) return go(std::false_type{});
     return go(std::true_type{});
 }
 

@@ -16,8 +16,8 @@
 // not fit the registers).  Warp 12: products.  Tiles are quanta of 128 tokens; pieces follow one another with a barrier
 // between.
 //
-// Measured, 4 bits: 512 new tokens of one sequence of 8192, 16 query heads over 4 of 128: 147 us, 21 of them the join,
-// 234 TFLOP/s (quant_mma.cu 218); 128 new tokens of each of 4 ragged sequences of up to 4096, 16 heads over 4 of 64: 50 us
+// Measured, 4 bits: 512 new tokens of one sequence of 8192, 16 query heads over 4 of 128: 145 us, 21 of them the join,
+// 237 TFLOP/s (quant_mma.cu 218); 128 new tokens of each of 4 ragged sequences of up to 4096, 16 heads over 4 of 64: 50 us
 // (64).  Nothing is at its limit: a tile of 128 channels takes 8700 cycles, of which its instructions need 3800 to be issued
 // and the tensor core is busy for 1000.  The rest is the chain of a tile: scores, maximum, the two warps' meeting, the wait
 // for the tile before's product, exponentials, P, product.
@@ -38,6 +38,7 @@ constexpr int QR_THREADS = 416;
 constexpr int QR_MMA_WARP = 12;
 constexpr int QR_SOFTMAX = 256;  // threads
 constexpr int QR_ROWS = 128;
+constexpr int QR_SUMS = 16;    // tiles after which long pieces' sums are moved
 constexpr int QR_PARAMS = 4;  // tiles whose parameters are kept: a tile's are read until its values are asked for
 constexpr float kRowsNone = -3e38f;
 
@@ -53,7 +54,8 @@ struct QrCfg {
     static constexpr int TOP = VP + QR_PARAMS * 128 * 16;    // largest value step of a tile, per unpacking warp
     static constexpr int QS = TOP + QR_PARAMS * 16;          // per row: sums of q per group, score factor
     static constexpr int XM = QS + QR_ROWS * (G + 1) * 4;    // a row's maxima, by tile parity and half; at the end its sums
-    static constexpr int BARS = XM + 2 * 2 * QR_ROWS * 4 * 2;
+    static constexpr int MS = XM + 2 * 2 * QR_ROWS * 4 * 2;  // a softmax thread's reference that its moved sums go by
+    static constexpr int BARS = MS + QR_SOFTMAX * 4;
     static constexpr int SMEM = BARS + 17 * 8 + 16 + 1024;
     static constexpr int OUT = D + 3;                        // floats of a row of results (odd: rows in other banks)
     static_assert(QR_ROWS * OUT * 4 <= 4 * TILE, "the results fit the key and value tiles");
@@ -88,12 +90,44 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 
+// Where a softmax thread's sums are: [channel][row] for each CTA, behind the records.
+template <int D>
+__device__ __forceinline__ float* moved_sums(const QuantStep& s, float* part, int half, int r) {
+    return part + s.slot((int)gridDim.x, 0, 0) + ((int64_t)blockIdx.x * D + half * (D / 2)) * QR_ROWS + r;
+}
+
+// A row's sums of QR_SUMS tiles, half of its channels, go from tensor memory there: as values, added to f times what
+// is there, or the first ones.  inv: 1 / vs.
+template <int BITS, int D>
+__device__ __forceinline__ void move_sums(uint32_t taddr, float* sums, bool first, float f, float inv) {
+#pragma unroll 1
+    for (int c = 0; c < D / 2; c += 32, sums += 32 * QR_ROWS) {
+        uint32_t o[32];
+        tmem_ld32(taddr + c, o);
+        tmem_wait_ld();
+        reg_fence(o);
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+            float old[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) old[k] = first ? 0.f : sums[(e + k) * QR_ROWS];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                sums[(e + k) * QR_ROWS] = fmaf(__uint_as_float(o[e + k]) * (1.f / unit_of<BITS>(k)), inv, f * old[k]);
+        }
+    }
+}
+
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <int BITS, int D>
+// LONG: the sums go to memory every QR_SUMS tiles, where they are added in fp32, as the tensor core cuts off what its sums
+// cannot hold, always towards zero (2.8e-8 of a sum of codes with each of a tile's eight products).  For pieces of more than
+// kQuantRowsLong tokens: 8 rows of a head over 20 x 32768 tokens of values around zero were off by 2.6 % at 4 bits and 3.7 %
+// at 8, of which bf16's rounding is 0.17 %, and are by 0.19 and 0.29 %; it takes 5 % longer (1182 us | 1238).
+template <int BITS, int D, bool LONG>
 __global__ void __launch_bounds__(QR_THREADS, 1)
     quant_rows_kernel(const QuantStep s, const QuantPlane pk, const QuantPlane pv, const __nv_bfloat16* __restrict__ Q, int64_t ldq,
                       __nv_bfloat16* __restrict__ O, int64_t ldo, const int32_t* __restrict__ lengths, float scale_log2,
@@ -316,7 +350,8 @@ __global__ void __launch_bounds__(QR_THREADS, 1)
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
                             mma_bf16_ts(tmem + C::O_COL + 64 * u, tmem + C::P_COL + 64 * u + kk * 8,
-                                        vd + (uint64_t)((u * C::CHUNK + kk * 2048) >> 4), idesc_o, (i > 0 || kk > 0) ? 1u : 0u);
+                                        vd + (uint64_t)((u * C::CHUNK + kk * 2048) >> 4), idesc_o,
+                                        ((LONG ? i % QR_SUMS : i) > 0 || kk > 0) ? 1u : 0u);
                     tc_commit(pv_done);
                     tc_commit(v_empty + 8u * st);
                 }
@@ -347,6 +382,18 @@ __global__ void __launch_bounds__(QR_THREADS, 1)
 #pragma unroll 1
             for (int i = 0; i < n_tiles && ok; ++i) {
                 const int n = n0 + i, key0 = k0 + 128 * i + c0;
+                if (LONG && i > 0 && i % QR_SUMS == 0) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (uint32_t)(n - 1) & 1u, abort_flag, status));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (!idle) {
+                        volatile float* m_sums = reinterpret_cast<float*>(sm + C::MS) + half * QR_ROWS + r;
+                        const bool first = i == QR_SUMS;
+                        move_sums<BITS, D>(trow + C::O_COL + half * (D / 2), moved_sums<D>(s, part, half, r), first,
+                                           first ? 0.f : ex2_approx(*m_sums - m), 1.f / vs);
+                        *m_sums = m;
+                    }
+                }
                 const uint32_t st = (uint32_t)n & 1u, ph = (uint32_t)(n >> 1) & 1u;
                 // (Not k_full: the tile after the next may be there before a late warp asks, and the barrier's parity be this
                 // one's again.  Every other barrier's next phase but one waits for those who wait for this one.)
@@ -422,7 +469,7 @@ __global__ void __launch_bounds__(QR_THREADS, 1)
                 }
                 tc_fence_after();
                 if (!idle) {
-                    if (i > 0 && __any_sync(0xffffffffu, moved)) {  // each of the two warps half of the columns
+                    if ((LONG ? i % QR_SUMS : i) > 0 && __any_sync(0xffffffffu, moved)) {  // each of the two warps half of the columns
                         #pragma unroll
                         for (int c = 0; c < D / 64; ++c) {
                             uint32_t o[32];
@@ -483,6 +530,9 @@ __global__ void __launch_bounds__(QR_THREADS, 1)
                 // every key and value tile is used: the rows meet there, to be written as rows
                 float* row = reinterpret_cast<float*>(sm + C::K) + r * C::OUT;
                 const float inv = z.whole() ? 1.f / l : 1.f, back = 1.f / vs;  // (vs goes down to 2^-126: 2^24 / vs may be infinite)
+                const bool moved = LONG && n_tiles > QR_SUMS;
+                const float f_sums = moved ? ex2_approx(reinterpret_cast<const float*>(sm + C::MS)[half * QR_ROWS + r] - m) : 0.f;
+                const float* sums = moved_sums<D>(s, part, half, r);
                 if (half == 0) row[0] = m, row[1] = l;
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
@@ -495,8 +545,11 @@ __global__ void __launch_bounds__(QR_THREADS, 1)
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
 #pragma unroll
-                        for (int p = 0; p < 8; ++p)
-                            row[2 + col + e + channel_of<BITS>(p)] = inv * fmaf(__uint_as_float(o[e + p]) * (1.f / unit_of<BITS>(p)), back, z0);
+                        for (int p = 0; p < 8; ++p) {
+                            const float before = moved ? fmaf(f_sums, sums[(32 * c + e + p) * QR_ROWS], z0) : z0;
+                            row[2 + col + e + channel_of<BITS>(p)] =
+                                inv * fmaf(__uint_as_float(o[e + p]) * (1.f / unit_of<BITS>(p)), back, before);
+                        }
                 }
             }
         }
@@ -543,12 +596,16 @@ template <int BITS, int D>
 cudaError_t launch(const QuantStep& s, const QuantPlane& pk, const QuantPlane& pv, const void* Q, int64_t ldq, void* O, int64_t ldo,
                    const int32_t* lengths, float* part, int* status, cudaStream_t stream) {
     using C = QrCfg<BITS, D>;
-    static std::atomic<uint64_t> done{0};
     const float scale = (float)(1.4426950408889634 / sqrt((double)D));
-    return launch_with_smem(quant_rows_kernel<BITS, D>, C::SMEM, done, [&] {
-        return launch_pdl(quant_rows_kernel<BITS, D>, dim3((unsigned)s.ctas), dim3(QR_THREADS), C::SMEM, stream, s, pk, pv,
-                          static_cast<const __nv_bfloat16*>(Q), ldq, static_cast<__nv_bfloat16*>(O), ldo, lengths, scale, part, status);
-    });
+    auto go = [&](auto is_long) {
+        auto kernel = quant_rows_kernel<BITS, D, is_long.value>;
+        static std::atomic<uint64_t> done{0};
+        return launch_with_smem(kernel, C::SMEM, done, [&] {
+            return launch_pdl(kernel, dim3((unsigned)s.ctas), dim3(QR_THREADS), C::SMEM, stream, s, pk, pv,
+                              static_cast<const __nv_bfloat16*>(Q), ldq, static_cast<__nv_bfloat16*>(O), ldo, lengths, scale, part, status);
+        });
+    };
+    return quant_most_tokens(s) > kQuantRowsLong ? go(std::true_type{}) : go(std::false_type{});
 }
 
 }  // namespace
