@@ -533,15 +533,16 @@ size_t mha_decode_quant_workspace_size(mha_t handle, int B, int T_q, int T_max);
  * keys and values are those that the codes stand for, s code + m, without further rounding.  Q, O, cache_lengths as
  * for mha_decode (an L_b outside [T_q, T_max] makes that batch's rows NaN and records MHA_ERR_BAD_LENGTH).  O must
  * not overlap an input.  Needs a workspace of mha_decode_quant_workspace_size(B, T_q, T_max) bytes.  One or two
- * launches; results do not depend on the order in which the GPU runs them.  Scores, sums and the lowest values' part
- * are fp32; the tensor core cuts its sums off instead of rounding them, so those are of at most 256 products each, which
- * takes at most 2^-16 of the part that the codes add to an output.  Weighted sums are held before the division, by weights
- * of up to 2^8 each: outputs are finite as long as the values a row sees, in magnitude, add up to less than 2^120.  Products of a weight and a step are held in
- * fp16 (bf16 layers) or as two of them (fp32 layers with d_k == d_v <= 128) against a power of two that follows the
- * row: each is off by at most 2^-11 (2^-22) of itself, and by 2^-23 of the row's largest besides.  Queries are held
- * likewise: bf16 ones are off by at most 2^-34 of a row's largest element, fp32 ones by 2^-22 of themselves and 2^-38
- * of that; elements of 2^118 and more overflow.  MHA_ERR_UNSUPPORTED where B * h_kv * ceil(h / h_kv * T_q / 4)
- * * ceil(T_max / 128) may exceed 2^31.
+ * launches; results do not depend on the order in which the GPU runs them.  Scores, sums and the lowest values'
+ * part are fp32; the tensor core cuts its sums off instead of rounding them, so those are of at most 256 products
+ * each, which takes at most 2^-16 of the part that the codes add to an output.  Weighted sums are held before the
+ * division, by weights of up to 2^8 each: outputs are finite as long as the largest magnitudes of a group of
+ * channels, over the tokens a row sees, add up to less than 2^118.  Products of a weight and a step are held in
+ * fp16 (bf16 layers) or as two of them (fp32 layers with d_k == d_v <= 128) against a power of two that follows
+ * the row: each is off by at most 2^-11 (2^-22) of itself, and by 2^-23 of the row's largest besides.  Queries are
+ * held likewise: bf16 ones are off by at most 2^-34 of a row's largest element, fp32 ones by 2^-22 of themselves
+ * and 2^-38 of that; elements of 2^118 and more overflow.  MHA_ERR_UNSUPPORTED where B * h_kv * ceil(h / h_kv *
+ * T_q / 4) * ceil(T_max / 128) may exceed 2^31.
  */
 mha_status mha_decode_quant(mha_t handle, int bits, int B, int T_q, int T_max, const void* Q, int64_t ldq,
                             const void* cache, const int32_t* cache_lengths, void* O, int64_t ldo, void* stream);
