@@ -442,7 +442,8 @@ __global__ void __launch_bounds__(QR_THREADS, 1)
                         moved = true;
                     }
                     const float4 w = *reinterpret_cast<const float4*>(sm + C::TOP + (n % QR_PARAMS) * 16);
-                    moved = moved || fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w)) * vs > kQuantStepMost;
+                    // (rows past nr have queries of some earlier block, and no say in when the others' scales follow)
+                    moved = (moved || fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w)) * vs > kQuantStepMost) && r < nr;
                     if (__any_sync(0xffffffffu, moved)) {  // (so says the row's other warp)
                         const uint32_t par = base + C::VP + (uint32_t)(((n % QR_PARAMS) * 128 + c0) * 16);
                         float need = 0.f;
